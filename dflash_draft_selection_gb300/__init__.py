@@ -7,14 +7,18 @@ the first call loads the library and raises if it is missing.
 """
 from .binding import (  # noqa: F401
     DFlash2Error,
+    KVCache,
     Workspace,
     conv2tap,
     ctx_gate,
     device_error,
     dynconv2tap,
+    kv_evict,
     lmhead_topk16,
     load_library,
     pair_score_walk,
+    paged_attn,
+    rope_append,
     sampling_params,
     test_hold,
     topk16,

@@ -31,6 +31,17 @@ _lib = None
 _lock = threading.Lock()
 
 
+ATTN_CAUSAL, ATTN_WEIGHTS = 1, 2
+
+
+class _CacheRecord(ctypes.Structure):
+    """dflash2_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("Hkv", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dt", ctypes.c_int32)]
+
+
 class DFlash2Error(RuntimeError):
     def __init__(self, fn: str, code: int):
         self.code = code
@@ -65,6 +76,16 @@ def load_library():
                                      vp, sz, vp]
         L.dflash2_conv2tap.argtypes = [vp, vp, vp, vp, i32, i64, i32, i64, i32, vp, vp]
         L.dflash2_dynconv2tap.argtypes = [vp, vp, vp, i32, i64, i32, i64, i32, vp, vp, vp]
+        f32 = ctypes.c_float
+        L.dflash2_rope_append.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, vp, i64,
+                                          i32, vp, i32, vp, i32, vp, vp, f32, vp, vp, vp]
+        L.dflash2_paged_attn_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32]
+        L.dflash2_paged_attn_workspace_bytes.restype = sz
+        L.dflash2_paged_attn.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, i32, i32, f32, i32, u32, vp, vp, vp, sz,
+                                         vp]
+        L.dflash2_kv_evict_workspace_bytes.argtypes = [i64, i32, i64, i32]
+        L.dflash2_kv_evict_workspace_bytes.restype = sz
+        L.dflash2_kv_evict.argtypes = [vp, vp, i32, vp, vp, i64, i32, i32, i32, vp, vp, sz, vp]
         L.dflash2_status_string.argtypes = [i32]
         L.dflash2_status_string.restype = ctypes.c_char_p
         L.dflash2_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
@@ -73,7 +94,7 @@ def load_library():
                    "dflash2_lmhead_topk16",
                    "dflash2_ctx_gate", "dflash2_pair_score_walk",
                    "dflash2_verify", "dflash2_conv2tap", "dflash2_dynconv2tap", "dflash2_device_error",
-                   "dflash2_test_hold"):
+                   "dflash2_test_hold", "dflash2_rope_append", "dflash2_paged_attn", "dflash2_kv_evict"):
             getattr(L, fn).restype = i32
         _lib = L
         return _lib
@@ -101,6 +122,28 @@ def _dtype(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return F32
     raise TypeError(f"unsupported dtype {t.dtype}")
+
+
+def _dtype_code(dt: torch.dtype) -> int:
+    if dt == torch.bfloat16:
+        return BF16
+    if dt == torch.float32:
+        return F32
+    raise TypeError(f"unsupported dtype {dt}")
+
+
+def _int32(B: int, **ts):
+    """Per-request arrays: contiguous int32 [B] (None passes)."""
+    for name, t in ts.items():
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B or not t.is_contiguous()):
+            raise ValueError(f"{name}: contiguous int32 [{B}]")
+    _need_cuda(*ts.values())
+
+
+def _page_table(table: torch.Tensor, B: int):
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
+        raise ValueError(f"page_table: contiguous int32 [{B}, pages]")
+    _need_cuda(table)
 
 
 def _stream(device) -> ctypes.c_void_p:
@@ -155,6 +198,50 @@ class Workspace:
     @staticmethod
     def for_verify(B: int, K: int, device="cuda") -> "Workspace":
         return Workspace(load_library().dflash2_verify_workspace_bytes(B, K), device)
+
+    @staticmethod
+    def for_paged_attn(B: int, T: int, Hq: int, Hkv: int, d: int, dtype, device="cuda") -> "Workspace":
+        return Workspace(load_library().dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, _dtype_code(dtype)),
+                         device)
+
+    @staticmethod
+    def for_kv_evict(B: int, Hkv: int, capacity: int, budget: int, device="cuda") -> "Workspace":
+        """capacity: the slots a request's page table can hold (pages * page size)."""
+        return Workspace(load_library().dflash2_kv_evict_workspace_bytes(B, Hkv, capacity, budget), device)
+
+
+class KVCache:
+    """A paged key-value cache: k and v [num_pages, Hkv, page_size, d] (bf16 or f32), of any strides with
+    contiguous rows of d (a [num_pages, page_size, Hkv, d] pool is passed transposed), and the optional side
+    arrays weight (f32) and pos (i32), contiguous [num_pages, Hkv, page_size].  Holds views, copies nothing."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, weight: torch.Tensor | None = None,
+                 pos: torch.Tensor | None = None):
+        _need_cuda(k, v, weight, pos)
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v: one shape [num_pages, Hkv, page_size, d], one type and one layout, rows of d "
+                             "contiguous")
+        for name, t, dt in (("weight", weight, torch.float32), ("pos", pos, torch.int32)):
+            if t is not None and (t.dtype != dt or t.shape != k.shape[:3] or not t.is_contiguous()):
+                raise ValueError(f"{name}: contiguous {dt} [num_pages, Hkv, page_size]")
+        if any(t is not None and t.device != k.device for t in (v, weight, pos)):
+            raise ValueError("a cache's tensors lie on one device")
+        self.k, self.v, self.weight, self.pos = k, v, weight, pos
+        self.num_pages, self.Hkv, self.page_size, self.d = k.shape
+        self.device, self.dtype = k.device, k.dtype
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._rec = _CacheRecord(ptr(k), ptr(v), ptr(weight), ptr(pos), self.num_pages, k.stride(0), k.stride(1),
+                                 k.stride(2), self.Hkv, self.page_size, self.d, _dtype(k))
+        self._ref = ctypes.byref(self._rec)
+
+    @staticmethod
+    def empty(num_pages: int, Hkv: int, page_size: int, d: int, dtype=torch.bfloat16, weights: bool = False,
+              positions: bool = False, device="cuda") -> "KVCache":
+        """Uninitialised pages (weights and positions zero)."""
+        kv = torch.empty(2, num_pages, Hkv, page_size, d, dtype=dtype, device=device)
+        side = (num_pages, Hkv, page_size)
+        return KVCache(kv[0], kv[1], torch.zeros(side, device=device) if weights else None,
+                       torch.zeros(side, dtype=torch.int32, device=device) if positions else None)
 
 
 # ------------------------------------------------------------------ calls ----
@@ -351,6 +438,91 @@ def dynconv2tap(x, x_prev, Wd, group: int = 1, out=None):
     _check("dflash2_dynconv2tap", L.dflash2_dynconv2tap(_ptr(x), _ptr(x_prev), _ptr(Wd), _dtype(x), B, T, H, group,
                                                         _ptr(taps), _ptr(y), _stream(x.device)))
     return taps, y
+
+
+def rope_append(q, k, v, cos_sin, pos_ids, cache: KVCache, page_table, kv_len, pair_axis=None,
+                interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6, q_len=None, seq_pos=None,
+                out=None):
+    """dflash2_rope_append.  q [B, T, Hq, d], k and v [B, T, Hkv, d] of the cache's type (slices of a fused
+    projection are taken as they are); cos_sin [n_pos, rot] f32; pos_ids [axes, B, T] int32; pair_axis [rot / 2]
+    uint8; kv_len [B] int32, the slots in use before the call.  Returns (rotated q [B, T, Hq, d], kv_len + q_len)."""
+    L = load_library()
+    B, T, Hq, d = q.shape
+    _need_cuda(q, k, v, cos_sin, pos_ids, pair_axis, q_norm, k_norm)
+    for name, t, H in (("q", q, Hq), ("k", k, cache.Hkv), ("v", v, cache.Hkv)):
+        if t.dtype != cache.dtype or t.shape != (B, T, H, cache.d) or \
+                (t.numel() and (t.stride(3) != 1 or (H > 1 and t.stride(2) != d) or
+                                (B > 1 and T > 1 and t.stride(0) != T * t.stride(1)))):
+            raise ValueError(f"{name}: {cache.dtype} [{B}, {T}, {H}, {cache.d}] with contiguous heads and one stride "
+                             "from token to token")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin: contiguous float32 [n_pos, rot]")
+    if pos_ids.dtype != torch.int32 or pos_ids.dim() != 3 or pos_ids.shape[1:] != (B, T) or not pos_ids.is_contiguous():
+        raise ValueError(f"pos_ids: contiguous int32 [axes, {B}, {T}]")
+    rot = cos_sin.shape[1]
+    if pair_axis is not None and (pair_axis.dtype != torch.uint8 or pair_axis.shape != (rot // 2,) or
+                                  not pair_axis.is_contiguous()):
+        raise ValueError(f"pair_axis: contiguous uint8 [{rot // 2}]")
+    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if t is not None and (t.dtype != cache.dtype or t.shape != (d,) or not t.is_contiguous()):
+            raise ValueError(f"{name}: contiguous {cache.dtype} [{d}]")
+    _page_table(page_table, B)
+    _int32(B, kv_len=kv_len, q_len=q_len, seq_pos=seq_pos)
+    if out is None:
+        out = (torch.empty(B, T, Hq, d, dtype=q.dtype, device=q.device),
+               torch.empty(B, dtype=torch.int32, device=q.device))
+    q_out, kv_len_out = out
+    step = lambda t: t.stride(1) if T > 1 else (t.stride(0) if B > 1 else t.shape[2] * d)  # noqa: E731
+    _check("dflash2_rope_append",
+           L.dflash2_rope_append(cache._ref, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(q_len),
+                                 _ptr(seq_pos), _ptr(q), _ptr(k), _ptr(v), step(q), step(k), step(v), B, T, Hq,
+                                 _ptr(cos_sin), cos_sin.shape[0], rot, _ptr(pos_ids), pos_ids.shape[0],
+                                 _ptr(pair_axis), int(interleaved), _ptr(q_norm), _ptr(k_norm), eps, _ptr(q_out),
+                                 _ptr(kv_len_out), _stream(q.device)))
+    return q_out, kv_len_out
+
+
+def paged_attn(q, cache: KVCache, page_table, kv_len, scale: float | None = None, causal: bool = True,
+               window: int = 0, q_len=None, seq_pos=None, add_weights: bool = False, ws=None, out=None):
+    """dflash2_paged_attn.  q [B, T, Hq, d] of the cache's type; kv_len [B] int32, the slots in use with the block's
+    own among them; scale 1 / sqrt(d) unless given; add_weights adds every cached key's softmax weight to
+    cache.weight.  Returns (out [B, T, Hq, d], lse [B, T, Hq] f32)."""
+    L = load_library()
+    _need_cuda(q)
+    B, T, Hq, d = q.shape
+    if q.dtype != cache.dtype or d != cache.d or not q.is_contiguous():
+        raise ValueError(f"q: contiguous {cache.dtype} [B, T, Hq, {cache.d}]")
+    _page_table(page_table, B)
+    _int32(B, kv_len=kv_len, q_len=q_len, seq_pos=seq_pos)
+    if ws is None:
+        ws = Workspace.for_paged_attn(B, T, Hq, cache.Hkv, d, q.dtype, q.device)
+    if out is None:
+        out = (torch.empty_like(q), torch.empty(B, T, Hq, dtype=torch.float32, device=q.device))
+    o, lse = out
+    flags = (ATTN_CAUSAL if causal else 0) | (ATTN_WEIGHTS if add_weights else 0)
+    _check("dflash2_paged_attn",
+           L.dflash2_paged_attn(cache._ref, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(q_len),
+                                _ptr(seq_pos), _ptr(q), B, T, Hq, d ** -0.5 if scale is None else scale, window,
+                                flags, _ptr(o), _ptr(lse), ws.ptr(), ws.nbytes, _stream(q.device)))
+    return o, lse
+
+
+def kv_evict(cache: KVCache, page_table, kv_len, budget: int, recent: int = 0, sink: int = 0, seq_len=None, ws=None,
+             out=None):
+    """dflash2_kv_evict.  Every head keeps `budget` slots of a request that has more: those of the `recent` newest and
+    `sink` first positions, then the most attended.  Returns min(kv_len, budget) [B] int32."""
+    L = load_library()
+    B = kv_len.shape[0]
+    _page_table(page_table, B)
+    _int32(B, kv_len=kv_len, seq_len=seq_len)
+    if ws is None:
+        ws = Workspace.for_kv_evict(B, cache.Hkv, page_table.shape[1] * cache.page_size, budget, kv_len.device)
+    if out is None:
+        out = torch.empty_like(kv_len)
+    _check("dflash2_kv_evict",
+           L.dflash2_kv_evict(cache._ref, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(seq_len), B,
+                              budget, recent, sink, _ptr(out), ws.ptr(), ws.nbytes, _stream(kv_len.device)))
+    return out
 
 
 def device_error(clear: bool = False) -> int:

@@ -1,0 +1,493 @@
+// kvcache.cu -- dflash2_rope_append and dflash2_kv_evict: what writes to the
+// paged cache.
+#include "common.cuh"
+#include "host.hpp"
+
+namespace dfl {
+
+bool kv_cache_ok(const dflash2_kv_cache *c, const int32_t *table, int32_t max_pages);
+
+// ------------------------------------------------------------------ append --
+struct AppendArgs {
+    char *ck, *cv;
+    float *weight;
+    int32_t *pos;
+    int64_t num_pages, page_stride, head_stride, slot_stride;
+    int Hkv, page_size, d;
+    const int32_t *table;
+    int max_pages;
+    const int32_t *kv_len, *q_len, *seq_pos;
+    const char *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t tokens;  // B * T
+    int T, Hq;
+    const float *cos_sin;
+    int64_t n_pos;
+    int rot;
+    const int32_t *pos_ids;
+    int axes;
+    const uint8_t *pair_axis;
+    const void *q_norm, *k_norm;
+    float eps;
+    void *q_out;
+    int32_t *kv_len_out;
+    int head_steps;  // heads a thread takes: head, head + head_steps, ..
+};
+
+// Where a new token goes.
+struct AppendToken {
+    bool live;     // t < q_len
+    int64_t slot;  // index (page * Hkv * page_size + off) parts:
+    int page, off;
+    int seq;
+};
+
+__device__ __forceinline__ AppendToken append_token(const AppendArgs &a, int64_t tok, bool lead) {
+    AppendToken r;
+    const int64_t b = tok / a.T;
+    const int t = static_cast<int>(tok - b * a.T);
+    const int n = a.kv_len[b];
+    int nq = a.q_len ? a.q_len[b] : a.T;
+    nq = nq < 0 ? 0 : (nq > a.T ? a.T : nq);
+    r.live = t < nq;
+    r.slot = static_cast<int64_t>(n) + t;
+    r.page = -1;
+    r.off = 0;
+    if (n >= 0) {
+        const int64_t pi = r.slot / a.page_size;
+        if (pi < a.max_pages) {
+            const int page = a.table[b * a.max_pages + pi];
+            if (page >= 0 && page < a.num_pages) r.page = page;
+            r.off = static_cast<int>(r.slot - pi * a.page_size);
+        }
+    }
+    r.seq = (a.seq_pos ? a.seq_pos[b] : n) + t;
+    if (lead && t == 0 && a.kv_len_out) a.kv_len_out[b] = n + nq;
+    return r;
+}
+
+template <typename E>
+__device__ __forceinline__ float ld1(const void *p, int64_t i);
+template <>
+__device__ __forceinline__ float ld1<float>(const void *p, int64_t i) {
+    return static_cast<const float *>(p)[i];
+}
+template <>
+__device__ __forceinline__ float ld1<unsigned short>(const void *p, int64_t i) {
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const unsigned short *>(p)[i]) << 16);
+}
+__device__ __forceinline__ void st1(float *p, int64_t i, float v) { p[i] = v; }
+__device__ __forceinline__ void st1(unsigned short *p, int64_t i, float v) {
+    unsigned short o;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(o) : "f"(v));
+    p[i] = o;
+}
+
+// Any d and rot: one warp per (token, head), a pair of entries per step.
+template <typename E, bool INTER>
+__global__ void __launch_bounds__(256) k_append_any(AppendArgs a) {
+    pdl_wait();
+    const int heads = a.Hq + 2 * a.Hkv, lane = threadIdx.x & 31, half = a.rot / 2;
+    const int64_t units = a.tokens * heads, step = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += step) {
+        const int64_t tok = u / heads;
+        const int head = static_cast<int>(u - tok * heads);
+        const AppendToken at = append_token(a, tok, head == 0 && lane == 0);
+        const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hkv;
+        const int kh = is_q ? 0 : (is_v ? head - a.Hq - a.Hkv : head - a.Hq);
+        const E *src;
+        E *dst;
+        if (is_q) {
+            src = reinterpret_cast<const E *>(a.q) + tok * a.q_stride + static_cast<int64_t>(head) * a.d;
+            dst = static_cast<E *>(a.q_out) + (tok * a.Hq + head) * a.d;
+            if (!at.live || at.page < 0) {
+                for (int i = lane; i < a.d; i += 32) st1(dst, i, at.live ? NAN : 0.f);
+                continue;
+            }
+        } else {
+            if (!at.live || at.page < 0) continue;
+            src = is_v ? reinterpret_cast<const E *>(a.v) + tok * a.v_stride + static_cast<int64_t>(kh) * a.d
+                       : reinterpret_cast<const E *>(a.k) + tok * a.k_stride + static_cast<int64_t>(kh) * a.d;
+            dst = reinterpret_cast<E *>(is_v ? a.cv : a.ck) + at.page * a.page_stride + kh * a.head_stride +
+                  at.off * a.slot_stride;
+        }
+        if (is_v) {
+            for (int i = lane; i < a.d; i += 32) dst[i] = src[i];
+            continue;
+        }
+        if (!is_q && lane == 0) {
+            const int64_t si = (static_cast<int64_t>(at.page) * a.Hkv + kh) * a.page_size + at.off;
+            if (a.weight) a.weight[si] = 0.f;
+            if (a.pos) a.pos[si] = at.seq;
+        }
+        const void *nw = is_q ? a.q_norm : a.k_norm;
+        float f = 1.f;
+        if (nw) {
+            float ss = 0.f;
+            for (int i = lane; i < a.d; i += 32) {
+                const float x = ld1<E>(src, i);
+                ss = fmaf(x, x, ss);
+            }
+            f = 1.0f / sqrtf(warp_sum(ss) / a.d + a.eps);
+        }
+        for (int p = lane; p < half; p += 32) {
+            const int i = INTER ? 2 * p : p, j = INTER ? 2 * p + 1 : p + half;
+            int ax = a.pair_axis ? a.pair_axis[p] : 0;
+            ax = ax < a.axes ? ax : a.axes - 1;
+            const int id = a.pos_ids[ax * a.tokens + tok];
+            float cs = NAN, sn = NAN;
+            if (id >= 0 && id < a.n_pos) {
+                cs = a.cos_sin[static_cast<int64_t>(id) * a.rot + p];
+                sn = a.cos_sin[static_cast<int64_t>(id) * a.rot + half + p];
+            }
+            float x = ld1<E>(src, i), y = ld1<E>(src, j);
+            if (nw) {
+                x = x * f * ld1<E>(nw, i);
+                y = y * f * ld1<E>(nw, j);
+            }
+            st1(dst, i, fmaf(x, cs, -y * sn));
+            st1(dst, j, fmaf(y, cs, x * sn));
+        }
+        for (int i = a.rot + lane; i < a.d; i += 32) {
+            float x = ld1<E>(src, i);
+            if (nw) x = x * f * ld1<E>(nw, i);
+            st1(dst, i, x);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- evict --
+struct EvictArgs {
+    char *ck, *cv;
+    float *weight;
+    int32_t *pos;
+    int64_t num_pages, page_bytes, head_bytes, slot_bytes;  // strides in bytes
+    int Hkv, page_size, row_bytes;
+    const int32_t *table;
+    int max_pages;
+    const int32_t *kv_len, *seq_len;
+    int budget, recent, sink;
+    int32_t *kv_len_out;
+    int *count;     // [B * Hkv]
+    int2 *moves;    // [B * Hkv][max_moves]: (from, to) slots
+    int64_t max_moves;
+};
+
+constexpr int EV_THREADS = 1024;
+
+__device__ __forceinline__ int evict_page(const EvictArgs &a, int64_t b, int slot) {
+    const int page = a.table[b * a.max_pages + slot / a.page_size];
+    return page >= 0 && page < a.num_pages ? page : -1;
+}
+
+// The rank of a slot among its head's: larger stays.  Protected slots above
+// every weight, NaN below, a slot without a page last.
+__device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, int64_t b, int h, int slot, int64_t newest) {
+    const int page = evict_page(a, b, slot);
+    if (page < 0) return 0u;
+    const int64_t i = (static_cast<int64_t>(page) * a.Hkv + h) * a.page_size + slot % a.page_size;
+    const int p = a.pos[i];
+    if (p >= newest - a.recent || p < a.sink) return 0xffffffffu;
+    const float w = a.weight[i];
+    if (w != w) return 1u;
+    return f2ord(w == 0.f ? 0.f : w);
+}
+
+// One CTA per (request, head): the budget-th largest key by four passes of a
+// radix select (8 bits each), then the kept slots in slot order by ballots.
+__global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
+    __shared__ int hist[256];
+    __shared__ int s_warp[3][32];
+    __shared__ uint32_t s_prefix;
+    __shared__ int s_left;
+    pdl_wait();
+    const int64_t b = blockIdx.x / a.Hkv;
+    const int h = static_cast<int>(blockIdx.x % a.Hkv);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
+    const int64_t n64 = a.kv_len[b] < cap ? a.kv_len[b] : cap;
+    const int n = static_cast<int>(n64);
+    if (n <= a.budget) {
+        if (tid == 0) a.count[blockIdx.x] = 0;
+        return;
+    }
+    const int64_t newest = a.seq_len ? a.seq_len[b] : n64;
+    if (tid == 0) {
+        s_prefix = 0;
+        s_left = a.budget;
+    }
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        const uint32_t prefix = s_prefix;
+        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+        for (int s = tid; s < n; s += EV_THREADS) {
+            const uint32_t k = evict_key(a, b, h, s, newest);
+            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // from the largest digit down: the one in which the s_left-th key lies
+            int mine[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                mine[i] = hist[255 - (lane * 8 + i)];
+                sum += mine[i];
+            }
+            int inc = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(FULL, inc, d);
+                if (lane >= d) inc += o;
+            }
+            int before = inc - sum;
+            const int left = s_left;
+            __syncwarp();
+            if (before < left && left <= inc) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (before < left && left <= before + mine[i]) {
+                        s_prefix = prefix | (static_cast<uint32_t>(255 - (lane * 8 + i)) << shift);
+                        s_left = left - before;
+                    }
+                    before += mine[i];
+                }
+            }
+        }
+        __syncthreads();
+    }
+    const uint32_t T = s_prefix;
+    const int ties = s_left;  // of the keys equal to T, the first `ties` slots stay
+    // each warp takes a stretch of slots
+    const int per = ((n + 31) / 32 + 31) / 32 * 32, s0 = warp * per, s1 = s0 + per < n ? s0 + per : n;
+    int eq = 0;
+    for (int s = s0; s < s1; s += 32) {
+        const bool in = s + lane < n;
+        eq += __popc(__ballot_sync(FULL, in && evict_key(a, b, h, in ? s + lane : 0, newest) == T));
+    }
+    if (lane == 0) s_warp[0][warp] = eq;
+    __syncthreads();
+    int eq_before = 0;
+    for (int w = 0; w < warp; ++w) eq_before += s_warp[0][w];
+    for (int pass = 0; pass < 2; ++pass) {
+        int holes = 0, movers = 0, seen = eq_before;
+        if (pass == 1)
+            for (int w = 0; w < warp; ++w) {
+                holes += s_warp[1][w];
+                movers += s_warp[2][w];
+            }
+        for (int s = s0; s < s1; s += 32) {
+            const int slot = s + lane;
+            const bool in = slot < n;
+            const uint32_t k = evict_key(a, b, h, in ? slot : 0, newest);
+            const unsigned tie = __ballot_sync(FULL, in && k == T);
+            const unsigned below = (1u << lane) - 1u;
+            const bool kept = in && (k > T || (k == T && seen + __popc(tie & below) < ties));
+            seen += __popc(tie);
+            const bool hole = in && !kept && slot < a.budget, mover = kept && slot >= a.budget;
+            const unsigned bh = __ballot_sync(FULL, hole), bm = __ballot_sync(FULL, mover);
+            if (pass == 1) {
+                int2 *m = a.moves + static_cast<int64_t>(blockIdx.x) * a.max_moves;
+                if (hole) m[holes + __popc(bh & below)].y = slot;
+                if (mover) m[movers + __popc(bm & below)].x = slot;
+            }
+            holes += __popc(bh);
+            movers += __popc(bm);
+        }
+        if (pass == 0) {
+            if (lane == 0) {
+                s_warp[1][warp] = holes;
+                s_warp[2][warp] = movers;
+            }
+            __syncthreads();
+        } else if (warp == 31 && lane == 0) {
+            a.count[blockIdx.x] = holes;
+        }
+    }
+}
+
+// The moves of every (request, head): a warp per move, 16 bytes per lane.
+__global__ void __launch_bounds__(256) k_evict_move(EvictArgs a) {
+    pdl_wait();
+    const int64_t b = blockIdx.x / a.Hkv;
+    const int h = static_cast<int>(blockIdx.x % a.Hkv);
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
+        const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
+        const int64_t n = a.kv_len[b] < cap ? a.kv_len[b] : cap;
+        a.kv_len_out[b] = static_cast<int>(n < 0 ? 0 : (n < a.budget ? n : a.budget));
+    }
+    const int count = a.count[blockIdx.x];
+    const int2 *m = a.moves + static_cast<int64_t>(blockIdx.x) * a.max_moves;
+    const int vecs = a.row_bytes / 16;
+    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < count; i += gridDim.y * 8) {
+        const int2 mv = m[i];
+        const int ps = evict_page(a, b, mv.x), pd = evict_page(a, b, mv.y);
+        if (ps < 0 || pd < 0) continue;
+        const int os = mv.x % a.page_size, od = mv.y % a.page_size;
+        const int64_t from = ps * a.page_bytes + h * a.head_bytes + os * a.slot_bytes;
+        const int64_t to = pd * a.page_bytes + h * a.head_bytes + od * a.slot_bytes;
+        for (int j = lane; j < 2 * vecs; j += 32) {
+            char *base = j < vecs ? a.ck : a.cv;
+            const int64_t o = static_cast<int64_t>(j < vecs ? j : j - vecs) * 16;
+            *reinterpret_cast<uint4 *>(base + to + o) = *reinterpret_cast<const uint4 *>(base + from + o);
+        }
+        if (lane == 0) {
+            const int64_t is = (static_cast<int64_t>(ps) * a.Hkv + h) * a.page_size + os;
+            const int64_t id = (static_cast<int64_t>(pd) * a.Hkv + h) * a.page_size + od;
+            a.weight[id] = a.weight[is];
+            a.pos[id] = a.pos[is];
+        }
+    }
+}
+
+template <typename A>
+static dflash2_status launch_pdl(void (*fn)(A), const A &a, dim3 grid, int threads, size_t smem, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) return DFLASH2_ERR_CUDA;
+    return after_launch();
+}
+
+static int64_t evict_max_moves(int64_t capacity, int32_t budget) {
+    const int64_t over = capacity > budget ? capacity - budget : 0;
+    return over < budget ? over : budget;
+}
+static size_t evict_count_bytes(int64_t B, int32_t Hkv) {
+    return (static_cast<size_t>(B) * Hkv * sizeof(int) + 255) / 256 * 256;
+}
+
+}  // namespace dfl
+
+using namespace dfl;
+
+static bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t *page_table,
+                                              int32_t max_pages, const int32_t *kv_len, const int32_t *q_len,
+                                              const int32_t *seq_pos, const void *q, const void *k, const void *v,
+                                              int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t B,
+                                              int32_t T, int32_t Hq, const float *cos_sin, int64_t n_pos, int32_t rot,
+                                              const int32_t *pos_ids, int32_t axes, const uint8_t *pair_axis,
+                                              int32_t interleaved, const void *q_norm, const void *k_norm, float eps,
+                                              void *q_out, int32_t *kv_len_out, dflash2_stream stream) {
+    if (!kv_cache_ok(cache, page_table, max_pages) || B < 0 || T < 0 || Hq < 1 || rot < 2 || rot % 2 != 0 ||
+        rot > cache->d || axes < 1 || n_pos < 1)
+        return DFLASH2_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return DFLASH2_OK;
+    const int e = esize(cache->dt);
+    const int64_t d = cache->d;
+    if (!q || !k || !v || !q_out || !kv_len || !cos_sin || !pos_ids || !aligned16(q) || !aligned16(k) ||
+        !aligned16(v) || !aligned16(q_out) || !aligned16(q_norm) || !aligned16(k_norm) || !aligned16(cos_sin) ||
+        !al4(kv_len) || !al4(q_len) || !al4(seq_pos) || !al4(pos_ids) || !al4(kv_len_out) || q_stride < Hq * d ||
+        k_stride < cache->Hkv * d || v_stride < cache->Hkv * d || q_stride * e % 16 || k_stride * e % 16 ||
+        v_stride * e % 16)
+        return DFLASH2_ERR_INVALID_ARG;
+    if (d > 1024 || B * T >= (int64_t(1) << 31)) return DFLASH2_ERR_UNSUPPORTED;
+    AppendArgs a = {};
+    a.ck = static_cast<char *>(cache->k);
+    a.cv = static_cast<char *>(cache->v);
+    a.weight = cache->weight;
+    a.pos = cache->pos;
+    a.num_pages = cache->num_pages;
+    a.page_stride = cache->page_stride;
+    a.head_stride = cache->head_stride;
+    a.slot_stride = cache->slot_stride;
+    a.Hkv = cache->Hkv;
+    a.page_size = cache->page_size;
+    a.d = cache->d;
+    a.table = page_table;
+    a.max_pages = max_pages;
+    a.kv_len = kv_len;
+    a.q_len = q_len;
+    a.seq_pos = seq_pos;
+    a.q = static_cast<const char *>(q);
+    a.k = static_cast<const char *>(k);
+    a.v = static_cast<const char *>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.tokens = B * T;
+    a.T = T;
+    a.Hq = Hq;
+    a.cos_sin = cos_sin;
+    a.n_pos = n_pos;
+    a.rot = rot;
+    a.pos_ids = pos_ids;
+    a.axes = axes;
+    a.pair_axis = axes > 1 ? pair_axis : nullptr;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.eps = eps;
+    a.q_out = q_out;
+    a.kv_len_out = kv_len_out;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t units = a.tokens * (Hq + 2 * cache->Hkv);
+    const int64_t blocks = (units + 7) / 8, most = static_cast<int64_t>(sm_count()) * 64;
+    const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
+    if (cache->dt == DFLASH2_BF16)
+        return interleaved ? launch_pdl(k_append_any<unsigned short, true>, a, grid, 256, 0, s)
+                           : launch_pdl(k_append_any<unsigned short, false>, a, grid, 256, 0, s);
+    return interleaved ? launch_pdl(k_append_any<float, true>, a, grid, 256, 0, s)
+                       : launch_pdl(k_append_any<float, false>, a, grid, 256, 0, s);
+}
+
+extern "C" size_t dflash2_kv_evict_workspace_bytes(int64_t B, int32_t Hkv, int64_t capacity, int32_t budget) {
+    if (B < 0 || Hkv < 1 || capacity < 0 || budget < 1) return 0;
+    return evict_count_bytes(B, Hkv) +
+           static_cast<size_t>(B) * Hkv * evict_max_moves(capacity, budget) * sizeof(int2);
+}
+
+extern "C" dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const int32_t *page_table,
+                                           int32_t max_pages, const int32_t *kv_len, const int32_t *seq_len, int64_t B,
+                                           int32_t budget, int32_t recent, int32_t sink, int32_t *kv_len_out, void *ws,
+                                           size_t ws_bytes, dflash2_stream stream) {
+    if (!kv_cache_ok(cache, page_table, max_pages) || !cache->weight || !cache->pos || B < 0 || budget < 1 ||
+        recent < 0 || sink < 0)
+        return DFLASH2_ERR_INVALID_ARG;
+    if (B == 0) return DFLASH2_OK;
+    if (!kv_len || !kv_len_out || !ws || !aligned16(ws) || !al4(kv_len) || !al4(kv_len_out) || !al4(seq_len))
+        return DFLASH2_ERR_INVALID_ARG;
+    const int64_t cap = static_cast<int64_t>(max_pages) * cache->page_size;
+    if (cap >= (int64_t(1) << 31) - 2048 || B * cache->Hkv >= (int64_t(1) << 31)) return DFLASH2_ERR_UNSUPPORTED;
+    if (ws_bytes < dflash2_kv_evict_workspace_bytes(B, cache->Hkv, cap, budget)) return DFLASH2_ERR_WORKSPACE;
+    const int e = esize(cache->dt);
+    EvictArgs a = {};
+    a.ck = static_cast<char *>(cache->k);
+    a.cv = static_cast<char *>(cache->v);
+    a.weight = cache->weight;
+    a.pos = cache->pos;
+    a.num_pages = cache->num_pages;
+    a.page_bytes = cache->page_stride * e;
+    a.head_bytes = cache->head_stride * e;
+    a.slot_bytes = cache->slot_stride * e;
+    a.Hkv = cache->Hkv;
+    a.page_size = cache->page_size;
+    a.row_bytes = cache->d * e;
+    a.table = page_table;
+    a.max_pages = max_pages;
+    a.kv_len = kv_len;
+    a.seq_len = seq_len;
+    a.budget = budget;
+    a.recent = recent;
+    a.sink = sink;
+    a.kv_len_out = kv_len_out;
+    a.count = static_cast<int *>(ws);
+    a.moves = reinterpret_cast<int2 *>(static_cast<char *>(ws) + evict_count_bytes(B, cache->Hkv));
+    a.max_moves = evict_max_moves(cap, budget);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t heads = B * cache->Hkv;
+    dflash2_status st = launch_pdl(k_evict_select, a, dim3(static_cast<unsigned>(heads)), EV_THREADS, 0, s);
+    if (st != DFLASH2_OK) return st;
+    int64_t x = (a.max_moves + 7) / 8;
+    const int64_t want = (static_cast<int64_t>(sm_count()) * 8 + heads - 1) / heads;
+    if (x > want) x = want;
+    if (x < 1) x = 1;
+    return launch_pdl(k_evict_move, a, dim3(static_cast<unsigned>(heads), static_cast<unsigned>(x)), 256, 0, s);
+}

@@ -370,6 +370,170 @@ dflash2_status dflash2_dynconv2tap(const void *x, const void *x_prev, const void
                                    int64_t B, int32_t T, int64_t H, int32_t group_size, float *taps, void *y,
                                    dflash2_stream stream);
 
+/*
+ * ------------------------------------------------- the paged cache path ----
+ *
+ * The attention that the drafter and the target run around this library's
+ * selection and verify, on a paged key-value cache: dflash2_rope_append puts
+ * a block's new keys and values into the cache, dflash2_paged_attn lets the
+ * block's queries attend to it, dflash2_kv_evict keeps a cache within a
+ * budget.  No counterpart on the pages beyond the shapes: blocks of K + 1
+ * tokens per request, causal in a verify and seen both ways in a drafter's
+ * block ([P] "What upstream shipped"), a drafter's cache bounded by a window
+ * of 2048 positions ([F] Details).  Additions of this library.
+ *
+ * The cache is a pool of pages.  Slot s of request b lies in page
+ * page_table[b, s / page_size] at offset s % page_size; slots 0 .. n - 1 are
+ * in use.  Element (page, head, offset, c) of k and of v is at
+ *   page * page_stride + head * head_stride + offset * slot_stride + c
+ * (in elements), so both [num_pages, Hkv, page_size, d] and
+ * [num_pages, page_size, Hkv, d] pools are taken.  Optional side arrays, both
+ * contiguous [num_pages, Hkv, page_size]: `weight`, the attention weight each
+ * cached key has received so far, and `pos`, the position of the key in its
+ * sequence (after an eviction a slot's number no longer is; without the array
+ * slot s holds position s).  A page may belong to several requests as long as
+ * no call writes to it (append, weights, evict).
+ *
+ * Page table entries outside [0, num_pages) and tables that are too short
+ * never lead to an access outside the pool: see each call.
+ *
+ * Common errors of the three calls: INVALID_ARG for a NULL cache, k, v or
+ * page_table; num_pages, Hkv, page_size, d or max_pages < 1; k, v, the
+ * strides or d * elem size not multiples of 16 bytes; slot_stride < d,
+ * head_stride or page_stride < 0; side arrays, page_table or per-request
+ * arrays not 4-byte aligned; B or T < 0.
+ */
+typedef struct {
+    void *k;              /* device, of dt */
+    void *v;              /* device, of dt, laid out as k */
+    float *weight;        /* device [num_pages, Hkv, page_size] or NULL */
+    int32_t *pos;         /* device [num_pages, Hkv, page_size] or NULL */
+    int64_t num_pages;
+    int64_t page_stride;  /* elements */
+    int64_t head_stride;
+    int64_t slot_stride;
+    int32_t Hkv;
+    int32_t page_size;
+    int32_t d;            /* head dimension */
+    dflash2_dtype dt;
+} dflash2_kv_cache;
+
+/*
+ * dflash2_rope_append -- rotary positions on one or several axes, and the
+ * append to the cache, in one pass over a block's new tokens.
+ *
+ * For new token t < q_len[b] of request b, with x the query or key head:
+ *   y = x / sqrt(mean(x^2) + eps) * w       (q_norm / k_norm given; else y = x)
+ *   (y_i, y_j) -> (y_i cos - y_j sin, y_j cos + y_i sin)   for each pair of
+ * the first rot entries: pair p is (p, p + rot / 2), or (2p, 2p + 1) with
+ * interleaved != 0; the others stay.  cos and sin come from row
+ * pos_ids[pair_axis[p], b, t] of the table, columns p and rot / 2 + p (the
+ * table is made once, in as many bits as the caller likes, so a position of
+ * any size is exact).  All arithmetic in fp32, one rounding to dt at the end.
+ * Rotated queries go to q_out, keys and values to slot kv_len[b] + t, the
+ * slot's weight is set to 0 and its position to seq_pos[b] + t.
+ *
+ * q [B, T, Hq, d], k and v [B, T, Hkv, d] of the cache's dt; heads contiguous,
+ *   q_stride, k_stride, v_stride elements from one token to the next (slices
+ *   of one fused projection are taken as they are).
+ * kv_len [B]: slots in use before the call.  q_len [B] or NULL (all T);
+ *   clamped to 0 .. T; queries of tokens t >= q_len[b] come out 0 and their
+ *   keys are not stored.  seq_pos [B] or NULL (kv_len).
+ * cos_sin [n_pos, rot] f32.  pos_ids [axes, B, T].  pair_axis [rot / 2] or
+ *   NULL (axis 0); values above axes - 1 count as axes - 1.
+ * q_norm, k_norm [d] of dt, or NULL.
+ * q_out [B, T, Hq, d], contiguous.  kv_len_out [B] or NULL: kv_len + q_len;
+ *   must not overlap kv_len.
+ * A token whose position id is outside [0, n_pos) gets NaN in the rotated
+ * entries of its query and key.  A token whose slot has no valid page (past
+ * the table, or a page id out of range) is not stored and its query comes
+ * out NaN.
+ * Errors: the common ones; INVALID_ARG for NULL q, k, v, q_out, kv_len,
+ * cos_sin or pos_ids; Hq < 1, rot odd, < 2 or > d, axes < 1, n_pos < 1, strides
+ * below the width of a token's heads or not multiples of 16 bytes; dt not
+ * F32 or BF16.  UNSUPPORTED for d > 1024 or B * T >= 2^31.
+ */
+dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t *page_table, int32_t max_pages,
+                                   const int32_t *kv_len, const int32_t *q_len, const int32_t *seq_pos,
+                                   const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, int64_t B, int32_t T, int32_t Hq, const float *cos_sin,
+                                   int64_t n_pos, int32_t rot, const int32_t *pos_ids, int32_t axes,
+                                   const uint8_t *pair_axis, int32_t interleaved, const void *q_norm,
+                                   const void *k_norm, float eps, void *q_out, int32_t *kv_len_out,
+                                   dflash2_stream stream);
+
+/*
+ * dflash2_paged_attn -- attention of a block of T new tokens per request over
+ * the request's paged cache (the new tokens' own slots are in it).
+ *
+ * Query head h of token t reads the cached head h / (Hq / Hkv).  It sees slot
+ * s < kv_len[b] at position P(s) (the cache's `pos`, or s) if
+ *   P(s) <= seq_pos[b] + t            (with DFLASH2_ATTN_CAUSAL), and
+ *   P(s) >  seq_pos[b] + t - window   (with window > 0).
+ * Over the slots it sees, with x_s = scale * <q, k_s>:
+ *   lse = log sum_s exp(x_s),  p_s = exp(x_s - lse),  out = sum_s p_s v_s.
+ * With DFLASH2_ATTN_WEIGHTS every cached key's `weight` grows by the sum of
+ * its p_s over the block's tokens and the query heads that share it.
+ * A row that sees nothing (or sees only x_s = -inf) gets out 0, lse -inf and
+ * adds no weight; tokens t >= q_len[b] are such rows.  What lies in slots
+ * that a row does not see (NaN and Inf too) does not touch it.
+ *
+ * q, out [B, T, Hq, d] of dt, contiguous; lse [B, T, Hq] f32 (may be NULL
+ *   without DFLASH2_ATTN_WEIGHTS).
+ * kv_len [B]: slots in use, the new tokens among them; clamped to what the
+ *   table can hold.  q_len [B] or NULL (all T).  seq_pos [B]: the position
+ *   of the block's first token, or NULL (kv_len - q_len).
+ * Slots whose page id is out of range are seen by no row.
+ * Scores, softmax statistics and sums are fp32.  The cache's length is split
+ * over the GPU and the parts are joined in a fixed order: the same call gives
+ * the same bits.
+ * ws: dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, dt) bytes.
+ * Errors: the common ones; INVALID_ARG for NULL q, out or kv_len, lse or the
+ * cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a positive multiple of
+ * Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
+ * small; UNSUPPORTED for d > 256, Hq / Hkv > 128, num_pages >= 2^31 or
+ * max_pages * page_size >= 2^31 - 256.
+ */
+enum { DFLASH2_ATTN_CAUSAL = 1, DFLASH2_ATTN_WEIGHTS = 2 };
+size_t dflash2_paged_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
+                                          dflash2_dtype dt);
+dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, const int32_t *page_table, int32_t max_pages,
+                                  const int32_t *kv_len, const int32_t *q_len, const int32_t *seq_pos, const void *q,
+                                  int64_t B, int32_t T, int32_t Hq, float scale, int32_t window, uint32_t flags,
+                                  void *out, float *lse, void *ws, size_t ws_bytes, dflash2_stream stream);
+
+/*
+ * dflash2_kv_evict -- eviction by accumulated attention weight.
+ *
+ * A request with n = kv_len[b] <= budget slots is left alone.  Of any other,
+ * every head keeps `budget` of its n slots on its own: first those at
+ * positions >= seq_len[b] - recent or < sink, then the others in the order of
+ * their weight, largest first (NaN counts as the smallest; equal weights: the
+ * lower slot first).
+ * Kept slots below `budget` stay where they are; kept slots from `budget` on
+ * move, in order, to the evicted slots below `budget`, in order, with their
+ * key, value, weight and position.  So the least is moved, and slots are in
+ * no order of position afterwards (`pos` says which is which).  Slots from
+ * `budget` on keep what was in them; the caller may release their pages.
+ *
+ * kv_len [B]: slots in use (clamped to what the table holds).  seq_len [B]:
+ *   the length of the sequence (the newest key's position + 1), or NULL
+ *   (kv_len).  kv_len_out [B]: min(kv_len, budget); may be kv_len itself.
+ * A slot whose page id is out of range is never kept before another one and
+ * never copied.
+ * If more than `budget` slots are protected, the lower slots stay.
+ * ws: dflash2_kv_evict_workspace_bytes(B, Hkv, max_pages * page_size, budget)
+ *   bytes.
+ * Errors: the common ones; INVALID_ARG for the cache's weight or pos NULL,
+ * NULL kv_len or kv_len_out, budget < 1, recent < 0 or sink < 0; WORKSPACE;
+ * UNSUPPORTED for max_pages * page_size >= 2^31 - 2048 or B * Hkv >= 2^31.
+ */
+size_t dflash2_kv_evict_workspace_bytes(int64_t B, int32_t Hkv, int64_t capacity, int32_t budget);
+dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const int32_t *page_table, int32_t max_pages,
+                                const int32_t *kv_len, const int32_t *seq_len, int64_t B, int32_t budget,
+                                int32_t recent, int32_t sink, int32_t *kv_len_out, void *ws, size_t ws_bytes,
+                                dflash2_stream stream);
+
 /* Human-readable name of a status code (static string). */
 const char *dflash2_status_string(dflash2_status s);
 
