@@ -1,12 +1,19 @@
-// attn.cu -- dflash2_paged_attn: the entry point and the CUDA-core kernels.
+// attn.cu -- dflash2_paged_attn: the entry point, and the CUDA-core kernels
+// that take float32 caches and the head dimensions the tensor-core kernels
+// (attn_tc.cu) do not.
 //
 //   x_s = scale <q, k_s>,  out = sum_s exp(x_s) v_s / sum_s exp(x_s)
 // in one pass over the cache: a row keeps its running maximum m and sum l,
 // and what it has summed so far is multiplied by exp(m - m') when the maximum
 // grows to m'.  Everything is fp32; exponentials are taken in base 2.
 #include "attn.cuh"
+#include "tc.cuh"
 
 namespace dfl {
+
+// The tensor-core kernels (attn_tc.cu).
+bool attn_tc_takes(const AttnArgs &a);
+dflash2_status attn_tc_launch(AttnArgs a, cudaStream_t s);
 
 constexpr int SIMT_THREADS = 256;
 constexpr int SIMT_KEYS = 32;  // keys per tile: one per lane in the score step
@@ -375,6 +382,6 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
         st = launch_simt<float>(a, s);
         return st == DFLASH2_OK && weights ? launch_weights_simt<float>(a, s) : st;
     }
-    st = launch_simt<unsigned short>(a, s);
+    st = attn_tc_takes(a) ? attn_tc_launch(a, s) : launch_simt<unsigned short>(a, s);
     return st == DFLASH2_OK && weights ? launch_weights_simt<unsigned short>(a, s) : st;
 }
