@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdflash2.so")
-SOURCES = ["topk16.cu", "verify.cu", "walk.cu", "gate.cu", "lmhead.cu", "conv.cu", "attn.cu", "attn_tc.cu", "kvcache.cu", "api.cu"]
+SOURCES = ["topk16.cu", "verify.cu", "walk.cu", "gate.cu", "lmhead.cu", "conv.cu", "attn.cu", "attn_tc.cu",
+           "attn_tc64.cu", "attn_tc128.cu", "attn_tc256.cu", "kvcache.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

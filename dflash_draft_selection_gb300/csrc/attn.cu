@@ -16,7 +16,7 @@ bool attn_tc_takes(const AttnArgs &a);
 dflash2_status attn_tc_launch(AttnArgs a, cudaStream_t s);
 
 constexpr int SIMT_THREADS = 256;
-constexpr int SIMT_KEYS = 32;  // keys per tile: one per lane in the score step
+constexpr int SIMT_KEYS_LOG2 = 5, SIMT_KEYS = 32;  // keys per tile: one per lane in the score step
 constexpr int SIMT_ROWS = 16;  // query rows per block: two per warp in the score step
 
 template <typename E>
@@ -81,9 +81,9 @@ static __device__ __forceinline__ void cta_sync() { __syncthreads(); }
 template <typename E>
 __global__ void __launch_bounds__(SIMT_THREADS) k_attn_simt(AttnArgs a) {
     extern __shared__ float smem[];
-    __shared__ int64_t scratch[SIMT_THREADS / 32 + 2];
+    __shared__ int scratch[SIMT_THREADS / 32 + 2];
     __shared__ int s_page[SIMT_KEYS], s_lo[SIMT_KEYS], s_hi[SIMT_KEYS], s_flag;
-    __shared__ float s_p[SIMT_ROWS][SIMT_KEYS], s_f[SIMT_ROWS];
+    __shared__ float s_p[SIMT_ROWS][SIMT_KEYS], s_f[SIMT_ROWS], s_inv[128];
     const int d = a.d, ld = d + 4, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *sq = smem, *sk = sq + SIMT_ROWS * ld, *sv = sk + SIMT_KEYS * ld;
     pdl_wait();
@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_attn_simt(AttnArgs a) {
                 }
             }
         }
-        if (!w.whole) attn_join<E>(a, w, rows, h, tok0, SIMT_THREADS, tid, &s_flag, cta_sync);
+        if (!w.whole)
+            attn_join<E>(a, p, w, rows, h, tok0, SIMT_THREADS, tid, &s_flag, smem, SIMT_KEYS * ld, s_inv, cta_sync);
     }
 }
 
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_attn_simt(AttnArgs a) {
 template <typename E>
 __global__ void __launch_bounds__(SIMT_THREADS) k_weights_simt(AttnArgs a) {
     extern __shared__ float smem[];
-    __shared__ int64_t scratch[SIMT_THREADS / 32 + 2];
+    __shared__ int scratch[SIMT_THREADS / 32 + 2];
     __shared__ int s_page[SIMT_KEYS], s_lo[SIMT_KEYS], s_hi[SIMT_KEYS];
     __shared__ float s_w[8][SIMT_KEYS];
     const int d = a.d, ld = d + 4, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -274,7 +275,7 @@ static int64_t simt_grid(const AttnArgs &a, const void *fn) {
     const int64_t per = blocks_per_sm(fn, SIMT_THREADS, simt_smem(256));
     const int64_t slots = static_cast<int64_t>(sm_count()) * (per < 3 ? per : 3);
     const int64_t most = slots < ATTN_MAX_CTAS ? slots : ATTN_MAX_CTAS;
-    const int64_t cap = (static_cast<int64_t>(a.max_pages) * a.page_size + a.tile - 1) / a.tile;
+    const int64_t cap = (static_cast<int64_t>(a.max_pages) * a.page_size + SIMT_KEYS - 1) / SIMT_KEYS;
     const double t = static_cast<double>(a.B) * a.items * cap;
     return t < most ? static_cast<int64_t>(t) : most;
 }
@@ -282,7 +283,7 @@ static int64_t simt_grid(const AttnArgs &a, const void *fn) {
 template <typename E>
 static dflash2_status launch_simt(AttnArgs a, cudaStream_t s) {
     void *fn = reinterpret_cast<void *>(&k_attn_simt<E>);
-    a.tile = SIMT_KEYS;
+    a.tile_log2 = SIMT_KEYS_LOG2;
     a.tok_block = SIMT_ROWS / a.group > 0 ? SIMT_ROWS / a.group : 1;
     if (a.tok_block > a.T) a.tok_block = a.T;
     a.row_blocks = (a.T + a.tok_block - 1) / a.tok_block;
@@ -294,7 +295,7 @@ static dflash2_status launch_simt(AttnArgs a, cudaStream_t s) {
 template <typename E>
 static dflash2_status launch_weights_simt(AttnArgs a, cudaStream_t s) {
     void *fn = reinterpret_cast<void *>(&k_weights_simt<E>);
-    a.tile = SIMT_KEYS;
+    a.tile_log2 = SIMT_KEYS_LOG2;
     a.items = a.Hkv;
     return launch_simple(fn, a, SIMT_THREADS, simt_smem(a.d), simt_grid(a, fn), s);
 }
@@ -344,6 +345,10 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
     const int group = Hq / cache->Hkv;
     if (cache->d > 256 || group > 128 || cache->num_pages >= (int64_t(1) << 31) ||
         static_cast<int64_t>(max_pages) * cache->page_size >= (int64_t(1) << 31) - 256)
+        return DFLASH2_ERR_UNSUPPORTED;
+    // the tiles of a call are counted in 31 bits (32 keys and one token at the least)
+    if (static_cast<double>(B) * cache->Hkv * T * (static_cast<double>(max_pages) * cache->page_size / SIMT_KEYS + 1) >=
+        2147483648.0)
         return DFLASH2_ERR_UNSUPPORTED;
     if (ws_bytes < dflash2_paged_attn_workspace_bytes(B, T, Hq, cache->Hkv, cache->d, cache->dt))
         return DFLASH2_ERR_WORKSPACE;

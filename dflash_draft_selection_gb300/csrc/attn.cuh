@@ -34,13 +34,14 @@ struct AttnArgs {
     int window, causal;
     void *out;
     float *lse;
-    int tile;        // keys per tile
+    int tile_log2;   // keys per tile
     int tok_block;   // tokens of a row block (tok_block * group rows)
     int row_blocks;  // row blocks per request
     int items;       // items per request: Hkv * row_blocks (weights pass: Hkv)
     int rows_cap;    // rows of a part in the workspace
     int *tickets;    // [gridDim.x], zero between calls
     float *parts;    // [2 * gridDim.x][attn_part_floats(rows_cap, d)]
+    unsigned int *err;  // the library's error word of these kernels
 };
 
 // Floats of a part: O [rows][d], m [rows], l [rows], padded to 16 bytes.
@@ -51,7 +52,8 @@ __host__ __device__ __forceinline__ int64_t attn_part_floats(int rows, int d) {
 constexpr int ATTN_MAX_CTAS = 1024;
 constexpr size_t ATTN_TICKET_BYTES = ATTN_MAX_CTAS * sizeof(int);
 
-// One request as the call sees it.
+// One request as the call sees it.  (Slots, and the tiles of a call, are
+// below 2^31: checked by the caller.)
 struct AttnReq {
     int n;        // slots that may be seen
     int nq;       // tokens
@@ -60,95 +62,107 @@ struct AttnReq {
     int nt;       // tiles from there (at least one: its rows are written even if nothing is seen)
 };
 
-__device__ __forceinline__ AttnReq attn_req(const AttnArgs &a, int64_t b) {
+__device__ __forceinline__ AttnReq attn_req(const AttnArgs &a, int b) {
     AttnReq r;
-    const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
-    int64_t n = a.kv_len[b];
-    n = n < 0 ? 0 : (n > cap ? cap : n);
-    int nq = a.q_len ? a.q_len[b] : a.T;
-    nq = nq < 0 ? 0 : (nq > a.T ? a.T : nq);
+    int n = a.kv_len[b], nq = a.q_len ? a.q_len[b] : a.T;
+    const int sp = a.seq_pos ? a.seq_pos[b] : 0;
+    n = min(max(n, 0), a.max_pages * a.page_size);
+    nq = min(max(nq, 0), a.T);
     r.nq = nq;
-    r.q0 = a.seq_pos ? a.seq_pos[b] : n - nq;
-    int64_t lo = 0;
+    r.q0 = a.seq_pos ? sp : n - nq;
+    int lo = 0;
     if (!a.pos) {  // slot = position: the slots outside every token's view are not visited
-        if (a.causal) n = min(n, max(r.q0 + nq, static_cast<int64_t>(0)));
-        if (a.window > 0) lo = max(r.q0 - a.window + 1, static_cast<int64_t>(0));
+        if (a.causal) n = static_cast<int>(min(static_cast<int64_t>(n), max(r.q0 + nq, static_cast<int64_t>(0))));
+        if (a.window > 0)
+            lo = static_cast<int>(min(static_cast<int64_t>(n), max(r.q0 - a.window + 1, static_cast<int64_t>(0))));
     }
     if (nq == 0) n = 0;
-    r.n = static_cast<int>(n);
-    const int last = static_cast<int>((n + a.tile - 1) / a.tile);
-    r.first = static_cast<int>(min(lo / a.tile, static_cast<int64_t>(last > 0 ? last - 1 : 0)));
-    r.nt = last > r.first ? last - r.first : 1;
+    r.n = n;
+    const int last = (n + (1 << a.tile_log2) - 1) >> a.tile_log2;
+    r.first = min(lo >> a.tile_log2, max(last - 1, 0));
+    r.nt = max(last - r.first, 1);
     return r;
 }
 
 // This CTA's stretch [begin, end) of the line and the request that holds its
-// start (`base`: the line's tiles before that request).  All threads call it.
+// start (`base`: the line's tiles before that request).
 struct AttnPlan {
-    int64_t total, begin, end, base, b;
-    int ctas;  // the CTAs that have a stretch: no more than there are tiles, so that no stretch is empty
+    int total, begin, end, base, b;
+    int ctas;   // the CTAs that have a stretch: no more than there are tiles, so that no stretch is empty
+    int q, rem; // tiles of a stretch: q, and one more in the first rem
+    __device__ __forceinline__ int at(int cta) const { return q * cta + min(cta, rem); }
+    // The CTA whose stretch holds tile x.
+    __device__ __forceinline__ int owner(int x) const {
+        const int cut = rem * (q + 1);
+        return x < cut ? x / (q + 1) : rem + (x - cut) / q;
+    }
 };
 
-__device__ __forceinline__ int64_t attn_begin(int64_t total, int cta, int ctas) { return total * cta / ctas; }
-// The CTA whose stretch holds tile x.
-__device__ __forceinline__ int attn_owner(int64_t total, int64_t x, int ctas) {
-    return static_cast<int>(((x + 1) * ctas - 1) / total);
-}
-
+// All threads call it.
 template <int THREADS>
-__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int64_t *scratch /* [THREADS / 32 + 2] */) {
+__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /* [THREADS / 32 + 2] */) {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int B = static_cast<int>(a.B);
     AttnPlan p;
-    int64_t sum = 0, mine = 0;
-    for (int64_t b = tid; b < a.B; b += THREADS) {
-        mine = static_cast<int64_t>(attn_req(a, b).nt) * a.items;
+    int sum = 0, mine = 0;
+    for (int b = tid; b < B; b += THREADS) {
+        mine = attn_req(a, b).nt * a.items;
         sum += mine;
     }
+    if (B == 1) {  // the only request's tiles, known to thread 0
+        if (tid == 0) scratch[0] = mine;
+        __syncthreads();
+        p.total = scratch[0];
+    } else {
+        sum = __reduce_add_sync(FULL, sum);
+        if (lane == 0) scratch[warp] = sum;
+        __syncthreads();
+        p.total = 0;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
-    if (lane == 0) scratch[warp] = sum;
-    __syncthreads();
-    p.total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) p.total += scratch[w];
-    __syncthreads();
-    p.ctas = static_cast<int>(min(p.total, static_cast<int64_t>(gridDim.x)));
+        for (int w = 0; w < W; ++w) p.total += scratch[w];
+    }
+    p.ctas = min(p.total, static_cast<int>(gridDim.x));
+    p.q = p.total / p.ctas;
+    p.rem = p.total - p.q * p.ctas;
     p.b = 0;
     p.base = 0;
     p.begin = p.end = 0;
-    if (blockIdx.x >= p.ctas) return p;
-    p.begin = attn_begin(p.total, blockIdx.x, p.ctas);
-    p.end = attn_begin(p.total, blockIdx.x + 1, p.ctas);
+    if (static_cast<int>(blockIdx.x) >= p.ctas) return p;
+    p.begin = p.at(blockIdx.x);
+    p.end = p.at(blockIdx.x + 1);
+    if (B == 1) return p;
     // find the request that holds `begin`
-    int64_t carry = 0;
-    for (int64_t at = 0; at < a.B; at += THREADS) {
-        const int64_t b = at + tid;
-        const int64_t v = b < a.B ? (a.B <= THREADS ? mine : static_cast<int64_t>(attn_req(a, b).nt) * a.items) : 0;
-        int64_t inc = v;
+    __syncthreads();
+    int carry = 0;
+    for (int at = 0; at < B; at += THREADS) {
+        const int b = at + tid;
+        const int v = b < B ? (B <= THREADS ? mine : attn_req(a, b).nt * a.items) : 0;
+        int inc = v;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(FULL, inc, d);
+            const int o = __shfl_up_sync(FULL, inc, d);
             if (lane >= d) inc += o;
         }
         if (lane == 31) scratch[warp] = inc;
         __syncthreads();
-        int64_t before = carry;
-        for (int w = 0; w < warp; ++w) before += scratch[w];
-        int64_t all = 0;
+        int before = carry, all = 0;
 #pragma unroll
-        for (int w = 0; w < W; ++w) all += scratch[w];
-        const int64_t lo = before + inc - v;
-        __syncthreads();
-        if (v > 0 && lo <= p.begin && p.begin < lo + v) {
+        for (int w = 0; w < W; ++w) {
+            const int x = scratch[w];
+            if (w < warp) before += x;
+            all += x;
+        }
+        const int lo = before + inc - v;
+        if (v > 0 && lo <= p.begin && p.begin - lo < v) {
             scratch[W] = b;
             scratch[W + 1] = lo;
         }
-        const bool here = p.begin < carry + all;
+        const bool here = p.begin - carry < all;
         carry += all;
+        __syncthreads();
         if (here) break;
     }
-    __syncthreads();
     p.b = scratch[W];
     p.base = scratch[W + 1];
     return p;
@@ -157,8 +171,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int64_t *scratc
 // Walks the items of a stretch.
 struct AttnWalk {
     AttnReq r;
-    int64_t b, base, at, end, total;
-    int ctas;
+    int b, base, at, end;
     int item;     // within the request
     int t0, t1;   // this stretch's tiles of the item (absolute: the first key is t0 * tile)
     bool whole;   // the stretch holds all of the item's tiles
@@ -169,34 +182,31 @@ struct AttnWalk {
         base = p.base;
         at = p.begin;
         end = p.end;
-        total = p.total;
-        ctas = p.ctas;
         r = attn_req(a, b);
     }
     // The next item; false at the end of the stretch.
     __device__ __forceinline__ bool next(const AttnArgs &a) {
         if (at >= end) return false;
-        while (at >= base + static_cast<int64_t>(r.nt) * a.items) {
-            base += static_cast<int64_t>(r.nt) * a.items;
+        while (at - base >= r.nt * a.items) {
+            base += r.nt * a.items;
             ++b;
             r = attn_req(a, b);
         }
-        item = static_cast<int>((at - base) / r.nt);
-        const int64_t first = base + static_cast<int64_t>(item) * r.nt;
-        const int64_t last = min(first + r.nt, end);
-        t0 = r.first + static_cast<int>(at - first);
-        t1 = r.first + static_cast<int>(last - first);
+        item = (at - base) / r.nt;
+        const int first = base + item * r.nt, last = min(first + r.nt, end);
+        t0 = r.first + at - first;
+        t1 = r.first + last - first;
         starts = at == first;
         whole = starts && last == first + r.nt;
         at = last;
         return true;
     }
-    __device__ __forceinline__ int64_t item_base() const { return base + static_cast<int64_t>(item) * r.nt; }
+    __device__ __forceinline__ int item_base() const { return base + item * r.nt; }
 };
 
 // The page of a slot, or -1.
-__device__ __forceinline__ int attn_page(const AttnArgs &a, int64_t b, int slot) {
-    const int page = a.table[b * a.max_pages + slot / a.page_size];
+__device__ __forceinline__ int attn_page(const AttnArgs &a, int b, int slot) {
+    const int page = a.table[static_cast<int64_t>(b) * a.max_pages + slot / a.page_size];
     return static_cast<unsigned>(page) < static_cast<unsigned long long>(a.num_pages) ? page : -1;
 }
 
@@ -212,7 +222,7 @@ __device__ __forceinline__ void attn_view(const AttnArgs &a, const AttnReq &r, i
 
 // ... for slot s of the request in cached head h (nothing is seen of a slot
 // past the request's or without a page).
-__device__ __forceinline__ void attn_view_slot(const AttnArgs &a, const AttnReq &r, int64_t b, int h, int s, int &lo,
+__device__ __forceinline__ void attn_view_slot(const AttnArgs &a, const AttnReq &r, int b, int h, int s, int &lo,
                                                int &hi, int &page) {
     lo = hi = 0;
     page = -1;
@@ -225,8 +235,8 @@ __device__ __forceinline__ void attn_view_slot(const AttnArgs &a, const AttnReq 
 }
 
 // Query row r of a row block: token tok0 + r / group, head h * group + r % group.
-__device__ __forceinline__ int64_t attn_row(const AttnArgs &a, int64_t b, int h, int tok0, int r) {
-    return (b * a.T + tok0 + r / a.group) * a.Hq + static_cast<int64_t>(h) * a.group + r % a.group;
+__device__ __forceinline__ int64_t attn_row(const AttnArgs &a, int b, int h, int tok0, int r) {
+    return (static_cast<int64_t>(b) * a.T + tok0 + r / a.group) * a.Hq + static_cast<int64_t>(h) * a.group + r % a.group;
 }
 
 __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t i, float v, float *) {
@@ -238,76 +248,136 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t i, float v
     static_cast<unsigned short *>(a.out)[i] = o;
 }
 
+__device__ __forceinline__ void attn_store4(const AttnArgs &a, int64_t i, float x, float y, float z, float w, float *) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = make_float4(x, y, z, w);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void attn_store4(const AttnArgs &a, int64_t i, float x, float y, float z, float w,
+                                            unsigned short *) {
+    *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(a.out) + i) = make_uint2(pack_bf16(x, y), pack_bf16(z, w));
+}
+
 __device__ __forceinline__ float *attn_part(const AttnArgs &a, int cta, bool starts) {
     return a.parts + (static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * attn_part_floats(a.rows_cap, a.d);
 }
 
+// The join's sum over the parts: U vectors of four entries per thread and K
+// parts at a time, all their loads in flight together.
+template <typename E, int U, int K>
+__device__ __forceinline__ void attn_join_sum(const AttnArgs &a, const AttnWalk &w, int h, int tok0, int rows, int real,
+                                              int n, const float *base, int64_t step, bool fits, const float *scratch,
+                                              const float *inv, int threads, int tid) {
+    const int d4 = a.d / 4, total = rows * d4;
+    for (int i0 = tid; i0 < total; i0 += U * threads) {
+        float4 o[U];
+        int r[U], c[U];
+        float g[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * threads, total - 1);
+            r[u] = i / d4;
+            c[u] = (i - r[u] * d4) * 4;
+            g[u] = r[u] < real ? inv[r[u]] : 0.f;
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int k0 = 0; k0 < n; k0 += K) {
+            float4 x[U * K];
+            float f[U * K];
+#pragma unroll
+            for (int v = 0; v < U * K; ++v) {
+                const int u = v % U, k = k0 + v / U;
+                f[v] = 0.f;
+                x[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (g[u] != 0.f && k < n) {
+                    const float *q = base + (k == 0 ? 0 : 2 * k - 1) * step;
+                    x[v] = __ldcg(reinterpret_cast<const float4 *>(q + r[u] * a.d + c[u]));
+                    if (fits)
+                        f[v] = scratch[r[u] * n + k];
+                    else if (__ldcg(q + a.rows_cap * (a.d + 1) + r[u]) != 0.f)
+                        f[v] = ex2(__ldcg(q + a.rows_cap * a.d + r[u]) - scratch[r[u]]);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < U * K; ++v) {
+                const int u = v % U;
+                if (f[v] == 0.f) continue;
+                o[u].x = fmaf(x[v].x, f[v], o[u].x);
+                o[u].y = fmaf(x[v].y, f[v], o[u].y);
+                o[u].z = fmaf(x[v].z, f[v], o[u].z);
+                o[u].w = fmaf(x[v].w, f[v], o[u].w);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * threads < total) {
+                const int64_t at = attn_row(a, w.b, h, tok0, r[u]) * a.d + c[u];
+                attn_store4(a, at, o[u].x * g[u], o[u].y * g[u], o[u].z * g[u], o[u].w * g[u],
+                            static_cast<E *>(nullptr));
+            }
+    }
+}
+
 // After this CTA's part of a cut item is written: take the item's ticket, and
-// if every other part is there, join them (all threads call it; E is the
-// output's element type).  Part layout: O [rows][d], m [rows], l [rows], m in
-// units of log2.
-constexpr int JOIN_BATCH = 8;
+// if every other part is there, join them in order (all `threads` threads call
+// it; E is the output's element type).  m is in units of log2.  `scratch`
+// (`cap` floats) holds a weight 2^(m - M) per row and part; where it is too
+// small the weights are taken again from the parts.
 template <typename E, typename Sync>
-__device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnWalk &w, int rows, int h, int tok0, int nthreads,
-                                          int tid, int *flag /* shared */, Sync sync) {
-    const int64_t first = w.item_base();
-    const int c0 = attn_owner(w.total, first, w.ctas);
-    const int c1 = attn_owner(w.total, first + w.r.nt - 1, w.ctas);
+__device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnPlan &p, const AttnWalk &w, int rows, int h,
+                                          int tok0, int threads, int tid, int *flag /* shared */, float *scratch,
+                                          int cap, float *inv /* shared, [rows] */, Sync sync) {
+    const int first = w.item_base();
+    const int c0 = p.owner(first), n = p.owner(first + w.r.nt - 1) - c0 + 1;
     __threadfence();
     sync();
     if (tid == 0) {
         const int old = atomic_add_acq_rel(&a.tickets[c0], 1);
-        *flag = old == c1 - c0;
-        if (old == c1 - c0) a.tickets[c0] = 0;
+        *flag = old == n - 1;
+        if (old == n - 1) a.tickets[c0] = 0;
     }
     sync();
-    const bool last = *flag != 0;
-    if (!last) return;
+    if (!*flag) return;
     __threadfence();
     const int64_t step = attn_part_floats(a.rows_cap, a.d);
     const int real = min(rows, max(w.r.nq - tok0, 0) * a.group);
-    // the parts in order: c0's second slot, then the first slots of c0 + 1 .. c1
-    auto part = [&](int c) { return a.parts + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * step; };
-    const int d4 = a.d / 4;
-    for (int i = tid; i < rows * d4; i += nthreads) {
-        const int r = i / d4, c4 = i % d4;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // part k of the item: c0's second slot, then the first slots of c0 + 1 ..
+    const float *base = a.parts + (static_cast<int64_t>(c0) * 2 + 1) * step;
+    auto part = [&](int k) { return base + (k == 0 ? 0 : 2 * k - 1) * step; };
+    const bool fits = rows * n <= cap;
+    // a row's weights: `per` neighbouring lanes share it
+    int per = 32;
+    while (per > 1 && rows * per > threads) per >>= 1;
+    for (int r0 = 0; r0 < rows; r0 += threads / per) {
+        const int r = r0 + tid / per, lane = tid % per;
         float M = NEG_INF, L = 0.f;
-        if (r < real) {
-            for (int c = c0; c <= c1; c += JOIN_BATCH) {  // a batch's loads are in flight together
-                float m[JOIN_BATCH], l[JOIN_BATCH];
-                float4 x[JOIN_BATCH];
-#pragma unroll
-                for (int k = 0; k < JOIN_BATCH; ++k) {
-                    const float *p = part(min(c + k, c1));
-                    m[k] = __ldcg(p + a.rows_cap * a.d + r);
-                    l[k] = c + k <= c1 ? __ldcg(p + a.rows_cap * (a.d + 1) + r) : 0.f;
-                    x[k] = __ldcg(reinterpret_cast<const float4 *>(p + static_cast<int64_t>(r) * a.d) + c4);
-                }
-#pragma unroll
-                for (int k = 0; k < JOIN_BATCH; ++k) {
-                    if (l[k] == 0.f) continue;  // the part saw nothing (a NaN sum is taken along)
-                    const float nm = fmax_nan(M, m[k]);
-                    const float wo = M == NEG_INF ? 0.f : ex2(M - nm), wn = ex2(m[k] - nm);
-                    o.x = o.x * wo + x[k].x * wn;
-                    o.y = o.y * wo + x[k].y * wn;
-                    o.z = o.z * wo + x[k].z * wn;
-                    o.w = o.w * wo + x[k].w * wn;
-                    L = L * wo + l[k] * wn;
-                    M = nm;
-                }
+        if (r < real)
+            for (int k = lane; k < n; k += per) M = fmax_nan(M, __ldcg(part(k) + a.rows_cap * a.d + r));
+        for (int d = per >> 1; d >= 1; d >>= 1) M = fmax_nan(M, __shfl_xor_sync(FULL, M, d));
+        if (r < real)
+            for (int k = lane; k < n; k += per) {
+                const float l = __ldcg(part(k) + a.rows_cap * (a.d + 1) + r);
+                // a part that saw nothing has l = 0 (and a sum that is NaN is taken along)
+                const float f = l == 0.f ? 0.f : ex2(__ldcg(part(k) + a.rows_cap * a.d + r) - M);
+                L += l * f;
+                if (fits) scratch[r * n + k] = f;
             }
+        for (int d = per >> 1; d >= 1; d >>= 1) L += __shfl_xor_sync(FULL, L, d);
+        if (r < rows && lane == 0) {
+            inv[r] = L == 0.f ? 0.f : 1.0f / L;
+            if (!fits && r < real) scratch[r] = M;
+            if (a.lse) a.lse[attn_row(a, w.b, h, tok0, r)] = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
         }
-        const float inv = L == 0.f ? 0.f : 1.0f / L;
-        const int64_t row = attn_row(a, w.b, h, tok0, r);
-        const int64_t at = row * a.d + c4 * 4;
-        attn_store(a, at, o.x * inv, static_cast<E *>(nullptr));
-        attn_store(a, at + 1, o.y * inv, static_cast<E *>(nullptr));
-        attn_store(a, at + 2, o.z * inv, static_cast<E *>(nullptr));
-        attn_store(a, at + 3, o.w * inv, static_cast<E *>(nullptr));
-        if (c4 == 0 && a.lse) a.lse[row] = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
     }
+    sync();
+    const int total = rows * (a.d / 4);
+    if (total <= threads)
+        attn_join_sum<E, 1, 8>(a, w, h, tok0, rows, real, n, base, step, fits, scratch, inv, threads, tid);
+    else
+        attn_join_sum<E, 4, 2>(a, w, h, tok0, rows, real, n, base, step, fits, scratch, inv, threads, tid);
 }
-
 
 }  // namespace dfl
