@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_attn_simt(AttnArgs a) {
     __shared__ int scratch[SIMT_THREADS / 32 + 2];
     __shared__ int s_page[SIMT_KEYS], s_lo[SIMT_KEYS], s_hi[SIMT_KEYS], s_flag;
     __shared__ float s_p[SIMT_ROWS][SIMT_KEYS], s_f[SIMT_ROWS], s_inv[128];
+    __shared__ int64_t s_row[128];
     const int d = a.d, ld = d + 4, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float *sq = smem, *sk = sq + SIMT_ROWS * ld, *sv = sk + SIMT_KEYS * ld;
     pdl_wait();
@@ -195,8 +196,10 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_attn_simt(AttnArgs a) {
                 }
             }
         }
-        if (!w.whole)
-            attn_join<E>(a, p, w, rows, h, tok0, SIMT_THREADS, tid, &s_flag, smem, SIMT_KEYS * ld, s_inv, cta_sync);
+        if (!w.whole) {
+            if (tid < rows) s_row[tid] = attn_row(a, w.b, h, tok0, tid);
+            attn_join<E, 0>(a, AttnParts(a, p, w), w, rows, tok0, SIMT_THREADS, tid, &s_flag, smem, SIMT_KEYS * ld, s_inv, s_row, cta_sync);
+        }
     }
 }
 
@@ -346,8 +349,8 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
     if (cache->d > 256 || group > 128 || cache->num_pages >= (int64_t(1) << 31) ||
         static_cast<int64_t>(max_pages) * cache->page_size >= (int64_t(1) << 31) - 256)
         return DFLASH2_ERR_UNSUPPORTED;
-    // the tiles of a call are counted in 31 bits (32 keys and one token at the least)
-    if (static_cast<double>(B) * cache->Hkv * T * (static_cast<double>(max_pages) * cache->page_size / SIMT_KEYS + 1) >=
+    // the places of a call's line are counted in 31 bits (32 keys and one token at the least)
+    if (static_cast<double>(B) * cache->Hkv * T * (static_cast<double>(max_pages) * cache->page_size / SIMT_KEYS + 4) >=
         2147483648.0)
         return DFLASH2_ERR_UNSUPPORTED;
     if (ws_bytes < dflash2_paged_attn_workspace_bytes(B, T, Hq, cache->Hkv, cache->d, cache->dt))

@@ -38,6 +38,7 @@ struct AttnArgs {
     int tok_block;   // tokens of a row block (tok_block * group rows)
     int row_blocks;  // row blocks per request
     int items;       // items per request: Hkv * row_blocks (weights pass: Hkv)
+    int item_cost;   // what an item costs beside its tiles, in tiles
     int rows_cap;    // rows of a part in the workspace
     int *tickets;    // [gridDim.x], zero between calls
     float *parts;    // [2 * gridDim.x][attn_part_floats(rows_cap, d)]
@@ -85,13 +86,13 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs &a, int b) {
 }
 
 // This CTA's stretch [begin, end) of the line and the request that holds its
-// start (`base`: the line's tiles before that request).
+// start (`base`: the line's places before that request).
 struct AttnPlan {
     int total, begin, end, base, b;
-    int ctas;   // the CTAs that have a stretch: no more than there are tiles, so that no stretch is empty
-    int q, rem; // tiles of a stretch: q, and one more in the first rem
+    int ctas;   // the CTAs that have a stretch: no more than there are places, so that no stretch is empty
+    int q, rem; // places of a stretch: q, and one more in the first rem
     __device__ __forceinline__ int at(int cta) const { return q * cta + min(cta, rem); }
-    // The CTA whose stretch holds tile x.
+    // The CTA whose stretch holds place x.
     __device__ __forceinline__ int owner(int x) const {
         const int cut = rem * (q + 1);
         return x < cut ? x / (q + 1) : rem + (x - cut) / q;
@@ -107,7 +108,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /*
     AttnPlan p;
     int sum = 0, mine = 0;
     for (int b = tid; b < B; b += THREADS) {
-        mine = attn_req(a, b).nt * a.items;
+        mine = (attn_req(a, b).nt + a.item_cost) * a.items;
         sum += mine;
     }
     if (B == 1) {  // the only request's tiles, known to thread 0
@@ -137,7 +138,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /*
     int carry = 0;
     for (int at = 0; at < B; at += THREADS) {
         const int b = at + tid;
-        const int v = b < B ? (B <= THREADS ? mine : attn_req(a, b).nt * a.items) : 0;
+        const int v = b < B ? (B <= THREADS ? mine : (attn_req(a, b).nt + a.item_cost) * a.items) : 0;
         int inc = v;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -184,24 +185,32 @@ struct AttnWalk {
         end = p.end;
         r = attn_req(a, b);
     }
-    // The next item; false at the end of the stretch.
+    // The next item that has tiles here; false at the end of the stretch.
     __device__ __forceinline__ bool next(const AttnArgs &a) {
-        if (at >= end) return false;
-        while (at - base >= r.nt * a.items) {
-            base += r.nt * a.items;
-            ++b;
-            r = attn_req(a, b);
+        while (at < end) {
+            int len = r.nt + a.item_cost;
+            while (at - base >= len * a.items) {
+                base += len * a.items;
+                ++b;
+                r = attn_req(a, b);
+                len = r.nt + a.item_cost;
+            }
+            item = (at - base) / len;
+            const int first = base + item * len, from = at - first - a.item_cost;  // in tiles of the item
+            const int last = min(len, end - first), to = last - a.item_cost;
+            at = first + last;
+            t0 = r.first + max(from, 0);
+            t1 = r.first + to;
+            starts = from <= 0;
+            whole = starts && to == r.nt;
+            if (t0 < t1) return true;
         }
-        item = (at - base) / r.nt;
-        const int first = base + item * r.nt, last = min(first + r.nt, end);
-        t0 = r.first + at - first;
-        t1 = r.first + last - first;
-        starts = at == first;
-        whole = starts && last == first + r.nt;
-        at = last;
-        return true;
+        return false;
     }
-    __device__ __forceinline__ int item_base() const { return base + item * r.nt; }
+    // The place of the item's first tile.
+    __device__ __forceinline__ int item_base(const AttnArgs &a) const {
+        return base + item * (r.nt + a.item_cost) + a.item_cost;
+    }
 };
 
 // The page of a slot, or -1.
@@ -266,118 +275,154 @@ __device__ __forceinline__ float *attn_part(const AttnArgs &a, int cta, bool sta
 }
 
 // The join's sum over the parts: U vectors of four entries per thread and K
-// parts at a time, all their loads in flight together.
-template <typename E, int U, int K>
-__device__ __forceinline__ void attn_join_sum(const AttnArgs &a, const AttnWalk &w, int h, int tok0, int rows, int real,
-                                              int n, const float *base, int64_t step, bool fits, const float *scratch,
-                                              const float *inv, int threads, int tid) {
-    const int d4 = a.d / 4, total = rows * d4;
+// parts at a time, all their loads in flight together.  D: the head dimension
+// (0: a.d).
+template <typename E, int D, bool FITS, int U, int K>
+__device__ __forceinline__ void attn_join_sum(const AttnArgs &a, int rows, int real, int n, const float *base,
+                                              int64_t step, const float *scratch, const float *inv,
+                                              const int64_t *row_at, int threads, int tid) {
+    const int d = D ? D : a.d, d4 = d / 4, total = rows * d4;
+#pragma unroll 1
     for (int i0 = tid; i0 < total; i0 += U * threads) {
         float4 o[U];
-        int r[U], c[U];
-        float g[U];
+        int r[U], at[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = min(i0 + u * threads, total - 1);
             r[u] = i / d4;
-            c[u] = (i - r[u] * d4) * 4;
-            g[u] = r[u] < real ? inv[r[u]] : 0.f;
+            at[u] = i * 4;
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+#pragma unroll 1
         for (int k0 = 0; k0 < n; k0 += K) {
             float4 x[U * K];
-            float f[U * K];
 #pragma unroll
             for (int v = 0; v < U * K; ++v) {
-                const int u = v % U, k = k0 + v / U;
-                f[v] = 0.f;
-                x[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (g[u] != 0.f && k < n) {
-                    const float *q = base + (k == 0 ? 0 : 2 * k - 1) * step;
-                    x[v] = __ldcg(reinterpret_cast<const float4 *>(q + r[u] * a.d + c[u]));
-                    if (fits)
-                        f[v] = scratch[r[u] * n + k];
-                    else if (__ldcg(q + a.rows_cap * (a.d + 1) + r[u]) != 0.f)
-                        f[v] = ex2(__ldcg(q + a.rows_cap * a.d + r[u]) - scratch[r[u]]);
-                }
+                const int k = min(k0 + v / U, n - 1);
+                x[v] = __ldcg(reinterpret_cast<const float4 *>(base + (k == 0 ? 0 : 2 * k - 1) * step + at[v % U]));
             }
 #pragma unroll
             for (int v = 0; v < U * K; ++v) {
-                const int u = v % U;
-                if (f[v] == 0.f) continue;
-                o[u].x = fmaf(x[v].x, f[v], o[u].x);
-                o[u].y = fmaf(x[v].y, f[v], o[u].y);
-                o[u].z = fmaf(x[v].z, f[v], o[u].z);
-                o[u].w = fmaf(x[v].w, f[v], o[u].w);
+                const int u = v % U, k = k0 + v / U;
+                float f = 0.f;
+                if (k < n && r[u] < real) {
+                    if (FITS)
+                        f = scratch[r[u] * n + k];
+                    else
+                        f = ex2(__ldcg(base + (k == 0 ? 0 : 2 * k - 1) * step + a.rows_cap * d + r[u]) - scratch[r[u]]);
+                }
+                if (f == 0.f) continue;
+                o[u].x = fmaf(x[v].x, f, o[u].x);
+                o[u].y = fmaf(x[v].y, f, o[u].y);
+                o[u].z = fmaf(x[v].z, f, o[u].z);
+                o[u].w = fmaf(x[v].w, f, o[u].w);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i0 + u * threads < total) {
-                const int64_t at = attn_row(a, w.b, h, tok0, r[u]) * a.d + c[u];
-                attn_store4(a, at, o[u].x * g[u], o[u].y * g[u], o[u].z * g[u], o[u].w * g[u],
+                const float g = inv[r[u]];
+                attn_store4(a, row_at[r[u]] * d + (at[u] - r[u] * d), g == 0.f ? 0.f : o[u].x * g,
+                            g == 0.f ? 0.f : o[u].y * g, g == 0.f ? 0.f : o[u].z * g, g == 0.f ? 0.f : o[u].w * g,
                             static_cast<E *>(nullptr));
             }
     }
 }
 
+// The parts of a cut item: n of them, the first from CTA c0; part k's place in
+// the workspace (c0's second slot, then the first slots of c0 + 1 ..).
+struct AttnParts {
+    int c0, n;
+    int64_t step;
+    const float *base;
+    __device__ __forceinline__ AttnParts(const AttnArgs &a, const AttnPlan &p, const AttnWalk &w) {
+        const int first = w.item_base(a);
+        c0 = p.owner(first);
+        n = p.owner(first + w.r.nt - 1) - c0 + 1;
+        step = attn_part_floats(a.rows_cap, a.d);
+        base = a.parts + (static_cast<int64_t>(c0) * 2 + 1) * step;
+    }
+    __device__ __forceinline__ const float *at(int k) const { return base + (k == 0 ? 0 : 2 * k - 1) * step; }
+};
+
+// Row r's weights over the parts: f_k = 2^(m_k - M) (0 for a part that saw
+// nothing), their sum with the parts' sums, 1 / L in `inv`, and the row's lse.
+// Part `own` (or none, -1) is this CTA's: its m and l are given.  The f_k go
+// to scratch[k], or M alone if they do not fit.  Every sum over parts runs in
+// their order, so the result is the same whoever takes it.
+__device__ __forceinline__ float attn_join_row(const AttnArgs &a, const AttnParts &q, int r, bool seen, int own,
+                                               float own_m, float own_l, bool fits, float *scratch, float *lse) {
+    constexpr int K = 4;
+    float M = NEG_INF, L = 0.f;
+    if (seen) {
+        const int64_t om = static_cast<int64_t>(a.rows_cap) * a.d + r;
+        for (int k0 = 0; k0 < q.n; k0 += K) {
+            float m[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) m[k] = __ldcg(q.at(min(k0 + k, q.n - 1)) + om);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k0 + k < q.n) M = fmax_nan(M, k0 + k == own ? own_m : m[k]);
+        }
+        for (int k0 = 0; k0 < q.n; k0 += K) {
+            float m[K], l[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                m[k] = __ldcg(q.at(min(k0 + k, q.n - 1)) + om);
+                l[k] = __ldcg(q.at(min(k0 + k, q.n - 1)) + om + a.rows_cap);
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (k0 + k >= q.n) continue;
+                const float mk = k0 + k == own ? own_m : m[k], lk = k0 + k == own ? own_l : l[k];
+                // a part that saw nothing has l = 0 (and a sum that is NaN is taken along)
+                const float f = lk == 0.f ? 0.f : ex2(mk - M);
+                L = fmaf(lk, f, L);
+                if (fits) scratch[k0 + k] = f;
+            }
+        }
+        if (!fits) scratch[0] = M;
+    } else if (fits) {
+        for (int k = 0; k < q.n; ++k) scratch[k] = 0.f;
+    }
+    *lse = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
+    return L == 0.f ? 0.f : 1.0f / L;
+}
+
 // After this CTA's part of a cut item is written: take the item's ticket, and
-// if every other part is there, join them in order (all `threads` threads call
-// it; E is the output's element type).  m is in units of log2.  `scratch`
-// (`cap` floats) holds a weight 2^(m - M) per row and part; where it is too
-// small the weights are taken again from the parts.
-template <typename E, typename Sync>
-__device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnPlan &p, const AttnWalk &w, int rows, int h,
-                                          int tok0, int threads, int tid, int *flag /* shared */, float *scratch,
-                                          int cap, float *inv /* shared, [rows] */, Sync sync) {
-    const int first = w.item_base();
-    const int c0 = p.owner(first), n = p.owner(first + w.r.nt - 1) - c0 + 1;
+// if every other part is there, join them (all `threads` threads call it; E is
+// the output's element type, D the head dimension or 0).  `scratch` (`cap`
+// floats) holds the rows' weights; row_at: the rows' indexes in lse.
+template <typename E, int D, typename Sync>
+__device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnParts &q, const AttnWalk &w, int rows, int tok0,
+                                          int threads, int tid, int *flag /* shared */, float *scratch, int cap,
+                                          float *inv /* shared, [rows] */, const int64_t *row_at /* shared */,
+                                          Sync sync) {
     __threadfence();
     sync();
     if (tid == 0) {
-        const int old = atomic_add_acq_rel(&a.tickets[c0], 1);
-        *flag = old == n - 1;
-        if (old == n - 1) a.tickets[c0] = 0;
+        const int old = atomic_add_acq_rel(&a.tickets[q.c0], 1);
+        *flag = old == q.n - 1;
+        if (old == q.n - 1) a.tickets[q.c0] = 0;
     }
     sync();
     if (!*flag) return;
     __threadfence();
-    const int64_t step = attn_part_floats(a.rows_cap, a.d);
     const int real = min(rows, max(w.r.nq - tok0, 0) * a.group);
-    // part k of the item: c0's second slot, then the first slots of c0 + 1 ..
-    const float *base = a.parts + (static_cast<int64_t>(c0) * 2 + 1) * step;
-    auto part = [&](int k) { return base + (k == 0 ? 0 : 2 * k - 1) * step; };
-    const bool fits = rows * n <= cap;
-    // a row's weights: `per` neighbouring lanes share it
-    int per = 32;
-    while (per > 1 && rows * per > threads) per >>= 1;
-    for (int r0 = 0; r0 < rows; r0 += threads / per) {
-        const int r = r0 + tid / per, lane = tid % per;
-        float M = NEG_INF, L = 0.f;
-        if (r < real)
-            for (int k = lane; k < n; k += per) M = fmax_nan(M, __ldcg(part(k) + a.rows_cap * a.d + r));
-        for (int d = per >> 1; d >= 1; d >>= 1) M = fmax_nan(M, __shfl_xor_sync(FULL, M, d));
-        if (r < real)
-            for (int k = lane; k < n; k += per) {
-                const float l = __ldcg(part(k) + a.rows_cap * (a.d + 1) + r);
-                // a part that saw nothing has l = 0 (and a sum that is NaN is taken along)
-                const float f = l == 0.f ? 0.f : ex2(__ldcg(part(k) + a.rows_cap * a.d + r) - M);
-                L += l * f;
-                if (fits) scratch[r * n + k] = f;
-            }
-        for (int d = per >> 1; d >= 1; d >>= 1) L += __shfl_xor_sync(FULL, L, d);
-        if (r < rows && lane == 0) {
-            inv[r] = L == 0.f ? 0.f : 1.0f / L;
-            if (!fits && r < real) scratch[r] = M;
-            if (a.lse) a.lse[attn_row(a, w.b, h, tok0, r)] = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
-        }
+    const bool fits = rows * q.n <= cap;
+    if (tid < rows) {
+        float lse;
+        inv[tid] = attn_join_row(a, q, tid, tid < real, -1, 0.f, 0.f, fits, scratch + (fits ? tid * q.n : tid), &lse);
+        if (a.lse) a.lse[row_at[tid]] = lse;
     }
     sync();
-    const int total = rows * (a.d / 4);
-    if (total <= threads)
-        attn_join_sum<E, 1, 8>(a, w, h, tok0, rows, real, n, base, step, fits, scratch, inv, threads, tid);
+    const bool small = rows * (a.d / 4) <= threads;
+    if (fits && small)
+        attn_join_sum<E, D, true, 1, 8>(a, rows, real, q.n, q.base, q.step, scratch, inv, row_at, threads, tid);
+    else if (fits)
+        attn_join_sum<E, D, true, 4, 2>(a, rows, real, q.n, q.base, q.step, scratch, inv, row_at, threads, tid);
     else
-        attn_join_sum<E, 4, 2>(a, w, h, tok0, rows, real, n, base, step, fits, scratch, inv, threads, tid);
+        attn_join_sum<E, D, false, 4, 2>(a, rows, real, q.n, q.base, q.step, scratch, inv, row_at, threads, tid);
 }
 
 }  // namespace dfl

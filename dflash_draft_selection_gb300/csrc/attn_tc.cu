@@ -6,6 +6,9 @@ namespace dfl {
 
 static __device__ unsigned int g_err_attn;
 
+// What an item costs beside its tiles: the drain of the pipeline, its sums and outputs, the first tile's maxima.
+constexpr int ATTN_ITEM_COST = 2;
+
 dflash2_status attn_tc64(TcLaunch &t);
 dflash2_status attn_tc128(TcLaunch &t);
 dflash2_status attn_tc256(TcLaunch &t);
@@ -60,6 +63,7 @@ dflash2_status attn_tc_launch(AttnArgs a, cudaStream_t s) {
     a.row_blocks = (a.T + a.tok_block - 1) / a.tok_block;
     a.rows_cap = a.tok_block * a.group;
     a.items = a.Hkv * a.row_blocks;
+    a.item_cost = ATTN_ITEM_COST;
     a.err = err_word();
     if (!a.err) return DFLASH2_ERR_CUDA;
     t.n = a.rows_cap <= 16 ? 16 : a.rows_cap <= 32 ? 32 : a.rows_cap <= 48 ? 48 : a.rows_cap <= 64 ? 64

@@ -173,6 +173,16 @@ __device__ __forceinline__ bool soft_any(int half, bool p) {
     return r != 0;
 }
 
+// ... with an L2 policy for the lines it reads.
+__device__ __forceinline__ void tma_load_4d_hint(void *sdst, const CUtensorMap *tmap, int x, int y, int z, int w,
+                                                 uint64_t *bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+        "{%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_addr(sdst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "l"(pol)
+        : "memory");
+}
+
 __device__ __forceinline__ bool tc_aborted(TcShared &sm) { return *reinterpret_cast<volatile int *>(&sm.abort) != 0; }
 // A bounded wait that gives up at once when another role has.
 static __device__ __noinline__ bool tc_wait_long(TcShared &sm, uint64_t *bar, uint32_t parity, unsigned int *err) {
@@ -277,7 +287,7 @@ struct BoxAt {
 // boxes takes up to twice as long).
 template <int DS, typename Ring>
 __device__ __forceinline__ bool copy_tile(TcShared &sm, unsigned char *ring, Ring &rp, bool leader,
-                                          const CUtensorMap *map, const BoxAt &box, int box_log2, int h,
+                                          const CUtensorMap *map, const BoxAt &box, int box_log2, int h, uint64_t pol,
                                           unsigned int *err) {
     using D = TcDims<DS>;
     const int nb = TK >> box_log2, lane = threadIdx.x & 31, slot = lane / nb;
@@ -295,8 +305,8 @@ __device__ __forceinline__ bool copy_tile(TcShared &sm, unsigned char *ring, Rin
         }
         if (!__all_sync(FULL, ok)) return false;
         if (box.page >= 0 && slot < D::US)
-            tma_load_4d(ring + rp.unit * D::UNIT + dst, map, (u * D::US + slot) * 64, box.off, h, box.page,
-                        &sm.full[rp.unit]);
+            tma_load_4d_hint(ring + rp.unit * D::UNIT + dst, map, (u * D::US + slot) * 64, box.off, h, box.page,
+                             &sm.full[rp.unit], pol);
         rp.step();
     }
     return true;
@@ -325,6 +335,12 @@ __device__ __forceinline__ bool issue_scores(TcShared &sm, uint64_t kd, uint64_t
     return true;
 }
 
+// The largest of the warp's values (NaN only if all are).
+__device__ __forceinline__ float warp_max_one(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ bool bad_bf16(uint32_t h) { return (h & 0x7f80u) == 0x7f80u; }
 
 // Sums of v[0 .. 7] over the warp's lanes: lane l returns row l / 4's.
@@ -420,6 +436,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
     } else if (work && warp >= K_WARP) {
         const bool keys = warp == K_WARP, leader = elect_one();
         const int dpi = TK / a.page_size, doff = TK % a.page_size;
+        const uint64_t pol = l2_policy_evict_first();
         KRing kr;
         VRing vr;
         uint32_t n = 0;
@@ -435,9 +452,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                 if (keys) {  // for the softmax warps: slots in use without a page
                     const bool hole = __any_sync(FULL, box.page < 0 && box.s < w.r.n);
                     if (leader) sm.hole[n % HOLES] = hole;
-                    ok = copy_tile<DS>(sm, ring, kr, leader, &mk, box, box_log2, h, err);
+                    ok = copy_tile<DS>(sm, ring, kr, leader, &mk, box, box_log2, h, pol, err);
                 } else {
-                    ok = copy_tile<DS>(sm, ring, vr, leader, &mv, box, box_log2, h, err);
+                    ok = copy_tile<DS>(sm, ring, vr, leader, &mv, box, box_log2, h, pol, err);
                 }
                 box.step(a, dpi, doff);
             }
@@ -552,12 +569,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                 // which rows see this thread's key; nothing to look at if all rows see the whole tile
                 int r0 = 0, r1 = NR;
                 bool none = false, poison = false;
-                bool masked = t < clean0 || t >= clean1 || *reinterpret_cast<volatile int *>(&sm.hole[n % HOLES]);
+                const bool hole = *reinterpret_cast<volatile int *>(&sm.hole[n % HOLES]);
+                bool masked = hole || t < clean0 || t >= clean1;
                 if (masked) {
                     int lo = 0, hi = 0;
                     if (a.pos) {
                         if (page_now >= 0) attn_view(a, w.r, pos_now, lo, hi);
-                    } else if (ks + key < w.r.n && attn_page(a, w.b, ks + key) >= 0) {
+                    } else if (ks + key < w.r.n && (!hole || attn_page(a, w.b, ks + key) >= 0)) {
                         attn_view(a, w.r, ks + key, lo, hi);
                     }
                     lo = max(lo - tok0, 0) * a.group;
@@ -624,7 +642,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         float mine = NEG_INF;
 #pragma unroll
                         for (int j = c; j < NR && j < c + 32; ++j) {
-                            const float y = warp_max_f(masked && (j < r0 || j >= r1) ? NEG_INF : x[j] * c2);
+                            const float y = warp_max_one(masked && (j < r0 || j >= r1) ? NEG_INF : x[j] * c2);
                             if (lane == j - c) mine = y;
                         }
                         if (c + lane < NR) sm.part[warp & 3][row0 + c + lane] = mine;
@@ -746,42 +764,93 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                 if ((lane & 3) == 0) sm.part[warp & 3][row0 + j + lane / 4] = v;
             }
             soft_sync(half);
-            float *part = w.whole ? nullptr : attn_part(a, blockIdx.x, w.starts);
             const int mine = min(rows - row0, NR);  // rows of this group (none or negative: the group has none)
+            float L = 0.f;
+            const float m_row = key < NR ? -neg_m[key] : 0.f;
             if (key < mine) {
                 const int r = row0 + key;
-                float L = sm.part[0][r] + sm.part[1][r] + sm.part[2][r] + sm.part[3][r];
-                const float m = -neg_m[key];
+                L = sm.part[0][r] + sm.part[1][r] + sm.part[2][r] + sm.part[3][r];
                 if (tc_aborted(sm)) L = NAN;
                 else if (r >= real) L = 0.f;
-                sm.inv[r] = L == 0.f ? 0.f : (w.whole ? 1.0f / L : 1.f);
-                if (w.whole) {
-                    if (a.lse) a.lse[sm.row_at[r]] = L == 0.f ? NEG_INF : (m + log2f(L)) * 0.6931471805599453f;
-                } else {
-                    part[a.rows_cap * a.d + r] = m;
-                    part[a.rows_cap * (a.d + 1) + r] = L;
-                }
+            }
+            // A cut item whose other parts are all there is joined at once with what is still in tensor memory (the
+            // next CTA takes its part first, so this is the usual case at the end of a stretch).
+            const AttnParts q(a, plan, w);
+            float *weights = reinterpret_cast<float *>(sp);  // [rows][q.n], once the last product has read P
+            const bool fits = rows * q.n <= p_bytes(N) / 4;
+            if (!w.whole && tid == 0) {
+                int there;
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(a.tickets + q.c0) : "memory");
+                sm.flag = fits && there == q.n - 1;
             }
             tc_wait(sm, &sm.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
-            soft_sync(half);
+            both_sync();
             tc_fence_after();
+            const bool direct = !w.whole && sm.flag != 0;
+            const int own = direct ? static_cast<int>(blockIdx.x) - q.c0 : -1;
+            float *part = w.whole || direct ? nullptr : attn_part(a, blockIdx.x, w.starts);
+            if (key < mine) {
+                const int r = row0 + key;
+                if (part) {
+                    sm.inv[r] = L == 0.f ? 0.f : 1.f;
+                    part[a.rows_cap * a.d + r] = m_row;
+                    part[a.rows_cap * (a.d + 1) + r] = L;
+                } else {
+                    float lse = L == 0.f ? NEG_INF : (m_row + log2f(L)) * 0.6931471805599453f, g = L == 0.f ? 0.f : 1.0f / L;
+                    if (direct) {
+                        __threadfence();
+                        g = attn_join_row(a, q, r, r < real, own, m_row, L, true, weights + r * q.n, &lse);
+                    }
+                    sm.inv[r] = g;
+                    if (a.lse) a.lse[sm.row_at[r]] = lse;
+                }
+            }
+            soft_sync(half);
             if (DS > 1 || (warp & 3) < 2) {
+                constexpr int CR = NR % 16 == 0 ? 16 : 8;  // rows at a time
 #pragma unroll 1
                 for (int m = 0; m < MB; ++m) {
+                    const int e = m * 128 + key;
 #pragma unroll 1
-                    for (int j0 = 0; j0 < mine; j0 += 8) {
-                        uint32_t o[8];
-                        tmem_ld<8>(tm_o + lanes + m * N + row0 + j0, o);
+                    for (int j0 = 0; j0 < mine; j0 += CR) {
+                        float o[CR];
+                        tmem_ld<CR>(tm_o + lanes + m * N + row0 + j0, reinterpret_cast<uint32_t *>(o));
+                        if (direct) {
+                            float sum[CR];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int r = row0 + j0 + j, e = m * 128 + key;
+                            for (int j = 0; j < CR; ++j) sum[j] = 0.f;
+#pragma unroll 1
+                            for (int k = 0; k < q.n; ++k) {
+                                const float *f = weights + (row0 + j0) * q.n + k;
+                                const int last = mine - 1 - j0;
+                                float x[CR];
+                                if (k == own) {
+#pragma unroll
+                                    for (int j = 0; j < CR; ++j) x[j] = o[j];
+                                } else {
+                                    const float *src = q.at(k) + (row0 + j0) * (DS * 64) + e;
+#pragma unroll
+                                    for (int j = 0; j < CR; ++j) x[j] = __ldcg(src + min(j, last) * (DS * 64));
+                                }
+#pragma unroll
+                                for (int j = 0; j < CR; ++j) {
+                                    const float g = f[min(j, last) * q.n];
+                                    sum[j] = g == 0.f ? sum[j] : fmaf(x[j], g, sum[j]);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < CR; ++j) o[j] = sum[j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < CR; ++j) {
+                            const int r = row0 + j0 + j;
                             const float f = sm.inv[r];
-                            const float v = f == 0.f ? 0.f : __uint_as_float(o[j]) * f;
+                            const float v = f == 0.f ? 0.f : o[j] * f;
                             if (j0 + j < mine) {
-                                if (w.whole)
-                                    attn_store(a, sm.row_at[r] * (DS * 64) + e, v, static_cast<unsigned short *>(nullptr));
-                                else
+                                if (part)
                                     part[r * (DS * 64) + e] = v;
+                                else
+                                    attn_store(a, sm.row_at[r] * (DS * 64) + e, v, static_cast<unsigned short *>(nullptr));
                             }
                         }
                     }
@@ -789,9 +858,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             }
             tc_fence_before();
             both_sync();
-            if (!w.whole) {
-                attn_join<unsigned short>(a, plan, w, rows, h, tok0, 256, tid, &sm.flag, reinterpret_cast<float *>(sp),
-                                          p_bytes(N) / 4, sm.inv, both_sync);
+            if (direct && tid == 0) a.tickets[q.c0] = 0;
+            if (part) {
+                attn_join<unsigned short, DS * 64>(a, q, w, rows, tok0, 256, tid, &sm.flag, weights, p_bytes(N) / 4,
+                                                   sm.inv, sm.row_at, both_sync);
                 both_sync();
             }
         }
