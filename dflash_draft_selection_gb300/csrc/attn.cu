@@ -13,7 +13,7 @@ namespace dfl {
 
 // The tensor-core kernels (attn_tc.cu).
 bool attn_tc_takes(const AttnArgs &a);
-dflash2_status attn_tc_launch(AttnArgs a, cudaStream_t s);
+dflash2_status attn_tc_launch(AttnArgs a, bool weights, cudaStream_t s);
 
 constexpr int SIMT_THREADS = 256;
 constexpr int SIMT_KEYS_LOG2 = 5, SIMT_KEYS = 32;  // keys per tile: one per lane in the score step
@@ -390,6 +390,7 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
         st = launch_simt<float>(a, s);
         return st == DFLASH2_OK && weights ? launch_weights_simt<float>(a, s) : st;
     }
-    st = attn_tc_takes(a) ? attn_tc_launch(a, s) : launch_simt<unsigned short>(a, s);
+    if (attn_tc_takes(a)) return attn_tc_launch(a, weights, s);
+    st = launch_simt<unsigned short>(a, s);
     return st == DFLASH2_OK && weights ? launch_weights_simt<unsigned short>(a, s) : st;
 }

@@ -54,7 +54,7 @@ bool attn_tc_takes(const AttnArgs &a) {
            a.slot_stride * a.page_size < lim / a.Hkv && static_cast<int64_t>(a.T) * a.Hq * a.d < lim;
 }
 
-dflash2_status attn_tc_launch(AttnArgs a, cudaStream_t s) {
+dflash2_status attn_tc_launch(AttnArgs a, bool weights, cudaStream_t s) {
     TcLaunch t;
     a.tile_log2 = 7;
     const int most = TK / a.group;                            // tokens that fit a block
@@ -85,12 +85,20 @@ dflash2_status attn_tc_launch(AttnArgs a, cudaStream_t s) {
     if (!make_map_4d(&t.mk, a.k, cd, cs, 1u << t.box_log2, 1) || !make_map_4d(&t.mv, a.v, cd, cs, 1u << t.box_log2, 1) ||
         !make_map_4d(&t.mq, a.q, qd, qs, a.group, a.tok_block))
         return DFLASH2_ERR_CUDA;
-    const double tiles = static_cast<double>(a.B) * a.items *
-                         ((static_cast<int64_t>(a.max_pages) * a.page_size + TK - 1) / TK);
-    t.ctas = tiles < sm_count() ? static_cast<int64_t>(tiles) : sm_count();
-    t.a = a;
+    const double cap = static_cast<double>((static_cast<int64_t>(a.max_pages) * a.page_size + TK - 1) / TK);
+    auto launch = [&](bool second) {
+        const double tiles = static_cast<double>(a.B) * a.items * cap;
+        t.ctas = tiles < sm_count() ? static_cast<int64_t>(tiles) : sm_count();
+        t.a = a;
+        t.weights = second;
+        return a.d == 64 ? attn_tc64(t) : a.d == 128 ? attn_tc128(t) : attn_tc256(t);
+    };
     t.stream = s;
-    return a.d == 64 ? attn_tc64(t) : a.d == 128 ? attn_tc128(t) : attn_tc256(t);
+    const dflash2_status st = launch(false);
+    if (st != DFLASH2_OK || !weights) return st;
+    a.items = a.Hkv;
+    a.item_cost = 1;
+    return launch(true);
 }
 
 }  // namespace dfl

@@ -57,7 +57,7 @@ constexpr int SM_BYTES = 232448;   // shared memory of a CTA
 struct TcShared {
     uint64_t full[MAX_UNITS], empty[MAX_UNITS];
     uint64_t s_full[2];   // scores of tile n in buffer n & 1
-    uint64_t p_full[2];   // P of tile n written (weights pass: scores read)
+    uint64_t p_full[2];   // P of tile n written (weights pass: its scores read)
     uint64_t pv_done[2];  // output product of tile n complete
     uint64_t q_full, q_empty, done;
     int64_t row_at[128];  // index of the row in lse (times d: in out)
@@ -363,7 +363,7 @@ __device__ __forceinline__ float lane_sums8(const float *v, int lane) {
 }
 
 // Barriers, tensor memory, and Q's rows that no copy reaches (they stay zero).
-__device__ __forceinline__ void tc_setup(TcShared &sm, unsigned char *sq, int qbytes, int units, int cols) {
+__device__ __forceinline__ void tc_setup(TcShared &sm, unsigned char *sq, int qbytes, int units, int cols, int readers) {
     const int tid = threadIdx.x;
     if (tid == 0) {
         for (int i = 0; i < units; ++i) {
@@ -373,7 +373,7 @@ __device__ __forceinline__ void tc_setup(TcShared &sm, unsigned char *sq, int qb
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 8);
+            mbar_init(&sm.p_full[i], readers);
             mbar_init(&sm.pv_done[i], 1);
         }
         mbar_init(&sm.q_full, 1);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *sq = ring + UNITS * D::UNIT, *sp = sq + q_bytes(N, DS);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    tc_setup(sm, sq, q_bytes(N, DS), UNITS, COLS);
+    tc_setup(sm, sq, q_bytes(N, DS), UNITS, COLS, 8);
     const uint32_t tm_s = sm.tmem, tm_o = tm_s + 2 * N;
     unsigned int *err = a.err;
     pdl_wait();
@@ -877,18 +877,193 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
     if (warp == MMA_WARP) tmem_dealloc(tm_s, COLS);
 }
 
+// weight_s += sum over the rows that see s of exp(x_s - lse): the second pass,
+// over the keys alone, with the first one's lse.  Work is cut by (request,
+// cached head) and a row block is a round over the stretch's tiles, so one
+// CTA has all of a key's rows, one thread adds to a key's word, and its
+// additions have an order.  Warps 0-3 take the even tiles and warps 4-7 the
+// odd ones, each thread one key and all rows.  Bound: the keys' bytes.
+template <int N, int DS>
+__global__ void __launch_bounds__(TC_THREADS, 1) k_weights_tc(const __grid_constant__ CUtensorMap mk,
+                                                              const __grid_constant__ CUtensorMap mq,
+                                                              const __grid_constant__ AttnArgs a, int box_log2) {
+    using D = TcDims<DS>;
+    constexpr int UNITS = ring_units(N, DS), COLS = tmem_cols(2 * N);
+    using KRing = RingPos<0, UNITS>;
+    extern __shared__ unsigned char raw[];
+    __shared__ TcShared sm;
+    unsigned char *ring =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char *sq = ring + UNITS * D::UNIT;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    tc_setup(sm, sq, q_bytes(N, DS), UNITS, COLS, 4);
+    const uint32_t tm_s = sm.tmem;
+    unsigned int *err = a.err;
+    pdl_wait();
+    const AttnPlan plan = attn_plan<TC_THREADS>(a, sm.scratch);
+    const bool work = plan.begin < plan.end;
+    AttnWalk w;
+    if (work) w.start(a, plan);
+
+    if (work && warp == Q_WARP) {
+        if (lane == 0) {
+            uint32_t seg = 0;
+            bool ok = true;
+            while (ok && w.next(a)) {
+                for (int rb = 0; ok && rb < a.row_blocks; ++rb) {
+                    ok = seg == 0 || tc_wait(sm, &sm.q_empty, (seg - 1) & 1, err);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&sm.q_full, a.tok_block * a.group * 128 * DS);
+#pragma unroll
+                    for (int s = 0; s < DS; ++s)
+                        tma_load_4d(sq + s * N * 128, &mq, s * 64, w.item * a.group, rb * a.tok_block, w.b, &sm.q_full);
+                    sm.q_filled = ++seg;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (work && warp == K_WARP) {
+        const bool leader = elect_one();
+        const int dpi = TK / a.page_size, doff = TK % a.page_size;
+        const uint64_t pol = l2_policy_evict_first();
+        KRing kr;
+        bool ok = true;
+        while (ok && w.next(a)) {
+            for (int rb = 0; ok && rb < a.row_blocks; ++rb) {
+                BoxAt box;
+                PageWindow pages;
+                box.start(a, w, box_log2, lane);
+                pages.start(a, w, lane);
+                for (int t = w.t0; ok && t < w.t1; ++t) {
+                    box.look(a, w, pages, lane);
+                    ok = copy_tile<DS>(sm, ring, kr, leader, &mk, box, box_log2, w.item, pol, err);
+                    box.step(a, dpi, doff);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (work && warp == MMA_WARP) {
+        if (lane == 0) {
+            KRing kr;
+            const uint32_t ids = tc_idesc(N, false);
+            const uint64_t kd = sw128_desc(ring), qd = sw128_desc(sq);
+            uint32_t seg = 0, used[2] = {0, 0};
+            bool ok = true;
+            while (ok && w.next(a)) {
+                const int nt = w.t1 - w.t0;
+                for (int rb = 0; ok && rb < a.row_blocks; ++rb, ++seg) {
+                    ok = tc_wait(sm, &sm.q_full, seg & 1, err);
+                    for (int i = 0; ok && i < nt; ++i) {
+                        const int buf = i & 1;
+                        if (used[buf] > 0) ok = tc_wait(sm, &sm.p_full[buf], (used[buf] - 1) & 1, err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        ok = issue_scores<DS>(sm, kd, qd, kr, tm_s + buf * N, ids, N, err);
+                        if (!ok) break;
+                        mma_commit(&sm.s_full[buf]);
+                        ++used[buf];
+                        if (i + 1 == nt) mma_commit(&sm.q_empty);
+                    }
+                }
+            }
+            mma_commit(&sm.done);
+            mbar_wait(&sm.done, 0, TC_DRAIN);
+        }
+        __syncwarp();
+    } else if (work && warp < MMA_WARP) {
+        constexpr int CH = N < 32 ? N : 16;  // columns at a time
+        const int half = warp >> 2, key = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tm_s + lanes + half * N;
+        const float c2 = a.scale * LOG2E;
+        uint32_t used = 0;
+        while (w.next(a)) {
+            const int h = w.item, nt = w.t1 - w.t0;
+            for (int rb = 0; rb < a.row_blocks; ++rb) {
+                const int tok0 = rb * a.tok_block, toks = min(a.tok_block, a.T - tok0);
+                const int real = max(min(w.r.nq - tok0, toks), 0) * a.group;
+                both_sync();
+                if (tid < N) {  // -lse in log2; a row that saw nothing adds nothing
+                    float z = NEG_INF;
+                    if (tid < real) z = a.lse[attn_row(a, w.b, h, tok0, tid)];
+                    sm.neg_m[tid] = z == NEG_INF ? NEG_INF : -z * LOG2E;
+                }
+                both_sync();
+                auto look = [&](int i) {
+                    const int s = (w.t0 + i) * TK + key;
+                    return i < nt && s < w.r.n ? attn_page(a, w.b, s) : -1;
+                };
+                auto place = [&](int i, int page) {
+                    return (static_cast<int64_t>(page) * a.Hkv + h) * a.page_size + ((w.t0 + i) * TK + key) % a.page_size;
+                };
+                // pages, and positions where the cache has them, ahead of their use
+                int page = look(half), page_next = look(half + 2);
+                int pos = a.pos && page >= 0 ? a.pos[place(half, page)] : 0;
+                for (int i = half; i < nt; i += 2, ++used) {
+                    const int page_after = look(i + 4);
+                    const int pos_next = a.pos && page_next >= 0 ? a.pos[place(i + 2, page_next)] : 0;
+                    int r0 = 0, r1 = 0;
+                    if (page >= 0) {
+                        attn_view(a, w.r, a.pos ? pos : (w.t0 + i) * TK + key, r0, r1);
+                        r0 = max(r0 - tok0, 0) * a.group;
+                        r1 = min((r1 - tok0) * a.group, real);
+                    }
+                    tc_wait(sm, &sm.s_full[half], used & 1, err);
+                    __syncwarp();
+                    tc_fence_after();
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int c = 0; c < N; c += CH) {
+                        if (c >= real) break;
+                        float x[CH];
+                        tmem_ld<CH>(ts + c, reinterpret_cast<uint32_t *>(x));
+#pragma unroll
+                        for (int j = 0; j < CH; j += 4) {
+                            const float4 m = *reinterpret_cast<const float4 *>(sm.neg_m + c + j);
+                            const float z[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int r = c + j + k;
+                                const float p = ex2(fmaf(x[j + k], c2, z[k]));
+                                sum[k] += r >= r0 && r < r1 && z[k] != NEG_INF ? p : 0.f;
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[half]);
+                    if (r0 < r1) atomicAdd(a.weight + place(i, page), (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    page = page_next;
+                    page_next = page_after;
+                    pos = pos_next;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tc_aborted(sm)) {  // leave no copy in flight into this CTA's shared memory
+        if (tid < UNITS && sm.filled[tid] > 0) mbar_wait(&sm.full[tid], (sm.filled[tid] - 1) & 1, TC_DRAIN);
+        if (tid == UNITS && sm.q_filled > 0) mbar_wait(&sm.q_full, (sm.q_filled - 1) & 1, TC_DRAIN);
+        __syncthreads();
+    }
+    if (warp == MMA_WARP) tmem_dealloc(tm_s, COLS);
+}
+
 // Launches the kernel of N rows (host).
 struct TcLaunch {
     CUtensorMap mk, mv, mq;
     AttnArgs a;
     int box_log2, n;
     int64_t ctas;
+    bool weights;  // the second pass
     cudaStream_t stream;
 };
 
 template <int N, int DS>
 static dflash2_status tc_launch_n(TcLaunch &t) {
-    void *fn = reinterpret_cast<void *>(&k_attn_tc<N, DS>);
+    void *fn = t.weights ? reinterpret_cast<void *>(&k_weights_tc<N, DS>) : reinterpret_cast<void *>(&k_attn_tc<N, DS>);
     blocks_per_sm(fn, TC_THREADS, tc_smem(N, DS));  // raises the shared-memory limit, once per device
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(t.ctas), 1, 1);
@@ -898,8 +1073,8 @@ static dflash2_status tc_launch_n(TcLaunch &t) {
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void *args[5] = {&t.mk, &t.mv, &t.mq, &t.a, &t.box_log2};
-    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) return DFLASH2_ERR_CUDA;
+    void *args[5] = {&t.mk, &t.mv, &t.mq, &t.a, &t.box_log2}, *wargs[4] = {&t.mk, &t.mq, &t.a, &t.box_log2};
+    if (cudaLaunchKernelExC(&cfg, fn, t.weights ? wargs : args) != cudaSuccess) return DFLASH2_ERR_CUDA;
     return after_launch();
 }
 
