@@ -31,7 +31,7 @@ struct AppendArgs {
     float eps;
     void *q_out;
     int32_t *kv_len_out;
-    int head_steps;  // heads a thread takes: head, head + head_steps, ..
+    int head_steps;  // units of a token: a thread takes heads unit, unit + head_steps, .. (at most four)
 };
 
 // Where a new token goes.
@@ -156,6 +156,203 @@ __global__ void __launch_bounds__(256) k_append_any(AppendArgs a) {
     }
 }
 
+// 16-byte vectors: a lane takes two vectors of a head that are rotated
+// together (x of the pairs and y, or two vectors of neighbouring pairs), so
+// its cosines and sines serve all the heads it walks through.  A head is
+// `lanes` neighbouring lanes, which share the norm's sum.
+//
+// Bound: the heads' bytes, read and written once (6.7 TB/s); the table's rows
+// are shared by a token's heads and stay in L1 and L2.
+constexpr int APPEND_BATCH = 4;  // heads whose loads a thread has in flight
+
+template <typename E>
+struct Vec {
+    static constexpr int N = 16 / sizeof(E);
+    uint4 v;
+};
+template <typename E>
+__device__ __forceinline__ void unpack(const uint4 &v, float *x);
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4 &v, float *x) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+}
+template <>
+__device__ __forceinline__ void unpack<unsigned short>(const uint4 &v, float *x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16lo(w[i]);
+        x[2 * i + 1] = bf16hi(w[i]);
+    }
+}
+template <typename E>
+__device__ __forceinline__ uint4 pack(const float *x);
+template <>
+__device__ __forceinline__ uint4 pack<float>(const float *x) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+template <>
+__device__ __forceinline__ uint4 pack<unsigned short>(const float *x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename E, bool INTER, bool NORM>
+__global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2) {
+    constexpr int N = Vec<E>::N;
+    pdl_wait();
+    const int heads = a.Hq + 2 * a.Hkv, half = a.rot / 2;
+    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> lanes_log2;
+    const int c = threadIdx.x & ((1 << lanes_log2) - 1);  // the lane's pair of vectors
+    const bool inside = unit < a.tokens * a.head_steps, mine = inside && c * 2 * N < a.d;
+    const int64_t tok = inside ? unit / a.head_steps : 0;
+    const int head0 = inside ? static_cast<int>(unit - tok * a.head_steps) : 0;
+    const AppendToken at = append_token(a, tok, inside && head0 == 0 && c == 0);
+    const bool turned = mine && c * 2 * N < a.rot;
+    int e0, e1;  // the vectors' first entries
+    if (turned && !INTER) {
+        e0 = c * N;
+        e1 = half + c * N;
+    } else {
+        e0 = c * 2 * N;
+        e1 = e0 + N;
+    }
+    float cs[N], sn[N];
+    if (turned) {
+        if (a.axes == 1) {
+            const int id = a.pos_ids[tok];
+            const bool ok = id >= 0 && id < a.n_pos;
+            const float *row = a.cos_sin + static_cast<int64_t>(ok ? id : 0) * a.rot + c * N;
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(row + i);
+                const float4 y = *reinterpret_cast<const float4 *>(row + half + i);
+                cs[i] = ok ? x.x : NAN;
+                cs[i + 1] = ok ? x.y : NAN;
+                cs[i + 2] = ok ? x.z : NAN;
+                cs[i + 3] = ok ? x.w : NAN;
+                sn[i] = y.x;
+                sn[i + 1] = y.y;
+                sn[i + 2] = y.z;
+                sn[i + 3] = y.w;
+            }
+        } else {
+            int id[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                int ax = a.pair_axis ? a.pair_axis[c * N + i] : 0;
+                ax = ax < a.axes ? ax : a.axes - 1;
+                id[i] = a.pos_ids[ax * a.tokens + tok];
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool ok = id[i] >= 0 && id[i] < a.n_pos;
+                const float *row = a.cos_sin + static_cast<int64_t>(ok ? id[i] : 0) * a.rot + c * N + i;
+                cs[i] = ok ? row[0] : NAN;
+                sn[i] = row[half];
+            }
+        }
+    }
+    uint4 qn[2], kn[2];
+    if (NORM && mine) {
+        const uint4 one = make_uint4(0, 0, 0, 0);
+        qn[0] = a.q_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.q_norm) + e0) : one;
+        qn[1] = a.q_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.q_norm) + e1) : one;
+        kn[0] = a.k_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.k_norm) + e0) : one;
+        kn[1] = a.k_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.k_norm) + e1) : one;
+    }
+    const bool stored = at.live && at.page >= 0;
+    const int64_t slot = at.page * a.page_stride + at.off * a.slot_stride;
+    uint4 x[APPEND_BATCH], y[APPEND_BATCH];
+#pragma unroll
+    for (int i = 0; i < APPEND_BATCH; ++i) {
+        const int h = head0 + i * a.head_steps;
+        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        if (h < heads && mine && stored) {
+            const E *src = h < a.Hq ? reinterpret_cast<const E *>(a.q) + tok * a.q_stride + static_cast<int64_t>(h) * a.d
+                           : h < a.Hq + a.Hkv
+                               ? reinterpret_cast<const E *>(a.k) + tok * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.d
+                               : reinterpret_cast<const E *>(a.v) + tok * a.v_stride +
+                                     static_cast<int64_t>(h - a.Hq - a.Hkv) * a.d;
+            x[i] = *reinterpret_cast<const uint4 *>(src + e0);
+            y[i] = *reinterpret_cast<const uint4 *>(src + e1);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < APPEND_BATCH; ++i) {
+        const int h = head0 + i * a.head_steps;
+        if (i * a.head_steps >= heads) break;  // the same for all lanes
+        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+        float u[N], v[N];
+        unpack<E>(x[i], u);
+        unpack<E>(y[i], v);
+        if (NORM) {
+            float ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) ss = fmaf(u[k], u[k], fmaf(v[k], v[k], ss));
+            for (int d = 1 << lanes_log2 >> 1; d >= 1; d >>= 1) ss += __shfl_xor_sync(FULL, ss, d);
+            if (!is_v && (is_q ? a.q_norm : a.k_norm)) {
+                const float f = 1.0f / sqrtf(ss / a.d + a.eps);
+                float wu[N], wv[N];
+                unpack<E>(is_q ? qn[0] : kn[0], wu);
+                unpack<E>(is_q ? qn[1] : kn[1], wv);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    u[k] = u[k] * f * wu[k];
+                    v[k] = v[k] * f * wv[k];
+                }
+            }
+        }
+        if (turned && !is_v) {
+            float s[N], t[N];
+            if (INTER) {
+#pragma unroll
+                for (int k = 0; k < N; k += 2) {
+                    s[k] = fmaf(u[k], cs[k / 2], -u[k + 1] * sn[k / 2]);
+                    s[k + 1] = fmaf(u[k + 1], cs[k / 2], u[k] * sn[k / 2]);
+                    t[k] = fmaf(v[k], cs[N / 2 + k / 2], -v[k + 1] * sn[N / 2 + k / 2]);
+                    t[k + 1] = fmaf(v[k + 1], cs[N / 2 + k / 2], v[k] * sn[N / 2 + k / 2]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    s[k] = fmaf(u[k], cs[k], -v[k] * sn[k]);
+                    t[k] = fmaf(v[k], cs[k], u[k] * sn[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                u[k] = s[k];
+                v[k] = t[k];
+            }
+        }
+        if (!mine || h >= heads) continue;
+        if (is_q) {
+            if (!stored)
+#pragma unroll
+                for (int k = 0; k < N; ++k) u[k] = v[k] = at.live ? NAN : 0.f;
+            E *dst = static_cast<E *>(a.q_out) + (tok * a.Hq + h) * a.d;
+            *reinterpret_cast<uint4 *>(dst + e0) = pack<E>(u);
+            *reinterpret_cast<uint4 *>(dst + e1) = pack<E>(v);
+        } else if (stored) {
+            const int kh = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+            E *dst = reinterpret_cast<E *>(is_v ? a.cv : a.ck) + slot + kh * a.head_stride;
+            *reinterpret_cast<uint4 *>(dst + e0) = is_v ? x[i] : pack<E>(u);
+            *reinterpret_cast<uint4 *>(dst + e1) = is_v ? y[i] : pack<E>(v);
+            if (!is_v && c == 0) {
+                const int64_t si = (static_cast<int64_t>(at.page) * a.Hkv + kh) * a.page_size + at.off;
+                if (a.weight) a.weight[si] = 0.f;
+                if (a.pos) a.pos[si] = at.seq;
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------- evict --
 struct EvictArgs {
     char *ck, *cv;
@@ -195,8 +392,15 @@ __device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, int64_t b, int
 
 // One CTA per (request, head): the budget-th largest key by four passes of a
 // radix select (8 bits each), then the kept slots in slot order by ballots.
+// The keys are made once and stay in shared memory (KEYS: the table's slots
+// fit it, 50000 of them), so weights and positions are read once; otherwise
+// every pass makes them again.  Bound: those reads, and the passes' latency.
+constexpr int EV_KEYS = 50000;
+constexpr int EV_HISTS = 8;  // histograms, to spread the equal digits that weights have
+template <bool KEYS>
 __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
-    __shared__ int hist[256];
+    extern __shared__ uint32_t keys[];
+    __shared__ int hists[EV_HISTS][256];
     __shared__ int s_warp[3][32];
     __shared__ uint32_t s_prefix;
     __shared__ int s_left;
@@ -216,14 +420,27 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
         s_prefix = 0;
         s_left = a.budget;
     }
+    if (KEYS) {
+#pragma unroll 4
+        for (int s = tid; s < n; s += EV_THREADS) keys[s] = evict_key(a, b, h, s, newest);
+    }
+    auto key_of = [&](int s) { return KEYS ? keys[s] : evict_key(a, b, h, s, newest); };
+    int *hist = hists[warp % EV_HISTS];
     for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+        for (int i = tid; i < EV_HISTS * 256; i += EV_THREADS) (&hists[0][0])[i] = 0;
         __syncthreads();
         const uint32_t prefix = s_prefix;
         const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
         for (int s = tid; s < n; s += EV_THREADS) {
-            const uint32_t k = evict_key(a, b, h, s, newest);
+            const uint32_t k = key_of(s);
             if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+        }
+        __syncthreads();
+        if (tid < 256) {
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < EV_HISTS; ++i) sum += hists[i][tid];
+            hists[0][tid] = sum;
         }
         __syncthreads();
         if (warp == 0) {
@@ -231,7 +448,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
             int mine[8], sum = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                mine[i] = hist[255 - (lane * 8 + i)];
+                mine[i] = hists[0][255 - (lane * 8 + i)];
                 sum += mine[i];
             }
             int inc = sum;
@@ -263,7 +480,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
     int eq = 0;
     for (int s = s0; s < s1; s += 32) {
         const bool in = s + lane < n;
-        eq += __popc(__ballot_sync(FULL, in && evict_key(a, b, h, in ? s + lane : 0, newest) == T));
+        eq += __popc(__ballot_sync(FULL, in && key_of(in ? s + lane : 0) == T));
     }
     if (lane == 0) s_warp[0][warp] = eq;
     __syncthreads();
@@ -279,7 +496,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
         for (int s = s0; s < s1; s += 32) {
             const int slot = s + lane;
             const bool in = slot < n;
-            const uint32_t k = evict_key(a, b, h, in ? slot : 0, newest);
+            const uint32_t k = key_of(in ? slot : 0);
             const unsigned tie = __ballot_sync(FULL, in && k == T);
             const unsigned below = (1u << lane) - 1u;
             const bool kept = in && (k > T || (k == T && seen + __popc(tie & below) < ties));
@@ -306,7 +523,9 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
     }
 }
 
-// The moves of every (request, head): a warp per move, 16 bytes per lane.
+// The moves of every (request, head): a warp takes eight at a time, one lane
+// per move for its places, and 16 bytes per lane of all of them in flight.
+constexpr int EV_BATCH = 8;
 __global__ void __launch_bounds__(256) k_evict_move(EvictArgs a) {
     pdl_wait();
     const int64_t b = blockIdx.x / a.Hkv;
@@ -320,23 +539,37 @@ __global__ void __launch_bounds__(256) k_evict_move(EvictArgs a) {
     const int count = a.count[blockIdx.x];
     const int2 *m = a.moves + static_cast<int64_t>(blockIdx.x) * a.max_moves;
     const int vecs = a.row_bytes / 16;
-    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < count; i += gridDim.y * 8) {
-        const int2 mv = m[i];
-        const int ps = evict_page(a, b, mv.x), pd = evict_page(a, b, mv.y);
-        if (ps < 0 || pd < 0) continue;
-        const int os = mv.x % a.page_size, od = mv.y % a.page_size;
-        const int64_t from = ps * a.page_bytes + h * a.head_bytes + os * a.slot_bytes;
-        const int64_t to = pd * a.page_bytes + h * a.head_bytes + od * a.slot_bytes;
+    for (int i = (blockIdx.y * 8 + (threadIdx.x >> 5)) * EV_BATCH; i < count; i += gridDim.y * 8 * EV_BATCH) {
+        int64_t from = -1, to = 0;  // of lane's move, if it has one
+        if (lane < EV_BATCH && i + lane < count) {
+            const int2 mv = m[i + lane];
+            const int ps = evict_page(a, b, mv.x), pd = evict_page(a, b, mv.y);
+            if (ps >= 0 && pd >= 0) {
+                const int os = mv.x % a.page_size, od = mv.y % a.page_size;
+                from = ps * a.page_bytes + h * a.head_bytes + os * a.slot_bytes;
+                to = pd * a.page_bytes + h * a.head_bytes + od * a.slot_bytes;
+                const int64_t is = (static_cast<int64_t>(ps) * a.Hkv + h) * a.page_size + os;
+                const int64_t id = (static_cast<int64_t>(pd) * a.Hkv + h) * a.page_size + od;
+                a.weight[id] = a.weight[is];
+                a.pos[id] = a.pos[is];
+            }
+        }
+        int64_t f[EV_BATCH], t[EV_BATCH];
+#pragma unroll
+        for (int k = 0; k < EV_BATCH; ++k) {
+            f[k] = __shfl_sync(FULL, from, k);
+            t[k] = __shfl_sync(FULL, to, k);
+        }
         for (int j = lane; j < 2 * vecs; j += 32) {
             char *base = j < vecs ? a.ck : a.cv;
             const int64_t o = static_cast<int64_t>(j < vecs ? j : j - vecs) * 16;
-            *reinterpret_cast<uint4 *>(base + to + o) = *reinterpret_cast<const uint4 *>(base + from + o);
-        }
-        if (lane == 0) {
-            const int64_t is = (static_cast<int64_t>(ps) * a.Hkv + h) * a.page_size + os;
-            const int64_t id = (static_cast<int64_t>(pd) * a.Hkv + h) * a.page_size + od;
-            a.weight[id] = a.weight[is];
-            a.pos[id] = a.pos[is];
+            uint4 x[EV_BATCH];
+#pragma unroll
+            for (int k = 0; k < EV_BATCH; ++k)
+                if (f[k] >= 0) x[k] = *reinterpret_cast<const uint4 *>(base + f[k] + o);
+#pragma unroll
+            for (int k = 0; k < EV_BATCH; ++k)
+                if (f[k] >= 0) *reinterpret_cast<uint4 *>(base + t[k] + o) = x[k];
         }
     }
 }
@@ -352,6 +585,26 @@ static dflash2_status launch_pdl(void (*fn)(A), const A &a, dim3 grid, int threa
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) return DFLASH2_ERR_CUDA;
+    return after_launch();
+}
+
+static dflash2_status launch_append_vec(AppendArgs &a, dflash2_dtype dt, bool inter, bool norm, int lanes_log2, dim3 grid,
+                                        cudaStream_t s) {
+    using Fn = void (*)(AppendArgs, int);
+    using H = unsigned short;
+    static const Fn table[8] = {k_append_vec<H, false, false>,     k_append_vec<H, false, true>,
+                                k_append_vec<H, true, false>,      k_append_vec<H, true, true>,
+                                k_append_vec<float, false, false>, k_append_vec<float, false, true>,
+                                k_append_vec<float, true, false>,  k_append_vec<float, true, true>};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const Fn fn = table[(dt == DFLASH2_F32 ? 4 : 0) + (inter ? 2 : 0) + (norm ? 1 : 0)];
+    if (cudaLaunchKernelEx(&cfg, fn, a, lanes_log2) != cudaSuccess) return DFLASH2_ERR_CUDA;
     return after_launch();
 }
 
@@ -428,6 +681,21 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
     a.q_out = q_out;
     a.kv_len_out = kv_len_out;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int heads = Hq + 2 * cache->Hkv, two = 32 / e;  // entries of two vectors
+    if (rot % two == 0 && d % two == 0 && d / two <= 32) {
+        int lanes_log2 = 0;
+        while ((1 << lanes_log2) * two < d) ++lanes_log2;
+        // Many tokens: a thread takes four heads, so that a token's cosines are read by a quarter of the threads;
+        // few: one, so that there are enough threads (512 per SM).
+        const int64_t few = (static_cast<int64_t>(heads) + APPEND_BATCH - 1) / APPEND_BATCH;
+        a.head_steps = static_cast<int>((a.tokens * few << lanes_log2) >= static_cast<int64_t>(sm_count()) * 512 ? few : heads);
+        const int64_t threads = a.tokens * a.head_steps << lanes_log2;
+        if ((threads + 255) / 256 < (int64_t(1) << 31)) {
+            const dim3 vgrid(static_cast<unsigned>((threads + 255) / 256));
+            const bool norm = q_norm || k_norm;
+            return launch_append_vec(a, cache->dt, interleaved != 0, norm, lanes_log2, vgrid, s);
+        }
+    }
     const int64_t units = a.tokens * (Hq + 2 * cache->Hkv);
     const int64_t blocks = (units + 7) / 8, most = static_cast<int64_t>(sm_count()) * 64;
     const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
@@ -483,10 +751,17 @@ extern "C" dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const 
     a.max_moves = evict_max_moves(cap, budget);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int64_t heads = B * cache->Hkv;
-    dflash2_status st = launch_pdl(k_evict_select, a, dim3(static_cast<unsigned>(heads)), EV_THREADS, 0, s);
+    const dim3 sgrid(static_cast<unsigned>(heads));
+    dflash2_status st;
+    if (cap <= EV_KEYS) {
+        blocks_per_sm(reinterpret_cast<const void *>(&k_evict_select<true>), EV_THREADS, EV_KEYS * 4);
+        st = launch_pdl(k_evict_select<true>, a, sgrid, EV_THREADS, static_cast<size_t>(cap) * 4, s);
+    } else {
+        st = launch_pdl(k_evict_select<false>, a, sgrid, EV_THREADS, 0, s);
+    }
     if (st != DFLASH2_OK) return st;
-    int64_t x = (a.max_moves + 7) / 8;
-    const int64_t want = (static_cast<int64_t>(sm_count()) * 8 + heads - 1) / heads;
+    int64_t x = (a.max_moves + 8 * EV_BATCH - 1) / (8 * EV_BATCH);
+    const int64_t want = (static_cast<int64_t>(sm_count()) * 16 + heads - 1) / heads;
     if (x > want) x = want;
     if (x < 1) x = 1;
     return launch_pdl(k_evict_move, a, dim3(static_cast<unsigned>(heads), static_cast<unsigned>(x)), 256, 0, s);
