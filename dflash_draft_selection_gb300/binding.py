@@ -132,18 +132,45 @@ def _dtype_code(dt: torch.dtype) -> int:
     raise TypeError(f"unsupported dtype {dt}")
 
 
-def _int32(B: int, **ts):
-    """Per-request arrays: contiguous int32 [B] (None passes)."""
-    for name, t in ts.items():
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B or not t.is_contiguous()):
-            raise ValueError(f"{name}: contiguous int32 [{B}]")
-    _need_cuda(*ts.values())
+def _int32(B: int, name: str, t):
+    """A per-request array: contiguous int32 [B] on the GPU (None passes).  Returns its address."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: contiguous int32 [{B}] on the GPU")
+    return t.data_ptr()
 
 
-def _page_table(table: torch.Tensor, B: int):
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
-        raise ValueError(f"page_table: contiguous int32 [{B}, pages]")
-    _need_cuda(table)
+def _page_table(t: torch.Tensor, B: int):
+    """Address and pages per request of a page table."""
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != B or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"page_table: contiguous int32 [{B}, pages] on the GPU")
+    return t.data_ptr(), shape[1]
+
+
+def _heads(name: str, t: torch.Tensor, dt, B: int, T: int, H: int, d: int):
+    """Address and token stride of [B, T, H, d] with contiguous heads and one stride from token to token."""
+    st = t.stride()
+    if t.dtype is not dt or t.shape != (B, T, H, d) or not t.is_cuda:
+        raise ValueError(f"{name}: {dt} [{B}, {T}, {H}, {d}] on the GPU")
+    if (st[3] != 1 and d > 1) or (st[2] != d and H > 1) or (B > 1 and T > 1 and st[0] != T * st[1]):
+        raise ValueError(f"{name}: contiguous heads and one stride from token to token")
+    return t.data_ptr(), st[1] if T > 1 else (st[0] if B > 1 else H * d)
+
+
+def _dense(name: str, t, dt, shape):
+    """Address of a contiguous tensor of a type and shape on the GPU (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is not dt or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: contiguous {dt} {list(shape)} on the GPU")
+    return t.data_ptr()
+
+
+def _raw_stream(t: torch.Tensor) -> int:
+    """The current stream of a tensor's device as a number (torch.cuda.current_stream without its object)."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _stream(device) -> ctypes.c_void_p:
@@ -446,40 +473,29 @@ def rope_append(q, k, v, cos_sin, pos_ids, cache: KVCache, page_table, kv_len, p
     """dflash2_rope_append.  q [B, T, Hq, d], k and v [B, T, Hkv, d] of the cache's type (slices of a fused
     projection are taken as they are); cos_sin [n_pos, rot] f32; pos_ids [axes, B, T] int32; pair_axis [rot / 2]
     uint8; kv_len [B] int32, the slots in use before the call.  Returns (rotated q [B, T, Hq, d], kv_len + q_len)."""
-    L = load_library()
     B, T, Hq, d = q.shape
-    _need_cuda(q, k, v, cos_sin, pos_ids, pair_axis, q_norm, k_norm)
-    for name, t, H in (("q", q, Hq), ("k", k, cache.Hkv), ("v", v, cache.Hkv)):
-        if t.dtype != cache.dtype or t.shape != (B, T, H, cache.d) or \
-                (t.numel() and (t.stride(3) != 1 or (H > 1 and t.stride(2) != d) or
-                                (B > 1 and T > 1 and t.stride(0) != T * t.stride(1)))):
-            raise ValueError(f"{name}: {cache.dtype} [{B}, {T}, {H}, {cache.d}] with contiguous heads and one stride "
-                             "from token to token")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin: contiguous float32 [n_pos, rot]")
-    if pos_ids.dtype != torch.int32 or pos_ids.dim() != 3 or pos_ids.shape[1:] != (B, T) or not pos_ids.is_contiguous():
-        raise ValueError(f"pos_ids: contiguous int32 [axes, {B}, {T}]")
-    rot = cos_sin.shape[1]
-    if pair_axis is not None and (pair_axis.dtype != torch.uint8 or pair_axis.shape != (rot // 2,) or
-                                  not pair_axis.is_contiguous()):
-        raise ValueError(f"pair_axis: contiguous uint8 [{rot // 2}]")
-    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if t is not None and (t.dtype != cache.dtype or t.shape != (d,) or not t.is_contiguous()):
-            raise ValueError(f"{name}: contiguous {cache.dtype} [{d}]")
-    _page_table(page_table, B)
-    _int32(B, kv_len=kv_len, q_len=q_len, seq_pos=seq_pos)
+    dt, Hkv = cache.dtype, cache.Hkv
+    if d != cache.d:
+        raise ValueError(f"q: heads of {cache.d}")
+    qp, qs = _heads("q", q, dt, B, T, Hq, d)
+    kp, ks = _heads("k", k, dt, B, T, Hkv, d)
+    vp, vs = _heads("v", v, dt, B, T, Hkv, d)
+    n_pos, rot = cos_sin.shape
+    axes = pos_ids.shape[0]
+    table, pages = _page_table(page_table, B)
     if out is None:
-        out = (torch.empty(B, T, Hq, d, dtype=q.dtype, device=q.device),
-               torch.empty(B, dtype=torch.int32, device=q.device))
+        out = (torch.empty((B, T, Hq, d), dtype=dt, device=q.device), torch.empty_like(kv_len))
     q_out, kv_len_out = out
-    step = lambda t: t.stride(1) if T > 1 else (t.stride(0) if B > 1 else t.shape[2] * d)  # noqa: E731
     _check("dflash2_rope_append",
-           L.dflash2_rope_append(cache._ref, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(q_len),
-                                 _ptr(seq_pos), _ptr(q), _ptr(k), _ptr(v), step(q), step(k), step(v), B, T, Hq,
-                                 _ptr(cos_sin), cos_sin.shape[0], rot, _ptr(pos_ids), pos_ids.shape[0],
-                                 _ptr(pair_axis), int(interleaved), _ptr(q_norm), _ptr(k_norm), eps, _ptr(q_out),
-                                 _ptr(kv_len_out), _stream(q.device)))
-    return q_out, kv_len_out
+           (_lib or load_library()).dflash2_rope_append(
+               cache._ref, table, pages, _int32(B, "kv_len", kv_len), _int32(B, "q_len", q_len),
+               _int32(B, "seq_pos", seq_pos), qp, kp, vp, qs, ks, vs, B, T, Hq,
+               _dense("cos_sin", cos_sin, torch.float32, (n_pos, rot)), n_pos, rot,
+               _dense("pos_ids", pos_ids, torch.int32, (axes, B, T)), axes,
+               _dense("pair_axis", pair_axis, torch.uint8, (rot // 2,)), interleaved,
+               _dense("q_norm", q_norm, dt, (d,)), _dense("k_norm", k_norm, dt, (d,)), eps,
+               _dense("out", q_out, dt, (B, T, Hq, d)), _int32(B, "out", kv_len_out), _raw_stream(q)))
+    return out
 
 
 def paged_attn(q, cache: KVCache, page_table, kv_len, scale: float | None = None, causal: bool = True,
@@ -487,41 +503,40 @@ def paged_attn(q, cache: KVCache, page_table, kv_len, scale: float | None = None
     """dflash2_paged_attn.  q [B, T, Hq, d] of the cache's type; kv_len [B] int32, the slots in use with the block's
     own among them; scale 1 / sqrt(d) unless given; add_weights adds every cached key's softmax weight to
     cache.weight.  Returns (out [B, T, Hq, d], lse [B, T, Hq] f32)."""
-    L = load_library()
-    _need_cuda(q)
-    B, T, Hq, d = q.shape
-    if q.dtype != cache.dtype or d != cache.d or not q.is_contiguous():
-        raise ValueError(f"q: contiguous {cache.dtype} [B, T, Hq, {cache.d}]")
-    _page_table(page_table, B)
-    _int32(B, kv_len=kv_len, q_len=q_len, seq_pos=seq_pos)
+    B, T, Hq, d = shape = q.shape
+    dt = cache.dtype
+    if d != cache.d:
+        raise ValueError(f"q: heads of {cache.d}")
+    table, pages = _page_table(page_table, B)
     if ws is None:
-        ws = Workspace.for_paged_attn(B, T, Hq, cache.Hkv, d, q.dtype, q.device)
+        ws = Workspace.for_paged_attn(B, T, Hq, cache.Hkv, d, dt, q.device)
     if out is None:
-        out = (torch.empty_like(q), torch.empty(B, T, Hq, dtype=torch.float32, device=q.device))
+        out = (torch.empty_like(q), torch.empty((B, T, Hq), dtype=torch.float32, device=q.device))
     o, lse = out
-    flags = (ATTN_CAUSAL if causal else 0) | (ATTN_WEIGHTS if add_weights else 0)
     _check("dflash2_paged_attn",
-           L.dflash2_paged_attn(cache._ref, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(q_len),
-                                _ptr(seq_pos), _ptr(q), B, T, Hq, d ** -0.5 if scale is None else scale, window,
-                                flags, _ptr(o), _ptr(lse), ws.ptr(), ws.nbytes, _stream(q.device)))
-    return o, lse
+           (_lib or load_library()).dflash2_paged_attn(
+               cache._ref, table, pages, _int32(B, "kv_len", kv_len), _int32(B, "q_len", q_len),
+               _int32(B, "seq_pos", seq_pos), _dense("q", q, dt, shape), B, T, Hq,
+               d ** -0.5 if scale is None else scale, window,
+               (ATTN_CAUSAL if causal else 0) | (ATTN_WEIGHTS if add_weights else 0), _dense("out", o, dt, shape),
+               _dense("out", lse, torch.float32, (B, T, Hq)), ws.buf.data_ptr(), ws.buf.numel(), _raw_stream(q)))
+    return out
 
 
 def kv_evict(cache: KVCache, page_table, kv_len, budget: int, recent: int = 0, sink: int = 0, seq_len=None, ws=None,
              out=None):
     """dflash2_kv_evict.  Every head keeps `budget` slots of a request that has more: those of the `recent` newest and
     `sink` first positions, then the most attended.  Returns min(kv_len, budget) [B] int32."""
-    L = load_library()
     B = kv_len.shape[0]
-    _page_table(page_table, B)
-    _int32(B, kv_len=kv_len, seq_len=seq_len)
+    table, pages = _page_table(page_table, B)
     if ws is None:
-        ws = Workspace.for_kv_evict(B, cache.Hkv, page_table.shape[1] * cache.page_size, budget, kv_len.device)
+        ws = Workspace.for_kv_evict(B, cache.Hkv, pages * cache.page_size, budget, kv_len.device)
     if out is None:
         out = torch.empty_like(kv_len)
     _check("dflash2_kv_evict",
-           L.dflash2_kv_evict(cache._ref, _ptr(page_table), page_table.shape[1], _ptr(kv_len), _ptr(seq_len), B,
-                              budget, recent, sink, _ptr(out), ws.ptr(), ws.nbytes, _stream(kv_len.device)))
+           (_lib or load_library()).dflash2_kv_evict(
+               cache._ref, table, pages, _int32(B, "kv_len", kv_len), _int32(B, "seq_len", seq_len), B, budget, recent,
+               sink, _int32(B, "out", out), ws.buf.data_ptr(), ws.buf.numel(), _raw_stream(kv_len)))
     return out
 
 

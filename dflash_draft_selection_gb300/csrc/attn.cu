@@ -17,7 +17,13 @@ dflash2_status attn_tc_launch(AttnArgs a, bool weights, cudaStream_t s);
 
 constexpr int SIMT_THREADS = 256;
 constexpr int SIMT_KEYS_LOG2 = 5, SIMT_KEYS = 32;  // keys per tile: one per lane in the score step
-constexpr int SIMT_ROWS = 16;  // query rows per block: two per warp in the score step
+constexpr int SIMT_TILE_ROWS = 32;  // query rows of a block: four per warp in the score step
+constexpr int SIMT_ROWS = 16;       // ... of the weights pass: two per warp
+
+template <bool V>
+struct BoolC {
+    static constexpr bool value = V;
+};
 
 template <typename E>
 __device__ __forceinline__ float4 ld4(const void *p, int64_t i);
@@ -78,119 +84,195 @@ __device__ __forceinline__ void simt_scores(const float *sq, const float *sk, in
 
 static __device__ __forceinline__ void cta_sync() { __syncthreads(); }
 
+// One CTA per stretch, 32 query rows against tiles of 32 keys, which arrive by
+// asynchronous copies one tile ahead.  Scores: warp w has rows 4 w .. 4 w + 3
+// and lane l key l, so a row's maximum and sum are the warp's; the four rows
+// share the reads of the key.  Output: a thread has RPT rows x 4 dims, so a
+// value read from shared memory feeds RPT products.
+// Bound: the fp32 units (rows * d * 4 operations per key) once more than a
+// few rows share a key, the bytes below that.
 template <typename E>
-__global__ void __launch_bounds__(SIMT_THREADS) k_attn_simt(AttnArgs a) {
+struct SimtTile {
+    static constexpr int PAD = 16 / sizeof(E);  // elements between rows: the lanes' reads fall into different banks
+};
+constexpr int P_LD = SIMT_TILE_ROWS + 4;
+
+template <typename E>
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+
+// Asks for a tile's keys and values; rows without a page become zero.
+template <typename E>
+__device__ __forceinline__ void simt_ask(const AttnArgs &a, int b, int h, const AttnReq &r, int tile, E *sk, E *sv,
+                                         int ld) {
+    constexpr int N = 16 / sizeof(E);
+    const int vecs = a.d / N;
+    for (int i = threadIdx.x; i < SIMT_KEYS * vecs; i += SIMT_THREADS) {
+        const int j = i / vecs, c = (i - j * vecs) * N, slot = tile * SIMT_KEYS + j;
+        const int page = slot < r.n ? attn_page(a, b, slot) : -1;
+        E *dk = sk + j * ld + c, *dv = sv + j * ld + c;
+        if (page >= 0) {
+            const int64_t at = page * a.page_stride + h * a.head_stride + (slot % a.page_size) * a.slot_stride + c;
+            cp_async16<E>(dk, reinterpret_cast<const E *>(a.k) + at);
+            cp_async16<E>(dv, reinterpret_cast<const E *>(a.v) + at);
+        } else {
+            *reinterpret_cast<uint4 *>(dk) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(dv) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <typename E, int RPT>
+__global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
     extern __shared__ float smem[];
     __shared__ int scratch[SIMT_THREADS / 32 + 2];
-    __shared__ int s_page[SIMT_KEYS], s_lo[SIMT_KEYS], s_hi[SIMT_KEYS], s_flag;
-    __shared__ float s_p[SIMT_ROWS][SIMT_KEYS], s_f[SIMT_ROWS], s_inv[128];
+    __shared__ int s_lo[2][SIMT_KEYS], s_hi[2][SIMT_KEYS], s_flag;
+    __shared__ alignas(16) float s_p[SIMT_KEYS * P_LD];
+    __shared__ float s_f[SIMT_TILE_ROWS], s_m[SIMT_TILE_ROWS], s_inv[128];
     __shared__ int64_t s_row[128];
-    const int d = a.d, ld = d + 4, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float *sq = smem, *sk = sq + SIMT_ROWS * ld, *sv = sk + SIMT_KEYS * ld;
+    const int d = a.d, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ld = d + SimtTile<E>::PAD, ldq = d + 4;
+    float *sq = smem;
+    E *kv = reinterpret_cast<E *>(sq + SIMT_TILE_ROWS * ldq);  // [2][keys, values][KEYS][ld]
     pdl_wait();
     const AttnPlan p = attn_plan<SIMT_THREADS>(a, scratch);
     if (p.begin >= p.end) return;
-    const int d4 = d / 4, groups = SIMT_THREADS / d4;  // output step: thread = (4 dims, rows og, og + groups, ..)
-    const int oc = (tid % d4) * 4, og = tid / d4;
+    const int d4 = d / 4, oc = (tid % d4) * 4, or0 = tid / d4 * RPT;  // output step: dims oc .., rows or0 ..
+    const bool out_on = or0 < SIMT_TILE_ROWS;
     const float c2 = a.scale * LOG2E;
     AttnWalk w;
     w.start(a, p);
     while (w.next(a)) {
         const int h = w.item / a.row_blocks, tok0 = (w.item % a.row_blocks) * a.tok_block;
         const int rows = min(a.tok_block, a.T - tok0) * a.group;
-        for (int row0 = 0; row0 < rows; row0 += SIMT_ROWS) {  // more than one pass only where group > ROWS
+        for (int row0 = 0; row0 < rows; row0 += SIMT_TILE_ROWS) {  // more than one round only where group > 32
             __syncthreads();
-            simt_load_q<E>(a, w, h, tok0, row0, rows, sq, ld);
-            float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
-            float4 acc[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int t = w.t0; t < w.t1; ++t) {
-                __syncthreads();
+            simt_ask<E>(a, w.b, h, w.r, w.t0, kv, kv + SIMT_KEYS * ld, ld);
+            for (int i = tid; i < SIMT_TILE_ROWS * d4; i += SIMT_THREADS) {
+                const int r = i / d4, c = (i - r * d4) * 4;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row0 + r < rows) x = ld4<E>(a.q, attn_row(a, w.b, h, tok0, row0 + r) * d + c);
+                *reinterpret_cast<float4 *>(sq + r * ldq + c) = x;
+            }
+            auto view = [&](int t, int buf) {
                 if (tid < SIMT_KEYS) {
                     int lo, hi, page;
                     attn_view_slot(a, w.r, w.b, h, t * SIMT_KEYS + tid, lo, hi, page);
-                    s_page[tid] = page;
-                    s_lo[tid] = (lo - tok0) * a.group - row0;  // rows of this block that see the key
-                    s_hi[tid] = (hi - tok0) * a.group - row0;
+                    s_lo[buf][tid] = (lo - tok0) * a.group - row0;  // rows of this block that see the key
+                    s_hi[buf][tid] = (hi - tok0) * a.group - row0;
                 }
+            };
+            view(w.t0, 0);
+            float m[4], l[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[k] = NEG_INF;
+                l[k] = 0.f;
+            }
+            float4 acc[RPT];
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int t = w.t0; t < w.t1; ++t) {
+                const int buf = (t - w.t0) & 1;
+                const E *sk = kv + buf * 2 * SIMT_KEYS * ld, *sv = sk + SIMT_KEYS * ld;
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncthreads();
-                simt_load_tile<E>(a, a.k, s_page, h, t, sk, ld);
-                simt_load_tile<E>(a, a.v, s_page, h, t, sv, d);
-                __syncthreads();
-                float x0, x1;
-                simt_scores(sq, sk, ld, d, warp, lane, x0, x1);
-                const int lo = s_lo[lane], hi = s_hi[lane];
-                const bool on0 = warp >= lo && warp < hi, on1 = warp + 8 >= lo && warp + 8 < hi;
-                x0 = on0 ? x0 * c2 : NEG_INF;
-                x1 = on1 ? x1 * c2 : NEG_INF;
-                const float n0 = fmaxf(m0, warp_max_f(x0)), n1 = fmaxf(m1, warp_max_f(x1));
-                // a row that has seen nothing yet keeps m = -inf and adds nothing; a NaN score stays NaN
-                const float p0 = !on0 || (n0 == NEG_INF && x0 == NEG_INF) ? 0.f : ex2(x0 - n0);
-                const float p1 = !on1 || (n1 == NEG_INF && x1 == NEG_INF) ? 0.f : ex2(x1 - n1);
-                const float f0 = m0 == NEG_INF ? 0.f : ex2(m0 - n0), f1 = m1 == NEG_INF ? 0.f : ex2(m1 - n1);
-                l0 = (m0 == NEG_INF ? l0 : l0 * f0) + warp_sum(p0);
-                l1 = (m1 == NEG_INF ? l1 : l1 * f1) + warp_sum(p1);
-                m0 = n0;
-                m1 = n1;
-                s_p[warp][lane] = p0;
-                s_p[warp + 8][lane] = p1;
-                if (lane == 0) {
-                    s_f[warp] = f0;
-                    s_f[warp + 8] = f1;
+                if (t + 1 < w.t1) {
+                    E *next = kv + (buf ^ 1) * 2 * SIMT_KEYS * ld;
+                    simt_ask<E>(a, w.b, h, w.r, t + 1, next, next + SIMT_KEYS * ld, ld);
+                    view(t + 1, buf ^ 1);
                 }
-                __syncthreads();
-                if (og < groups) {
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                const E *kp = sk + lane * ld;
+                const float *qp = sq + warp * 4 * ldq;
+#pragma unroll 4
+                for (int c = 0; c < d; c += 4) {
+                    const float4 k = ld4<E>(kp, c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = og + i * groups;
-                        if (r >= SIMT_ROWS) break;
-                        const float f = s_f[r];
-                        float4 o = acc[i];
-                        if (f != 1.f) o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll 8
-                        for (int j = 0; j < SIMT_KEYS; ++j) {
-                            const float q = s_p[r][j];
-                            const float4 v = *reinterpret_cast<const float4 *>(sv + j * d + oc);
-                            if (q != 0.f) {  // what a row does not see may be NaN
-                                o.x = fmaf(q, v.x, o.x);
-                                o.y = fmaf(q, v.y, o.y);
-                                o.z = fmaf(q, v.z, o.z);
-                                o.w = fmaf(q, v.w, o.w);
-                            }
-                        }
-                        acc[i] = o;
+                        const float4 q = *reinterpret_cast<const float4 *>(qp + i * ldq + c);
+                        x[i] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, x[i]))));
                     }
+                }
+                const int lo = s_lo[buf][lane], hi = s_hi[buf][lane];
+                float f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = warp * 4 + i;
+                    const bool on = r >= lo && r < hi;
+                    x[i] = on ? x[i] * c2 : NEG_INF;
+                    const float n = fmaxf(m[i], warp_max_f(x[i]));
+                    // a row that has seen nothing yet keeps m = -inf and adds nothing; a NaN score stays NaN
+                    const float e = !on || (n == NEG_INF && x[i] == NEG_INF) ? 0.f : ex2(x[i] - n);
+                    f[i] = m[i] == NEG_INF ? 0.f : ex2(m[i] - n);
+                    l[i] = (m[i] == NEG_INF ? l[i] : l[i] * f[i]) + warp_sum(e);
+                    m[i] = n;
+                    x[i] = e;
+                }
+                *reinterpret_cast<float4 *>(s_p + lane * P_LD + warp * 4) = make_float4(x[0], x[1], x[2], x[3]);
+                if (lane == 0) *reinterpret_cast<float4 *>(s_f + warp * 4) = make_float4(f[0], f[1], f[2], f[3]);
+                // some row does not see some key: what it does not see may be NaN
+                const bool partial = __syncthreads_or(lo > 0 || hi < min(rows - row0, SIMT_TILE_ROWS));
+                if (out_on) {
+#pragma unroll
+                    for (int i = 0; i < RPT; ++i) {
+                        const float g = s_f[or0 + i];
+                        acc[i] = make_float4(acc[i].x * g, acc[i].y * g, acc[i].z * g, acc[i].w * g);
+                    }
+                    auto add = [&](auto checked) {
+#pragma unroll 4
+                        for (int j = 0; j < SIMT_KEYS; ++j) {
+                            const float4 v = ld4<E>(sv + j * ld, oc);
+                            float q[RPT];
+#pragma unroll
+                            for (int i = 0; i < RPT; i += 2) {
+                                const float2 y = *reinterpret_cast<const float2 *>(s_p + j * P_LD + or0 + i);
+                                q[i] = y.x;
+                                q[i + 1] = y.y;
+                            }
+#pragma unroll
+                            for (int i = 0; i < RPT; ++i)
+                                if (!decltype(checked)::value || q[i] != 0.f) {
+                                    acc[i].x = fmaf(q[i], v.x, acc[i].x);
+                                    acc[i].y = fmaf(q[i], v.y, acc[i].y);
+                                    acc[i].z = fmaf(q[i], v.z, acc[i].z);
+                                    acc[i].w = fmaf(q[i], v.w, acc[i].w);
+                                }
+                        }
+                    };
+                    if (partial)
+                        add(BoolC<true>());
+                    else
+                        add(BoolC<false>());
                 }
             }
             // l and m of the rows to everyone
             __syncthreads();
             if (lane == 0) {
-                s_f[warp] = l0;
-                s_f[warp + 8] = l1;
-                s_p[0][warp] = m0;
-                s_p[0][warp + 8] = m1;
+                *reinterpret_cast<float4 *>(s_f + warp * 4) = make_float4(l[0], l[1], l[2], l[3]);
+                *reinterpret_cast<float4 *>(s_m + warp * 4) = make_float4(m[0], m[1], m[2], m[3]);
             }
             __syncthreads();
             float *part = w.whole ? nullptr : attn_part(a, blockIdx.x, w.starts);
-            if (og < groups) {
+            if (out_on) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = og + i * groups;
-                    if (r >= SIMT_ROWS || row0 + r >= rows) break;
-                    const float l = s_f[r];
+                for (int i = 0; i < RPT; ++i) {
+                    const int r = or0 + i;
+                    if (row0 + r >= rows) break;
+                    const float L = s_f[r];
                     if (w.whole) {
-                        const float inv = l == 0.f ? 0.f : 1.0f / l;
-                        const int64_t row = attn_row(a, w.b, h, tok0, row0 + r), at = row * d + oc;
-                        const float o[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) attn_store(a, at + k, l == 0.f ? 0.f : o[k] * inv, static_cast<E *>(nullptr));
-                        if (oc == 0 && a.lse) a.lse[row] = l == 0.f ? NEG_INF : (s_p[0][r] + log2f(l)) * 0.6931471805599453f;
+                        const float inv = L == 0.f ? 0.f : 1.0f / L;
+                        const int64_t row = attn_row(a, w.b, h, tok0, row0 + r);
+                        const bool on = L != 0.f;
+                        attn_store4(a, row * d + oc, on ? acc[i].x * inv : 0.f, on ? acc[i].y * inv : 0.f,
+                                    on ? acc[i].z * inv : 0.f, on ? acc[i].w * inv : 0.f, static_cast<E *>(nullptr));
+                        if (oc == 0 && a.lse) a.lse[row] = on ? (s_m[r] + log2f(L)) * 0.6931471805599453f : NEG_INF;
                     } else {
                         *reinterpret_cast<float4 *>(part + static_cast<int64_t>(row0 + r) * d + oc) = acc[i];
                         if (oc == 0) {
-                            part[a.rows_cap * d + row0 + r] = s_p[0][r];
-                            part[a.rows_cap * (d + 1) + row0 + r] = l;
+                            part[a.rows_cap * d + row0 + r] = s_m[r];
+                            part[a.rows_cap * (d + 1) + row0 + r] = L;
                         }
                     }
                 }
@@ -198,7 +280,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_attn_simt(AttnArgs a) {
         }
         if (!w.whole) {
             if (tid < rows) s_row[tid] = attn_row(a, w.b, h, tok0, tid);
-            attn_join<E, 0>(a, AttnParts(a, p, w), w, rows, tok0, SIMT_THREADS, tid, &s_flag, smem, SIMT_KEYS * ld, s_inv, s_row, cta_sync);
+            attn_join<E, 0>(a, AttnParts(a, p, w), w, rows, tok0, SIMT_THREADS, tid, &s_flag, smem,
+                            SIMT_TILE_ROWS * ldq, s_inv, s_row, cta_sync);
         }
     }
 }
@@ -255,6 +338,9 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_weights_simt(AttnArgs a) {
     }
 }
 
+static size_t attn_simt_smem(int d, int e) {
+    return static_cast<size_t>(SIMT_TILE_ROWS) * (d + 4) * 4 + static_cast<size_t>(4) * SIMT_KEYS * (d + 16 / e) * e;
+}
 static size_t simt_smem(int d) { return static_cast<size_t>((SIMT_ROWS + SIMT_KEYS) * (d + 4) + SIMT_KEYS * d) * 4; }
 
 static dflash2_status launch_simple(void *fn, AttnArgs &a, int threads, size_t smem, int64_t ctas, cudaStream_t s) {
@@ -271,28 +357,31 @@ static dflash2_status launch_simple(void *fn, AttnArgs &a, int threads, size_t s
     return after_launch();
 }
 
-static int attn_ctas() { return sm_count() * 3 < ATTN_MAX_CTAS ? sm_count() * 3 : ATTN_MAX_CTAS; }
+// CTAs of the CUDA-core kernels at most: two per SM (their registers).  The tensor-core kernels take one per SM.
+static int attn_ctas() { return sm_count() * 2 < ATTN_MAX_CTAS ? sm_count() * 2 : ATTN_MAX_CTAS; }
 
-// CTAs of a call: as many as are resident, no more than there can be tiles.
-static int64_t simt_grid(const AttnArgs &a, const void *fn) {
-    const int64_t per = blocks_per_sm(fn, SIMT_THREADS, simt_smem(256));
-    const int64_t slots = static_cast<int64_t>(sm_count()) * (per < 3 ? per : 3);
-    const int64_t most = slots < ATTN_MAX_CTAS ? slots : ATTN_MAX_CTAS;
+// CTAs of a call: no more than there can be tiles.
+static int64_t simt_grid(const AttnArgs &a) {
     const int64_t cap = (static_cast<int64_t>(a.max_pages) * a.page_size + SIMT_KEYS - 1) / SIMT_KEYS;
     const double t = static_cast<double>(a.B) * a.items * cap;
-    return t < most ? static_cast<int64_t>(t) : most;
+    return t < attn_ctas() ? static_cast<int64_t>(t) : attn_ctas();
 }
 
 template <typename E>
 static dflash2_status launch_simt(AttnArgs a, cudaStream_t s) {
-    void *fn = reinterpret_cast<void *>(&k_attn_simt<E>);
+    // rows a thread has in the output step: 256 threads over d / 4 vectors and 32 rows
+    void *fn = a.d <= 64 ? reinterpret_cast<void *>(&k_attn_simt<E, 2>)
+               : a.d <= 128 ? reinterpret_cast<void *>(&k_attn_simt<E, 4>)
+                            : reinterpret_cast<void *>(&k_attn_simt<E, 8>);
+    blocks_per_sm(fn, SIMT_THREADS, attn_simt_smem(256, sizeof(E)));  // raises the shared-memory limit, once per device
     a.tile_log2 = SIMT_KEYS_LOG2;
-    a.tok_block = SIMT_ROWS / a.group > 0 ? SIMT_ROWS / a.group : 1;
+    a.tok_block = SIMT_TILE_ROWS / a.group > 0 ? SIMT_TILE_ROWS / a.group : 1;
     if (a.tok_block > a.T) a.tok_block = a.T;
     a.row_blocks = (a.T + a.tok_block - 1) / a.tok_block;
     a.rows_cap = a.tok_block * a.group;
     a.items = a.Hkv * a.row_blocks;
-    return launch_simple(fn, a, SIMT_THREADS, simt_smem(a.d), simt_grid(a, fn), s);
+    a.item_cost = 1;
+    return launch_simple(fn, a, SIMT_THREADS, attn_simt_smem(a.d, sizeof(E)), simt_grid(a), s);
 }
 
 template <typename E>
@@ -300,7 +389,8 @@ static dflash2_status launch_weights_simt(AttnArgs a, cudaStream_t s) {
     void *fn = reinterpret_cast<void *>(&k_weights_simt<E>);
     a.tile_log2 = SIMT_KEYS_LOG2;
     a.items = a.Hkv;
-    return launch_simple(fn, a, SIMT_THREADS, simt_smem(a.d), simt_grid(a, fn), s);
+    blocks_per_sm(fn, SIMT_THREADS, simt_smem(256));
+    return launch_simple(fn, a, SIMT_THREADS, simt_smem(a.d), simt_grid(a), s);
 }
 
 // Rows of one part in the workspace, for either kind of kernel.
