@@ -84,6 +84,10 @@ __device__ __forceinline__ void simt_scores(const float *sq, const float *sk, in
 
 static __device__ __forceinline__ void cta_sync() { __syncthreads(); }
 
+static __host__ __device__ size_t attn_simt_smem(int d, int e) {
+    return static_cast<size_t>(SIMT_TILE_ROWS) * (d + 4) * 4 + static_cast<size_t>(4) * SIMT_KEYS * (d + 16 / e) * e;
+}
+
 // One CTA per stretch, 32 query rows against tiles of 32 keys, which arrive by
 // asynchronous copies one tile ahead.  Scores: warp w has rows 4 w .. 4 w + 3
 // and lane l key l, so a row's maximum and sum are the warp's; the four rows
@@ -102,18 +106,21 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 
+// A tile's keys: their pages and places in them, and the rows that see them.
+struct SimtKeys {
+    int page[SIMT_KEYS], off[SIMT_KEYS], lo[SIMT_KEYS], hi[SIMT_KEYS];
+};
+
 // Asks for a tile's keys and values; rows without a page become zero.
 template <typename E>
-__device__ __forceinline__ void simt_ask(const AttnArgs &a, int b, int h, const AttnReq &r, int tile, E *sk, E *sv,
-                                         int ld) {
+__device__ __forceinline__ void simt_ask(const AttnArgs &a, int h, const SimtKeys &t, E *sk, E *sv, int ld) {
     constexpr int N = 16 / sizeof(E);
     const int vecs = a.d / N;
     for (int i = threadIdx.x; i < SIMT_KEYS * vecs; i += SIMT_THREADS) {
-        const int j = i / vecs, c = (i - j * vecs) * N, slot = tile * SIMT_KEYS + j;
-        const int page = slot < r.n ? attn_page(a, b, slot) : -1;
+        const int j = i / vecs, c = (i - j * vecs) * N, page = t.page[j];
         E *dk = sk + j * ld + c, *dv = sv + j * ld + c;
         if (page >= 0) {
-            const int64_t at = page * a.page_stride + h * a.head_stride + (slot % a.page_size) * a.slot_stride + c;
+            const int64_t at = page * a.page_stride + h * a.head_stride + t.off[j] * a.slot_stride + c;
             cp_async16<E>(dk, reinterpret_cast<const E *>(a.k) + at);
             cp_async16<E>(dv, reinterpret_cast<const E *>(a.v) + at);
         } else {
@@ -128,7 +135,8 @@ template <typename E, int RPT>
 __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
     extern __shared__ float smem[];
     __shared__ int scratch[SIMT_THREADS / 32 + 2];
-    __shared__ int s_lo[2][SIMT_KEYS], s_hi[2][SIMT_KEYS], s_flag;
+    __shared__ SimtKeys s_keys[3];  // this tile's, the next one's and the one after
+    __shared__ int s_flag;
     __shared__ alignas(16) float s_p[SIMT_KEYS * P_LD];
     __shared__ float s_f[SIMT_TILE_ROWS], s_m[SIMT_TILE_ROWS], s_inv[128];
     __shared__ int64_t s_row[128];
@@ -147,23 +155,30 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
         const int h = w.item / a.row_blocks, tok0 = (w.item % a.row_blocks) * a.tok_block;
         const int rows = min(a.tok_block, a.T - tok0) * a.group;
         for (int row0 = 0; row0 < rows; row0 += SIMT_TILE_ROWS) {  // more than one round only where group > 32
+            // one warp looks a tile's pages and positions up, two tiles ahead
+            auto look = [&](int t) {
+                if (tid < SIMT_KEYS) {
+                    SimtKeys &k = s_keys[(t - w.t0) % 3];
+                    const int slot = t * SIMT_KEYS + tid;
+                    int lo = 0, hi = 0, page = -1;
+                    if (t < w.t1) attn_view_slot(a, w.r, w.b, h, slot, lo, hi, page);
+                    k.page[tid] = page;
+                    k.off[tid] = slot % a.page_size;
+                    k.lo[tid] = (lo - tok0) * a.group - row0;  // rows of this block that see the key
+                    k.hi[tid] = (hi - tok0) * a.group - row0;
+                }
+            };
             __syncthreads();
-            simt_ask<E>(a, w.b, h, w.r, w.t0, kv, kv + SIMT_KEYS * ld, ld);
+            look(w.t0);
+            look(w.t0 + 1);
+            __syncthreads();
+            simt_ask<E>(a, h, s_keys[0], kv, kv + SIMT_KEYS * ld, ld);
             for (int i = tid; i < SIMT_TILE_ROWS * d4; i += SIMT_THREADS) {
                 const int r = i / d4, c = (i - r * d4) * 4;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (row0 + r < rows) x = ld4<E>(a.q, attn_row(a, w.b, h, tok0, row0 + r) * d + c);
                 *reinterpret_cast<float4 *>(sq + r * ldq + c) = x;
             }
-            auto view = [&](int t, int buf) {
-                if (tid < SIMT_KEYS) {
-                    int lo, hi, page;
-                    attn_view_slot(a, w.r, w.b, h, t * SIMT_KEYS + tid, lo, hi, page);
-                    s_lo[buf][tid] = (lo - tok0) * a.group - row0;  // rows of this block that see the key
-                    s_hi[buf][tid] = (hi - tok0) * a.group - row0;
-                }
-            };
-            view(w.t0, 0);
             float m[4], l[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -180,8 +195,8 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
                 __syncthreads();
                 if (t + 1 < w.t1) {
                     E *next = kv + (buf ^ 1) * 2 * SIMT_KEYS * ld;
-                    simt_ask<E>(a, w.b, h, w.r, t + 1, next, next + SIMT_KEYS * ld, ld);
-                    view(t + 1, buf ^ 1);
+                    simt_ask<E>(a, h, s_keys[(t + 1 - w.t0) % 3], next, next + SIMT_KEYS * ld, ld);
+                    look(t + 2);
                 }
                 float x[4] = {0.f, 0.f, 0.f, 0.f};
                 const E *kp = sk + lane * ld;
@@ -195,18 +210,19 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
                         x[i] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, x[i]))));
                     }
                 }
-                const int lo = s_lo[buf][lane], hi = s_hi[buf][lane];
+                const SimtKeys &keys = s_keys[(t - w.t0) % 3];
+                const int lo = keys.lo[lane], hi = keys.hi[lane];
                 float f[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = warp * 4 + i;
                     const bool on = r >= lo && r < hi;
                     x[i] = on ? x[i] * c2 : NEG_INF;
-                    const float n = fmaxf(m[i], warp_max_f(x[i]));
+                    const float n = fmaxf(m[i], warp_max_one(x[i]));
                     // a row that has seen nothing yet keeps m = -inf and adds nothing; a NaN score stays NaN
                     const float e = !on || (n == NEG_INF && x[i] == NEG_INF) ? 0.f : ex2(x[i] - n);
                     f[i] = m[i] == NEG_INF ? 0.f : ex2(m[i] - n);
-                    l[i] = (m[i] == NEG_INF ? l[i] : l[i] * f[i]) + warp_sum(e);
+                    l[i] = (m[i] == NEG_INF ? l[i] : l[i] * f[i]) + e;  // the lane's keys; the warp's at the end
                     m[i] = n;
                     x[i] = e;
                 }
@@ -249,6 +265,8 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
             }
             // l and m of the rows to everyone
             __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) l[k] = warp_sum(l[k]);
             if (lane == 0) {
                 *reinterpret_cast<float4 *>(s_f + warp * 4) = make_float4(l[0], l[1], l[2], l[3]);
                 *reinterpret_cast<float4 *>(s_m + warp * 4) = make_float4(m[0], m[1], m[2], m[3]);
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
         if (!w.whole) {
             if (tid < rows) s_row[tid] = attn_row(a, w.b, h, tok0, tid);
             attn_join<E, 0>(a, AttnParts(a, p, w), w, rows, tok0, SIMT_THREADS, tid, &s_flag, smem,
-                            SIMT_TILE_ROWS * ldq, s_inv, s_row, cta_sync);
+                            static_cast<int>(attn_simt_smem(d, sizeof(E)) / 4), s_inv, s_row, cta_sync);
         }
     }
 }
@@ -338,9 +356,6 @@ __global__ void __launch_bounds__(SIMT_THREADS) k_weights_simt(AttnArgs a) {
     }
 }
 
-static size_t attn_simt_smem(int d, int e) {
-    return static_cast<size_t>(SIMT_TILE_ROWS) * (d + 4) * 4 + static_cast<size_t>(4) * SIMT_KEYS * (d + 16 / e) * e;
-}
 static size_t simt_smem(int d) { return static_cast<size_t>((SIMT_ROWS + SIMT_KEYS) * (d + 4) + SIMT_KEYS * d) * 4; }
 
 static dflash2_status launch_simple(void *fn, AttnArgs &a, int threads, size_t smem, int64_t ctas, cudaStream_t s) {

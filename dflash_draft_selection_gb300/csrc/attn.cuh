@@ -270,63 +270,15 @@ __device__ __forceinline__ void attn_store4(const AttnArgs &a, int64_t i, float 
     *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(a.out) + i) = make_uint2(pack_bf16(x, y), pack_bf16(z, w));
 }
 
-__device__ __forceinline__ float *attn_part(const AttnArgs &a, int cta, bool starts) {
-    return a.parts + (static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * attn_part_floats(a.rows_cap, a.d);
+// The largest of the warp's values (NaN only if all are).
+__device__ __forceinline__ float warp_max_one(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// The join's sum over the parts: U vectors of four entries per thread and K
-// parts at a time, all their loads in flight together.  D: the head dimension
-// (0: a.d).
-template <typename E, int D, bool FITS, int U, int K>
-__device__ __forceinline__ void attn_join_sum(const AttnArgs &a, int rows, int real, int n, const float *base,
-                                              int64_t step, const float *scratch, const float *inv,
-                                              const int64_t *row_at, int threads, int tid) {
-    const int d = D ? D : a.d, d4 = d / 4, total = rows * d4;
-#pragma unroll 1
-    for (int i0 = tid; i0 < total; i0 += U * threads) {
-        float4 o[U];
-        int r[U], at[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = min(i0 + u * threads, total - 1);
-            r[u] = i / d4;
-            at[u] = i * 4;
-            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll 1
-        for (int k0 = 0; k0 < n; k0 += K) {
-            float4 x[U * K];
-#pragma unroll
-            for (int v = 0; v < U * K; ++v) {
-                const int k = min(k0 + v / U, n - 1);
-                x[v] = __ldcg(reinterpret_cast<const float4 *>(base + (k == 0 ? 0 : 2 * k - 1) * step + at[v % U]));
-            }
-#pragma unroll
-            for (int v = 0; v < U * K; ++v) {
-                const int u = v % U, k = k0 + v / U;
-                float f = 0.f;
-                if (k < n && r[u] < real) {
-                    if (FITS)
-                        f = scratch[r[u] * n + k];
-                    else
-                        f = ex2(__ldcg(base + (k == 0 ? 0 : 2 * k - 1) * step + a.rows_cap * d + r[u]) - scratch[r[u]]);
-                }
-                if (f == 0.f) continue;
-                o[u].x = fmaf(x[v].x, f, o[u].x);
-                o[u].y = fmaf(x[v].y, f, o[u].y);
-                o[u].z = fmaf(x[v].z, f, o[u].z);
-                o[u].w = fmaf(x[v].w, f, o[u].w);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u * threads < total) {
-                const float g = inv[r[u]];
-                attn_store4(a, row_at[r[u]] * d + (at[u] - r[u] * d), g == 0.f ? 0.f : o[u].x * g,
-                            g == 0.f ? 0.f : o[u].y * g, g == 0.f ? 0.f : o[u].z * g, g == 0.f ? 0.f : o[u].w * g,
-                            static_cast<E *>(nullptr));
-            }
-    }
+__device__ __forceinline__ float *attn_part(const AttnArgs &a, int cta, bool starts) {
+    return a.parts + (static_cast<int64_t>(cta) * 2 + (starts ? 1 : 0)) * attn_part_floats(a.rows_cap, a.d);
 }
 
 // The parts of a cut item: n of them, the first from CTA c0; part k's place in
@@ -345,54 +297,76 @@ struct AttnParts {
     __device__ __forceinline__ const float *at(int k) const { return base + (k == 0 ? 0 : 2 * k - 1) * step; }
 };
 
-// Row r's weights over the parts: f_k = 2^(m_k - M) (0 for a part that saw
-// nothing), their sum with the parts' sums, 1 / L in `inv`, and the row's lse.
-// Part `own` (or none, -1) is this CTA's: its m and l are given.  The f_k go
-// to scratch[k], or M alone if they do not fit.  Every sum over parts runs in
-// their order, so the result is the same whoever takes it.
-__device__ __forceinline__ float attn_join_row(const AttnArgs &a, const AttnParts &q, int r, bool seen, int own,
-                                               float own_m, float own_l, bool fits, float *scratch, float *lse) {
-    constexpr int K = 4;
+// A row's weights over n parts with (m_k, l_k): f_k = 2^(m_k - M), 0 for a part
+// that saw nothing, written over m; 1 / sum l_k f_k is returned (0 for a row
+// that saw nothing) and the row's lse.  Sums over parts run in their order, so
+// the result is the same whoever takes them.
+__device__ __forceinline__ float attn_join_row(int n, float *m, const float *l, float *lse) {
     float M = NEG_INF, L = 0.f;
-    if (seen) {
-        const int64_t om = static_cast<int64_t>(a.rows_cap) * a.d + r;
-        for (int k0 = 0; k0 < q.n; k0 += K) {
-            float m[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) m[k] = __ldcg(q.at(min(k0 + k, q.n - 1)) + om);
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (k0 + k < q.n) M = fmax_nan(M, k0 + k == own ? own_m : m[k]);
-        }
-        for (int k0 = 0; k0 < q.n; k0 += K) {
-            float m[K], l[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                m[k] = __ldcg(q.at(min(k0 + k, q.n - 1)) + om);
-                l[k] = __ldcg(q.at(min(k0 + k, q.n - 1)) + om + a.rows_cap);
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (k0 + k >= q.n) continue;
-                const float mk = k0 + k == own ? own_m : m[k], lk = k0 + k == own ? own_l : l[k];
-                // a part that saw nothing has l = 0 (and a sum that is NaN is taken along)
-                const float f = lk == 0.f ? 0.f : ex2(mk - M);
-                L = fmaf(lk, f, L);
-                if (fits) scratch[k0 + k] = f;
-            }
-        }
-        if (!fits) scratch[0] = M;
-    } else if (fits) {
-        for (int k = 0; k < q.n; ++k) scratch[k] = 0.f;
+    for (int k = 0; k < n; ++k) M = fmax_nan(M, m[k]);
+    for (int k = 0; k < n; ++k) {
+        const float lk = l[k];
+        const float f = lk == 0.f ? 0.f : ex2(m[k] - M);  // a sum that is NaN is taken along
+        L = fmaf(lk, f, L);
+        m[k] = f;
     }
     *lse = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
     return L == 0.f ? 0.f : 1.0f / L;
 }
 
+// The join's sum over the parts: U vectors of four entries per thread and K
+// parts at a time, all their loads in flight together (other CTAs keep the
+// memory busy: a load's latency is what a join costs).  D: the head dimension
+// (0: a.d).
+template <typename E, int D, int U, int K, typename Weight>
+__device__ __forceinline__ void attn_join_sum(const AttnArgs &a, const AttnParts &q, int rows, Weight weight,
+                                              const float *inv, const int64_t *row_at, int threads, int tid) {
+    const int d = D ? D : a.d, d4 = d / 4, total = rows * d4;
+#pragma unroll 1
+    for (int i0 = tid; i0 < total; i0 += U * threads) {
+        float4 o[U];
+        int r[U], at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * threads, total - 1);
+            r[u] = i / d4;
+            at[u] = i * 4;
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < q.n; k0 += K) {
+            float4 x[U * K];
+#pragma unroll
+            for (int v = 0; v < U * K; ++v)
+                x[v] = __ldcg(reinterpret_cast<const float4 *>(q.at(min(k0 + v / U, q.n - 1)) + at[v % U]));
+#pragma unroll
+            for (int v = 0; v < U * K; ++v) {
+                const int u = v % U, k = k0 + v / U;
+                const float f = k < q.n ? weight(r[u], k) : 0.f;
+                if (f == 0.f) continue;
+                o[u].x = fmaf(x[v].x, f, o[u].x);
+                o[u].y = fmaf(x[v].y, f, o[u].y);
+                o[u].z = fmaf(x[v].z, f, o[u].z);
+                o[u].w = fmaf(x[v].w, f, o[u].w);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * threads < total) {
+                const float g = inv[r[u]];
+                attn_store4(a, row_at[r[u]] * d + (at[u] - r[u] * d), g == 0.f ? 0.f : o[u].x * g,
+                            g == 0.f ? 0.f : o[u].y * g, g == 0.f ? 0.f : o[u].z * g, g == 0.f ? 0.f : o[u].w * g,
+                            static_cast<E *>(nullptr));
+            }
+    }
+}
+
 // After this CTA's part of a cut item is written: take the item's ticket, and
 // if every other part is there, join them (all `threads` threads call it; E is
-// the output's element type, D the head dimension or 0).  `scratch` (`cap`
-// floats) holds the rows' weights; row_at: the rows' indexes in lse.
+// the output's element type, D the head dimension or 0).  `scratch`
+// (`cap` floats) holds the rows' m and l; where they do not fit (very many
+// parts of many rows) the weights go over the m of the parts, which nobody
+// else reads any more.  row_at: the rows' indexes in lse.
 template <typename E, int D, typename Sync>
 __device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnParts &q, const AttnWalk &w, int rows, int tok0,
                                           int threads, int tid, int *flag /* shared */, float *scratch, int cap,
@@ -408,21 +382,53 @@ __device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnParts &q,
     sync();
     if (!*flag) return;
     __threadfence();
-    const int real = min(rows, max(w.r.nq - tok0, 0) * a.group);
-    const bool fits = rows * q.n <= cap;
+    const int real = min(rows, max(w.r.nq - tok0, 0) * a.group), all = rows * q.n;
+    const int64_t om = static_cast<int64_t>(a.rows_cap) * a.d;
+    if (2 * all > cap) {
+        float lse;
+        if (tid < rows) {
+            float M = NEG_INF, L = 0.f;
+            for (int k = 0; k < q.n; ++k) M = fmax_nan(M, __ldcg(q.at(k) + om + tid));
+            for (int k = 0; k < q.n; ++k) {
+                const float l = tid < real ? __ldcg(q.at(k) + om + a.rows_cap + tid) : 0.f;
+                float *m = const_cast<float *>(q.at(k)) + om + tid;
+                const float f = l == 0.f ? 0.f : ex2(__ldcg(m) - M);
+                L = fmaf(l, f, L);
+                __stcg(m, f);
+            }
+            lse = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
+            inv[tid] = L == 0.f ? 0.f : 1.0f / L;
+            if (a.lse) a.lse[row_at[tid]] = lse;
+        }
+        __threadfence();
+        sync();
+        attn_join_sum<E, D, 4, 4>(
+            a, q, rows, [&](int r, int k) { return __ldcg(q.at(k) + om + r); }, inv, row_at, threads, tid);
+        return;
+    }
+    float *m = scratch, *l = scratch + all;
+#pragma unroll 4
+    for (int i = tid; i < all; i += threads) {
+        const int r = i / q.n;
+        const float *x = q.at(i - r * q.n) + om + r;
+        const float mk = __ldcg(x), lk = __ldcg(x + a.rows_cap);
+        m[i] = mk;
+        l[i] = r < real ? lk : 0.f;
+    }
+    sync();
     if (tid < rows) {
         float lse;
-        inv[tid] = attn_join_row(a, q, tid, tid < real, -1, 0.f, 0.f, fits, scratch + (fits ? tid * q.n : tid), &lse);
+        inv[tid] = attn_join_row(q.n, m + tid * q.n, l + tid * q.n, &lse);
         if (a.lse) a.lse[row_at[tid]] = lse;
     }
     sync();
-    const bool small = rows * (a.d / 4) <= threads;
-    if (fits && small)
-        attn_join_sum<E, D, true, 1, 8>(a, rows, real, q.n, q.base, q.step, scratch, inv, row_at, threads, tid);
-    else if (fits)
-        attn_join_sum<E, D, true, 4, 2>(a, rows, real, q.n, q.base, q.step, scratch, inv, row_at, threads, tid);
+    auto weight = [&](int r, int k) { return m[r * q.n + k]; };
+    if (rows * (a.d / 4) <= threads)
+        attn_join_sum<E, D, 1, 16>(a, q, rows, weight, inv, row_at, threads, tid);
+    else if (q.n > 2)
+        attn_join_sum<E, D, 2, 8>(a, q, rows, weight, inv, row_at, threads, tid);
     else
-        attn_join_sum<E, D, false, 4, 2>(a, rows, real, q.n, q.base, q.step, scratch, inv, row_at, threads, tid);
+        attn_join_sum<E, D, 8, 2>(a, q, rows, weight, inv, row_at, threads, tid);
 }
 
 }  // namespace dfl

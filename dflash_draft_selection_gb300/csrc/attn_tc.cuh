@@ -335,12 +335,6 @@ __device__ __forceinline__ bool issue_scores(TcShared &sm, uint64_t kd, uint64_t
     return true;
 }
 
-// The largest of the warp's values (NaN only if all are).
-__device__ __forceinline__ float warp_max_one(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
 __device__ __forceinline__ bool bad_bf16(uint32_t h) { return (h & 0x7f80u) == 0x7f80u; }
 
 // Sums of v[0 .. 7] over the warp's lanes: lane l returns row l / 4's.
@@ -773,15 +767,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                 if (tc_aborted(sm)) L = NAN;
                 else if (r >= real) L = 0.f;
             }
-            // A cut item whose other parts are all there is joined at once with what is still in tensor memory (the
+            // An item cut in two whose other part is there is joined at once with what is still in tensor memory (the
             // next CTA takes its part first, so this is the usual case at the end of a stretch).
             const AttnParts q(a, plan, w);
-            float *weights = reinterpret_cast<float *>(sp);  // [rows][q.n], once the last product has read P
-            const bool fits = rows * q.n <= p_bytes(N) / 4;
+            float *scratch = reinterpret_cast<float *>(sp);  // once the last product has read P
             if (!w.whole && tid == 0) {
                 int there;
                 asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(a.tickets + q.c0) : "memory");
-                sm.flag = fits && there == q.n - 1;
+                sm.flag = q.n == 2 && there == 1;
             }
             tc_wait(sm, &sm.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
             both_sync();
@@ -799,7 +792,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     float lse = L == 0.f ? NEG_INF : (m_row + log2f(L)) * 0.6931471805599453f, g = L == 0.f ? 0.f : 1.0f / L;
                     if (direct) {
                         __threadfence();
-                        g = attn_join_row(a, q, r, r < real, own, m_row, L, true, weights + r * q.n, &lse);
+                        const float *x = q.at(own ^ 1) + static_cast<int64_t>(a.rows_cap) * a.d + r;
+                        float ml[4];
+                        ml[own] = m_row;
+                        ml[own ^ 1] = __ldcg(x);
+                        ml[2 + own] = L;
+                        ml[2 + (own ^ 1)] = r < real ? __ldcg(x + a.rows_cap) : 0.f;
+                        g = attn_join_row(2, ml, ml + 2, &lse);
+                        scratch[2 * r] = ml[0];
+                        scratch[2 * r + 1] = ml[1];
                     }
                     sm.inv[r] = g;
                     if (a.lse) a.lse[sm.row_at[r]] = lse;
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             }
             soft_sync(half);
             if (DS > 1 || (warp & 3) < 2) {
-                constexpr int CR = NR % 16 == 0 ? 16 : 8;  // rows at a time
+                constexpr int CR = NR % 24 == 0 ? 24 : NR % 16 == 0 ? 16 : 8;  // rows at a time
 #pragma unroll 1
                 for (int m = 0; m < MB; ++m) {
                     const int e = m * 128 + key;
@@ -816,30 +817,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         float o[CR];
                         tmem_ld<CR>(tm_o + lanes + m * N + row0 + j0, reinterpret_cast<uint32_t *>(o));
                         if (direct) {
-                            float sum[CR];
+                            // f0 x0 + f1 x1 in the parts' order, as attn_join_sum has it
+                            const int last = mine - 1 - j0;
+                            const float *src = q.at(own ^ 1) + (row0 + j0) * (DS * 64) + e;
+                            float x[CR];
 #pragma unroll
-                            for (int j = 0; j < CR; ++j) sum[j] = 0.f;
-#pragma unroll 1
-                            for (int k = 0; k < q.n; ++k) {
-                                const float *f = weights + (row0 + j0) * q.n + k;
-                                const int last = mine - 1 - j0;
-                                float x[CR];
-                                if (k == own) {
+                            for (int j = 0; j < CR; ++j) x[j] = __ldcg(src + min(j, last) * (DS * 64));
 #pragma unroll
-                                    for (int j = 0; j < CR; ++j) x[j] = o[j];
-                                } else {
-                                    const float *src = q.at(k) + (row0 + j0) * (DS * 64) + e;
-#pragma unroll
-                                    for (int j = 0; j < CR; ++j) x[j] = __ldcg(src + min(j, last) * (DS * 64));
-                                }
-#pragma unroll
-                                for (int j = 0; j < CR; ++j) {
-                                    const float g = f[min(j, last) * q.n];
-                                    sum[j] = g == 0.f ? sum[j] : fmaf(x[j], g, sum[j]);
-                                }
+                            for (int j = 0; j < CR; ++j) {
+                                const float2 f = *reinterpret_cast<const float2 *>(scratch + 2 * (row0 + j0 + min(j, last)));
+                                const float x0 = own == 0 ? o[j] : x[j], x1 = own == 0 ? x[j] : o[j];
+                                float sum = f.x == 0.f ? 0.f : fmaf(x0, f.x, 0.f);
+                                sum = f.y == 0.f ? sum : fmaf(x1, f.y, sum);
+                                o[j] = sum;
                             }
-#pragma unroll
-                            for (int j = 0; j < CR; ++j) o[j] = sum[j];
                         }
 #pragma unroll
                         for (int j = 0; j < CR; ++j) {
@@ -860,7 +851,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             both_sync();
             if (direct && tid == 0) a.tickets[q.c0] = 0;
             if (part) {
-                attn_join<unsigned short, DS * 64>(a, q, w, rows, tok0, 256, tid, &sm.flag, weights, p_bytes(N) / 4,
+                attn_join<unsigned short, DS * 64>(a, q, w, rows, tok0, 256, tid, &sm.flag, scratch, p_bytes(N) / 4,
                                                    sm.inv, sm.row_at, both_sync);
                 both_sync();
             }
