@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
     __shared__ int s_flag;
     __shared__ alignas(16) float s_p[SIMT_KEYS * P_LD];
     __shared__ float s_f[SIMT_TILE_ROWS], s_m[SIMT_TILE_ROWS], s_inv[128];
-    __shared__ int64_t s_row[128];
+    __shared__ int s_row[128];
     const int d = a.d, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ld = d + SimtTile<E>::PAD, ldq = d + 4;
     float *sq = smem;
     E *kv = reinterpret_cast<E *>(sq + SIMT_TILE_ROWS * ldq);  // [2][keys, values][KEYS][ld]
@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
             }
         }
         if (!w.whole) {
-            if (tid < rows) s_row[tid] = attn_row(a, w.b, h, tok0, tid);
+            if (tid < rows) s_row[tid] = tid / a.group * a.Hq + tid % a.group;
             attn_join<E, 0>(a, AttnParts(a, p, w), w, rows, tok0, SIMT_THREADS, tid, &s_flag, smem,
-                            static_cast<int>(attn_simt_smem(d, sizeof(E)) / 4), s_inv, s_row, cta_sync);
+                            static_cast<int>(attn_simt_smem(d, sizeof(E)) / 4), s_inv, attn_row(a, w.b, h, tok0, 0), s_row, cta_sync);
         }
     }
 }

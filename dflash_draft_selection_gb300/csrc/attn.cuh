@@ -63,10 +63,23 @@ struct AttnReq {
     int nt;       // tiles from there (at least one: its rows are written even if nothing is seen)
 };
 
-__device__ __forceinline__ AttnReq attn_req(const AttnArgs &a, int b) {
+// What the call's arrays say of a request (0 past the last one).
+struct AttnRaw {
+    int n, nq, sp;
+};
+__device__ __forceinline__ AttnRaw attn_raw(const AttnArgs &a, int b) {
+    AttnRaw x = {0, 0, 0};
+    if (b < a.B) {
+        x.n = a.kv_len[b];
+        x.nq = a.q_len ? a.q_len[b] : a.T;
+        x.sp = a.seq_pos ? a.seq_pos[b] : 0;
+    }
+    return x;
+}
+__device__ __forceinline__ AttnReq attn_req(const AttnArgs &a, const AttnRaw &x) {
     AttnReq r;
-    int n = a.kv_len[b], nq = a.q_len ? a.q_len[b] : a.T;
-    const int sp = a.seq_pos ? a.seq_pos[b] : 0;
+    int n = x.n, nq = x.nq;
+    const int sp = x.sp;
     n = min(max(n, 0), a.max_pages * a.page_size);
     nq = min(max(nq, 0), a.T);
     r.nq = nq;
@@ -84,6 +97,7 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs &a, int b) {
     r.nt = max(last - r.first, 1);
     return r;
 }
+__device__ __forceinline__ AttnReq attn_req(const AttnArgs &a, int b) { return attn_req(a, attn_raw(a, b)); }
 
 // This CTA's stretch [begin, end) of the line and the request that holds its
 // start (`base`: the line's places before that request).
@@ -172,6 +186,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /*
 // Walks the items of a stretch.
 struct AttnWalk {
     AttnReq r;
+    AttnRaw ahead;  // of request b + 1: read before it is needed
     int b, base, at, end;
     int item;     // within the request
     int t0, t1;   // this stretch's tiles of the item (absolute: the first key is t0 * tile)
@@ -184,6 +199,7 @@ struct AttnWalk {
         at = p.begin;
         end = p.end;
         r = attn_req(a, b);
+        ahead = attn_raw(a, b + 1);
     }
     // The next item that has tiles here; false at the end of the stretch.
     __device__ __forceinline__ bool next(const AttnArgs &a) {
@@ -192,7 +208,8 @@ struct AttnWalk {
             while (at - base >= len * a.items) {
                 base += len * a.items;
                 ++b;
-                r = attn_req(a, b);
+                r = attn_req(a, ahead);
+                ahead = attn_raw(a, b + 1);
                 len = r.nt + a.item_cost;
             }
             item = (at - base) / len;
@@ -248,14 +265,6 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs &a, int b, int h, int
     return (static_cast<int64_t>(b) * a.T + tok0 + r / a.group) * a.Hq + static_cast<int64_t>(h) * a.group + r % a.group;
 }
 
-__device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t i, float v, float *) {
-    static_cast<float *>(a.out)[i] = v;
-}
-__device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t i, float v, unsigned short *) {
-    unsigned short o;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(o) : "f"(v));
-    static_cast<unsigned short *>(a.out)[i] = o;
-}
 
 __device__ __forceinline__ void attn_store4(const AttnArgs &a, int64_t i, float x, float y, float z, float w, float *) {
     *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = make_float4(x, y, z, w);
@@ -320,7 +329,8 @@ __device__ __forceinline__ float attn_join_row(int n, float *m, const float *l, 
 // (0: a.d).
 template <typename E, int D, int U, int K, typename Weight>
 __device__ __forceinline__ void attn_join_sum(const AttnArgs &a, const AttnParts &q, int rows, Weight weight,
-                                              const float *inv, const int64_t *row_at, int threads, int tid) {
+                                              const float *inv, int64_t first_row, const int *row_at, int threads,
+                                              int tid) {
     const int d = D ? D : a.d, d4 = d / 4, total = rows * d4;
 #pragma unroll 1
     for (int i0 = tid; i0 < total; i0 += U * threads) {
@@ -354,7 +364,7 @@ __device__ __forceinline__ void attn_join_sum(const AttnArgs &a, const AttnParts
         for (int u = 0; u < U; ++u)
             if (i0 + u * threads < total) {
                 const float g = inv[r[u]];
-                attn_store4(a, row_at[r[u]] * d + (at[u] - r[u] * d), g == 0.f ? 0.f : o[u].x * g,
+                attn_store4(a, (first_row + row_at[r[u]]) * d + (at[u] - r[u] * d), g == 0.f ? 0.f : o[u].x * g,
                             g == 0.f ? 0.f : o[u].y * g, g == 0.f ? 0.f : o[u].z * g, g == 0.f ? 0.f : o[u].w * g,
                             static_cast<E *>(nullptr));
             }
@@ -366,11 +376,12 @@ __device__ __forceinline__ void attn_join_sum(const AttnArgs &a, const AttnParts
 // the output's element type, D the head dimension or 0).  `scratch`
 // (`cap` floats) holds the rows' m and l; where they do not fit (very many
 // parts of many rows) the weights go over the m of the parts, which nobody
-// else reads any more.  row_at: the rows' indexes in lse.
+// else reads any more.  first_row + row_at: the rows' indexes in lse.
 template <typename E, int D, typename Sync>
 __device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnParts &q, const AttnWalk &w, int rows, int tok0,
                                           int threads, int tid, int *flag /* shared */, float *scratch, int cap,
-                                          float *inv /* shared, [rows] */, const int64_t *row_at /* shared */,
+                                          float *inv /* shared, [rows] */, int64_t first_row,
+                                          const int *row_at /* shared */,
                                           Sync sync) {
     __threadfence();
     sync();
@@ -398,12 +409,12 @@ __device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnParts &q,
             }
             lse = L == 0.f ? NEG_INF : (M + log2f(L)) * 0.6931471805599453f;
             inv[tid] = L == 0.f ? 0.f : 1.0f / L;
-            if (a.lse) a.lse[row_at[tid]] = lse;
+            if (a.lse) a.lse[first_row + row_at[tid]] = lse;
         }
         __threadfence();
         sync();
         attn_join_sum<E, D, 4, 4>(
-            a, q, rows, [&](int r, int k) { return __ldcg(q.at(k) + om + r); }, inv, row_at, threads, tid);
+            a, q, rows, [&](int r, int k) { return __ldcg(q.at(k) + om + r); }, inv, first_row, row_at, threads, tid);
         return;
     }
     float *m = scratch, *l = scratch + all;
@@ -419,16 +430,16 @@ __device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnParts &q,
     if (tid < rows) {
         float lse;
         inv[tid] = attn_join_row(q.n, m + tid * q.n, l + tid * q.n, &lse);
-        if (a.lse) a.lse[row_at[tid]] = lse;
+        if (a.lse) a.lse[first_row + row_at[tid]] = lse;
     }
     sync();
     auto weight = [&](int r, int k) { return m[r * q.n + k]; };
     if (rows * (a.d / 4) <= threads)
-        attn_join_sum<E, D, 1, 16>(a, q, rows, weight, inv, row_at, threads, tid);
+        attn_join_sum<E, D, 1, 16>(a, q, rows, weight, inv, first_row, row_at, threads, tid);
     else if (q.n > 2)
-        attn_join_sum<E, D, 2, 8>(a, q, rows, weight, inv, row_at, threads, tid);
+        attn_join_sum<E, D, 2, 8>(a, q, rows, weight, inv, first_row, row_at, threads, tid);
     else
-        attn_join_sum<E, D, 8, 2>(a, q, rows, weight, inv, row_at, threads, tid);
+        attn_join_sum<E, D, 8, 2>(a, q, rows, weight, inv, first_row, row_at, threads, tid);
 }
 
 }  // namespace dfl

@@ -7,7 +7,7 @@ namespace dfl {
 static __device__ unsigned int g_err_attn;
 
 // What an item costs beside its tiles: the drain of the pipeline, its sums and outputs, the first tile's maxima.
-constexpr int ATTN_ITEM_COST = 2;
+constexpr int ATTN_ITEM_COST = 4;
 
 dflash2_status attn_tc64(TcLaunch &t);
 dflash2_status attn_tc128(TcLaunch &t);

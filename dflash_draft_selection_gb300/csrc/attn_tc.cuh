@@ -60,7 +60,7 @@ struct TcShared {
     uint64_t p_full[2];   // P of tile n written (weights pass: its scores read)
     uint64_t pv_done[2];  // output product of tile n complete
     uint64_t q_full, q_empty, done;
-    int64_t row_at[128];  // index of the row in lse (times d: in out)
+    int row_at[128];  // index of the row in lse (times d: in out) from the item's first row's
     int scratch[TC_THREADS / 32 + 2];
     alignas(16) float neg_m[128];
     alignas(16) float fac[128];
@@ -335,6 +335,11 @@ __device__ __forceinline__ bool issue_scores(TcShared &sm, uint64_t kd, uint64_t
     return true;
 }
 
+__device__ __forceinline__ void st_bf16(unsigned short *p, float v) {
+    unsigned short o;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(o) : "f"(v));
+    *p = o;
+}
 __device__ __forceinline__ bool bad_bf16(uint32_t h) { return (h & 0x7f80u) == 0x7f80u; }
 
 // Sums of v[0 .. 7] over the warp's lanes: lane l returns row l / 4's.
@@ -354,6 +359,25 @@ __device__ __forceinline__ float lane_sums8(const float *v, int lane) {
     float c = keep + __shfl_xor_sync(FULL, send, 4);
     c += __shfl_xor_sync(FULL, c, 2);
     return c + __shfl_xor_sync(FULL, c, 1);
+}
+
+// The same for maxima.
+__device__ __forceinline__ float lane_max8(const float *v, int lane) {
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float send = (lane & 16) ? v[i] : v[i + 4], keep = (lane & 16) ? v[i + 4] : v[i];
+        a[i] = fmaxf(keep, __shfl_xor_sync(FULL, send, 16));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float send = (lane & 8) ? a[i] : a[i + 2], keep = (lane & 8) ? a[i + 2] : a[i];
+        b[i] = fmaxf(keep, __shfl_xor_sync(FULL, send, 8));
+    }
+    const float send = (lane & 4) ? b[0] : b[1], keep = (lane & 4) ? b[1] : b[0];
+    float c = fmaxf(keep, __shfl_xor_sync(FULL, send, 4));
+    c = fmaxf(c, __shfl_xor_sync(FULL, c, 2));
+    return fmaxf(c, __shfl_xor_sync(FULL, c, 1));
 }
 
 // Barriers, tensor memory, and Q's rows that no copy reaches (they stay zero).
@@ -518,12 +542,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             const int toks = min(a.tok_block, a.T - tok0), rows = toks * a.group;
             const int live = max(min(w.r.nq - tok0, toks), 0), real = live * a.group;
             const int nt = w.t1 - w.t0;
+            const int64_t first_row = attn_row(a, w.b, h, tok0, 0);
             float l[NR];
 #pragma unroll
             for (int i = 0; i < NR; ++i) l[i] = 0.f;
             if (key < NR) {
                 neg_m[key] = -M_NONE;
-                if (row0 + key < rows) sm.row_at[row0 + key] = attn_row(a, w.b, h, tok0, row0 + key);
+                if (row0 + key < rows)
+                    sm.row_at[row0 + key] = (row0 + key) / a.group * a.Hq + (row0 + key) % a.group;
             }
             if (tid == 0) sm.acc_first = 0;
             soft_sync(half);
@@ -549,6 +575,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     clean0 = static_cast<int>(
                         min((max(see0 + live - a.window, static_cast<int64_t>(0)) + TK - 1) / TK, int64_t(1) << 30));
             }
+            // This thread's key's values of tile i, 64 dims at a time (once they are there).
+            auto v_row = [&](int i, int e) {
+                const int q = seq + i * D::UPT + e / D::US;
+                tc_wait(sm, &sm.full[KU + q % VU], (q / VU) & 1, err);
+                return reinterpret_cast<uint4 *>(ring + ((KU + q % VU) * D::US + e % D::US) * SLOT_BYTES + key * 128);
+            };
             int page_now = slot_page(w.t0), page_next = slot_page(w.t0 + 1);
             int pos_now = slot_pos(w.t0, page_now);
             for (int i = 0; i < nt; ++i, ++n) {
@@ -579,26 +611,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     r0 = lo - row0;
                     r1 = none ? r0 : hi - row0;
                     masked = __any_sync(FULL, none || part);
-                    // Values of a key that no row sees are set to zero: p = 0 times NaN would be NaN.  Of a key that
-                    // only some rows see, values that are not finite are taken out and added by hand.
-                    if ((none && half == 0) || part) {
-                        const int vseq = seq + i * D::UPT;
+                    // Of a key that only some rows see, values that are not finite are taken out of the tile and
+                    // added by hand: p = 0 times NaN would be NaN.
+                    if (part) {
                         for (int e = 0; e < DS; ++e) {
-                            const int q = vseq + e / D::US;
-                            tc_wait(sm, &sm.full[KU + q % VU], (q / VU) & 1, err);
-                            uint4 *row = reinterpret_cast<uint4 *>(
-                                ring + ((KU + q % VU) * D::US + e % D::US) * SLOT_BYTES + key * 128);
+                            const uint4 *row = v_row(i, e);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                if (none) {
-                                    row[j] = make_uint4(0, 0, 0, 0);
-                                } else {
-                                    const uint4 v = row[j];
-                                    poison = poison || bad_bf16(v.x) || bad_bf16(v.x >> 16) || bad_bf16(v.y) ||
-                                             bad_bf16(v.y >> 16) || bad_bf16(v.z) || bad_bf16(v.z >> 16) ||
-                                             bad_bf16(v.w) || bad_bf16(v.w >> 16);
-                                }
+                                const uint4 v = row[j];
+                                poison = poison || bad_bf16(v.x) || bad_bf16(v.x >> 16) || bad_bf16(v.y) ||
+                                         bad_bf16(v.y >> 16) || bad_bf16(v.z) || bad_bf16(v.z >> 16) ||
+                                         bad_bf16(v.w) || bad_bf16(v.w >> 16);
                             }
+                        }
+                    }
+                if (none && half == 0) {
+                        for (int e = 0; e < DS; ++e) {
+                            uint4 *row = v_row(i, e);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) row[j] = make_uint4(0, 0, 0, 0);
                         }
                     }
                     __syncwarp();
@@ -632,14 +663,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     // the rows' maxima over the tile, new references, and what has been summed scaled to them
                     if (i > 0) tmem_ld<NR>(ts, reinterpret_cast<uint32_t *>(x));
 #pragma unroll
-                    for (int c = 0; c < NR; c += 32) {
-                        float mine = NEG_INF;
+                    for (int c = 0; c < NR; c += 8) {
+                        float y[8];
 #pragma unroll
-                        for (int j = c; j < NR && j < c + 32; ++j) {
-                            const float y = warp_max_one(masked && (j < r0 || j >= r1) ? NEG_INF : x[j] * c2);
-                            if (lane == j - c) mine = y;
-                        }
-                        if (c + lane < NR) sm.part[warp & 3][row0 + c + lane] = mine;
+                        for (int j = 0; j < 8; ++j)
+                            y[j] = masked && (c + j < r0 || c + j >= r1) ? NEG_INF : x[c + j] * c2;
+                        const float v = lane_max8(y, lane);
+                        if ((lane & 3) == 0) sm.part[warp & 3][row0 + c + lane / 4] = v;
                     }
                     soft_sync(half);
                     if (key < NR) {
@@ -803,11 +833,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         scratch[2 * r + 1] = ml[1];
                     }
                     sm.inv[r] = g;
-                    if (a.lse) a.lse[sm.row_at[r]] = lse;
+                    if (a.lse) a.lse[first_row + sm.row_at[r]] = lse;
                 }
             }
             soft_sync(half);
             if (DS > 1 || (warp & 3) < 2) {
+                unsigned short *out = static_cast<unsigned short *>(a.out) + first_row * (DS * 64);
                 constexpr int CR = NR % 24 == 0 ? 24 : NR % 16 == 0 ? 16 : 8;  // rows at a time
 #pragma unroll 1
                 for (int m = 0; m < MB; ++m) {
@@ -841,7 +872,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                                 if (part)
                                     part[r * (DS * 64) + e] = v;
                                 else
-                                    attn_store(a, sm.row_at[r] * (DS * 64) + e, v, static_cast<unsigned short *>(nullptr));
+                                    st_bf16(out + sm.row_at[r] * (DS * 64) + e, v);
                             }
                         }
                     }
@@ -852,7 +883,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             if (direct && tid == 0) a.tickets[q.c0] = 0;
             if (part) {
                 attn_join<unsigned short, DS * 64>(a, q, w, rows, tok0, 256, tid, &sm.flag, scratch, p_bytes(N) / 4,
-                                                   sm.inv, sm.row_at, both_sync);
+                                                   sm.inv, first_row, sm.row_at, both_sync);
                 both_sync();
             }
         }

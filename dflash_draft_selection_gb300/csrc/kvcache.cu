@@ -36,33 +36,41 @@ struct AppendArgs {
 
 // Where a new token goes.
 struct AppendToken {
-    bool live;     // t < q_len
-    int64_t slot;  // index (page * Hkv * page_size + off) parts:
-    int page, off;
-    int seq;
+    bool live;      // t < q_len
+    int page, off;  // page -1: nowhere
+    int seq;        // position in the sequence
 };
 
-__device__ __forceinline__ AppendToken append_token(const AppendArgs &a, int64_t tok, bool lead) {
+// What the call's arrays say of a token's request.
+struct AppendRaw {
+    int64_t b;
+    int t, n, nq, sp;
+};
+__device__ __forceinline__ AppendRaw append_raw(const AppendArgs &a, int64_t tok) {
+    AppendRaw x;
+    x.b = tok / a.T;
+    x.t = static_cast<int>(tok - x.b * a.T);
+    x.n = a.kv_len[x.b];
+    x.nq = a.q_len ? a.q_len[x.b] : a.T;
+    x.sp = a.seq_pos ? a.seq_pos[x.b] : x.n;
+    return x;
+}
+__device__ __forceinline__ AppendToken append_token(const AppendArgs &a, const AppendRaw &x, bool lead) {
     AppendToken r;
-    const int64_t b = tok / a.T;
-    const int t = static_cast<int>(tok - b * a.T);
-    const int n = a.kv_len[b];
-    int nq = a.q_len ? a.q_len[b] : a.T;
-    nq = nq < 0 ? 0 : (nq > a.T ? a.T : nq);
-    r.live = t < nq;
-    r.slot = static_cast<int64_t>(n) + t;
+    const int nq = x.nq < 0 ? 0 : (x.nq > a.T ? a.T : x.nq);
+    r.live = x.t < nq;
     r.page = -1;
     r.off = 0;
-    if (n >= 0) {
-        const int64_t pi = r.slot / a.page_size;
+    if (x.n >= 0) {
+        const int64_t slot = static_cast<int64_t>(x.n) + x.t, pi = slot / a.page_size;
         if (pi < a.max_pages) {
-            const int page = a.table[b * a.max_pages + pi];
+            const int page = a.table[x.b * a.max_pages + pi];
             if (page >= 0 && page < a.num_pages) r.page = page;
-            r.off = static_cast<int>(r.slot - pi * a.page_size);
+            r.off = static_cast<int>(slot - pi * a.page_size);
         }
     }
-    r.seq = (a.seq_pos ? a.seq_pos[b] : n) + t;
-    if (lead && t == 0 && a.kv_len_out) a.kv_len_out[b] = n + nq;
+    r.seq = x.sp + x.t;
+    if (lead && x.t == 0 && a.kv_len_out) a.kv_len_out[x.b] = x.n + nq;
     return r;
 }
 
@@ -92,7 +100,7 @@ __global__ void __launch_bounds__(256) k_append_any(AppendArgs a) {
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += step) {
         const int64_t tok = u / heads;
         const int head = static_cast<int>(u - tok * heads);
-        const AppendToken at = append_token(a, tok, head == 0 && lane == 0);
+        const AppendToken at = append_token(a, append_raw(a, tok), head == 0 && lane == 0);
         const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hkv;
         const int kh = is_q ? 0 : (is_v ? head - a.Hq - a.Hkv : head - a.Hq);
         const E *src;
@@ -212,7 +220,6 @@ __global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2
     const bool inside = unit < a.tokens * a.head_steps, mine = inside && c * 2 * N < a.d;
     const int64_t tok = inside ? unit / a.head_steps : 0;
     const int head0 = inside ? static_cast<int>(unit - tok * a.head_steps) : 0;
-    const AppendToken at = append_token(a, tok, inside && head0 == 0 && c == 0);
     const bool turned = mine && c * 2 * N < a.rot;
     int e0, e1;  // the vectors' first entries
     if (turned && !INTER) {
@@ -222,12 +229,30 @@ __global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2
         e0 = c * 2 * N;
         e1 = e0 + N;
     }
+    // The reads in the order of their dependence: what the arrays say of the token, its heads, then its row of the
+    // table and its page.
+    const AppendRaw raw = append_raw(a, tok);
+    const int id0 = a.pos_ids[tok];
+    uint4 x[APPEND_BATCH], y[APPEND_BATCH];
+#pragma unroll
+    for (int i = 0; i < APPEND_BATCH; ++i) {
+        const int h = head0 + i * a.head_steps;
+        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        if (h < heads && mine) {  // before it is known where the token goes: the reads do not wait for each other
+            const E *src = h < a.Hq ? reinterpret_cast<const E *>(a.q) + tok * a.q_stride + static_cast<int64_t>(h) * a.d
+                           : h < a.Hq + a.Hkv
+                               ? reinterpret_cast<const E *>(a.k) + tok * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.d
+                               : reinterpret_cast<const E *>(a.v) + tok * a.v_stride +
+                                     static_cast<int64_t>(h - a.Hq - a.Hkv) * a.d;
+            x[i] = *reinterpret_cast<const uint4 *>(src + e0);
+            y[i] = *reinterpret_cast<const uint4 *>(src + e1);
+        }
+    }
     float cs[N], sn[N];
     if (turned) {
         if (a.axes == 1) {
-            const int id = a.pos_ids[tok];
-            const bool ok = id >= 0 && id < a.n_pos;
-            const float *row = a.cos_sin + static_cast<int64_t>(ok ? id : 0) * a.rot + c * N;
+            const bool ok = id0 >= 0 && id0 < a.n_pos;
+            const float *row = a.cos_sin + static_cast<int64_t>(ok ? id0 : 0) * a.rot + c * N;
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
                 const float4 x = *reinterpret_cast<const float4 *>(row + i);
@@ -266,23 +291,9 @@ __global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2
         kn[0] = a.k_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.k_norm) + e0) : one;
         kn[1] = a.k_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.k_norm) + e1) : one;
     }
+    const AppendToken at = append_token(a, raw, inside && head0 == 0 && c == 0);
     const bool stored = at.live && at.page >= 0;
     const int64_t slot = at.page * a.page_stride + at.off * a.slot_stride;
-    uint4 x[APPEND_BATCH], y[APPEND_BATCH];
-#pragma unroll
-    for (int i = 0; i < APPEND_BATCH; ++i) {
-        const int h = head0 + i * a.head_steps;
-        x[i] = y[i] = make_uint4(0, 0, 0, 0);
-        if (h < heads && mine && stored) {
-            const E *src = h < a.Hq ? reinterpret_cast<const E *>(a.q) + tok * a.q_stride + static_cast<int64_t>(h) * a.d
-                           : h < a.Hq + a.Hkv
-                               ? reinterpret_cast<const E *>(a.k) + tok * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.d
-                               : reinterpret_cast<const E *>(a.v) + tok * a.v_stride +
-                                     static_cast<int64_t>(h - a.Hq - a.Hkv) * a.d;
-            x[i] = *reinterpret_cast<const uint4 *>(src + e0);
-            y[i] = *reinterpret_cast<const uint4 *>(src + e1);
-        }
-    }
 #pragma unroll
     for (int i = 0; i < APPEND_BATCH; ++i) {
         const int h = head0 + i * a.head_steps;
