@@ -151,12 +151,12 @@ def _page_table(t: torch.Tensor, B: int):
 
 def _heads(name: str, t: torch.Tensor, dt, B: int, T: int, H: int, d: int):
     """Address and token stride of [B, T, H, d] with contiguous heads and one stride from token to token."""
-    st = t.stride()
     if t.dtype is not dt or t.shape != (B, T, H, d) or not t.is_cuda:
         raise ValueError(f"{name}: {dt} [{B}, {T}, {H}, {d}] on the GPU")
-    if (st[3] != 1 and d > 1) or (st[2] != d and H > 1) or (B > 1 and T > 1 and st[0] != T * st[1]):
+    s0, s1, s2, s3 = t.stride()
+    if (s3 != 1 and d > 1) or (s2 != d and H > 1) or (B > 1 and T > 1 and s0 != T * s1):
         raise ValueError(f"{name}: contiguous heads and one stride from token to token")
-    return t.data_ptr(), st[1] if T > 1 else (st[0] if B > 1 else H * d)
+    return t.data_ptr(), s1 if T > 1 else (s0 if B > 1 else H * d)
 
 
 def _dense(name: str, t, dt, shape):

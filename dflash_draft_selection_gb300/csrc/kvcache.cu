@@ -31,7 +31,6 @@ struct AppendArgs {
     float eps;
     void *q_out;
     int32_t *kv_len_out;
-    int head_steps;  // units of a token: a thread takes heads unit, unit + head_steps, .. (at most four)
 };
 
 // Where a new token goes.
@@ -48,8 +47,9 @@ struct AppendRaw {
 };
 __device__ __forceinline__ AppendRaw append_raw(const AppendArgs &a, int64_t tok) {
     AppendRaw x;
-    x.b = tok / a.T;
-    x.t = static_cast<int>(tok - x.b * a.T);
+    const uint32_t tk = static_cast<uint32_t>(tok), b = tk / static_cast<uint32_t>(a.T);  // B * T < 2^31
+    x.b = b;
+    x.t = static_cast<int>(tk - b * static_cast<uint32_t>(a.T));
     x.n = a.kv_len[x.b];
     x.nq = a.q_len ? a.q_len[x.b] : a.T;
     x.sp = a.seq_pos ? a.seq_pos[x.b] : x.n;
@@ -62,11 +62,12 @@ __device__ __forceinline__ AppendToken append_token(const AppendArgs &a, const A
     r.page = -1;
     r.off = 0;
     if (x.n >= 0) {
-        const int64_t slot = static_cast<int64_t>(x.n) + x.t, pi = slot / a.page_size;
-        if (pi < a.max_pages) {
+        const uint32_t slot = static_cast<uint32_t>(x.n) + static_cast<uint32_t>(x.t);
+        const uint32_t pi = slot / static_cast<uint32_t>(a.page_size);
+        if (pi < static_cast<uint32_t>(a.max_pages)) {
             const int page = a.table[x.b * a.max_pages + pi];
             if (page >= 0 && page < a.num_pages) r.page = page;
-            r.off = static_cast<int>(slot - pi * a.page_size);
+            r.off = static_cast<int>(slot - pi * static_cast<uint32_t>(a.page_size));
         }
     }
     r.seq = x.sp + x.t;
@@ -164,10 +165,11 @@ __global__ void __launch_bounds__(256) k_append_any(AppendArgs a) {
     }
 }
 
-// 16-byte vectors: a lane takes two vectors of a head that are rotated
-// together (x of the pairs and y, or two vectors of neighbouring pairs), so
-// its cosines and sines serve all the heads it walks through.  A head is
-// `lanes` neighbouring lanes, which share the norm's sum.
+// 16-byte vectors: a lane takes two vectors of a head, rotated together (x of
+// the pairs and y; interleaved pairs lie within a vector), so its cosines and
+// sines serve the heads it walks through, which are all queries, all keys or
+// all values.  A head is `lanes` neighbouring lanes, which share the norm's
+// sum.  Arithmetic in packed pairs.
 //
 // Bound: the heads' bytes, read and written once (6.7 TB/s); the table's rows
 // are shared by a token's heads and stay in L1 and L2.
@@ -176,190 +178,206 @@ constexpr int APPEND_BATCH = 4;  // heads whose loads a thread has in flight
 template <typename E>
 struct Vec {
     static constexpr int N = 16 / sizeof(E);
-    uint4 v;
 };
+// A vector's entries as packed pairs of floats.
 template <typename E>
-__device__ __forceinline__ void unpack(const uint4 &v, float *x);
+__device__ __forceinline__ void unpack(const uint4 &v, uint64_t *x);
 template <>
-__device__ __forceinline__ void unpack<float>(const uint4 &v, float *x) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
+__device__ __forceinline__ void unpack<float>(const uint4 &v, uint64_t *x) {
+    x[0] = pack2(v.x, v.y);
+    x[1] = pack2(v.z, v.w);
 }
 template <>
-__device__ __forceinline__ void unpack<unsigned short>(const uint4 &v, float *x) {
+__device__ __forceinline__ void unpack<unsigned short>(const uint4 &v, uint64_t *x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16lo(w[i]);
-        x[2 * i + 1] = bf16hi(w[i]);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = pack2(w[i] << 16, w[i] & 0xffff0000u);
 }
 template <typename E>
-__device__ __forceinline__ uint4 pack(const float *x);
+__device__ __forceinline__ uint4 pack(const uint64_t *x);
 template <>
-__device__ __forceinline__ uint4 pack<float>(const float *x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+__device__ __forceinline__ uint4 pack<float>(const uint64_t *x) {
+    return make_uint4(lo32(x[0]), hi32(x[0]), lo32(x[1]), hi32(x[1]));
 }
 template <>
-__device__ __forceinline__ uint4 pack<unsigned short>(const float *x) {
+__device__ __forceinline__ uint4 pack<unsigned short>(const uint64_t *x) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+            : "=r"(w[i])
+            : "f"(__uint_as_float(hi32(x[i]))), "f"(__uint_as_float(lo32(x[i]))));
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    return pack2(__float_as_uint(lo), __float_as_uint(hi));
+}
+
+template <int W>
+__device__ __forceinline__ void cos_load(const float *p, float *x) {
+    if (W == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+        x[W > 2 ? 2 : 0] = v.z;
+        x[W > 3 ? 3 : 0] = v.w;
+    } else {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+    }
 }
 
 template <typename E, bool INTER, bool NORM>
-__global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2) {
-    constexpr int N = Vec<E>::N;
+__global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2, int per) {
+    constexpr int N = Vec<E>::N, H = N / 2;  // entries and pairs of a vector
     pdl_wait();
-    const int heads = a.Hq + 2 * a.Hkv, half = a.rot / 2;
-    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> lanes_log2;
+    const int half = a.rot / 2;
+    // a token's units: those of its queries, of its keys, of its values; a unit has heads first, first + step, ..
+    const int nq = (a.Hq + per - 1) / per, nk = (a.Hkv + per - 1) / per;
+    const uint32_t unit = blockIdx.x * (256u >> lanes_log2) + (threadIdx.x >> lanes_log2);  // below 2^32
     const int c = threadIdx.x & ((1 << lanes_log2) - 1);  // the lane's pair of vectors
-    const bool inside = unit < a.tokens * a.head_steps, mine = inside && c * 2 * N < a.d;
-    const int64_t tok = inside ? unit / a.head_steps : 0;
-    const int head0 = inside ? static_cast<int>(unit - tok * a.head_steps) : 0;
+    const uint32_t units = static_cast<uint32_t>(nq + 2 * nk), tk = unit / units;
+    const bool inside = tk < a.tokens, mine = inside && c * 2 * N < a.d;
+    const int64_t tok = inside ? tk : 0;
+    int first = inside ? static_cast<int>(unit - tk * units) : 0;
+    const bool is_q = first < nq, is_v = first >= nq + nk, lead = inside && first == 0 && c == 0;
+    first -= is_q ? 0 : is_v ? nq + nk : nq;
+    const int step = is_q ? nq : nk, heads = is_q ? a.Hq : a.Hkv;
     const bool turned = mine && c * 2 * N < a.rot;
-    int e0, e1;  // the vectors' first entries
-    if (turned && !INTER) {
-        e0 = c * N;
-        e1 = half + c * N;
-    } else {
-        e0 = c * 2 * N;
-        e1 = e0 + N;
-    }
+    // The vectors' first entries: one in each half of what is rotated, or of the rest, so that neighbouring lanes'
+    // vectors lie side by side.
+    const int e0 = turned ? c * N : a.rot + (c - half / N) * N;
+    const int e1 = e0 + (turned ? half : (a.d - a.rot) / 2);
     // The reads in the order of their dependence: what the arrays say of the token, its heads, then its row of the
     // table and its page.
     const AppendRaw raw = append_raw(a, tok);
     const int id0 = a.pos_ids[tok];
+    const E *src = is_q   ? reinterpret_cast<const E *>(a.q) + tok * a.q_stride
+                   : is_v ? reinterpret_cast<const E *>(a.v) + tok * a.v_stride
+                          : reinterpret_cast<const E *>(a.k) + tok * a.k_stride;
     uint4 x[APPEND_BATCH], y[APPEND_BATCH];
 #pragma unroll
     for (int i = 0; i < APPEND_BATCH; ++i) {
-        const int h = head0 + i * a.head_steps;
+        const int h = first + i * step;
         x[i] = y[i] = make_uint4(0, 0, 0, 0);
-        if (h < heads && mine) {  // before it is known where the token goes: the reads do not wait for each other
-            const E *src = h < a.Hq ? reinterpret_cast<const E *>(a.q) + tok * a.q_stride + static_cast<int64_t>(h) * a.d
-                           : h < a.Hq + a.Hkv
-                               ? reinterpret_cast<const E *>(a.k) + tok * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.d
-                               : reinterpret_cast<const E *>(a.v) + tok * a.v_stride +
-                                     static_cast<int64_t>(h - a.Hq - a.Hkv) * a.d;
-            x[i] = *reinterpret_cast<const uint4 *>(src + e0);
-            y[i] = *reinterpret_cast<const uint4 *>(src + e1);
+        if (i < per && h < heads && mine) {
+            x[i] = *reinterpret_cast<const uint4 *>(src + h * a.d + e0);
+            y[i] = *reinterpret_cast<const uint4 *>(src + h * a.d + e1);
         }
     }
+    // cosine i of the lane is pair pair(i)'s: entries e0 + i and e1 + i, or, interleaved, first the pairs within the
+    // vector at e0, then those within the one at e1
+    constexpr int W = INTER ? N / 2 : 4;
+    auto pair = [&](int i) { return !INTER ? c * N + i : i < N / 2 ? c * N / 2 + i : (half + c * N) / 2 + i - N / 2; };
     float cs[N], sn[N];
-    if (turned) {
+    if (turned && !is_v) {
         if (a.axes == 1) {
             const bool ok = id0 >= 0 && id0 < a.n_pos;
-            const float *row = a.cos_sin + static_cast<int64_t>(ok ? id0 : 0) * a.rot + c * N;
+            const float *row = a.cos_sin + static_cast<int64_t>(ok ? id0 : 0) * a.rot;
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(row + i);
-                const float4 y = *reinterpret_cast<const float4 *>(row + half + i);
-                cs[i] = ok ? x.x : NAN;
-                cs[i + 1] = ok ? x.y : NAN;
-                cs[i + 2] = ok ? x.z : NAN;
-                cs[i + 3] = ok ? x.w : NAN;
-                sn[i] = y.x;
-                sn[i + 1] = y.y;
-                sn[i + 2] = y.z;
-                sn[i + 3] = y.w;
+            for (int i = 0; i < N; i += W) {
+                cos_load<W>(row + pair(i), cs + i);
+                cos_load<W>(row + half + pair(i), sn + i);
             }
+#pragma unroll
+            for (int i = 0; i < N; ++i) cs[i] = ok ? cs[i] : NAN;
         } else {
             int id[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                int ax = a.pair_axis ? a.pair_axis[c * N + i] : 0;
+                int ax = a.pair_axis ? a.pair_axis[pair(i)] : 0;
                 ax = ax < a.axes ? ax : a.axes - 1;
                 id[i] = a.pos_ids[ax * a.tokens + tok];
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const bool ok = id[i] >= 0 && id[i] < a.n_pos;
-                const float *row = a.cos_sin + static_cast<int64_t>(ok ? id[i] : 0) * a.rot + c * N + i;
+                const float *row = a.cos_sin + static_cast<int64_t>(ok ? id[i] : 0) * a.rot + pair(i);
                 cs[i] = ok ? row[0] : NAN;
                 sn[i] = row[half];
             }
         }
     }
-    uint4 qn[2], kn[2];
-    if (NORM && mine) {
-        const uint4 one = make_uint4(0, 0, 0, 0);
-        qn[0] = a.q_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.q_norm) + e0) : one;
-        qn[1] = a.q_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.q_norm) + e1) : one;
-        kn[0] = a.k_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.k_norm) + e0) : one;
-        kn[1] = a.k_norm ? *reinterpret_cast<const uint4 *>(static_cast<const E *>(a.k_norm) + e1) : one;
+    const void *nw = is_q ? a.q_norm : a.k_norm;
+    const bool norm = NORM && !is_v && nw;
+    uint64_t wx[H], wy[H];
+    if (norm && mine) {
+        unpack<E>(*reinterpret_cast<const uint4 *>(static_cast<const E *>(nw) + e0), wx);
+        unpack<E>(*reinterpret_cast<const uint4 *>(static_cast<const E *>(nw) + e1), wy);
     }
-    const AppendToken at = append_token(a, raw, inside && head0 == 0 && c == 0);
+    const AppendToken at = append_token(a, raw, lead);
     const bool stored = at.live && at.page >= 0;
-    const int64_t slot = at.page * a.page_stride + at.off * a.slot_stride;
+    E *dst = is_q ? static_cast<E *>(a.q_out) + tok * a.Hq * a.d
+                  : reinterpret_cast<E *>(is_v ? a.cv : a.ck) + (at.page * a.page_stride + at.off * a.slot_stride);
+    const int64_t dst_step = is_q ? a.d : a.head_stride;
+    const float inv_d = 1.0f / a.d;
 #pragma unroll
     for (int i = 0; i < APPEND_BATCH; ++i) {
-        const int h = head0 + i * a.head_steps;
-        if (i * a.head_steps >= heads) break;  // the same for all lanes
-        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-        float u[N], v[N];
-        unpack<E>(x[i], u);
-        unpack<E>(y[i], v);
+        if (i >= per) break;
+        const int h = first + i * step;
+        uint64_t u[H], v[H];
+        if (!is_v) {
+            unpack<E>(x[i], u);
+            unpack<E>(y[i], v);
+        }
         if (NORM) {
             float ss = 0.f;
+            if (norm) {
+                uint64_t s2 = mul2(u[0], u[0]);
 #pragma unroll
-            for (int k = 0; k < N; ++k) ss = fmaf(u[k], u[k], fmaf(v[k], v[k], ss));
+                for (int k = 1; k < H; ++k) s2 = fma2(u[k], u[k], s2);
+#pragma unroll
+                for (int k = 0; k < H; ++k) s2 = fma2(v[k], v[k], s2);
+                ss = __uint_as_float(lo32(s2)) + __uint_as_float(hi32(s2));
+            }
             for (int d = 1 << lanes_log2 >> 1; d >= 1; d >>= 1) ss += __shfl_xor_sync(FULL, ss, d);
-            if (!is_v && (is_q ? a.q_norm : a.k_norm)) {
-                const float f = 1.0f / sqrtf(ss / a.d + a.eps);
-                float wu[N], wv[N];
-                unpack<E>(is_q ? qn[0] : kn[0], wu);
-                unpack<E>(is_q ? qn[1] : kn[1], wv);
+            if (norm) {
+                const float f = rsqrtf(ss * inv_d + a.eps);
+                const uint64_t ff = pair_of(f, f);
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    u[k] = u[k] * f * wu[k];
-                    v[k] = v[k] * f * wv[k];
+                for (int k = 0; k < H; ++k) {
+                    u[k] = mul2(mul2(u[k], ff), wx[k]);
+                    v[k] = mul2(mul2(v[k], ff), wy[k]);
                 }
             }
         }
         if (turned && !is_v) {
-            float s[N], t[N];
-            if (INTER) {
 #pragma unroll
-                for (int k = 0; k < N; k += 2) {
-                    s[k] = fmaf(u[k], cs[k / 2], -u[k + 1] * sn[k / 2]);
-                    s[k + 1] = fmaf(u[k + 1], cs[k / 2], u[k] * sn[k / 2]);
-                    t[k] = fmaf(v[k], cs[N / 2 + k / 2], -v[k + 1] * sn[N / 2 + k / 2]);
-                    t[k + 1] = fmaf(v[k + 1], cs[N / 2 + k / 2], v[k] * sn[N / 2 + k / 2]);
+            for (int k = 0; k < H; ++k) {
+                if (INTER) {  // (x, y) -> (x c - y s, y c + x s) within the pair
+                    const uint64_t us = pack2(hi32(u[k]), lo32(u[k])), vs = pack2(hi32(v[k]), lo32(v[k]));
+                    u[k] = fma2(u[k], pair_of(cs[k], cs[k]), mul2(us, pair_of(-sn[k], sn[k])));
+                    v[k] = fma2(v[k], pair_of(cs[H + k], cs[H + k]), mul2(vs, pair_of(-sn[H + k], sn[H + k])));
+                } else {
+                    const uint64_t c2 = pair_of(cs[2 * k], cs[2 * k + 1]), s2 = pair_of(sn[2 * k], sn[2 * k + 1]);
+                    const uint64_t t = fma2(v[k], c2, mul2(u[k], s2));
+                    u[k] = fma2(u[k], c2, mul2(v[k], pair_of(-sn[2 * k], -sn[2 * k + 1])));
+                    v[k] = t;
                 }
-            } else {
-#pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    s[k] = fmaf(u[k], cs[k], -v[k] * sn[k]);
-                    t[k] = fmaf(v[k], cs[k], u[k] * sn[k]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                u[k] = s[k];
-                v[k] = t[k];
             }
         }
-        if (!mine || h >= heads) continue;
-        if (is_q) {
-            if (!stored)
-#pragma unroll
-                for (int k = 0; k < N; ++k) u[k] = v[k] = at.live ? NAN : 0.f;
-            E *dst = static_cast<E *>(a.q_out) + (tok * a.Hq + h) * a.d;
-            *reinterpret_cast<uint4 *>(dst + e0) = pack<E>(u);
-            *reinterpret_cast<uint4 *>(dst + e1) = pack<E>(v);
-        } else if (stored) {
-            const int kh = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
-            E *dst = reinterpret_cast<E *>(is_v ? a.cv : a.ck) + slot + kh * a.head_stride;
-            *reinterpret_cast<uint4 *>(dst + e0) = is_v ? x[i] : pack<E>(u);
-            *reinterpret_cast<uint4 *>(dst + e1) = is_v ? y[i] : pack<E>(v);
-            if (!is_v && c == 0) {
-                const int64_t si = (static_cast<int64_t>(at.page) * a.Hkv + kh) * a.page_size + at.off;
-                if (a.weight) a.weight[si] = 0.f;
-                if (a.pos) a.pos[si] = at.seq;
-            }
+        if (!mine || h >= heads || (!is_q && !stored)) continue;
+        uint4 ox = x[i], oy = y[i];
+        if (!is_v) {
+            ox = pack<E>(u);
+            oy = pack<E>(v);
+        }
+        if (is_q && !stored) {
+            const uint32_t w = !at.live ? 0u : sizeof(E) == 2 ? 0x7fc07fc0u : 0x7fc00000u;  // 0 or NaN
+            ox = oy = make_uint4(w, w, w, w);
+        }
+        *reinterpret_cast<uint4 *>(dst + h * dst_step + e0) = ox;
+        *reinterpret_cast<uint4 *>(dst + h * dst_step + e1) = oy;
+        if (!is_q && !is_v && c == 0) {
+            const int64_t si = (static_cast<int64_t>(at.page) * a.Hkv + h) * a.page_size + at.off;
+            if (a.weight) a.weight[si] = 0.f;
+            if (a.pos) a.pos[si] = at.seq;
         }
     }
 }
@@ -381,7 +399,8 @@ struct EvictArgs {
     int64_t max_moves;
 };
 
-constexpr int EV_THREADS = 1024;
+constexpr int EV_THREADS = 512;  // two CTAs per SM
+constexpr int EV_WARPS = EV_THREADS / 32;
 
 __device__ __forceinline__ int evict_page(const EvictArgs &a, int64_t b, int slot) {
     const int page = a.table[b * a.max_pages + slot / a.page_size];
@@ -409,10 +428,10 @@ __device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, int64_t b, int
 constexpr int EV_KEYS = 50000;
 constexpr int EV_HISTS = 8;  // histograms, to spread the equal digits that weights have
 template <bool KEYS>
-__global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
+__global__ void __launch_bounds__(EV_THREADS, 2) k_evict_select(EvictArgs a) {
     extern __shared__ uint32_t keys[];
     __shared__ int hists[EV_HISTS][256];
-    __shared__ int s_warp[3][32];
+    __shared__ int s_warp[3][EV_WARPS];
     __shared__ uint32_t s_prefix;
     __shared__ int s_left;
     pdl_wait();
@@ -432,7 +451,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
         s_left = a.budget;
     }
     if (KEYS) {
-#pragma unroll 4
+#pragma unroll 8
         for (int s = tid; s < n; s += EV_THREADS) keys[s] = evict_key(a, b, h, s, newest);
     }
     auto key_of = [&](int s) { return KEYS ? keys[s] : evict_key(a, b, h, s, newest); };
@@ -487,7 +506,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
     const uint32_t T = s_prefix;
     const int ties = s_left;  // of the keys equal to T, the first `ties` slots stay
     // each warp takes a stretch of slots
-    const int per = ((n + 31) / 32 + 31) / 32 * 32, s0 = warp * per, s1 = s0 + per < n ? s0 + per : n;
+    const int per = ((n + EV_WARPS - 1) / EV_WARPS + 31) / 32 * 32, s0 = warp * per, s1 = s0 + per < n ? s0 + per : n;
     int eq = 0;
     for (int s = s0; s < s1; s += 32) {
         const bool in = s + lane < n;
@@ -528,7 +547,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(EvictArgs a) {
                 s_warp[2][warp] = movers;
             }
             __syncthreads();
-        } else if (warp == 31 && lane == 0) {
+        } else if (warp == EV_WARPS - 1 && lane == 0) {
             a.count[blockIdx.x] = holes;
         }
     }
@@ -599,9 +618,9 @@ static dflash2_status launch_pdl(void (*fn)(A), const A &a, dim3 grid, int threa
     return after_launch();
 }
 
-static dflash2_status launch_append_vec(AppendArgs &a, dflash2_dtype dt, bool inter, bool norm, int lanes_log2, dim3 grid,
-                                        cudaStream_t s) {
-    using Fn = void (*)(AppendArgs, int);
+static dflash2_status launch_append_vec(AppendArgs &a, dflash2_dtype dt, bool inter, bool norm, int lanes_log2, int per,
+                                        dim3 grid, cudaStream_t s) {
+    using Fn = void (*)(AppendArgs, int, int);
     using H = unsigned short;
     static const Fn table[8] = {k_append_vec<H, false, false>,     k_append_vec<H, false, true>,
                                 k_append_vec<H, true, false>,      k_append_vec<H, true, true>,
@@ -615,7 +634,7 @@ static dflash2_status launch_append_vec(AppendArgs &a, dflash2_dtype dt, bool in
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const Fn fn = table[(dt == DFLASH2_F32 ? 4 : 0) + (inter ? 2 : 0) + (norm ? 1 : 0)];
-    if (cudaLaunchKernelEx(&cfg, fn, a, lanes_log2) != cudaSuccess) return DFLASH2_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, fn, a, lanes_log2, per) != cudaSuccess) return DFLASH2_ERR_CUDA;
     return after_launch();
 }
 
@@ -692,19 +711,20 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
     a.q_out = q_out;
     a.kv_len_out = kv_len_out;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int heads = Hq + 2 * cache->Hkv, two = 32 / e;  // entries of two vectors
+    const int two = 32 / e;  // entries of two vectors
     if (rot % two == 0 && d % two == 0 && d / two <= 32) {
         int lanes_log2 = 0;
         while ((1 << lanes_log2) * two < d) ++lanes_log2;
         // Many tokens: a thread takes four heads, so that a token's cosines are read by a quarter of the threads;
         // few: one, so that there are enough threads (512 per SM).
-        const int64_t few = (static_cast<int64_t>(heads) + APPEND_BATCH - 1) / APPEND_BATCH;
-        a.head_steps = static_cast<int>((a.tokens * few << lanes_log2) >= static_cast<int64_t>(sm_count()) * 512 ? few : heads);
-        const int64_t threads = a.tokens * a.head_steps << lanes_log2;
-        if ((threads + 255) / 256 < (int64_t(1) << 31)) {
+        auto units = [&](int64_t per) { return (Hq + per - 1) / per + 2 * ((cache->Hkv + per - 1) / per); };
+        const int per = (a.tokens * units(APPEND_BATCH) << lanes_log2) >= static_cast<int64_t>(sm_count()) * 512
+                            ? APPEND_BATCH : 1;
+        const int64_t threads = a.tokens * units(per) << lanes_log2;
+        if (a.tokens * units(per) < (int64_t(1) << 32) - 256 && (threads + 255) / 256 < (int64_t(1) << 31)) {
             const dim3 vgrid(static_cast<unsigned>((threads + 255) / 256));
             const bool norm = q_norm || k_norm;
-            return launch_append_vec(a, cache->dt, interleaved != 0, norm, lanes_log2, vgrid, s);
+            return launch_append_vec(a, cache->dt, interleaved != 0, norm, lanes_log2, per, vgrid, s);
         }
     }
     const int64_t units = a.tokens * (Hq + 2 * cache->Hkv);
