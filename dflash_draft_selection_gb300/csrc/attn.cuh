@@ -105,6 +105,7 @@ struct AttnPlan {
     int total, begin, end, base, b;
     int ctas;   // the CTAs that have a stretch: no more than there are places, so that no stretch is empty
     int q, rem; // places of a stretch: q, and one more in the first rem
+    int cost;   // an item's places beside its tiles
     __device__ __forceinline__ int at(int cta) const { return q * cta + min(cta, rem); }
     // The CTA whose stretch holds place x.
     __device__ __forceinline__ int owner(int x) const {
@@ -122,7 +123,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /*
     AttnPlan p;
     int sum = 0, mine = 0;
     for (int b = tid; b < B; b += THREADS) {
-        mine = (attn_req(a, b).nt + a.item_cost) * a.items;
+        mine = attn_req(a, b).nt * a.items;
         sum += mine;
     }
     if (B == 1) {  // the only request's tiles, known to thread 0
@@ -137,6 +138,9 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /*
 #pragma unroll
         for (int w = 0; w < W; ++w) p.total += scratch[w];
     }
+    // where every tile has a CTA of its own there is nothing to balance
+    p.cost = p.total <= static_cast<int>(gridDim.x) ? 0 : a.item_cost;
+    p.total += B * a.items * p.cost;
     p.ctas = min(p.total, static_cast<int>(gridDim.x));
     p.q = p.total / p.ctas;
     p.rem = p.total - p.q * p.ctas;
@@ -152,7 +156,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /*
     int carry = 0;
     for (int at = 0; at < B; at += THREADS) {
         const int b = at + tid;
-        const int v = b < B ? (B <= THREADS ? mine : (attn_req(a, b).nt + a.item_cost) * a.items) : 0;
+        const int v = b < B ? (B <= THREADS ? mine : attn_req(a, b).nt * a.items) + p.cost * a.items : 0;
         int inc = v;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -187,7 +191,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int *scratch /*
 struct AttnWalk {
     AttnReq r;
     AttnRaw ahead;  // of request b + 1: read before it is needed
-    int b, base, at, end;
+    int b, base, at, end, cost;
     int item;     // within the request
     int t0, t1;   // this stretch's tiles of the item (absolute: the first key is t0 * tile)
     bool whole;   // the stretch holds all of the item's tiles
@@ -198,23 +202,24 @@ struct AttnWalk {
         base = p.base;
         at = p.begin;
         end = p.end;
+        cost = p.cost;
         r = attn_req(a, b);
         ahead = attn_raw(a, b + 1);
     }
     // The next item that has tiles here; false at the end of the stretch.
     __device__ __forceinline__ bool next(const AttnArgs &a) {
         while (at < end) {
-            int len = r.nt + a.item_cost;
+            int len = r.nt + cost;
             while (at - base >= len * a.items) {
                 base += len * a.items;
                 ++b;
                 r = attn_req(a, ahead);
                 ahead = attn_raw(a, b + 1);
-                len = r.nt + a.item_cost;
+                len = r.nt + cost;
             }
             item = (at - base) / len;
-            const int first = base + item * len, from = at - first - a.item_cost;  // in tiles of the item
-            const int last = min(len, end - first), to = last - a.item_cost;
+            const int first = base + item * len, from = at - first - cost;  // in tiles of the item
+            const int last = min(len, end - first), to = last - cost;
             at = first + last;
             t0 = r.first + max(from, 0);
             t1 = r.first + to;
@@ -225,8 +230,8 @@ struct AttnWalk {
         return false;
     }
     // The place of the item's first tile.
-    __device__ __forceinline__ int item_base(const AttnArgs &a) const {
-        return base + item * (r.nt + a.item_cost) + a.item_cost;
+    __device__ __forceinline__ int item_base() const {
+        return base + item * (r.nt + cost) + cost;
     }
 };
 
@@ -297,7 +302,7 @@ struct AttnParts {
     int64_t step;
     const float *base;
     __device__ __forceinline__ AttnParts(const AttnArgs &a, const AttnPlan &p, const AttnWalk &w) {
-        const int first = w.item_base(a);
+        const int first = w.item_base();
         c0 = p.owner(first);
         n = p.owner(first + w.r.nt - 1) - c0 + 1;
         step = attn_part_floats(a.rows_cap, a.d);
