@@ -448,7 +448,7 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
     if (B == 0 || T == 0) return DFLASH2_OK;
     auto al4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; };
     if (!q || !out || !kv_len || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws) || !al4(kv_len) ||
-        !al4(q_len) || !al4(seq_pos) || !al4(lse))
+        !al4(q_len) || !al4(seq_pos) || !al4(lse) || out == q)
         return DFLASH2_ERR_INVALID_ARG;
     const int group = Hq / cache->Hkv;
     if (cache->d > 256 || group > 128 || cache->num_pages >= (int64_t(1) << 31) ||

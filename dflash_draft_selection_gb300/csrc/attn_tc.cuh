@@ -575,9 +575,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     clean0 = static_cast<int>(
                         min((max(see0 + live - a.window, static_cast<int64_t>(0)) + TK - 1) / TK, int64_t(1) << 30));
             }
-            // This thread's key's values of tile i, 64 dims at a time (once they are there).
+            // This thread's key's values of tile i, 64 dims at a time (once they are there).  The ring may hold no more
+            // than one tile's values: only after the product before tile i's are its units' last contents used up, and
+            // the phase that is waited for the next one.
             auto v_row = [&](int i, int e) {
                 const int q = seq + i * D::UPT + e / D::US;
+                if (n > 0) tc_wait(sm, &sm.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
                 tc_wait(sm, &sm.full[KU + q % VU], (q / VU) & 1, err);
                 return reinterpret_cast<uint4 *>(ring + ((KU + q % VU) * D::US + e % D::US) * SLOT_BYTES + key * 128);
             };
@@ -625,7 +628,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                             }
                         }
                     }
-                if (none && half == 0) {
+                    // Values of a key that no row sees are set to zero.
+                    if (none && half == 0) {
                         for (int e = 0; e < DS; ++e) {
                             uint4 *row = v_row(i, e);
 #pragma unroll

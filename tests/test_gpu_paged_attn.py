@@ -75,6 +75,14 @@ def test_heads_and_block_lengths(dtype, d, T, Hq, Hkv):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 128, 1), (2, 128, 1), (3, 33, 1), (5, 94, 2), (1, 17, 17), (40, 3, 1)])
+def test_many_heads_on_one_cached_head(dtype, T, Hq, Hkv):
+    """Groups above a block's rows, groups that leave a block's rows unused, long blocks."""
+    check(Case(T * Hq, [max(n, T) for n in (1, 90, 290)], T, Hq, Hkv, 128, 16, dtype, held=T == 3), weights=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("page", [1, 3, 8, 16, 24, 48, 64, 128, 192, 256, 1024])
 @pytest.mark.parametrize("nhd", [False, True])
 def test_page_sizes_and_layouts(dtype, page, nhd):
@@ -192,6 +200,43 @@ def test_one_long_request_is_split_and_joined():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 8, 2), (8, 10, 2), (8, 24, 4), (16, 24, 4), (16, 16, 2)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_long_ragged_batches(d, T, Hq, Hkv, window):
+    """Batches whose stretches hold many tiles, so that copies, products and the softmax run far apart: against 64 bits
+    on the GPU, and the same bits each time.  bf16: 2^-8 sum p |v| + 2^-8 |out| as above, with e = 2^-14 for the rest."""
+    dev = cuda_or_skip()
+    B, page, G = 12, 64, Hq // Hkv
+    g = torch.Generator(device=dev).manual_seed(d + T)
+    lens = [T, 127, 9001, 300, 5003, 12288, 64, 2500, 7777, 1111, 4096, 10000]
+    per = -(-max(lens) // page)
+    k, v = (torch.randn(B * per, Hkv, page, d, generator=g, device=dev).bfloat16() for _ in range(2))
+    q = torch.randn(B, T, Hq, d, generator=g, device=dev).bfloat16()
+    table = torch.randperm(B * per, generator=g, device=dev).to(torch.int32).view(B, per)
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    cache = d2.KVCache(k, v)
+    ws = d2.Workspace.for_paged_attn(B, T, Hq, Hkv, d, BF)
+    out, lse = d2.paged_attn(q, cache, table, n, window=window, ws=ws)
+    for b in range(B):
+        s = torch.arange(lens[b], device=dev)
+        K, V = (x[table[b].long()[s // page], :, s % page].double() for x in (k, v))       # [n, Hkv, d]
+        x = torch.einsum("thgd,nhd->htgn", q[b].double().view(T, Hkv, G, d), K) * d ** -0.5
+        far = (lens[b] - T + torch.arange(T, device=dev))[:, None] - s
+        x = x.masked_fill(((far < 0) | (far >= (window or 2 ** 31)))[None, :, None], -math.inf)
+        p = x.softmax(-1)
+        r, pv = (torch.einsum("htgn,nhd->thgd", p, y).reshape(T, Hq, d) for y in (V, V.abs()))
+        off = (out[b].double() - r).abs() - (2.0 ** -8 + 2.0 ** -14) * pv - 2.0 ** -8 * r.abs()
+        assert (off <= 0).all(), (b, off.max().item())
+        z = torch.logsumexp(x, -1).permute(1, 0, 2).reshape(T, Hq)
+        assert ((lse[b].double() - z).abs() <= 2.0 ** -14 * (1 + z.abs())).all()
+    for _ in range(6):
+        again = d2.paged_attn(q, cache, table, n, window=window, ws=ws)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    assert d2.device_error() == 0
+
+
+@pytest.mark.gpu
 def test_many_requests():
     """More requests than threads of a CTA: the split over CTAs sums them in several rounds."""
     rng = np.random.default_rng(0)
@@ -283,7 +328,7 @@ def test_refusals():
     def call(cache=None, null=(), **kw):
         r = _CacheRecord(**{**ok, **(cache or {})})
         a = dict(cache=ctypes.byref(r), table=p, max_pages=4, kv_len=p, q_len=p, seq_pos=p, q=p, B=2, T=2, Hq=4,
-                 scale=0.125, window=0, flags=1, out=p, lse=p, ws=p, ws_bytes=1 << 30, stream=None)
+                 scale=0.125, window=0, flags=1, out=ctypes.c_void_p(1024), lse=p, ws=p, ws_bytes=1 << 30, stream=None)
         a.update(kw)
         for n in null:
             a[n] = None
@@ -297,7 +342,7 @@ def test_refusals():
                 dict(weight=258), dict(pos=257), dict(dt=7), dict(Hkv=3)):
         assert call(bad) == INVALID, bad
     for kw in (dict(B=-1), dict(T=-1), dict(Hq=0), dict(Hq=5), dict(scale=math.nan), dict(scale=math.inf),
-               dict(window=-1), dict(flags=4), dict(max_pages=0), dict(q=ctypes.c_void_p(264)),
+               dict(window=-1), dict(flags=4), dict(out=ctypes.c_void_p(512), q=ctypes.c_void_p(512)), dict(max_pages=0), dict(q=ctypes.c_void_p(264)),
                dict(kv_len=ctypes.c_void_p(258))):
         assert call(**kw) == INVALID, kw
     assert call(flags=2, lse=None) == INVALID and call(dict(weight=None), flags=2) == INVALID
