@@ -670,7 +670,7 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
         !aligned16(v) || !aligned16(q_out) || !aligned16(q_norm) || !aligned16(k_norm) || !aligned16(cos_sin) ||
         !al4(kv_len) || !al4(q_len) || !al4(seq_pos) || !al4(pos_ids) || !al4(kv_len_out) || q_stride < Hq * d ||
         k_stride < cache->Hkv * d || v_stride < cache->Hkv * d || q_stride * e % 16 || k_stride * e % 16 ||
-        v_stride * e % 16)
+        v_stride * e % 16 || kv_len_out == kv_len)
         return DFLASH2_ERR_INVALID_ARG;
     if (d > 1024 || B * T >= (int64_t(1) << 31)) return DFLASH2_ERR_UNSUPPORTED;
     AppendArgs a = {};

@@ -449,7 +449,7 @@ typedef struct {
  * the table, or a page id out of range) is not stored and its query comes
  * out NaN.
  * Errors: the common ones; INVALID_ARG for NULL q, k, v, q_out, kv_len,
- * cos_sin or pos_ids; Hq < 1, rot odd, < 2 or > d, axes < 1, n_pos < 1, strides
+ * cos_sin or pos_ids; kv_len_out the same as kv_len; Hq < 1, rot odd, < 2 or > d, axes < 1, n_pos < 1, strides
  * below the width of a token's heads or not multiples of 16 bytes; dt not
  * F32 or BF16.  UNSUPPORTED for d > 1024 or B * T >= 2^31.
  */
@@ -478,8 +478,8 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  * adds no weight; tokens t >= q_len[b] are such rows.  What lies in slots
  * that a row does not see (NaN and Inf too) does not touch it.
  *
- * q, out [B, T, Hq, d] of dt, contiguous; lse [B, T, Hq] f32 (may be NULL
- *   without DFLASH2_ATTN_WEIGHTS).
+ * q, out [B, T, Hq, d] of dt, contiguous, not overlapping; lse [B, T, Hq] f32
+ *   (may be NULL without DFLASH2_ATTN_WEIGHTS).
  * kv_len [B]: slots in use, the new tokens among them; clamped to what the
  *   table can hold.  q_len [B] or NULL (all T).  seq_pos [B]: the position
  *   of the block's first token, or NULL (kv_len - q_len).
@@ -488,8 +488,8 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  * over the GPU and the parts are joined in a fixed order: the same call gives
  * the same bits.
  * ws: dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, dt) bytes.
- * Errors: the common ones; INVALID_ARG for NULL q, out or kv_len, lse or the
- * cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a positive multiple of
+ * Errors: the common ones; INVALID_ARG for NULL q, out or kv_len, out the same
+ * as q, lse or the cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a positive multiple of
  * Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
  * small; UNSUPPORTED for d > 256, Hq / Hkv > 128, num_pages >= 2^31,
  * max_pages * page_size >= 2^31 - 256 or

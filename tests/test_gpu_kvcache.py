@@ -227,6 +227,32 @@ def test_evict_bad_page_ids():
         assert torch.equal(bits(x), bits(y))
 
 
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Appends to and evictions in pages at the end of a pool of more than 2^31 elements."""
+    dev = cuda_or_skip()
+    c = Case(16, [60, 33], 3, 8, 2, 128, 32, held=True)
+    m, extra = c.k.shape[0], 2 ** 31 // (2 * 32 * 128) + 64
+    pools = [torch.zeros(extra, 2, 32, 128, dtype=BF, device=dev) for _ in range(2)]
+    side = [torch.zeros(extra, 2, 32, dtype=t, device=dev) for t in (torch.float32, torch.int32)]
+    small = c.on(dev)["cache"]
+    for x, y in zip(pools + side, (small.k, small.v, small.weight, small.pos)):
+        x[-m:] = y
+    far = d2.KVCache(*pools, weight=side[0], pos=side[1])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    a = append_inputs(c, 1)
+    x = a["qkv"].to(dev)
+    tables = c.table.to(dev), (c.table.to(dev) + (extra - m)).to(torch.int32)
+    got = [d2.rope_append(x[:, :, :8], x[:, :, 8:10], x[:, :, 10:], a["cos_sin"].to(dev), a["pos_ids"].to(dev), cache,
+                          table, i32([57, 30])) for cache, table in zip((small, far), tables)]
+    assert torch.equal(got[0][0], got[1][0])
+    lens = [d2.kv_evict(cache, table, n, 40, recent=3, sink=1, seq_len=i32([200, 200]))
+            for cache, table, (_, n) in zip((small, far), tables, got)]
+    assert lens[0].tolist() == lens[1].tolist() == [40, 33]
+    for y, z in zip((small.k, small.v, small.weight, small.pos), (far.k, far.v, far.weight, far.pos)):
+        assert torch.equal(bits(y), bits(z[-m:]))
+
+
 def test_refusals():
     """Bad arguments are refused before anything is launched (no GPU needed)."""
     from dflash_draft_selection_gb300 import build
@@ -242,7 +268,7 @@ def test_refusals():
         r = _CacheRecord(**{**ok, **(rec or {})})
         a = dict(cache=ctypes.byref(r), table=p, max_pages=4, kv_len=p, q_len=p, seq_pos=p, q=p, k=p, v=p, qs=256,
                  ks=128, vs=128, B=2, T=2, Hq=4, cos_sin=p, n_pos=10, rot=64, pos_ids=p, axes=1, pair_axis=None,
-                 interleaved=0, q_norm=p, k_norm=p, eps=1e-6, q_out=p, kv_len_out=p, stream=None)
+                 interleaved=0, q_norm=p, k_norm=p, eps=1e-6, q_out=p, kv_len_out=ctypes.c_void_p(512), stream=None)
         a.update(kw)
         return L.dflash2_rope_append(*a.values())
 
@@ -255,6 +281,7 @@ def test_refusals():
                dict(qs=248), dict(ks=120), dict(vs=129), dict(q=ctypes.c_void_p(264)), dict(kv_len=odd),
                dict(q_norm=ctypes.c_void_p(264)), dict(kv_len_out=odd), dict(max_pages=0)):
         assert append(**kw) == INVALID, kw
+    assert append(kv_len_out=p) == INVALID     # the lengths before and after in one array
     assert append(dict(d=1032, slot_stride=1032), qs=8192, ks=4096, vs=4096) == UNSUPPORTED
     assert append(B=2 ** 30, T=2) == UNSUPPORTED
 
