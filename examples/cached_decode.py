@@ -30,9 +30,10 @@ class Model:
         self.V, self.hidden, self.Hq, self.Hkv, self.d, self.K = V, hidden, Hq, Hkv, d, K
         self.embed = rand(V, hidden, s=1.0)
         self.qkv = rand(hidden, (Hq + 2 * Hkv) * d, s=hidden ** -0.5)
-        self.out = rand(Hq * d, hidden, s=(Hq * d) ** -0.5)
+        self.out = rand(Hq * d, hidden, s=0.2 * (Hq * d) ** -0.5)
         self.head = rand(V, hidden, s=4 * hidden ** -0.5)
-        self.draft = rand(K, hidden, s=0.5)                    # one offset per drafted position
+        # one offset per drafted position; none for the first, which the drafter therefore often gets right
+        self.draft = rand(K, hidden, s=0.5) * (torch.arange(K, device=device) > 0)[:, None]
         self.q_norm, self.k_norm = 1 + rand(d, s=0.1), 1 + rand(d, s=0.1)
         self.A, self.Bt, self.Wg = rand(V, rank, s=1 / 16), rand(V, rank, s=1 / 16), rand(rank, hidden, s=1 / 16)
         angle = torch.arange(max_pos, device=device).double()[:, None] * \
@@ -53,7 +54,6 @@ class Server:
         i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device=dev)  # noqa: E731
         self.slots, self.length = i32(B), i32(B)               # slots in use, tokens in the sequence
         self.last = torch.randint(0, m.V, (B,), device=dev, dtype=torch.int32)
-        self.hidden = m.embed[self.last.long()]                # of the last accepted token
         self.step_ids = torch.arange(self.T, device=dev, dtype=torch.int32)
         self.ws_head = d2.Workspace.for_lmhead(B * m.K, m.V)
         self.ws_attn = d2.Workspace.for_paged_attn(B, self.T, m.Hq, m.Hkv, m.d, torch.bfloat16)
@@ -77,7 +77,7 @@ class Server:
         """One draft, verify and cut.  Returns (accepted tokens per request, the block's output tokens, the block's
         tokens, its hidden states)."""
         m, B, K = self.m, self.B, self.m.K
-        h = (self.hidden[:, None] + m.draft).contiguous()      # [B, K, hidden]
+        h = m.embed[self.last.long()][:, None] + m.draft       # [B, K, hidden]
         cand, U, _ = d2.lmhead_topk16(h.view(B * K, -1), m.head, ws=self.ws_head)
         gate = d2.ctx_gate(h.view(B * K, -1), m.Wg)
         cand, U = cand.view(B, K, 16), U.view(B, K, 16)
@@ -88,9 +88,7 @@ class Server:
         accepted, out, _ = d2.verify(logits, path, cand, q_sel, slot, ws=self.ws_verify)
         keep = accepted + 1                                    # the block's first token and the accepted ones
         self.slots, self.length = self.slots + keep, self.length + keep
-        at = accepted.long()
-        self.last = out.gather(1, at[:, None])[:, 0].contiguous()
-        self.hidden = states[torch.arange(B, device=at.device), at]
+        self.last = out.gather(1, accepted.long()[:, None])[:, 0].contiguous()
         self.slots = d2.kv_evict(self.cache, self.table, self.slots, self.budget, recent=self.recent, sink=self.sink,
                                  seq_len=self.length, ws=self.ws_evict)
         return accepted, out, block, states
