@@ -6,8 +6,10 @@
 // keys and the head dimension on its 128-wide M side:
 //   S^T [128 keys x N rows]  = K [128 x d] . Q^T       per tile of 128 keys
 //   O^T [d x N rows]        += V^T [d x 128] . P^T      (d in blocks of 128)
-// N is 16 to 128: a single token's few rows cost a sixteenth of the
-// tensor work that padding the rows to the M side would.  K and V tiles go
+// N is 16 to 128, so the softmax works on the rows there are; padded to the M
+// side, a single token's few rows would cost it 128.  (The products take the
+// same time either way: 56 cycles for 16 steps of the contraction at N up to
+// 64, 64 cycles at 128, whatever the operands' layouts.)  K and V tiles go
 // from the pages to shared memory by TMA exactly as they lie there (V^T is
 // the M-major reading of the same rows), and each is read once.
 //
@@ -26,9 +28,20 @@
 // overflows, and the result is the same up to rounding): then the sums and
 // O^T are multiplied by 2^(m - m'), which is rare.
 //
-// Bound: HBM.  A tile is d * 512 bytes (3000 cycles of an SM's share of
-// bandwidth for d = 128); the tensor cores need 16 k-steps of N / 2 cycles
-// for it.
+// Bound: HBM.  A tile is d * 512 bytes, 2800 cycles of an SM's share of the
+// bandwidth for d = 128, and 900 to 1000 cycles of the tensor cores.
+// Measured (d 128 unless said, bytes of keys and values over the time):
+//   one token, 5 rows, 131071 slots x 8 heads         89 us, 6.0 TB/s
+//   32 requests of 1 to 16384 slots, 40 rows         181 us, 6.2 TB/s
+//   16 requests of 500 to 16384 slots, d 256, 96 rows 117 us, 4.8 TB/s
+//   64 requests, window 2048, 40 rows                 61 us, 4.0 TB/s
+// What is left is the change from item to item: the last product's drain, the
+// outputs, the join of cut items and the next item's first tile take 10000 to
+// 16000 cycles, during which only the ring fills.  With wide heads and 96 rows
+// the ring holds one tile, so copies also wait for products.
+// Tried and slower: one ring for keys and values (256 us for the second case
+// with four times the copies per tile), a lane looping over a tile's copies
+// (340 us), cp.async (3 TB/s at best).
 //
 // Rounding: scores, sums and O^T are fp32; P is rounded to bf16 because the
 // MMA takes bf16 beside bf16 values; the sums are of the unrounded p.
@@ -908,7 +921,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
 // cached head) and a row block is a round over the stretch's tiles, so one
 // CTA has all of a key's rows, one thread adds to a key's word, and its
 // additions have an order.  Warps 0-3 take the even tiles and warps 4-7 the
-// odd ones, each thread one key and all rows.  Bound: the keys' bytes.
+// odd ones, each thread one key and all rows.  Bound: the keys' bytes; 16
+// requests of 2048 to 4160 slots x 8 heads of 128, 4 rows: 30 us (105 MB, 3.5
+// TB/s), of them 10 before the first tile and after the last.
 template <int N, int DS>
 __global__ void __launch_bounds__(TC_THREADS, 1) k_weights_tc(const __grid_constant__ CUtensorMap mk,
                                                               const __grid_constant__ CUtensorMap mq,

@@ -171,8 +171,12 @@ __global__ void __launch_bounds__(256) k_append_any(AppendArgs a) {
 // all values.  A head is `lanes` neighbouring lanes, which share the norm's
 // sum.  Arithmetic in packed pairs.
 //
-// Bound: the heads' bytes, read and written once (6.7 TB/s); the table's rows
-// are shared by a token's heads and stay in L1 and L2.
+// Bound: the heads' bytes, read and written once; the table's rows are shared
+// by a token's heads and stay in L1 and L2.  16384 tokens of 32 heads of 256,
+// three axes, normalised (537 MB): 150 us, 3.6 TB/s, where the issue slots of
+// two CTAs per SM are half used and the rest waits for dependent reads; more
+// CTAs in fewer registers (158 to 188 us), eight heads per thread (206 us) and
+// two (190 us) were slower.  One token of 28 heads: 2.4 us.
 constexpr int APPEND_BATCH = 4;  // heads whose loads a thread has in flight
 
 template <typename E>
@@ -424,7 +428,9 @@ __device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, int64_t b, int
 // radix select (8 bits each), then the kept slots in slot order by ballots.
 // The keys are made once and stay in shared memory (KEYS: the table's slots
 // fit it, 50000 of them), so weights and positions are read once; otherwise
-// every pass makes them again.  Bound: those reads, and the passes' latency.
+// every pass makes them again.  Bound: the latency of the passes and their
+// barriers (8 heads of 32 requests with up to 8192 slots: 35 us for 16 MB;
+// 2112 slots: 15 us).  Adding once per digit and warp (match) was slower, 43 us.
 constexpr int EV_KEYS = 50000;
 constexpr int EV_HISTS = 8;  // histograms, to spread the equal digits that weights have
 template <bool KEYS>
@@ -555,8 +561,10 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_evict_select(EvictArgs a) {
 
 // The moves of every (request, head): a warp takes eight at a time, one lane
 // per move for its places, and 16 bytes per lane of all of them in flight.
+// 32 requests cut from 8192 to 4096 keys (144 MB moved): 57 us, 4.6 TB/s read and written; three CTAs per SM instead
+// of two took it from 64.
 constexpr int EV_BATCH = 8;
-__global__ void __launch_bounds__(256) k_evict_move(EvictArgs a) {
+__global__ void __launch_bounds__(256, 3) k_evict_move(EvictArgs a) {
     pdl_wait();
     const int64_t b = blockIdx.x / a.Hkv;
     const int h = static_cast<int>(blockIdx.x % a.Hkv);
