@@ -424,6 +424,54 @@ __device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, int64_t b, int
     return f2ord(w == 0.f ? 0.f : w);
 }
 
+__device__ __forceinline__ void evict_length(const EvictArgs &a, int64_t b) {
+    const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
+    const int64_t n = a.kv_len[b] < cap ? a.kv_len[b] : cap;
+    a.kv_len_out[b] = static_cast<int>(n < 0 ? 0 : (n < a.budget ? n : a.budget));
+}
+
+// Moves of a (request, head): a warp takes eight at a time (the first warp of
+// `stride` warps has moves 8 first .. 8 first + 7), one lane per move for its
+// places, and 16 bytes per lane of all of them in flight.
+constexpr int EV_BATCH = 8;
+__device__ __forceinline__ void evict_moves(const EvictArgs &a, int64_t b, int h, const int2 *m, int count, int first,
+                                            int stride, int lane) {
+    const int vecs = a.row_bytes / 16;
+    for (int i = first * EV_BATCH; i < count; i += stride * EV_BATCH) {
+        int64_t from = -1, to = 0;  // of lane's move, if it has one
+        if (lane < EV_BATCH && i + lane < count) {
+            const int2 mv = m[i + lane];
+            const int ps = evict_page(a, b, mv.x), pd = evict_page(a, b, mv.y);
+            if (ps >= 0 && pd >= 0) {
+                const int os = mv.x % a.page_size, od = mv.y % a.page_size;
+                from = ps * a.page_bytes + h * a.head_bytes + os * a.slot_bytes;
+                to = pd * a.page_bytes + h * a.head_bytes + od * a.slot_bytes;
+                const int64_t is = (static_cast<int64_t>(ps) * a.Hkv + h) * a.page_size + os;
+                const int64_t id = (static_cast<int64_t>(pd) * a.Hkv + h) * a.page_size + od;
+                a.weight[id] = a.weight[is];
+                a.pos[id] = a.pos[is];
+            }
+        }
+        int64_t f[EV_BATCH], t[EV_BATCH];
+#pragma unroll
+        for (int k = 0; k < EV_BATCH; ++k) {
+            f[k] = __shfl_sync(FULL, from, k);
+            t[k] = __shfl_sync(FULL, to, k);
+        }
+        for (int j = lane; j < 2 * vecs; j += 32) {
+            char *base = j < vecs ? a.ck : a.cv;
+            const int64_t o = static_cast<int64_t>(j < vecs ? j : j - vecs) * 16;
+            uint4 x[EV_BATCH];
+#pragma unroll
+            for (int k = 0; k < EV_BATCH; ++k)
+                if (f[k] >= 0) x[k] = *reinterpret_cast<const uint4 *>(base + f[k] + o);
+#pragma unroll
+            for (int k = 0; k < EV_BATCH; ++k)
+                if (f[k] >= 0) *reinterpret_cast<uint4 *>(base + t[k] + o) = x[k];
+        }
+    }
+}
+
 // One CTA per (request, head): the budget-th largest key by four passes of a
 // radix select (8 bits each), then the kept slots in slot order by ballots.
 // The keys are made once and stay in shared memory (KEYS: the table's slots
@@ -432,8 +480,13 @@ __device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, int64_t b, int
 // barriers (8 heads of 32 requests with up to 8192 slots: 35 us for 16 MB;
 // 2112 slots: 15 us).  Adding once per digit and warp (match) was slower, 43 us.
 constexpr int EV_KEYS = 50000;
+// Moves per head up to which the selecting CTA makes them itself.  GPU time of one launch and of two, in us: 64 moves,
+// 128 heads 14.9 and 15.5, 16 heads 14.4 and 15.3; 256 moves 19.7 and 19.9, 18.9 and 16.5; 1024 moves 48.5 and 38.8,
+// 34.5 and 18.2.  A launch less also saves the caller 3 us.
+constexpr int EVICT_FEW = 128;
 constexpr int EV_HISTS = 8;  // histograms, to spread the equal digits that weights have
-template <bool KEYS>
+// MOVE: the CTA carries its head's moves out itself, in one launch.
+template <bool KEYS, bool MOVE>
 __global__ void __launch_bounds__(EV_THREADS, 2) k_evict_select(EvictArgs a) {
     extern __shared__ uint32_t keys[];
     __shared__ int hists[EV_HISTS][256];
@@ -447,8 +500,9 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_evict_select(EvictArgs a) {
     const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
     const int64_t n64 = a.kv_len[b] < cap ? a.kv_len[b] : cap;
     const int n = static_cast<int>(n64);
+    if (MOVE && h == 0 && tid == 0) evict_length(a, b);
     if (n <= a.budget) {
-        if (tid == 0) a.count[blockIdx.x] = 0;
+        if (!MOVE && tid == 0) a.count[blockIdx.x] = 0;
         return;
     }
     const int64_t newest = a.seq_len ? a.seq_len[b] : n64;
@@ -554,62 +608,28 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_evict_select(EvictArgs a) {
             }
             __syncthreads();
         } else if (warp == EV_WARPS - 1 && lane == 0) {
-            a.count[blockIdx.x] = holes;
+            if (MOVE)
+                s_left = holes;
+            else
+                a.count[blockIdx.x] = holes;
         }
+    }
+    if (MOVE) {
+        __syncthreads();
+        evict_moves(a, b, h, a.moves + static_cast<int64_t>(blockIdx.x) * a.max_moves, s_left, warp, EV_WARPS, lane);
     }
 }
 
-// The moves of every (request, head): a warp takes eight at a time, one lane
-// per move for its places, and 16 bytes per lane of all of them in flight.
-// 32 requests cut from 8192 to 4096 keys (144 MB moved): 57 us, 4.6 TB/s read and written; three CTAs per SM instead
+// The moves as a kernel of their own.  32 requests cut from 8192 to 4096 keys
+// (144 MB moved): 57 us, 4.6 TB/s read and written; three CTAs per SM instead
 // of two took it from 64.
-constexpr int EV_BATCH = 8;
 __global__ void __launch_bounds__(256, 3) k_evict_move(EvictArgs a) {
     pdl_wait();
     const int64_t b = blockIdx.x / a.Hkv;
     const int h = static_cast<int>(blockIdx.x % a.Hkv);
-    const int lane = threadIdx.x & 31;
-    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
-        const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
-        const int64_t n = a.kv_len[b] < cap ? a.kv_len[b] : cap;
-        a.kv_len_out[b] = static_cast<int>(n < 0 ? 0 : (n < a.budget ? n : a.budget));
-    }
-    const int count = a.count[blockIdx.x];
-    const int2 *m = a.moves + static_cast<int64_t>(blockIdx.x) * a.max_moves;
-    const int vecs = a.row_bytes / 16;
-    for (int i = (blockIdx.y * 8 + (threadIdx.x >> 5)) * EV_BATCH; i < count; i += gridDim.y * 8 * EV_BATCH) {
-        int64_t from = -1, to = 0;  // of lane's move, if it has one
-        if (lane < EV_BATCH && i + lane < count) {
-            const int2 mv = m[i + lane];
-            const int ps = evict_page(a, b, mv.x), pd = evict_page(a, b, mv.y);
-            if (ps >= 0 && pd >= 0) {
-                const int os = mv.x % a.page_size, od = mv.y % a.page_size;
-                from = ps * a.page_bytes + h * a.head_bytes + os * a.slot_bytes;
-                to = pd * a.page_bytes + h * a.head_bytes + od * a.slot_bytes;
-                const int64_t is = (static_cast<int64_t>(ps) * a.Hkv + h) * a.page_size + os;
-                const int64_t id = (static_cast<int64_t>(pd) * a.Hkv + h) * a.page_size + od;
-                a.weight[id] = a.weight[is];
-                a.pos[id] = a.pos[is];
-            }
-        }
-        int64_t f[EV_BATCH], t[EV_BATCH];
-#pragma unroll
-        for (int k = 0; k < EV_BATCH; ++k) {
-            f[k] = __shfl_sync(FULL, from, k);
-            t[k] = __shfl_sync(FULL, to, k);
-        }
-        for (int j = lane; j < 2 * vecs; j += 32) {
-            char *base = j < vecs ? a.ck : a.cv;
-            const int64_t o = static_cast<int64_t>(j < vecs ? j : j - vecs) * 16;
-            uint4 x[EV_BATCH];
-#pragma unroll
-            for (int k = 0; k < EV_BATCH; ++k)
-                if (f[k] >= 0) x[k] = *reinterpret_cast<const uint4 *>(base + f[k] + o);
-#pragma unroll
-            for (int k = 0; k < EV_BATCH; ++k)
-                if (f[k] >= 0) *reinterpret_cast<uint4 *>(base + t[k] + o) = x[k];
-        }
-    }
+    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) evict_length(a, b);
+    evict_moves(a, b, h, a.moves + static_cast<int64_t>(blockIdx.x) * a.max_moves, a.count[blockIdx.x],
+                blockIdx.y * 8 + (threadIdx.x >> 5), gridDim.y * 8, threadIdx.x & 31);
 }
 
 template <typename A>
@@ -791,14 +811,19 @@ extern "C" dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int64_t heads = B * cache->Hkv;
     const dim3 sgrid(static_cast<unsigned>(heads));
-    dflash2_status st;
-    if (cap <= EV_KEYS) {
-        blocks_per_sm(reinterpret_cast<const void *>(&k_evict_select<true>), EV_THREADS, EV_KEYS * 4);
-        st = launch_pdl(k_evict_select<true>, a, sgrid, EV_THREADS, static_cast<size_t>(cap) * 4, s);
-    } else {
-        st = launch_pdl(k_evict_select<false>, a, sgrid, EV_THREADS, 0, s);
-    }
-    if (st != DFLASH2_OK) return st;
+    // One launch where a head has few moves to make; a launch of its own spreads many over the GPU.  Lengths in one
+    // array need the second launch: heads read what one would write.
+    const bool one = a.max_moves <= EVICT_FEW && kv_len_out != kv_len;
+    auto select = [&](auto *fn, size_t most, size_t bytes) {
+        blocks_per_sm(reinterpret_cast<const void *>(fn), EV_THREADS, most);  // raises the shared-memory limit, once
+        return launch_pdl(fn, a, sgrid, EV_THREADS, bytes, s);
+    };
+    const size_t keys = cap <= EV_KEYS ? static_cast<size_t>(cap) * 4 : 0;
+    const dflash2_status st = keys ? (one ? select(&k_evict_select<true, true>, EV_KEYS * 4, keys)
+                                          : select(&k_evict_select<true, false>, EV_KEYS * 4, keys))
+                                   : (one ? select(&k_evict_select<false, true>, 0, 0)
+                                          : select(&k_evict_select<false, false>, 0, 0));
+    if (st != DFLASH2_OK || one) return st;
     int64_t x = (a.max_moves + 8 * EV_BATCH - 1) / (8 * EV_BATCH);
     const int64_t want = (static_cast<int64_t>(sm_count()) * 16 + heads - 1) / heads;
     if (x > want) x = want;
