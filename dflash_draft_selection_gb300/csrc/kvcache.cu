@@ -173,10 +173,11 @@ __global__ void __launch_bounds__(256) k_append_any(AppendArgs a) {
 //
 // Bound: the heads' bytes, read and written once; the table's rows are shared
 // by a token's heads and stay in L1 and L2.  16384 tokens of 32 heads of 256,
-// three axes, normalised (537 MB): 150 us, 3.6 TB/s, where the issue slots of
-// two CTAs per SM are half used and the rest waits for dependent reads; more
-// CTAs in fewer registers (158 to 188 us), eight heads per thread (206 us) and
-// two (190 us) were slower.  One token of 28 heads: 2.4 us.
+// three axes, normalised (537 MB): 155 us, 3.5 TB/s, where the issue slots of
+// two CTAs per SM are half used and the rest waits for dependent reads (such
+// blocks stream through shared memory instead, below); more CTAs in fewer
+// registers (158 to 188 us), eight heads per thread (206 us) and two (190 us)
+// were slower.  One token of 28 heads: 2.4 us.
 constexpr int APPEND_BATCH = 4;  // heads whose loads a thread has in flight
 
 template <typename E>
@@ -234,6 +235,38 @@ __device__ __forceinline__ void cos_load(const float *p, float *x) {
         const float2 v = *reinterpret_cast<const float2 *>(p);
         x[0] = v.x;
         x[1] = v.y;
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ float sum_squares(const uint4 &x, const uint4 &y) {
+    constexpr int H = Vec<E>::N / 2;
+    uint64_t u[H], v[H];
+    unpack<E>(x, u);
+    unpack<E>(y, v);
+    uint64_t s2 = mul2(u[0], u[0]);
+#pragma unroll
+    for (int k = 1; k < H; ++k) s2 = fma2(u[k], u[k], s2);
+#pragma unroll
+    for (int k = 0; k < H; ++k) s2 = fma2(v[k], v[k], s2);
+    return __uint_as_float(lo32(s2)) + __uint_as_float(hi32(s2));
+}
+
+// A vector pair's rotation: (x, y) -> (x c - y s, y c + x s).
+template <bool INTER, int H>
+__device__ __forceinline__ void append_turn(uint64_t *u, uint64_t *v, const float *cs, const float *sn) {
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+        if (INTER) {  // within the packed pair
+            const uint64_t us = pack2(hi32(u[k]), lo32(u[k])), vs = pack2(hi32(v[k]), lo32(v[k]));
+            u[k] = fma2(u[k], pair_of(cs[k], cs[k]), mul2(us, pair_of(-sn[k], sn[k])));
+            v[k] = fma2(v[k], pair_of(cs[H + k], cs[H + k]), mul2(vs, pair_of(-sn[H + k], sn[H + k])));
+        } else {
+            const uint64_t c2 = pair_of(cs[2 * k], cs[2 * k + 1]), s2 = pair_of(sn[2 * k], sn[2 * k + 1]);
+            const uint64_t t = fma2(v[k], c2, mul2(u[k], s2));
+            u[k] = fma2(u[k], c2, mul2(v[k], pair_of(-sn[2 * k], -sn[2 * k + 1])));
+            v[k] = t;
+        }
     }
 }
 
@@ -321,6 +354,14 @@ __global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2
                   : reinterpret_cast<E *>(is_v ? a.cv : a.ck) + (at.page * a.page_stride + at.off * a.slot_stride);
     const int64_t dst_step = is_q ? a.d : a.head_stride;
     const float inv_d = 1.0f / a.d;
+    float ss[APPEND_BATCH];
+    if (NORM) {  // the heads' sums go through the lanes side by side
+#pragma unroll
+        for (int i = 0; i < APPEND_BATCH; ++i) ss[i] = norm ? sum_squares<E>(x[i], y[i]) : 0.f;
+        for (int d = 1 << lanes_log2 >> 1; d >= 1; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < APPEND_BATCH; ++i) ss[i] += __shfl_xor_sync(FULL, ss[i], d);
+    }
 #pragma unroll
     for (int i = 0; i < APPEND_BATCH; ++i) {
         if (i >= per) break;
@@ -330,42 +371,16 @@ __global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2
             unpack<E>(x[i], u);
             unpack<E>(y[i], v);
         }
-        if (NORM) {
-            float ss = 0.f;
-            if (norm) {
-                uint64_t s2 = mul2(u[0], u[0]);
-#pragma unroll
-                for (int k = 1; k < H; ++k) s2 = fma2(u[k], u[k], s2);
-#pragma unroll
-                for (int k = 0; k < H; ++k) s2 = fma2(v[k], v[k], s2);
-                ss = __uint_as_float(lo32(s2)) + __uint_as_float(hi32(s2));
-            }
-            for (int d = 1 << lanes_log2 >> 1; d >= 1; d >>= 1) ss += __shfl_xor_sync(FULL, ss, d);
-            if (norm) {
-                const float f = rsqrtf(ss * inv_d + a.eps);
-                const uint64_t ff = pair_of(f, f);
-#pragma unroll
-                for (int k = 0; k < H; ++k) {
-                    u[k] = mul2(mul2(u[k], ff), wx[k]);
-                    v[k] = mul2(mul2(v[k], ff), wy[k]);
-                }
-            }
-        }
-        if (turned && !is_v) {
+        if (NORM && norm) {
+            const float f = rsqrtf(ss[i] * inv_d + a.eps);
+            const uint64_t ff = pair_of(f, f);
 #pragma unroll
             for (int k = 0; k < H; ++k) {
-                if (INTER) {  // (x, y) -> (x c - y s, y c + x s) within the pair
-                    const uint64_t us = pack2(hi32(u[k]), lo32(u[k])), vs = pack2(hi32(v[k]), lo32(v[k]));
-                    u[k] = fma2(u[k], pair_of(cs[k], cs[k]), mul2(us, pair_of(-sn[k], sn[k])));
-                    v[k] = fma2(v[k], pair_of(cs[H + k], cs[H + k]), mul2(vs, pair_of(-sn[H + k], sn[H + k])));
-                } else {
-                    const uint64_t c2 = pair_of(cs[2 * k], cs[2 * k + 1]), s2 = pair_of(sn[2 * k], sn[2 * k + 1]);
-                    const uint64_t t = fma2(v[k], c2, mul2(u[k], s2));
-                    u[k] = fma2(u[k], c2, mul2(v[k], pair_of(-sn[2 * k], -sn[2 * k + 1])));
-                    v[k] = t;
-                }
+                u[k] = mul2(mul2(u[k], ff), wx[k]);
+                v[k] = mul2(mul2(v[k], ff), wy[k]);
             }
         }
+        if (turned && !is_v) append_turn<INTER, H>(u, v, cs, sn);
         if (!mine || h >= heads || (!is_q && !stored)) continue;
         uint4 ox = x[i], oy = y[i];
         if (!is_v) {
@@ -382,6 +397,264 @@ __global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2
             const int64_t si = (static_cast<int64_t>(at.page) * a.Hkv + h) * a.page_size + at.off;
             if (a.weight) a.weight[si] = 0.f;
             if (a.pos) a.pos[si] = at.seq;
+        }
+    }
+}
+
+// Long blocks: tokens stream through shared memory by bulk copies, one CTA per
+// SM.  A slot of the ring holds a token's queries, keys and values and has a
+// warp that fills it (three copies, the token's cosines, sines and place in the
+// cache) and that, when the heads have been turned in place, stores it (its
+// queries in one copy, each cached row in one; values are never touched) and
+// waits until the copies have read it.  Teams of warps turn the heads, each
+// every n-th token; the number of slots is a multiple of theirs, so that a slot
+// is always the same team's and neither side of a barrier is ever more than a
+// round ahead.
+//
+// Bound: the heads' bytes, once the turning keeps up: with 16 KB tokens its
+// chain of shared-memory reads, sums over lanes and stores takes a warp 1000
+// cycles a round, so several tokens are turned at once.  16384 tokens of 32
+// heads of 256, three axes, normalised (537 MB): 94.5 us, 5.7 TB/s, against
+// 155 us in k_append_vec; four teams of two warps 108 us, two of four 136, a
+// team for each slot 118 to 129.  float32 (1.07 GB): 169 us, 6.3 TB/s, against
+// 223; its six slots do better with two teams of four than of six (182 us).
+constexpr int AS_SLOTS = 12, AS_TURN = 12;  // slots and turning warps at most
+constexpr int64_t STREAM_SMEM = 224 * 1024;
+constexpr long long AS_WAIT = 4000000000ll, AS_DRAIN = 400000000ll;  // cycles after which a wait gives up
+// Which calls: tokens of 7 KB and more, 24 and more of them per SM, else a
+// token's fixed costs and the ring's start weigh more than the smoother stream.
+// Measured, this against k_append_vec: 3040 tokens of 7 KB 9.7 against 9.1 us,
+// 4864 14.5 against 15.5, 1824 of 16 KB 16.0 against 16.1; 16384 of 4 KB 30.7
+// against 32.1 but 4864 of them 11.3 against 7.7; of 3 KB 25.5 against 16.0.
+// float32 without a norm has little to compute and stays with k_append_vec:
+// 16384 tokens of 28 KB 156 against 139 us.
+constexpr int STREAM_TOKENS = 24, STREAM_LEAST = 7 * 1024;
+
+struct StreamShared {
+    uint64_t full[AS_SLOTS], done[AS_SLOTS];
+    int live[AS_SLOTS], stored[AS_SLOTS];
+    int abort;
+};
+static __device__ unsigned int g_err_append;
+unsigned int read_error_append(bool clear) {
+    unsigned int v = 0;
+    cudaMemcpyFromSymbol(&v, g_err_append, sizeof v);
+    if (clear && v) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_err_append, &z, sizeof z);
+    }
+    return v;
+}
+
+static __device__ __noinline__ bool stream_wait_long(StreamShared &sm, uint64_t *bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (*reinterpret_cast<volatile int *>(&sm.abort) == 0) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > AS_WAIT) {
+            atomicOr(&g_err_append, ERR_WAIT_TIMEOUT);
+            *reinterpret_cast<volatile int *>(&sm.abort) = 1;
+        }
+    }
+    return false;
+}
+// A whole warp's wait, with one answer for its lanes.
+__device__ __forceinline__ bool stream_wait(StreamShared &sm, uint64_t *bar, uint32_t parity) {
+    return __all_sync(FULL, mbar_try_wait(bar, parity) || stream_wait_long(sm, bar, parity));
+}
+__device__ __forceinline__ void bulk_s2g(void *gdst, const void *ssrc, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(smem_addr(ssrc)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// The heads of one kind in a slot, norm and rotation in place.
+template <typename E, bool INTER, bool NORM>
+__device__ __forceinline__ void stream_turn(const AppendArgs &a, E *base, int heads, const E *nw, bool norm, bool mine,
+                                            bool turned, int e0, int e1, int gt, int step, int lanes_log2,
+                                            const float *cs, const float *sn) {
+    constexpr int N = Vec<E>::N, H = N / 2;
+    const float inv_d = 1.0f / a.d;
+    const int rounds = (heads + step - 1) / step;
+    E *p = base + (gt >> lanes_log2) * a.d;
+    int h = gt >> lanes_log2;
+#pragma unroll 2
+    for (int r = 0; r < rounds; ++r, h += step, p += step * a.d) {
+        const bool in = mine && h < heads;
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (in) {
+            x = *reinterpret_cast<const uint4 *>(p + e0);
+            y = *reinterpret_cast<const uint4 *>(p + e1);
+        }
+        uint64_t u[H], v[H];
+        unpack<E>(x, u);
+        unpack<E>(y, v);
+        if (NORM && norm) {
+            uint64_t s2 = mul2(u[0], u[0]);
+#pragma unroll
+            for (int k = 1; k < H; ++k) s2 = fma2(u[k], u[k], s2);
+#pragma unroll
+            for (int k = 0; k < H; ++k) s2 = fma2(v[k], v[k], s2);
+            float ss = __uint_as_float(lo32(s2)) + __uint_as_float(hi32(s2));
+            for (int d = 1 << lanes_log2 >> 1; d >= 1; d >>= 1) ss += __shfl_xor_sync(FULL, ss, d);
+            const float f = rsqrtf(ss * inv_d + a.eps);
+            const uint64_t ff = pair_of(f, f);
+            uint64_t wx[H], wy[H];
+            unpack<E>(*reinterpret_cast<const uint4 *>(nw + (mine ? e0 : 0)), wx);
+            unpack<E>(*reinterpret_cast<const uint4 *>(nw + (mine ? e1 : 0)), wy);
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                u[k] = mul2(mul2(u[k], ff), wx[k]);
+                v[k] = mul2(mul2(v[k], ff), wy[k]);
+            }
+        }
+        if (turned) append_turn<INTER, H>(u, v, cs, sn);
+        if (in && (turned || (NORM && norm))) {
+            *reinterpret_cast<uint4 *>(p + e0) = pack<E>(u);
+            *reinterpret_cast<uint4 *>(p + e1) = pack<E>(v);
+        }
+    }
+}
+
+template <typename E, bool INTER, bool NORM>
+__global__ void __launch_bounds__((AS_SLOTS + AS_TURN) * 32, 1)
+    k_append_stream(AppendArgs a, int lanes_log2, int slots, int teams, int team, int slot_bytes) {
+    constexpr int N = Vec<E>::N;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ StreamShared sm;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = a.rot / 2, row = a.d * static_cast<int>(sizeof(E));
+    const int q_bytes = a.Hq * row, kv_bytes = a.Hkv * row, data = q_bytes + 2 * kv_bytes;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < slots; ++i) {
+            mbar_init(&sm.full[i], 2);
+            mbar_init(&sm.done[i], team);
+        }
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    E *const norms = reinterpret_cast<E *>(ring + static_cast<size_t>(slots) * slot_bytes);  // the queries', the keys'
+    if (NORM)
+        for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
+            if (a.q_norm) norms[i] = static_cast<const E *>(a.q_norm)[i];
+            if (a.k_norm) norms[a.d + i] = static_cast<const E *>(a.k_norm)[i];
+        }
+    __syncthreads();
+    const int64_t G = gridDim.x;
+    if (warp >= teams * team) {
+        const int s = warp - teams * team;
+        unsigned char *const slot = ring + static_cast<size_t>(s) * slot_bytes;
+        float *const trig = reinterpret_cast<float *>(slot + data);
+        uint64_t *const full = &sm.full[s], *const done = &sm.done[s];
+        const uint64_t pol = l2_policy_evict_first();
+        AppendToken was = {};
+        int64_t was_tok = 0;
+        uint32_t k = 0;
+        auto store = [&]() {
+            if (lane == 0) bulk_s2g(static_cast<char *>(a.q_out) + was_tok * q_bytes, slot, q_bytes);
+            if (was.live && was.page >= 0)
+                for (int r = lane; r < 2 * a.Hkv; r += 32) {
+                    const bool v = r >= a.Hkv;
+                    const int h = v ? r - a.Hkv : r;
+                    bulk_s2g((v ? a.cv : a.ck) + (was.page * a.page_stride + h * a.head_stride +
+                                                  was.off * a.slot_stride) * static_cast<int64_t>(sizeof(E)),
+                             slot + q_bytes + r * row, row);
+                }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        };
+        for (int64_t tok = blockIdx.x + s * G; tok < a.tokens; tok += slots * G, ++k) {
+            const AppendToken at = append_token(a, append_raw(a, tok), lane == 0);
+            if (k > 0) {
+                if (!stream_wait(sm, done, (k - 1) & 1)) break;
+                store();
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full, data);
+            __syncwarp();
+            if (lane < 3) {
+                const char *src = lane == 0 ? a.q + tok * a.q_stride * static_cast<int64_t>(sizeof(E))
+                                  : lane == 1 ? a.k + tok * a.k_stride * static_cast<int64_t>(sizeof(E))
+                                              : a.v + tok * a.v_stride * static_cast<int64_t>(sizeof(E));
+                bulk_g2s_hint(slot + (lane == 0 ? 0 : lane == 1 ? q_bytes : q_bytes + kv_bytes), src,
+                              lane == 0 ? q_bytes : kv_bytes, full, pol);
+            }
+            for (int p = lane; p < half; p += 32) {
+                int ax = a.pair_axis ? a.pair_axis[p] : 0;
+                ax = ax < a.axes ? ax : a.axes - 1;
+                const int id = a.pos_ids[ax * a.tokens + tok];
+                const bool ok = id >= 0 && id < a.n_pos;
+                const float *t = a.cos_sin + static_cast<int64_t>(ok ? id : 0) * a.rot + p;
+                const float c = t[0], sn = t[half];
+                trig[p] = ok ? c : NAN;
+                trig[half + p] = sn;
+            }
+            const bool stored = at.live && at.page >= 0;
+            if (lane == 0) {
+                sm.live[s] = at.live;
+                sm.stored[s] = stored;
+            }
+            if (stored)
+                for (int h = lane; h < a.Hkv; h += 32) {
+                    const int64_t si = (static_cast<int64_t>(at.page) * a.Hkv + h) * a.page_size + at.off;
+                    if (a.weight) a.weight[si] = 0.f;
+                    if (a.pos) a.pos[si] = at.seq;
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+            was = at;
+            was_tok = tok;
+        }
+        if (k > 0) {
+            if (stream_wait(sm, done, (k - 1) & 1))
+                store();
+            else
+                mbar_wait(full, (k - 1) & 1, AS_DRAIN);
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+        return;
+    }
+    int s = warp / team;
+    const int first = s, gt = (warp - s * team) * 32 + lane, step = (team * 32) >> lanes_log2;
+    const int c = lane & ((1 << lanes_log2) - 1);
+    const bool mine = c * 2 * N < a.d, turned = mine && c * 2 * N < a.rot;
+    const int e0 = turned ? c * N : a.rot + (c - half / N) * N;
+    const int e1 = e0 + (turned ? half : (a.d - a.rot) / 2);
+    uint32_t parity = 0;
+    for (int64_t tok = blockIdx.x + first * G; tok < a.tokens; tok += teams * G) {
+        if (!stream_wait(sm, &sm.full[s], parity)) return;
+        unsigned char *const slot = ring + static_cast<size_t>(s) * slot_bytes;
+        E *const base = reinterpret_cast<E *>(slot);
+        if (sm.stored[s]) {
+            constexpr int W = INTER ? N / 2 : 4;
+            auto pair = [&](int i) {
+                return !INTER ? c * N + i : i < N / 2 ? c * N / 2 + i : (half + c * N) / 2 + i - N / 2;
+            };
+            const float *trig = reinterpret_cast<const float *>(slot + data);
+            float cs[N], sn[N];
+            if (turned) {
+#pragma unroll
+                for (int i = 0; i < N; i += W) {
+                    cos_load<W>(trig + pair(i), cs + i);
+                    cos_load<W>(trig + half + pair(i), sn + i);
+                }
+            }
+            stream_turn<E, INTER, NORM>(a, base, a.Hq, norms, a.q_norm != nullptr, mine, turned, e0, e1, gt, step,
+                                        lanes_log2, cs, sn);
+            stream_turn<E, INTER, NORM>(a, base + a.Hq * a.d, a.Hkv, norms + a.d, a.k_norm != nullptr, mine, turned,
+                                        e0, e1, gt, step, lanes_log2, cs, sn);
+        } else {  // zeros past q_len, NaN for a token that has no place
+            const uint32_t w = !sm.live[s] ? 0u : sizeof(E) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+            for (int i = gt; i < q_bytes / 16; i += team * 32)
+                reinterpret_cast<uint4 *>(slot)[i] = make_uint4(w, w, w, w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.done[s]);
+        s += teams;
+        if (s >= slots) {
+            s = first;
+            parity ^= 1;
         }
     }
 }
@@ -666,6 +939,33 @@ static dflash2_status launch_append_vec(AppendArgs &a, dflash2_dtype dt, bool in
     return after_launch();
 }
 
+static dflash2_status launch_append_stream(AppendArgs &a, dflash2_dtype dt, bool inter, bool norm, int lanes_log2,
+                                           cudaStream_t s) {
+    using Fn = void (*)(AppendArgs, int, int, int, int, int);
+    using H = unsigned short;
+    static const Fn table[8] = {k_append_stream<H, false, false>,     k_append_stream<H, false, true>,
+                                k_append_stream<H, true, false>,      k_append_stream<H, true, true>,
+                                nullptr,                              k_append_stream<float, false, true>,
+                                nullptr,                              k_append_stream<float, true, true>};
+    const Fn fn = table[(dt == DFLASH2_F32 ? 4 : 0) + (inter ? 2 : 0) + (norm ? 1 : 0)];
+    // raises the shared-memory limit, once
+    blocks_per_sm(reinterpret_cast<const void *>(fn), (AS_SLOTS + AS_TURN) * 32, STREAM_SMEM);
+    const int row = a.d * esize(dt), slot_bytes = (a.Hq + 2 * a.Hkv) * row + (a.rot * 4 + 15) / 16 * 16;
+    const int most = static_cast<int>((STREAM_SMEM - 2 * row) / slot_bytes), teams = most >= AS_SLOTS ? 6 : 2,
+              team = most >= AS_SLOTS ? 2 : 4, slots = (most < AS_SLOTS ? most : AS_SLOTS) / teams * teams;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sm_count());
+    cfg.blockDim = dim3((teams * team + slots) * 32, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(slots) * slot_bytes + 2 * row;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, a, lanes_log2, slots, teams, team, slot_bytes) != cudaSuccess)
+        return DFLASH2_ERR_CUDA;
+    return after_launch();
+}
+
 static int64_t evict_max_moves(int64_t capacity, int32_t budget) {
     const int64_t over = capacity > budget ? capacity - budget : 0;
     return over < budget ? over : budget;
@@ -743,15 +1043,19 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
     if (rot % two == 0 && d % two == 0 && d / two <= 32) {
         int lanes_log2 = 0;
         while ((1 << lanes_log2) * two < d) ++lanes_log2;
+        const bool norm = q_norm || k_norm;
+        const int64_t token_bytes = (static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(cache->Hkv)) * d * e;
+        if ((norm || cache->dt == DFLASH2_BF16) && a.tokens >= static_cast<int64_t>(sm_count()) * STREAM_TOKENS &&
+            token_bytes >= STREAM_LEAST && token_bytes <= STREAM_SMEM / 4 - 4096)
+            return launch_append_stream(a, cache->dt, interleaved != 0, norm, lanes_log2, s);
         // Many tokens: a thread takes four heads, so that a token's cosines are read by a quarter of the threads;
-        // few: one, so that there are enough threads (512 per SM).
+        // few: one, so that there are enough threads (192 per SM).
         auto units = [&](int64_t per) { return (Hq + per - 1) / per + 2 * ((cache->Hkv + per - 1) / per); };
-        const int per = (a.tokens * units(APPEND_BATCH) << lanes_log2) >= static_cast<int64_t>(sm_count()) * 512
+        const int per = (a.tokens * units(APPEND_BATCH) << lanes_log2) >= static_cast<int64_t>(sm_count()) * 192
                             ? APPEND_BATCH : 1;
         const int64_t threads = a.tokens * units(per) << lanes_log2;
         if (a.tokens * units(per) < (int64_t(1) << 32) - 256 && (threads + 255) / 256 < (int64_t(1) << 31)) {
             const dim3 vgrid(static_cast<unsigned>((threads + 255) / 256));
-            const bool norm = q_norm || k_norm;
             return launch_append_vec(a, cache->dt, interleaved != 0, norm, lanes_log2, per, vgrid, s);
         }
     }

@@ -118,6 +118,22 @@ def test_append_shapes(dtype, B, T, Hq, Hkv, nhd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv,d,rot,nhd", [(20, 4, 128, 128, False), (14, 2, 256, 64, True), (50, 10, 80, 48, False),
+                                              (32, 16, 64, 64, False), (50, 25, 256, 256, False), (1, 20, 48, 16, True)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_long_blocks(dtype, Hq, Hkv, d, rot, nhd, interleaved):
+    """Blocks of many tokens: ragged, one without a token, one that its page table ends in, pages that are nowhere."""
+    T, lens = 925, [0, 17, 60, 5]
+    c = Case(Hq + d, [985, 985, 985, 400], T, Hq, Hkv, d, 24, dtype, q_lens=[925, 700, 925, 0], held=True, nhd=nhd)
+    c.table[0, 3] = -1
+    c.table[2, 14] = c.k.shape[0] + 2
+    lens[1] = c.table.shape[1] * 24 - 200
+    for axes, norm in ((1, False), (3, True)):
+        check_append(c, lens, append_inputs(c, rot, axes, rot, norm), interleaved, split=norm)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 128), (BF, 40)])
 def test_append_bad_positions_and_pages(dtype, d):
     """Position ids outside the table, a full page table, page ids out of range: NaN queries, nothing else written."""
