@@ -980,6 +980,27 @@ using namespace dfl;
 
 static bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
+// Memory that a device copy can reach.
+static bool registered(const void *p) {
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();  // no device: nothing is the device's
+        return false;
+    }
+    return at.type != cudaMemoryTypeUnregistered;
+}
+
+// A block of no tokens: the lengths stay what they were.  Lengths that are not the device's (the arguments' checks
+// tried alone, on a machine without a GPU too) are not touched.
+static dflash2_status append_no_tokens(const int32_t *kv_len, int64_t B, int32_t *kv_len_out, cudaStream_t s) {
+    if (!kv_len_out) return DFLASH2_OK;
+    if (!kv_len || !al4(kv_len) || !al4(kv_len_out) || kv_len_out == kv_len) return DFLASH2_ERR_INVALID_ARG;
+    if (!registered(kv_len) || !registered(kv_len_out)) return DFLASH2_OK;
+    const cudaError_t e = cudaMemcpyAsync(kv_len_out, kv_len, static_cast<size_t>(B) * sizeof(int32_t),
+                                          cudaMemcpyDeviceToDevice, s);
+    return e == cudaSuccess ? DFLASH2_OK : DFLASH2_ERR_CUDA;
+}
+
 extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t *page_table,
                                               int32_t max_pages, const int32_t *kv_len, const int32_t *q_len,
                                               const int32_t *seq_pos, const void *q, const void *k, const void *v,
@@ -991,7 +1012,8 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
     if (!kv_cache_ok(cache, page_table, max_pages) || B < 0 || T < 0 || Hq < 1 || rot < 2 || rot % 2 != 0 ||
         rot > cache->d || axes < 1 || n_pos < 1)
         return DFLASH2_ERR_INVALID_ARG;
-    if (B == 0 || T == 0) return DFLASH2_OK;
+    if (B == 0) return DFLASH2_OK;
+    if (T == 0) return append_no_tokens(kv_len, B, kv_len_out, reinterpret_cast<cudaStream_t>(stream));
     const int e = esize(cache->dt);
     const int64_t d = cache->d;
     if (!q || !k || !v || !q_out || !kv_len || !cos_sin || !pos_ids || !aligned16(q) || !aligned16(k) ||

@@ -443,7 +443,8 @@ typedef struct {
  *   NULL (axis 0); values above axes - 1 count as axes - 1.
  * q_norm, k_norm [d] of dt, or NULL.
  * q_out [B, T, Hq, d], contiguous.  kv_len_out [B] or NULL: kv_len + q_len;
- *   must not overlap kv_len.
+ *   must not overlap kv_len.  With T = 0 it is kv_len, and nothing else is
+ *   read or written.
  * A token whose position id is outside [0, n_pos) gets NaN in the rotated
  * entries of its query and key.  A token whose slot has no valid page (past
  * the table, or a page id out of range) is not stored and its query comes

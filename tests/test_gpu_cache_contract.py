@@ -1,0 +1,56 @@
+"""What the calls of the paged cache path promise beside their formulas: empty blocks and batches, arrays and workspaces
+that several calls share."""
+import pytest
+import torch
+
+import dflash_draft_selection_gb300 as d2
+from tests._cache import Case
+from tests._util import cuda_or_skip
+from tests.test_gpu_kvcache import append_inputs, bits
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+SIDES = ("k", "v", "weight", "pos")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_of_no_tokens(dtype):
+    """T = 0: nothing is appended and the lengths are what they were."""
+    dev = cuda_or_skip()
+    c = Case(1, [40, 0, 7], 1, 4, 2, 64, 16, dtype, held=True)
+    on = c.on(dev)
+    cache, lens = on["cache"], on["kv_len"]
+    before = [getattr(cache, n).clone() for n in SIDES]
+    x = torch.empty(3, 0, 8, 64, dtype=dtype, device=dev)
+    ids = torch.empty(1, 3, 0, dtype=torch.int32, device=dev)
+    out = (torch.empty(3, 0, 4, 64, dtype=dtype, device=dev), torch.full((3,), -99, dtype=torch.int32, device=dev))
+    kw = dict(q_len=torch.tensor([5, 0, -1], dtype=torch.int32, device=dev))
+    for o in (None, out):
+        q, n = d2.rope_append(x[:, :, :4], x[:, :, 4:6], x[:, :, 6:], torch.ones(10, 64, device=dev), ids, cache,
+                              on["page_table"], lens, out=o, **kw)
+        assert q.shape == (3, 0, 4, 64) and n.tolist() == [40, 0, 7] == lens.tolist()
+    for x, n in zip(before, SIDES):
+        assert torch.equal(bits(x), bits(getattr(cache, n)))
+    assert d2.paged_attn(q, cache, on["page_table"], lens)[0].shape == (3, 0, 4, 64)
+    assert d2.device_error() == 0
+
+
+def test_append_of_no_tokens_in_a_graph():
+    """The copied lengths are part of a captured graph."""
+    dev = cuda_or_skip()
+    cache = d2.KVCache.empty(4, 2, 16, 64, device=dev)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    x = torch.empty(2, 0, 8, 64, dtype=BF, device=dev)
+    n, table = i32(3, 9), torch.zeros(2, 2, dtype=torch.int32, device=dev)
+    args = (x[:, :, :4], x[:, :, 4:6], x[:, :, 6:], torch.ones(10, 64, device=dev),
+            torch.empty(1, 2, 0, dtype=torch.int32, device=dev), cache, table, n)
+    out = (torch.empty(2, 0, 4, 64, dtype=BF, device=dev), i32(-1, -1))
+    d2.rope_append(*args, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d2.rope_append(*args, out=out)
+    n += 5
+    g.replay()
+    torch.cuda.synchronize()
+    assert out[1].tolist() == [8, 14]
