@@ -417,11 +417,13 @@ static int part_rows(int32_t T, int32_t group) {
     return rows < 128 ? static_cast<int>(rows) : 128;
 }
 
-bool kv_cache_ok(const dflash2_kv_cache *c, const int32_t *table, int32_t max_pages) {
-    if (!c || !c->k || !c->v || !table || !dtype_ok(c->dt)) return false;
+// The cache, and the page table of B requests (an empty batch has none).
+bool kv_cache_ok(const dflash2_kv_cache *c, const int32_t *table, int32_t max_pages, int64_t B) {
+    if (!c || !c->k || !c->v || !dtype_ok(c->dt)) return false;
+    if (B != 0 && (!table || max_pages < 1)) return false;
     const int e = esize(c->dt);
     auto al4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; };
-    return c->num_pages >= 1 && c->Hkv >= 1 && c->page_size >= 1 && c->d >= 1 && max_pages >= 1 && aligned16(c->k) &&
+    return c->num_pages >= 1 && c->Hkv >= 1 && c->page_size >= 1 && c->d >= 1 && max_pages >= 0 && aligned16(c->k) &&
            aligned16(c->v) && c->page_stride * e % 16 == 0 && c->head_stride * e % 16 == 0 &&
            c->slot_stride * e % 16 == 0 && static_cast<int64_t>(c->d) * e % 16 == 0 && c->slot_stride >= c->d &&
            c->head_stride >= 0 && c->page_stride >= 0 && al4(c->weight) && al4(c->pos) && al4(table);
@@ -443,12 +445,13 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
                                              const int32_t *seq_pos, const void *q, int64_t B, int32_t T, int32_t Hq,
                                              float scale, int32_t window, uint32_t flags, void *out, float *lse,
                                              void *ws, size_t ws_bytes, dflash2_stream stream) {
-    if (!kv_cache_ok(cache, page_table, max_pages) || B < 0 || T < 0 || Hq < 1 || Hq % cache->Hkv != 0 ||
+    if (!kv_cache_ok(cache, page_table, max_pages, B) || B < 0 || T < 0 || Hq < 1 || Hq % cache->Hkv != 0 ||
         !(scale - scale == 0.f) || window < 0 || (flags & ~3u))
         return DFLASH2_ERR_INVALID_ARG;
     const bool weights = (flags & DFLASH2_ATTN_WEIGHTS) != 0;
-    if (weights && (!lse || !cache->weight)) return DFLASH2_ERR_INVALID_ARG;
-    if (B == 0 || T == 0) return DFLASH2_OK;
+    if (weights && !cache->weight) return DFLASH2_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return DFLASH2_OK;  // outputs of no elements may be NULL
+    if (weights && !lse) return DFLASH2_ERR_INVALID_ARG;
     auto al4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; };
     if (!q || !out || !kv_len || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws) || !al4(kv_len) ||
         !al4(q_len) || !al4(seq_pos) || !al4(lse) || out == q)

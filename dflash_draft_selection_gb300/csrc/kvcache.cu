@@ -5,7 +5,7 @@
 
 namespace dfl {
 
-bool kv_cache_ok(const dflash2_kv_cache *c, const int32_t *table, int32_t max_pages);
+bool kv_cache_ok(const dflash2_kv_cache *c, const int32_t *table, int32_t max_pages, int64_t B);
 
 // ------------------------------------------------------------------ append --
 struct AppendArgs {
@@ -1009,7 +1009,7 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
                                               const int32_t *pos_ids, int32_t axes, const uint8_t *pair_axis,
                                               int32_t interleaved, const void *q_norm, const void *k_norm, float eps,
                                               void *q_out, int32_t *kv_len_out, dflash2_stream stream) {
-    if (!kv_cache_ok(cache, page_table, max_pages) || B < 0 || T < 0 || Hq < 1 || rot < 2 || rot % 2 != 0 ||
+    if (!kv_cache_ok(cache, page_table, max_pages, B) || B < 0 || T < 0 || Hq < 1 || rot < 2 || rot % 2 != 0 ||
         rot > cache->d || axes < 1 || n_pos < 1)
         return DFLASH2_ERR_INVALID_ARG;
     if (B == 0) return DFLASH2_OK;
@@ -1101,7 +1101,7 @@ extern "C" dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const 
                                            int32_t max_pages, const int32_t *kv_len, const int32_t *seq_len, int64_t B,
                                            int32_t budget, int32_t recent, int32_t sink, int32_t *kv_len_out, void *ws,
                                            size_t ws_bytes, dflash2_stream stream) {
-    if (!kv_cache_ok(cache, page_table, max_pages) || !cache->weight || !cache->pos || B < 0 || budget < 1 ||
+    if (!kv_cache_ok(cache, page_table, max_pages, B) || !cache->weight || !cache->pos || B < 0 || budget < 1 ||
         recent < 0 || sink < 0)
         return DFLASH2_ERR_INVALID_ARG;
     if (B == 0) return DFLASH2_OK;

@@ -401,7 +401,8 @@ dflash2_status dflash2_dynconv2tap(const void *x, const void *x_prev, const void
  * page_table; num_pages, Hkv, page_size, d or max_pages < 1; k, v, the
  * strides or d * elem size not multiples of 16 bytes; slot_stride < d,
  * head_stride or page_stride < 0; side arrays, page_table or per-request
- * arrays not 4-byte aligned; B or T < 0.
+ * arrays not 4-byte aligned; B or T < 0.  B = 0 is an empty batch: nothing is
+ * launched, and page_table may be NULL and max_pages 0.
  */
 typedef struct {
     void *k;              /* device, of dt */

@@ -1,0 +1,57 @@
+"""Arguments of the paged cache path's calls that are taken or refused on the host (no GPU needed: the pointers are never
+dereferenced)."""
+import ctypes
+
+import dflash_draft_selection_gb300 as d2
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 4
+P = ctypes.c_void_p(4096)
+CACHE = dict(k=4096, v=4096, weight=4096, pos=4096, num_pages=4, page_stride=2 * 16 * 64, head_stride=16 * 64,
+             slot_stride=64, Hkv=2, page_size=16, d=64, dt=1)
+
+
+def library():
+    from dflash_draft_selection_gb300 import build
+    build.build()
+    return d2.load_library()
+
+
+def record(**kw):
+    from dflash_draft_selection_gb300.binding import _CacheRecord
+    return _CacheRecord(**{**CACHE, **kw})
+
+
+def append(cache=None, **kw):
+    r = record(**(cache or {}))
+    a = dict(cache=ctypes.byref(r), table=P, max_pages=4, kv_len=P, q_len=ctypes.c_void_p(8192),
+             seq_pos=ctypes.c_void_p(12288), q=P, k=P, v=P, qs=256, ks=128, vs=128, B=2, T=2, Hq=4, cos_sin=P, n_pos=10,
+             rot=64, pos_ids=P, axes=1, pair_axis=None, interleaved=0, q_norm=P, k_norm=P, eps=1e-6,
+             q_out=ctypes.c_void_p(16384), kv_len_out=ctypes.c_void_p(512), stream=None)
+    a.update(kw)
+    return library().dflash2_rope_append(*a.values())
+
+
+def attend(cache=None, **kw):
+    r = record(**(cache or {}))
+    a = dict(cache=ctypes.byref(r), table=P, max_pages=4, kv_len=P, q_len=P, seq_pos=P, q=P, B=2, T=2, Hq=4,
+             scale=0.125, window=0, flags=1, out=ctypes.c_void_p(1024), lse=P, ws=P, ws_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return library().dflash2_paged_attn(*a.values())
+
+
+def evict(cache=None, **kw):
+    r = record(**(cache or {}))
+    a = dict(cache=ctypes.byref(r), table=P, max_pages=4, kv_len=P, seq_len=P, B=2, budget=8, recent=0, sink=0, out=P,
+             ws=P, ws_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return library().dflash2_kv_evict(*a.values())
+
+
+def test_an_empty_batch_has_no_table():
+    for call in (append, attend, evict):
+        assert call(B=0) == call(B=0, table=None) == call(B=0, max_pages=0) == call(B=0, table=None, max_pages=0) == OK
+        assert call(B=0, max_pages=-1) == call(B=-1) == INVALID
+        assert call(table=None) == call(max_pages=0) == INVALID
+    for no in (dict(B=0), dict(T=0)):
+        assert attend(q=None, out=None, lse=None, flags=3, **no) == OK
+    assert attend(lse=None, flags=3) == INVALID

@@ -54,3 +54,20 @@ def test_append_of_no_tokens_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert out[1].tolist() == [8, 14]
+
+
+@pytest.mark.parametrize("pages", [0, 3])
+def test_no_requests(pages):
+    """B = 0 is an empty batch, with a page table of no rows."""
+    dev = cuda_or_skip()
+    cache = d2.KVCache.empty(4, 2, 16, 64, weights=True, positions=True, device=dev)
+    i32 = lambda *n: torch.empty(*n, dtype=torch.int32, device=dev)  # noqa: E731
+    x = torch.empty(0, 3, 8, 64, dtype=BF, device=dev)
+    q, n = d2.rope_append(x[:, :, :4], x[:, :, 4:6], x[:, :, 6:], torch.ones(10, 64, device=dev), i32(1, 0, 3), cache,
+                          i32(0, pages), i32(0))
+    out, lse = d2.paged_attn(q, cache, i32(0, pages), n, add_weights=True)
+    left = d2.kv_evict(cache, i32(0, pages), n, 8)
+    assert q.shape == out.shape == (0, 3, 4, 64) and lse.shape == (0, 3, 4) and n.shape == left.shape == (0,)
+    x = torch.empty(2, 0, 4, 64, dtype=BF, device=dev)          # two requests, no tokens
+    assert d2.paged_attn(x, cache, torch.zeros_like(i32(2, 3)), torch.zeros_like(i32(2)), add_weights=True)[0].shape == x.shape
+    assert d2.device_error() == 0
