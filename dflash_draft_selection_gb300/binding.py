@@ -202,7 +202,9 @@ def _params_from(params, device):
 
 
 class Workspace:
-    """A zero-filled device workspace, reusable across calls (kept zeroed by them)."""
+    """A zero-filled device workspace, reusable across calls of one kind: for one entry point and set of sizes, or for
+    calls of paged_attn and kv_evict of any sizes that fit.  What a call needs zero it leaves zero; ``buf.zero_()``
+    before the workspace goes to another kind of call."""
 
     def __init__(self, nbytes: int, device="cuda"):
         self.buf = torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)

@@ -436,7 +436,7 @@ using namespace dfl;
 extern "C" size_t dflash2_paged_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,
                                                      dflash2_dtype dt) {
     if (B < 0 || T < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || d < 1 || !dtype_ok(dt)) return 0;
-    return ATTN_TICKET_BYTES +
+    return WS_ZERO_BYTES +
            static_cast<size_t>(attn_ctas()) * 2 * attn_part_floats(part_rows(T, Hq / Hkv), d) * sizeof(float);
 }
 
@@ -494,7 +494,7 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
     a.out = out;
     a.lse = lse;
     a.tickets = static_cast<int *>(ws);
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + ATTN_TICKET_BYTES);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + WS_ZERO_BYTES);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     dflash2_status st;
     if (cache->dt == DFLASH2_F32) {

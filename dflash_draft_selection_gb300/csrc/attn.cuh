@@ -52,6 +52,7 @@ __host__ __device__ __forceinline__ int64_t attn_part_floats(int rows, int d) {
 
 constexpr int ATTN_MAX_CTAS = 1024;
 constexpr size_t ATTN_TICKET_BYTES = ATTN_MAX_CTAS * sizeof(int);
+static_assert(ATTN_TICKET_BYTES <= WS_ZERO_BYTES, "the tickets lie in what other calls leave alone");
 
 // One request as the call sees it.  (Slots, and the tiles of a call, are
 // below 2^31: checked by the caller.)

@@ -70,6 +70,11 @@ inline dflash2_status after_launch() {
     return cudaPeekAtLastError() == cudaSuccess ? DFLASH2_OK : DFLASH2_ERR_CUDA;
 }
 
+// The front of a workspace of dflash2_paged_attn and dflash2_kv_evict: the
+// attention's tickets, which are zero between calls.  Both keep everything
+// else behind it, so the two may share a workspace.
+constexpr size_t WS_ZERO_BYTES = 4096;
+
 inline int esize(dflash2_dtype dt) { return dt == DFLASH2_BF16 ? 2 : 4; }
 
 inline bool dtype_ok(dflash2_dtype dt) { return dt == DFLASH2_BF16 || dt == DFLASH2_F32; }

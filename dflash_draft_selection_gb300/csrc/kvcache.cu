@@ -1093,7 +1093,7 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
 
 extern "C" size_t dflash2_kv_evict_workspace_bytes(int64_t B, int32_t Hkv, int64_t capacity, int32_t budget) {
     if (B < 0 || Hkv < 1 || capacity < 0 || budget < 1) return 0;
-    return evict_count_bytes(B, Hkv) +
+    return WS_ZERO_BYTES + evict_count_bytes(B, Hkv) +
            static_cast<size_t>(B) * Hkv * evict_max_moves(capacity, budget) * sizeof(int2);
 }
 
@@ -1131,8 +1131,9 @@ extern "C" dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const 
     a.recent = recent;
     a.sink = sink;
     a.kv_len_out = kv_len_out;
-    a.count = static_cast<int *>(ws);
-    a.moves = reinterpret_cast<int2 *>(static_cast<char *>(ws) + evict_count_bytes(B, cache->Hkv));
+    char *const scratch = static_cast<char *>(ws) + WS_ZERO_BYTES;
+    a.count = reinterpret_cast<int *>(scratch);
+    a.moves = reinterpret_cast<int2 *>(scratch + evict_count_bytes(B, cache->Hkv));
     a.max_moves = evict_max_moves(cap, budget);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int64_t heads = B * cache->Hkv;

@@ -23,12 +23,18 @@
  *     request in `status` (DFLASH2_ST_*) or as -1 / NaN outputs.
  *   - Workspaces (`ws`) are caller-provided device buffers of at least the
  *     size returned by the matching *_workspace_bytes function.  They must be
- *     zero-filled once before first use; every call that runs to the end
- *     leaves them zeroed again.  After a call that returned DFLASH2_ERR_CUDA,
- *     or after dflash2_device_error reported a nonzero code (a kernel gave up
- *     on a bounded wait), zero-fill the workspaces of the calls involved
- *     again before reusing them.  Two calls that share a workspace must not
- *     run concurrently.
+ *     zero-filled once before first use.  A call needs zeros only where it
+ *     counts (its tickets and marks) and leaves zeros there; behind them it
+ *     leaves its scratch.  So a workspace is for calls of one kind: the scans
+ *     (dflash2_topk16, _shard, dflash2_verify) keep one workspace per entry
+ *     point and set of sizes (rows, or B and K), and dflash2_paged_attn and
+ *     dflash2_kv_evict may share one, for calls of any sizes that it is large
+ *     enough for.  Zero-fill a workspace before it goes to another kind of
+ *     call.  After a call that returned DFLASH2_ERR_CUDA, or after
+ *     dflash2_device_error reported a nonzero code (a kernel gave up on a
+ *     bounded wait), zero-fill the workspaces of the calls involved again
+ *     before reusing them.  Two calls that share a workspace must not run
+ *     concurrently.
  *   - The first call on a device performs one-time set-up (device attributes,
  *     kernel attributes); make it before any stream capture.  Later calls are
  *     capturable into CUDA graphs.
@@ -489,7 +495,8 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  * Scores, softmax statistics and sums are fp32.  The cache's length is split
  * over the GPU and the parts are joined in a fixed order: the same call gives
  * the same bits.
- * ws: dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, dt) bytes.
+ * ws: dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, dt) bytes, the first
+ *   4096 zero at the start and left zero.
  * Errors: the common ones; INVALID_ARG for NULL q, out or kv_len, out the same
  * as q, lse or the cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a positive multiple of
  * Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
@@ -526,7 +533,7 @@ dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, const int32_t *
  * never copied.
  * If more than `budget` slots are protected, the lower slots stay.
  * ws: dflash2_kv_evict_workspace_bytes(B, Hkv, max_pages * page_size, budget)
- *   bytes.
+ *   bytes, of which no zeros are needed; the first 4096 are not touched.
  * Errors: the common ones; INVALID_ARG for the cache's weight or pos NULL,
  * NULL kv_len or kv_len_out, budget < 1, recent < 0 or sink < 0; WORKSPACE;
  * UNSUPPORTED for max_pages * page_size >= 2^31 - 2048 or B * Hkv >= 2^31.

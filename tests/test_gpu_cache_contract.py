@@ -71,3 +71,30 @@ def test_no_requests(pages):
     x = torch.empty(2, 0, 4, 64, dtype=BF, device=dev)          # two requests, no tokens
     assert d2.paged_attn(x, cache, torch.zeros_like(i32(2, 3)), torch.zeros_like(i32(2)), add_weights=True)[0].shape == x.shape
     assert d2.device_error() == 0
+
+
+@pytest.mark.parametrize("budget", [40, 700])      # the moves in the selecting launch, and in one of their own
+def test_eviction_and_attention_in_one_workspace(budget):
+    """Calls that follow each other share a workspace: each leaves it as the other needs it."""
+    dev = cuda_or_skip()
+    lens = [1500, 900, 1203] if budget == 700 else [100, 41, 112]
+    c = Case(3, lens, 1, 4, 4, 64, 16, held=True)
+    a = Case(4, [3000, 900, 4000], 4, 10, 2, 128, 16)
+    seq = torch.tensor([s + 1 for s in c.seq_pos], dtype=torch.int32, device=dev)
+    cap = c.table.shape[1] * 16
+    L = d2.load_library()
+    need = [L.dflash2_kv_evict_workspace_bytes(3, 4, cap, budget), L.dflash2_paged_attn_workspace_bytes(3, 4, 10, 2, 128, 1)]
+    one = d2.Workspace(max(need), dev)
+    qa, on_a = a.q.to(dev), a.on(dev)
+    results = []
+    for shared in (False, True):
+        on = c.on(dev)
+        for _ in range(3):
+            on = {**on, **c.on(dev)}
+            n = d2.kv_evict(on["cache"], on["page_table"], on["kv_len"], budget, 3, 1, seq_len=seq,
+                            ws=one if shared else None)
+            got = d2.paged_attn(qa, ws=one if shared else None, **on_a)
+        results.append([n, *got] + [bits(getattr(on["cache"], x)) for x in SIDES])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+    assert d2.device_error() == 0
