@@ -460,8 +460,10 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
     if (cache->d > 256 || group > 128 || cache->num_pages >= (int64_t(1) << 31) ||
         static_cast<int64_t>(max_pages) * cache->page_size >= (int64_t(1) << 31) - 256)
         return DFLASH2_ERR_UNSUPPORTED;
-    // the places of a call's line are counted in 31 bits (32 keys and one token at the least)
-    if (static_cast<double>(B) * cache->Hkv * T * (static_cast<double>(max_pages) * cache->page_size / SIMT_KEYS + 4) >=
+    // The places of a call's line are counted in 31 bits.  There are at most B Hkv T items, each of the tiles of cap
+    // slots (32 keys at the least: cap / 32 + 1) and of its cost beside them (1 or ATTN_ITEM_COST).
+    if (static_cast<double>(B) * cache->Hkv * T *
+            (static_cast<double>(max_pages) * cache->page_size / SIMT_KEYS + 1 + ATTN_ITEM_COST) >=
         2147483648.0)
         return DFLASH2_ERR_UNSUPPORTED;
     if (ws_bytes < dflash2_paged_attn_workspace_bytes(B, T, Hq, cache->Hkv, cache->d, cache->dt))

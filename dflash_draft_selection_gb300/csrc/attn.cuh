@@ -54,6 +54,13 @@ constexpr int ATTN_MAX_CTAS = 1024;
 constexpr size_t ATTN_TICKET_BYTES = ATTN_MAX_CTAS * sizeof(int);
 static_assert(ATTN_TICKET_BYTES <= WS_ZERO_BYTES, "the tickets lie in what other calls leave alone");
 
+// What an item of the tensor-core kernels costs beside its tiles, in tiles:
+// the drain of the pipeline, its sums and outputs, the join of a cut one, the
+// first tile's maxima.  Measured with 1, 2, 3, 4, 6, 8: 64 requests in a window
+// 78, 71, 70, 66, 70, 68 us; 32 ragged ones 207, 194, 188, 185, 184, 187; 16
+// with wide heads 136, 139, 123, 121, 118, 116.
+constexpr int ATTN_ITEM_COST = 4;
+
 // One request as the call sees it.  (Slots, and the tiles of a call, are
 // below 2^31: checked by the caller.)
 struct AttnReq {

@@ -6,11 +6,6 @@ namespace dfl {
 
 static __device__ unsigned int g_err_attn;
 
-// What an item costs beside its tiles, in tiles: the drain of the pipeline, its sums and outputs, the join of a cut one,
-// the first tile's maxima.  Measured with 1, 2, 3, 4, 6, 8: 64 requests in a window 78, 71, 70, 66, 70, 68 us; 32 ragged
-// ones 207, 194, 188, 185, 184, 187; 16 with wide heads 136, 139, 123, 121, 118, 116.
-constexpr int ATTN_ITEM_COST = 4;
-
 dflash2_status attn_tc64(TcLaunch &t);
 dflash2_status attn_tc128(TcLaunch &t);
 dflash2_status attn_tc256(TcLaunch &t);

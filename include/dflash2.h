@@ -502,7 +502,7 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  * Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
  * small; UNSUPPORTED for d > 256, Hq / Hkv > 128, num_pages >= 2^31,
  * max_pages * page_size >= 2^31 - 256 or
- * B * Hkv * T * (max_pages * page_size / 32 + 4) >= 2^31.
+ * B * Hkv * T * (max_pages * page_size / 32 + 5) >= 2^31.
  */
 enum { DFLASH2_ATTN_CAUSAL = 1, DFLASH2_ATTN_WEIGHTS = 2 };
 size_t dflash2_paged_attn_workspace_bytes(int64_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t d,

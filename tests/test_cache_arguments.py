@@ -55,3 +55,14 @@ def test_an_empty_batch_has_no_table():
     for no in (dict(B=0), dict(T=0)):
         assert attend(q=None, out=None, lse=None, flags=3, **no) == OK
     assert attend(lse=None, flags=3) == INVALID
+
+
+def test_a_call_of_more_places_than_31_bits_is_refused():
+    """An item takes at most cap / 32 + 5 places of a call's line (a tile of 128 keys that is not full, and 4 beside)."""
+    small = dict(Hkv=1, page_size=8)
+    per = 8 / 32 + 5
+    for dt in (0, 1):
+        assert attend(dict(small, dt=dt), B=480_000_000, T=1, Hq=1, max_pages=1) == UNSUPPORTED
+        assert attend(dict(small, dt=dt), B=int(2 ** 31 / per) + 1, T=1, Hq=1, max_pages=1) == UNSUPPORTED
+        # one request less passes the guard, and is stopped by the next check
+        assert attend(dict(small, dt=dt), B=int(2 ** 31 / per), T=1, Hq=1, max_pages=1, ws_bytes=0) == WORKSPACE
