@@ -11,7 +11,7 @@ unsigned int read_error_lmhead(bool clear);
 unsigned int read_error_attn(bool clear);
 unsigned int read_error_append(bool clear);
 
-// dflash2_test_hold's setting: read by every scan launch (make_geom).
+// dflash2_test_hold's setting: read by every launch that the hook holds.
 static std::mutex g_hold_mu;
 static const unsigned int *g_hold_flag = nullptr;
 static long long g_hold_cycles = 0;

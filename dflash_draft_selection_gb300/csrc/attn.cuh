@@ -43,6 +43,8 @@ struct AttnArgs {
     int *tickets;    // [gridDim.x], zero between calls
     float *parts;    // [2 * gridDim.x][attn_part_floats(rows_cap, d)]
     unsigned int *err;  // the library's error word of these kernels
+    const unsigned int *hold;  // test hook: NULL, or a word that a copying warp of the tensor-core kernels waits on
+    long long hold_cycles;
 };
 
 // Floats of a part: O [rows][d], m [rows], l [rows], padded to 16 bytes.

@@ -63,6 +63,7 @@ dflash2_status attn_tc_launch(AttnArgs a, bool weights, cudaStream_t s) {
     a.item_cost = ATTN_ITEM_COST;
     a.err = err_word();
     if (!a.err) return DFLASH2_ERR_CUDA;
+    scan_hold(&a.hold, &a.hold_cycles);
     t.n = a.rows_cap <= 16 ? 16 : a.rows_cap <= 32 ? 32 : a.rows_cap <= 48 ? 48 : a.rows_cap <= 64 ? 64
           : a.rows_cap <= 96 ? 96 : 128;
     t.box_log2 = 3;

@@ -73,6 +73,8 @@ struct TcShared {
     uint64_t p_full[2];   // P of tile n written (weights pass: its scores read)
     uint64_t pv_done[2];  // output product of tile n complete
     uint64_t q_full, q_empty, done;
+    uint64_t meet;        // the two softmax groups, where they add values by hand
+    uint32_t meets[8];    // how often each of their warps has come
     int row_at[128];  // index of the row in lse (times d: in out) from the item's first row's
     int scratch[TC_THREADS / 32 + 2];
     alignas(16) float neg_m[128];
@@ -211,6 +213,33 @@ static __device__ __noinline__ bool tc_wait_long(TcShared &sm, uint64_t *bar, ui
 }
 __device__ __forceinline__ bool tc_wait(TcShared &sm, uint64_t *bar, uint32_t parity, unsigned int *err) {
     return mbar_try_wait(bar, parity) || tc_wait_long(sm, bar, parity, err);
+}
+
+// The softmax groups (a lane of each of the 8 warps arrives) meet where after a
+// time-out one of them may not come: a bounded wait, and one answer for a warp.
+// (A warp's count of the meetings lies in shared memory: it is rarely needed.)
+static __device__ __noinline__ bool both_meet(TcShared &sm, unsigned int *err) {
+    volatile uint32_t *const meets = &sm.meets[threadIdx.x >> 5];
+    const uint32_t m = *meets;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        *meets = m + 1;
+        mbar_arrive(&sm.meet);
+    }
+    return __all_sync(FULL, tc_wait(sm, &sm.meet, m & 1, err));
+}
+
+// Test hook: a copying warp waits for the hook's word; if that runs out the
+// kernel gives up as after any time-out.  One answer for the warp.
+__device__ __forceinline__ bool tc_hold(TcShared &sm, const AttnArgs &a) {
+    if (a.hold == nullptr) return true;
+    int seen = 1;
+    if ((threadIdx.x & 31) == 0 && !hold_wait(a.hold, a.hold_cycles)) {
+        atomicOr(a.err, ERR_WAIT_TIMEOUT);
+        *reinterpret_cast<volatile int *>(&sm.abort) = 1;
+        seen = 0;
+    }
+    return __shfl_sync(FULL, seen, 0) != 0;
 }
 
 // A place in the ring of keys (units 0 .. K - 1) or of values (the others).
@@ -410,6 +439,8 @@ __device__ __forceinline__ void tc_setup(TcShared &sm, unsigned char *sq, int qb
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.done, 1);
+        mbar_init(&sm.meet, 8);
+        for (int i = 0; i < 8; ++i) sm.meets[i] = 0;
         sm.abort = 0;
         sm.acc_first = 0;
         sm.q_filled = 0;
@@ -471,7 +502,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
         KRing kr;
         VRing vr;
         uint32_t n = 0;
-        bool ok = true;
+        bool ok = keys || tc_hold(sm, a);
         while (ok && w.next(a)) {
             const int h = w.item / a.row_blocks, nt = w.t1 - w.t0;
             BoxAt box;
@@ -739,7 +770,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         make_uint4(pk[j / 2], pk[j / 2 + 1], pk[j / 2 + 2], pk[j / 2 + 3]);
                 if (any_poison) {
                     // Keys that some rows see and some do not, with values that are not finite: their products with p
-                    // go straight into O^T.  Both groups find the same keys and go through them together.
+                    // go straight into O^T.  Both groups find the same keys and go through them together, unless a wait
+                    // has run out: then they may not, and whoever is left alone gives up.
                     const int vseq = seq + i * D::UPT;
                     const unsigned mine = __ballot_sync(FULL, poison);
                     if (half == 0 && lane == 0) sm.bad[warp] = mine;
@@ -752,9 +784,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         tmem_wait_st();
                         if (tid == 0) sm.acc_first = 1;
                     }
-                    both_sync();
-                    for (int k = 0; k < TK; ++k) {
-                        if (!(sm.bad[k >> 5] >> (k & 31) & 1)) continue;
+                    bool together = both_meet(sm, err);
+                    for (int k = 0; together && k < TK; ++k) {
+                        // one word for the warp, whatever the other group does meanwhile
+                        const unsigned bad = __shfl_sync(FULL, reinterpret_cast<volatile uint32_t *>(sm.bad)[k >> 5], 0);
+                        if (!(bad >> (k & 31) & 1)) continue;
                         if (tid == k) {
                             for (int e = 0; e < DS * 64; ++e) {
                                 const int q = vseq + e / 64 / D::US, chunk = (e % 64) / 8;
@@ -766,7 +800,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                                 if (b) *v = 0;
                             }
                         }
-                        both_sync();
+                        together = both_meet(sm, err);
+                        if (!together) break;
                         for (int m = 0; m < MB; ++m) {
                             const int e = DS > 1 ? m * 128 + key : key & 63;
                             const float v = __uint_as_float(static_cast<uint32_t>(sm.side[e]) << 16);
@@ -786,7 +821,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                             }
                         }
                         tmem_wait_st();
-                        both_sync();
+                        together = both_meet(sm, err);
                     }
                 }
                 fence_proxy_async_smem();
@@ -968,7 +1003,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_weights_tc(const __grid_const
         const int dpi = TK / a.page_size, doff = TK % a.page_size;
         const uint64_t pol = l2_policy_evict_first();
         KRing kr;
-        bool ok = true;
+        bool ok = tc_hold(sm, a);
         while (ok && w.next(a)) {
             for (int rb = 0; ok && rb < a.row_blocks; ++rb) {
                 BoxAt box;

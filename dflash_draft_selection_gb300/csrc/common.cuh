@@ -81,6 +81,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
     return false;
 }
 
+// Test hook: one thread waits until *flag is nonzero, for at most max_cycles SM
+// clock cycles.  True if the word was seen set.
+__device__ __forceinline__ bool hold_wait(const unsigned int *flag, long long max_cycles) {
+    const long long t0 = clock64();
+    while (*reinterpret_cast<const volatile unsigned int *>(flag) == 0) {
+        if (clock64() - t0 > max_cycles) return false;
+        __nanosleep(256);
+    }
+    return true;
+}
+
 // Order this thread's earlier generic-proxy accesses to shared memory before
 // its later async-proxy (bulk copy) accesses.
 __device__ __forceinline__ void fence_proxy_async_smem() {

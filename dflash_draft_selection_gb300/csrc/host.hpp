@@ -70,6 +70,9 @@ inline dflash2_status after_launch() {
     return cudaPeekAtLastError() == cudaSuccess ? DFLASH2_OK : DFLASH2_ERR_CUDA;
 }
 
+// dflash2_test_hold's current setting, process-wide.
+void scan_hold(const unsigned int **flag, long long *cycles);
+
 // The front of a workspace of dflash2_paged_attn and dflash2_kv_evict: the
 // attention's tickets, which are zero between calls.  Both keep everything
 // else behind it, so the two may share a workspace.

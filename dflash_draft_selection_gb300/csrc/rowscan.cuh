@@ -49,6 +49,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "host.hpp"
 
 namespace dfl {
 
@@ -80,9 +81,6 @@ struct ScanGeom {
     const unsigned int *hold;
     long long hold_cycles;
 };
-
-// The hook's current setting, process-wide (host side; set by dflash2_test_hold).
-void scan_hold(const unsigned int **flag, long long *cycles);
 
 // Partial result of a row reduced by several CTAs.
 struct PartRec {
@@ -217,17 +215,6 @@ __device__ __forceinline__ void stream_issue(ScanSmem &sm, const ScanGeom &g, Wa
         ws.iss_c -= g.cpr;
         ws.iss_row += g.ld_bytes;
     }
-}
-
-// Test hook: lane 0 waits until *flag is nonzero, for at most max_cycles SM
-// clock cycles.  True if the word was seen set.
-__device__ __forceinline__ bool hold_wait(const unsigned int *flag, long long max_cycles) {
-    const long long t0 = clock64();
-    while (*reinterpret_cast<const volatile unsigned int *>(flag) == 0) {
-        if (clock64() - t0 > max_cycles) return false;
-        __nanosleep(256);
-    }
-    return true;
 }
 
 // Set up warp w's chunk stream over flat chunks [begin, end) and issue its

@@ -565,8 +565,10 @@ dflash2_status dflash2_device_error(uint32_t *code, int clear);
  * after max_cycles SM clock cycles (1 .. 2^32).  A warp that gives up issues
  * no copy, sets the device error word (DFLASH2_DEVERR_WAIT_TIMEOUT) and goes
  * through its rows as after any time-out: their outputs are -1 / NaN, and a
- * verify request that reads such a row gets status DFLASH2_ST_NAN.  flag NULL
- * switches the hook off.  Kernels already launched or captured keep the
+ * verify request that reads such a row gets status DFLASH2_ST_NAN.  The same
+ * holds for the warps of dflash2_paged_attn's tensor-core kernels that copy
+ * the values (and, for the weights, the keys): they give up as after any
+ * time-out.  flag NULL switches the hook off.  Kernels already launched or captured keep the
  * setting they were launched with.
  * Errors: INVALID_ARG for a misaligned flag or max_cycles out of range.
  */

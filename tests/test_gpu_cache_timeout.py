@@ -1,0 +1,51 @@
+"""Bounded waits of the paged cache path's kernels that run out, made on the host without a fault: the test hook keeps the
+warps that copy the values (for the weights' pass: the keys) from their first copy until a word is set that nothing sets.
+The kernels have to return, set the error word and leave the context usable; with the workspace zero-filled again
+the next call is as good as any."""
+import math
+
+import pytest
+import torch
+
+import dflash_draft_selection_gb300 as d2
+from tests._cache import Case
+from tests._util import cuda_or_skip
+from tests.test_gpu_paged_attn import check
+from tests.test_gpu_wait_timeout import LIMIT, held
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,G,lens", [(8, 2, [300, 8, 1000]), (8, 8, [260]), (16, 6, [16, 100, 2000, 264]), (1, 5, [777]),
+                                      (16, 8, [140] * 200)])
+@pytest.mark.parametrize("weights", [False, True])
+def test_attention_gives_up_and_recovers(d, T, G, lens, weights):
+    """Whole and cut items, tiles that some rows see in part, values that are not finite among them."""
+    dev = cuda_or_skip()
+    c = Case(d + T, lens, T, 2 * G, 2, d, 16)
+    for b, n in enumerate(lens):
+        pg, o = c.slot(b, n - 1)
+        c.v[pg, :, o] = math.nan
+    ws = d2.Workspace.for_paged_attn(len(lens), T, 2 * G, 2, d, BF)
+    q = c.q.to(dev)
+    on = c.on(dev)
+    _, code = held(lambda: d2.paged_attn(q, add_weights=weights, ws=ws, **on))
+    assert code == 1   # DFLASH2_DEVERR_WAIT_TIMEOUT
+    ws.buf.zero_()
+    fresh = Case(d + T, lens, T, 2 * G, 2, d, 16)
+    check(fresh, got=d2.paged_attn(q, ws=ws, **fresh.on(dev)))
+
+
+def test_a_hook_that_is_set_in_time_changes_nothing():
+    dev = cuda_or_skip()
+    c = Case(2, [500, 20], 8, 8, 2, 128, 16)
+    want = d2.paged_attn(c.q.to(dev), **c.on(dev))
+    flag = torch.ones(1, dtype=torch.int32, device=dev)
+    d2.test_hold(flag, LIMIT)
+    try:
+        got = d2.paged_attn(c.q.to(dev), add_weights=True, **c.on(dev))
+    finally:
+        d2.test_hold(None)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and d2.device_error() == 0
