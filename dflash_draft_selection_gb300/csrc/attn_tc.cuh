@@ -845,9 +845,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             const float m_row = key < NR ? -neg_m[key] : 0.f;
             if (key < mine) {
                 const int r = row0 + key;
-                L = sm.part[0][r] + sm.part[1][r] + sm.part[2][r] + sm.part[3][r];
-                if (tc_aborted(sm)) L = NAN;
-                else if (r >= real) L = 0.f;
+                L = r < real ? sm.part[0][r] + sm.part[1][r] + sm.part[2][r] + sm.part[3][r] : 0.f;
             }
             // An item cut in two whose other part is there is joined at once with what is still in tensor memory (the
             // next CTA takes its part first, so this is the usual case at the end of a stretch).
@@ -861,6 +859,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             tc_wait(sm, &sm.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err);
             both_sync();
             tc_fence_after();
+            if (tc_aborted(sm)) L = NAN;  // asked once nothing of the item is waited for any more
             const bool direct = !w.whole && sm.flag != 0;
             const int own = direct ? static_cast<int>(blockIdx.x) - q.c0 : -1;
             float *part = w.whole || direct ? nullptr : attn_part(a, blockIdx.x, w.starts);

@@ -49,3 +49,14 @@ def test_a_hook_that_is_set_in_time_changes_nothing():
     finally:
         d2.test_hold(None)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and d2.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,G,lens", [(1, 4, [100, 3, 128, 77]), (8, 6, [120, 60, 8]), (1, 5, [1500]), (8, 8, [2000, 900])])
+def test_attention_that_gave_up_is_nan(d, T, G, lens):
+    """Items of one tile, whose sums are complete before the product that never comes, and cut ones."""
+    dev = cuda_or_skip()
+    c = Case(d + T, lens, T, 2 * G, 2, d, 16)
+    on = c.on(dev)
+    (out, lse), code = held(lambda: d2.paged_attn(c.q.to(dev), **on))
+    assert code == 1 and torch.isnan(out).all() and torch.isnan(lse).all()
