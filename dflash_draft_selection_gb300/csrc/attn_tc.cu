@@ -63,7 +63,8 @@ dflash2_status attn_tc_launch(AttnArgs a, bool weights, cudaStream_t s) {
     a.item_cost = ATTN_ITEM_COST;
     a.err = err_word();
     if (!a.err) return DFLASH2_ERR_CUDA;
-    scan_hold(&a.hold, &a.hold_cycles);
+    const unsigned int *hold;
+    scan_hold(&hold, &a.hold_cycles);
     t.n = a.rows_cap <= 16 ? 16 : a.rows_cap <= 32 ? 32 : a.rows_cap <= 48 ? 48 : a.rows_cap <= 64 ? 64
           : a.rows_cap <= 96 ? 96 : 128;
     t.box_log2 = 3;
@@ -87,6 +88,7 @@ dflash2_status attn_tc_launch(AttnArgs a, bool weights, cudaStream_t s) {
     auto launch = [&](bool second) {
         const double tiles = static_cast<double>(a.B) * a.items * cap;
         t.ctas = tiles < sm_count() ? static_cast<int64_t>(tiles) : sm_count();
+        a.hold = second == weights ? hold : nullptr;  // the call's last launch
         t.a = a;
         t.weights = second;
         return a.d == 64 ? attn_tc64(t) : a.d == 128 ? attn_tc128(t) : attn_tc256(t);

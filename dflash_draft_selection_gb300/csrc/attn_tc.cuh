@@ -1083,7 +1083,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_weights_tc(const __grid_const
                         r0 = max(r0 - tok0, 0) * a.group;
                         r1 = min((r1 - tok0) * a.group, real);
                     }
-                    tc_wait(sm, &sm.s_full[half], used & 1, err);
+                    const bool ok = tc_wait(sm, &sm.s_full[half], used & 1, err);
                     __syncwarp();
                     tc_fence_after();
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1107,7 +1107,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_weights_tc(const __grid_const
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[half]);
-                    if (r0 < r1) atomicAdd(a.weight + place(i, page), (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    if (r0 < r1) atomicAdd(a.weight + place(i, page), ok ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : NAN);
                     page = page_next;
                     page_next = page_after;
                     pos = pos_next;

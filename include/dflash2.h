@@ -567,8 +567,8 @@ dflash2_status dflash2_device_error(uint32_t *code, int clear);
  * through its rows as after any time-out: their outputs are -1 / NaN, and a
  * verify request that reads such a row gets status DFLASH2_ST_NAN.  The same
  * holds for the warps of dflash2_paged_attn's tensor-core kernels that copy
- * the values (and, for the weights, the keys): they give up as after any
- * time-out.  flag NULL switches the hook off.  Kernels already launched or captured keep the
+ * the values (with DFLASH2_ATTN_WEIGHTS, the keys of the weights' pass
+ * instead): they give up as after any time-out.  flag NULL switches the hook off.  Kernels already launched or captured keep the
  * setting they were launched with.
  * Errors: INVALID_ARG for a misaligned flag or max_cycles out of range.
  */

@@ -60,3 +60,26 @@ def test_attention_that_gave_up_is_nan(d, T, G, lens):
     on = c.on(dev)
     (out, lse), code = held(lambda: d2.paged_attn(c.q.to(dev), **on))
     assert code == 1 and torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,G", [(1, 4), (8, 8), (16, 8)])
+def test_weights_that_gave_up_are_nan(d, T, G):
+    """The outputs of the first pass stand; every key that some row sees gets NaN, the others keep theirs."""
+    dev = cuda_or_skip()
+    c = Case(d + T, [T + 200, T, 900], T, 2 * G, 2, d, 16)
+    want = d2.paged_attn(c.q.to(dev), **c.on(dev))
+    on = c.on(dev)
+    w0 = on["cache"].weight.clone()
+    got, code = held(lambda: d2.paged_attn(c.q.to(dev), add_weights=True, **on))
+    assert code == 1 and all(torch.equal(x, y) for x, y in zip(got, want))
+    w1 = on["cache"].weight
+    for b in range(3):
+        for h in range(2):
+            assert torch.isnan(c.gather(w1.cpu(), b, h)).all()
+    used = torch.zeros_like(w0, dtype=torch.bool)
+    for b, n in enumerate(c.lens):
+        for s in range(n):
+            pg, o = c.slot(b, s)
+            used[pg, :, o] = True
+    assert torch.equal(w1[~used].nan_to_num(-1.0), w0[~used].nan_to_num(-1.0))
