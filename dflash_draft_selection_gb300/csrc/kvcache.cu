@@ -31,6 +31,8 @@ struct AppendArgs {
     float eps;
     void *q_out;
     int32_t *kv_len_out;
+    const unsigned int *hold;  // test hook: NULL, or a word that the streaming kernel's filling warps wait on
+    long long hold_cycles;
 };
 
 // Where a new token goes.
@@ -461,6 +463,38 @@ static __device__ __noinline__ bool stream_wait_long(StreamShared &sm, uint64_t 
 __device__ __forceinline__ bool stream_wait(StreamShared &sm, uint64_t *bar, uint32_t parity) {
     return __all_sync(FULL, mbar_try_wait(bar, parity) || stream_wait_long(sm, bar, parity));
 }
+// Test hook: a warp waits for the hook's word; if that runs out it gives up as after any time-out.
+__device__ __forceinline__ bool stream_hold(StreamShared &sm, const AppendArgs &a) {
+    if (a.hold == nullptr) return true;
+    int seen = 1;
+    if ((threadIdx.x & 31) == 0 && !hold_wait(a.hold, a.hold_cycles)) {
+        atomicOr(&g_err_append, ERR_WAIT_TIMEOUT);
+        *reinterpret_cast<volatile int *>(&sm.abort) = 1;
+        seen = 0;
+    }
+    return __shfl_sync(FULL, seen, 0) != 0;
+}
+// A token that a time-out kept from being turned: NaN in its queries, and in its keys and values if it has a place.
+template <typename E>
+__device__ __forceinline__ void append_lost(const AppendArgs &a, int64_t tok, int lane) {
+    const AppendToken at = append_token(a, append_raw(a, tok), lane == 0);
+    const uint32_t w = !at.live ? 0u : sizeof(E) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+    const uint4 x = make_uint4(w, w, w, w);
+    const int vecs = a.d * static_cast<int>(sizeof(E)) / 16;
+    uint4 *const q = reinterpret_cast<uint4 *>(static_cast<E *>(a.q_out) + tok * a.Hq * a.d);
+    for (int i = lane; i < a.Hq * vecs; i += 32) q[i] = x;
+    if (!at.live || at.page < 0) return;
+    for (int h = 0; h < a.Hkv; ++h) {
+        const int64_t row = at.page * a.page_stride + h * a.head_stride + at.off * a.slot_stride;
+        for (int i = lane; i < vecs; i += 32) {
+            reinterpret_cast<uint4 *>(reinterpret_cast<E *>(a.ck) + row)[i] = x;
+            reinterpret_cast<uint4 *>(reinterpret_cast<E *>(a.cv) + row)[i] = x;
+        }
+        const int64_t si = (static_cast<int64_t>(at.page) * a.Hkv + h) * a.page_size + at.off;
+        if (lane == 0 && a.weight) a.weight[si] = 0.f;
+        if (lane == 0 && a.pos) a.pos[si] = at.seq;
+    }
+}
 __device__ __forceinline__ void bulk_s2g(void *gdst, const void *ssrc, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(smem_addr(ssrc)),
                  "r"(bytes)
@@ -562,10 +596,13 @@ __global__ void __launch_bounds__((AS_SLOTS + AS_TURN) * 32, 1)
                 }
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         };
-        for (int64_t tok = blockIdx.x + s * G; tok < a.tokens; tok += slots * G, ++k) {
+        int64_t tok = blockIdx.x + s * G;
+        bool ok = stream_hold(sm, a);
+        for (; ok && tok < a.tokens; tok += slots * G, ++k) {
             const AppendToken at = append_token(a, append_raw(a, tok), lane == 0);
             if (k > 0) {
-                if (!stream_wait(sm, done, (k - 1) & 1)) break;
+                ok = stream_wait(sm, done, (k - 1) & 1);
+                if (!ok) break;
                 store();
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
@@ -606,12 +643,15 @@ __global__ void __launch_bounds__((AS_SLOTS + AS_TURN) * 32, 1)
             was_tok = tok;
         }
         if (k > 0) {
-            if (stream_wait(sm, done, (k - 1) & 1))
+            ok = ok && stream_wait(sm, done, (k - 1) & 1);
+            if (ok)
                 store();
             else
                 mbar_wait(full, (k - 1) & 1, AS_DRAIN);
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (!ok) tok -= slots * G;  // the slot's token was not stored
         }
+        for (; tok < a.tokens; tok += slots * G) append_lost<E>(a, tok, lane);  // only after a time-out
         return;
     }
     int s = warp / team;
@@ -948,6 +988,7 @@ static dflash2_status launch_append_stream(AppendArgs &a, dflash2_dtype dt, bool
                                 nullptr,                              k_append_stream<float, false, true>,
                                 nullptr,                              k_append_stream<float, true, true>};
     const Fn fn = table[(dt == DFLASH2_F32 ? 4 : 0) + (inter ? 2 : 0) + (norm ? 1 : 0)];
+    scan_hold(&a.hold, &a.hold_cycles);
     // raises the shared-memory limit, once
     blocks_per_sm(reinterpret_cast<const void *>(fn), (AS_SLOTS + AS_TURN) * 32, STREAM_SMEM);
     const int row = a.d * esize(dt), slot_bytes = (a.Hq + 2 * a.Hkv) * row + (a.rot * 4 + 15) / 16 * 16;

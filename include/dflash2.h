@@ -550,7 +550,7 @@ const char *dflash2_status_string(dflash2_status s);
 /*
  * Error word of the library's kernels on the current device: nonzero after a
  * kernel gave up on a bounded wait (it then wrote -1 / NaN outputs instead of
- * hanging; the word then holds DFLASH2_DEVERR_WAIT_TIMEOUT).  Synchronises
+ * hanging, dflash2_rope_append NaN to the cached keys and values too; the word then holds DFLASH2_DEVERR_WAIT_TIMEOUT).  Synchronises
  * the device.  clear != 0 resets the word.
  */
 #define DFLASH2_DEVERR_WAIT_TIMEOUT 1u
@@ -568,7 +568,8 @@ dflash2_status dflash2_device_error(uint32_t *code, int clear);
  * verify request that reads such a row gets status DFLASH2_ST_NAN.  The same
  * holds for the warps of dflash2_paged_attn's tensor-core kernels that copy
  * the values (with DFLASH2_ATTN_WEIGHTS, the keys of the weights' pass
- * instead): they give up as after any time-out.  flag NULL switches the hook off.  Kernels already launched or captured keep the
+ * instead) and of dflash2_rope_append's kernel for long blocks: they give up
+ * as after any time-out.  flag NULL switches the hook off.  Kernels already launched or captured keep the
  * setting they were launched with.
  * Errors: INVALID_ARG for a misaligned flag or max_cycles out of range.
  */

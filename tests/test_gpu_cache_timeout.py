@@ -10,6 +10,7 @@ import torch
 import dflash_draft_selection_gb300 as d2
 from tests._cache import Case
 from tests._util import cuda_or_skip
+from tests.test_gpu_kvcache import append_inputs, bits, check_append
 from tests.test_gpu_paged_attn import check
 from tests.test_gpu_wait_timeout import LIMIT, held
 
@@ -83,3 +84,35 @@ def test_weights_that_gave_up_are_nan(d, T, G):
             pg, o = c.slot(b, s)
             used[pg, :, o] = True
     assert torch.equal(w1[~used].nan_to_num(-1.0), w0[~used].nan_to_num(-1.0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_long_appends_that_gave_up_are_nan(dtype, interleaved):
+    """No token is turned: NaN queries, keys and values (zeros past q_len), nothing else in the cache."""
+    dev = cuda_or_skip()
+    mk = lambda: Case(7, [985] * 4, 925, 20, 4, 128, 24, dtype, q_lens=[925, 700, 0, 925], held=True)  # noqa: E731
+    c, lens = mk(), [0, 17, 5, 60]
+    c.table[3, 14] = c.k.shape[0] + 2                       # a page that is nowhere
+    a = append_inputs(c, 128, 1, 128, True)
+    on = c.on(dev)
+    cache = on["cache"]
+    want = {n: getattr(cache, n).clone() for n in ("k", "v", "weight", "pos")}
+    x = a["qkv"].to(dev)
+    kw = dict(interleaved=interleaved, q_norm=a["q_norm"].to(dev), k_norm=a["k_norm"].to(dev), q_len=on["q_len"])
+    (q, n), code = held(lambda: d2.rope_append(x[:, :, :20], x[:, :, 20:24], x[:, :, 24:], a["cos_sin"].to(dev),
+                                               a["pos_ids"].to(dev), cache, on["page_table"],
+                                               torch.tensor(lens, dtype=torch.int32, device=dev), **kw))
+    assert code == 1 and n.tolist() == [925, 717, 5, 985]
+    for b, m in enumerate(c.q_lens):
+        assert torch.isnan(q[b, :m]).all() and (q[b, m:] == 0).all()
+        s = lens[b] + torch.arange(m)
+        pg = c.table[b].long()[s // 24]
+        at = pg < c.k.shape[0]
+        pg, off, s = pg[at].to(dev), (s % 24)[at].to(dev), s[at].to(dev)
+        want["k"][pg, :, off] = want["v"][pg, :, off] = math.nan
+        want["weight"][pg, :, off] = 0.0
+        want["pos"][pg, :, off] = s[:, None].to(torch.int32)
+    for name in want:
+        assert torch.equal(bits(getattr(cache, name)), bits(want[name])), name
+    check_append(mk(), lens, append_inputs(c, 128, 1, 128, True), interleaved)
