@@ -1181,7 +1181,7 @@ extern "C" dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const 
     const dim3 sgrid(static_cast<unsigned>(heads));
     // One launch where a head has few moves to make; a launch of its own spreads many over the GPU.  Lengths in one
     // array need the second launch: heads read what one would write.
-    const bool one = a.max_moves <= EVICT_FEW && kv_len_out != kv_len;
+    const bool one = a.max_moves <= EVICT_FEW && kv_len_out != kv_len && kv_len_out != seq_len;
     auto select = [&](auto *fn, size_t most, size_t bytes) {
         blocks_per_sm(reinterpret_cast<const void *>(fn), EV_THREADS, most);  // raises the shared-memory limit, once
         return launch_pdl(fn, a, sgrid, EV_THREADS, bytes, s);

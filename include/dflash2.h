@@ -528,7 +528,8 @@ dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, const int32_t *
  *
  * kv_len [B]: slots in use (clamped to what the table holds).  seq_len [B]:
  *   the length of the sequence (the newest key's position + 1), or NULL
- *   (kv_len).  kv_len_out [B]: min(kv_len, budget); may be kv_len itself.
+ *   (kv_len).  kv_len_out [B]: min(kv_len, budget); may be kv_len or seq_len
+ *   itself, and must not overlap them otherwise.
  * A slot whose page id is out of range is never kept before another one and
  * never copied.
  * If more than `budget` slots are protected, the lower slots stay.

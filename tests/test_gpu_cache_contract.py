@@ -98,3 +98,20 @@ def test_eviction_and_attention_in_one_workspace(budget):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(*results))
     assert d2.device_error() == 0
+
+
+def test_evicted_lengths_over_the_sequences_lengths():
+    """kv_len_out may be kv_len or seq_len: every head reads both before either is written."""
+    dev = cuda_or_skip()
+    lens, budget = [60 + i % 5 for i in range(300)], 40
+    c = Case(5, lens, 1, 8, 8, 8, 16, held=True)
+    results = []
+    for shared in (False, True):
+        on = c.on(dev)
+        seq = torch.tensor([s + 1 for s in c.seq_pos], dtype=torch.int32, device=dev)
+        n = d2.kv_evict(on["cache"], on["page_table"], on["kv_len"], budget, 20, 2, seq_len=seq,
+                        out=seq if shared else None)
+        torch.cuda.synchronize()
+        assert n.tolist() == [budget] * 300
+        results.append([bits(getattr(on["cache"], x)) for x in SIDES])
+    assert all(torch.equal(x, y) for x, y in zip(*results))
