@@ -1035,7 +1035,7 @@ static bool registered(const void *p) {
 // tried alone, on a machine without a GPU too) are not touched.
 static dflash2_status append_no_tokens(const int32_t *kv_len, int64_t B, int32_t *kv_len_out, cudaStream_t s) {
     if (!kv_len_out) return DFLASH2_OK;
-    if (!kv_len || !al4(kv_len) || !al4(kv_len_out) || kv_len_out == kv_len) return DFLASH2_ERR_INVALID_ARG;
+    if (!kv_len || !al4(kv_len) || !al4(kv_len_out)) return DFLASH2_ERR_INVALID_ARG;
     if (!registered(kv_len) || !registered(kv_len_out)) return DFLASH2_OK;
     const cudaError_t e = cudaMemcpyAsync(kv_len_out, kv_len, static_cast<size_t>(B) * sizeof(int32_t),
                                           cudaMemcpyDeviceToDevice, s);
@@ -1054,6 +1054,9 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
         rot > cache->d || axes < 1 || n_pos < 1)
         return DFLASH2_ERR_INVALID_ARG;
     if (B == 0) return DFLASH2_OK;
+    // tokens read what one of them would write
+    if (kv_len_out && (kv_len_out == kv_len || kv_len_out == q_len || kv_len_out == seq_pos))
+        return DFLASH2_ERR_INVALID_ARG;
     if (T == 0) return append_no_tokens(kv_len, B, kv_len_out, reinterpret_cast<cudaStream_t>(stream));
     const int e = esize(cache->dt);
     const int64_t d = cache->d;
@@ -1061,7 +1064,7 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
         !aligned16(v) || !aligned16(q_out) || !aligned16(q_norm) || !aligned16(k_norm) || !aligned16(cos_sin) ||
         !al4(kv_len) || !al4(q_len) || !al4(seq_pos) || !al4(pos_ids) || !al4(kv_len_out) || q_stride < Hq * d ||
         k_stride < cache->Hkv * d || v_stride < cache->Hkv * d || q_stride * e % 16 || k_stride * e % 16 ||
-        v_stride * e % 16 || kv_len_out == kv_len)
+        v_stride * e % 16)
         return DFLASH2_ERR_INVALID_ARG;
     if (d > 1024 || B * T >= (int64_t(1) << 31)) return DFLASH2_ERR_UNSUPPORTED;
     AppendArgs a = {};

@@ -66,3 +66,10 @@ def test_a_call_of_more_places_than_31_bits_is_refused():
         assert attend(dict(small, dt=dt), B=int(2 ** 31 / per) + 1, T=1, Hq=1, max_pages=1) == UNSUPPORTED
         # one request less passes the guard, and is stopped by the next check
         assert attend(dict(small, dt=dt), B=int(2 ** 31 / per), T=1, Hq=1, max_pages=1, ws_bytes=0) == WORKSPACE
+
+
+def test_appended_lengths_over_an_array_that_tokens_read_are_refused():
+    for T in (0, 2):
+        for n in ("kv_len", "q_len", "seq_pos"):
+            p = ctypes.c_void_p(65536)
+            assert append(T=T, kv_len_out=p, **{n: p}) == INVALID, n
