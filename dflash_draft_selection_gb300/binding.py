@@ -132,45 +132,60 @@ def _dtype_code(dt: torch.dtype) -> int:
     raise TypeError(f"unsupported dtype {dt}")
 
 
-def _int32(B: int, name: str, t):
-    """A per-request array: contiguous int32 [B] on the GPU (None passes).  Returns its address."""
+def _here(cache) -> int:
+    """The index of a cache's device, which has to be the current one: a call launches there."""
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"the cache lies on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def _int32(B: int, name: str, t, dev: int):
+    """A per-request array: contiguous int32 [B] on GPU `dev` (None passes).  Returns its address."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: contiguous int32 [{B}] on the GPU")
+    if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: contiguous int32 [{B}] on the cache's GPU")
     return t.data_ptr()
 
 
-def _page_table(t: torch.Tensor, B: int):
+def _page_table(t: torch.Tensor, B: int, dev: int):
     """Address and pages per request of a page table."""
     shape = t.shape
-    if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != B or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"page_table: contiguous int32 [{B}, pages] on the GPU")
+    if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != B or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"page_table: contiguous int32 [{B}, pages] on the cache's GPU")
     return t.data_ptr(), shape[1]
 
 
-def _heads(name: str, t: torch.Tensor, dt, B: int, T: int, H: int, d: int):
+def _heads(name: str, t: torch.Tensor, dt, B: int, T: int, H: int, d: int, dev: int):
     """Address and token stride of [B, T, H, d] with contiguous heads and one stride from token to token."""
-    if t.dtype is not dt or t.shape != (B, T, H, d) or not t.is_cuda:
-        raise ValueError(f"{name}: {dt} [{B}, {T}, {H}, {d}] on the GPU")
+    if t.dtype is not dt or t.shape != (B, T, H, d) or t.get_device() != dev:
+        raise ValueError(f"{name}: {dt} [{B}, {T}, {H}, {d}] on the cache's GPU")
     s0, s1, s2, s3 = t.stride()
     if (s3 != 1 and d > 1) or (s2 != d and H > 1) or (B > 1 and T > 1 and s0 != T * s1):
         raise ValueError(f"{name}: contiguous heads and one stride from token to token")
     return t.data_ptr(), s1 if T > 1 else (s0 if B > 1 else H * d)
 
 
-def _dense(name: str, t, dt, shape):
-    """Address of a contiguous tensor of a type and shape on the GPU (None passes)."""
+def _dense(name: str, t, dt, shape, dev: int):
+    """Address of a contiguous tensor of a type and shape on GPU `dev` (None passes)."""
     if t is None:
         return None
-    if t.dtype is not dt or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: contiguous {dt} {list(shape)} on the GPU")
+    if t.dtype is not dt or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: contiguous {dt} {list(shape)} on the cache's GPU")
     return t.data_ptr()
 
 
-def _raw_stream(t: torch.Tensor) -> int:
-    """The current stream of a tensor's device as a number (torch.cuda.current_stream without its object)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+def _scratch(ws, dev: int):
+    """Address and size of a workspace."""
+    if ws.buf.get_device() != dev:
+        raise ValueError("ws: a workspace on the cache's GPU")
+    return ws.buf.data_ptr(), ws.buf.numel()
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream of a device as a number (torch.cuda.current_stream without its object)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _stream(device) -> ctypes.c_void_p:
@@ -242,7 +257,8 @@ class Workspace:
 class KVCache:
     """A paged key-value cache: k and v [num_pages, Hkv, page_size, d] (bf16 or f32), of any strides with
     contiguous rows of d (a [num_pages, page_size, Hkv, d] pool is passed transposed), and the optional side
-    arrays weight (f32) and pos (i32), contiguous [num_pages, Hkv, page_size].  Holds views, copies nothing."""
+    arrays weight (f32) and pos (i32), contiguous [num_pages, Hkv, page_size].  Holds views, copies nothing.  A call
+    takes tensors of the cache's device, which has to be the current one."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, weight: torch.Tensor | None = None,
                  pos: torch.Tensor | None = None):
@@ -257,7 +273,7 @@ class KVCache:
             raise ValueError("a cache's tensors lie on one device")
         self.k, self.v, self.weight, self.pos = k, v, weight, pos
         self.num_pages, self.Hkv, self.page_size, self.d = k.shape
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype, self._dev = k.device, k.dtype, k.get_device()
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self._rec = _CacheRecord(ptr(k), ptr(v), ptr(weight), ptr(pos), self.num_pages, k.stride(0), k.stride(1),
                                  k.stride(2), self.Hkv, self.page_size, self.d, _dtype(k))
@@ -476,27 +492,27 @@ def rope_append(q, k, v, cos_sin, pos_ids, cache: KVCache, page_table, kv_len, p
     projection are taken as they are); cos_sin [n_pos, rot] f32; pos_ids [axes, B, T] int32; pair_axis [rot / 2]
     uint8; kv_len [B] int32, the slots in use before the call.  Returns (rotated q [B, T, Hq, d], kv_len + q_len)."""
     B, T, Hq, d = q.shape
-    dt, Hkv = cache.dtype, cache.Hkv
+    dt, Hkv, dev = cache.dtype, cache.Hkv, _here(cache)
     if d != cache.d:
         raise ValueError(f"q: heads of {cache.d}")
-    qp, qs = _heads("q", q, dt, B, T, Hq, d)
-    kp, ks = _heads("k", k, dt, B, T, Hkv, d)
-    vp, vs = _heads("v", v, dt, B, T, Hkv, d)
+    qp, qs = _heads("q", q, dt, B, T, Hq, d, dev)
+    kp, ks = _heads("k", k, dt, B, T, Hkv, d, dev)
+    vp, vs = _heads("v", v, dt, B, T, Hkv, d, dev)
     n_pos, rot = cos_sin.shape
     axes = pos_ids.shape[0]
-    table, pages = _page_table(page_table, B)
+    table, pages = _page_table(page_table, B, dev)
     if out is None:
         out = (torch.empty((B, T, Hq, d), dtype=dt, device=q.device), torch.empty_like(kv_len))
     q_out, kv_len_out = out
     _check("dflash2_rope_append",
            (_lib or load_library()).dflash2_rope_append(
-               cache._ref, table, pages, _int32(B, "kv_len", kv_len), _int32(B, "q_len", q_len),
-               _int32(B, "seq_pos", seq_pos), qp, kp, vp, qs, ks, vs, B, T, Hq,
-               _dense("cos_sin", cos_sin, torch.float32, (n_pos, rot)), n_pos, rot,
-               _dense("pos_ids", pos_ids, torch.int32, (axes, B, T)), axes,
-               _dense("pair_axis", pair_axis, torch.uint8, (rot // 2,)), interleaved,
-               _dense("q_norm", q_norm, dt, (d,)), _dense("k_norm", k_norm, dt, (d,)), eps,
-               _dense("out", q_out, dt, (B, T, Hq, d)), _int32(B, "out", kv_len_out), _raw_stream(q)))
+               cache._ref, table, pages, _int32(B, "kv_len", kv_len, dev), _int32(B, "q_len", q_len, dev),
+               _int32(B, "seq_pos", seq_pos, dev), qp, kp, vp, qs, ks, vs, B, T, Hq,
+               _dense("cos_sin", cos_sin, torch.float32, (n_pos, rot), dev), n_pos, rot,
+               _dense("pos_ids", pos_ids, torch.int32, (axes, B, T), dev), axes,
+               _dense("pair_axis", pair_axis, torch.uint8, (rot // 2,), dev), interleaved,
+               _dense("q_norm", q_norm, dt, (d,), dev), _dense("k_norm", k_norm, dt, (d,), dev), eps,
+               _dense("out", q_out, dt, (B, T, Hq, d), dev), _int32(B, "out", kv_len_out, dev), _raw_stream(dev)))
     return out
 
 
@@ -506,10 +522,10 @@ def paged_attn(q, cache: KVCache, page_table, kv_len, scale: float | None = None
     own among them; scale 1 / sqrt(d) unless given; add_weights adds every cached key's softmax weight to
     cache.weight.  Returns (out [B, T, Hq, d], lse [B, T, Hq] f32)."""
     B, T, Hq, d = shape = q.shape
-    dt = cache.dtype
+    dt, dev = cache.dtype, _here(cache)
     if d != cache.d:
         raise ValueError(f"q: heads of {cache.d}")
-    table, pages = _page_table(page_table, B)
+    table, pages = _page_table(page_table, B, dev)
     if ws is None:
         ws = Workspace.for_paged_attn(B, T, Hq, cache.Hkv, d, dt, q.device)
     if out is None:
@@ -517,11 +533,11 @@ def paged_attn(q, cache: KVCache, page_table, kv_len, scale: float | None = None
     o, lse = out
     _check("dflash2_paged_attn",
            (_lib or load_library()).dflash2_paged_attn(
-               cache._ref, table, pages, _int32(B, "kv_len", kv_len), _int32(B, "q_len", q_len),
-               _int32(B, "seq_pos", seq_pos), _dense("q", q, dt, shape), B, T, Hq,
+               cache._ref, table, pages, _int32(B, "kv_len", kv_len, dev), _int32(B, "q_len", q_len, dev),
+               _int32(B, "seq_pos", seq_pos, dev), _dense("q", q, dt, shape, dev), B, T, Hq,
                d ** -0.5 if scale is None else scale, window,
-               (ATTN_CAUSAL if causal else 0) | (ATTN_WEIGHTS if add_weights else 0), _dense("out", o, dt, shape),
-               _dense("out", lse, torch.float32, (B, T, Hq)), ws.buf.data_ptr(), ws.buf.numel(), _raw_stream(q)))
+               (ATTN_CAUSAL if causal else 0) | (ATTN_WEIGHTS if add_weights else 0), _dense("out", o, dt, shape, dev),
+               _dense("out", lse, torch.float32, (B, T, Hq), dev), *_scratch(ws, dev), _raw_stream(dev)))
     return out
 
 
@@ -529,16 +545,16 @@ def kv_evict(cache: KVCache, page_table, kv_len, budget: int, recent: int = 0, s
              out=None):
     """dflash2_kv_evict.  Every head keeps `budget` slots of a request that has more: those of the `recent` newest and
     `sink` first positions, then the most attended.  Returns min(kv_len, budget) [B] int32."""
-    B = kv_len.shape[0]
-    table, pages = _page_table(page_table, B)
+    B, dev = kv_len.shape[0], _here(cache)
+    table, pages = _page_table(page_table, B, dev)
     if ws is None:
         ws = Workspace.for_kv_evict(B, cache.Hkv, pages * cache.page_size, budget, kv_len.device)
     if out is None:
         out = torch.empty_like(kv_len)
     _check("dflash2_kv_evict",
            (_lib or load_library()).dflash2_kv_evict(
-               cache._ref, table, pages, _int32(B, "kv_len", kv_len), _int32(B, "seq_len", seq_len), B, budget, recent,
-               sink, _int32(B, "out", out), ws.buf.data_ptr(), ws.buf.numel(), _raw_stream(kv_len)))
+               cache._ref, table, pages, _int32(B, "kv_len", kv_len, dev), _int32(B, "seq_len", seq_len, dev), B, budget,
+               recent, sink, _int32(B, "out", out, dev), *_scratch(ws, dev), _raw_stream(dev)))
     return out
 
 
