@@ -1067,6 +1067,8 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
         v_stride * e % 16)
         return DFLASH2_ERR_INVALID_ARG;
     if (d > 1024 || B * T >= (int64_t(1) << 31)) return DFLASH2_ERR_UNSUPPORTED;
+    // a token's queries would go where another's queries, or a key or value, are still to be read
+    if ((q_out == q && q_stride != Hq * d && B * T > 1) || q_out == k || q_out == v) return DFLASH2_ERR_INVALID_ARG;
     AppendArgs a = {};
     a.ck = static_cast<char *>(cache->k);
     a.cv = static_cast<char *>(cache->v);

@@ -449,15 +449,17 @@ typedef struct {
  * cos_sin [n_pos, rot] f32.  pos_ids [axes, B, T].  pair_axis [rot / 2] or
  *   NULL (axis 0); values above axes - 1 count as axes - 1.
  * q_norm, k_norm [d] of dt, or NULL.
- * q_out [B, T, Hq, d], contiguous.  kv_len_out [B] or NULL: kv_len + q_len;
- *   must not overlap kv_len, q_len or seq_pos.  With T = 0 it is kv_len, and nothing else is
- *   read or written.
+ * q_out [B, T, Hq, d], contiguous; may be q itself where q is contiguous
+ *   (q_stride = Hq * d), and must not overlap q, k or v otherwise.
+ * kv_len_out [B] or NULL: kv_len + q_len; must not overlap kv_len, q_len or
+ *   seq_pos.  With T = 0 it is kv_len, and nothing else is read or written.
  * A token whose position id is outside [0, n_pos) gets NaN in the rotated
  * entries of its query and key.  A token whose slot has no valid page (past
  * the table, or a page id out of range) is not stored and its query comes
  * out NaN.
  * Errors: the common ones; INVALID_ARG for NULL q, k, v, q_out, kv_len,
- * cos_sin or pos_ids; kv_len_out the same as kv_len, q_len or seq_pos; Hq < 1,
+ * cos_sin or pos_ids; kv_len_out the same as kv_len, q_len or seq_pos; q_out the
+ * same as k, v or a q of several tokens that is not contiguous; Hq < 1,
  * rot odd, < 2 or > d, axes < 1, n_pos < 1, strides below the width of a
  * token's heads or not multiples of 16 bytes; dt not F32 or BF16.
  * UNSUPPORTED for d > 1024 or B * T >= 2^31.

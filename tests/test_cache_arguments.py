@@ -73,3 +73,9 @@ def test_appended_lengths_over_an_array_that_tokens_read_are_refused():
         for n in ("kv_len", "q_len", "seq_pos"):
             p = ctypes.c_void_p(65536)
             assert append(T=T, kv_len_out=p, **{n: p}) == INVALID, n
+
+
+def test_queries_turned_in_place_have_to_be_contiguous():
+    p, q = ctypes.c_void_p(65536), ctypes.c_void_p(131072)
+    assert append(q=p, q_out=p, qs=512) == INVALID           # slices of a fused projection
+    assert append(k=q, q_out=q) == append(v=q, q_out=q) == INVALID

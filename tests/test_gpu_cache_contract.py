@@ -115,3 +115,25 @@ def test_evicted_lengths_over_the_sequences_lengths():
         assert n.tolist() == [budget] * 300
         results.append([bits(getattr(on["cache"], x)) for x in SIDES])
     assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,rot", [(3, 5, 6, 2, 128, 128), (2, 3, 4, 2, 40, 10), (4, 1000, 20, 4, 128, 64)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_queries_turned_in_place(dtype, B, T, Hq, Hkv, d, rot, interleaved):
+    """q_out may be a contiguous q: in vectors, entry by entry and in long blocks."""
+    dev = cuda_or_skip()
+    c = Case(d + T, [T + 10] * B, T, Hq, Hkv, d, 24, dtype, held=True)
+    a = append_inputs(c, T, 1, rot, True)
+    x = a["qkv"].to(dev)
+    k, v = x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+    lens = torch.full((B,), 10, dtype=torch.int32, device=dev)
+    results = []
+    for in_place in (False, True):
+        on, q = c.on(dev), x[:, :, :Hq].contiguous()
+        out = (q if in_place else torch.empty_like(q), torch.empty_like(lens))
+        d2.rope_append(q, k, v, a["cos_sin"].to(dev), a["pos_ids"].to(dev), on["cache"], on["page_table"], lens,
+                       interleaved=interleaved, q_norm=a["q_norm"].to(dev), k_norm=a["k_norm"].to(dev), out=out)
+        torch.cuda.synchronize()
+        results.append([bits(out[0]), out[1]] + [bits(getattr(on["cache"], n)) for n in SIDES])
+    assert all(torch.equal(y, z) for y, z in zip(*results))
