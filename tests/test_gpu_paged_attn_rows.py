@@ -1,0 +1,58 @@
+"""dflash2_paged_attn over the row counts that the tensor-core kernels are built for (16, 32, 48, 64, 96 and 128 rows
+per cached key), each with head dimensions 64, 128 and 256, with the attention weights.  Bounds as in
+test_gpu_paged_attn."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import dflash_draft_selection_gb300 as d2
+from tests._cache import Case, attn64
+from tests._util import cuda_or_skip
+from tests.test_gpu_paged_attn import check
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,G", [(2, 8), (8, 4), (4, 6), (8, 6), (8, 8), (16, 4), (16, 6), (20, 4), (16, 8), (31, 4)])
+def test_every_row_count(d, T, G):
+    """Lengths of several tiles, so that both score buffers and both P buffers are used again, and a cut item."""
+    check(Case(d + T + G, [T, 640 + T, 1500, 129], T, 2 * G, 2, d, 32), weights=True)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("T,G", [(8, 4), (8, 8), (16, 4), (16, 6), (16, 8)])
+def test_every_row_count_with_positions_and_a_window(d, T, G):
+    check(Case(d * T + G, [T, 700, 400], T, G, 1, d, 16, held=True), window=300, weights=True)
+    check(Case(d * T + G, [T, 700, 400], T, G, 1, d, 16), window=130, causal=False, weights=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,G", [(8, 2), (8, 8), (16, 6), (16, 8)])
+def test_values_that_are_not_finite_in_neighbouring_tiles(d, T, G):
+    """The block's keys lie on both sides of a tile's edge and hold NaN and Inf that only later tokens see."""
+    n = 256 + T // 2
+    mk = lambda: Case(d + G, [n, 100], T, G, 1, d, 16)  # noqa: E731
+    c, first = mk(), n - T
+    nan_at, inf_at, col = first + 2, 256 + 1, d - 3          # tokens 2 and T / 2 + 1 are the first to see them
+    pg, o = c.slot(0, nan_at)
+    c.v[pg, 0, o, 5] = math.nan
+    pg, o = c.slot(0, inf_at)
+    c.v[pg, 0, o, col] = -math.inf
+    c.v[pg, 0, o, 7] = math.inf
+    dev = cuda_or_skip()
+    out, lse = d2.paged_attn(c.q.to(dev), **c.on(dev))
+    torch.cuda.synchronize()
+    r_out, r_lse, _, pv, _ = attn64(mk(), d ** -0.5, True, 0)
+    g = out.float().cpu().numpy()
+    assert np.isnan(g[0, 2:, :, 5]).all()
+    assert (g[0, T // 2 + 1:, :, col] == -math.inf).all() and (g[0, T // 2 + 1:, :, 7] == math.inf).all()
+    fine = np.ones(g.shape, dtype=bool)
+    fine[0, 2:, :, 5] = fine[0, T // 2 + 1:, :, col] = fine[0, T // 2 + 1:, :, 7] = False
+    # two roundings to bf16 (p and the result) and the fp32 rest
+    assert (np.abs(g - r_out)[fine] <= (2.0 ** -7 * pv + 1e-6)[fine]).all()
+    np.testing.assert_allclose(lse.cpu().numpy(), r_lse, atol=1e-4)
+    assert d2.device_error() == 0
