@@ -62,7 +62,12 @@ constexpr int MMA_WARP = 8, K_WARP = 9, V_WARP = 10, Q_WARP = 11;
 constexpr int HOLES = 16;          // tiles whose flags are kept: more than the ring holds
 constexpr int MAX_UNITS = 12;
 constexpr float M_STEP = 8.f;      // a row's reference moves when a score exceeds it by more (in log2)
-constexpr float M_NONE = -1e30f;   // the reference of a row that has seen nothing
+// The reference of a row that has seen nothing: below every finite score, so that the first one replaces it or, if it is
+// no larger, is taken from it.
+constexpr float M_NONE = -3.402823466e38f;
+// x = s c2 - m in one fused step leaves what the reference's own product was rounded by, up to ulp(m) / 2: nothing to
+// speak of, but past this reference 2 and more, and past 2^31 more than an exponent holds.
+constexpr float M_HUGE = 16777216.f;
 constexpr long long TC_WAIT = 4000000000ll;  // ~2 s
 constexpr long long TC_DRAIN = 200000000ll;  // ~0.1 s
 constexpr int SM_BYTES = 232448;   // shared memory of a CTA
@@ -87,6 +92,7 @@ struct TcShared {
     uint32_t bad[4];
     uint32_t tmem;
     int abort, acc_first, flag, q_filled;
+    int huge[2];  // a row of the group has a reference beyond M_HUGE
 };
 
 // A head dimension's slots and units, and a call's ring.
@@ -596,6 +602,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     sm.row_at[row0 + key] = (row0 + key) / a.group * a.Hq + (row0 + key) % a.group;
             }
             if (tid == 0) sm.acc_first = 0;
+            if (key == 0) sm.huge[half] = 0;
+            bool huge = false;
             soft_sync(half);
             // With an array of positions a key's view takes two dependent loads: the page one tile further ahead than
             // the position.
@@ -682,15 +690,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     }
                     __syncwarp();
                 }
-                // x = s c2 - m, in place
-                auto exponents = [&]() {
+                // x = s f - m, in place
+                auto exponents = [&](float f) {
 #pragma unroll
                     for (int j = 0; j < NR; j += 4) {
                         const float4 m = *reinterpret_cast<const float4 *>(neg_m + j);
-                        x[j] = fmaf(x[j], c2, m.x);
-                        x[j + 1] = fmaf(x[j + 1], c2, m.y);
-                        x[j + 2] = fmaf(x[j + 2], c2, m.z);
-                        x[j + 3] = fmaf(x[j + 3], c2, m.w);
+                        x[j] = fmaf(x[j], f, m.x);
+                        x[j + 1] = fmaf(x[j + 1], f, m.y);
+                        x[j + 2] = fmaf(x[j + 2], f, m.z);
+                        x[j + 3] = fmaf(x[j + 3], f, m.w);
                     }
                     if (masked) {
 #pragma unroll
@@ -699,8 +707,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     }
                 };
                 bool slow = true;
-                if (i > 0) {
-                    exponents();
+                if (i > 0 && !huge) {
+                    exponents(c2);
                     float xm = NEG_INF;
 #pragma unroll
                     for (int j = 0; j < NR; ++j) xm = fmaxf(xm, x[j]);
@@ -727,9 +735,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         mn = fmaxf(mn, mo);
                         fac[key] = ex2(mo - mn);
                         neg_m[key] = -mn;
+                        if (mn != M_NONE && fabsf(mn) > M_HUGE) sm.huge[half] = 1;
                     }
                     any_poison = soft_any(half, poison);
-                    exponents();
+                    huge = *reinterpret_cast<volatile int *>(&sm.huge[half]) != 0;
+                    if (huge) {  // the products rounded as the references are
+#pragma unroll
+                        for (int j = 0; j < NR; ++j) x[j] *= c2;
+                    }
+                    exponents(huge ? 1.f : c2);
                     if (i > 0) {
 #pragma unroll
                         for (int j = 0; j < NR; ++j) l[j] *= fac[j];

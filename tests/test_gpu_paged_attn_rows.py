@@ -56,3 +56,55 @@ def test_values_that_are_not_finite_in_neighbouring_tiles(d, T, G):
     assert (np.abs(g - r_out)[fine] <= (2.0 ** -7 * pv + 1e-6)[fine]).all()
     np.testing.assert_allclose(lse.cpu().numpy(), r_lse, atol=1e-4)
     assert d2.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("big", [1e15, 1e17, 1e18])
+def test_scores_far_below_zero(dtype, d, big):
+    """Scores of -1e30 and less are scores: equal ones give the mean of the values, whatever their size."""
+    T, lens = 3, [3, 200, 700]
+    c = Case(d, lens, T, 4, 2, d, 16, dtype)
+    c.q[:] = big
+    c.k[:] = -big
+    dev = cuda_or_skip()
+    out, lse = d2.paged_attn(c.q.to(dev), **c.on(dev))
+    torch.cuda.synchronize()
+    score = -float(c.q[0, 0, 0, 0]) * -float(c.k[0, 0, 0, 0]) * d * d ** -0.5
+    assert torch.isfinite(lse).all() and (lse.double().cpu() / -abs(score) - 1).abs().max() <= 2.0 ** -18
+    for b, n in enumerate(lens):
+        for t in range(T):
+            m = n - T + t + 1
+            for h in range(4):
+                V = c.gather(c.v, b, h // 2)[:m].double()
+                lim = (2.0 ** -7 * (dtype == BF) + (m + 8) * 2.0 ** -24 + 2.0 ** -20) * V.abs().mean(0)
+                assert ((out[b, t, h].double().cpu() - V.mean(0)).abs() <= lim).all()
+    assert d2.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("big", [3e3, 1e5, 1e8, 1e16])
+def test_scores_far_apart(dtype, d, big):
+    """Scores of 1e7 to 1e33 of either sign: the largest one takes it all, and its value comes out."""
+    T, lens = 3, [40, 300, 700]
+    c = Case(d + 1, lens, T, 4, 2, d, 16, dtype, sigma=big)
+    c.q = (c.q.float() * big).to(dtype)
+    dev = cuda_or_skip()
+    out, lse = d2.paged_attn(c.q.to(dev), **c.on(dev))
+    torch.cuda.synchronize()
+    sure = 0
+    for b, n in enumerate(lens):
+        for t in range(T):
+            m = n - T + t + 1
+            for h in range(4):
+                K, V = (c.gather(x, b, h // 2)[:m].double() for x in (c.k, c.v))
+                x = K @ c.q[b, t, h].double() * d ** -0.5
+                top = x.topk(2)
+                off = float((K.abs() @ c.q[b, t, h].double().abs()).max()) * d ** -0.5 * (d + 4) * 2.0 ** -24
+                assert abs(float(lse[b, t, h]) - float(top.values[0])) <= off + 2.0 ** -20 * abs(float(top.values[0])) + 1
+                if float(top.values[0] - top.values[1]) <= 2 * off + 100:
+                    continue               # two scores that fp32 may not tell apart
+                sure += 1
+                assert ((out[b, t, h].double().cpu() - V[top.indices[0]]).abs() <= 1e-6 * V.abs().max()).all()
+    assert sure > 30 and d2.device_error() == 0
