@@ -176,6 +176,13 @@ def _dense(name: str, t, dt, shape, dev: int):
     return t.data_ptr()
 
 
+def _count(name: str, n: int) -> int:
+    """A number that C takes in 32 bits (ctypes would drop the others)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}: {n} does not fit 32 bits")
+    return n
+
+
 def _scratch(ws, dev: int):
     """Address and size of a workspace."""
     if ws.buf.get_device() != dev:
@@ -535,7 +542,7 @@ def paged_attn(q, cache: KVCache, page_table, kv_len, scale: float | None = None
            (_lib or load_library()).dflash2_paged_attn(
                cache._ref, table, pages, _int32(B, "kv_len", kv_len, dev), _int32(B, "q_len", q_len, dev),
                _int32(B, "seq_pos", seq_pos, dev), _dense("q", q, dt, shape, dev), B, T, Hq,
-               d ** -0.5 if scale is None else scale, window,
+               d ** -0.5 if scale is None else scale, _count("window", window),
                (ATTN_CAUSAL if causal else 0) | (ATTN_WEIGHTS if add_weights else 0), _dense("out", o, dt, shape, dev),
                _dense("out", lse, torch.float32, (B, T, Hq), dev), *_scratch(ws, dev), _raw_stream(dev)))
     return out
@@ -547,6 +554,7 @@ def kv_evict(cache: KVCache, page_table, kv_len, budget: int, recent: int = 0, s
     `sink` first positions, then the most attended.  Returns min(kv_len, budget) [B] int32."""
     B, dev = kv_len.shape[0], _here(cache)
     table, pages = _page_table(page_table, B, dev)
+    _count("budget", budget)
     if ws is None:
         ws = Workspace.for_kv_evict(B, cache.Hkv, pages * cache.page_size, budget, kv_len.device)
     if out is None:
@@ -554,7 +562,8 @@ def kv_evict(cache: KVCache, page_table, kv_len, budget: int, recent: int = 0, s
     _check("dflash2_kv_evict",
            (_lib or load_library()).dflash2_kv_evict(
                cache._ref, table, pages, _int32(B, "kv_len", kv_len, dev), _int32(B, "seq_len", seq_len, dev), B, budget,
-               recent, sink, _int32(B, "out", out, dev), *_scratch(ws, dev), _raw_stream(dev)))
+               _count("recent", recent), _count("sink", sink), _int32(B, "out", out, dev), *_scratch(ws, dev),
+               _raw_stream(dev)))
     return out
 
 

@@ -79,3 +79,21 @@ def test_tensors_of_another_device_are_refused(monkeypatch, name):
     with pytest.raises(ValueError):                          # the cache's device is not the current one
         call(**a)
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("name,number", [("paged_attn", "window"), ("kv_evict", "budget"), ("kv_evict", "recent"),
+                                         ("kv_evict", "sink")])
+def test_numbers_that_do_not_fit_are_refused(monkeypatch, name, number):
+    """2^32 + 5 is not 5."""
+    calls = []
+    monkeypatch.setattr(binding, "_lib", types.SimpleNamespace(**{"dflash2_" + name: lambda *a: calls.append(a) or 0}))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    call = getattr(binding, name)
+    for n in (2 ** 31 - 1, 5):
+        call(**{**arguments()[name], number: n})
+        assert n in calls[-1]
+    for n in (2 ** 32 + 5, 2 ** 32, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            call(**{**arguments()[name], number: n})
+    assert len(calls) == 2
