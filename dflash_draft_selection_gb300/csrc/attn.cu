@@ -457,7 +457,8 @@ extern "C" dflash2_status dflash2_paged_attn(const dflash2_kv_cache *cache, cons
         !al4(q_len) || !al4(seq_pos) || !al4(lse) || out == q)
         return DFLASH2_ERR_INVALID_ARG;
     const int group = Hq / cache->Hkv;
-    if (cache->d > 256 || group > 128 || cache->num_pages >= (int64_t(1) << 31) ||
+    // 128 rows of Hq heads are counted in 31 bits
+    if (cache->d > 256 || group > 128 || Hq >= (1 << 24) || cache->num_pages >= (int64_t(1) << 31) ||
         static_cast<int64_t>(max_pages) * cache->page_size >= (int64_t(1) << 31) - 256)
         return DFLASH2_ERR_UNSUPPORTED;
     // The places of a call's line are counted in 31 bits.  There are at most B Hkv T items, each of the tiles of cap

@@ -42,13 +42,15 @@ static bool make_map_4d(CUtensorMap *m, const void *ptr, const cuuint64_t (&dims
 }
 
 // Whether the tensor-core kernels take a bf16 call: copies of at least 8 keys
-// (one swizzle pattern) and strides that a tensor map can hold.
+// (one swizzle pattern), strides that a tensor map can hold, and a block's
+// outputs within 2^31 elements of its first row's.
 bool attn_tc_takes(const AttnArgs &a) {
     const int64_t lim = int64_t(1) << 38;
     return (a.d == 64 || a.d == 128 || a.d == 256) && a.page_size % 8 == 0 &&
            (a.Hkv == 1 || (a.head_stride > 0 && a.head_stride < lim)) &&
            (a.num_pages == 1 || (a.page_stride > 0 && a.page_stride < lim)) &&
-           a.slot_stride * a.page_size < lim / a.Hkv && static_cast<int64_t>(a.T) * a.Hq * a.d < lim;
+           a.slot_stride * a.page_size < lim / a.Hkv && static_cast<int64_t>(a.T) * a.Hq * a.d < lim &&
+           static_cast<int64_t>(a.T < TK ? a.T : TK) * a.Hq * a.d < (int64_t(1) << 31);
 }
 
 dflash2_status attn_tc_launch(AttnArgs a, bool weights, cudaStream_t s) {

@@ -503,7 +503,7 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  * Errors: the common ones; INVALID_ARG for NULL q, out or kv_len, out the same
  * as q, lse or the cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a positive multiple of
  * Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
- * small; UNSUPPORTED for d > 256, Hq / Hkv > 128, num_pages >= 2^31,
+ * small; UNSUPPORTED for d > 256, Hq / Hkv > 128, Hq >= 2^24, num_pages >= 2^31,
  * max_pages * page_size >= 2^31 - 256 or
  * B * Hkv * T * (max_pages * page_size / 32 + 5) >= 2^31.
  */

@@ -79,3 +79,9 @@ def test_queries_turned_in_place_have_to_be_contiguous():
     p, q = ctypes.c_void_p(65536), ctypes.c_void_p(131072)
     assert append(q=p, q_out=p, qs=512) == INVALID           # slices of a fused projection
     assert append(k=q, q_out=q) == append(v=q, q_out=q) == INVALID
+
+
+def test_more_heads_than_a_block_can_count_are_refused():
+    big = dict(Hkv=1 << 24, page_size=1)
+    assert attend(big, T=4, Hq=1 << 24, B=1, max_pages=1, ws_bytes=0) == UNSUPPORTED
+    assert attend(dict(big, Hkv=(1 << 24) - 1), T=4, Hq=(1 << 24) - 1, B=1, max_pages=1, ws_bytes=0) == WORKSPACE

@@ -108,3 +108,23 @@ def test_scores_far_apart(dtype, d, big):
                 sure += 1
                 assert ((out[b, t, h].double().cpu() - V[top.indices[0]]).abs() <= 1e-6 * V.abs().max()).all()
     assert sure > 30 and d2.device_error() == 0
+
+
+def test_a_block_of_more_outputs_than_31_bits():
+    """127 tokens of 67000 heads of 256: the last row of a block lies more than 2^31 elements behind its first."""
+    dev = cuda_or_skip()
+    T, H, d, n, step = 127, 67000, 256, 8, 4000
+    assert (T - 1) * H * d > 2 ** 31 - 1
+    g = torch.Generator(device=dev).manual_seed(0)
+    k, v = (torch.randn(1, H, n, d, generator=g, device=dev, dtype=BF) for _ in range(2))
+    q = torch.randn(1, T, H, d, generator=g, device=dev, dtype=BF)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    out, lse = d2.paged_attn(q, d2.KVCache(k, v), i32(0)[None], i32(n), causal=False)
+    for h in range(0, H, step):
+        x = torch.einsum("thd,hsd->ths", q[0, :, h:h + step].float(), k[0, h:h + step].float()) * d ** -0.5
+        want = torch.einsum("ths,hsd->thd", x.softmax(-1), v[0, h:h + step].float())
+        big = torch.einsum("ths,hsd->thd", x.softmax(-1), v[0, h:h + step].float().abs())
+        # p and the result rounded to bf16, and the fp32 rest
+        assert ((out[0, :, h:h + step].float() - want).abs() <= 2.0 ** -7 * big + 2.0 ** -12).all()
+        assert torch.allclose(lse[0, :, h:h + step], x.logsumexp(-1), rtol=2.0 ** -16, atol=2.0 ** -12)
+    assert d2.device_error() == 0
