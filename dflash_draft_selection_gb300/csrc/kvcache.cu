@@ -1066,7 +1066,8 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
         k_stride < cache->Hkv * d || v_stride < cache->Hkv * d || q_stride * e % 16 || k_stride * e % 16 ||
         v_stride * e % 16)
         return DFLASH2_ERR_INVALID_ARG;
-    if (d > 1024 || B * T >= (int64_t(1) << 31)) return DFLASH2_ERR_UNSUPPORTED;
+    const int64_t heads = static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(cache->Hkv);
+    if (d > 1024 || B * T >= (int64_t(1) << 31) || heads >= (int64_t(1) << 31)) return DFLASH2_ERR_UNSUPPORTED;
     // a token's queries would go where another's queries, or a key or value, are still to be read
     if ((q_out == q && q_stride != Hq * d && B * T > 1) || q_out == k || q_out == v) return DFLASH2_ERR_INVALID_ARG;
     AppendArgs a = {};
@@ -1108,11 +1109,12 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
     a.kv_len_out = kv_len_out;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int two = 32 / e;  // entries of two vectors
-    if (rot % two == 0 && d % two == 0 && d / two <= 32) {
+    // in vectors: places within a token are counted in 31 bits
+    if (rot % two == 0 && d % two == 0 && d / two <= 32 && heads * d < (int64_t(1) << 31)) {
         int lanes_log2 = 0;
         while ((1 << lanes_log2) * two < d) ++lanes_log2;
         const bool norm = q_norm || k_norm;
-        const int64_t token_bytes = (static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(cache->Hkv)) * d * e;
+        const int64_t token_bytes = heads * d * e;
         if ((norm || cache->dt == DFLASH2_BF16) && a.tokens >= static_cast<int64_t>(sm_count()) * STREAM_TOKENS &&
             token_bytes >= STREAM_LEAST && token_bytes <= STREAM_SMEM / 4 - 4096)
             return launch_append_stream(a, cache->dt, interleaved != 0, norm, lanes_log2, s);
@@ -1127,7 +1129,7 @@ extern "C" dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, con
             return launch_append_vec(a, cache->dt, interleaved != 0, norm, lanes_log2, per, vgrid, s);
         }
     }
-    const int64_t units = a.tokens * (Hq + 2 * cache->Hkv);
+    const int64_t units = a.tokens * heads;
     const int64_t blocks = (units + 7) / 8, most = static_cast<int64_t>(sm_count()) * 64;
     const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
     if (cache->dt == DFLASH2_BF16)

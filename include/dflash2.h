@@ -462,7 +462,7 @@ typedef struct {
  * same as k, v or a q of several tokens that is not contiguous; Hq < 1,
  * rot odd, < 2 or > d, axes < 1, n_pos < 1, strides below the width of a
  * token's heads or not multiples of 16 bytes; dt not F32 or BF16.
- * UNSUPPORTED for d > 1024 or B * T >= 2^31.
+ * UNSUPPORTED for d > 1024, B * T >= 2^31 or Hq + 2 Hkv >= 2^31.
  */
 dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t *page_table, int32_t max_pages,
                                    const int32_t *kv_len, const int32_t *q_len, const int32_t *seq_pos,

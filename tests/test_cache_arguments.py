@@ -85,3 +85,9 @@ def test_more_heads_than_a_block_can_count_are_refused():
     big = dict(Hkv=1 << 24, page_size=1)
     assert attend(big, T=4, Hq=1 << 24, B=1, max_pages=1, ws_bytes=0) == UNSUPPORTED
     assert attend(dict(big, Hkv=(1 << 24) - 1), T=4, Hq=(1 << 24) - 1, B=1, max_pages=1, ws_bytes=0) == WORKSPACE
+
+
+def test_appends_of_more_heads_than_31_bits_are_refused():
+    for Hq, Hkv in ((2 ** 31 - 1, 1), (2, 2 ** 30)):
+        assert append(dict(Hkv=Hkv, d=8, slot_stride=8), B=1, T=1, rot=8, Hq=Hq, qs=2 ** 40, ks=2 ** 40,
+                      vs=2 ** 40) == UNSUPPORTED

@@ -137,3 +137,34 @@ def test_queries_turned_in_place(dtype, B, T, Hq, Hkv, d, rot, interleaved):
         torch.cuda.synchronize()
         results.append([bits(out[0]), out[1]] + [bits(getattr(on["cache"], n)) for n in SIDES])
     assert all(torch.equal(y, z) for y, z in zip(*results))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_a_token_of_more_entries_than_31_bits(interleaved):
+    """2^24 + 9 query heads of 128: places within a token pass 2^31."""
+    dev = cuda_or_skip()
+    H, d, step = 2 ** 24 + 9, 128, 2 ** 21
+    cache = d2.KVCache.empty(2, 1, 16, d, positions=True, device=dev)
+    g = torch.Generator(device=dev).manual_seed(1)
+    q = torch.randn(1, 1, H, d, generator=g, device=dev, dtype=BF)
+    k, v = (torch.randn(1, 1, 1, d, generator=g, device=dev, dtype=BF) for _ in range(2))
+    angle = torch.arange(20, device=dev).double()[:, None] * 1e4 ** (-torch.arange(0, d, 2, device=dev).double() / d)
+    cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    out, n = d2.rope_append(q, k, v, cos_sin, i32(7).view(1, 1, 1), cache, i32(1, 0)[None], i32(3),
+                            interleaved=interleaved)
+    cs, sn = cos_sin[7].chunk(2)
+
+    def turn(x):
+        x = x.float()
+        a, b = (x[..., 0::2], x[..., 1::2]) if interleaved else x.chunk(2, -1)
+        y, z = a * cs - b * sn, b * cs + a * sn
+        return torch.stack([y, z], -1).flatten(-2) if interleaved else torch.cat([y, z], -1)
+
+    for h in range(0, H, step):
+        x = q[0, 0, h:h + step]
+        pair = x.float().abs().amax(-1, keepdim=True)
+        # the result rounded to bf16, and four fp32 roundings on entries no larger than the row's largest
+        assert ((out[0, 0, h:h + step].float() - turn(x)).abs() <= 2.0 ** -8 * turn(x).abs() + 2.0 ** -20 * pair).all()
+    assert n.tolist() == [4] and cache.pos[1, 0, 3].item() == 3 and torch.equal(cache.v[1, 0, 3], v[0, 0, 0])
+    assert ((cache.k[1, 0, 3].float() - turn(k[0, 0, 0])).abs() <= 2.0 ** -7 * k.float().abs().max()).all()
