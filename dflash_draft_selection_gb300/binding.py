@@ -527,7 +527,7 @@ def paged_attn(q, cache: KVCache, page_table, kv_len, scale: float | None = None
                window: int = 0, q_len=None, seq_pos=None, add_weights: bool = False, ws=None, out=None):
     """dflash2_paged_attn.  q [B, T, Hq, d] of the cache's type; kv_len [B] int32, the slots in use with the block's
     own among them; scale 1 / sqrt(d) unless given; add_weights adds every cached key's softmax weight to
-    cache.weight.  Returns (out [B, T, Hq, d], lse [B, T, Hq] f32)."""
+    cache.weight (of all the block's tokens, before a verify has rejected any).  Returns (out [B, T, Hq, d], lse [B, T, Hq] f32)."""
     B, T, Hq, d = shape = q.shape
     dt, dev = cache.dtype, _here(cache)
     if d != cache.d:

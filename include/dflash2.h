@@ -484,7 +484,8 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  * Over the slots it sees, with x_s = scale * <q, k_s>:
  *   lse = log sum_s exp(x_s),  p_s = exp(x_s - lse),  out = sum_s p_s v_s.
  * With DFLASH2_ATTN_WEIGHTS every cached key's `weight` grows by the sum of
- * its p_s over the block's tokens and the query heads that share it.
+ * its p_s over the block's tokens and the query heads that share it: all
+ * tokens t < q_len[b], also those that a verify rejects afterwards.
  * A row that sees nothing (or sees only x_s = -inf) gets out 0, lse -inf and
  * adds no weight; tokens t >= q_len[b] are such rows.  What lies in slots
  * that a row does not see (NaN and Inf too) does not touch it.
@@ -495,14 +496,19 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  *   table can hold.  q_len [B] or NULL (all T).  seq_pos [B]: the position
  *   of the block's first token, or NULL (kv_len - q_len).
  * Slots whose page id is out of range are seen by no row.
- * Scores, softmax statistics and sums are fp32.  The cache's length is split
- * over the GPU and the parts are joined in a fixed order: the same call gives
- * the same bits.
+ * Scores, softmax statistics and sums are fp32.  On the tensor cores (bf16, d
+ * 64, 128 or 256, pages of a multiple of 8 slots) exp(x_s - m), m near the
+ * row's maximum, is rounded to bf16 once where it multiplies the values, so
+ * out is within 2^-8 sum_s p_s |v_s| of the definition before its own rounding
+ * to bf16; the other kernels (f32, other d and pages) keep it in fp32.  A
+ * weight is added as exp(x_s - lse) with the fp32 lse, so it is off by a
+ * factor of up to 1 + 2^-23 |lse|.  The cache's length is split over the GPU
+ * and the parts are joined in a fixed order: the same call gives the same bits.
  * ws: dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, dt) bytes, the first
  *   4096 zero at the start and left zero.
  * Errors: the common ones; INVALID_ARG for NULL q, out or kv_len, out the same
- * as q, lse or the cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a positive multiple of
- * Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
+ * as q, lse or the cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a
+ * positive multiple of Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
  * small; UNSUPPORTED for d > 256, Hq / Hkv > 128, Hq >= 2^24, num_pages >= 2^31,
  * max_pages * page_size >= 2^31 - 256 or
  * B * Hkv * T * (max_pages * page_size / 32 + 5) >= 2^31.
