@@ -502,15 +502,15 @@ dflash2_status dflash2_rope_append(const dflash2_kv_cache *cache, const int32_t 
  * out is within 2^-8 sum_s p_s |v_s| of the definition before its own rounding
  * to bf16; the other kernels (f32, other d and pages) keep it in fp32.  A
  * weight is added as exp(x_s - lse) with the fp32 lse, so it is off by a
- * factor of up to 1 + 2^-23 |lse|.  The cache's length is split over the GPU
+ * factor of up to exp(2^-23 |lse|).  The cache's length is split over the GPU
  * and the parts are joined in a fixed order: the same call gives the same bits.
  * ws: dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, dt) bytes, the first
  *   4096 zero at the start and left zero.
  * Errors: the common ones; INVALID_ARG for NULL q, out or kv_len, out the same
  * as q, lse or the cache's weight NULL with DFLASH2_ATTN_WEIGHTS, Hq not a
- * positive multiple of Hkv, scale not finite, window < 0, unknown flags; WORKSPACE if ws is too
- * small; UNSUPPORTED for d > 256, Hq / Hkv > 128, Hq >= 2^24, num_pages >= 2^31,
- * max_pages * page_size >= 2^31 - 256 or
+ * positive multiple of Hkv, scale not finite, window < 0, unknown flags;
+ * WORKSPACE if ws is too small; UNSUPPORTED for d > 256, Hq / Hkv > 128,
+ * Hq >= 2^24, num_pages >= 2^31, max_pages * page_size >= 2^31 - 256 or
  * B * Hkv * T * (max_pages * page_size / 32 + 5) >= 2^31.
  */
 enum { DFLASH2_ATTN_CAUSAL = 1, DFLASH2_ATTN_WEIGHTS = 2 };
