@@ -100,7 +100,8 @@ def main():
     ap.add_argument("--steps", type=int, default=64)
     ap.add_argument("--budget", type=int, default=256)
     a = ap.parse_args()
-    server = Server(Model(), a.requests, a.budget)
+    # positions: a warm-up step and a.steps more take up to K + 1 = 8 tokens each
+    server = Server(Model(max_pos=max(4096, 8 * (a.steps + 1))), a.requests, a.budget)
     total = torch.zeros(a.requests, dtype=torch.int64, device="cuda")
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     server.step()
