@@ -78,8 +78,6 @@ struct TcShared {
     uint64_t p_full[2];   // P of tile n written (weights pass: its scores read)
     uint64_t pv_done[2];  // output product of tile n complete
     uint64_t q_full, q_empty, done;
-    uint64_t meet;        // the two softmax groups, where they add values by hand
-    uint32_t meets[8];    // how often each of their warps has come
     int row_at[128];  // index of the row in lse (times d: in out) from the item's first row's
     int scratch[TC_THREADS / 32 + 2];
     alignas(16) float neg_m[128];
@@ -92,7 +90,6 @@ struct TcShared {
     uint32_t bad[4];
     uint32_t tmem;
     int abort, acc_first, flag, q_filled;
-    int huge[2];  // a row of the group has a reference beyond M_HUGE
 };
 
 // A head dimension's slots and units, and a call's ring.
@@ -193,6 +190,20 @@ __device__ __forceinline__ bool soft_any(int half, bool p) {
         : "memory");
     return r != 0;
 }
+// ... over both groups.
+__device__ __forceinline__ bool both_any(bool p) {
+    __syncwarp();
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 3, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(p ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
 
 // ... with an L2 policy for the lines it reads.
 __device__ __forceinline__ void tma_load_4d_hint(void *sdst, const CUtensorMap *tmap, int x, int y, int z, int w,
@@ -221,24 +232,11 @@ __device__ __forceinline__ bool tc_wait(TcShared &sm, uint64_t *bar, uint32_t pa
     return mbar_try_wait(bar, parity) || tc_wait_long(sm, bar, parity, err);
 }
 
-// The softmax groups (a lane of each of the 8 warps arrives) meet where after a
-// time-out one of them may not come: a bounded wait, and one answer for a warp.
-// (A warp's count of the meetings lies in shared memory: it is rarely needed.)
-static __device__ __noinline__ bool both_meet(TcShared &sm, unsigned int *err) {
-    volatile uint32_t *const meets = &sm.meets[threadIdx.x >> 5];
-    const uint32_t m = *meets;
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-        *meets = m + 1;
-        mbar_arrive(&sm.meet);
-    }
-    return __all_sync(FULL, tc_wait(sm, &sm.meet, m & 1, err));
-}
-
-// Test hook: a copying warp waits for the hook's word; if that runs out the
-// kernel gives up as after any time-out.  One answer for the warp.
-__device__ __forceinline__ bool tc_hold(TcShared &sm, const AttnArgs &a) {
-    if (a.hold == nullptr) return true;
+// Test hook: warp `warp` waits for the hook's word; if that runs out it takes
+// no part in the work, as after any time-out.  (Asked before the roles begin:
+// within the copying warps' loops the question alone cost 1 to 2 us a call.)
+__device__ __forceinline__ bool tc_hold(TcShared &sm, const AttnArgs &a, int warp) {
+    if (a.hold == nullptr || static_cast<int>(threadIdx.x >> 5) != warp) return true;
     int seen = 1;
     if ((threadIdx.x & 31) == 0 && !hold_wait(a.hold, a.hold_cycles)) {
         atomicOr(a.err, ERR_WAIT_TIMEOUT);
@@ -445,8 +443,6 @@ __device__ __forceinline__ void tc_setup(TcShared &sm, unsigned char *sq, int qb
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.done, 1);
-        mbar_init(&sm.meet, 8);
-        for (int i = 0; i < 8; ++i) sm.meets[i] = 0;
         sm.abort = 0;
         sm.acc_first = 0;
         sm.q_filled = 0;
@@ -482,7 +478,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
     unsigned int *err = a.err;
     pdl_wait();
     const AttnPlan plan = attn_plan<TC_THREADS>(a, sm.scratch);
-    const bool work = plan.begin < plan.end;
+    const bool work = plan.begin < plan.end && tc_hold(sm, a, V_WARP);
     AttnWalk w;
     if (work) w.start(a, plan);
 
@@ -508,7 +504,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
         KRing kr;
         VRing vr;
         uint32_t n = 0;
-        bool ok = keys || tc_hold(sm, a);
+        bool ok = true;
         while (ok && w.next(a)) {
             const int h = w.item / a.row_blocks, nt = w.t1 - w.t0;
             BoxAt box;
@@ -602,8 +598,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     sm.row_at[row0 + key] = (row0 + key) / a.group * a.Hq + (row0 + key) % a.group;
             }
             if (tid == 0) sm.acc_first = 0;
-            if (key == 0) sm.huge[half] = 0;
-            bool huge = false;
             soft_sync(half);
             // With an array of positions a key's view takes two dependent loads: the page one tile further ahead than
             // the position.
@@ -638,6 +632,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
             };
             int page_now = slot_page(w.t0), page_next = slot_page(w.t0 + 1);
             int pos_now = slot_pos(w.t0, page_now);
+            bool huge = false;  // a row of the group has a reference beyond M_HUGE
             for (int i = 0; i < nt; ++i, ++n) {
                 const int t = w.t0 + i, ks = t * TK;
                 const int page_after = slot_page(t + 2), pos_next = slot_pos(t + 1, page_next);
@@ -707,14 +702,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                     }
                 };
                 bool slow = true;
-                if (i > 0 && !huge) {
+                if (i > 0) {
                     exponents(c2);
                     float xm = NEG_INF;
 #pragma unroll
                     for (int j = 0; j < NR; ++j) xm = fmaxf(xm, x[j]);
-                    slow = soft_any(half, xm > M_STEP || poison);
+                    slow = soft_any(half, xm > M_STEP || poison || huge);
                 }
-                bool any_poison = false;
                 if (slow) {
                     // the rows' maxima over the tile, new references, and what has been summed scaled to them
                     if (i > 0) tmem_ld<NR>(ts, reinterpret_cast<uint32_t *>(x));
@@ -728,6 +722,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         if ((lane & 3) == 0) sm.part[warp & 3][row0 + c + lane / 4] = v;
                     }
                     soft_sync(half);
+                    bool far = false;
                     if (key < NR) {
                         const int r = row0 + key;
                         const float mo = -neg_m[key];
@@ -735,10 +730,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         mn = fmaxf(mn, mo);
                         fac[key] = ex2(mo - mn);
                         neg_m[key] = -mn;
-                        if (mn != M_NONE && fabsf(mn) > M_HUGE) sm.huge[half] = 1;
+                        far = mn != M_NONE && fabsf(mn) > M_HUGE;
                     }
-                    any_poison = soft_any(half, poison);
-                    huge = *reinterpret_cast<volatile int *>(&sm.huge[half]) != 0;
+                    huge = soft_any(half, far);
                     if (huge) {  // the products rounded as the references are
 #pragma unroll
                         for (int j = 0; j < NR; ++j) x[j] *= c2;
@@ -782,10 +776,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                 for (int j = 0; j < NR; j += 8)
                     *reinterpret_cast<uint4 *>(pb + ((row0 + j) / 8) * (TK * 16) + key * 16) =
                         make_uint4(pk[j / 2], pk[j / 2 + 1], pk[j / 2 + 2], pk[j / 2 + 3]);
-                if (any_poison) {
-                    // Keys that some rows see and some do not, with values that are not finite: their products with p
-                    // go straight into O^T.  Both groups find the same keys and go through them together, unless a wait
-                    // has run out: then they may not, and whoever is left alone gives up.
+                // Keys that some rows see and some do not, with values that are not finite: their products with p go
+                // straight into O^T.  Both groups vote, in every tile that can hold such keys, and go through them
+                // together: whether they do hangs on nothing that a time-out leaves open to one of them alone.
+                if ((a.pos || t < clean0 || t >= clean1) && both_any(poison)) {
                     const int vseq = seq + i * D::UPT;
                     const unsigned mine = __ballot_sync(FULL, poison);
                     if (half == 0 && lane == 0) sm.bad[warp] = mine;
@@ -798,11 +792,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                         tmem_wait_st();
                         if (tid == 0) sm.acc_first = 1;
                     }
-                    bool together = both_meet(sm, err);
-                    for (int k = 0; together && k < TK; ++k) {
-                        // one word for the warp, whatever the other group does meanwhile
-                        const unsigned bad = __shfl_sync(FULL, reinterpret_cast<volatile uint32_t *>(sm.bad)[k >> 5], 0);
-                        if (!(bad >> (k & 31) & 1)) continue;
+                    both_sync();
+                    for (int k = 0; k < TK; ++k) {
+                        if (!(sm.bad[k >> 5] >> (k & 31) & 1)) continue;
                         if (tid == k) {
                             for (int e = 0; e < DS * 64; ++e) {
                                 const int q = vseq + e / 64 / D::US, chunk = (e % 64) / 8;
@@ -814,8 +806,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                                 if (b) *v = 0;
                             }
                         }
-                        together = both_meet(sm, err);
-                        if (!together) break;
+                        both_sync();
                         for (int m = 0; m < MB; ++m) {
                             const int e = DS > 1 ? m * 128 + key : key & 63;
                             const float v = __uint_as_float(static_cast<uint32_t>(sm.side[e]) << 16);
@@ -835,7 +826,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attn_tc(const __grid_constant
                             }
                         }
                         tmem_wait_st();
-                        together = both_meet(sm, err);
+                        both_sync();
                     }
                 }
                 fence_proxy_async_smem();
@@ -990,7 +981,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_weights_tc(const __grid_const
     unsigned int *err = a.err;
     pdl_wait();
     const AttnPlan plan = attn_plan<TC_THREADS>(a, sm.scratch);
-    const bool work = plan.begin < plan.end;
+    const bool work = plan.begin < plan.end && tc_hold(sm, a, K_WARP);
     AttnWalk w;
     if (work) w.start(a, plan);
 
@@ -1016,7 +1007,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_weights_tc(const __grid_const
         const int dpi = TK / a.page_size, doff = TK % a.page_size;
         const uint64_t pol = l2_policy_evict_first();
         KRing kr;
-        bool ok = tc_hold(sm, a);
+        bool ok = true;
         while (ok && w.next(a)) {
             for (int rb = 0; ok && rb < a.row_blocks; ++rb) {
                 BoxAt box;
