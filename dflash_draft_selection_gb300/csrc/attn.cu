@@ -96,8 +96,12 @@ static __host__ __device__ size_t attn_simt_smem(int d, int e) {
 // Bound: the fp32 units (rows * d * 4 operations per key) once more than a
 // few rows share a key, the bytes below that; short calls are bound by the
 // chain of lookups, copies and the join.  4 requests of 100 to 4096 slots, 32
-// rows on 4 heads of 64 (23 MB, 0.37 GFLOP): 34 us on 304 CTAs of 3.5 tiles,
+// rows on 4 heads of 64 (23 MB, 0.37 GFLOP): 35 us on 304 CTAs of 3.5 tiles,
 // about 20 of them the plan, the first copy and the join of 19 parts.
+// bf16 caches that the tensor-core kernels do not take: 32 requests of 8 to 8192
+// slots, 8 tokens, 40 heads on 8: d 80 789 us, d 96 924, d 192 1631, pages of 20
+// slots 1087 (d 128), 15 to 18 TFLOP/s, 15 to 17 times their bytes' time.  The
+// score step reads five vectors of shared memory for sixteen products.
 template <typename E>
 struct SimtTile {
     static constexpr int PAD = 16 / sizeof(E);  // elements between rows: the lanes' reads fall into different banks
@@ -309,7 +313,11 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_simt(AttnArgs a) {
 
 // weight_s += sum over the rows that see s of exp(x_s - lse): the second pass,
 // over the keys alone.  One CTA owns a (request, head)'s tile, so no two add
-// to the same word, and the rows are added in a fixed order.
+// to the same word, and the rows are added in a fixed order.  Bound: the loads of
+// the rows, again for each tile of 32 keys, and of the tile, with no copy ahead.  4
+// requests of 100 to 4096 slots, 8 tokens, 16 heads on 4 of 64, float32: 56 us
+// with the attention; 16 requests of 2048 to 4028 slots, a token of 32 heads on 8
+// of 96, bf16: 391 us with the attention.
 template <typename E>
 __global__ void __launch_bounds__(SIMT_THREADS) k_weights_simt(AttnArgs a) {
     extern __shared__ float smem[];

@@ -21,8 +21,9 @@
 // second, each thread one key: it reads the key's scores from tensor memory,
 // takes p = 2^(x - m) with the row's reference m, adds p to its own share of
 // the row sums (reduced over the threads only at the end of an item) and
-// writes P^T for the second product.  The halves share no row, so they never
-// wait for each other within a tile.
+// writes P^T for the second product.  The halves share no row, so within a tile
+// they wait for each other only where some rows see a key and some do not: there
+// they vote on whether its values are finite.
 // The reference m of a row is the maximum of the item's first tile and moves
 // only when a score exceeds it by more than 8 (p <= 256, so nothing
 // overflows, and the result is the same up to rounding): then the sums and
@@ -32,13 +33,19 @@
 // bandwidth for d = 128, and 900 to 1000 cycles of the tensor cores.
 // Measured (d 128 unless said, bytes of keys and values over the time):
 //   one token, 5 rows, 131071 slots x 8 heads         89 us, 6.0 TB/s
-//   32 requests of 1 to 16384 slots, 40 rows         181 us, 6.2 TB/s
-//   16 requests of 500 to 16384 slots, d 256, 96 rows 117 us, 4.8 TB/s
-//   64 requests, window 2048, 40 rows                 61 us, 4.0 TB/s
-// What is left is the change from item to item: the last product's drain, the
-// outputs, the join of cut items and the next item's first tile take 10000 to
-// 16000 cycles, during which only the ring fills.  With wide heads and 96 rows
-// the ring holds one tile, so copies also wait for products.
+//   32 requests of 1 to 16384 slots, 40 rows         182 us, 6.1 TB/s
+//   16 requests of 500 to 16384 slots, d 256, 96 rows 116 us, 4.9 TB/s
+//   64 requests, window 2048, 40 rows                 63 us, 4.0 TB/s
+//   32 requests of 8 to 8192 slots, 64 rows          102 us, 4.7 TB/s
+// What is left is the change from item to item, 10000 to 16000 cycles: the eight
+// softmax warps take the last product's drain, the outputs and the join of cut
+// items one after the other, and the next item's copies and first scores, which
+// run ahead, wait for them.  (Warps of their own for it would need registers:
+// 384 threads have 168 each.)  With wide heads and 96 rows the ring holds one
+// tile, so copies also wait for products.
+// Long blocks (prompts) are right but slow: every row block walks all slots that
+// some token of the block's request sees.  8192 tokens, 40 heads on 8: 5300 us for
+// 687 GFLOP of visible pairs.
 // Tried and slower: one ring for keys and values (256 us for the second case
 // with four times the copies per tile), a lane looping over a tile's copies
 // (340 us), cp.async (3 TB/s at best).

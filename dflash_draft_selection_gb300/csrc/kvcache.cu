@@ -95,6 +95,10 @@ __device__ __forceinline__ void st1(unsigned short *p, int64_t i, float v) {
 }
 
 // Any d and rot: one warp per (token, head), a pair of entries per step.
+// Bound: one entry per load and store, and the table's row read by every head.
+// 28 heads of 96, rot 24: 3.6 us a token; 512 tokens of 56 such heads 15.7 us
+// (11 MB), 16384 of 32 236 us (201 MB, 0.9 TB/s); 4096 tokens of 12 heads of 1024
+// 93 us (201 MB, 2.2 TB/s).
 template <typename E, bool INTER>
 __global__ void __launch_bounds__(256) k_append_any(AppendArgs a) {
     pdl_wait();
@@ -416,18 +420,19 @@ __global__ void __launch_bounds__(256) k_append_vec(AppendArgs a, int lanes_log2
 // Bound: the heads' bytes, once the turning keeps up: with 16 KB tokens its
 // chain of shared-memory reads, sums over lanes and stores takes a warp 1000
 // cycles a round, so several tokens are turned at once.  16384 tokens of 32
-// heads of 256, three axes, normalised (537 MB): 94.5 us, 5.7 TB/s, against
+// heads of 256, three axes, normalised (537 MB): 95.6 us, 5.6 TB/s, against
 // 155 us in k_append_vec; four teams of two warps 108 us, two of four 136, a
-// team for each slot 118 to 129.  float32 (1.07 GB): 169 us, 6.3 TB/s, against
-// 223; its six slots do better with two teams of four than of six (182 us).
+// team for each slot 118 to 129.  float32 (1.07 GB): 169 us, 6.4 TB/s, against
+// 222; its six slots do better with two teams of four than of six (182 us).
 constexpr int AS_SLOTS = 12, AS_TURN = 12;  // slots and turning warps at most
 constexpr int64_t STREAM_SMEM = 224 * 1024;
 constexpr long long AS_WAIT = 4000000000ll, AS_DRAIN = 400000000ll;  // cycles after which a wait gives up
 // Which calls: tokens of 7 KB and more, 24 and more of them per SM, else a
 // token's fixed costs and the ring's start weigh more than the smoother stream.
-// Measured, this against k_append_vec: 3040 tokens of 7 KB 9.7 against 9.1 us,
-// 4864 14.5 against 15.5, 1824 of 16 KB 16.0 against 16.1; 16384 of 4 KB 30.7
-// against 32.1 but 4864 of them 11.3 against 7.7; of 3 KB 25.5 against 16.0.
+// Measured, this against k_append_vec: 3040 tokens of 7 KB 10.2 against 9.1 us,
+// 4864 14.7 against 15.2, 16384 44.8 against 52.3; 1824 of 16 KB 16.2 against
+// 15.9, 3648 26.2 against 37.0; 16384 of 4 KB 31.9 against 32.4 but 4864 of them
+// 11.3 against 7.8; 512 of 14 KB 7.5 against 5.3.
 // float32 without a norm has little to compute and stays with k_append_vec:
 // 16384 tokens of 28 KB 156 against 139 us.
 constexpr int STREAM_TOKENS = 24, STREAM_LEAST = 7 * 1024;
@@ -791,7 +796,9 @@ __device__ __forceinline__ void evict_moves(const EvictArgs &a, int64_t b, int h
 // fit it, 50000 of them), so weights and positions are read once; otherwise
 // every pass makes them again.  Bound: the latency of the passes and their
 // barriers (8 heads of 32 requests with up to 8192 slots: 35 us for 16 MB;
-// 2112 slots: 15 us).  Adding once per digit and warp (match) was slower, 43 us.
+// 2112 slots: 15 us).  Longer tables read weights, positions and pages in all
+// seven passes: 4 requests of 8 heads from 65536 to 32768 slots 615 us with the
+// moves (554 MB, 83 us).  Adding once per digit and warp (match) was slower, 43 us.
 constexpr int EV_KEYS = 50000;
 // Moves per head up to which the selecting CTA makes them itself.  GPU time of one launch and of two, in us: 64 moves,
 // 128 heads 14.9 and 15.5, 16 heads 14.4 and 15.3; 256 moves 19.7 and 19.9, 18.9 and 16.5; 1024 moves 48.5 and 38.8,
