@@ -26,11 +26,11 @@
  *     zero-filled once before first use.  A call needs zeros only where it
  *     counts (its tickets and marks) and leaves zeros there; behind them it
  *     leaves its scratch.  So a workspace is for calls of one kind: the scans
- *     (dflash2_topk16, _shard, dflash2_verify) keep one workspace per entry
- *     point and set of sizes (rows, or B and K), and dflash2_paged_attn and
- *     dflash2_kv_evict may share one, for calls of any sizes that it is large
- *     enough for.  Zero-fill a workspace before it goes to another kind of
- *     call.  After a call that returned DFLASH2_ERR_CUDA, or after
+ *     and the fused LM head (dflash2_topk16, _shard, dflash2_verify,
+ *     dflash2_lmhead_topk16) keep one workspace per entry point and set of
+ *     sizes (rows, V, or B and K), and dflash2_paged_attn and dflash2_kv_evict
+ *     may share one, for calls of any sizes that it is large enough for.
+ *     Zero-fill a workspace before it goes to another kind of call.  After a call that returned DFLASH2_ERR_CUDA, or after
  *     dflash2_device_error reported a nonzero code (a kernel gave up on a
  *     bounded wait), zero-fill the workspaces of the calls involved again
  *     before reusing them.  Two calls that share a workspace must not run
@@ -560,8 +560,10 @@ const char *dflash2_status_string(dflash2_status s);
 /*
  * Error word of the library's kernels on the current device: nonzero after a
  * kernel gave up on a bounded wait (it then wrote -1 / NaN outputs instead of
- * hanging, dflash2_rope_append NaN to the cached keys and values too; the word then holds DFLASH2_DEVERR_WAIT_TIMEOUT).  Synchronises
- * the device.  clear != 0 resets the word.
+ * hanging, dflash2_rope_append NaN to the cached keys and values and
+ * dflash2_paged_attn to the weights too; the word then holds
+ * DFLASH2_DEVERR_WAIT_TIMEOUT).  Synchronises the device.  clear != 0 resets
+ * the word.
  */
 #define DFLASH2_DEVERR_WAIT_TIMEOUT 1u
 dflash2_status dflash2_device_error(uint32_t *code, int clear);
@@ -579,8 +581,8 @@ dflash2_status dflash2_device_error(uint32_t *code, int clear);
  * holds for the warps of dflash2_paged_attn's tensor-core kernels that copy
  * the values (with DFLASH2_ATTN_WEIGHTS, the keys of the weights' pass
  * instead) and of dflash2_rope_append's kernel for long blocks: they give up
- * as after any time-out.  flag NULL switches the hook off.  Kernels already launched or captured keep the
- * setting they were launched with.
+ * as after any time-out.  flag NULL switches the hook off.  Kernels already
+ * launched or captured keep the setting they were launched with.
  * Errors: INVALID_ARG for a misaligned flag or max_cycles out of range.
  */
 dflash2_status dflash2_test_hold(const uint32_t *flag, int64_t max_cycles);

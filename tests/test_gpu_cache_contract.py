@@ -168,3 +168,27 @@ def test_a_token_of_more_entries_than_31_bits(interleaved):
         assert ((out[0, 0, h:h + step].float() - turn(x)).abs() <= 2.0 ** -8 * turn(x).abs() + 2.0 ** -20 * pair).all()
     assert n.tolist() == [4] and cache.pos[1, 0, 3].item() == 3 and torch.equal(cache.v[1, 0, 3], v[0, 0, 0])
     assert ((cache.k[1, 0, 3].float() - turn(k[0, 0, 0])).abs() <= 2.0 ** -7 * k.float().abs().max()).all()
+
+
+def test_one_buffer_for_calls_of_every_kind():
+    """Zero-filled before it goes to another kind of call, a workspace serves them all."""
+    dev = cuda_or_skip()
+    g = torch.Generator(device=dev).manual_seed(3)
+    z = torch.randn(3, 262144, generator=g, device=dev).bfloat16()       # rows split over the GPU
+    a = Case(4, [3000, 900, 4000], 4, 10, 2, 128, 16)
+    c = Case(3, [1500, 900, 1203], 1, 4, 4, 64, 16, held=True)
+    qa, on_a = a.q.to(dev), a.on(dev)
+    seq = torch.tensor([s + 1 for s in c.seq_pos], dtype=torch.int32, device=dev)
+    one = d2.Workspace(64 << 20, dev)
+    want, got = [], []
+    for results, ws in ((want, lambda: None), (got, lambda: one)):
+        for _ in range(2):
+            results += d2.topk16(z, ws=ws())
+            one.buf.zero_()
+            results += d2.paged_attn(qa, ws=ws(), **on_a)
+            on = c.on(dev)
+            d2.kv_evict(on["cache"], on["page_table"], on["kv_len"], 700, 3, 1, seq_len=seq, ws=ws())
+            results += [bits(getattr(on["cache"], x)) for x in SIDES]
+            one.buf.zero_()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and d2.device_error() == 0
