@@ -196,11 +196,13 @@ def _grouped(x, group, fill):
 def _plain_quant(s):
     c = s["case"]
     w = _grouped(s["w"].float(), c["group"], 0.0)
+    top = w.abs().amax(2)
+    steps = torch.full_like(top, 15.0 if c["zero"] else 7.0)    # a tensor: a scalar is multiplied by its reciprocal
     if c["zero"]:
         lo, hi = w.amin(2).clamp(max=0.0), w.amax(2).clamp(min=0.0)
-        scale = (hi / 15 - lo / 15).bfloat16()
+        scale = (hi / steps - lo / steps).bfloat16()
     else:
-        scale = (w.abs().amax(2) / 7).bfloat16()
+        scale = (top / steps).bfloat16()
     step = torch.where(scale == 0, 1.0, scale.float())
     zero = torch.round(-lo / step).clamp(0, 15) if c["zero"] else torch.full_like(step, 8.0)
     code = (torch.round(w / step[..., None]) + zero[..., None]).clamp(0, 15)
