@@ -8,17 +8,22 @@ the first call loads the library and raises if it is missing.
 from .binding import (  # noqa: F401
     DFlash2Error,
     KVCache,
+    Weight4,
     Workspace,
     conv2tap,
     ctx_gate,
+    dequant4,
     device_error,
     dynconv2tap,
     kv_evict,
+    linear4,
     lmhead_topk16,
     load_library,
     pair_score_walk,
     paged_attn,
+    quant4,
     rope_append,
+    sample,
     sampling_params,
     test_hold,
     topk16,

@@ -42,6 +42,13 @@ class _CacheRecord(ctypes.Structure):
                 ("d", ctypes.c_int32), ("dt", ctypes.c_int32)]
 
 
+class _Weight4Record(ctypes.Structure):
+    """dflash2_weight4."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("code_stride", ctypes.c_int64),
+                ("side_stride", ctypes.c_int64), ("group", ctypes.c_int32), ("side_dt", ctypes.c_int32)]
+
+
 class DFlash2Error(RuntimeError):
     def __init__(self, fn: str, code: int):
         self.code = code
@@ -86,6 +93,10 @@ def load_library():
         L.dflash2_kv_evict_workspace_bytes.argtypes = [i64, i32, i64, i32]
         L.dflash2_kv_evict_workspace_bytes.restype = sz
         L.dflash2_kv_evict.argtypes = [vp, vp, i32, vp, vp, i64, i32, i32, i32, vp, vp, sz, vp]
+        L.dflash2_quant4.argtypes = [vp, i32, i64, vp, vp]
+        L.dflash2_dequant4.argtypes = [vp, vp, i32, i64, vp]
+        L.dflash2_linear4.argtypes = [vp, i32, i64, i64, vp, vp, i32, i64, vp]
+        L.dflash2_sample.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp]
         L.dflash2_status_string.argtypes = [i32]
         L.dflash2_status_string.restype = ctypes.c_char_p
         L.dflash2_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
@@ -94,7 +105,8 @@ def load_library():
                    "dflash2_lmhead_topk16",
                    "dflash2_ctx_gate", "dflash2_pair_score_walk",
                    "dflash2_verify", "dflash2_conv2tap", "dflash2_dynconv2tap", "dflash2_device_error",
-                   "dflash2_test_hold", "dflash2_rope_append", "dflash2_paged_attn", "dflash2_kv_evict"):
+                   "dflash2_test_hold", "dflash2_rope_append", "dflash2_paged_attn", "dflash2_kv_evict",
+                   "dflash2_quant4", "dflash2_dequant4", "dflash2_linear4", "dflash2_sample"):
             getattr(L, fn).restype = i32
         _lib = L
         return _lib
@@ -132,11 +144,11 @@ def _dtype_code(dt: torch.dtype) -> int:
     raise TypeError(f"unsupported dtype {dt}")
 
 
-def _here(cache) -> int:
-    """The index of a cache's device, which has to be the current one: a call launches there."""
+def _here(cache, what: str = "cache") -> int:
+    """The index of a cache's (or weights') device, which has to be the current one: a call launches there."""
     dev = cache._dev
     if torch._C._cuda_getDevice() != dev:
-        raise ValueError(f"the cache lies on cuda:{dev}, which is not the current device")
+        raise ValueError(f"the {what} lies on cuda:{dev}, which is not the current device")
     return dev
 
 
@@ -167,12 +179,12 @@ def _heads(name: str, t: torch.Tensor, dt, B: int, T: int, H: int, d: int, dev: 
     return t.data_ptr(), s1 if T > 1 else (s0 if B > 1 else H * d)
 
 
-def _dense(name: str, t, dt, shape, dev: int):
+def _dense(name: str, t, dt, shape, dev: int, owner: str = "cache"):
     """Address of a contiguous tensor of a type and shape on GPU `dev` (None passes)."""
     if t is None:
         return None
     if t.dtype is not dt or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name}: contiguous {dt} {list(shape)} on the cache's GPU")
+        raise ValueError(f"{name}: contiguous {dt} {list(shape)} on the {owner}'s GPU")
     return t.data_ptr()
 
 
@@ -294,6 +306,48 @@ class KVCache:
         side = (num_pages, Hkv, page_size)
         return KVCache(kv[0], kv[1], torch.zeros(side, device=device) if weights else None,
                        torch.zeros(side, dtype=torch.int32, device=device) if positions else None)
+
+
+class Weight4:
+    """A matrix [N, K] held in 4 bits: codes uint8 [N, bytes] (two to a byte, the even column in the low half; bytes a
+    multiple of 16 that covers K), scale [N, groups] (bf16 or f32) and the optional zero points of the same type (8
+    without).  Rows may lie apart, rows themselves are contiguous, so slices of rows are taken as they are.  Holds
+    views, copies nothing.  A call takes tensors of the codes' device, which has to be the current one."""
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = None,
+                 K: int | None = None, group: int = 128):
+        _need_cuda(codes, scale, zero)
+        if codes.dim() != 2 or codes.dtype is not torch.uint8 or (codes.stride(1) != 1 and codes.shape[1] > 1):
+            raise ValueError("codes: uint8 [N, bytes] with contiguous rows")
+        N = codes.shape[0]
+        K = 2 * codes.shape[1] if K is None else K
+        if group not in (32, 64, 128) or K < 1:
+            raise ValueError("groups of 32, 64 or 128 and at least one column")
+        if codes.shape[1] < -(-K // 32) * 16:
+            raise ValueError(f"codes: {K} columns take {-(-K // 32) * 16} bytes a row")
+        G = -(-K // group)
+        _dtype(scale)
+        for name, t in (("scale", scale), ("zero", zero)):
+            if t is not None and (t.dtype is not scale.dtype or t.shape != (N, G) or t.device != codes.device or
+                                  (t.stride(1) != 1 and G > 1)):
+                raise ValueError(f"{name}: {scale.dtype} [{N}, {G}] with contiguous rows, beside the codes")
+        if zero is not None and N > 1 and zero.stride(0) != scale.stride(0):
+            raise ValueError("scale and zero: one distance from row to row")
+        self.codes, self.scale, self.zero = codes, scale, zero
+        self.N, self.K, self.group = N, K, group
+        self.device, self._dev = codes.device, codes.get_device()
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._rec = _Weight4Record(ptr(codes), ptr(scale), ptr(zero), N, K,
+                                   codes.stride(0) if N > 1 else -(-codes.shape[1] // 16) * 16,
+                                   scale.stride(0) if N > 1 else G, group, _dtype(scale))
+        self._ref = ctypes.byref(self._rec)
+
+    @staticmethod
+    def empty(N: int, K: int, group: int = 128, zero: bool = False, dtype=torch.bfloat16, device="cuda") -> "Weight4":
+        """Uninitialised codes, scales and (with zero) zero points."""
+        side = lambda: torch.empty(N, -(-K // group), dtype=dtype, device=device)  # noqa: E731
+        return Weight4(torch.empty(N, -(-K // 32) * 16, dtype=torch.uint8, device=device), side(),
+                       side() if zero else None, K, group)
 
 
 # ------------------------------------------------------------------ calls ----
@@ -563,6 +617,89 @@ def kv_evict(cache: KVCache, page_table, kv_len, budget: int, recent: int = 0, s
            (_lib or load_library()).dflash2_kv_evict(
                cache._ref, table, pages, _int32(B, "kv_len", kv_len, dev), _int32(B, "seq_len", seq_len, dev), B, budget,
                _count("recent", recent), _count("sink", sink), _int32(B, "out", out, dev), *_scratch(ws, dev),
+               _raw_stream(dev)))
+    return out
+
+
+def _rows(name: str, t, shape, dev: int):
+    """Address and row stride of a matrix with contiguous rows on GPU `dev`."""
+    if t.dim() != 2 or tuple(t.shape) != shape or t.get_device() != dev or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: [{shape[0]}, {shape[1]}] with contiguous rows on the weights' GPU")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+
+
+def quant4(W: torch.Tensor, group: int = 128, zero: bool = False, dtype=torch.bfloat16, out=None) -> Weight4:
+    """dflash2_quant4.  W [N, K] (bf16/f32, contiguous rows).  Returns its Weight4 (scales of `dtype`), or fills
+    `out`."""
+    L = load_library()
+    _need_cuda(W)
+    if W.dim() != 2:
+        raise ValueError("W: [N, K]")
+    if out is None:
+        out = Weight4.empty(W.shape[0], W.shape[1], group, zero, dtype, W.device)
+    dev = _here(out, "weights")
+    p, ld = _rows("W", W, (out.N, out.K), dev)
+    _check("dflash2_quant4", L.dflash2_quant4(p, _dtype(W), ld, out._ref, _raw_stream(dev)))
+    return out
+
+
+def dequant4(w: Weight4, dtype=torch.bfloat16, out=None) -> torch.Tensor:
+    """dflash2_dequant4.  Returns [N, K] of `dtype`, or fills `out` (contiguous rows)."""
+    L = load_library()
+    dev = _here(w, "weights")
+    if out is None:
+        out = torch.empty(w.N, w.K, dtype=dtype, device=w.device)
+    p, ld = _rows("out", out, (w.N, w.K), dev)
+    _check("dflash2_dequant4", L.dflash2_dequant4(w._ref, p, _dtype(out), ld, _raw_stream(dev)))
+    return out
+
+
+def linear4(x: torch.Tensor, w: Weight4, dtype=None, out=None) -> torch.Tensor:
+    """dflash2_linear4.  x [rows, K] (bf16/f32, contiguous rows).  Returns x . W^T [rows, N] of x's type or float32, or
+    fills `out` (contiguous rows, any distance from row to row)."""
+    dev = _here(w, "weights")
+    rows = x.shape[0]
+    xp, xs = _rows("x", x, (rows, w.K), dev)
+    if out is None:
+        out = torch.empty((rows, w.N), dtype=x.dtype if dtype is None else dtype, device=x.device)
+    yp, ys = _rows("out", out, (rows, w.N), dev)
+    _check("dflash2_linear4", (_lib or load_library()).dflash2_linear4(xp, _dtype(x), rows, xs, w._ref, yp, _dtype(out),
+                                                                       ys, _raw_stream(dev)))
+    return out
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, params=None, min_p=None, rows_per_param: int = 1,
+           V: int | None = None, out=None):
+    """dflash2_sample.  logits [rows, ld] (bf16/f32), u [rows] f32 uniforms, min_p [n] f32 for the n = ceil(rows /
+    rows_per_param) entries of params (or alone: greedy).  Returns (token [rows] int32, prob [rows] f32)."""
+    _need_cuda(logits, u, min_p)
+    rows, dev = logits.shape[0], logits.get_device()
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"the logits lie on cuda:{dev}, which is not the current device")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits: [rows, ld] with contiguous rows")
+    _count("rows_per_param", rows_per_param)
+    n = -(-rows // max(rows_per_param, 1))
+    p = _params_from(params, logits.device)
+    if p is not None and (p.get_device() != dev or not p.is_contiguous() or
+                          p.numel() * p.element_size() < 12 * n):
+        raise ValueError(f"params: {n} records on the logits' GPU")
+    if out is None:
+        out = (torch.empty(rows, dtype=torch.int32, device=logits.device),
+               torch.empty(rows, dtype=torch.float32, device=logits.device))
+    token, prob = out
+    ld = logits.stride(0)
+    if rows <= 1:                                        # a single row's stride says nothing
+        ld = -(-logits.shape[1] * logits.element_size() // 16) * 16 // logits.element_size()
+    V = logits.shape[1] if V is None else V
+    if V > logits.shape[1]:
+        raise ValueError("V: more entries than a row has")
+    f32 = torch.float32
+    _check("dflash2_sample",
+           (_lib or load_library()).dflash2_sample(
+               logits.data_ptr(), _dtype(logits), rows, V, ld, None if p is None else p.data_ptr(),
+               _dense("min_p", min_p, f32, (n,), dev, "logits"), rows_per_param, _dense("u", u, f32, (rows,), dev, "logits"),
+               _dense("out", token, torch.int32, (rows,), dev, "logits"), _dense("out", prob, f32, (rows,), dev, "logits"),
                _raw_stream(dev)))
     return out
 

@@ -558,6 +558,108 @@ dflash2_status dflash2_kv_evict(const dflash2_kv_cache *cache, const int32_t *pa
 const char *dflash2_status_string(dflash2_status s);
 
 /*
+ * Weights held in 4 bits -- [R] and [F] run this path for targets and drafters
+ * with 4-bit weights; the pages give no kernel.  An addition of this library.
+ *
+ * A record stands for a matrix W [N, K].  Each row is cut into groups of
+ * `group` neighbours (the last one may be short), and
+ *   W[n, k] = (code[n, k] - zero[n, k / group]) * scale[n, k / group].
+ * codes  [N, code_stride] bytes, two codes of 0..15 to a byte, the even k in
+ *        the low half.  code_stride is a multiple of 16 and at least
+ *        16 * ceil(K / 32); what the codes behind K hold does not matter.
+ * scale  [N, side_stride] of side_dt, side_stride >= ceil(K / group).
+ * zero   the same as scale, or NULL: 8 everywhere.
+ * Rows may lie further apart than they are long, so that some rows, or some
+ * columns from a multiple of `group` and 32 on, of a larger matrix are a
+ * record too.  The record is read on the host by each call; it holds device
+ * pointers (codes 16-byte aligned, scale and zero aligned to their type).
+ */
+typedef struct {
+    void *codes;
+    void *scale;
+    void *zero;
+    int64_t N;
+    int64_t K;
+    int64_t code_stride;
+    int64_t side_stride;
+    int32_t group; /* 32, 64 or 128 */
+    dflash2_dtype side_dt;
+} dflash2_weight4;
+
+/*
+ * dflash2_quant4 -- codes, scales and (where the record has room for them)
+ * zero points of W [N, ld] (dt; row stride ld elements), nearest codes.  In
+ * f32, every step rounded to nearest even:
+ *   without zero points  scale = max|w| / 7;  code = w / scale + 8
+ *   with zero points     scale = max(w, 0) / 15 - min(w, 0) / 15;
+ *                        zero = -min(w, 0) / scale;  code = w / scale + zero
+ * with scale rounded to side_dt before it divides, the quotients rounded to
+ * whole numbers, zero and code held within 0..15, and a scale of 0 dividing as 1.  A group
+ * with a NaN or an infinity gets scale NaN (codes and zero 8).  The codes
+ * behind K, up to a multiple of 32, are 8.
+ *
+ * dflash2_dequant4 -- out [N, ld] (dt): what the record stands for, in f32
+ * and rounded once.
+ *
+ * Errors: INVALID_ARG for a NULL or misaligned pointer (W and out: aligned to
+ * their type), N < 0 or above 2^31 - 1, K < 1 or above 2^31 - 129, a group other than 32, 64, 128,
+ * strides that are too small or (code_stride) no multiple of 16, ld < K;
+ * UNSUPPORTED for matrices of more than 2^36 entries.
+ */
+dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w,
+                              dflash2_stream stream);
+dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dtype dt, int64_t ld,
+                                dflash2_stream stream);
+
+/*
+ * dflash2_linear4 -- y = x . W^T with 4-bit weights: the LM head or a
+ * projection of one decoded token, of a verify block, or of many.
+ *
+ * x [rows, x_stride] (dt), the first K entries of a row count.
+ * y [rows, y_stride] (y_dt): the first N entries of a row are written.
+ *   y_dt is dt, or f32.  A row of x that holds a NaN or an infinity gives a
+ *   row of NaN.
+ * Errors: INVALID_ARG for a NULL or misaligned pointer (x and y: aligned to
+ * their type), rows < 0, x_stride < K, y_stride < N, f32 x with bf16 y, or a
+ * record that dflash2_dequant4 refuses.
+ */
+dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
+                               const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride,
+                               dflash2_stream stream);
+
+/*
+ * dflash2_sample -- one token per row of logits from a given uniform: what a
+ * request decodes without a draft (its first token, or every token when it
+ * runs without a drafter).  [F] Speed gives the filters' values; min_p and
+ * this entry point are additions of this library.
+ *
+ * logits [rows, ld] of dt as for dflash2_topk16 (V >= 1).
+ * params [ceil(rows / rows_per_param)] or NULL (all greedy), min_p the same
+ *   or NULL (0, off); row r uses entry r / rows_per_param.
+ * u      [rows] f32 uniforms in [0, 1).
+ * Tokens are ranked by logit, ties by the lower id, with the masses
+ * w = exp((z - max) / T).  top_k keeps the first top_k; top_p the shortest
+ * prefix of those whose mass reaches top_p of theirs; min_p those with w >=
+ * min_p (the best one's w is 1).  The row draws the first kept token, in
+ * rank order, whose running mass exceeds u times the kept mass, else the
+ * last one with any mass.  Greedy rows take the first token.
+ * token [rows] int32; prob [rows] f32: the drawn token's share of the kept
+ *   mass (1 for greedy rows).
+ * Masses are summed as whole numbers of 2^-45 (of 2^-(63 - ceil(log2 V)) for V
+ *   above 2^18), so a row's token depends neither on the other rows nor on
+ *   how the row is split.
+ * A row with a NaN or +Inf, nothing above -Inf, a NaN uniform or invalid
+ * parameters (as DFLASH2_ST_BAD_PARAMS; min_p outside [0, 1]) gets token -1 and
+ * prob NaN.
+ * Errors: INVALID_ARG for a NULL or misaligned pointer (logits: 16 bytes; the
+ * others: 4), rows < 0, V < 1 or V >= 2^31, ld < V, ld * elem size not a
+ * multiple of 16, rows_per_param < 1.
+ */
+dflash2_status dflash2_sample(const void *logits, dflash2_dtype dt, int64_t rows, int64_t V, int64_t ld,
+                              const dflash2_sampling *params, const float *min_p, int64_t rows_per_param,
+                              const float *u, int32_t *token, float *prob, dflash2_stream stream);
+
+/*
  * Error word of the library's kernels on the current device: nonzero after a
  * kernel gave up on a bounded wait (it then wrote -1 / NaN outputs instead of
  * hanging, dflash2_rope_append NaN to the cached keys and values and
