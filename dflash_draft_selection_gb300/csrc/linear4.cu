@@ -4,6 +4,7 @@
 // TensorRT-LLM issue 18085 and FreeToken PR 857 run this path for targets and
 // drafters whose weights are held in 4 bits; the pages name the formats and give
 // no kernel.
+#include "tc.cuh"
 #include "weight4.cuh"
 
 namespace dfl {
@@ -79,31 +80,418 @@ __global__ void __launch_bounds__(256) k_dequant4(dflash2_weight4 w, void *out, 
     else static_cast<uint16_t *>(out)[n * ld + k] = bf16_bits(v);
 }
 
-// One warp per weight row and 8 rows of x.
-__global__ void __launch_bounds__(256) k_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
-                                                 dflash2_weight4 w, void *y, dflash2_dtype y_dt, int64_t y_stride) {
-    const int lane = threadIdx.x & 31;
-    const int64_t n = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (n >= w.N) return;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 8;
-    float acc[8] = {};
-    for (int64_t k = lane; k < w.K; k += 32) {
-        const float v = weight_at(w, n, k);
+// ---------------------------------------------------------- few rows: mma ----
+// y = x . W^T for a few rows of x, bound by reading the codes once.
+//
+// A warp takes tiles of 16 weight rows in blocks of 128 columns (1 KB of codes
+// by cp.async, L4_STAGES blocks ahead) and multiplies them with up to 32 rows
+// of x by mma.sync m16n8k16 (x on the n side, 8 rows a tile): the codes go from
+// shared memory into the operand's registers with no second trip.
+//
+//   Codes are operands as they lie.  A bf16 whose exponent field is 0 or 1 is
+//   its low 8 bits times 2^-133 (subnormal, then the first normal binade), so
+//   w & 0x000f000f is a pair of codes times 2^-133 and w & 0x00f000f0 another
+//   pair times 2^-129: five instructions for eight codes.  The rows of x are
+//   scaled by a power of two (largest entry near 2^126) and, at the second
+//   pairs' columns, by 2^-4; both are exact, and are taken back with the scale.
+//   A group of columns is summed from zero, so that
+//     acc += scale * 2^e * (sum of code * x - zero * sum of x)
+//   in f32: products of a code and a bf16 are exact.  f32 rows are split into
+//   three bf16 parts, which is exact too.
+//
+// The CTA's range of x stays in shared memory for all its tiles.  Few tiles are
+// cut along K: over the warps of a CTA (kw), then over a cluster (ks CTAs, read
+// back through distributed shared memory); parts are added in order.
+constexpr int L4_THREADS = 256;
+constexpr int L4_WARPS = L4_THREADS / 32;
+constexpr int L4_STAGES = 4;
+constexpr int L4_BLOCK = 128;  // columns of a block: 64 bytes of a row
+constexpr int L4_SMEM_MAX = 226 * 1024;
+constexpr int L4_SMEM_GOOD = 112 * 1024;  // two CTAs to an SM
+constexpr int L4_WARP_TARGET = 16;        // warps of an SM that have a tile before tiles are shared no further
+constexpr int L4_PER_SM = 2;              // CTAs of an SM that share the tiles
+
+struct Lin4 {
+    const void *x;
+    int64_t rows, x_stride;
+    dflash2_weight4 w;
+    void *y;
+    int64_t y_stride;
+    dflash2_dtype y_dt;
+    int G;          // groups in a row
+    int gpb_log2;   // log2 of the groups in a block
+    int rb;         // rows of x to a CTA
+    int kblocks;    // blocks in a row
+    int kper;       // blocks of the largest range of a CTA
+    int kw_log2;    // log2 of the warps that share a tile
+    int ks;         // CTAs that share a tile
+    int64_t tiles;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126..127
+// v * 2^e for e in -252..254
+__device__ __forceinline__ float scale2(float v, int e) { return v * pow2f(e / 2) * pow2f(e - e / 2); }
+
+// Eight neighbours of a row of x, entries from `end` on zero.
+template <bool F32X>
+__device__ __forceinline__ void load8(const void *x, int64_t at, int left, bool vec, float (&v)[8]) {
+    if (left >= 8 && vec) {
+        if (F32X) {
+            const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at);
+            const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at + 4);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at);
+            const uint32_t q[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r0 + r < rows) {
-                const float a = load_f(x, dt, (r0 + r) * x_stride + k);
-                acc[r] = fmaf(isfinite(a) ? a : NAN, v, acc[r]);
-            }
+            for (int i = 0; i < 4; ++i) v[2 * i] = bf16lo(q[i]), v[2 * i + 1] = bf16hi(q[i]);
+        }
+        return;
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const float v = warp_sum(acc[r]);
-        if (lane == 0 && r0 + r < rows) {
-            if (y_dt == DFLASH2_F32) static_cast<float *>(y)[(r0 + r) * y_stride + n] = v;
-            else static_cast<uint16_t *>(y)[(r0 + r) * y_stride + n] = bf16_bits(v);
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? load_f(x, F32X ? DFLASH2_F32 : DFLASH2_BF16, at + i) : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Floats of the cross-warp sums: [row of x][16 + 1] per warp.
+__host__ __device__ constexpr int l4_red(int nt) { return nt * 8 * 17; }
+
+template <int NT, bool F32X>
+__global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
+    constexpr int PARTS = F32X ? 3 : 1;
+    extern __shared__ __align__(128) unsigned char raw[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int rank = p.ks > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rb;
+    const int nr = static_cast<int>(p.rows - r0 < p.rb ? p.rows - r0 : p.rb);
+    const int kb_lo = p.kblocks * rank / p.ks, nkb = p.kblocks * (rank + 1) / p.ks - kb_lo;
+    const int gpb = 1 << p.gpb_log2;
+    const uint32_t pitch = static_cast<uint32_t>(p.kper) * (L4_BLOCK * 2) + 64;  // 64 past 128: rows take turns in the banks
+    unsigned char *ring = raw;
+    float *red = reinterpret_cast<float *>(ring + L4_WARPS * L4_STAGES * 1024);
+    float *xsum = red + (p.kw_log2 + (p.ks > 1) ? L4_WARPS * l4_red(NT) : 0);  // [group][rb]
+    float *half = xsum + p.kper * gpb * p.rb;                                   // [rb]: sqrt of the power of two
+    uint32_t *top = reinterpret_cast<uint32_t *>(half + p.rb);                  // [rb]: bits of the largest |x|
+    unsigned char *xs = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(top + p.rb) + 127) & ~static_cast<uintptr_t>(127));
+
+    // ---- this warp's tiles and blocks
+    const int kw = 1 << p.kw_log2, sub = warp & (kw - 1);
+    const int kb0 = nkb * sub / kw, kb1 = nkb * (sub + 1) / kw;  // within the CTA's range
+    const int64_t step = static_cast<int64_t>(gridDim.x / p.ks) * (L4_WARPS >> p.kw_log2);
+    const int64_t first = static_cast<int64_t>(blockIdx.x / p.ks) * (L4_WARPS >> p.kw_log2) + (warp >> p.kw_log2);
+    const int row_bytes = static_cast<int>((p.w.K + 31) / 32 * 16);
+    const uint32_t my_ring = smem_addr(ring) + warp * (L4_STAGES * 1024);
+    float side[L4_STAGES][2], zero[L4_STAGES][2];
+    int64_t it = first;  // the block to copy next
+    int ikb = kb0;
+    auto issue = [&](int s) {
+        if (it < p.tiles && kb0 < kb1) {
+            const int64_t n0 = it * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                int64_t n = n0 + i * 8 + (lane >> 2);
+                n = n < p.w.N ? n : p.w.N - 1;
+                const int at = (kb_lo + ikb) * (L4_BLOCK / 2) + (lane & 3) * 16;
+                const bool take = at < row_bytes;
+                const int r = i * 8 + (lane >> 2);
+                cp_async16(my_ring + s * 1024 + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4),
+                           static_cast<const unsigned char *>(p.w.codes) + n * p.w.code_stride + (take ? at : 0), take);
+                const int gi = (kb_lo + ikb) * gpb + (t & (gpb - 1));
+                side[s][i] = gi < p.G ? side_at(p.w.scale, p.w.side_dt, n * p.w.side_stride + gi) : 0.0f;
+                zero[s][i] = gi < p.G && p.w.zero ? side_at(p.w.zero, p.w.side_dt, n * p.w.side_stride + gi) : 8.0f;
+            }
+            if (++ikb == kb1) ikb = kb0, it += step;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < L4_STAGES - 1; ++s) issue(s);
+
+    // ---- x: largest entry of each row, then scaled, split, reordered, and its group sums
+    if (threadIdx.x < p.rb) top[threadIdx.x] = 0;
+    __syncthreads();
+    const int chunks = nkb * (L4_BLOCK / 8);
+    const bool vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride * (F32X ? 4 : 2) % 16 == 0;
+    for (int i = threadIdx.x; i < nr * chunks; i += L4_THREADS) {
+        const int r = i / chunks, k = (i - r * chunks) * 8 + kb_lo * L4_BLOCK;
+        float v[8];
+        load8<F32X>(p.x, (r0 + r) * p.x_stride + k, static_cast<int>(p.w.K) - k, vec, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        // lanes of one half-warp share a row (a range has a multiple of 16 chunks)
+#pragma unroll
+        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffu << (lane & 16), m, d));
+        if ((lane & 15) == 0) atomicMax(&top[r], m);
+    }
+    __syncthreads();
+    if (threadIdx.x < nr) {
+        const uint32_t m = top[threadIdx.x];
+        // the largest entry ends up below 2^127; odd, so that 133 - e is even
+        int e = m >= 0x7f800000u || m == 0 ? 133 : (252 - static_cast<int>(m >> 23)) | 1;
+        if (e > 251) e = 251;
+        half[threadIdx.x] = m >= 0x7f800000u ? NAN : pow2f((133 - e) / 2);
+        top[threadIdx.x] = static_cast<uint32_t>(e);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nr * chunks; i += L4_THREADS) {
+        const int r = i / chunks, c = i - r * chunks, k = c * 8 + kb_lo * L4_BLOCK;
+        float v[8];
+        load8<F32X>(p.x, (r0 + r) * p.x_stride + k, static_cast<int>(p.w.K) - k, vec, v);
+        const int e = static_cast<int>(top[r]);
+        const bool bad = isnan(half[r]);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (bad) v[j] = 0.0f;
+            sum += scale2(v[j], e - 133);
+            v[j] = scale2(v[j], (j & 1) ? e - 4 : e);
+        }
+        const int lanes = 4 << (2 - p.gpb_log2);  // chunks of a group
+        for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (lane & 16), sum, d);
+        if ((c & (lanes - 1)) == 0) xsum[c / lanes * p.rb + r] = sum;
+        unsigned char *dst = xs + r * pitch + c * 16;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            uint4 o;
+            uint32_t *ow = &o.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ow[j] = bf16_pair(v[j], v[j + 4]);
+                if (PARTS > 1) v[j] -= bf16lo(ow[j]), v[j + 4] -= bf16hi(ow[j]);
+            }
+            *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(q) * p.rb * pitch) = o;
         }
     }
+    __syncthreads();
+
+    // ---- tiles
+    const unsigned char *xb[NT];
+    float hf[NT][2];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+        const int r = q * 8 + g;
+        xb[q] = xs + (r < nr ? r : nr - 1) * pitch + t * 16;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = q * 8 + 2 * t + j;
+            hf[q][j] = half[c < nr ? c : nr - 1];
+        }
+    }
+    int s = 0;  // stage of the next block
+    for (int64_t tile0 = first - (warp >> p.kw_log2); tile0 < p.tiles; tile0 += step) {
+        const int64_t tile = tile0 + (warp >> p.kw_log2);
+        float acc[NT][4];
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[q][j] = 0.0f;
+        if (tile < p.tiles) {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                float sd[2], zr[2];
+#pragma unroll
+                for (int i = 0; i < L4_STAGES; ++i)
+                    if (s == i) {
+                        issue((i + L4_STAGES - 1) % L4_STAGES);
+                        sd[0] = side[i][0], sd[1] = side[i][1], zr[0] = zero[i][0], zr[1] = zero[i][1];
+                    }
+                cp_async_wait<L4_STAGES - 1>();
+                __syncwarp();
+                const uint32_t *blk = reinterpret_cast<const uint32_t *>(ring + (warp * L4_STAGES + s) * 1024);
+                float part[NT][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if ((j & ((4 >> p.gpb_log2) - 1)) == 0)
+#pragma unroll
+                        for (int q = 0; q < NT; ++q) part[q][0] = part[q][1] = part[q][2] = part[q][3] = 0.0f;
+                    const uint32_t wl = blk[g * 16 + ((j ^ ((g >> 1) & 3)) << 2) + t];
+                    const uint32_t wh = blk[(g + 8) * 16 + ((j ^ ((g >> 1) & 3)) << 2) + t];
+                    const uint32_t ul = wl >> 8, uh = wh >> 8;
+#pragma unroll
+                    for (int q = 0; q < NT; ++q)
+#pragma unroll
+                        for (int h = 0; h < PARTS; ++h) {
+                            const uint4 b = *reinterpret_cast<const uint4 *>(
+                                xb[q] + static_cast<size_t>(h) * p.rb * pitch + (kb * 16 + j * 4) * 16);
+                            mma_16816(part[q], wl & 0x000f000fu, wh & 0x000f000fu, wl & 0x00f000f0u, wh & 0x00f000f0u,
+                                      b.x, b.y);
+                            mma_16816(part[q], ul & 0x000f000fu, uh & 0x000f000fu, ul & 0x00f000f0u, uh & 0x00f000f0u,
+                                      b.z, b.w);
+                        }
+                    if (((j + 1) & ((4 >> p.gpb_log2) - 1)) == 0) {
+                        const int gj = j >> (2 - p.gpb_log2), from = (lane & ~3) | (p.gpb_log2 == 0 ? t : gj);
+                        const float s0 = __shfl_sync(FULL, sd[0], from), s1 = __shfl_sync(FULL, sd[1], from);
+                        const float z0 = __shfl_sync(FULL, zr[0], from), z1 = __shfl_sync(FULL, zr[1], from);
+                        const float *sums = xsum + (kb * gpb + gj) * p.rb;
+#pragma unroll
+                        for (int q = 0; q < NT; ++q)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int c = q * 8 + 2 * t + i;
+                                const float xg = sums[c < nr ? c : nr - 1];
+                                acc[q][i] = fmaf(s0 * hf[q][i] * hf[q][i], fmaf(-z0, xg, part[q][i]), acc[q][i]);
+                                acc[q][2 + i] = fmaf(s1 * hf[q][i] * hf[q][i], fmaf(-z1, xg, part[q][2 + i]), acc[q][2 + i]);
+                            }
+                    }
+                }
+                __syncwarp();
+                s = (s + 1) % L4_STAGES;
+            }
+        }
+        if (kw == 1 && p.ks == 1) {
+            if (tile < p.tiles)
+#pragma unroll
+                for (int q = 0; q < NT; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = q * 8 + 2 * t + (j & 1);
+                        const int64_t n = tile * 16 + g + (j >> 1) * 8;
+                        if (c < nr && n < p.w.N) {
+                            const int64_t at = (r0 + c) * p.y_stride + n;
+                            if (p.y_dt == DFLASH2_F32) static_cast<float *>(p.y)[at] = acc[q][j];
+                            else static_cast<uint16_t *>(p.y)[at] = bf16_bits(acc[q][j]);
+                        }
+                    }
+            continue;
+        }
+        // parts of a tile: the warps of a CTA in order, then the CTAs of the cluster in order
+        float *mine = red + warp * l4_red(NT);
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mine[(q * 8 + 2 * t + (j & 1)) * 17 + g + (j >> 1) * 8] = acc[q][j];
+        if (p.ks > 1) cluster_sync();
+        else __syncthreads();
+        const int per_tile = nr * 16, here = (L4_WARPS >> p.kw_log2) * per_tile;
+        for (int i = threadIdx.x + rank * L4_THREADS; i < here; i += L4_THREADS * p.ks) {
+            const int slot = i / per_tile, c = (i - slot * per_tile) >> 4, n16 = i & 15;
+            const int64_t n = (tile0 + slot) * 16 + n16;
+            float v = 0.0f;
+            for (int q = 0; q < p.ks; ++q)
+                for (int w = 0; w < kw; ++w) {
+                    const float *src = red + ((slot << p.kw_log2) + w) * l4_red(NT) + c * 17 + n16;
+                    if (p.ks > 1) {
+                        uint32_t remote;
+                        float f;
+                        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(src)), "r"(q));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(remote));
+                        v += f;
+                    } else {
+                        v += *src;
+                    }
+                }
+            if (n < p.w.N) {
+                const int64_t at = (r0 + c) * p.y_stride + n;
+                if (p.y_dt == DFLASH2_F32) static_cast<float *>(p.y)[at] = v;
+                else static_cast<uint16_t *>(p.y)[at] = bf16_bits(v);
+            }
+        }
+        if (p.ks > 1) cluster_sync();
+        else __syncthreads();
+    }
+    cp_async_wait<0>();
+}
+
+// ------------------------------------------------------------------ host ----
+// Shared memory of a CTA.
+static size_t l4_smem(const Lin4 &p, int nt, int parts) {
+    size_t b = static_cast<size_t>(L4_WARPS) * L4_STAGES * 1024;
+    if (p.kw_log2 || p.ks > 1) b += static_cast<size_t>(L4_WARPS) * l4_red(nt) * 4;
+    b += (static_cast<size_t>(p.kper << p.gpb_log2) * p.rb + 2 * p.rb) * 4 + 128;
+    return b + (static_cast<size_t>(p.kper) * (L4_BLOCK * 2) + 64) * p.rb * parts;
+}
+
+template <int NT, bool F32X>
+static dflash2_status launch_l4(const Lin4 &p, size_t smem, unsigned gx, unsigned gy, cudaStream_t s) {
+    auto fn = &k_linear4_mma<NT, F32X>;
+    {
+        static int opted[64] = {0};
+        static std::mutex mu;
+        const int dev = current_device();
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev < 0 || dev >= 64 || !opted[dev]) {
+            if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L4_SMEM_MAX) != cudaSuccess)
+                return DFLASH2_ERR_CUDA;
+            if (dev >= 0 && dev < 64) opted[dev] = 1;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(gx, gy, 1);
+    cfg.blockDim = dim3(L4_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.ks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.ks > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) return DFLASH2_ERR_CUDA;
+    return after_launch();
+}
+
+static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
+    const int parts = f32x ? 3 : 1;
+    const int most_rows = f32x ? 16 : 32;
+    p.rb = static_cast<int>(p.rows < most_rows ? p.rows : most_rows);
+    if (p.rows > most_rows) {  // even blocks of rows
+        const int64_t nb = (p.rows + most_rows - 1) / most_rows;
+        p.rb = static_cast<int>((p.rows + nb - 1) / nb);
+    }
+    p.tiles = (p.w.N + 15) / 16;
+    p.kblocks = static_cast<int>((p.w.K + L4_BLOCK - 1) / L4_BLOCK);
+    const int64_t sms = sm_count();
+    for (;; p.rb = (p.rb + 1) / 2) {
+        const int nt = (p.rb + 7) / 8;
+        // warps that share a tile: until every warp slot of the GPU has work
+        p.kw_log2 = 0;
+        while (p.kw_log2 < 3 && (p.tiles << p.kw_log2) < sms * L4_WARP_TARGET && (2 << p.kw_log2) <= p.kblocks) ++p.kw_log2;
+        for (p.ks = 1;; p.ks *= 2) {
+            p.kper = (p.kblocks + p.ks - 1) / p.ks;
+            const bool fits = l4_smem(p, nt, parts) <= L4_SMEM_GOOD;
+            const int64_t ctas = (p.tiles + (L4_WARPS >> p.kw_log2) - 1) / (L4_WARPS >> p.kw_log2);
+            const bool more = ctas * p.ks * 2 <= sms && (p.kper >> p.kw_log2) >= 2;
+            if (p.ks == 8 || p.ks * 2 > p.kblocks || (fits && !more)) break;
+        }
+        if (l4_smem(p, nt, parts) <= L4_SMEM_MAX) break;
+        if (p.rb == 1) return DFLASH2_ERR_UNSUPPORTED;
+    }
+    const int nt = (p.rb + 7) / 8;
+    const size_t smem = l4_smem(p, nt, parts);
+    const int64_t gy = (p.rows + p.rb - 1) / p.rb;
+    if (gy > 65535) return DFLASH2_ERR_UNSUPPORTED;
+    const int64_t sets = (p.tiles + (L4_WARPS >> p.kw_log2) - 1) / (L4_WARPS >> p.kw_log2);
+    int64_t per_sm = static_cast<int64_t>(L4_SMEM_MAX + 1024) / static_cast<int64_t>(smem + 1024);
+    if (per_sm > L4_PER_SM) per_sm = L4_PER_SM;
+    int64_t ctas = sms * per_sm / (gy < per_sm ? gy : per_sm) / p.ks;
+    if (ctas < 1) ctas = 1;
+    if (ctas > sets) ctas = sets;
+    const unsigned gx = static_cast<unsigned>(ctas * p.ks);
+    if (f32x) return nt == 1 ? launch_l4<1, true>(p, smem, gx, gy, s) : launch_l4<2, true>(p, smem, gx, gy, s);
+    if (nt == 1) return launch_l4<1, false>(p, smem, gx, gy, s);
+    if (nt == 2) return launch_l4<2, false>(p, smem, gx, gy, s);
+    if (nt == 3) return launch_l4<3, false>(p, smem, gx, gy, s);
+    return launch_l4<4, false>(p, smem, gx, gy, s);
 }
 
 }  // namespace dfl
@@ -140,9 +528,10 @@ extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64
         return DFLASH2_ERR_INVALID_ARG;
     if (rows == 0 || w->N == 0) return DFLASH2_OK;
     if (!x || !y || !aligned_to(x, dt) || !aligned_to(y, y_dt)) return DFLASH2_ERR_INVALID_ARG;
-    const int64_t by = (rows + 7) / 8;
-    if (by > 65535) return DFLASH2_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>((w->N + 7) / 8), static_cast<unsigned>(by));
-    k_linear4<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(x, dt, rows, x_stride, *w, y, y_dt, y_stride);
-    return after_launch();
+    if (w->K > (1 << 17)) return DFLASH2_ERR_UNSUPPORTED;
+    Lin4 p = {};
+    p.x = x, p.rows = rows, p.x_stride = x_stride, p.w = *w, p.y = y, p.y_stride = y_stride, p.y_dt = y_dt;
+    p.G = static_cast<int>(groups_of(w));
+    p.gpb_log2 = w->group == 128 ? 0 : w->group == 64 ? 1 : 2;
+    return linear4_mma(p, dt == DFLASH2_F32, reinterpret_cast<cudaStream_t>(stream));
 }
