@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) k_dequant4(dflash2_weight4 w, void *out, 
 //   scaled by a power of two (largest entry near 2^126) and, at the second
 //   pairs' columns, by 2^-4; both are exact, and are taken back with the scale.
 //   A group of columns is summed from zero, so that
-//     acc += scale * 2^e * (sum of code * x - zero * sum of x)
+//     acc += scale * (sum of code * x - zero * sum of x)
 //   in f32: products of a code and a bf16 are exact.  f32 rows are split into
 //   three bf16 parts, which is exact too.
 //
@@ -119,7 +119,7 @@ struct Lin4 {
     int64_t y_stride;
     dflash2_dtype y_dt;
     int G;          // groups in a row
-    int gpb_log2;   // log2 of the groups in a block
+    int gpb_log2;   // log2 of the groups in a block (the kernels' LG)
     int rb;         // rows of x to a CTA
     int kblocks;    // blocks in a row
     int kper;       // blocks of the largest range of a CTA
@@ -172,63 +172,103 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ void lds32(uint32_t at, uint32_t (&v)[1]) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(at));
+}
+__device__ __forceinline__ void lds64(uint32_t at, uint32_t (&v)[2]) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+}
+__device__ __forceinline__ void lds128(uint32_t at, uint32_t (&v)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
+}
+
 // Floats of the cross-warp sums: [row of x][16 + 1] per warp.
 __host__ __device__ constexpr int l4_red(int nt) { return nt * 8 * 17; }
 
-template <int NT, bool F32X>
+// LG: log2 of the groups in a block.
+template <int NT, int LG, bool F32X>
 __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
-    constexpr int PARTS = F32X ? 3 : 1;
+    constexpr int PARTS = F32X ? 3 : 1, GPB = 1 << LG, WPG = 4 >> LG;  // words of a thread in a group's row
     extern __shared__ __align__(128) unsigned char raw[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int rank = p.ks > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rb;
     const int nr = static_cast<int>(p.rows - r0 < p.rb ? p.rows - r0 : p.rb);
     const int kb_lo = p.kblocks * rank / p.ks, nkb = p.kblocks * (rank + 1) / p.ks - kb_lo;
-    const int gpb = 1 << p.gpb_log2;
     const uint32_t pitch = static_cast<uint32_t>(p.kper) * (L4_BLOCK * 2) + 64;  // 64 past 128: rows take turns in the banks
+    const int sums_ld = NT * 8 + 2;
     unsigned char *ring = raw;
     float *red = reinterpret_cast<float *>(ring + L4_WARPS * L4_STAGES * 1024);
-    float *xsum = red + (p.kw_log2 + (p.ks > 1) ? L4_WARPS * l4_red(NT) : 0);  // [group][rb]
-    float *half = xsum + p.kper * gpb * p.rb;                                   // [rb]: sqrt of the power of two
-    uint32_t *top = reinterpret_cast<uint32_t *>(half + p.rb);                  // [rb]: bits of the largest |x|
+    float *xsum = red + ((p.kw_log2 || p.ks > 1) ? L4_WARPS * l4_red(NT) : 0);  // [group][sums_ld]
+    float *half = xsum + p.kper * GPB * sums_ld;                                // [NT * 8]: root of the power of two
+    uint32_t *top = reinterpret_cast<uint32_t *>(half + NT * 8);                // [NT * 8]: bits of the largest |x|
     unsigned char *xs = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(top + p.rb) + 127) & ~static_cast<uintptr_t>(127));
+        (reinterpret_cast<uintptr_t>(top + NT * 8) + 127) & ~static_cast<uintptr_t>(127));
 
     // ---- this warp's tiles and blocks
     const int kw = 1 << p.kw_log2, sub = warp & (kw - 1);
-    const int kb0 = nkb * sub / kw, kb1 = nkb * (sub + 1) / kw;  // within the CTA's range
+    const int kb0 = nkb * sub / kw, count = nkb * (sub + 1) / kw - kb0;  // within the CTA's range
     const int64_t step = static_cast<int64_t>(gridDim.x / p.ks) * (L4_WARPS >> p.kw_log2);
     const int64_t first = static_cast<int64_t>(blockIdx.x / p.ks) * (L4_WARPS >> p.kw_log2) + (warp >> p.kw_log2);
     const int row_bytes = static_cast<int>((p.w.K + 31) / 32 * 16);
-    const uint32_t my_ring = smem_addr(ring) + warp * (L4_STAGES * 1024);
-    float side[L4_STAGES][2], zero[L4_STAGES][2];
-    int64_t it = first;  // the block to copy next
-    int ikb = kb0;
-    auto issue = [&](int s) {
-        if (it < p.tiles && kb0 < kb1) {
-            const int64_t n0 = it * 16;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                int64_t n = n0 + i * 8 + (lane >> 2);
-                n = n < p.w.N ? n : p.w.N - 1;
-                const int at = (kb_lo + ikb) * (L4_BLOCK / 2) + (lane & 3) * 16;
-                const bool take = at < row_bytes;
-                const int r = i * 8 + (lane >> 2);
-                cp_async16(my_ring + s * 1024 + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4),
-                           static_cast<const unsigned char *>(p.w.codes) + n * p.w.code_stride + (take ? at : 0), take);
-                const int gi = (kb_lo + ikb) * gpb + (t & (gpb - 1));
-                side[s][i] = gi < p.G ? side_at(p.w.scale, p.w.side_dt, n * p.w.side_stride + gi) : 0.0f;
-                zero[s][i] = gi < p.G && p.w.zero ? side_at(p.w.zero, p.w.side_dt, n * p.w.side_stride + gi) : 8.0f;
-            }
-            if (++ikb == kb1) ikb = kb0, it += step;
+    const int at0 = (kb_lo + kb0) * (L4_BLOCK / 2);
+    // row of the tile that this lane copies (and r + 8), and where the copy lands; the swizzle spreads the reads below
+    const uint32_t copy_to = smem_addr(ring) + warp * (L4_STAGES * 1024) + g * 64 +
+                             ((t ^ (LG == 0 ? 0 : LG == 1 ? g & 2 : (g >> 1) & 3)) << 4);
+    int64_t c_tile = first;  // the block to copy next
+    int c_left = 0;
+    const unsigned char *c0 = nullptr, *c1 = nullptr;
+    int c_at = 0;
+    auto copy = [&](uint32_t stage) {
+        if (c_left == 0 && c_tile < p.tiles && count) {
+            int64_t n0 = c_tile * 16 + g, n1 = n0 + 8;
+            n0 = n0 < p.w.N ? n0 : p.w.N - 1, n1 = n1 < p.w.N ? n1 : p.w.N - 1;
+            c0 = static_cast<const unsigned char *>(p.w.codes) + n0 * p.w.code_stride + at0 + t * 16;
+            c1 = static_cast<const unsigned char *>(p.w.codes) + n1 * p.w.code_stride + at0 + t * 16;
+            c_at = at0 + t * 16;
+            c_left = count;
+            c_tile += step;
+        }
+        if (c_left) {
+            const bool take = c_at < row_bytes;
+            const void *q = p.w.codes;
+            cp_async16(copy_to + stage, take ? c0 : q, take);
+            cp_async16(copy_to + stage + 512, take ? c1 : q, take);
+            c0 += 64, c1 += 64, c_at += 64, --c_left;
         }
         cp_async_commit();
     };
+    // scales and zero points, four groups (a quad's lane each) at a time, one step ahead
+    int64_t s_tile = first;
+    int s_left = 0, s_gi = 0;
+    int64_t s_at0 = 0, s_at1 = 0;
+    float sn0 = 0.0f, sn1 = 0.0f, zn0 = 8.0f, zn1 = 8.0f;
+    auto sides = [&]() {
+        if (s_left == 0 && s_tile < p.tiles && count) {
+            int64_t n0 = s_tile * 16 + g, n1 = n0 + 8;
+            n0 = n0 < p.w.N ? n0 : p.w.N - 1, n1 = n1 < p.w.N ? n1 : p.w.N - 1;
+            s_gi = (kb_lo + kb0) * GPB + t;
+            s_at0 = n0 * p.w.side_stride + s_gi, s_at1 = n1 * p.w.side_stride + s_gi;
+            s_left = (count * GPB + 3) / 4;
+            s_tile += step;
+        }
+        if (s_left) {
+            const bool in = s_gi < p.G;
+            sn0 = in ? side_at(p.w.scale, p.w.side_dt, s_at0) : 0.0f;
+            sn1 = in ? side_at(p.w.scale, p.w.side_dt, s_at1) : 0.0f;
+            if (p.w.zero) {
+                zn0 = in ? side_at(p.w.zero, p.w.side_dt, s_at0) : 8.0f;
+                zn1 = in ? side_at(p.w.zero, p.w.side_dt, s_at1) : 8.0f;
+            }
+            s_gi += 4, s_at0 += 4, s_at1 += 4, --s_left;
+        }
+    };
 #pragma unroll
-    for (int s = 0; s < L4_STAGES - 1; ++s) issue(s);
+    for (int s = 0; s < L4_STAGES - 1; ++s) copy(s * 1024);
+    sides();
 
     // ---- x: largest entry of each row, then scaled, split, reordered, and its group sums
-    if (threadIdx.x < p.rb) top[threadIdx.x] = 0;
+    if (threadIdx.x < NT * 8) top[threadIdx.x] = 0;
     __syncthreads();
     const int chunks = nkb * (L4_BLOCK / 8);
     const bool vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride * (F32X ? 4 : 2) % 16 == 0;
@@ -267,10 +307,13 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
             sum += scale2(v[j], e - 133);
             v[j] = scale2(v[j], (j & 1) ? e - 4 : e);
         }
-        const int lanes = 4 << (2 - p.gpb_log2);  // chunks of a group
-        for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (lane & 16), sum, d);
-        if ((c & (lanes - 1)) == 0) xsum[c / lanes * p.rb + r] = sum;
-        unsigned char *dst = xs + r * pitch + c * 16;
+        constexpr int LANES = 16 >> LG;  // chunks of a group
+#pragma unroll
+        for (int d = LANES >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (lane & 16), sum, d);
+        if ((c & (LANES - 1)) == 0) xsum[c / LANES * sums_ld + r] = sum;
+        // where thread t finds its j-th word's columns: the words of a group lie WPG to a thread
+        const int cc = c & 15, cg = cc / LANES, ci = cc % LANES;
+        unsigned char *dst = xs + r * pitch + ((c & ~15) + (cg * WPG + ci % WPG) * 4 + ci / WPG) * 16;
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
             uint4 o;
@@ -286,19 +329,27 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
     __syncthreads();
 
     // ---- tiles
-    const unsigned char *xb[NT];
+    uint32_t xb[NT];
     float hf[NT][2];
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
         const int r = q * 8 + g;
-        xb[q] = xs + (r < nr ? r : nr - 1) * pitch + t * 16;
+        xb[q] = smem_addr(xs) + (r < nr ? r : nr - 1) * pitch + t * 16 + kb0 * (L4_BLOCK * 2);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int c = q * 8 + 2 * t + j;
             hf[q][j] = half[c < nr ? c : nr - 1];
         }
     }
-    int s = 0;  // stage of the next block
+    uint32_t words[WPG == 4 ? 1 : GPB];  // where this lane's words of a group lie in a block
+#pragma unroll
+    for (int j = 0; j < (WPG == 4 ? 1 : GPB); ++j)
+        words[j] = smem_addr(ring) + warp * (L4_STAGES * 1024) + g * 64 +
+                   (LG == 0   ? t * 16
+                    : LG == 1 ? ((((2 * j + (t >> 1)) ^ (g & 2)) << 4) + (t & 1) * 8)
+                              : (((j ^ ((g >> 1) & 3)) << 4) + t * 4));
+    const float *sums0 = xsum + kb0 * GPB * sums_ld + 2 * t;
+    uint32_t s = 0, s_next = (L4_STAGES - 1) * 1024;  // stage of the next block, and of the next copy
     for (int64_t tile0 = first - (warp >> p.kw_log2); tile0 < p.tiles; tile0 += step) {
         const int64_t tile = tile0 + (warp >> p.kw_log2);
         float acc[NT][4];
@@ -307,56 +358,68 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[q][j] = 0.0f;
         if (tile < p.tiles) {
-            for (int kb = kb0; kb < kb1; ++kb) {
-                float sd[2], zr[2];
-#pragma unroll
-                for (int i = 0; i < L4_STAGES; ++i)
-                    if (s == i) {
-                        issue((i + L4_STAGES - 1) % L4_STAGES);
-                        sd[0] = side[i][0], sd[1] = side[i][1], zr[0] = zero[i][0], zr[1] = zero[i][1];
-                    }
+            float sd0 = 0.0f, sd1 = 0.0f, zr0 = 8.0f, zr1 = 8.0f;
+            const float *sums = sums0;
+            uint32_t xo = 0;
+            for (int i = 0; i < count; ++i, xo += L4_BLOCK * 2) {
+                copy(s_next);
+                if (LG == 2 || (i & (WPG - 1)) == 0) {
+                    sd0 = sn0, sd1 = sn1, zr0 = zn0, zr1 = zn1;
+                    sides();
+                }
                 cp_async_wait<L4_STAGES - 1>();
                 __syncwarp();
-                const uint32_t *blk = reinterpret_cast<const uint32_t *>(ring + (warp * L4_STAGES + s) * 1024);
-                float part[NT][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if ((j & ((4 >> p.gpb_log2) - 1)) == 0)
+                for (int j = 0; j < GPB; ++j, sums += sums_ld) {
+                    uint32_t wl[WPG], wh[WPG];
+                    if constexpr (LG == 0) {
+                        lds128(words[0] + s, wl), lds128(words[0] + s + 512, wh);
+                    } else if constexpr (LG == 1) {
+                        lds64(words[j] + s, wl), lds64(words[j] + s + 512, wh);
+                    } else {
+                        lds32(words[j] + s, wl), lds32(words[j] + s + 512, wh);
+                    }
+                    const int from = (lane & ~3) | (LG == 2 ? j : ((i << LG) + j) & 3);
+                    const float s0 = __shfl_sync(FULL, sd0, from), s1 = __shfl_sync(FULL, sd1, from);
+                    float z0 = 8.0f, z1 = 8.0f;
+                    if (p.w.zero) z0 = __shfl_sync(FULL, zr0, from), z1 = __shfl_sync(FULL, zr1, from);
+                    // the sum starts at - zero * sum of x
+                    float part[NT][4];
 #pragma unroll
-                        for (int q = 0; q < NT; ++q) part[q][0] = part[q][1] = part[q][2] = part[q][3] = 0.0f;
-                    const uint32_t wl = blk[g * 16 + ((j ^ ((g >> 1) & 3)) << 2) + t];
-                    const uint32_t wh = blk[(g + 8) * 16 + ((j ^ ((g >> 1) & 3)) << 2) + t];
-                    const uint32_t ul = wl >> 8, uh = wh >> 8;
+                    for (int q = 0; q < NT; ++q) {
+                        const float2 xg = *reinterpret_cast<const float2 *>(sums + q * 8);
+                        part[q][0] = -z0 * xg.x, part[q][1] = -z0 * xg.y;
+                        part[q][2] = -z1 * xg.x, part[q][3] = -z1 * xg.y;
+                    }
 #pragma unroll
-                    for (int q = 0; q < NT; ++q)
-#pragma unroll
-                        for (int h = 0; h < PARTS; ++h) {
-                            const uint4 b = *reinterpret_cast<const uint4 *>(
-                                xb[q] + static_cast<size_t>(h) * p.rb * pitch + (kb * 16 + j * 4) * 16);
-                            mma_16816(part[q], wl & 0x000f000fu, wh & 0x000f000fu, wl & 0x00f000f0u, wh & 0x00f000f0u,
-                                      b.x, b.y);
-                            mma_16816(part[q], ul & 0x000f000fu, uh & 0x000f000fu, ul & 0x00f000f0u, uh & 0x00f000f0u,
-                                      b.z, b.w);
-                        }
-                    if (((j + 1) & ((4 >> p.gpb_log2) - 1)) == 0) {
-                        const int gj = j >> (2 - p.gpb_log2), from = (lane & ~3) | (p.gpb_log2 == 0 ? t : gj);
-                        const float s0 = __shfl_sync(FULL, sd[0], from), s1 = __shfl_sync(FULL, sd[1], from);
-                        const float z0 = __shfl_sync(FULL, zr[0], from), z1 = __shfl_sync(FULL, zr[1], from);
-                        const float *sums = xsum + (kb * gpb + gj) * p.rb;
+                    for (int v = 0; v < WPG; ++v) {
+                        const uint32_t ul = wl[v] >> 8, uh = wh[v] >> 8;
 #pragma unroll
                         for (int q = 0; q < NT; ++q)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int c = q * 8 + 2 * t + i;
-                                const float xg = sums[c < nr ? c : nr - 1];
-                                acc[q][i] = fmaf(s0 * hf[q][i] * hf[q][i], fmaf(-z0, xg, part[q][i]), acc[q][i]);
-                                acc[q][2 + i] = fmaf(s1 * hf[q][i] * hf[q][i], fmaf(-z1, xg, part[q][2 + i]), acc[q][2 + i]);
+                            for (int h = 0; h < PARTS; ++h) {
+                                uint32_t b[4];
+                                lds128(xb[q] + h * p.rb * pitch + xo + (j * WPG + v) * 64, b);
+                                mma_16816(part[q], wl[v] & 0x000f000fu, wh[v] & 0x000f000fu, wl[v] & 0x00f000f0u,
+                                          wh[v] & 0x00f000f0u, b[0], b[1]);
+                                mma_16816(part[q], ul & 0x000f000fu, uh & 0x000f000fu, ul & 0x00f000f0u,
+                                          uh & 0x00f000f0u, b[2], b[3]);
                             }
+                    }
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) {
+                        acc[q][0] = fmaf(s0, part[q][0], acc[q][0]), acc[q][1] = fmaf(s0, part[q][1], acc[q][1]);
+                        acc[q][2] = fmaf(s1, part[q][2], acc[q][2]), acc[q][3] = fmaf(s1, part[q][3], acc[q][3]);
                     }
                 }
                 __syncwarp();
-                s = (s + 1) % L4_STAGES;
+                s_next = s;
+                s = s == (L4_STAGES - 1) * 1024 ? 0 : s + 1024;
             }
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[q][j] = acc[q][j] * hf[q][j & 1] * hf[q][j & 1];
         }
         if (kw == 1 && p.ks == 1) {
             if (tile < p.tiles)
@@ -417,13 +480,13 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
 static size_t l4_smem(const Lin4 &p, int nt, int parts) {
     size_t b = static_cast<size_t>(L4_WARPS) * L4_STAGES * 1024;
     if (p.kw_log2 || p.ks > 1) b += static_cast<size_t>(L4_WARPS) * l4_red(nt) * 4;
-    b += (static_cast<size_t>(p.kper << p.gpb_log2) * p.rb + 2 * p.rb) * 4 + 128;
+    b += (static_cast<size_t>(p.kper << p.gpb_log2) * (nt * 8 + 2) + 2 * nt * 8) * 4 + 128;
     return b + (static_cast<size_t>(p.kper) * (L4_BLOCK * 2) + 64) * p.rb * parts;
 }
 
-template <int NT, bool F32X>
+template <int NT, int LG, bool F32X>
 static dflash2_status launch_l4(const Lin4 &p, size_t smem, unsigned gx, unsigned gy, cudaStream_t s) {
-    auto fn = &k_linear4_mma<NT, F32X>;
+    auto fn = &k_linear4_mma<NT, LG, F32X>;
     {
         static int opted[64] = {0};
         static std::mutex mu;
@@ -448,6 +511,13 @@ static dflash2_status launch_l4(const Lin4 &p, size_t smem, unsigned gx, unsigne
     cfg.numAttrs = p.ks > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) return DFLASH2_ERR_CUDA;
     return after_launch();
+}
+
+template <int NT, bool F32X>
+static dflash2_status launch_l4_groups(const Lin4 &p, size_t smem, unsigned gx, unsigned gy, cudaStream_t s) {
+    if (p.gpb_log2 == 0) return launch_l4<NT, 0, F32X>(p, smem, gx, gy, s);
+    if (p.gpb_log2 == 1) return launch_l4<NT, 1, F32X>(p, smem, gx, gy, s);
+    return launch_l4<NT, 2, F32X>(p, smem, gx, gy, s);
 }
 
 static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
@@ -487,11 +557,11 @@ static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
     if (ctas < 1) ctas = 1;
     if (ctas > sets) ctas = sets;
     const unsigned gx = static_cast<unsigned>(ctas * p.ks);
-    if (f32x) return nt == 1 ? launch_l4<1, true>(p, smem, gx, gy, s) : launch_l4<2, true>(p, smem, gx, gy, s);
-    if (nt == 1) return launch_l4<1, false>(p, smem, gx, gy, s);
-    if (nt == 2) return launch_l4<2, false>(p, smem, gx, gy, s);
-    if (nt == 3) return launch_l4<3, false>(p, smem, gx, gy, s);
-    return launch_l4<4, false>(p, smem, gx, gy, s);
+    if (f32x) return nt == 1 ? launch_l4_groups<1, true>(p, smem, gx, gy, s) : launch_l4_groups<2, true>(p, smem, gx, gy, s);
+    if (nt == 1) return launch_l4_groups<1, false>(p, smem, gx, gy, s);
+    if (nt == 2) return launch_l4_groups<2, false>(p, smem, gx, gy, s);
+    if (nt == 3) return launch_l4_groups<3, false>(p, smem, gx, gy, s);
+    return launch_l4_groups<4, false>(p, smem, gx, gy, s);
 }
 
 }  // namespace dfl
