@@ -645,8 +645,8 @@ dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, in
  * last one with any mass.  Greedy rows take the first token.
  * token [rows] int32; prob [rows] f32: the drawn token's share of the kept
  *   mass (1 for greedy rows).
- * Masses are summed as whole numbers of 2^-45 (of 2^-(63 - ceil(log2 V)) for V
- *   above 2^18), so a row's token depends neither on the other rows nor on
+ * Masses are summed as whole numbers of 2^-44 (of 2^-(63 - ceil(log2(V + 1)))
+ *   for V above 2^19), so a row's token depends neither on the other rows nor on
  *   how the row is split.
  * A row with a NaN or +Inf, nothing above -Inf, a NaN uniform or invalid
  * parameters (as DFLASH2_ST_BAD_PARAMS; min_p outside [0, 1]) gets token -1 and
