@@ -95,7 +95,9 @@ def load_library():
         L.dflash2_kv_evict.argtypes = [vp, vp, i32, vp, vp, i64, i32, i32, i32, vp, vp, sz, vp]
         L.dflash2_quant4.argtypes = [vp, i32, i64, vp, vp]
         L.dflash2_dequant4.argtypes = [vp, vp, i32, i64, vp]
-        L.dflash2_linear4.argtypes = [vp, i32, i64, i64, vp, vp, i32, i64, vp]
+        L.dflash2_linear4_workspace_bytes.argtypes = [i32, i64, i64, i64]
+        L.dflash2_linear4_workspace_bytes.restype = sz
+        L.dflash2_linear4.argtypes = [vp, i32, i64, i64, vp, vp, i32, i64, vp, sz, vp]
         L.dflash2_sample.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp]
         L.dflash2_status_string.argtypes = [i32]
         L.dflash2_status_string.restype = ctypes.c_char_p
@@ -198,7 +200,7 @@ def _count(name: str, n: int) -> int:
 def _scratch(ws, dev: int):
     """Address and size of a workspace."""
     if ws.buf.get_device() != dev:
-        raise ValueError("ws: a workspace on the cache's GPU")
+        raise ValueError("ws: a workspace on the GPU of the other tensors")
     return ws.buf.data_ptr(), ws.buf.numel()
 
 
@@ -266,6 +268,10 @@ class Workspace:
     def for_paged_attn(B: int, T: int, Hq: int, Hkv: int, d: int, dtype, device="cuda") -> "Workspace":
         return Workspace(load_library().dflash2_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, _dtype_code(dtype)),
                          device)
+
+    @staticmethod
+    def for_linear4(rows: int, N: int, K: int, dtype=torch.bfloat16, device="cuda") -> "Workspace":
+        return Workspace(load_library().dflash2_linear4_workspace_bytes(_dtype_code(dtype), rows, N, K), device)
 
     @staticmethod
     def for_kv_evict(B: int, Hkv: int, capacity: int, budget: int, device="cuda") -> "Workspace":
@@ -654,7 +660,7 @@ def dequant4(w: Weight4, dtype=torch.bfloat16, out=None) -> torch.Tensor:
     return out
 
 
-def linear4(x: torch.Tensor, w: Weight4, dtype=None, out=None) -> torch.Tensor:
+def linear4(x: torch.Tensor, w: Weight4, dtype=None, ws=None, out=None) -> torch.Tensor:
     """dflash2_linear4.  x [rows, K] (bf16/f32, contiguous rows).  Returns x . W^T [rows, N] of x's type or float32, or
     fills `out` (contiguous rows, any distance from row to row)."""
     dev = _here(w, "weights")
@@ -663,8 +669,15 @@ def linear4(x: torch.Tensor, w: Weight4, dtype=None, out=None) -> torch.Tensor:
     if out is None:
         out = torch.empty((rows, w.N), dtype=x.dtype if dtype is None else dtype, device=x.device)
     yp, ys = _rows("out", out, (rows, w.N), dev)
-    _check("dflash2_linear4", (_lib or load_library()).dflash2_linear4(xp, _dtype(x), rows, xs, w._ref, yp, _dtype(out),
-                                                                       ys, _raw_stream(dev)))
+    L, dt = _lib or load_library(), _dtype(x)
+    if ws is None:
+        need = L.dflash2_linear4_workspace_bytes(dt, rows, w.N, w.K)
+        buf = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        scratch = (buf.data_ptr(), need) if need else (None, 0)
+    else:
+        scratch = _scratch(ws, dev)
+    _check("dflash2_linear4", L.dflash2_linear4(xp, dt, rows, xs, w._ref, yp, _dtype(out), ys, *scratch,
+                                                _raw_stream(dev)))
     return out
 
 

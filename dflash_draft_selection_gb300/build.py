@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdflash2.so")
 SOURCES = ["topk16.cu", "verify.cu", "walk.cu", "gate.cu", "lmhead.cu", "conv.cu", "attn.cu", "attn_tc.cu",
-           "attn_tc64.cu", "attn_tc128.cu", "attn_tc256.cu", "kvcache.cu", "linear4.cu", "sample.cu", "api.cu"]
+           "attn_tc64.cu", "attn_tc128.cu", "attn_tc256.cu", "kvcache.cu", "linear4.cu", "linear4_tc.cu",
+           "sample.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -10,6 +10,7 @@ unsigned int read_error_gate(bool clear);
 unsigned int read_error_lmhead(bool clear);
 unsigned int read_error_attn(bool clear);
 unsigned int read_error_append(bool clear);
+unsigned int read_error_linear4(bool clear);
 
 // dflash2_test_hold's setting: read by every launch that the hook holds.
 static std::mutex g_hold_mu;
@@ -49,6 +50,7 @@ extern "C" dflash2_status dflash2_device_error(uint32_t *code, int clear) {
     if (cudaDeviceSynchronize() != cudaSuccess) return DFLASH2_ERR_CUDA;
     *code = dfl::read_error_topk(clear != 0) | dfl::read_error_verify(clear != 0) |
             dfl::read_error_gate(clear != 0) | dfl::read_error_lmhead(clear != 0) |
-            dfl::read_error_attn(clear != 0) | dfl::read_error_append(clear != 0);
+            dfl::read_error_attn(clear != 0) | dfl::read_error_append(clear != 0) |
+            dfl::read_error_linear4(clear != 0);
     return cudaPeekAtLastError() == cudaSuccess ? DFLASH2_OK : DFLASH2_ERR_CUDA;
 }

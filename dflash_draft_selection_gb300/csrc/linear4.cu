@@ -4,8 +4,8 @@
 // TensorRT-LLM issue 18085 and FreeToken PR 857 run this path for targets and
 // drafters whose weights are held in 4 bits; the pages name the formats and give
 // no kernel.
+#include "linear4.cuh"
 #include "tc.cuh"
-#include "weight4.cuh"
 
 namespace dfl {
 
@@ -88,12 +88,7 @@ __global__ void __launch_bounds__(256) k_dequant4(dflash2_weight4 w, void *out, 
 // of x by mma.sync m16n8k16 (x on the n side, 8 rows a tile): the codes go from
 // shared memory into the operand's registers with no second trip.
 //
-//   Codes are operands as they lie.  A bf16 whose exponent field is 0 or 1 is
-//   its low 8 bits times 2^-133 (subnormal, then the first normal binade), so
-//   w & 0x000f000f is a pair of codes times 2^-133 and w & 0x00f000f0 another
-//   pair times 2^-129: five instructions for eight codes.  The rows of x are
-//   scaled by a power of two (largest entry near 2^126) and, at the second
-//   pairs' columns, by 2^-4; both are exact, and are taken back with the scale.
+//   Codes are operands as they lie (linear4.cuh).
 //   A group of columns is summed from zero, so that
 //     acc += scale * (sum of code * x - zero * sum of x)
 //   in f32: products of a code and a bf16 are exact.  f32 rows are split into
@@ -105,7 +100,8 @@ __global__ void __launch_bounds__(256) k_dequant4(dflash2_weight4 w, void *out, 
 constexpr int L4_THREADS = 256;
 constexpr int L4_WARPS = L4_THREADS / 32;
 constexpr int L4_STAGES = 4;
-constexpr int L4_BLOCK = 128;  // columns of a block: 64 bytes of a row
+constexpr int64_t L4_MAX_K = 1 << 17, L4_MAX_ROWS = 1 << 19;
+constexpr int64_t L4_MANY_ROWS = 17, L4_MANY_N = 4096;
 constexpr int L4_SMEM_MAX = 226 * 1024;
 constexpr int L4_SMEM_GOOD = 112 * 1024;  // two CTAs to an SM
 constexpr int L4_WARP_TARGET = 16;        // warps of an SM that have a tile before tiles are shared no further
@@ -128,48 +124,11 @@ struct Lin4 {
     int64_t tiles;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126..127
-// v * 2^e for e in -252..254
-__device__ __forceinline__ float scale2(float v, int e) { return v * pow2f(e / 2) * pow2f(e - e / 2); }
-
-// Eight neighbours of a row of x, entries from `end` on zero.
-template <bool F32X>
-__device__ __forceinline__ void load8(const void *x, int64_t at, int left, bool vec, float (&v)[8]) {
-    if (left >= 8 && vec) {
-        if (F32X) {
-            const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at);
-            const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at + 4);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at);
-            const uint32_t q[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[2 * i] = bf16lo(q[i]), v[2 * i + 1] = bf16hi(q[i]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? load_f(x, F32X ? DFLASH2_F32 : DFLASH2_BF16, at + i) : 0.0f;
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 __device__ __forceinline__ void lds32(uint32_t at, uint32_t (&v)[1]) {
@@ -287,10 +246,8 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
     __syncthreads();
     if (threadIdx.x < nr) {
         const uint32_t m = top[threadIdx.x];
-        // the largest entry ends up below 2^127; odd, so that 133 - e is even
-        int e = m >= 0x7f800000u || m == 0 ? 133 : (252 - static_cast<int>(m >> 23)) | 1;
-        if (e > 251) e = 251;
-        half[threadIdx.x] = m >= 0x7f800000u ? NAN : pow2f((133 - e) / 2);
+        const int e = x_exponent(m);
+        half[threadIdx.x] = x_root(m, e);
         top[threadIdx.x] = static_cast<uint32_t>(e);
     }
     __syncthreads();
@@ -300,13 +257,7 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
         load8<F32X>(p.x, (r0 + r) * p.x_stride + k, static_cast<int>(p.w.K) - k, vec, v);
         const int e = static_cast<int>(top[r]);
         const bool bad = isnan(half[r]);
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (bad) v[j] = 0.0f;
-            sum += scale2(v[j], e - 133);
-            v[j] = scale2(v[j], (j & 1) ? e - 4 : e);
-        }
+        float sum = scale8(v, e, bad);
         constexpr int LANES = 16 >> LG;  // chunks of a group
 #pragma unroll
         for (int d = LANES >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (lane & 16), sum, d);
@@ -549,7 +500,6 @@ static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
     const int nt = (p.rb + 7) / 8;
     const size_t smem = l4_smem(p, nt, parts);
     const int64_t gy = (p.rows + p.rb - 1) / p.rb;
-    if (gy > 65535) return DFLASH2_ERR_UNSUPPORTED;
     const int64_t sets = (p.tiles + (L4_WARPS >> p.kw_log2) - 1) / (L4_WARPS >> p.kw_log2);
     int64_t per_sm = static_cast<int64_t>(L4_SMEM_MAX + 1024) / static_cast<int64_t>(smem + 1024);
     if (per_sm > L4_PER_SM) per_sm = L4_PER_SM;
@@ -590,18 +540,34 @@ extern "C" dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, 
     return after_launch();
 }
 
+// Many rows: the tensor cores' tiles have to be enough for the GPU.
+static bool l4_many(dflash2_dtype dt, int64_t rows, int64_t N) {
+    return dt == DFLASH2_BF16 && rows >= L4_MANY_ROWS && N >= L4_MANY_N;
+}
+
+extern "C" size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K) {
+    if (!dtype_ok(dt) || rows < 1 || N < 1 || K < 1 || K > L4_MAX_K || rows > L4_MAX_ROWS || !l4_many(dt, rows, N)) return 0;
+    return linear4_tc_bytes(rows, K);
+}
+
 extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
                                           const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride,
-                                          dflash2_stream stream) {
+                                          void *ws, size_t ws_bytes, dflash2_stream stream) {
     if (!dtype_ok(dt) || !dtype_ok(y_dt) || (dt == DFLASH2_F32 && y_dt != DFLASH2_F32) || !weight4_ok(w) || rows < 0 ||
         x_stride < w->K || y_stride < w->N)
         return DFLASH2_ERR_INVALID_ARG;
     if (rows == 0 || w->N == 0) return DFLASH2_OK;
     if (!x || !y || !aligned_to(x, dt) || !aligned_to(y, y_dt)) return DFLASH2_ERR_INVALID_ARG;
-    if (w->K > (1 << 17)) return DFLASH2_ERR_UNSUPPORTED;
+    if (w->K > L4_MAX_K || rows > L4_MAX_ROWS) return DFLASH2_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (l4_many(dt, rows, w->N)) {
+        if (!ws || !aligned16(ws)) return DFLASH2_ERR_INVALID_ARG;
+        if (ws_bytes < linear4_tc_bytes(rows, w->K)) return DFLASH2_ERR_WORKSPACE;
+        return linear4_tc(x, rows, x_stride, w, y, y_dt, y_stride, ws, s);
+    }
     Lin4 p = {};
     p.x = x, p.rows = rows, p.x_stride = x_stride, p.w = *w, p.y = y, p.y_stride = y_stride, p.y_dt = y_dt;
     p.G = static_cast<int>(groups_of(w));
     p.gpb_log2 = w->group == 128 ? 0 : w->group == 64 ? 1 : 2;
-    return linear4_mma(p, dt == DFLASH2_F32, reinterpret_cast<cudaStream_t>(stream));
+    return linear4_mma(p, dt == DFLASH2_F32, s);
 }

@@ -1,0 +1,434 @@
+// linear4_tc.cu -- dflash2_linear4 for many rows, on the 5th-generation tensor
+// cores.
+//
+// Weights on the M side (128 rows), x on the N side (up to 128 rows):
+//   part[128 x R] = codes[128 x group] . x'[R x group]^T     per group of columns
+//   acc += scale * (part - zero * sum of x)                  in registers, f32
+// so products are exact whatever the scales, and a result is rounded once.
+//
+// The codes go from global memory through a warp's own copies (cp.async) and
+// its registers into tensor memory, where the MMA takes its A operand: with A in
+// shared memory its 4 KB per step of 16 columns bound the MMA to 56 cycles at R
+// = 64, from tensor memory it takes 32.  x' (scaled and reordered once by a
+// kernel of its own into the workspace) comes by TMA, 128-byte swizzle, with its
+// groups' sums beside it.
+//
+// One CTA per SM walks its tiles of 128 weight rows; a tile's blocks of x rows
+// follow each other, so its codes come from L2 after the first.
+//   warps 0-7    epilogue: a weight row per lane, half of the R columns each
+//   warps 8-15   operand: warps 8-11 the even blocks of 128 columns, 12-15 the odd
+//   warp 16      copies of x', warp 17 the MMAs
+// Tensor memory: 2 accumulators of R columns, 4 blocks of A of 64 columns.
+//
+// Waits are bounded: after a time-out every role stops waiting, the error word
+// is set and the CTA's remaining outputs are NaN.
+#include "host.hpp"
+#include "linear4.cuh"
+#include "tc.cuh"
+
+namespace dfl {
+
+static __device__ unsigned int g_err_linear4;
+
+constexpr int T4_THREADS = 576;
+constexpr int T4_COPY = 16, T4_MMA = 17;
+constexpr int T4_XS = 4;   // stages of x'
+constexpr int T4_AS = 4;   // blocks of A in tensor memory
+constexpr int T4_RING = 4; // blocks ahead of an operand warp
+constexpr int T4_M = 128;
+constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
+
+struct Tc4Shared {
+    uint64_t x_full[T4_XS], x_empty[T4_XS];
+    uint64_t a_full[T4_AS], a_empty[T4_AS];
+    uint64_t d_full[2], d_empty[2];
+    uint64_t done;
+    uint32_t tmem;
+    int abort;
+};
+
+struct Tc4 {
+    dflash2_weight4 w;
+    void *y;
+    int64_t rows, y_stride;
+    dflash2_dtype y_dt;
+    int lg, G, kblocks, rblocks;
+    int64_t tiles;
+    int64_t rows_pad;   // rows of x' in all blocks
+    const float *sums;  // [kblocks << lg][rows_pad]
+    const float *root;  // [rows_pad]
+    const unsigned int *hold;
+    long long hold_cycles;
+};
+
+// ---------------------------------------------------------------- x' ----
+// One CTA per row: x' [rows_pad, kblocks * 128], the groups' sums, the root of the power of two.  Rows past the last are
+// zeros.
+__global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t rows, int64_t x_stride, int K, int lg,
+                                                      int kblocks, int64_t rows_pad, uint16_t *out, float *sums,
+                                                      float *root) {
+    __shared__ uint32_t top;
+    const int64_t r = blockIdx.x;
+    const int chunks = kblocks * (L4_BLOCK / 8), lanes = 16 >> lg;
+    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0;
+    if (threadIdx.x == 0) top = 0;
+    __syncthreads();
+    uint32_t m = 0;
+    if (r < rows)
+        for (int c = threadIdx.x; c < chunks; c += 256) {
+            float v[8];
+            load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        }
+    m = __reduce_max_sync(FULL, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(&top, m);
+    __syncthreads();
+    m = top;
+    const int e = x_exponent(m);
+    const bool bad = m >= 0x7f800000u;
+    if (threadIdx.x == 0) root[r] = x_root(m, e);
+    for (int c = threadIdx.x; c < chunks; c += 256) {  // chunks is a multiple of 16: half-warps stay whole
+        float v[8] = {};
+        if (r < rows) load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
+        float sum = scale8(v, e, bad);
+        for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), sum, d);
+        if ((c & (lanes - 1)) == 0) sums[static_cast<int64_t>(c / lanes) * rows_pad + r] = sum;
+        uint4 o;
+        o.x = bf16_pair(v[0], v[4]), o.y = bf16_pair(v[1], v[5]), o.z = bf16_pair(v[2], v[6]), o.w = bf16_pair(v[3], v[7]);
+        *reinterpret_cast<uint4 *>(out + (r * kblocks * L4_BLOCK + c * 8)) = o;
+    }
+}
+
+// ------------------------------------------------------------- product ----
+__device__ __forceinline__ bool t4_aborted(Tc4Shared &sm) { return *reinterpret_cast<volatile int *>(&sm.abort) != 0; }
+__device__ __forceinline__ void t4_abort(Tc4Shared &sm) {
+    atomicOr(&g_err_linear4, ERR_WAIT_TIMEOUT);
+    *reinterpret_cast<volatile int *>(&sm.abort) = 1;
+}
+// False after a time-out, this one or another role's.
+__device__ __forceinline__ bool t4_wait(Tc4Shared &sm, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!t4_aborted(sm)) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > T4_WAIT) t4_abort(sm);
+    }
+    return false;
+}
+
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void bulk_g2s(void *sdst, const void *gsrc, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(sdst)),
+                 "l"(gsrc), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// RH: half of the block's rows of x, the columns of an epilogue warp.
+template <int RH>
+__global__ void __launch_bounds__(T4_THREADS, 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x, const Tc4 p) {
+    constexpr int R = RH * 2, XB = R * L4_BLOCK * 2;  // bytes of a stage of x'
+    extern __shared__ unsigned char raw[];
+    __shared__ Tc4Shared sm;
+    unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    float *sums = reinterpret_cast<float *>(xs + T4_XS * XB);  // [stage][group of the block][R]
+    const int gpb = 1 << p.lg;
+    unsigned char *rings = reinterpret_cast<unsigned char *>(sums + T4_XS * gpb * R);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < T4_XS; ++i) mbar_init(&sm.x_full[i], 1), mbar_init(&sm.x_empty[i], 9);
+        for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_full[i], 4), mbar_init(&sm.a_empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_empty[i], 8);
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == T4_MMA) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem, tmem_a = tmem + 2 * R;
+    const int64_t per_tile = static_cast<int64_t>(p.rblocks) * p.kblocks;
+    const int64_t mine = p.tiles > blockIdx.x ? (p.tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;  // tiles of this CTA
+    const int64_t total = mine * per_tile;                                                       // and their blocks
+
+    if (warp == T4_COPY) {
+        if (lane == 0) {
+            int64_t i = 0;
+            bool ok = true;
+            if (p.hold != nullptr && !hold_wait(p.hold, p.hold_cycles)) t4_abort(sm), ok = false;
+            for (; ok && i < total; ++i) {
+                const int s = static_cast<int>(i % T4_XS);
+                if (i >= T4_XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / T4_XS - 1) & 1)) break;
+                const int64_t in = i % per_tile;
+                const int rb = static_cast<int>(in / p.kblocks), kb = static_cast<int>(in % p.kblocks);
+                mbar_arrive_expect_tx(&sm.x_full[s], XB + gpb * R * 4);
+                tma_load_2d(xs + s * XB, &tm_x, kb * L4_BLOCK, rb * R, &sm.x_full[s]);
+                tma_load_2d(xs + s * XB + XB / 2, &tm_x, kb * L4_BLOCK + 64, rb * R, &sm.x_full[s]);
+                for (int j = 0; j < gpb; ++j)
+                    bulk_g2s(sums + (s * gpb + j) * R, p.sums + (static_cast<int64_t>(kb) * gpb + j) * p.rows_pad + rb * R,
+                             R * 4, &sm.x_full[s]);
+            }
+            // leave no copy in flight into this CTA's shared memory
+            for (int64_t j = i > T4_XS ? i - T4_XS : 0; j < i; ++j)
+                mbar_wait(&sm.x_full[j % T4_XS], static_cast<uint32_t>(j / T4_XS) & 1, T4_DRAIN);
+        }
+    } else if (warp == T4_MMA) {
+        if (lane == 0) {
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(R >> 3) << 17) |
+                                   (static_cast<uint32_t>(T4_M >> 4) << 24);
+            const int steps = 8 >> p.lg;  // of 16 columns in a group
+            int64_t d = 0;
+            bool ok = true;
+            for (int64_t i = 0; ok && i < total; ++i) {
+                const int s = static_cast<int>(i % T4_XS), sa = static_cast<int>(i % T4_AS);
+                if (!t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1) ||
+                    !t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / T4_AS) & 1))
+                    break;
+                const uint64_t b0 = sw128_desc(xs + s * XB), b1 = sw128_desc(xs + s * XB + XB / 2);
+                for (int j = 0; j < gpb; ++j, ++d) {
+                    if (d >= 2 && !t4_wait(sm, &sm.d_empty[d & 1], static_cast<uint32_t>(d / 2 - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int k = 0; k < steps; ++k) {
+                        const int at = j * steps + k;
+                        mma_bf16_ts(tmem + static_cast<uint32_t>(d & 1) * R, tmem_a + sa * 64 + at * 8,
+                                    (at < 4 ? b0 : b1) + 2 * (at & 3), idesc, k > 0);
+                    }
+                    mma_commit(&sm.d_full[d & 1]);
+                }
+                if (!ok) break;
+                mma_commit(&sm.a_empty[sa]);
+                mma_commit(&sm.x_empty[s]);
+            }
+            // every MMA issued has completed once this commit arrives
+            mma_commit(&sm.done);
+            mbar_wait(&sm.done, 0, T4_DRAIN);
+        }
+    } else if (warp >= 8) {
+        // the operand: 32 weight rows of every second block
+        const int quad = warp & 3, odd = (warp - 8) >> 2;
+        const uint32_t ring = smem_addr(rings) + (warp - 8) * (T4_RING * 2048);
+        const int row_bytes = static_cast<int>((p.w.K + 31) / 32 * 16);
+        // lane l copies chunk l % 4 of rows l / 4 + 8 j
+        int64_t c = odd;
+        auto copy = [&](int stage) {
+            if (c < total) {
+                const int64_t tile = blockIdx.x + c / per_tile * gridDim.x;
+                const int kb = static_cast<int>(c % p.kblocks);
+                const int at = kb * (L4_BLOCK / 2) + (lane & 3) * 16;
+                const bool take = at < row_bytes;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = (lane >> 2) + 8 * j;
+                    int64_t n = tile * T4_M + quad * 32 + r;
+                    n = n < p.w.N ? n : p.w.N - 1;
+                    cp_async16(ring + stage * 2048 + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4),
+                               static_cast<const unsigned char *>(p.w.codes) + n * p.w.code_stride + (take ? at : 0), take);
+                }
+            }
+            cp_async_commit();
+            c += 2;
+        };
+#pragma unroll
+        for (int j = 0; j < T4_RING - 1; ++j) copy(j);
+        int st = 0;
+        for (int64_t i = odd; i < total; i += 2, st = (st + 1) % T4_RING) {
+            copy((st + T4_RING - 1) % T4_RING);
+            cp_async_wait<T4_RING - 1>();
+            __syncwarp();
+            const int sa = static_cast<int>(i % T4_AS);
+            bool ok = true;
+            if (i >= T4_AS) ok = t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(i / T4_AS - 1) & 1);
+            if (!__all_sync(FULL, ok)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t a[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t v[4];
+                    const uint32_t from = ring + st * 2048 + lane * 64 + (((h * 2 + q) ^ ((lane >> 1) & 3)) << 4);
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(from));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t u = v[j] >> 8;
+                        a[q * 16 + j * 4] = v[j] & 0x000f000fu, a[q * 16 + j * 4 + 1] = v[j] & 0x00f000f0u;
+                        a[q * 16 + j * 4 + 2] = u & 0x000f000fu, a[q * 16 + j * 4 + 3] = u & 0x00f000f0u;
+                    }
+                }
+                tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 64 + h * 32, a);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.a_full[sa]);
+        }
+        cp_async_wait<0>();
+    } else {
+        // epilogue
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * RH;
+        int64_t i = 0, d = 0;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+            const int64_t n = tile * T4_M + quad * 32 + lane;
+            const int64_t side0 = (n < p.w.N ? n : p.w.N - 1) * p.w.side_stride;
+            for (int rb = 0; rb < p.rblocks; ++rb) {
+                uint64_t acc[RH / 2];
+#pragma unroll
+                for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
+                float sn = side_at(p.w.scale, p.w.side_dt, side0), zn = p.w.zero ? side_at(p.w.zero, p.w.side_dt, side0) : 8.0f;
+                int gi = 0;
+                for (int kb = 0; ok && kb < p.kblocks; ++kb, ++i) {
+                    const int s = static_cast<int>(i % T4_XS);
+                    ok = __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1));
+                    for (int j = 0; ok && j < gpb; ++j, ++d, ++gi) {
+                        const float sc = gi < p.G ? sn : 0.0f, z = zn;
+                        if (gi + 1 < p.G) {
+                            sn = side_at(p.w.scale, p.w.side_dt, side0 + gi + 1);
+                            if (p.w.zero) zn = side_at(p.w.zero, p.w.side_dt, side0 + gi + 1);
+                        }
+                        const float nz = gi < p.G ? -sc * z : 0.0f;
+                        const uint64_t s2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
+                        const uint64_t z2 = pack2(__float_as_uint(nz), __float_as_uint(nz));
+                        const float *xg = sums + (s * gpb + j) * R + half * RH;
+                        ok = __all_sync(FULL, t4_wait(sm, &sm.d_full[d & 1], static_cast<uint32_t>(d / 2) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        constexpr int CH = RH < 32 ? RH : 32;
+#pragma unroll
+                        for (int c = 0; c < RH; c += CH) {
+                            uint32_t v[CH];
+                            if constexpr (CH == 8) {
+                                tmem_ld8(tm + static_cast<uint32_t>(d & 1) * R, v);
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < CH; q += 16) tmem_ld16_nowait(tm + static_cast<uint32_t>(d & 1) * R + c + q, v + q);
+                            }
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int q = 0; q < CH; q += 4) {
+                                const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(xg + c + q);
+                                const int at = (c + q) / 2;
+                                acc[at] = fma2(z2, x2.x, fma2(s2, pack2(v[q], v[q + 1]), acc[at]));
+                                acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[q + 2], v[q + 3]), acc[at + 1]));
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.d_empty[d & 1]);
+                    }
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
+                }
+                if (n < p.w.N) {
+#pragma unroll
+                    for (int j = 0; j < RH; ++j) {
+                        const int64_t r = static_cast<int64_t>(rb) * R + half * RH + j;
+                        if (r < p.rows) {
+                            const float f = __ldg(p.root + r);
+                            const float v = ok ? __uint_as_float((j & 1) ? hi32(acc[j / 2]) : lo32(acc[j / 2])) * f * f : NAN;
+                            if (p.y_dt == DFLASH2_F32) static_cast<float *>(p.y)[r * p.y_stride + n] = v;
+                            else static_cast<uint16_t *>(p.y)[r * p.y_stride + n] = bf16_bits(v);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == T4_MMA) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host ----
+// Rows of x to a block.
+static int t4_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+static int64_t t4_pad(int64_t rows) { return (rows + t4_rows(rows) - 1) / t4_rows(rows) * t4_rows(rows); }
+static int64_t t4_kpad(int64_t K) { return (K + L4_BLOCK - 1) / L4_BLOCK * L4_BLOCK; }
+
+// Workspace: x', the sums (of the smallest groups), the roots.
+size_t linear4_tc_bytes(int64_t rows, int64_t K) {
+    return static_cast<size_t>(t4_pad(rows)) * (t4_kpad(K) * 2 + t4_kpad(K) / 32 * 4 + 4);
+}
+
+template <int RH>
+static dflash2_status launch_tc4(const CUtensorMap &tm, const Tc4 &p, cudaStream_t s) {
+    auto fn = &k_linear4_tc<RH>;
+    constexpr int R = RH * 2;
+    const size_t smem = 1024 + T4_XS * (R * L4_BLOCK * 2 + (R * 4 << 2)) + 8 * T4_RING * 2048;
+    blocks_per_sm(reinterpret_cast<const void *>(fn), T4_THREADS, smem);  // raises the shared-memory limit once per device
+    const int64_t sms = sm_count();
+    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), T4_THREADS, smem, s>>>(tm, p);
+    return after_launch();
+}
+
+dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
+                          dflash2_dtype y_dt, int64_t y_stride, void *ws, cudaStream_t s) {
+    Tc4 p = {};
+    const int R = t4_rows(rows);
+    const int64_t kp = t4_kpad(w->K);
+    p.w = *w, p.y = y, p.rows = rows, p.y_stride = y_stride, p.y_dt = y_dt;
+    p.lg = w->group == 128 ? 0 : w->group == 64 ? 1 : 2;
+    p.G = static_cast<int>(groups_of(w));
+    p.kblocks = static_cast<int>(kp / L4_BLOCK);
+    p.rows_pad = t4_pad(rows);
+    p.rblocks = static_cast<int>(p.rows_pad / R);
+    p.tiles = (w->N + T4_M - 1) / T4_M;
+    uint16_t *xp = static_cast<uint16_t *>(ws);
+    float *sums = reinterpret_cast<float *>(xp + p.rows_pad * kp);
+    float *root = sums + p.rows_pad * (kp / 32);
+    p.sums = sums, p.root = root;
+    scan_hold(&p.hold, &p.hold_cycles);
+    CUtensorMap tm;
+    if (!make_map_k64(&tm, xp, static_cast<uint64_t>(kp), static_cast<uint64_t>(p.rows_pad), static_cast<uint32_t>(R)))
+        return DFLASH2_ERR_CUDA;
+    k_linear4_rows<<<static_cast<unsigned>(p.rows_pad), 256, 0, s>>>(x, rows, x_stride, static_cast<int>(w->K), p.lg,
+                                                                     p.kblocks, p.rows_pad, xp, sums, root);
+    const dflash2_status st = after_launch();
+    if (st != DFLASH2_OK) return st;
+    return R == 16 ? launch_tc4<8>(tm, p, s) : R == 32 ? launch_tc4<16>(tm, p, s) : R == 64 ? launch_tc4<32>(tm, p, s)
+                                                                                          : launch_tc4<64>(tm, p, s);
+}
+
+unsigned int read_error_linear4(bool clear) {
+    unsigned int v = 0;
+    cudaMemcpyFromSymbol(&v, g_err_linear4, sizeof v);
+    if (clear) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_err_linear4, &z, sizeof z);
+    }
+    return v;
+}
+
+}  // namespace dfl

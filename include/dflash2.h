@@ -619,13 +619,21 @@ dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dty
  * y [rows, y_stride] (y_dt): the first N entries of a row are written.
  *   y_dt is dt, or f32.  A row of x that holds a NaN or an infinity gives a
  *   row of NaN.
+ *   Sums are f32 sums of exact products of codes and of zero points with x;
+ *   entries of x below 2^-130 of their row's largest and scales below 2^-100
+ *   lose bits.
+ * ws: dflash2_linear4_workspace_bytes(dt, rows, N, K) bytes, which is 0 for
+ *   few rows (ws may then be NULL).  It needs no zeros and is left with
+ *   scratch.
  * Errors: INVALID_ARG for a NULL or misaligned pointer (x and y: aligned to
  * their type), rows < 0, x_stride < K, y_stride < N, f32 x with bf16 y, or a
- * record that dflash2_dequant4 refuses.
+ * record that dflash2_dequant4 refuses; UNSUPPORTED for K above 2^17 or rows
+ * above 2^19; WORKSPACE if ws_bytes is too small.
  */
+size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K);
 dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
-                               const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride,
-                               dflash2_stream stream);
+                               const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride, void *ws,
+                               size_t ws_bytes, dflash2_stream stream);
 
 /*
  * dflash2_sample -- one token per row of logits from a given uniform: what a

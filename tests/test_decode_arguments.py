@@ -9,7 +9,7 @@ import torch
 import dflash_draft_selection_gb300 as d2
 from dflash_draft_selection_gb300 import binding
 
-OK, INVALID, UNSUPPORTED = 0, 1, 2
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 4
 RECORD = dict(codes=4096, scale=8192, zero=None, N=40, K=200, code_stride=112, side_stride=2, group=128, side_dt=1)
 
 
@@ -34,7 +34,8 @@ def dequant(w=None, **kw):
 
 
 def linear(w=None, **kw):
-    a = dict(x=4096, dt=1, rows=3, x_stride=200, w=record(**(w or {})), y=4096, y_dt=1, y_stride=40, stream=None)
+    a = dict(x=4096, dt=1, rows=3, x_stride=200, w=record(**(w or {})), y=4096, y_dt=1, y_stride=40, ws=None, ws_bytes=0,
+             stream=None)
     return library().dflash2_linear4(*{**a, **kw}.values())
 
 
@@ -69,9 +70,17 @@ def test_calls_on_records():
                dict(y_stride=39), dict(dt=0, y_dt=1), dict(y_dt=5), dict(x=4098, dt=0, y_dt=0), dict(y=4098, y_dt=0)):
         assert linear(**kw) == INVALID, kw
     assert linear(rows=0, x=None, y=None) == linear(dict(N=0, codes=None, scale=None)) == OK
+    assert linear(dict(K=(1 << 17) + 1, code_stride=1 << 17, side_stride=1 << 17), x_stride=1 << 18) == UNSUPPORTED
+    assert linear(rows=(1 << 19) + 1) == UNSUPPORTED
     L = library()
+    need = L.dflash2_linear4_workspace_bytes
+    assert need(1, 1, 40, 200) == need(0, 512, 151936, 200) == need(1, 0, 40, 200) == need(1, 1 << 20, 1 << 20, 1) == 0
+    big = dict(N=151936)
+    assert need(1, 512, 151936, 200) >= 512 * 256 * 2
+    assert linear(big, rows=512, y_stride=151936) == linear(big, rows=512, y_stride=151936, ws=4104, ws_bytes=1 << 40) == INVALID
+    assert linear(big, rows=512, y_stride=151936, ws=4096, ws_bytes=need(1, 512, 151936, 200) - 1) == WORKSPACE
     assert L.dflash2_quant4(4096, 1, 200, None, None) == L.dflash2_dequant4(None, 4096, 1, 200, None) == INVALID
-    assert L.dflash2_linear4(4096, 1, 3, 200, None, 4096, 1, 40, None) == INVALID
+    assert L.dflash2_linear4(4096, 1, 3, 200, None, 4096, 1, 40, None, 0, None) == INVALID
 
 
 def test_sample():
@@ -123,7 +132,7 @@ def calls(monkeypatch):
 
     class Library:
         def __getattr__(self, name):
-            return lambda *a: made.append(name) or 0
+            return (lambda *a: 0) if name.endswith("_bytes") else lambda *a: made.append(name) or 0
 
     monkeypatch.setattr(binding, "_lib", Library())
     monkeypatch.setattr(binding, "load_library", lambda: binding._lib)

@@ -121,6 +121,19 @@ def test_products_bf16(rows, N, K, group, zero):
     assert d2.device_error() == 0
 
 
+@pytest.mark.parametrize("rows", [17, 31, 32, 33, 64, 65, 128, 129, 300])
+@pytest.mark.parametrize("N,K,group,zero,side", [(4096, 200, 64, True, BF), (4100, 1312, 32, True, F32), (4223, 31, 32, False, BF),
+                                                 (8000, 2560, 128, False, BF), (25000, 520, 128, True, F32)])
+def test_products_of_many_rows(rows, N, K, group, zero, side):
+    """Wide enough for the tensor cores' tiles: one and several to a CTA, the last ones cut."""
+    cuda_or_skip()
+    w = weights(N, K, group, zero, side, seed=N)
+    x = torch.randn(rows, K, generator=gen(rows), device="cuda", dtype=BF)
+    check(d2.linear4(x, w), x, w, "bf16")
+    check(d2.linear4(x, w, dtype=F32), x, w, "f32 out")
+    assert d2.device_error() == 0
+
+
 @pytest.mark.parametrize("rows", [1, 3, 8, 20, 70])
 @pytest.mark.parametrize("N,K,group,zero,side", [(1, 5, 32, False, F32), (129, 264, 32, True, F32), (500, 1024, 128, False, BF),
                                                  (64, 9000, 64, True, BF)])
@@ -149,28 +162,31 @@ def test_long_rows():
         check(d2.linear4(x, w, dtype=F32), x, w, K)
 
 
+@pytest.mark.parametrize("N", [193, 4097])
 @pytest.mark.parametrize("rows", [1, 8, 30, 100])
-def test_strides(rows):
+def test_strides(rows, N):
     """x cut out of a wider matrix at an odd column, outputs into one, weight rows and columns of a larger record."""
     cuda_or_skip()
     for dt in (BF, F32):
-        big = weights(300, 1024, 64, True, seed=2)
-        w = d2.Weight4(big.codes[7:200, 64:384], big.scale[7:200, 2:12], big.zero[7:200, 2:12], K=640, group=64)
+        big = weights(N + 100, 1024, 64, True, seed=2)
+        at = slice(7, 7 + N)
+        w = d2.Weight4(big.codes[at, 64:384], big.scale[at, 2:12], big.zero[at, 2:12], K=640, group=64)
         for a in (0, 1, 8):
             x = torch.randn(rows, 700, generator=gen(rows), device="cuda", dtype=dt)[:, a:a + 640]
-            out = torch.full((rows + 2, 230), 77.0, device="cuda", dtype=dt)
-            got = out[1:-1, 3:196]
+            out = torch.full((rows + 2, N + 37), 77.0, device="cuda", dtype=dt)
+            got = out[1:-1, 3:3 + N]
             assert d2.linear4(x, w, out=got) is got
             check(got, x, w, (rows, dt, a))
             got.fill_(77.0)
             assert (out == 77.0).all()
 
 
+@pytest.mark.parametrize("N", [100, 4096])
 @pytest.mark.parametrize("rows", [1, 8, 24, 100])
-def test_magnitudes(rows):
+def test_magnitudes(rows, N):
     """Rows of every magnitude, with entries far smaller than their largest; a row of zeros; one huge entry."""
     cuda_or_skip()
-    w = weights(100, 512, 128, True, seed=3)
+    w = weights(N, 512, 128, True, seed=3)
     g = gen(9)
     x = torch.randn(rows, 512, generator=g, device="cuda")
     x *= 10.0 ** (torch.arange(rows, device="cuda")[:, None] * 61 % 60 - 30).float()
@@ -183,15 +199,20 @@ def test_magnitudes(rows):
         want = xx.double() @ W.T
         zero = ref.per_column(w.zero, w.K, w.group)
         B = xx.double().abs() @ ((ref.unpack(w).double() + zero) * ref.per_column(w.scale, w.K, w.group).abs()).T
-        assert ((y.double() - want).abs() <= (512 + 16) * 2.0 ** -24 * B + 2.0 ** -149).all()
+        # Rows are scaled so that their largest entry lies in 2^125 .. 2^127 and codes are taken times 2^-133, so a
+        # product's f32 (units of 2^-149) drops entries below 2^-16 of those: 2^-141 of the largest, for each of the
+        # 512 terms, with codes and scales beside them.
+        drop = 512 * 2.0 ** -140 * xx.double().abs().amax(1, keepdim=True) * w.scale.double().abs().amax(1)
+        assert ((y.double() - want).abs() <= (512 + 16) * 2.0 ** -24 * B + drop + 2.0 ** -149).all()
         if rows > 2:
             assert (y[1] == 0).all()
 
 
+@pytest.mark.parametrize("N", [200, 4096])
 @pytest.mark.parametrize("rows", [2, 8, 24, 100])
-def test_a_row_with_nan_or_infinity_is_nan_alone(rows):
+def test_a_row_with_nan_or_infinity_is_nan_alone(rows, N):
     cuda_or_skip()
-    w = weights(200, 384, 128, False, seed=4)
+    w = weights(N, 384, 128, False, seed=4)
     for dt in (BF, F32):
         x = torch.randn(rows, 384, generator=gen(rows), device="cuda", dtype=dt)
         want = d2.linear4(x, w)
@@ -206,8 +227,8 @@ def test_a_row_with_nan_or_infinity_is_nan_alone(rows):
 
 def test_a_nan_scale_is_its_weight_rows_alone():
     cuda_or_skip()
-    for rows in (1, 8, 100):
-        w = weights(200, 384, 128, False, seed=4)
+    for rows, N in ((1, 200), (8, 200), (100, 200), (100, 4096)):
+        w = weights(N, 384, 128, False, seed=4)
         x = torch.randn(rows, 384, generator=gen(rows), device="cuda", dtype=BF)
         want = d2.linear4(x, w)
         w.scale[17, 1] = math.nan
