@@ -15,9 +15,10 @@
 //
 // One CTA per SM walks its tiles of 128 weight rows; a tile's blocks of x rows
 // follow each other, so its codes come from L2 after the first.
-//   warps 0-7    epilogue: a weight row per lane, half of the R columns each
-//   warps 8-15   operand: warps 8-11 the even blocks of 128 columns, 12-15 the odd
-//   warp 16      copies of x', warp 17 the MMAs
+//   8 warps      epilogue: a weight row per lane, half of the R columns each
+//   4 or 8 warps operand: 32 weight rows each; of 8, 4 take the odd blocks of 128
+//                columns
+//   2 warps      copies of x', MMAs
 // Tensor memory: 2 accumulators of R columns, 4 blocks of A of 64 columns.
 //
 // Waits are bounded: after a time-out every role stops waiting, the error word
@@ -30,11 +31,12 @@ namespace dfl {
 
 static __device__ unsigned int g_err_linear4;
 
-constexpr int T4_THREADS = 576;
-constexpr int T4_COPY = 16, T4_MMA = 17;
+// Warps: 8 for the epilogue, the operand's 4 (where the epilogue needs 128 registers a thread) or 8, copies, MMAs.
+constexpr int t4_sets(int rh) { return rh > 32 ? 1 : 2; }
+constexpr int t4_threads(int rh) { return (8 + 4 * t4_sets(rh) + 2) * 32; }
 constexpr int T4_XS = 4;   // stages of x'
 constexpr int T4_AS = 4;   // blocks of A in tensor memory
-constexpr int T4_RING = 4; // blocks ahead of an operand warp
+constexpr int t4_ring(int rh) { return 8 / t4_sets(rh); }  // blocks that an operand warp has room for
 constexpr int T4_M = 128;
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
@@ -52,7 +54,7 @@ struct Tc4 {
     void *y;
     int64_t rows, y_stride;
     dflash2_dtype y_dt;
-    int lg, G, kblocks, rblocks;
+    int lg, G, kblocks, rblocks;  // lg: log2 of the groups in a block
     int64_t tiles;
     int64_t rows_pad;   // rows of x' in all blocks
     const float *sums;  // [kblocks << lg][rows_pad]
@@ -148,15 +150,28 @@ __device__ __forceinline__ void bulk_g2s(void *sdst, const void *gsrc, uint32_t 
                  : "memory");
 }
 
-// RH: half of the block's rows of x, the columns of an epilogue warp.
-template <int RH>
-__global__ void __launch_bounds__(T4_THREADS, 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x, const Tc4 p) {
+// Walks a CTA's blocks: tile by tile, the tile's blocks of x rows, their blocks of columns.
+struct Walk4 {
+    int64_t tile;
+    int rb, kb;
+    __device__ __forceinline__ void next(const Tc4 &p) {
+        if (++kb == p.kblocks) {
+            kb = 0;
+            if (++rb == p.rblocks) rb = 0, tile += gridDim.x;
+        }
+    }
+};
+
+// RH: half of the block's rows of x, the columns of an epilogue warp.  LG: log2 of the groups in a block.
+template <int RH, int LG>
+__global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x, const Tc4 p) {
     constexpr int R = RH * 2, XB = R * L4_BLOCK * 2;  // bytes of a stage of x'
+    constexpr int gpb = 1 << LG, STEPS = 8 >> LG;      // groups of a block, steps of 16 columns in a group
+    constexpr int SETS = t4_sets(RH), RING = t4_ring(RH), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
     extern __shared__ unsigned char raw[];
     __shared__ Tc4Shared sm;
     unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     float *sums = reinterpret_cast<float *>(xs + T4_XS * XB);  // [stage][group of the block][R]
-    const int gpb = 1 << p.lg;
     unsigned char *rings = reinterpret_cast<unsigned char *>(sums + T4_XS * gpb * R);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -173,54 +188,56 @@ __global__ void __launch_bounds__(T4_THREADS, 1) k_linear4_tc(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem, tmem_a = tmem + 2 * R;
-    const int64_t per_tile = static_cast<int64_t>(p.rblocks) * p.kblocks;
-    const int64_t mine = p.tiles > blockIdx.x ? (p.tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;  // tiles of this CTA
-    const int64_t total = mine * per_tile;                                                       // and their blocks
+    const int mine = static_cast<int>((p.tiles - blockIdx.x - 1) / gridDim.x) + 1;  // tiles of this CTA
+    const int total = mine * p.rblocks * p.kblocks;                                 // and their blocks
 
     if (warp == T4_COPY) {
         if (lane == 0) {
-            int64_t i = 0;
+            int i = 0;
             bool ok = true;
             if (p.hold != nullptr && !hold_wait(p.hold, p.hold_cycles)) t4_abort(sm), ok = false;
-            for (; ok && i < total; ++i) {
-                const int s = static_cast<int>(i % T4_XS);
+            Walk4 at{0, 0, 0};
+            for (; ok && i < total; ++i, at.next(p)) {
+                const int s = i % T4_XS;
                 if (i >= T4_XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / T4_XS - 1) & 1)) break;
-                const int64_t in = i % per_tile;
-                const int rb = static_cast<int>(in / p.kblocks), kb = static_cast<int>(in % p.kblocks);
                 mbar_arrive_expect_tx(&sm.x_full[s], XB + gpb * R * 4);
-                tma_load_2d(xs + s * XB, &tm_x, kb * L4_BLOCK, rb * R, &sm.x_full[s]);
-                tma_load_2d(xs + s * XB + XB / 2, &tm_x, kb * L4_BLOCK + 64, rb * R, &sm.x_full[s]);
-                for (int j = 0; j < gpb; ++j)
-                    bulk_g2s(sums + (s * gpb + j) * R, p.sums + (static_cast<int64_t>(kb) * gpb + j) * p.rows_pad + rb * R,
-                             R * 4, &sm.x_full[s]);
+                tma_load_2d(xs + s * XB, &tm_x, at.kb * L4_BLOCK, at.rb * R, &sm.x_full[s]);
+                tma_load_2d(xs + s * XB + XB / 2, &tm_x, at.kb * L4_BLOCK + 64, at.rb * R, &sm.x_full[s]);
+                const float *from = p.sums + static_cast<int64_t>(at.kb) * gpb * p.rows_pad + at.rb * R;
+#pragma unroll
+                for (int j = 0; j < gpb; ++j, from += p.rows_pad)
+                    bulk_g2s(sums + (s * gpb + j) * R, from, R * 4, &sm.x_full[s]);
             }
             // leave no copy in flight into this CTA's shared memory
-            for (int64_t j = i > T4_XS ? i - T4_XS : 0; j < i; ++j)
+            for (int j = i > T4_XS ? i - T4_XS : 0; j < i; ++j)
                 mbar_wait(&sm.x_full[j % T4_XS], static_cast<uint32_t>(j / T4_XS) & 1, T4_DRAIN);
         }
     } else if (warp == T4_MMA) {
         if (lane == 0) {
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(R >> 3) << 17) |
-                                   (static_cast<uint32_t>(T4_M >> 4) << 24);
-            const int steps = 8 >> p.lg;  // of 16 columns in a group
-            int64_t d = 0;
+            constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(R >> 3) << 17) |
+                                       (static_cast<uint32_t>(T4_M >> 4) << 24);
+            const uint64_t x0 = sw128_desc(xs);
+            uint32_t d = 0;
             bool ok = true;
-            for (int64_t i = 0; ok && i < total; ++i) {
-                const int s = static_cast<int>(i % T4_XS), sa = static_cast<int>(i % T4_AS);
+            for (int i = 0; ok && i < total; ++i) {
+                const int s = i % T4_XS, sa = i % T4_AS;
                 if (!t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1) ||
                     !t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / T4_AS) & 1))
                     break;
-                const uint64_t b0 = sw128_desc(xs + s * XB), b1 = sw128_desc(xs + s * XB + XB / 2);
+                const uint64_t b0 = x0 + (s * XB >> 4);
+                const uint32_t a0 = tmem_a + sa * 64;
+#pragma unroll
                 for (int j = 0; j < gpb; ++j, ++d) {
-                    if (d >= 2 && !t4_wait(sm, &sm.d_empty[d & 1], static_cast<uint32_t>(d / 2 - 1) & 1)) {
+                    if (d >= 2 && !t4_wait(sm, &sm.d_empty[d & 1], (d / 2 - 1) & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    for (int k = 0; k < steps; ++k) {
-                        const int at = j * steps + k;
-                        mma_bf16_ts(tmem + static_cast<uint32_t>(d & 1) * R, tmem_a + sa * 64 + at * 8,
-                                    (at < 4 ? b0 : b1) + 2 * (at & 3), idesc, k > 0);
+                    const uint32_t to = tmem + (d & 1) * R;
+#pragma unroll
+                    for (int k = 0; k < STEPS; ++k) {
+                        const int at = j * STEPS + k;  // 16 columns: 32 bytes of x', 8 columns of tensor memory
+                        mma_bf16_ts(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc, k > 0);
                     }
                     mma_commit(&sm.d_full[d & 1]);
                 }
@@ -233,38 +250,48 @@ __global__ void __launch_bounds__(T4_THREADS, 1) k_linear4_tc(const __grid_const
             mbar_wait(&sm.done, 0, T4_DRAIN);
         }
     } else if (warp >= 8) {
-        // the operand: 32 weight rows of every second block
+        // the operand: 32 weight rows of every block, or of every second one
         const int quad = warp & 3, odd = (warp - 8) >> 2;
-        const uint32_t ring = smem_addr(rings) + (warp - 8) * (T4_RING * 2048);
+        const uint32_t ring = smem_addr(rings) + (warp - 8) * (RING * 2048);
         const int row_bytes = static_cast<int>((p.w.K + 31) / 32 * 16);
         // lane l copies chunk l % 4 of rows l / 4 + 8 j
-        int64_t c = odd;
+        Walk4 at{blockIdx.x, 0, 0};
+        const unsigned char *from[4];
+        auto rows_of = [&]() {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t n = at.tile * T4_M + quad * 32 + (lane >> 2) + 8 * j;
+                from[j] = static_cast<const unsigned char *>(p.w.codes) + (n < p.w.N ? n : p.w.N - 1) * p.w.code_stride + (lane & 3) * 16;
+            }
+        };
+        rows_of();
+        auto step = [&]() {
+            const int64_t was = at.tile;
+            at.next(p);
+            if (at.tile != was) rows_of();
+        };
+        if (odd) step();
+        int c = odd;
+        const uint32_t to = ring + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
         auto copy = [&](int stage) {
             if (c < total) {
-                const int64_t tile = blockIdx.x + c / per_tile * gridDim.x;
-                const int kb = static_cast<int>(c % p.kblocks);
-                const int at = kb * (L4_BLOCK / 2) + (lane & 3) * 16;
-                const bool take = at < row_bytes;
+                const int off = at.kb * (L4_BLOCK / 2);
+                const bool take = off + (lane & 3) * 16 < row_bytes;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = (lane >> 2) + 8 * j;
-                    int64_t n = tile * T4_M + quad * 32 + r;
-                    n = n < p.w.N ? n : p.w.N - 1;
-                    cp_async16(ring + stage * 2048 + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4),
-                               static_cast<const unsigned char *>(p.w.codes) + n * p.w.code_stride + (take ? at : 0), take);
-                }
+                for (int j = 0; j < 4; ++j) cp_async16(to + stage * 2048 + j * 512, from[j] + (take ? off : 0), take);
+                for (int j = 0; j < SETS; ++j) step();
             }
             cp_async_commit();
-            c += 2;
+            c += SETS;
         };
 #pragma unroll
-        for (int j = 0; j < T4_RING - 1; ++j) copy(j);
+        for (int j = 0; j < RING - 1; ++j) copy(j);
         int st = 0;
-        for (int64_t i = odd; i < total; i += 2, st = (st + 1) % T4_RING) {
-            copy((st + T4_RING - 1) % T4_RING);
-            cp_async_wait<T4_RING - 1>();
+        for (int i = odd; i < total; i += SETS, st = (st + 1) % RING) {
+            copy((st + RING - 1) % RING);
+            cp_async_wait<RING - 1>();
             __syncwarp();
-            const int sa = static_cast<int>(i % T4_AS);
+            const int sa = i % T4_AS;
             bool ok = true;
             if (i >= T4_AS) ok = t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(i / T4_AS - 1) & 1);
             if (!__all_sync(FULL, ok)) break;
@@ -296,7 +323,8 @@ __global__ void __launch_bounds__(T4_THREADS, 1) k_linear4_tc(const __grid_const
         // epilogue
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * RH;
-        int64_t i = 0, d = 0;
+        int i = 0;
+        uint32_t d = 0;
         bool ok = true;
         for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
             const int64_t n = tile * T4_M + quad * 32 + lane;
@@ -305,60 +333,66 @@ __global__ void __launch_bounds__(T4_THREADS, 1) k_linear4_tc(const __grid_const
                 uint64_t acc[RH / 2];
 #pragma unroll
                 for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
-                float sn = side_at(p.w.scale, p.w.side_dt, side0), zn = p.w.zero ? side_at(p.w.zero, p.w.side_dt, side0) : 8.0f;
-                int gi = 0;
-                for (int kb = 0; ok && kb < p.kblocks; ++kb, ++i) {
-                    const int s = static_cast<int>(i % T4_XS);
-                    ok = __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1));
-                    for (int j = 0; ok && j < gpb; ++j, ++d, ++gi) {
-                        const float sc = gi < p.G ? sn : 0.0f, z = zn;
-                        if (gi + 1 < p.G) {
-                            sn = side_at(p.w.scale, p.w.side_dt, side0 + gi + 1);
-                            if (p.w.zero) zn = side_at(p.w.zero, p.w.side_dt, side0 + gi + 1);
-                        }
-                        const float nz = gi < p.G ? -sc * z : 0.0f;
-                        const uint64_t s2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
+                // scales and zero points, four groups at a time, four ahead
+                float sn[4], zn[4], sc[4], zc[4];
+                auto sides = [&](int gi) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        sc[q] = sn[q], zc[q] = zn[q];
+                        sn[q] = gi + q < p.G ? side_at(p.w.scale, p.w.side_dt, side0 + gi + q) : 0.0f;
+                        zn[q] = p.w.zero && gi + q < p.G ? side_at(p.w.zero, p.w.side_dt, side0 + gi + q) : 8.0f;
+                    }
+                };
+                sides(0);
+                for (int kb = 0; ok && kb < p.kblocks; kb += 4 / gpb) {
+                    sides((kb + 4 / gpb) * gpb);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {  // group q of these four
+                        if (kb + q / gpb >= p.kblocks) break;
+                        const int s = i % T4_XS;
+                        if (q % gpb == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1));
+                        const float nz = -sc[q] * zc[q];
+                        const uint64_t s2 = pack2(__float_as_uint(sc[q]), __float_as_uint(sc[q]));
                         const uint64_t z2 = pack2(__float_as_uint(nz), __float_as_uint(nz));
-                        const float *xg = sums + (s * gpb + j) * R + half * RH;
-                        ok = __all_sync(FULL, t4_wait(sm, &sm.d_full[d & 1], static_cast<uint32_t>(d / 2) & 1));
+                        const float *xg = sums + (s * gpb + q % gpb) * R + half * RH;
+                        ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[d & 1], (d / 2) & 1));
                         if (!ok) break;
                         tc_fence_after();
-                        constexpr int CH = RH < 32 ? RH : 32;
+                        constexpr int CH = RH < 16 ? RH : 16;
 #pragma unroll
                         for (int c = 0; c < RH; c += CH) {
                             uint32_t v[CH];
-                            if constexpr (CH == 8) {
-                                tmem_ld8(tm + static_cast<uint32_t>(d & 1) * R, v);
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < CH; q += 16) tmem_ld16_nowait(tm + static_cast<uint32_t>(d & 1) * R + c + q, v + q);
-                            }
+                            if constexpr (CH == 8) tmem_ld8(tm + (d & 1) * R, v);
+                            else tmem_ld16_nowait(tm + (d & 1) * R + c, v);
                             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                            for (int q = 0; q < CH; q += 4) {
-                                const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(xg + c + q);
-                                const int at = (c + q) / 2;
-                                acc[at] = fma2(z2, x2.x, fma2(s2, pack2(v[q], v[q + 1]), acc[at]));
-                                acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[q + 2], v[q + 3]), acc[at + 1]));
+                            for (int k = 0; k < CH; k += 4) {
+                                const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(xg + c + k);
+                                const int at = (c + k) / 2;
+                                acc[at] = fma2(z2, x2.x, fma2(s2, pack2(v[k], v[k + 1]), acc[at]));
+                                acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[k + 2], v[k + 3]), acc[at + 1]));
                             }
                         }
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.d_empty[d & 1]);
-                    }
-                    __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
-                }
-                if (n < p.w.N) {
-#pragma unroll
-                    for (int j = 0; j < RH; ++j) {
-                        const int64_t r = static_cast<int64_t>(rb) * R + half * RH + j;
-                        if (r < p.rows) {
-                            const float f = __ldg(p.root + r);
-                            const float v = ok ? __uint_as_float((j & 1) ? hi32(acc[j / 2]) : lo32(acc[j / 2])) * f * f : NAN;
-                            if (p.y_dt == DFLASH2_F32) static_cast<float *>(p.y)[r * p.y_stride + n] = v;
-                            else static_cast<uint16_t *>(p.y)[r * p.y_stride + n] = bf16_bits(v);
+                        ++d;
+                        if (q % gpb == gpb - 1) {
+                            if (lane == 0) mbar_arrive(&sm.x_empty[s]);
+                            ++i;
                         }
+                    }
+                }
+                // the roots of columns l and 32 + l
+                const int64_t r0 = static_cast<int64_t>(rb) * R + half * RH;
+                const float f0 = lane < RH ? p.root[r0 + lane] : 0.0f, f1 = RH > 32 ? p.root[r0 + 32 + lane] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < RH; ++j) {
+                    const float f = __shfl_sync(FULL, j < 32 ? f0 : f1, j & 31);
+                    if (r0 + j < p.rows && n < p.w.N) {
+                        const float v = ok ? __uint_as_float((j & 1) ? hi32(acc[j / 2]) : lo32(acc[j / 2])) * f * f : NAN;
+                        if (p.y_dt == DFLASH2_F32) static_cast<float *>(p.y)[(r0 + j) * p.y_stride + n] = v;
+                        else static_cast<uint16_t *>(p.y)[(r0 + j) * p.y_stride + n] = bf16_bits(v);
                     }
                 }
                 __syncwarp();
@@ -382,19 +416,29 @@ size_t linear4_tc_bytes(int64_t rows, int64_t K) {
     return static_cast<size_t>(t4_pad(rows)) * (t4_kpad(K) * 2 + t4_kpad(K) / 32 * 4 + 4);
 }
 
-template <int RH>
+template <int RH, int LG>
 static dflash2_status launch_tc4(const CUtensorMap &tm, const Tc4 &p, cudaStream_t s) {
-    auto fn = &k_linear4_tc<RH>;
+    auto fn = &k_linear4_tc<RH, LG>;
     constexpr int R = RH * 2;
-    const size_t smem = 1024 + T4_XS * (R * L4_BLOCK * 2 + (R * 4 << 2)) + 8 * T4_RING * 2048;
-    blocks_per_sm(reinterpret_cast<const void *>(fn), T4_THREADS, smem);  // raises the shared-memory limit once per device
+    const size_t smem = 1024 + T4_XS * (R * L4_BLOCK * 2 + (R * 4 << LG)) + 4 * t4_sets(RH) * t4_ring(RH) * 2048;
+    blocks_per_sm(reinterpret_cast<const void *>(fn), t4_threads(RH), smem);  // raises the shared-memory limit once per device
     const int64_t sms = sm_count();
-    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), T4_THREADS, smem, s>>>(tm, p);
+    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), t4_threads(RH), smem, s>>>(tm, p);
     return after_launch();
+}
+
+template <int RH>
+static dflash2_status launch_tc4_groups(const CUtensorMap &tm, const Tc4 &p, cudaStream_t s) {
+    if (p.lg == 0) return launch_tc4<RH, 0>(tm, p, s);
+    if (p.lg == 1) return launch_tc4<RH, 1>(tm, p, s);
+    return launch_tc4<RH, 2>(tm, p, s);
 }
 
 dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
                           dflash2_dtype y_dt, int64_t y_stride, void *ws, cudaStream_t s) {
+    // a CTA's blocks are counted in 31 bits
+    if ((w->N / T4_M / sm_count() + 1) * (t4_pad(rows) / t4_rows(rows)) * (t4_kpad(w->K) / L4_BLOCK) > (1 << 30))
+        return DFLASH2_ERR_UNSUPPORTED;
     Tc4 p = {};
     const int R = t4_rows(rows);
     const int64_t kp = t4_kpad(w->K);
@@ -417,8 +461,8 @@ dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const d
                                                                      p.kblocks, p.rows_pad, xp, sums, root);
     const dflash2_status st = after_launch();
     if (st != DFLASH2_OK) return st;
-    return R == 16 ? launch_tc4<8>(tm, p, s) : R == 32 ? launch_tc4<16>(tm, p, s) : R == 64 ? launch_tc4<32>(tm, p, s)
-                                                                                          : launch_tc4<64>(tm, p, s);
+    return R == 16 ? launch_tc4_groups<8>(tm, p, s) : R == 32 ? launch_tc4_groups<16>(tm, p, s) : R == 64 ? launch_tc4_groups<32>(tm, p, s)
+                                                                                          : launch_tc4_groups<64>(tm, p, s);
 }
 
 unsigned int read_error_linear4(bool clear) {
