@@ -16,10 +16,10 @@
 // One CTA per SM walks its tiles of 128 weight rows; a tile's blocks of x rows
 // follow each other, so its codes come from L2 after the first.
 //   8 warps      epilogue: a weight row per lane, half of the R columns each
-//   4 or 8 warps operand: 32 weight rows each; of 8, 4 take the odd blocks of 128
-//                columns
+//   4 or 8 warps operand and scales: 32 weight rows each; of 8, 4 take the odd blocks
+//                of 128 columns
 //   2 warps      copies of x', MMAs
-// Tensor memory: 2 accumulators of R columns, 4 blocks of A of 64 columns.
+// Tensor memory: 4 accumulators of R columns (2 of 128), 4 blocks of A of 64 columns.
 //
 // Waits are bounded: after a time-out every role stops waiting, the error word
 // is set and the CTA's remaining outputs are NaN.
@@ -37,13 +37,14 @@ constexpr int t4_threads(int rh) { return (8 + 4 * t4_sets(rh) + 2) * 32; }
 constexpr int T4_XS = 4;   // stages of x'
 constexpr int T4_AS = 4;   // blocks of A in tensor memory
 constexpr int t4_ring(int rh) { return 8 / t4_sets(rh); }  // blocks that an operand warp has room for
+constexpr int T4_DS = 4;   // accumulators, at most: 2 of 128 columns
 constexpr int T4_M = 128;
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
 struct Tc4Shared {
     uint64_t x_full[T4_XS], x_empty[T4_XS];
     uint64_t a_full[T4_AS], a_empty[T4_AS];
-    uint64_t d_full[2], d_empty[2];
+    uint64_t d_full[T4_DS], d_empty[T4_DS];
     uint64_t done;
     uint32_t tmem;
     int abort;
@@ -119,14 +120,23 @@ __device__ __forceinline__ bool t4_wait(Tc4Shared &sm, uint64_t *bar, uint32_t p
     return false;
 }
 
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            bool accumulate) {
+template <bool ACCUMULATE>
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
         : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -172,12 +182,13 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
     __shared__ Tc4Shared sm;
     unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     float *sums = reinterpret_cast<float *>(xs + T4_XS * XB);  // [stage][group of the block][R]
-    unsigned char *rings = reinterpret_cast<unsigned char *>(sums + T4_XS * gpb * R);
+    float2 *sides = reinterpret_cast<float2 *>(sums + T4_XS * gpb * R);  // [block of A][group][weight row]: scale, -scale * zero
+    unsigned char *rings = reinterpret_cast<unsigned char *>(sides + T4_AS * gpb * T4_M);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < T4_XS; ++i) mbar_init(&sm.x_full[i], 1), mbar_init(&sm.x_empty[i], 9);
-        for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_full[i], 4), mbar_init(&sm.a_empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_empty[i], 8);
+        for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_full[i], 4), mbar_init(&sm.a_empty[i], 9);
+        for (int i = 0; i < T4_DS; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_empty[i], 8);
         mbar_init(&sm.done, 1);
         sm.abort = 0;
         fence_barrier_init();
@@ -187,7 +198,8 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem, tmem_a = tmem + 2 * R;
+    constexpr uint32_t DS = R > 64 ? 2 : 4;
+    const uint32_t tmem = sm.tmem, tmem_a = tmem + DS * R;
     const int mine = static_cast<int>((p.tiles - blockIdx.x - 1) / gridDim.x) + 1;  // tiles of this CTA
     const int total = mine * p.rblocks * p.kblocks;                                 // and their blocks
 
@@ -213,42 +225,48 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                 mbar_wait(&sm.x_full[j % T4_XS], static_cast<uint32_t>(j / T4_XS) & 1, T4_DRAIN);
         }
     } else if (warp == T4_MMA) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(R >> 3) << 17) |
-                                       (static_cast<uint32_t>(T4_M >> 4) << 24);
-            const uint64_t x0 = sw128_desc(xs);
-            uint32_t d = 0;
-            bool ok = true;
-            for (int i = 0; ok && i < total; ++i) {
-                const int s = i % T4_XS, sa = i % T4_AS;
-                if (!t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1) ||
-                    !t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / T4_AS) & 1))
-                    break;
-                const uint64_t b0 = x0 + (s * XB >> 4);
-                const uint32_t a0 = tmem_a + sa * 64;
+        // The whole warp walks, so that addresses stay in uniform registers; one thread issues.
+        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(R >> 3) << 17) |
+                                   (static_cast<uint32_t>(T4_M >> 4) << 24);
+        const uint64_t x0 = sw128_desc(xs);
+        const bool leader = elect_one();
+        uint32_t d = 0;
+        bool ok = true;
+        for (int i = 0; ok && i < total; ++i) {
+            const int s = i % T4_XS, sa = i % T4_AS;
+            ok = t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1) &&
+                 t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / T4_AS) & 1);
+            if (!__all_sync(FULL, ok)) break;
+            const uint64_t b0 = x0 + (s * XB >> 4);
+            const uint32_t a0 = tmem_a + sa * 64;
 #pragma unroll
-                for (int j = 0; j < gpb; ++j, ++d) {
-                    if (d >= 2 && !t4_wait(sm, &sm.d_empty[d & 1], (d / 2 - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t to = tmem + (d & 1) * R;
+            for (int j = 0; j < gpb; ++j, ++d) {
+                if (d >= DS) ok = __all_sync(FULL, t4_wait(sm, &sm.d_empty[d % DS], (d / DS - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t to = tmem + (d % DS) * R;
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < STEPS; ++k) {
                         const int at = j * STEPS + k;  // 16 columns: 32 bytes of x', 8 columns of tensor memory
-                        mma_bf16_ts(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc, k > 0);
+                        if (k == 0) mma_bf16_ts<false>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
+                        else mma_bf16_ts<true>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
                     }
-                    mma_commit(&sm.d_full[d & 1]);
+                    mma_commit(&sm.d_full[d % DS]);
                 }
-                if (!ok) break;
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (leader) {
                 mma_commit(&sm.a_empty[sa]);
                 mma_commit(&sm.x_empty[s]);
             }
-            // every MMA issued has completed once this commit arrives
-            mma_commit(&sm.done);
-            mbar_wait(&sm.done, 0, T4_DRAIN);
+            __syncwarp();
         }
+        // every MMA issued has completed once this commit arrives
+        if (leader) mma_commit(&sm.done);
+        __syncwarp();
+        mbar_wait(&sm.done, 0, T4_DRAIN);
     } else if (warp >= 8) {
         // the operand: 32 weight rows of every block, or of every second one
         const int quad = warp & 3, odd = (warp - 8) >> 2;
@@ -273,6 +291,33 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         if (odd) step();
         int c = odd;
         const uint32_t to = ring + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+        // scales and zero points of lane l's own row, two of the warp's blocks ahead
+        Walk4 sw{blockIdx.x, 0, 0};
+        int64_t side0 = 0;
+        float sr[2][gpb], zr[2][gpb];
+        auto side_row = [&]() {
+            const int64_t n = sw.tile * T4_M + quad * 32 + lane;
+            side0 = (n < p.w.N ? n : p.w.N - 1) * p.w.side_stride;
+        };
+        auto side_step = [&]() {
+            const int64_t was = sw.tile;
+            sw.next(p);
+            if (sw.tile != was) side_row();
+        };
+        auto load_sides = [&](int slot) {
+            if (sw.tile < p.tiles) {
+#pragma unroll
+                for (int j = 0; j < gpb; ++j) {
+                    const int gi = sw.kb * gpb + j;
+                    sr[slot][j] = gi < p.G ? side_at(p.w.scale, p.w.side_dt, side0 + gi) : 0.0f;
+                    zr[slot][j] = p.w.zero && gi < p.G ? side_at(p.w.zero, p.w.side_dt, side0 + gi) : 8.0f;
+                }
+                for (int j = 0; j < SETS; ++j) side_step();
+            }
+        };
+        side_row();
+        if (odd) side_step();
+        load_sides(0), load_sides(1);
         auto copy = [&](int stage) {
             if (c < total) {
                 const int off = at.kb * (L4_BLOCK / 2);
@@ -286,37 +331,51 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         };
 #pragma unroll
         for (int j = 0; j < RING - 1; ++j) copy(j);
-        int st = 0;
-        for (int i = odd; i < total; i += SETS, st = (st + 1) % RING) {
-            copy((st + RING - 1) % RING);
-            cp_async_wait<RING - 1>();
-            __syncwarp();
-            const int sa = i % T4_AS;
-            bool ok = true;
-            if (i >= T4_AS) ok = t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(i / T4_AS - 1) & 1);
-            if (!__all_sync(FULL, ok)) break;
-            tc_fence_after();
+        for (int i0 = odd, go = 1; go && i0 < total; i0 += SETS * RING) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t a[32];
+            for (int st = 0; st < RING; ++st) {
+                const int i = i0 + st * SETS;
+                if (i >= total) break;
+                float s_now[gpb], z_now[gpb];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t v[4];
-                    const uint32_t from = ring + st * 2048 + lane * 64 + (((h * 2 + q) ^ ((lane >> 1) & 3)) << 4);
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(from));
+                for (int j = 0; j < gpb; ++j) s_now[j] = sr[st & 1][j], z_now[j] = zr[st & 1][j];
+                load_sides(st & 1);
+                copy((st + RING - 1) % RING);
+                cp_async_wait<RING - 1>();
+                __syncwarp();
+                const int sa = i % T4_AS;
+                uint32_t v[4][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t u = v[j] >> 8;
-                        a[q * 16 + j * 4] = v[j] & 0x000f000fu, a[q * 16 + j * 4 + 1] = v[j] & 0x00f000f0u;
-                        a[q * 16 + j * 4 + 2] = u & 0x000f000fu, a[q * 16 + j * 4 + 3] = u & 0x00f000f0u;
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t at_q = ring + st * 2048 + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[q][0]), "=r"(v[q][1]), "=r"(v[q][2]), "=r"(v[q][3]) : "r"(at_q));
                 }
-                tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 64 + h * 32, a);
+                bool ok = true;
+                if (i >= T4_AS) ok = t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(i / T4_AS - 1) & 1);
+                if (!__all_sync(FULL, ok)) {
+                    go = 0;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a[32];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint32_t w = v[h * 2 + q / 4][q % 4], u = w >> 8;
+                        a[q * 4] = w & 0x000f000fu, a[q * 4 + 1] = w & 0x00f000f0u;
+                        a[q * 4 + 2] = u & 0x000f000fu, a[q * 4 + 3] = u & 0x00f000f0u;
+                    }
+                    tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 64 + h * 32, a);
+                }
+#pragma unroll
+                for (int j = 0; j < gpb; ++j)
+                    sides[(sa * gpb + j) * T4_M + quad * 32 + lane] = make_float2(s_now[j], s_now[j] == 0.0f && z_now[j] == 8.0f ? 0.0f : -s_now[j] * z_now[j]);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.a_full[sa]);
             }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.a_full[sa]);
         }
         cp_async_wait<0>();
     } else {
@@ -328,42 +387,35 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         bool ok = true;
         for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
             const int64_t n = tile * T4_M + quad * 32 + lane;
-            const int64_t side0 = (n < p.w.N ? n : p.w.N - 1) * p.w.side_stride;
             for (int rb = 0; rb < p.rblocks; ++rb) {
                 uint64_t acc[RH / 2];
 #pragma unroll
                 for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
-                // scales and zero points, four groups at a time, four ahead
-                float sn[4], zn[4], sc[4], zc[4];
-                auto sides = [&](int gi) {
+                for (int kb = 0; ok && kb < p.kblocks; ++kb, ++i) {
+                    const int s = i % T4_XS, sa = i % T4_AS;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        sc[q] = sn[q], zc[q] = zn[q];
-                        sn[q] = gi + q < p.G ? side_at(p.w.scale, p.w.side_dt, side0 + gi + q) : 0.0f;
-                        zn[q] = p.w.zero && gi + q < p.G ? side_at(p.w.zero, p.w.side_dt, side0 + gi + q) : 8.0f;
-                    }
-                };
-                sides(0);
-                for (int kb = 0; ok && kb < p.kblocks; kb += 4 / gpb) {
-                    sides((kb + 4 / gpb) * gpb);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // group q of these four
-                        if (kb + q / gpb >= p.kblocks) break;
-                        const int s = i % T4_XS;
-                        if (q % gpb == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1));
-                        const float nz = -sc[q] * zc[q];
-                        const uint64_t s2 = pack2(__float_as_uint(sc[q]), __float_as_uint(sc[q]));
-                        const uint64_t z2 = pack2(__float_as_uint(nz), __float_as_uint(nz));
-                        const float *xg = sums + (s * gpb + q % gpb) * R + half * RH;
-                        ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[d & 1], (d / 2) & 1));
+                    for (int j = 0; j < gpb; ++j, ++d) {
+                        ok = ok && t4_wait(sm, &sm.d_full[d % DS], (d / DS) & 1);
+                        // complete by then; waited for so that what was written beside them is seen
+                        if (j == 0) ok = ok && t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1) &&
+                                         t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / T4_AS) & 1);
+                        ok = __all_sync(FULL, ok);
                         if (!ok) break;
                         tc_fence_after();
-                        constexpr int CH = RH < 16 ? RH : 16;
+                        const float2 side = sides[(sa * gpb + j) * T4_M + quad * 32 + lane];
+                        const uint64_t s2 = pack2(__float_as_uint(side.x), __float_as_uint(side.x));
+                        const uint64_t z2 = pack2(__float_as_uint(side.y), __float_as_uint(side.y));
+                        const float *xg = sums + (s * gpb + j) * R + half * RH;
+                        constexpr int CH = RH < 16 ? RH : RH < 32 ? 16 : 32;
 #pragma unroll
                         for (int c = 0; c < RH; c += CH) {
                             uint32_t v[CH];
-                            if constexpr (CH == 8) tmem_ld8(tm + (d & 1) * R, v);
-                            else tmem_ld16_nowait(tm + (d & 1) * R + c, v);
+                            if constexpr (CH == 8) {
+                                tmem_ld8(tm + (d % DS) * R, v);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < CH; k += 16) tmem_ld16_nowait(tm + (d % DS) * R + c + k, v + k);
+                            }
                             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                             for (int k = 0; k < CH; k += 4) {
@@ -375,13 +427,9 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                         }
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.d_empty[d & 1]);
-                        ++d;
-                        if (q % gpb == gpb - 1) {
-                            if (lane == 0) mbar_arrive(&sm.x_empty[s]);
-                            ++i;
-                        }
+                        if (lane == 0) mbar_arrive(&sm.d_empty[d % DS]);
                     }
+                    if (ok && lane == 0) mbar_arrive(&sm.x_empty[s]), mbar_arrive(&sm.a_empty[sa]);
                 }
                 // the roots of columns l and 32 + l
                 const int64_t r0 = static_cast<int64_t>(rb) * R + half * RH;
@@ -420,7 +468,7 @@ template <int RH, int LG>
 static dflash2_status launch_tc4(const CUtensorMap &tm, const Tc4 &p, cudaStream_t s) {
     auto fn = &k_linear4_tc<RH, LG>;
     constexpr int R = RH * 2;
-    const size_t smem = 1024 + T4_XS * (R * L4_BLOCK * 2 + (R * 4 << LG)) + 4 * t4_sets(RH) * t4_ring(RH) * 2048;
+    const size_t smem = 1024 + T4_XS * (R * L4_BLOCK * 2 + (R * 4 << LG)) + (T4_AS * T4_M * 8 << LG) + 4 * t4_sets(RH) * t4_ring(RH) * 2048;
     blocks_per_sm(reinterpret_cast<const void *>(fn), t4_threads(RH), smem);  // raises the shared-memory limit once per device
     const int64_t sms = sm_count();
     fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), t4_threads(RH), smem, s>>>(tm, p);
