@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
     int64_t s_tile = first;
     int s_left = 0, s_gi = 0;
     int64_t s_at0 = 0, s_at1 = 0;
-    float sn0 = 0.0f, sn1 = 0.0f, zn0 = 8.0f, zn1 = 8.0f;
+    uint32_t sn0 = 0, sn1 = 0, zn0 = 0, zn1 = 0;
     auto sides = [&]() {
         if (s_left == 0 && s_tile < p.tiles && count) {
             int64_t n0 = s_tile * 16 + g, n1 = n0 + 8;
@@ -212,12 +212,10 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
             s_tile += step;
         }
         if (s_left) {
-            const bool in = s_gi < p.G;
-            sn0 = in ? side_at(p.w.scale, p.w.side_dt, s_at0) : 0.0f;
-            sn1 = in ? side_at(p.w.scale, p.w.side_dt, s_at1) : 0.0f;
-            if (p.w.zero) {
-                zn0 = in ? side_at(p.w.zero, p.w.side_dt, s_at0) : 8.0f;
-                zn1 = in ? side_at(p.w.zero, p.w.side_dt, s_at1) : 8.0f;
+            sn0 = sn1 = zn0 = zn1 = 0;
+            if (s_gi < p.G) {
+                sn0 = side_bits(p.w.scale, p.w.side_dt, s_at0), sn1 = side_bits(p.w.scale, p.w.side_dt, s_at1);
+                if (p.w.zero) zn0 = side_bits(p.w.zero, p.w.side_dt, s_at0), zn1 = side_bits(p.w.zero, p.w.side_dt, s_at1);
             }
             s_gi += 4, s_at0 += 4, s_at1 += 4, --s_left;
         }
@@ -315,7 +313,8 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
             for (int i = 0; i < count; ++i, xo += L4_BLOCK * 2) {
                 copy(s_next);
                 if (LG == 2 || (i & (WPG - 1)) == 0) {
-                    sd0 = sn0, sd1 = sn1, zr0 = zn0, zr1 = zn1;
+                    sd0 = side_of(sn0, p.w.side_dt), sd1 = side_of(sn1, p.w.side_dt);
+                    if (p.w.zero) zr0 = side_of(zn0, p.w.side_dt), zr1 = side_of(zn1, p.w.side_dt);
                     sides();
                 }
                 cp_async_wait<L4_STAGES - 1>();

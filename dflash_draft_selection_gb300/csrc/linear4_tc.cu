@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         // scales and zero points of lane l's own row, two of the warp's blocks ahead
         Walk4 sw{blockIdx.x, 0, 0};
         int64_t side0 = 0;
-        float sr[2][gpb], zr[2][gpb];
+        uint32_t sr[2][gpb], zr[2][gpb];
         auto side_row = [&]() {
             const int64_t n = sw.tile * T4_M + quad * 32 + lane;
             side0 = (n < p.w.N ? n : p.w.N - 1) * p.w.side_stride;
@@ -309,8 +309,11 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
 #pragma unroll
                 for (int j = 0; j < gpb; ++j) {
                     const int gi = sw.kb * gpb + j;
-                    sr[slot][j] = gi < p.G ? side_at(p.w.scale, p.w.side_dt, side0 + gi) : 0.0f;
-                    zr[slot][j] = p.w.zero && gi < p.G ? side_at(p.w.zero, p.w.side_dt, side0 + gi) : 8.0f;
+                    sr[slot][j] = zr[slot][j] = 0;
+                    if (gi < p.G) {
+                        sr[slot][j] = side_bits(p.w.scale, p.w.side_dt, side0 + gi);
+                        if (p.w.zero) zr[slot][j] = side_bits(p.w.zero, p.w.side_dt, side0 + gi);
+                    }
                 }
                 for (int j = 0; j < SETS; ++j) side_step();
             }
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             for (int st = 0; st < RING; ++st) {
                 const int i = i0 + st * SETS;
                 if (i >= total) break;
-                float s_now[gpb], z_now[gpb];
+                uint32_t s_now[gpb], z_now[gpb];
 #pragma unroll
                 for (int j = 0; j < gpb; ++j) s_now[j] = sr[st & 1][j], z_now[j] = zr[st & 1][j];
                 load_sides(st & 1);
@@ -369,8 +372,11 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                     tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 64 + h * 32, a);
                 }
 #pragma unroll
-                for (int j = 0; j < gpb; ++j)
-                    sides[(sa * gpb + j) * T4_M + quad * 32 + lane] = make_float2(s_now[j], s_now[j] == 0.0f && z_now[j] == 8.0f ? 0.0f : -s_now[j] * z_now[j]);
+                for (int j = 0; j < gpb; ++j) {
+                    const float sc = side_of(s_now[j], p.w.side_dt);
+                    sides[(sa * gpb + j) * T4_M + quad * 32 + lane] =
+                        make_float2(sc, -sc * (p.w.zero ? side_of(z_now[j], p.w.side_dt) : 8.0f));
+                }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();

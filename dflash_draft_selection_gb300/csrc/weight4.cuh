@@ -18,6 +18,14 @@ __device__ __forceinline__ float side_at(const void *p, dflash2_dtype dt, int64_
     return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
 }
 
+// The same in two steps: bits now, the number where it is needed (a conversion would wait for the load).
+__device__ __forceinline__ uint32_t side_bits(const void *p, dflash2_dtype dt, int64_t i) {
+    return dt == DFLASH2_F32 ? static_cast<const uint32_t *>(p)[i] : static_cast<const uint16_t *>(p)[i];
+}
+__device__ __forceinline__ float side_of(uint32_t bits, dflash2_dtype dt) {
+    return __uint_as_float(dt == DFLASH2_F32 ? bits : bits << 16);
+}
+
 // f32 to bf16, nearest, ties to even; NaN to a quiet NaN.
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
     uint16_t h;
