@@ -34,16 +34,14 @@ static __device__ unsigned int g_err_linear4;
 // Warps: 8 for the epilogue, the operand's 4 (where the epilogue needs 128 registers a thread) or 8, copies, MMAs.
 constexpr int t4_sets(int rh) { return rh > 32 ? 1 : 2; }
 constexpr int t4_threads(int rh) { return (8 + 4 * t4_sets(rh) + 2) * 32; }
-constexpr int T4_XS = 4;   // stages of x'
-constexpr int T4_AS = 4;   // blocks of A in tensor memory
+constexpr int T4_IN = 4;   // blocks of the operands: x' in shared memory, A in tensor memory
 constexpr int t4_ring(int rh) { return 8 / t4_sets(rh); }  // blocks that an operand warp has room for
 constexpr int T4_DS = 4;   // accumulators, at most: 2 of 128 columns
 constexpr int T4_M = 128;
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
 struct Tc4Shared {
-    uint64_t x_full[T4_XS], x_empty[T4_XS];
-    uint64_t a_full[T4_AS], a_empty[T4_AS];
+    uint64_t in_full[T4_IN], in_empty[T4_IN];
     uint64_t d_full[T4_DS], d_empty[T4_DS];
     uint64_t done;
     uint32_t tmem;
@@ -181,13 +179,13 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
     extern __shared__ unsigned char raw[];
     __shared__ Tc4Shared sm;
     unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float *sums = reinterpret_cast<float *>(xs + T4_XS * XB);  // [stage][group of the block][R]
-    float2 *sides = reinterpret_cast<float2 *>(sums + T4_XS * gpb * R);  // [block of A][group][weight row]: scale, -scale * zero
-    unsigned char *rings = reinterpret_cast<unsigned char *>(sides + T4_AS * gpb * T4_M);
+    float *sums = reinterpret_cast<float *>(xs + T4_IN * XB);  // [stage][group of the block][R]
+    float2 *sides = reinterpret_cast<float2 *>(sums + T4_IN * gpb * R);  // [block of A][group][weight row]: scale, -scale * zero
+    unsigned char *rings = reinterpret_cast<unsigned char *>(sides + T4_IN * gpb * T4_M);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < T4_XS; ++i) mbar_init(&sm.x_full[i], 1), mbar_init(&sm.x_empty[i], 9);
-        for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_full[i], 4), mbar_init(&sm.a_empty[i], 9);
+        // a block is there when x' and the operand's four warps are; it is free after its MMAs and the epilogue's warps
+        for (int i = 0; i < T4_IN; ++i) mbar_init(&sm.in_full[i], 5), mbar_init(&sm.in_empty[i], 9);
         for (int i = 0; i < T4_DS; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_empty[i], 8);
         mbar_init(&sm.done, 1);
         sm.abort = 0;
@@ -198,7 +196,8 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    constexpr uint32_t DS = R > 64 ? 2 : 4;
+    // accumulators, and how many of them the epilogue is given at a time
+    constexpr uint32_t DS = R > 64 ? 2 : 4, U = R > 64 ? 1 : 2;
     const uint32_t tmem = sm.tmem, tmem_a = tmem + DS * R;
     const int mine = static_cast<int>((p.tiles - blockIdx.x - 1) / gridDim.x) + 1;  // tiles of this CTA
     const int total = mine * p.rblocks * p.kblocks;                                 // and their blocks
@@ -210,19 +209,20 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             if (p.hold != nullptr && !hold_wait(p.hold, p.hold_cycles)) t4_abort(sm), ok = false;
             Walk4 at{0, 0, 0};
             for (; ok && i < total; ++i, at.next(p)) {
-                const int s = i % T4_XS;
-                if (i >= T4_XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / T4_XS - 1) & 1)) break;
-                mbar_arrive_expect_tx(&sm.x_full[s], XB + gpb * R * 4);
-                tma_load_2d(xs + s * XB, &tm_x, at.kb * L4_BLOCK, at.rb * R, &sm.x_full[s]);
-                tma_load_2d(xs + s * XB + XB / 2, &tm_x, at.kb * L4_BLOCK + 64, at.rb * R, &sm.x_full[s]);
+                const int s = i % T4_IN;
+                if (i >= T4_IN && !t4_wait(sm, &sm.in_empty[s], static_cast<uint32_t>(i / T4_IN - 1) & 1)) break;
+                mbar_arrive_expect_tx(&sm.in_full[s], XB + gpb * R * 4);
+                tma_load_2d(xs + s * XB, &tm_x, at.kb * L4_BLOCK, at.rb * R, &sm.in_full[s]);
+                tma_load_2d(xs + s * XB + XB / 2, &tm_x, at.kb * L4_BLOCK + 64, at.rb * R, &sm.in_full[s]);
                 const float *from = p.sums + static_cast<int64_t>(at.kb) * gpb * p.rows_pad + at.rb * R;
 #pragma unroll
                 for (int j = 0; j < gpb; ++j, from += p.rows_pad)
-                    bulk_g2s(sums + (s * gpb + j) * R, from, R * 4, &sm.x_full[s]);
+                    bulk_g2s(sums + (s * gpb + j) * R, from, R * 4, &sm.in_full[s]);
             }
-            // leave no copy in flight into this CTA's shared memory
-            for (int j = i > T4_XS ? i - T4_XS : 0; j < i; ++j)
-                mbar_wait(&sm.x_full[j % T4_XS], static_cast<uint32_t>(j / T4_XS) & 1, T4_DRAIN);
+            // Leave no copy in flight into this CTA's shared memory.  A block is waited for with its operand; after a
+            // time-out that may not come, and the copies have the whole limit to land.
+            for (int j = i > T4_IN ? i - T4_IN : 0; j < i; ++j)
+                mbar_wait(&sm.in_full[j % T4_IN], static_cast<uint32_t>(j / T4_IN) & 1, T4_DRAIN);
         }
     } else if (warp == T4_MMA) {
         // The whole warp walks, so that addresses stay in uniform registers; one thread issues.
@@ -233,15 +233,16 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         uint32_t d = 0;
         bool ok = true;
         for (int i = 0; ok && i < total; ++i) {
-            const int s = i % T4_XS, sa = i % T4_AS;
-            ok = t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1) &&
-                 t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / T4_AS) & 1);
-            if (!__all_sync(FULL, ok)) break;
+            const int s = i % T4_IN;
+            ok = __all_sync(FULL, t4_wait(sm, &sm.in_full[s], static_cast<uint32_t>(i / T4_IN) & 1));
+            if (!ok) break;
             const uint64_t b0 = x0 + (s * XB >> 4);
-            const uint32_t a0 = tmem_a + sa * 64;
+            const uint32_t a0 = tmem_a + s * 64;
 #pragma unroll
             for (int j = 0; j < gpb; ++j, ++d) {
-                if (d >= DS) ok = __all_sync(FULL, t4_wait(sm, &sm.d_empty[d % DS], (d / DS - 1) & 1));
+                // U accumulators at a time
+                const uint32_t u = d / U;
+                if (d % U == 0 && u >= DS / U) ok = __all_sync(FULL, t4_wait(sm, &sm.d_empty[u % (DS / U)], (u / (DS / U) - 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t to = tmem + (d % DS) * R;
@@ -252,14 +253,13 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                         if (k == 0) mma_bf16_ts<false>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
                         else mma_bf16_ts<true>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
                     }
-                    mma_commit(&sm.d_full[d % DS]);
+                    if (d % U == U - 1 || (i == total - 1 && j == gpb - 1)) mma_commit(&sm.d_full[u % (DS / U)]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
             if (leader) {
-                mma_commit(&sm.a_empty[sa]);
-                mma_commit(&sm.x_empty[s]);
+                mma_commit(&sm.in_empty[s]);
             }
             __syncwarp();
         }
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                 copy((st + RING - 1) % RING);
                 cp_async_wait<RING - 1>();
                 __syncwarp();
-                const int sa = i % T4_AS;
+                const int sa = i % T4_IN;
                 uint32_t v[4][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[q][0]), "=r"(v[q][1]), "=r"(v[q][2]), "=r"(v[q][3]) : "r"(at_q));
                 }
                 bool ok = true;
-                if (i >= T4_AS) ok = t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(i / T4_AS - 1) & 1);
+                if (i >= T4_IN) ok = t4_wait(sm, &sm.in_empty[sa], static_cast<uint32_t>(i / T4_IN - 1) & 1);
                 if (!__all_sync(FULL, ok)) {
                     go = 0;
                     break;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.a_full[sa]);
+                if (lane == 0) mbar_arrive(&sm.in_full[sa]);
             }
         }
         cp_async_wait<0>();
@@ -398,17 +398,15 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
 #pragma unroll
                 for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
                 for (int kb = 0; ok && kb < p.kblocks; ++kb, ++i) {
-                    const int s = i % T4_XS, sa = i % T4_AS;
+                    const int s = i % T4_IN;
+                    ok = __all_sync(FULL, t4_wait(sm, &sm.in_full[s], static_cast<uint32_t>(i / T4_IN) & 1));
 #pragma unroll
                     for (int j = 0; j < gpb; ++j, ++d) {
-                        ok = ok && t4_wait(sm, &sm.d_full[d % DS], (d / DS) & 1);
-                        // complete by then; waited for so that what was written beside them is seen
-                        if (j == 0) ok = ok && t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / T4_XS) & 1) &&
-                                         t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / T4_AS) & 1);
-                        ok = __all_sync(FULL, ok);
+                        const float2 side = sides[(s * gpb + j) * T4_M + quad * 32 + lane];
+                        const uint32_t u = d / U;
+                        if (d % U == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[u % (DS / U)], (u / (DS / U)) & 1));
                         if (!ok) break;
                         tc_fence_after();
-                        const float2 side = sides[(sa * gpb + j) * T4_M + quad * 32 + lane];
                         const uint64_t s2 = pack2(__float_as_uint(side.x), __float_as_uint(side.x));
                         const uint64_t z2 = pack2(__float_as_uint(side.y), __float_as_uint(side.y));
                         const float *xg = sums + (s * gpb + j) * R + half * RH;
@@ -431,11 +429,14 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                                 acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[k + 2], v[k + 3]), acc[at + 1]));
                             }
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.d_empty[d % DS]);
+                        if (d % U == U - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.d_empty[u % (DS / U)]);
+                        }
                     }
-                    if (ok && lane == 0) mbar_arrive(&sm.x_empty[s]), mbar_arrive(&sm.a_empty[sa]);
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&sm.in_empty[s]);
                 }
                 // the roots of columns l and 32 + l
                 const int64_t r0 = static_cast<int64_t>(rb) * R + half * RH;
@@ -474,7 +475,7 @@ template <int RH, int LG>
 static dflash2_status launch_tc4(const CUtensorMap &tm, const Tc4 &p, cudaStream_t s) {
     auto fn = &k_linear4_tc<RH, LG>;
     constexpr int R = RH * 2;
-    const size_t smem = 1024 + T4_XS * (R * L4_BLOCK * 2 + (R * 4 << LG)) + (T4_AS * T4_M * 8 << LG) + 4 * t4_sets(RH) * t4_ring(RH) * 2048;
+    const size_t smem = 1024 + T4_IN * (R * L4_BLOCK * 2 + (R * 4 << LG)) + (T4_IN * T4_M * 8 << LG) + 4 * t4_sets(RH) * t4_ring(RH) * 2048;
     blocks_per_sm(reinterpret_cast<const void *>(fn), t4_threads(RH), smem);  // raises the shared-memory limit once per device
     const int64_t sms = sm_count();
     fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), t4_threads(RH), smem, s>>>(tm, p);
