@@ -6,8 +6,8 @@
 //   acc += scale * (part - zero * sum of x)                  in registers, f32
 // so products are exact whatever the scales, and a result is rounded once.
 //
-// The codes go from global memory through a warp's own copies (cp.async) and
-// its registers into tensor memory, where the MMA takes its A operand: with A in
+// The codes go by TMA into a warp's own ring in shared memory and through its
+// registers into tensor memory, where the MMA takes its A operand: with A in
 // shared memory its 4 KB per step of 16 columns bound the MMA to 56 cycles at R
 // = 64, from tensor memory it takes 32.  x' (scaled and reordered once by a
 // kernel of its own into the workspace) comes by TMA, 128-byte swizzle, with its
@@ -15,11 +15,12 @@
 //
 // One CTA per SM walks its tiles of 128 weight rows; a tile's blocks of x rows
 // follow each other, so its codes come from L2 after the first.
-//   8 warps      epilogue: a weight row per lane, half of the R columns each
-//   4 or 8 warps operand and scales: 32 weight rows each; of 8, 4 take the odd blocks
-//                of 128 columns
+//   warps 0-7    epilogue: a weight row per lane, half of the R columns each
+//   4 or 8 warps operand and scales: 32 weight rows each; of 8, 4 take the odd pairs of
+//                blocks of 128 columns
 //   2 warps      copies of x', MMAs
-// Tensor memory: 4 accumulators of R columns (2 of 128), 4 blocks of A of 64 columns.
+// Tensor memory: 4 accumulators of R columns (2 of 128), 4 blocks of A of 64 columns
+// (two pairs).
 //
 // Waits are bounded: after a time-out every role stops waiting, the error word
 // is set and the CTA's remaining outputs are NaN.
@@ -31,17 +32,24 @@ namespace dfl {
 
 static __device__ unsigned int g_err_linear4;
 
-// Warps: 8 for the epilogue, the operand's 4 (where the epilogue needs 128 registers a thread) or 8, copies, MMAs.
+// Warps: 8 for the epilogue, the operand's 4 (where the epilogue needs 128 registers a thread) or 8, copies of x', MMAs.
 constexpr int t4_sets(int rh) { return rh > 32 ? 1 : 2; }
 constexpr int t4_threads(int rh) { return (8 + 4 * t4_sets(rh) + 2) * 32; }
-constexpr int T4_IN = 4;   // blocks of the operands: x' in shared memory, A in tensor memory
-constexpr int t4_ring(int rh) { return 8 / t4_sets(rh); }  // blocks that an operand warp has room for
-constexpr int T4_DS = 4;   // accumulators, at most: 2 of 128 columns
+constexpr int t4_stages(int rh) { return rh > 32 ? 4 : 6; }  // of x', 128 columns
+constexpr int t4_ring(int rh) { return rh > 32 ? 4 : 3; }    // pairs of blocks of codes that an operand warp has room for
+constexpr int T4_AS = 2;      // pairs of blocks of A in tensor memory
+// Blocks whose scales are kept.  A block's are overwritten when the operand is this many further on: it is at most 4
+// blocks ahead of the last MMA that completed, and that at most T4_DS accumulators (4, 2 or 1 blocks) ahead of the
+// epilogue.
+constexpr int t4_sides(int lg) { return lg == 0 ? 8 : 6; }
+constexpr int T4_DS = 4;      // accumulators, at most: 2 of 128 columns
 constexpr int T4_M = 128;
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
 struct Tc4Shared {
-    uint64_t in_full[T4_IN], in_empty[T4_IN];
+    uint64_t x_full[6], x_empty[6];
+    uint64_t a_full[T4_AS], a_empty[T4_AS];
+    uint64_t c_full[8][4];  // an operand warp's codes
     uint64_t d_full[T4_DS], d_empty[T4_DS];
     uint64_t done;
     uint32_t tmem;
@@ -53,10 +61,10 @@ struct Tc4 {
     void *y;
     int64_t rows, y_stride;
     dflash2_dtype y_dt;
-    int lg, G, kblocks, rblocks;  // lg: log2 of the groups in a block
+    int lg, G, kpairs, rblocks;  // lg: log2 of the groups in a block
     int64_t tiles;
     int64_t rows_pad;   // rows of x' in all blocks
-    const float *sums;  // [kblocks << lg][rows_pad]
+    const float *sums;  // [2 * kpairs << lg][rows_pad]
     const float *root;  // [rows_pad]
     const unsigned int *hold;
     long long hold_cycles;
@@ -163,7 +171,7 @@ struct Walk4 {
     int64_t tile;
     int rb, kb;
     __device__ __forceinline__ void next(const Tc4 &p) {
-        if (++kb == p.kblocks) {
+        if (++kb == 2 * p.kpairs) {
             kb = 0;
             if (++rb == p.rblocks) rb = 0, tile += gridDim.x;
         }
@@ -172,20 +180,26 @@ struct Walk4 {
 
 // RH: half of the block's rows of x, the columns of an epilogue warp.  LG: log2 of the groups in a block.
 template <int RH, int LG>
-__global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x, const Tc4 p) {
+__global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x,
+                                                              const __grid_constant__ CUtensorMap tm_c, const Tc4 p) {
     constexpr int R = RH * 2, XB = R * L4_BLOCK * 2;  // bytes of a stage of x'
     constexpr int gpb = 1 << LG, STEPS = 8 >> LG;      // groups of a block, steps of 16 columns in a group
-    constexpr int SETS = t4_sets(RH), RING = t4_ring(RH), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
+    constexpr int T4_SIDES = t4_sides(LG);
+    constexpr int XS = t4_stages(RH), RING = t4_ring(RH), SETS = t4_sets(RH), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
     extern __shared__ unsigned char raw[];
     __shared__ Tc4Shared sm;
     unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float *sums = reinterpret_cast<float *>(xs + T4_IN * XB);  // [stage][group of the block][R]
-    float2 *sides = reinterpret_cast<float2 *>(sums + T4_IN * gpb * R);  // [block of A][group][weight row]: scale, -scale * zero
-    unsigned char *rings = reinterpret_cast<unsigned char *>(sides + T4_IN * gpb * T4_M);
+    unsigned char *rings = xs + XS * XB;                              // 4 KB each: 32 rows of 256 codes
+    float *sums = reinterpret_cast<float *>(rings + 4 * SETS * RING * 4096);  // [stage][group of the block][R]
+    float2 *sides = reinterpret_cast<float2 *>(sums + XS * gpb * R);  // [block][group][weight row]: scale, -scale * zero
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        // a block is there when x' and the operand's four warps are; it is free after its MMAs and the epilogue's warps
-        for (int i = 0; i < T4_IN; ++i) mbar_init(&sm.in_full[i], 5), mbar_init(&sm.in_empty[i], 9);
+        // a block is there when x' has landed and the operand's four warps have left its scales; it is free after its
+        // MMAs and the epilogue's warps
+        for (int i = 0; i < XS; ++i) mbar_init(&sm.x_full[i], 5), mbar_init(&sm.x_empty[i], 9);
+        for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_full[i], 4), mbar_init(&sm.a_empty[i], 1);
+        for (int i = 0; i < 4 * SETS; ++i)
+            for (int j = 0; j < RING; ++j) mbar_init(&sm.c_full[i][j], 1);
         for (int i = 0; i < T4_DS; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_empty[i], 8);
         mbar_init(&sm.done, 1);
         sm.abort = 0;
@@ -200,7 +214,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
     constexpr uint32_t DS = R > 64 ? 2 : 4, U = R > 64 ? 1 : 2;
     const uint32_t tmem = sm.tmem, tmem_a = tmem + DS * R;
     const int mine = static_cast<int>((p.tiles - blockIdx.x - 1) / gridDim.x) + 1;  // tiles of this CTA
-    const int total = mine * p.rblocks * p.kblocks;                                 // and their blocks
+    const int total = mine * p.rblocks * p.kpairs * 2;                              // and their blocks
 
     if (warp == T4_COPY) {
         if (lane == 0) {
@@ -209,20 +223,20 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             if (p.hold != nullptr && !hold_wait(p.hold, p.hold_cycles)) t4_abort(sm), ok = false;
             Walk4 at{0, 0, 0};
             for (; ok && i < total; ++i, at.next(p)) {
-                const int s = i % T4_IN;
-                if (i >= T4_IN && !t4_wait(sm, &sm.in_empty[s], static_cast<uint32_t>(i / T4_IN - 1) & 1)) break;
-                mbar_arrive_expect_tx(&sm.in_full[s], XB + gpb * R * 4);
-                tma_load_2d(xs + s * XB, &tm_x, at.kb * L4_BLOCK, at.rb * R, &sm.in_full[s]);
-                tma_load_2d(xs + s * XB + XB / 2, &tm_x, at.kb * L4_BLOCK + 64, at.rb * R, &sm.in_full[s]);
+                const int s = i % XS;
+                if (i >= XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / XS - 1) & 1)) break;
+                mbar_arrive_expect_tx(&sm.x_full[s], XB + gpb * R * 4);
+                tma_load_2d(xs + s * XB, &tm_x, at.kb * L4_BLOCK, at.rb * R, &sm.x_full[s]);
+                tma_load_2d(xs + s * XB + XB / 2, &tm_x, at.kb * L4_BLOCK + 64, at.rb * R, &sm.x_full[s]);
                 const float *from = p.sums + static_cast<int64_t>(at.kb) * gpb * p.rows_pad + at.rb * R;
 #pragma unroll
                 for (int j = 0; j < gpb; ++j, from += p.rows_pad)
-                    bulk_g2s(sums + (s * gpb + j) * R, from, R * 4, &sm.in_full[s]);
+                    bulk_g2s(sums + (s * gpb + j) * R, from, R * 4, &sm.x_full[s]);
             }
-            // Leave no copy in flight into this CTA's shared memory.  A block is waited for with its operand; after a
-            // time-out that may not come, and the copies have the whole limit to land.
-            for (int j = i > T4_IN ? i - T4_IN : 0; j < i; ++j)
-                mbar_wait(&sm.in_full[j % T4_IN], static_cast<uint32_t>(j / T4_IN) & 1, T4_DRAIN);
+            // Leave no copy in flight into this CTA's shared memory.  A block is waited for with its scales; after a
+            // time-out those may not come, and the copies have the whole limit to land.
+            for (int j = i > XS ? i - XS : 0; j < i; ++j)
+                mbar_wait(&sm.x_full[j % XS], static_cast<uint32_t>(j / XS) & 1, T4_DRAIN);
         }
     } else if (warp == T4_MMA) {
         // The whole warp walks, so that addresses stay in uniform registers; one thread issues.
@@ -233,11 +247,12 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         uint32_t d = 0;
         bool ok = true;
         for (int i = 0; ok && i < total; ++i) {
-            const int s = i % T4_IN;
-            ok = __all_sync(FULL, t4_wait(sm, &sm.in_full[s], static_cast<uint32_t>(i / T4_IN) & 1));
-            if (!ok) break;
+            const int s = i % XS, sa = i / 2 % T4_AS;
+            if (i % 2 == 0) ok = t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / 2 / T4_AS) & 1);
+            ok = ok && t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / XS) & 1);
+            if (!__all_sync(FULL, ok)) break;
             const uint64_t b0 = x0 + (s * XB >> 4);
-            const uint32_t a0 = tmem_a + s * 64;
+            const uint32_t a0 = tmem_a + sa * 128 + i % 2 * 64;
 #pragma unroll
             for (int j = 0; j < gpb; ++j, ++d) {
                 // U accumulators at a time
@@ -259,7 +274,8 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             }
             if (!ok) break;
             if (leader) {
-                mma_commit(&sm.in_empty[s]);
+                if (i % 2) mma_commit(&sm.a_empty[sa]);
+                mma_commit(&sm.x_empty[s]);
             }
             __syncwarp();
         }
@@ -268,122 +284,103 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         __syncwarp();
         mbar_wait(&sm.done, 0, T4_DRAIN);
     } else if (warp >= 8) {
-        // the operand: 32 weight rows of every block, or of every second one
-        const int quad = warp & 3, odd = (warp - 8) >> 2;
-        const uint32_t ring = smem_addr(rings) + (warp - 8) * (RING * 2048);
-        const int row_bytes = static_cast<int>((p.w.K + 31) / 32 * 16);
-        // lane l copies chunk l % 4 of rows l / 4 + 8 j
-        Walk4 at{blockIdx.x, 0, 0};
-        const unsigned char *from[4];
-        auto rows_of = [&]() {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = at.tile * T4_M + quad * 32 + (lane >> 2) + 8 * j;
-                from[j] = static_cast<const unsigned char *>(p.w.codes) + (n < p.w.N ? n : p.w.N - 1) * p.w.code_stride + (lane & 3) * 16;
-            }
-        };
-        rows_of();
-        auto step = [&]() {
-            const int64_t was = at.tile;
-            at.next(p);
-            if (at.tile != was) rows_of();
-        };
-        if (odd) step();
+        // The operand: 32 weight rows of every (second) pair of blocks.  A warp's codes come by TMA, 128 bytes of its rows
+        // (zeros past the last row and column), 128-byte swizzle.
+        const int quad = warp & 3, odd = (warp - 8) >> 2, me = warp - 8;
+        unsigned char *ring = rings + me * (RING * 4096);
+        const uint32_t ring_row = smem_addr(ring) + lane * 128;
+        const int pairs = total / 2;
+        Walk4 cw{blockIdx.x, 0, 0};  // pair to copy next, and how far it is
+        auto pair_step = [&](Walk4 &w) { w.next(p), w.next(p); };
         int c = odd;
-        const uint32_t to = ring + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-        // scales and zero points of lane l's own row, two of the warp's blocks ahead
+        auto copy = [&](int stage) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.c_full[me][stage], 4096);
+                tma_load_2d(ring + stage * 4096, &tm_c, cw.kb * (L4_BLOCK / 2), static_cast<int>(cw.tile * T4_M) + quad * 32,
+                            &sm.c_full[me][stage]);
+            }
+            for (int j = 0; j < SETS; ++j) pair_step(cw);
+            c += SETS;
+        };
+        if (odd) pair_step(cw);
+        int issued = 0;
+#pragma unroll
+        for (int j = 0; j < RING; ++j)
+            if (c < pairs) copy(j), ++issued;
+        // scales and zero points of the lane's own row, one of the warp's pairs ahead
         Walk4 sw{blockIdx.x, 0, 0};
         int64_t side0 = 0;
-        uint32_t sr[2][gpb], zr[2][gpb];
+        uint32_t sr[2 * gpb], zr[2 * gpb];
         auto side_row = [&]() {
             const int64_t n = sw.tile * T4_M + quad * 32 + lane;
             side0 = (n < p.w.N ? n : p.w.N - 1) * p.w.side_stride;
         };
-        auto side_step = [&]() {
+        auto load_sides = [&]() {
+            if (sw.tile >= p.tiles) return;
             const int64_t was = sw.tile;
-            sw.next(p);
+#pragma unroll
+            for (int j = 0; j < 2 * gpb; ++j) {
+                const int gi = sw.kb * gpb + j;
+                sr[j] = zr[j] = 0;
+                if (gi < p.G) {
+                    sr[j] = side_bits(p.w.scale, p.w.side_dt, side0 + gi);
+                    if (p.w.zero) zr[j] = side_bits(p.w.zero, p.w.side_dt, side0 + gi);
+                }
+            }
+            for (int j = 0; j < SETS; ++j) pair_step(sw);
             if (sw.tile != was) side_row();
         };
-        auto load_sides = [&](int slot) {
-            if (sw.tile < p.tiles) {
-#pragma unroll
-                for (int j = 0; j < gpb; ++j) {
-                    const int gi = sw.kb * gpb + j;
-                    sr[slot][j] = zr[slot][j] = 0;
-                    if (gi < p.G) {
-                        sr[slot][j] = side_bits(p.w.scale, p.w.side_dt, side0 + gi);
-                        if (p.w.zero) zr[slot][j] = side_bits(p.w.zero, p.w.side_dt, side0 + gi);
-                    }
-                }
-                for (int j = 0; j < SETS; ++j) side_step();
-            }
-        };
+        if (odd) pair_step(sw);
         side_row();
-        if (odd) side_step();
-        load_sides(0), load_sides(1);
-        auto copy = [&](int stage) {
-            if (c < total) {
-                const int off = at.kb * (L4_BLOCK / 2);
-                const bool take = off + (lane & 3) * 16 < row_bytes;
+        load_sides();
+        int st = 0;
+        uint32_t round = 0;
+        for (int i = odd; i < pairs; i += SETS) {
+            const int sa = i % T4_AS;
+            bool ok = t4_wait(sm, &sm.c_full[me][st], round & 1);
+            if (i >= T4_AS) ok = ok && t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(i / T4_AS - 1) & 1);
+            if (!__all_sync(FULL, ok)) break;
+            tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) cp_async16(to + stage * 2048 + j * 512, from[j] + (take ? off : 0), take);
-                for (int j = 0; j < SETS; ++j) step();
-            }
-            cp_async_commit();
-            c += SETS;
-        };
+            for (int h = 0; h < 4; ++h) {  // 64 columns
+                uint32_t a[32];
 #pragma unroll
-        for (int j = 0; j < RING - 1; ++j) copy(j);
-        for (int i0 = odd, go = 1; go && i0 < total; i0 += SETS * RING) {
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(ring_row + st * 4096 + (((h * 2 + q) ^ (lane & 7)) << 4)));
 #pragma unroll
-            for (int st = 0; st < RING; ++st) {
-                const int i = i0 + st * SETS;
-                if (i >= total) break;
-                uint32_t s_now[gpb], z_now[gpb];
-#pragma unroll
-                for (int j = 0; j < gpb; ++j) s_now[j] = sr[st & 1][j], z_now[j] = zr[st & 1][j];
-                load_sides(st & 1);
-                copy((st + RING - 1) % RING);
-                cp_async_wait<RING - 1>();
-                __syncwarp();
-                const int sa = i % T4_IN;
-                uint32_t v[4][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t at_q = ring + st * 2048 + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[q][0]), "=r"(v[q][1]), "=r"(v[q][2]), "=r"(v[q][3]) : "r"(at_q));
-                }
-                bool ok = true;
-                if (i >= T4_IN) ok = t4_wait(sm, &sm.in_empty[sa], static_cast<uint32_t>(i / T4_IN - 1) & 1);
-                if (!__all_sync(FULL, ok)) {
-                    go = 0;
-                    break;
-                }
-                tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t a[32];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint32_t w = v[h * 2 + q / 4][q % 4], u = w >> 8;
-                        a[q * 4] = w & 0x000f000fu, a[q * 4 + 1] = w & 0x00f000f0u;
-                        a[q * 4 + 2] = u & 0x000f000fu, a[q * 4 + 3] = u & 0x00f000f0u;
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t u = v[j] >> 8;
+                        a[q * 16 + j * 4] = v[j] & 0x000f000fu, a[q * 16 + j * 4 + 1] = v[j] & 0x00f000f0u;
+                        a[q * 16 + j * 4 + 2] = u & 0x000f000fu, a[q * 16 + j * 4 + 3] = u & 0x00f000f0u;
                     }
-                    tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 64 + h * 32, a);
                 }
-#pragma unroll
-                for (int j = 0; j < gpb; ++j) {
-                    const float sc = side_of(s_now[j], p.w.side_dt);
-                    sides[(sa * gpb + j) * T4_M + quad * 32 + lane] =
-                        make_float2(sc, -sc * (p.w.zero ? side_of(z_now[j], p.w.side_dt) : 8.0f));
-                }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.in_full[sa]);
+                tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 128 + h * 32, a);
             }
+#pragma unroll
+            for (int j = 0; j < 2 * gpb; ++j) {
+                const float sc = side_of(sr[j], p.w.side_dt);
+                sides[((2 * i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane] =
+                    make_float2(sc, -sc * (p.w.zero ? side_of(zr[j], p.w.side_dt) : 8.0f));
+            }
+            load_sides();
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.a_full[sa]);
+                mbar_arrive(&sm.x_full[2 * i % XS]), mbar_arrive(&sm.x_full[(2 * i + 1) % XS]);
+            }
+            if (c < pairs) copy(st), ++issued;
+            if (++st == RING) st = 0, ++round;
         }
-        cp_async_wait<0>();
+        // leave no copy in flight
+        if (lane == 0)
+            for (int j = issued > RING ? issued - RING : 0; j < issued; ++j)
+                mbar_wait(&sm.c_full[me][j % RING], static_cast<uint32_t>(j / RING) & 1, T4_DRAIN);
+        __syncwarp();
     } else {
         // epilogue
         const int quad = warp & 3, half = warp >> 2;
@@ -397,12 +394,12 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                 uint64_t acc[RH / 2];
 #pragma unroll
                 for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
-                for (int kb = 0; ok && kb < p.kblocks; ++kb, ++i) {
-                    const int s = i % T4_IN;
-                    ok = __all_sync(FULL, t4_wait(sm, &sm.in_full[s], static_cast<uint32_t>(i / T4_IN) & 1));
+                for (int kb = 0; ok && kb < 2 * p.kpairs; ++kb, ++i) {
+                    const int s = i % XS;
+                    ok = __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / XS) & 1));
 #pragma unroll
                     for (int j = 0; j < gpb; ++j, ++d) {
-                        const float2 side = sides[(s * gpb + j) * T4_M + quad * 32 + lane];
+                        const float2 side = sides[((i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane];
                         const uint32_t u = d / U;
                         if (d % U == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[u % (DS / U)], (u / (DS / U)) & 1));
                         if (!ok) break;
@@ -436,7 +433,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                         }
                     }
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(&sm.in_empty[s]);
+                    if (ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
                 }
                 // the roots of columns l and 32 + l
                 const int64_t r0 = static_cast<int64_t>(rb) * R + half * RH;
@@ -464,7 +461,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
 // Rows of x to a block.
 static int t4_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 static int64_t t4_pad(int64_t rows) { return (rows + t4_rows(rows) - 1) / t4_rows(rows) * t4_rows(rows); }
-static int64_t t4_kpad(int64_t K) { return (K + L4_BLOCK - 1) / L4_BLOCK * L4_BLOCK; }
+static int64_t t4_kpad(int64_t K) { return (K + 2 * L4_BLOCK - 1) / (2 * L4_BLOCK) * (2 * L4_BLOCK); }
 
 // Workspace: x', the sums (of the smallest groups), the roots.
 size_t linear4_tc_bytes(int64_t rows, int64_t K) {
@@ -472,21 +469,35 @@ size_t linear4_tc_bytes(int64_t rows, int64_t K) {
 }
 
 template <int RH, int LG>
-static dflash2_status launch_tc4(const CUtensorMap &tm, const Tc4 &p, cudaStream_t s) {
+static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, cudaStream_t s) {
     auto fn = &k_linear4_tc<RH, LG>;
     constexpr int R = RH * 2;
-    const size_t smem = 1024 + T4_IN * (R * L4_BLOCK * 2 + (R * 4 << LG)) + (T4_IN * T4_M * 8 << LG) + 4 * t4_sets(RH) * t4_ring(RH) * 2048;
+    constexpr size_t smem = 1024 + t4_stages(RH) * (R * L4_BLOCK * 2 + (R * 4 << LG)) + 4 * t4_sets(RH) * t4_ring(RH) * 4096 +
+                        (t4_sides(LG) * T4_M * 8 << LG);
+    static_assert(smem + sizeof(Tc4Shared) <= 227 * 1024, "shared memory of a CTA");
     blocks_per_sm(reinterpret_cast<const void *>(fn), t4_threads(RH), smem);  // raises the shared-memory limit once per device
     const int64_t sms = sm_count();
-    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), t4_threads(RH), smem, s>>>(tm, p);
+    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), t4_threads(RH), smem, s>>>(tm, tc, p);
     return after_launch();
 }
 
 template <int RH>
-static dflash2_status launch_tc4_groups(const CUtensorMap &tm, const Tc4 &p, cudaStream_t s) {
-    if (p.lg == 0) return launch_tc4<RH, 0>(tm, p, s);
-    if (p.lg == 1) return launch_tc4<RH, 1>(tm, p, s);
-    return launch_tc4<RH, 2>(tm, p, s);
+static dflash2_status launch_tc4_groups(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, cudaStream_t s) {
+    if (p.lg == 0) return launch_tc4<RH, 0>(tm, tc, p, s);
+    if (p.lg == 1) return launch_tc4<RH, 1>(tm, tc, p, s);
+    return launch_tc4<RH, 2>(tm, tc, p, s);
+}
+
+// Codes [N, bytes of a row], boxes of 32 rows of 128 bytes; zeros past the edges.
+static bool codes_map(CUtensorMap *m, const dflash2_weight4 *w) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>((w->K + 31) / 32 * 16), static_cast<cuuint64_t>(w->N)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(w->code_stride)};
+    const cuuint32_t box[2] = {128u, 32u};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w->codes, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
@@ -500,7 +511,7 @@ dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const d
     p.w = *w, p.y = y, p.rows = rows, p.y_stride = y_stride, p.y_dt = y_dt;
     p.lg = w->group == 128 ? 0 : w->group == 64 ? 1 : 2;
     p.G = static_cast<int>(groups_of(w));
-    p.kblocks = static_cast<int>(kp / L4_BLOCK);
+    p.kpairs = static_cast<int>(kp / (2 * L4_BLOCK));
     p.rows_pad = t4_pad(rows);
     p.rblocks = static_cast<int>(p.rows_pad / R);
     p.tiles = (w->N + T4_M - 1) / T4_M;
@@ -512,12 +523,14 @@ dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const d
     CUtensorMap tm;
     if (!make_map_k64(&tm, xp, static_cast<uint64_t>(kp), static_cast<uint64_t>(p.rows_pad), static_cast<uint32_t>(R)))
         return DFLASH2_ERR_CUDA;
+    CUtensorMap tc;
+    if (!codes_map(&tc, w)) return DFLASH2_ERR_CUDA;
     k_linear4_rows<<<static_cast<unsigned>(p.rows_pad), 256, 0, s>>>(x, rows, x_stride, static_cast<int>(w->K), p.lg,
-                                                                     p.kblocks, p.rows_pad, xp, sums, root);
+                                                                     2 * p.kpairs, p.rows_pad, xp, sums, root);
     const dflash2_status st = after_launch();
     if (st != DFLASH2_OK) return st;
-    return R == 16 ? launch_tc4_groups<8>(tm, p, s) : R == 32 ? launch_tc4_groups<16>(tm, p, s) : R == 64 ? launch_tc4_groups<32>(tm, p, s)
-                                                                                          : launch_tc4_groups<64>(tm, p, s);
+    return R == 16 ? launch_tc4_groups<8>(tm, tc, p, s) : R == 32 ? launch_tc4_groups<16>(tm, tc, p, s) : R == 64 ? launch_tc4_groups<32>(tm, tc, p, s)
+                                                                                          : launch_tc4_groups<64>(tm, tc, p, s);
 }
 
 unsigned int read_error_linear4(bool clear) {
