@@ -35,8 +35,9 @@ static __device__ unsigned int g_err_linear4;
 // Warps: 8 for the epilogue, the operand's 4 (where the epilogue needs 128 registers a thread) or 8, copies of x', MMAs.
 constexpr int t4_sets(int rh) { return rh > 32 ? 1 : 2; }
 constexpr int t4_threads(int rh) { return (8 + 4 * t4_sets(rh) + 2) * 32; }
-constexpr int t4_stages(int rh) { return rh > 32 ? 4 : 6; }  // of x', 128 columns
-constexpr int t4_ring(int rh) { return rh > 32 ? 4 : 3; }    // pairs of blocks of codes that an operand warp has room for
+constexpr int T4_XS = 4;                                        // stages of x'
+constexpr int t4_blocks(int rh) { return rh > 32 ? 1 : 2; }  // of 128 columns in a stage: a barrier costs its waiter 150 cycles
+constexpr int t4_ring(int rh) { return rh > 32 ? 4 : 2; }    // pairs of blocks of codes that an operand warp has room for
 constexpr int T4_AS = 2;      // pairs of blocks of A in tensor memory
 // Blocks whose scales are kept.  A block's are overwritten when the operand is this many further on: it is at most 4
 // blocks ahead of the last MMA that completed, and that at most T4_DS accumulators (4, 2 or 1 blocks) ahead of the
@@ -47,8 +48,8 @@ constexpr int T4_M = 128;
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
 struct Tc4Shared {
-    uint64_t x_full[6], x_empty[6];
-    uint64_t a_full[T4_AS], a_empty[T4_AS];
+    uint64_t x_full[T4_XS], x_empty[T4_XS];
+    uint64_t a_empty[T4_AS];
     uint64_t c_full[8][4];  // an operand warp's codes
     uint64_t d_full[T4_DS], d_empty[T4_DS];
     uint64_t done;
@@ -63,8 +64,7 @@ struct Tc4 {
     dflash2_dtype y_dt;
     int lg, G, kpairs, rblocks;  // lg: log2 of the groups in a block
     int64_t tiles;
-    int64_t rows_pad;   // rows of x' in all blocks
-    const float *sums;  // [2 * kpairs << lg][rows_pad]
+    const float *sums;  // [row block][2 * kpairs << lg][R]
     const float *root;  // [rows_pad]
     const unsigned int *hold;
     long long hold_cycles;
@@ -74,7 +74,7 @@ struct Tc4 {
 // One CTA per row: x' [rows_pad, kblocks * 128], the groups' sums, the root of the power of two.  Rows past the last are
 // zeros.
 __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t rows, int64_t x_stride, int K, int lg,
-                                                      int kblocks, int64_t rows_pad, uint16_t *out, float *sums,
+                                                      int kblocks, int R, uint16_t *out, float *sums,
                                                       float *root) {
     __shared__ uint32_t top;
     const int64_t r = blockIdx.x;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
         if (r < rows) load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
         float sum = scale8(v, e, bad);
         for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), sum, d);
-        if ((c & (lanes - 1)) == 0) sums[static_cast<int64_t>(c / lanes) * rows_pad + r] = sum;
+        if ((c & (lanes - 1)) == 0) sums[(r / R * (chunks / lanes) + c / lanes) * R + r % R] = sum;
         uint4 o;
         o.x = bf16_pair(v[0], v[4]), o.y = bf16_pair(v[1], v[5]), o.z = bf16_pair(v[2], v[6]), o.w = bf16_pair(v[3], v[7]);
         *reinterpret_cast<uint4 *>(out + (r * kblocks * L4_BLOCK + c * 8)) = o;
@@ -185,22 +185,23 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
     constexpr int R = RH * 2, XB = R * L4_BLOCK * 2;  // bytes of a stage of x'
     constexpr int gpb = 1 << LG, STEPS = 8 >> LG;      // groups of a block, steps of 16 columns in a group
     constexpr int T4_SIDES = t4_sides(LG);
-    constexpr int XS = t4_stages(RH), RING = t4_ring(RH), SETS = t4_sets(RH), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
+    constexpr int XS = T4_XS, SB = t4_blocks(RH), RING = t4_ring(RH), SETS = t4_sets(RH), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
     extern __shared__ unsigned char raw[];
     __shared__ Tc4Shared sm;
     unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char *rings = xs + XS * XB;                              // 4 KB each: 32 rows of 256 codes
-    float *sums = reinterpret_cast<float *>(rings + 4 * SETS * RING * 4096);  // [stage][group of the block][R]
-    float2 *sides = reinterpret_cast<float2 *>(sums + XS * gpb * R);  // [block][group][weight row]: scale, -scale * zero
+    unsigned char *rings = xs + XS * SB * XB;                              // 4 KB each: 32 rows of 256 codes
+    float *sums = reinterpret_cast<float *>(rings + 4 * SETS * RING * 4096);  // [stage][group of the stage][R]
+    float2 *sides = reinterpret_cast<float2 *>(sums + XS * SB * gpb * R);  // [block][group][weight row]: scale, -scale * zero
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        // a block is there when x' has landed and the operand's four warps have left its scales; it is free after its
-        // MMAs and the epilogue's warps
+        // A stage is there when x' has landed and the operand's four warps have left its blocks in tensor memory and
+        // their scales; it is free after its MMAs and the epilogue's warps.  Accumulators are there when their MMAs are
+        // done and the warp that issued them, which has seen the stage's rest, says so.
         for (int i = 0; i < XS; ++i) mbar_init(&sm.x_full[i], 5), mbar_init(&sm.x_empty[i], 9);
-        for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_full[i], 4), mbar_init(&sm.a_empty[i], 1);
+        for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_empty[i], 1);
         for (int i = 0; i < 4 * SETS; ++i)
             for (int j = 0; j < RING; ++j) mbar_init(&sm.c_full[i][j], 1);
-        for (int i = 0; i < T4_DS; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_empty[i], 8);
+        for (int i = 0; i < T4_DS; ++i) mbar_init(&sm.d_full[i], 2), mbar_init(&sm.d_empty[i], 8);
         mbar_init(&sm.done, 1);
         sm.abort = 0;
         fence_barrier_init();
@@ -222,16 +223,18 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             bool ok = true;
             if (p.hold != nullptr && !hold_wait(p.hold, p.hold_cycles)) t4_abort(sm), ok = false;
             Walk4 at{0, 0, 0};
-            for (; ok && i < total; ++i, at.next(p)) {
+            for (; ok && i < total / SB; ++i) {
                 const int s = i % XS;
                 if (i >= XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / XS - 1) & 1)) break;
-                mbar_arrive_expect_tx(&sm.x_full[s], XB + gpb * R * 4);
-                tma_load_2d(xs + s * XB, &tm_x, at.kb * L4_BLOCK, at.rb * R, &sm.x_full[s]);
-                tma_load_2d(xs + s * XB + XB / 2, &tm_x, at.kb * L4_BLOCK + 64, at.rb * R, &sm.x_full[s]);
-                const float *from = p.sums + static_cast<int64_t>(at.kb) * gpb * p.rows_pad + at.rb * R;
+                mbar_arrive_expect_tx(&sm.x_full[s], SB * (XB + gpb * R * 4));
 #pragma unroll
-                for (int j = 0; j < gpb; ++j, from += p.rows_pad)
-                    bulk_g2s(sums + (s * gpb + j) * R, from, R * 4, &sm.x_full[s]);
+                for (int h = 0; h < 2 * SB; ++h)
+                    tma_load_2d(xs + (s * 2 * SB + h) * (XB / 2), &tm_x, at.kb * L4_BLOCK + h * 64, at.rb * R, &sm.x_full[s]);
+                // sums [row block][group][R]: a stage's lie together
+                bulk_g2s(sums + s * SB * gpb * R, p.sums + (static_cast<int64_t>(at.rb) * 2 * p.kpairs + at.kb) * gpb * R,
+                         SB * gpb * R * 4, &sm.x_full[s]);
+#pragma unroll
+                for (int h = 0; h < SB; ++h) at.next(p);
             }
             // Leave no copy in flight into this CTA's shared memory.  A block is waited for with its scales; after a
             // time-out those may not come, and the copies have the whole limit to land.
@@ -247,11 +250,10 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         uint32_t d = 0;
         bool ok = true;
         for (int i = 0; ok && i < total; ++i) {
-            const int s = i % XS, sa = i / 2 % T4_AS;
-            if (i % 2 == 0) ok = t4_wait(sm, &sm.a_full[sa], static_cast<uint32_t>(i / 2 / T4_AS) & 1);
-            ok = ok && t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / XS) & 1);
-            if (!__all_sync(FULL, ok)) break;
-            const uint64_t b0 = x0 + (s * XB >> 4);
+            const int s = i / SB % XS, sa = i / 2 % T4_AS;
+            if (i % SB == 0) ok = __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / SB / XS) & 1));
+            if (!ok) break;
+            const uint64_t b0 = x0 + ((s * SB + i % SB) * XB >> 4);
             const uint32_t a0 = tmem_a + sa * 128 + i % 2 * 64;
 #pragma unroll
             for (int j = 0; j < gpb; ++j, ++d) {
@@ -268,14 +270,14 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                         if (k == 0) mma_bf16_ts<false>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
                         else mma_bf16_ts<true>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
                     }
-                    if (d % U == U - 1 || (i == total - 1 && j == gpb - 1)) mma_commit(&sm.d_full[u % (DS / U)]);
+                    if (d % U == U - 1) mma_commit(&sm.d_full[u % (DS / U)]), mbar_arrive(&sm.d_full[u % (DS / U)]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
             if (leader) {
                 if (i % 2) mma_commit(&sm.a_empty[sa]);
-                mma_commit(&sm.x_empty[s]);
+                if (i % SB == SB - 1) mma_commit(&sm.x_empty[s]);
             }
             __syncwarp();
         }
@@ -370,8 +372,8 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sm.a_full[sa]);
-                mbar_arrive(&sm.x_full[2 * i % XS]), mbar_arrive(&sm.x_full[(2 * i + 1) % XS]);
+#pragma unroll
+                for (int j = 0; j < 2 / SB; ++j) mbar_arrive(&sm.x_full[(2 / SB * i + j) % XS]);
             }
             if (c < pairs) copy(st), ++issued;
             if (++st == RING) st = 0, ++round;
@@ -395,18 +397,17 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
 #pragma unroll
                 for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
                 for (int kb = 0; ok && kb < 2 * p.kpairs; ++kb, ++i) {
-                    const int s = i % XS;
-                    ok = __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / XS) & 1));
+                    const int s = i / SB % XS;
 #pragma unroll
                     for (int j = 0; j < gpb; ++j, ++d) {
-                        const float2 side = sides[((i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane];
                         const uint32_t u = d / U;
                         if (d % U == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[u % (DS / U)], (u / (DS / U)) & 1));
                         if (!ok) break;
                         tc_fence_after();
+                        const float2 side = sides[((i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane];
                         const uint64_t s2 = pack2(__float_as_uint(side.x), __float_as_uint(side.x));
                         const uint64_t z2 = pack2(__float_as_uint(side.y), __float_as_uint(side.y));
-                        const float *xg = sums + (s * gpb + j) * R + half * RH;
+                        const float *xg = sums + ((s * SB + i % SB) * gpb + j) * R + half * RH;
                         constexpr int CH = RH < 16 ? RH : RH < 32 ? 16 : 32;
 #pragma unroll
                         for (int c = 0; c < RH; c += CH) {
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                         }
                     }
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
+                    if (i % SB == SB - 1 && ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
                 }
                 // the roots of columns l and 32 + l
                 const int64_t r0 = static_cast<int64_t>(rb) * R + half * RH;
@@ -472,7 +473,7 @@ template <int RH, int LG>
 static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, cudaStream_t s) {
     auto fn = &k_linear4_tc<RH, LG>;
     constexpr int R = RH * 2;
-    constexpr size_t smem = 1024 + t4_stages(RH) * (R * L4_BLOCK * 2 + (R * 4 << LG)) + 4 * t4_sets(RH) * t4_ring(RH) * 4096 +
+    constexpr size_t smem = 1024 + T4_XS * t4_blocks(RH) * (R * L4_BLOCK * 2 + (R * 4 << LG)) + 4 * t4_sets(RH) * t4_ring(RH) * 4096 +
                         (t4_sides(LG) * T4_M * 8 << LG);
     static_assert(smem + sizeof(Tc4Shared) <= 227 * 1024, "shared memory of a CTA");
     blocks_per_sm(reinterpret_cast<const void *>(fn), t4_threads(RH), smem);  // raises the shared-memory limit once per device
@@ -512,21 +513,21 @@ dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const d
     p.lg = w->group == 128 ? 0 : w->group == 64 ? 1 : 2;
     p.G = static_cast<int>(groups_of(w));
     p.kpairs = static_cast<int>(kp / (2 * L4_BLOCK));
-    p.rows_pad = t4_pad(rows);
-    p.rblocks = static_cast<int>(p.rows_pad / R);
+    const int64_t rows_pad = t4_pad(rows);
+    p.rblocks = static_cast<int>(rows_pad / R);
     p.tiles = (w->N + T4_M - 1) / T4_M;
     uint16_t *xp = static_cast<uint16_t *>(ws);
-    float *sums = reinterpret_cast<float *>(xp + p.rows_pad * kp);
-    float *root = sums + p.rows_pad * (kp / 32);
+    float *sums = reinterpret_cast<float *>(xp + rows_pad * kp);
+    float *root = sums + rows_pad * (kp / 32);
     p.sums = sums, p.root = root;
     scan_hold(&p.hold, &p.hold_cycles);
     CUtensorMap tm;
-    if (!make_map_k64(&tm, xp, static_cast<uint64_t>(kp), static_cast<uint64_t>(p.rows_pad), static_cast<uint32_t>(R)))
+    if (!make_map_k64(&tm, xp, static_cast<uint64_t>(kp), static_cast<uint64_t>(rows_pad), static_cast<uint32_t>(R)))
         return DFLASH2_ERR_CUDA;
     CUtensorMap tc;
     if (!codes_map(&tc, w)) return DFLASH2_ERR_CUDA;
-    k_linear4_rows<<<static_cast<unsigned>(p.rows_pad), 256, 0, s>>>(x, rows, x_stride, static_cast<int>(w->K), p.lg,
-                                                                     2 * p.kpairs, p.rows_pad, xp, sums, root);
+    k_linear4_rows<<<static_cast<unsigned>(rows_pad), 256, 0, s>>>(x, rows, x_stride, static_cast<int>(w->K), p.lg,
+                                                                     2 * p.kpairs, R, xp, sums, root);
     const dflash2_status st = after_launch();
     if (st != DFLASH2_OK) return st;
     return R == 16 ? launch_tc4_groups<8>(tm, tc, p, s) : R == 32 ? launch_tc4_groups<16>(tm, tc, p, s) : R == 64 ? launch_tc4_groups<32>(tm, tc, p, s)
