@@ -32,12 +32,13 @@ namespace dfl {
 
 static __device__ unsigned int g_err_linear4;
 
-// Warps: 8 for the epilogue, the operand's 4 (where the epilogue needs 128 registers a thread) or 8, copies of x', MMAs.
-constexpr int t4_sets(int rh) { return rh > 32 ? 1 : 2; }
-constexpr int t4_threads(int rh) { return (8 + 4 * t4_sets(rh) + 2) * 32; }
-constexpr int T4_XS = 4;                                        // stages of x'
+// Warps: 8 for the epilogue, the operand's 4 (where the exact epilogue needs 128 registers a thread) or 8, copies of x',
+// MMAs.
+constexpr int t4_sets(int rh, bool exact) { return exact && rh > 32 ? 1 : 2; }
+constexpr int t4_threads(int rh, bool exact) { return (8 + 4 * t4_sets(rh, exact) + 2) * 32; }
+constexpr int T4_XS = 4;                                     // stages of x'
 constexpr int t4_blocks(int rh) { return rh > 32 ? 1 : 2; }  // of 128 columns in a stage: a barrier costs its waiter 150 cycles
-constexpr int t4_ring(int rh) { return rh > 32 ? 4 : 2; }    // pairs of blocks of codes that an operand warp has room for
+constexpr int t4_ring(int rh, bool exact) { return exact && rh > 32 ? 4 : 2; }  // pairs of blocks of codes that an operand warp has room for
 constexpr int T4_AS = 2;      // pairs of blocks of A in tensor memory
 // Blocks whose scales are kept.  A block's are overwritten when the operand is this many further on: it is at most 4
 // blocks ahead of the last MMA that completed, and that at most T4_DS accumulators (4, 2 or 1 blocks) ahead of the
@@ -74,7 +75,7 @@ struct Tc4 {
 // One CTA per row: x' [rows_pad, kblocks * 128], the groups' sums, the root of the power of two.  Rows past the last are
 // zeros.
 __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t rows, int64_t x_stride, int K, int lg,
-                                                      int kblocks, int R, uint16_t *out, float *sums,
+                                                      int kblocks, int R, bool scaled, uint16_t *out, float *sums,
                                                       float *root) {
     __shared__ uint32_t top;
     const int64_t r = blockIdx.x;
@@ -96,13 +97,18 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
     m = top;
     const int e = x_exponent(m);
     const bool bad = m >= 0x7f800000u;
-    if (threadIdx.x == 0) root[r] = x_root(m, e);
+    if (threadIdx.x == 0) root[r] = scaled || bad ? x_root(m, e) : 1.0f;
     for (int c = threadIdx.x; c < chunks; c += 256) {  // chunks is a multiple of 16: half-warps stay whole
         float v[8] = {};
         if (r < rows) load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
-        float sum = scale8(v, e, bad);
-        for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), sum, d);
-        if ((c & (lanes - 1)) == 0) sums[(r / R * (chunks / lanes) + c / lanes) * R + r % R] = sum;
+        if (!scaled) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = bad ? 0.0f : v[j];
+        } else {
+            float sum = scale8(v, e, bad);
+            for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), sum, d);
+            if ((c & (lanes - 1)) == 0) sums[(r / R * (chunks / lanes) + c / lanes) * R + r % R] = sum;
+        }
         uint4 o;
         o.x = bf16_pair(v[0], v[4]), o.y = bf16_pair(v[1], v[5]), o.z = bf16_pair(v[2], v[6]), o.w = bf16_pair(v[3], v[7]);
         *reinterpret_cast<uint4 *>(out + (r * kblocks * L4_BLOCK + c * 8)) = o;
@@ -126,14 +132,24 @@ __device__ __forceinline__ bool t4_wait(Tc4Shared &sm, uint64_t *bar, uint32_t p
     return false;
 }
 
-template <bool ACCUMULATE>
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -178,14 +194,15 @@ struct Walk4 {
     }
 };
 
-// RH: half of the block's rows of x, the columns of an epilogue warp.  LG: log2 of the groups in a block.
-template <int RH, int LG>
-__global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x,
+// RH: half of the block's rows of x, the columns of an epilogue warp.  LG: log2 of the groups in a block.  EXACT: the
+// operand is the codes; otherwise it is the weights in bf16.
+template <int RH, int LG, bool EXACT>
+__global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x,
                                                               const __grid_constant__ CUtensorMap tm_c, const Tc4 p) {
     constexpr int R = RH * 2, XB = R * L4_BLOCK * 2;  // bytes of a stage of x'
     constexpr int gpb = 1 << LG, STEPS = 8 >> LG;      // groups of a block, steps of 16 columns in a group
     constexpr int T4_SIDES = t4_sides(LG);
-    constexpr int XS = T4_XS, SB = t4_blocks(RH), RING = t4_ring(RH), SETS = t4_sets(RH), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
+    constexpr int XS = T4_XS, SB = t4_blocks(RH), RING = t4_ring(RH, EXACT), SETS = t4_sets(RH, EXACT), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
     extern __shared__ unsigned char raw[];
     __shared__ Tc4Shared sm;
     unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -197,7 +214,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         // A stage is there when x' has landed and the operand's four warps have left its blocks in tensor memory and
         // their scales; it is free after its MMAs and the epilogue's warps.  Accumulators are there when their MMAs are
         // done and the warp that issued them, which has seen the stage's rest, says so.
-        for (int i = 0; i < XS; ++i) mbar_init(&sm.x_full[i], 5), mbar_init(&sm.x_empty[i], 9);
+        for (int i = 0; i < XS; ++i) mbar_init(&sm.x_full[i], 5), mbar_init(&sm.x_empty[i], EXACT ? 9 : 1);
         for (int i = 0; i < T4_AS; ++i) mbar_init(&sm.a_empty[i], 1);
         for (int i = 0; i < 4 * SETS; ++i)
             for (int j = 0; j < RING; ++j) mbar_init(&sm.c_full[i][j], 1);
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
     __syncthreads();
     tc_fence_after();
     // accumulators, and how many of them the epilogue is given at a time
-    constexpr uint32_t DS = R > 64 ? 2 : 4, U = R > 64 ? 1 : 2;
+    constexpr uint32_t DS = R > 64 || !EXACT ? 2 : 4, U = R > 64 || !EXACT ? 1 : 2;
     const uint32_t tmem = sm.tmem, tmem_a = tmem + DS * R;
     const int mine = static_cast<int>((p.tiles - blockIdx.x - 1) / gridDim.x) + 1;  // tiles of this CTA
     const int total = mine * p.rblocks * p.kpairs * 2;                              // and their blocks
@@ -226,13 +243,14 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             for (; ok && i < total / SB; ++i) {
                 const int s = i % XS;
                 if (i >= XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / XS - 1) & 1)) break;
-                mbar_arrive_expect_tx(&sm.x_full[s], SB * (XB + gpb * R * 4));
+                mbar_arrive_expect_tx(&sm.x_full[s], SB * (XB + (EXACT ? gpb * R * 4 : 0)));
 #pragma unroll
                 for (int h = 0; h < 2 * SB; ++h)
                     tma_load_2d(xs + (s * 2 * SB + h) * (XB / 2), &tm_x, at.kb * L4_BLOCK + h * 64, at.rb * R, &sm.x_full[s]);
                 // sums [row block][group][R]: a stage's lie together
-                bulk_g2s(sums + s * SB * gpb * R, p.sums + (static_cast<int64_t>(at.rb) * 2 * p.kpairs + at.kb) * gpb * R,
-                         SB * gpb * R * 4, &sm.x_full[s]);
+                if (EXACT)
+                    bulk_g2s(sums + s * SB * gpb * R, p.sums + (static_cast<int64_t>(at.rb) * 2 * p.kpairs + at.kb) * gpb * R,
+                             SB * gpb * R * 4, &sm.x_full[s]);
 #pragma unroll
                 for (int h = 0; h < SB; ++h) at.next(p);
             }
@@ -248,6 +266,7 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
         const uint64_t x0 = sw128_desc(xs);
         const bool leader = elect_one();
         uint32_t d = 0;
+        int kb = 0;
         bool ok = true;
         for (int i = 0; ok && i < total; ++i) {
             const int s = i / SB % XS, sa = i / 2 % T4_AS;
@@ -255,26 +274,40 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
             if (!ok) break;
             const uint64_t b0 = x0 + ((s * SB + i % SB) * XB >> 4);
             const uint32_t a0 = tmem_a + sa * 128 + i % 2 * 64;
+            if constexpr (EXACT) {
 #pragma unroll
-            for (int j = 0; j < gpb; ++j, ++d) {
-                // U accumulators at a time
-                const uint32_t u = d / U;
-                if (d % U == 0 && u >= DS / U) ok = __all_sync(FULL, t4_wait(sm, &sm.d_empty[u % (DS / U)], (u / (DS / U) - 1) & 1));
+                for (int j = 0; j < gpb; ++j, ++d) {
+                    // U accumulators at a time
+                    const uint32_t u = d / U;
+                    if (d % U == 0 && u >= DS / U) ok = __all_sync(FULL, t4_wait(sm, &sm.d_empty[u % (DS / U)], (u / (DS / U) - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t to = tmem + (d % DS) * R;
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < STEPS; ++k) {
+                            const int at = j * STEPS + k;  // 16 columns: 32 bytes of x', 8 columns of tensor memory
+                            mma_bf16_ts(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc, k > 0);
+                        }
+                        if (d % U == U - 1) mma_commit(&sm.d_full[u % (DS / U)]), mbar_arrive(&sm.d_full[u % (DS / U)]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            } else {
+                if (kb == 0 && d >= DS) ok = __all_sync(FULL, t4_wait(sm, &sm.d_empty[d % DS], (d / DS - 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t to = tmem + (d % DS) * R;
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < STEPS; ++k) {
-                        const int at = j * STEPS + k;  // 16 columns: 32 bytes of x', 8 columns of tensor memory
-                        if (k == 0) mma_bf16_ts<false>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
-                        else mma_bf16_ts<true>(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc);
-                    }
-                    if (d % U == U - 1) mma_commit(&sm.d_full[u % (DS / U)]), mbar_arrive(&sm.d_full[u % (DS / U)]);
+                    for (int at = 0; at < 8; ++at)
+                        mma_bf16_ts(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc, at > 0 || kb > 0);
+                    if (kb == 2 * p.kpairs - 1) mma_commit(&sm.d_full[d % DS]), mbar_arrive(&sm.d_full[d % DS]);
                 }
                 __syncwarp();
+                if (++kb == 2 * p.kpairs) kb = 0, ++d;
             }
-            if (!ok) break;
             if (leader) {
                 if (i % 2) mma_commit(&sm.a_empty[sa]);
                 if (i % SB == SB - 1) mma_commit(&sm.x_empty[s]);
@@ -354,15 +387,27 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                                  : "r"(ring_row + st * 4096 + (((h * 2 + q) ^ (lane & 7)) << 4)));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t u = v[j] >> 8;
-                        a[q * 16 + j * 4] = v[j] & 0x000f000fu, a[q * 16 + j * 4 + 1] = v[j] & 0x00f000f0u;
-                        a[q * 16 + j * 4 + 2] = u & 0x000f000fu, a[q * 16 + j * 4 + 3] = u & 0x00f000f0u;
+                        uint32_t *o = a + q * 16 + j * 4;
+                        if constexpr (EXACT) {
+                            const uint32_t u = v[j] >> 8;
+                            o[0] = v[j] & 0x000f000fu, o[1] = v[j] & 0x00f000f0u;
+                            o[2] = u & 0x000f000fu, o[3] = u & 0x00f000f0u;
+                        } else {
+                            // 128 + code, less 128 + 8 or (exact) 128 and then the zero point, times the scale
+                            const int gj = (h * 64 + q * 32) >> (7 - LG);
+                            const uint32_t s2 = sr[gj] * 0x10001u, z2 = zr[gj] * 0x10001u;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t t = ((v[j] >> (4 * k)) & 0x000f000fu) | 0x43004300u;
+                                o[k] = mul_bf16x2(p.w.zero ? sub_bf16x2(sub_bf16x2(t, 0x43004300u), z2) : sub_bf16x2(t, 0x43084308u), s2);
+                            }
+                        }
                     }
                 }
                 tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 128 + h * 32, a);
             }
 #pragma unroll
-            for (int j = 0; j < 2 * gpb; ++j) {
+            for (int j = 0; j < (EXACT ? 2 * gpb : 0); ++j) {
                 const float sc = side_of(sr[j], p.w.side_dt);
                 sides[((2 * i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane] =
                     make_float2(sc, -sc * (p.w.zero ? side_of(zr[j], p.w.side_dt) : 8.0f));
@@ -396,45 +441,66 @@ __global__ void __launch_bounds__(t4_threads(RH), 1) k_linear4_tc(const __grid_c
                 uint64_t acc[RH / 2];
 #pragma unroll
                 for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
-                for (int kb = 0; ok && kb < 2 * p.kpairs; ++kb, ++i) {
-                    const int s = i / SB % XS;
+                if constexpr (EXACT) {
+                    for (int kb = 0; ok && kb < 2 * p.kpairs; ++kb, ++i) {
+                        const int s = i / SB % XS;
 #pragma unroll
-                    for (int j = 0; j < gpb; ++j, ++d) {
-                        const uint32_t u = d / U;
-                        if (d % U == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[u % (DS / U)], (u / (DS / U)) & 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const float2 side = sides[((i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane];
-                        const uint64_t s2 = pack2(__float_as_uint(side.x), __float_as_uint(side.x));
-                        const uint64_t z2 = pack2(__float_as_uint(side.y), __float_as_uint(side.y));
-                        const float *xg = sums + ((s * SB + i % SB) * gpb + j) * R + half * RH;
-                        constexpr int CH = RH < 16 ? RH : RH < 32 ? 16 : 32;
+                        for (int j = 0; j < gpb; ++j, ++d) {
+                            const uint32_t u = d / U;
+                            if (d % U == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[u % (DS / U)], (u / (DS / U)) & 1));
+                            if (!ok) break;
+                            tc_fence_after();
+                            const float2 side = sides[((i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane];
+                            const uint64_t s2 = pack2(__float_as_uint(side.x), __float_as_uint(side.x));
+                            const uint64_t z2 = pack2(__float_as_uint(side.y), __float_as_uint(side.y));
+                            const float *xg = sums + ((s * SB + i % SB) * gpb + j) * R + half * RH;
+                            constexpr int CH = RH < 16 ? RH : RH < 32 ? 16 : 32;
 #pragma unroll
-                        for (int c = 0; c < RH; c += CH) {
-                            uint32_t v[CH];
-                            if constexpr (CH == 8) {
-                                tmem_ld8(tm + (d % DS) * R, v);
-                            } else {
+                            for (int c = 0; c < RH; c += CH) {
+                                uint32_t v[CH];
+                                if constexpr (CH == 8) {
+                                    tmem_ld8(tm + (d % DS) * R, v);
+                                } else {
 #pragma unroll
-                                for (int k = 0; k < CH; k += 16) tmem_ld16_nowait(tm + (d % DS) * R + c + k, v + k);
+                                    for (int k = 0; k < CH; k += 16) tmem_ld16_nowait(tm + (d % DS) * R + c + k, v + k);
+                                }
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                                for (int k = 0; k < CH; k += 4) {
+                                    const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(xg + c + k);
+                                    const int at = (c + k) / 2;
+                                    acc[at] = fma2(z2, x2.x, fma2(s2, pack2(v[k], v[k + 1]), acc[at]));
+                                    acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[k + 2], v[k + 3]), acc[at + 1]));
+                                }
                             }
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                            for (int k = 0; k < CH; k += 4) {
-                                const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(xg + c + k);
-                                const int at = (c + k) / 2;
-                                acc[at] = fma2(z2, x2.x, fma2(s2, pack2(v[k], v[k + 1]), acc[at]));
-                                acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[k + 2], v[k + 3]), acc[at + 1]));
+                            if (d % U == U - 1) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&sm.d_empty[u % (DS / U)]);
                             }
                         }
-                        if (d % U == U - 1) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm.d_empty[u % (DS / U)]);
-                        }
+                        __syncwarp();
+                        if (i % SB == SB - 1 && ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
                     }
-                    __syncwarp();
-                    if (i % SB == SB - 1 && ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
+                } else {
+                    ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[d % DS], (d / DS) & 1));
+                    if (ok) {
+                        tc_fence_after();
+                        uint32_t v[RH];
+                        if constexpr (RH == 8) {
+                            tmem_ld8(tm + (d % DS) * R, v);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < RH; c += 16) tmem_ld16_nowait(tm + (d % DS) * R + c, v + c);
+                        }
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int c = 0; c < RH; c += 2) acc[c / 2] = pack2(v[c], v[c + 1]);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.d_empty[d % DS]);
+                        ++d;
+                    }
                 }
                 // the roots of columns l and 32 + l
                 const int64_t r0 = static_cast<int64_t>(rb) * R + half * RH;
@@ -469,24 +535,29 @@ size_t linear4_tc_bytes(int64_t rows, int64_t K) {
     return static_cast<size_t>(t4_pad(rows)) * (t4_kpad(K) * 2 + t4_kpad(K) / 32 * 4 + 4);
 }
 
-template <int RH, int LG>
+template <int RH, int LG, bool EXACT>
 static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, cudaStream_t s) {
-    auto fn = &k_linear4_tc<RH, LG>;
-    constexpr int R = RH * 2;
-    constexpr size_t smem = 1024 + T4_XS * t4_blocks(RH) * (R * L4_BLOCK * 2 + (R * 4 << LG)) + 4 * t4_sets(RH) * t4_ring(RH) * 4096 +
-                        (t4_sides(LG) * T4_M * 8 << LG);
+    auto fn = &k_linear4_tc<RH, LG, EXACT>;
+    constexpr int R = RH * 2, threads = t4_threads(RH, EXACT);
+    constexpr size_t smem = 1024 + T4_XS * t4_blocks(RH) * (R * L4_BLOCK * 2 + (EXACT ? R * 4 << LG : 0)) +
+                            4 * t4_sets(RH, EXACT) * t4_ring(RH, EXACT) * 4096 + (EXACT ? t4_sides(LG) * T4_M * 8 << LG : 0);
     static_assert(smem + sizeof(Tc4Shared) <= 227 * 1024, "shared memory of a CTA");
-    blocks_per_sm(reinterpret_cast<const void *>(fn), t4_threads(RH), smem);  // raises the shared-memory limit once per device
+    blocks_per_sm(reinterpret_cast<const void *>(fn), threads, smem);  // raises the shared-memory limit once per device
     const int64_t sms = sm_count();
-    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), t4_threads(RH), smem, s>>>(tm, tc, p);
+    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), threads, smem, s>>>(tm, tc, p);
     return after_launch();
 }
 
 template <int RH>
-static dflash2_status launch_tc4_groups(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, cudaStream_t s) {
-    if (p.lg == 0) return launch_tc4<RH, 0>(tm, tc, p, s);
-    if (p.lg == 1) return launch_tc4<RH, 1>(tm, tc, p, s);
-    return launch_tc4<RH, 2>(tm, tc, p, s);
+static dflash2_status launch_tc4_groups(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, bool exact, cudaStream_t s) {
+    if (exact) {
+        if (p.lg == 0) return launch_tc4<RH, 0, true>(tm, tc, p, s);
+        if (p.lg == 1) return launch_tc4<RH, 1, true>(tm, tc, p, s);
+        return launch_tc4<RH, 2, true>(tm, tc, p, s);
+    }
+    if (p.lg == 0) return launch_tc4<RH, 0, false>(tm, tc, p, s);
+    if (p.lg == 1) return launch_tc4<RH, 1, false>(tm, tc, p, s);
+    return launch_tc4<RH, 2, false>(tm, tc, p, s);
 }
 
 // Codes [N, bytes of a row], boxes of 32 rows of 128 bytes; zeros past the edges.
@@ -506,6 +577,8 @@ dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const d
     // a CTA's blocks are counted in 31 bits
     if ((w->N / T4_M / sm_count() + 1) * (t4_pad(rows) / t4_rows(rows)) * (t4_kpad(w->K) / L4_BLOCK) > (1 << 30))
         return DFLASH2_ERR_UNSUPPORTED;
+    // f32 results and f32 scales keep their bits; bf16 results are taken on weights in bf16
+    const bool exact = y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
     Tc4 p = {};
     const int R = t4_rows(rows);
     const int64_t kp = t4_kpad(w->K);
@@ -527,11 +600,13 @@ dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const d
     CUtensorMap tc;
     if (!codes_map(&tc, w)) return DFLASH2_ERR_CUDA;
     k_linear4_rows<<<static_cast<unsigned>(rows_pad), 256, 0, s>>>(x, rows, x_stride, static_cast<int>(w->K), p.lg,
-                                                                     2 * p.kpairs, R, xp, sums, root);
+                                                                     2 * p.kpairs, R, exact, xp, sums, root);
     const dflash2_status st = after_launch();
     if (st != DFLASH2_OK) return st;
-    return R == 16 ? launch_tc4_groups<8>(tm, tc, p, s) : R == 32 ? launch_tc4_groups<16>(tm, tc, p, s) : R == 64 ? launch_tc4_groups<32>(tm, tc, p, s)
-                                                                                          : launch_tc4_groups<64>(tm, tc, p, s);
+    if (R == 16) return launch_tc4_groups<8>(tm, tc, p, exact, s);
+    if (R == 32) return launch_tc4_groups<16>(tm, tc, p, exact, s);
+    if (R == 64) return launch_tc4_groups<32>(tm, tc, p, exact, s);
+    return launch_tc4_groups<64>(tm, tc, p, exact, s);
 }
 
 unsigned int read_error_linear4(bool clear) {
