@@ -19,8 +19,7 @@
 //   4 or 8 warps operand and scales: 32 weight rows each; of 8, 4 take the odd pairs of
 //                blocks of 128 columns
 //   2 warps      copies of x', MMAs
-// Tensor memory: 4 accumulators of R columns (2 of 128), 4 blocks of A of 64 columns
-// (two pairs).
+// Tensor memory: 4 accumulators of R columns (2 of 128), 4 blocks of A of 64 columns.
 //
 // Waits are bounded: after a time-out every role stops waiting, the error word
 // is set and the CTA's remaining outputs are NaN.
@@ -39,7 +38,7 @@ constexpr int t4_threads(int rh, bool exact) { return (8 + 4 * t4_sets(rh, exact
 constexpr int T4_XS = 4;                                     // stages of x'
 constexpr int t4_blocks(int rh) { return rh > 32 ? 1 : 2; }  // of 128 columns in a stage: a barrier costs its waiter 150 cycles
 constexpr int t4_ring(int rh, bool exact) { return exact && rh > 32 ? 4 : 2; }  // pairs of blocks of codes that an operand warp has room for
-constexpr int T4_AS = 2;      // pairs of blocks of A in tensor memory
+constexpr int T4_AS = 4;      // blocks of A in tensor memory
 // Blocks whose scales are kept.  A block's are overwritten when the operand is this many further on: it is at most 4
 // blocks ahead of the last MMA that completed, and that at most T4_DS accumulators (4, 2 or 1 blocks) ahead of the
 // epilogue.
@@ -160,14 +159,12 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(p));
     return p != 0;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
@@ -193,6 +190,33 @@ struct Walk4 {
         }
     }
 };
+
+// 128 columns of a weight row, 16 words of codes, into tensor memory.  KIND 0: the codes as they are; 1 and 2: the weights
+// in bf16, without and with zero points, from the groups' bits in bf16.
+template <int LG, int KIND>
+__device__ __forceinline__ void operand(const uint32_t *v, uint32_t to, const uint32_t *sr, const uint32_t *zr) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // 32 columns
+        const uint32_t s2 = sr[q * 32 >> (7 - LG)] * 0x10001u, z2 = zr[q * 32 >> (7 - LG)] * 0x10001u;
+        uint32_t a[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = v[q * 4 + j], u = w >> 8;
+            uint32_t *o = a + j * 4;
+            if constexpr (KIND == 0) {
+                o[0] = w & 0x000f000fu, o[1] = w & 0x00f000f0u, o[2] = u & 0x000f000fu, o[3] = u & 0x00f000f0u;
+            } else {
+                // 128 + code, less 128 + 8 or (exact) 128 and then the zero point, times the scale
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t t = (((k & 2 ? u : w) >> (4 * (k & 1))) & 0x000f000fu) | 0x43004300u;
+                    o[k] = mul_bf16x2(KIND == 2 ? sub_bf16x2(sub_bf16x2(t, 0x43004300u), z2) : sub_bf16x2(t, 0x43084308u), s2);
+                }
+            }
+        }
+        tmem_st16(to + q * 16, a);
+    }
+}
 
 // RH: half of the block's rows of x, the columns of an epilogue warp.  LG: log2 of the groups in a block.  EXACT: the
 // operand is the codes; otherwise it is the weights in bf16.
@@ -269,11 +293,11 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
         int kb = 0;
         bool ok = true;
         for (int i = 0; ok && i < total; ++i) {
-            const int s = i / SB % XS, sa = i / 2 % T4_AS;
+            const int s = i / SB % XS, sa = i % T4_AS;
             if (i % SB == 0) ok = __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / SB / XS) & 1));
             if (!ok) break;
             const uint64_t b0 = x0 + ((s * SB + i % SB) * XB >> 4);
-            const uint32_t a0 = tmem_a + sa * 128 + i % 2 * 64;
+            const uint32_t a0 = tmem_a + sa * 64;
             if constexpr (EXACT) {
 #pragma unroll
                 for (int j = 0; j < gpb; ++j, ++d) {
@@ -309,7 +333,7 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
                 if (++kb == 2 * p.kpairs) kb = 0, ++d;
             }
             if (leader) {
-                if (i % 2) mma_commit(&sm.a_empty[sa]);
+                mma_commit(&sm.a_empty[sa]);
                 if (i % SB == SB - 1) mma_commit(&sm.x_empty[s]);
             }
             __syncwarp();
@@ -370,57 +394,44 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
         load_sides();
         int st = 0;
         uint32_t round = 0;
-        for (int i = odd; i < pairs; i += SETS) {
-            const int sa = i % T4_AS;
-            bool ok = t4_wait(sm, &sm.c_full[me][st], round & 1);
-            if (i >= T4_AS) ok = ok && t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(i / T4_AS - 1) & 1);
-            if (!__all_sync(FULL, ok)) break;
-            tc_fence_after();
+        for (int i = odd, ok = 1; ok && i < pairs; i += SETS) {
+            ok = __all_sync(FULL, t4_wait(sm, &sm.c_full[me][st], round & 1));
+            if (!ok) break;
+            uint32_t v[32];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {  // 64 columns
-                uint32_t a[32];
+            for (int q = 0; q < 8; ++q)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[q * 4]), "=r"(v[q * 4 + 1]), "=r"(v[q * 4 + 2]), "=r"(v[q * 4 + 3])
+                             : "r"(ring_row + st * 4096 + ((q ^ (lane & 7)) << 4)));
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t v[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                 : "r"(ring_row + st * 4096 + (((h * 2 + q) ^ (lane & 7)) << 4)));
+            for (int h = 0; h < 2; ++h) {
+                const int b = 2 * i + h, sa = b % T4_AS;
+                if (b >= T4_AS) ok = __all_sync(FULL, t4_wait(sm, &sm.a_empty[sa], static_cast<uint32_t>(b / T4_AS - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t to = tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 64;
+                if (EXACT) operand<LG, 0>(v + h * 16, to, sr + h * gpb, zr + h * gpb);
+                else if (p.w.zero) operand<LG, 2>(v + h * 16, to, sr + h * gpb, zr + h * gpb);
+                else operand<LG, 1>(v + h * 16, to, sr + h * gpb, zr + h * gpb);
+                if (h == 0) {
+                    __syncwarp();  // every lane has its codes
+                    if (c < pairs) copy(st), ++issued;
+                }
+                if constexpr (EXACT) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t *o = a + q * 16 + j * 4;
-                        if constexpr (EXACT) {
-                            const uint32_t u = v[j] >> 8;
-                            o[0] = v[j] & 0x000f000fu, o[1] = v[j] & 0x00f000f0u;
-                            o[2] = u & 0x000f000fu, o[3] = u & 0x00f000f0u;
-                        } else {
-                            // 128 + code, less 128 + 8 or (exact) 128 and then the zero point, times the scale
-                            const int gj = (h * 64 + q * 32) >> (7 - LG);
-                            const uint32_t s2 = sr[gj] * 0x10001u, z2 = zr[gj] * 0x10001u;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t t = ((v[j] >> (4 * k)) & 0x000f000fu) | 0x43004300u;
-                                o[k] = mul_bf16x2(p.w.zero ? sub_bf16x2(sub_bf16x2(t, 0x43004300u), z2) : sub_bf16x2(t, 0x43084308u), s2);
-                            }
-                        }
+                    for (int j = 0; j < gpb; ++j) {
+                        const float sc = side_of(sr[h * gpb + j], p.w.side_dt);
+                        sides[((b % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane] =
+                            make_float2(sc, -sc * (p.w.zero ? side_of(zr[h * gpb + j], p.w.side_dt) : 8.0f));
                     }
                 }
-                tmem_st32(tmem_a + (static_cast<uint32_t>(quad * 32) << 16) + sa * 128 + h * 32, a);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && b % SB == SB - 1) mbar_arrive(&sm.x_full[b / SB % XS]);
             }
-#pragma unroll
-            for (int j = 0; j < (EXACT ? 2 * gpb : 0); ++j) {
-                const float sc = side_of(sr[j], p.w.side_dt);
-                sides[((2 * i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane] =
-                    make_float2(sc, -sc * (p.w.zero ? side_of(zr[j], p.w.side_dt) : 8.0f));
-            }
+            if (!ok) break;
             load_sides();
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-#pragma unroll
-                for (int j = 0; j < 2 / SB; ++j) mbar_arrive(&sm.x_full[(2 / SB * i + j) % XS]);
-            }
-            if (c < pairs) copy(st), ++issued;
             if (++st == RING) st = 0, ++round;
         }
         // leave no copy in flight
