@@ -45,6 +45,7 @@ constexpr int T4_AS = 4;      // blocks of A in tensor memory
 constexpr int t4_sides(int lg) { return lg == 0 ? 8 : 6; }
 constexpr int T4_DS = 4;      // accumulators, at most: 2 of 128 columns
 constexpr int T4_M = 128;
+constexpr int T4_DOWN = 40;   // weights in bf16 are held times 2^-40: scales from 2^-80 to 2^30 neither vanish nor overflow
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
 struct Tc4Shared {
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
     m = top;
     const int e = x_exponent(m);
     const bool bad = m >= 0x7f800000u;
-    if (threadIdx.x == 0) root[r] = scaled || bad ? x_root(m, e) : 1.0f;
+    if (threadIdx.x == 0) root[r] = scaled || bad ? x_root(m, e) : pow2f(T4_DOWN / 2);
     for (int c = threadIdx.x; c < chunks; c += 256) {  // chunks is a multiple of 16: half-warps stay whole
         float v[8] = {};
         if (r < rows) load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
@@ -140,10 +141,15 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {  // subnormals are kept
     uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
+}
+// A number of bf16, twice.
+__device__ __forceinline__ uint32_t pair_of(float v) {
+    const uint32_t h = __float_as_uint(v) >> 16;
+    return h | h << 16;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -192,25 +198,32 @@ struct Walk4 {
 };
 
 // 128 columns of a weight row, 16 words of codes, into tensor memory.  KIND 0: the codes as they are; 1 and 2: the weights
-// in bf16, without and with zero points, from the groups' bits in bf16.
+// times 2^-T4_DOWN in bf16, without and with zero points, from the groups' bits in bf16.  The masked codes are operands of
+// the fused step as they lie (times 2^-133 or, the second pairs, 2^-129), so that
+//   weight 2^-40 = code * (scale 2^-40) - 8 * (scale 2^-40)           one rounding
+//   with zero points: (code - zero) 2^-40, exact for whole zero points, times the scale.
 template <int LG, int KIND>
 __device__ __forceinline__ void operand(const uint32_t *v, uint32_t to, const uint32_t *sr, const uint32_t *zr) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {  // 32 columns
-        const uint32_t s2 = sr[q * 32 >> (7 - LG)] * 0x10001u, z2 = zr[q * 32 >> (7 - LG)] * 0x10001u;
+        uint32_t first = 0, second = 0, less = 0, scale = 0;
+        if constexpr (KIND != 0) {
+            const float sc = __uint_as_float(sr[q * 32 >> (7 - LG)] << 16);
+            const float f = KIND == 1 ? sc : 1.0f, z = KIND == 1 ? 8.0f * sc : __uint_as_float(zr[q * 32 >> (7 - LG)] << 16);
+            first = pair_of(f * pow2f(133 - T4_DOWN)), second = pair_of(f * pow2f(129 - T4_DOWN));
+            less = pair_of(-z * pow2f(-T4_DOWN)), scale = sr[q * 32 >> (7 - LG)] * 0x10001u;
+        }
         uint32_t a[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t w = v[q * 4 + j], u = w >> 8;
             uint32_t *o = a + j * 4;
-            if constexpr (KIND == 0) {
-                o[0] = w & 0x000f000fu, o[1] = w & 0x00f000f0u, o[2] = u & 0x000f000fu, o[3] = u & 0x00f000f0u;
-            } else {
-                // 128 + code, less 128 + 8 or (exact) 128 and then the zero point, times the scale
+            o[0] = w & 0x000f000fu, o[1] = w & 0x00f000f0u, o[2] = u & 0x000f000fu, o[3] = u & 0x00f000f0u;
+            if constexpr (KIND != 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t t = (((k & 2 ? u : w) >> (4 * (k & 1))) & 0x000f000fu) | 0x43004300u;
-                    o[k] = mul_bf16x2(KIND == 2 ? sub_bf16x2(sub_bf16x2(t, 0x43004300u), z2) : sub_bf16x2(t, 0x43084308u), s2);
+                    o[k] = fma_bf16x2(o[k], k & 1 ? second : first, less);
+                    if (KIND == 2) o[k] = mul_bf16x2(o[k], scale);
                 }
             }
         }

@@ -621,7 +621,9 @@ dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dty
  *   row of NaN.
  *   Sums are f32 sums of exact products of codes and of zero points with x;
  *   entries of x below 2^-130 of their row's largest and scales below 2^-100
- *   lose bits.
+ *   lose bits.  bf16 results for many rows (those that take a workspace) with
+ *   bf16 scales are sums of x times the weights rounded to bf16 (code - zero,
+ *   then its product with the scale); scales from 2^-80 to 2^30.
  * ws: dflash2_linear4_workspace_bytes(dt, rows, N, K) bytes, which is 0 for
  *   few rows (ws may then be NULL).  It needs no zeros and is left with
  *   scratch.
