@@ -9,75 +9,161 @@
 
 namespace dfl {
 
-__device__ __forceinline__ float load_f(const void *p, dflash2_dtype dt, int64_t i) { return side_at(p, dt, i); }
+// ----------------------------------------------------- to codes and back ----
+constexpr float Q4_MAGIC = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number
 
-// One warp per group: scale, zero point, codes.
-__global__ void __launch_bounds__(256) k_quant4(const void *W, dflash2_dtype dt, int64_t ld, dflash2_weight4 w, int64_t G) {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (item >= w.N * G) return;
-    const int64_t n = item / G, gi = item % G;
-    const int64_t k0 = gi * w.group;
-    const int per = w.group / 32;
-    float v[4];
-    float lo = 0.0f, hi = 0.0f;
-    bool bad = false;
-    for (int i = 0; i < per; ++i) {
-        const int64_t k = k0 + lane * per + i;
-        v[i] = k < w.K ? load_f(W, dt, n * ld + k) : 0.0f;
-        bad |= !isfinite(v[i]);
-        lo = fminf(lo, v[i]);
-        hi = fmaxf(hi, v[i]);
-    }
-    bad = __any_sync(FULL, bad);
+struct Quant4 {
+    const void *W;
+    dflash2_weight4 w;
+    int64_t ld;
+    uint32_t pieces;  // of 32 columns in a row, whole groups
+    uint32_t all;     // of them in all rows
+    int codes;        // vectors of 8 columns that have a place in a row
+    int span_log2;    // log2 of the lanes to a row (back)
+    bool vec;
+};
+
+// 32 columns to a thread, so that what a group costs (a scale and two or three divisions) is shared by as many; a group is
+// 4, 2 or 1 neighbouring lanes.  A quotient's whole number comes from the product with the reciprocal; where that (off by
+// at most 2^-18) is next to a half, the entry is read again and divided.
+// Bound: HBM, then the instructions (about 10 to an entry).
+template <bool F32W, int LG>
+__global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
+    constexpr int LANES = 4 >> LG;
+    const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+    const bool row = item < p.all;
+    const uint32_t n32 = row ? item / p.pieces : 0, c = item - n32 * p.pieces;
+    const int64_t n = n32, k0 = static_cast<int64_t>(c) * 32, base = n * p.ld + k0;
+    const int left = !row || k0 >= p.w.K ? 0 : p.w.K - k0 < 32 ? static_cast<int>(p.w.K - k0) : 32;
+    float v[32];
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
+    for (int q = 0; q < 4; ++q) {
+        float(&o)[8] = *reinterpret_cast<float(*)[8]>(v + q * 8);
+        if (left > q * 8) load8<F32W>(p.W, base + q * 8, left - q * 8, p.vec, o);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+    }
+    float lo = 0.0f, hi = 0.0f, none = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        none = fmaf(v[j], 0.0f, none);  // NaN where an entry is not finite
+        lo = fminf(lo, v[j]), hi = fmaxf(hi, v[j]);
+    }
+    hi = none == 0.0f ? hi : __builtin_huge_valf();
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) {
         lo = fminf(lo, __shfl_xor_sync(FULL, lo, d));
         hi = fmaxf(hi, __shfl_xor_sync(FULL, hi, d));
     }
-    float scale = w.zero ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
-    if (w.side_dt == DFLASH2_BF16) scale = __uint_as_float(static_cast<uint32_t>(bf16_bits(scale)) << 16);
-    const float step = scale == 0.0f ? 1.0f : scale;
-    const float zero = w.zero ? fminf(fmaxf(rintf(__fdiv_rn(-lo, step)), 0.0f), 15.0f) : 8.0f;
-    for (int i = 0; i < per; ++i) {
-        const int64_t k = k0 + lane * per + i;
-        const int c = bad ? 8 : static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(v[i], step)) + zero, 0.0f), 15.0f));
-        v[i] = static_cast<float>(k < w.K ? c : 8);
+    if (!row) return;
+    const bool bad = isinf(hi);
+    float scale = p.w.zero ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+    if (p.w.side_dt == DFLASH2_BF16) scale = __uint_as_float(static_cast<uint32_t>(bf16_bits(scale)) << 16);
+    const float step = scale == 0.0f ? 1.0f : scale, inv = __frcp_rn(step);
+    const float zero = p.w.zero ? fminf(fmaxf(rintf(__fdiv_rn(-lo, step)), 0.0f), 15.0f) : 8.0f;
+    uint32_t word[4], open = inv < 1e37f ? 0u : FULL;  // past that, products with the reciprocal say nothing
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        word[q] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float t = v[q * 8 + j] * inv, r = __fadd_rn(__fadd_rn(t, Q4_MAGIC), -Q4_MAGIC);
+            if (!(fabsf(t - r) < 0.49999f)) open |= 1u << (q * 8 + j);
+            const float f = __fadd_rn(fminf(fmaxf(r + zero, 0.0f), 15.0f), Q4_MAGIC);
+            word[q] |= (__float_as_uint(f) & 15u) << (4 * j);
+        }
     }
-    uint8_t *row = static_cast<uint8_t *>(w.codes) + n * w.code_stride;
-    const int64_t end = (w.K + 31) / 32 * 32;
-    for (int i = 0; i < per; ++i) {
-        const int64_t k = k0 + lane * per + i;
-        const float next = per == 1 ? __shfl_down_sync(FULL, v[0], 1) : v[i | 1];
-        if ((k & 1) == 0 && k < end) row[k / 2] = static_cast<uint8_t>(static_cast<int>(v[i]) | (static_cast<int>(next) << 4));
+    if (left < 32) open &= (1u << left) - 1;
+    if (bad) open = 0;
+    while (open) {
+        const int j = __ffs(open) - 1;
+        open &= open - 1;
+        const float q = rintf(__fdiv_rn(side_at(p.W, F32W ? DFLASH2_F32 : DFLASH2_BF16, base + j), step));
+        const uint32_t code = static_cast<uint32_t>(fminf(fmaxf(q + zero, 0.0f), 15.0f)) << (4 * (j & 7)), keep = ~(15u << (4 * (j & 7)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j >> 3 == i) word[i] = (word[i] & keep) | code;
     }
-    if (lane == 0) {
-        if (bad) scale = __uint_as_float(0x7fc00000u);
-        const int64_t at = n * w.side_stride + gi;
-        if (w.side_dt == DFLASH2_F32) {
-            static_cast<float *>(w.scale)[at] = scale;
-            if (w.zero) static_cast<float *>(w.zero)[at] = bad ? 8.0f : zero;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int have = left - q * 8;  // the codes behind the row are 8
+        if (bad || have <= 0) word[q] = 0x88888888u;
+        else if (have < 8) word[q] = (word[q] & ((1u << (4 * have)) - 1)) | (0x88888888u << (4 * have));
+    }
+    if (left > 0)
+        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.w.codes) + n * p.w.code_stride + k0 / 2) =
+            make_uint4(word[0], word[1], word[2], word[3]);
+    if (c % LANES == 0) {
+        const float s = bad ? __uint_as_float(0x7fc00000u) : scale, z = bad ? 8.0f : zero;
+        const int64_t at = n * p.w.side_stride + c / LANES;
+        if (p.w.side_dt == DFLASH2_F32) {
+            static_cast<float *>(p.w.scale)[at] = s;
+            if (p.w.zero) static_cast<float *>(p.w.zero)[at] = z;
         } else {
-            static_cast<uint16_t *>(w.scale)[at] = bf16_bits(scale);
-            if (w.zero) static_cast<uint16_t *>(w.zero)[at] = bf16_bits(bad ? 8.0f : zero);
+            static_cast<uint16_t *>(p.w.scale)[at] = bf16_bits(s);
+            if (p.w.zero) static_cast<uint16_t *>(p.w.zero)[at] = bf16_bits(z);
         }
     }
 }
 
-__device__ __forceinline__ float weight_at(const dflash2_weight4 &w, int64_t n, int64_t k) {
-    const uint8_t b = static_cast<const uint8_t *>(w.codes)[n * w.code_stride + k / 2];
-    const float code = static_cast<float>((k & 1) ? b >> 4 : b & 15);
-    const int64_t at = n * w.side_stride + k / w.group;
-    return (code - (w.zero ? side_at(w.zero, w.side_dt, at) : 8.0f)) * side_at(w.scale, w.side_dt, at);
-}
-
-__global__ void __launch_bounds__(256) k_dequant4(dflash2_weight4 w, void *out, dflash2_dtype dt, int64_t ld) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= w.N * w.K) return;
-    const int64_t n = i / w.K, k = i % w.K;
-    const float v = weight_at(w, n, k);
-    if (dt == DFLASH2_F32) static_cast<float *>(out)[n * ld + k] = v;
-    else static_cast<uint16_t *>(out)[n * ld + k] = bf16_bits(v);
+// Eight columns to a thread (4 bytes of codes, 16 of bf16); a warp takes a row, or several short ones, and reads Q4_AHEAD
+// vectors before it works on them.  Bound: HBM.
+constexpr int Q4_AHEAD = 4;
+template <bool F32W, int LG>
+__global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
+    constexpr int LANES = 16 >> LG;
+    const int lane = threadIdx.x & 31, span = 1 << p.span_log2;
+    const int64_t n = (((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) << (5 - p.span_log2)) + (lane >> p.span_log2);
+    if (n >= p.w.N) return;
+    const uint8_t *codes = static_cast<const uint8_t *>(p.w.codes) + n * p.w.code_stride;
+    for (int c0 = lane & (span - 1); c0 < p.codes; c0 += span * Q4_AHEAD) {
+        uint32_t word[Q4_AHEAD], sb[Q4_AHEAD], zb[Q4_AHEAD];
+#pragma unroll
+        for (int i = 0; i < Q4_AHEAD; ++i) {
+            const int c = c0 + i * span;
+            const int64_t at = n * p.w.side_stride + c / LANES;
+            word[i] = sb[i] = zb[i] = 0;
+            if (c * 8 < p.w.K) {
+                word[i] = *reinterpret_cast<const uint32_t *>(codes + c * 4);
+                sb[i] = side_bits(p.w.scale, p.w.side_dt, at);
+                if (p.w.zero) zb[i] = side_bits(p.w.zero, p.w.side_dt, at);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < Q4_AHEAD; ++i) {
+            const int c = c0 + i * span;
+            const int64_t left = p.w.K - static_cast<int64_t>(c) * 8, at = n * p.ld + c * 8;
+            if (left <= 0) break;
+            const float s = side_of(sb[i], p.w.side_dt), z = p.w.zero ? side_of(zb[i], p.w.side_dt) : 8.0f;
+            float v[8];
+            // 2^23 + code is a float whose low bits are the code
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(((word[i] >> (4 * j)) & 15u) | 0x4b000000u);
+            if (p.w.zero) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = ((v[j] - 8388608.0f) - z) * s;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = (v[j] - 8388616.0f) * s;
+            }
+            if (left >= 8 && p.vec) {
+                if (F32W) {
+                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+                    o[0] = make_float4(v[0], v[1], v[2], v[3]), o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
+                    uint4 o;
+                    o.x = bf16_pair(v[0], v[1]), o.y = bf16_pair(v[2], v[3]), o.z = bf16_pair(v[4], v[5]), o.w = bf16_pair(v[6], v[7]);
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = o;
+                }
+            } else {
+                for (int j = 0; j < 8 && j < left; ++j) {
+                    if (F32W) static_cast<float *>(out)[at + j] = v[j];
+                    else static_cast<uint16_t *>(out)[at + j] = bf16_bits(v[j]);
+                }
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------- few rows: mma ----
@@ -517,14 +603,45 @@ static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
 
 using namespace dfl;
 
+// The sizes that the two kernels share, and their grid.
+static Quant4 quant4_of(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w, bool back, unsigned *grid) {
+    Quant4 p = {};
+    p.W = W, p.w = *w, p.ld = ld;
+    p.pieces = static_cast<uint32_t>(groups_of(w) * (w->group / 32));
+    p.all = static_cast<uint32_t>(w->N * p.pieces);
+    p.codes = static_cast<int>((w->K + 31) / 32) * 4;
+    for (p.span_log2 = 2; p.span_log2 < 5 && (1 << p.span_log2) < p.codes;) ++p.span_log2;
+    p.vec = aligned16(W) && ld * esize(dt) % 16 == 0;
+    const int64_t warps = (w->N + (32 >> p.span_log2) - 1) / (32 >> p.span_log2);
+    *grid = back ? static_cast<unsigned>((warps + 7) / 8) : (p.all + 255) / 256;
+    return p;
+}
+
+// Matrices whose pieces of 32 columns, whole groups, are counted in 32 bits.
+static bool quant4_fits(const dflash2_weight4 *w) {
+    return groups_of(w) * (w->group / 32) <= ((int64_t(1) << 31) - 1) / w->N;
+}
+
+#define DFLASH2_QUANT4_LAUNCH(kernel, f32, ...)                                                      \
+    do {                                                                                             \
+        if (w->group == 128 && (f32)) kernel<true, 0><<<grid, 256, 0, s>>>(__VA_ARGS__);             \
+        else if (w->group == 128) kernel<false, 0><<<grid, 256, 0, s>>>(__VA_ARGS__);                \
+        else if (w->group == 64 && (f32)) kernel<true, 1><<<grid, 256, 0, s>>>(__VA_ARGS__);         \
+        else if (w->group == 64) kernel<false, 1><<<grid, 256, 0, s>>>(__VA_ARGS__);                 \
+        else if (f32) kernel<true, 2><<<grid, 256, 0, s>>>(__VA_ARGS__);                             \
+        else kernel<false, 2><<<grid, 256, 0, s>>>(__VA_ARGS__);                                     \
+    } while (0)
+
 extern "C" dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w,
                                          dflash2_stream stream) {
     if (!dtype_ok(dt) || !weight4_ok(w) || ld < w->K) return DFLASH2_ERR_INVALID_ARG;
     if (w->N == 0) return DFLASH2_OK;
     if (!W || !aligned_to(W, dt)) return DFLASH2_ERR_INVALID_ARG;
-    const int64_t G = groups_of(w), blocks = (w->N * G + 7) / 8;
-    if (w->K > (int64_t(1) << 36) / w->N) return DFLASH2_ERR_UNSUPPORTED;
-    k_quant4<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(W, dt, ld, *w, G);
+    if (!quant4_fits(w)) return DFLASH2_ERR_UNSUPPORTED;
+    unsigned grid;
+    const Quant4 p = quant4_of(W, dt, ld, w, false, &grid);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DFLASH2_QUANT4_LAUNCH(k_quant4, dt == DFLASH2_F32, p);
     return after_launch();
 }
 
@@ -533,9 +650,11 @@ extern "C" dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, 
     if (!dtype_ok(dt) || !weight4_ok(w) || ld < w->K) return DFLASH2_ERR_INVALID_ARG;
     if (w->N == 0) return DFLASH2_OK;
     if (!out || !aligned_to(out, dt)) return DFLASH2_ERR_INVALID_ARG;
-    const int64_t blocks = (w->N * w->K + 255) / 256;
-    if (w->K > (int64_t(1) << 36) / w->N) return DFLASH2_ERR_UNSUPPORTED;
-    k_dequant4<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(*w, out, dt, ld);
+    if (!quant4_fits(w)) return DFLASH2_ERR_UNSUPPORTED;
+    unsigned grid;
+    const Quant4 p = quant4_of(out, dt, ld, w, true, &grid);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DFLASH2_QUANT4_LAUNCH(k_dequant4, dt == DFLASH2_F32, p, out);
     return after_launch();
 }
 

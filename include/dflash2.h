@@ -604,7 +604,7 @@ typedef struct {
  * Errors: INVALID_ARG for a NULL or misaligned pointer (W and out: aligned to
  * their type), N < 0 or above 2^31 - 1, K < 1 or above 2^31 - 129, a group other than 32, 64, 128,
  * strides that are too small or (code_stride) no multiple of 16, ld < K;
- * UNSUPPORTED for matrices of more than 2^36 entries.
+ * UNSUPPORTED for matrices of 2^36 entries and more, counted in whole groups.
  */
 dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w,
                               dflash2_stream stream);
