@@ -27,7 +27,7 @@ struct Quant4 {
 // 4, 2 or 1 neighbouring lanes.  A quotient's whole number comes from the product with the reciprocal; where that (off by
 // at most 2^-18) is next to a half, the entry is read again and divided.
 // Bound: HBM, then the instructions (about 10 to an entry).
-template <bool F32W, int LG>
+template <bool F32W, int LG, bool ZERO>
 __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
     constexpr int LANES = 4 >> LG;
     const uint32_t item = blockIdx.x * 256u + threadIdx.x;
@@ -44,35 +44,43 @@ __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = 0.0f;
     }
-    float lo = 0.0f, hi = 0.0f, none = 0.0f;
+    // NaN propagates through the maxima, infinities are the largest
+    float lo = 0.0f, hi = 0.0f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-        none = fmaf(v[j], 0.0f, none);  // NaN where an entry is not finite
-        lo = fminf(lo, v[j]), hi = fmaxf(hi, v[j]);
+        hi = fmax_nan(hi, ZERO ? v[j] : fabsf(v[j]));
+        if (ZERO) lo = -fmax_nan(-lo, -v[j]);
     }
-    hi = none == 0.0f ? hi : __builtin_huge_valf();
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(FULL, lo, d));
-        hi = fmaxf(hi, __shfl_xor_sync(FULL, hi, d));
+        hi = fmax_nan(hi, __shfl_xor_sync(FULL, hi, d));
+        if (ZERO) lo = -fmax_nan(-lo, -__shfl_xor_sync(FULL, lo, d));
     }
     if (!row) return;
-    const bool bad = isinf(hi);
-    float scale = p.w.zero ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+    const bool bad = !(fmax_nan(hi, -lo) < __builtin_huge_valf());
+    float scale = ZERO ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)) : __fdiv_rn(hi, 7.0f);
     if (p.w.side_dt == DFLASH2_BF16) scale = __uint_as_float(static_cast<uint32_t>(bf16_bits(scale)) << 16);
     const float step = scale == 0.0f ? 1.0f : scale, inv = __frcp_rn(step);
-    const float zero = p.w.zero ? fminf(fmaxf(rintf(__fdiv_rn(-lo, step)), 0.0f), 15.0f) : 8.0f;
-    uint32_t word[4], open = inv < 1e37f ? 0u : FULL;  // past that, products with the reciprocal say nothing
+    const float zero = ZERO ? fminf(fmaxf(rintf(__fdiv_rn(-lo, step)), 0.0f), 15.0f) : 8.0f;
+    // Past 2^-123, where a scale has its full bits, quotients without zero points stay within 7.1: nothing to clamp.  Four
+    // codes are added up as one float below 2^24.
+    uint32_t word[4], open = step > 1e-37f ? 0u : FULL;
+    const float most = 15.0f - zero;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        word[q] = 0;
+        float four[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float t = v[q * 8 + j] * inv, r = __fadd_rn(__fadd_rn(t, Q4_MAGIC), -Q4_MAGIC);
-            if (!(fabsf(t - r) < 0.49999f)) open |= 1u << (q * 8 + j);
-            const float f = __fadd_rn(fminf(fmaxf(r + zero, 0.0f), 15.0f), Q4_MAGIC);
-            word[q] |= (__float_as_uint(f) & 15u) << (4 * j);
+        for (int h = 0; h < 2; ++h) {
+            four[h] = 8388608.0f + zero * 4369.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = v[q * 8 + h * 4 + j], r = __fadd_rn(fmaf(x, inv, Q4_MAGIC), -Q4_MAGIC);
+                if (!(fabsf(fmaf(x, inv, -r)) < 0.49999f)) open |= 1u << (q * 8 + h * 4 + j);
+                const float held = ZERO ? fminf(fmaxf(r, -zero), most) : r;
+                four[h] = fmaf(held, static_cast<float>(1 << (4 * j)), four[h]);
+            }
         }
+        word[q] = (__float_as_uint(four[0]) & 0xffffu) | (__float_as_uint(four[1]) << 16);
     }
     if (left < 32) open &= (1u << left) - 1;
     if (bad) open = 0;
@@ -622,15 +630,23 @@ static bool quant4_fits(const dflash2_weight4 *w) {
     return groups_of(w) * (w->group / 32) <= ((int64_t(1) << 31) - 1) / w->N;
 }
 
-#define DFLASH2_QUANT4_LAUNCH(kernel, f32, ...)                                                      \
-    do {                                                                                             \
-        if (w->group == 128 && (f32)) kernel<true, 0><<<grid, 256, 0, s>>>(__VA_ARGS__);             \
-        else if (w->group == 128) kernel<false, 0><<<grid, 256, 0, s>>>(__VA_ARGS__);                \
-        else if (w->group == 64 && (f32)) kernel<true, 1><<<grid, 256, 0, s>>>(__VA_ARGS__);         \
-        else if (w->group == 64) kernel<false, 1><<<grid, 256, 0, s>>>(__VA_ARGS__);                 \
-        else if (f32) kernel<true, 2><<<grid, 256, 0, s>>>(__VA_ARGS__);                             \
-        else kernel<false, 2><<<grid, 256, 0, s>>>(__VA_ARGS__);                                     \
-    } while (0)
+template <bool F32W, int LG>
+static void launch_quant4(const Quant4 &p, unsigned grid, cudaStream_t s) {
+    if (p.w.zero) k_quant4<F32W, LG, true><<<grid, 256, 0, s>>>(p);
+    else k_quant4<F32W, LG, false><<<grid, 256, 0, s>>>(p);
+}
+template <bool F32W>
+static void launch_quant4_groups(const Quant4 &p, unsigned grid, cudaStream_t s) {
+    if (p.w.group == 128) launch_quant4<F32W, 0>(p, grid, s);
+    else if (p.w.group == 64) launch_quant4<F32W, 1>(p, grid, s);
+    else launch_quant4<F32W, 2>(p, grid, s);
+}
+template <bool F32W>
+static void launch_dequant4(const Quant4 &p, void *out, unsigned grid, cudaStream_t s) {
+    if (p.w.group == 128) k_dequant4<F32W, 0><<<grid, 256, 0, s>>>(p, out);
+    else if (p.w.group == 64) k_dequant4<F32W, 1><<<grid, 256, 0, s>>>(p, out);
+    else k_dequant4<F32W, 2><<<grid, 256, 0, s>>>(p, out);
+}
 
 extern "C" dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w,
                                          dflash2_stream stream) {
@@ -641,7 +657,8 @@ extern "C" dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_
     unsigned grid;
     const Quant4 p = quant4_of(W, dt, ld, w, false, &grid);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    DFLASH2_QUANT4_LAUNCH(k_quant4, dt == DFLASH2_F32, p);
+    if (dt == DFLASH2_F32) launch_quant4_groups<true>(p, grid, s);
+    else launch_quant4_groups<false>(p, grid, s);
     return after_launch();
 }
 
@@ -654,7 +671,8 @@ extern "C" dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, 
     unsigned grid;
     const Quant4 p = quant4_of(out, dt, ld, w, true, &grid);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    DFLASH2_QUANT4_LAUNCH(k_dequant4, dt == DFLASH2_F32, p, out);
+    if (dt == DFLASH2_F32) launch_dequant4<true>(p, out, grid, s);
+    else launch_dequant4<false>(p, out, grid, s);
     return after_launch();
 }
 
