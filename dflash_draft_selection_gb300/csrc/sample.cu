@@ -66,7 +66,9 @@ struct alignas(128) SampleSmem {
     u64 go_a, go_b;
     uint32_t go_key, go_n;
     // the first CTA's alone
-    uint32_t list_n[3];  // one for a call of find in turn: a CTA may still read the last call's
+    uint32_t list_n[4];  // one for a call of find in turn: a CTA may still read the last call's; and the short list's
+    uint32_t floor_bin[2];
+    int go_i[3];
     u64 hit_above_n, hit_above_m;
     uint32_t hit_bin;
 };
@@ -128,9 +130,8 @@ struct Mass {
         const float f1 = fmaf(S, up, S_MAGIC), n1 = f1 - S_MAGIC;
         const float rest = fmaf(S, up, -n1);
         const float f2 = fmaf(fmaf(Se, up, rest), __int_as_float((127 + shift - 22) << 23), S_MAGIC);
-        const long long hi = __float_as_int(f1) - __float_as_int(S_MAGIC);
-        const long long lo = __float_as_int(f2) - __float_as_int(S_MAGIC);
-        return static_cast<u64>((hi << (shift - 22)) + lo);
+        const int hi = __float_as_int(f1) - __float_as_int(S_MAGIC), lo = __float_as_int(f2) - __float_as_int(S_MAGIC);
+        return static_cast<u64>(static_cast<long long>(hi) * (1 << (shift - 22)) + lo);
     }
     // Its value, rounded once.
     template <bool BF16>
@@ -281,6 +282,26 @@ struct Sampler {
         __syncthreads();
     }
 
+    // First CTA: the first cnt of the list, descending (bitonic), behind a barrier.
+    __device__ void sort_list(int cnt) {
+        int pow = 32;
+        while (pow < cnt) pow *= 2;
+        for (int i = threadIdx.x; i < pow; i += S_THREADS)
+            if (i >= cnt) sm->list[i] = 0;
+        __syncthreads();
+        for (int k = 2; k <= pow; k *= 2)
+            for (int j = k / 2; j > 0; j /= 2) {
+                for (int i = threadIdx.x; i < pow / 2; i += S_THREADS) {
+                    const int a = 2 * j * (i / j) + i % j, b = a + j;
+                    const u64 x = sm->list[a], y = sm->list[b];
+                    if ((x < y) == ((a & k) == 0)) sm->list[a] = y, sm->list[b] = x;
+                }
+                if (pow > 64) __syncthreads();
+                else __syncwarp();
+            }
+        __syncthreads();
+    }
+
     // Where the ranking's running count or mass reaches `target` (known to the first CTA; within the totals).  In the
     // first CTA: the running mass there (with the token), its key, and its id or, for a key with many ties, -1 and
     // which of them it is.
@@ -384,23 +405,7 @@ struct Sampler {
         }
         if (rank == 0) {
             const int cnt = static_cast<int>(*my_n);
-            int pow = 32;
-            while (pow < cnt) pow *= 2;
-            for (int i = threadIdx.x; i < pow; i += S_THREADS)
-                if (i >= cnt) sm->list[i] = 0;
-            __syncthreads();
-            // descending bitonic sort
-            for (int k = 2; k <= pow; k *= 2)
-                for (int j = k / 2; j > 0; j /= 2) {
-                    for (int i = threadIdx.x; i < pow / 2; i += S_THREADS) {
-                        const int a = 2 * j * (i / j) + i % j, b = a + j;
-                        const u64 x = sm->list[a], y = sm->list[b];
-                        if ((x < y) == ((a & k) == 0)) sm->list[a] = y, sm->list[b] = x;
-                    }
-                    if (pow > 64) __syncthreads();
-                    else __syncwarp();
-                }
-            __syncthreads();
+            sort_list(cnt);
             // running masses, two elements to a thread
             const int i0 = threadIdx.x * 2;
             u64 q[2];
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
     }
     if (a.min_p) min_p = a.min_p[r / a.rows_per_param];
     const float u = a.u[r];
-    if (threadIdx.x < 3) sm->list_n[threadIdx.x] = 0;
+    if (threadIdx.x < 4) sm->list_n[threadIdx.x] = 0;
     if (threadIdx.x < 32) {
         const double v = exp2(-static_cast<double>(threadIdx.x) / 32);
         const float h = static_cast<float>(v);
@@ -578,23 +583,108 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
     s.t_scale = S_BINS / s.t_cap;
     const bool by_k = top_k > 0 && top_k < a.V;
     u64 total_n = 0, total_m = 0;
-    if (by_k && top_k <= C * S_THREADS / 2) {
-        // the top_k-th largest of the threads' maxima is a floor: at least top_k tokens reach it
+    if (by_k && top_k <= C * S_THREADS) {
+        // A floor that at least top_k tokens reach: the best CTA's top_k-th largest of its threads' maxima, or the worst
+        // CTA's (top_k / C)-th, whichever is higher.
         s.clear(true);
         const float t = s.mass.template t_of<BF16>(mine);
         if (s.inside(mine, t)) atomicAdd(&sm->cnt[s.bin_of(t)], 1u);
-        cluster_sync();
-        if (s.rank == 0) {
-            s.gather_bins(&total_n, &total_m);
-            if (threadIdx.x == 0) sm->hit_bin = S_BINS - 1;
-            __syncthreads();
-            s.find_bin(false, top_k, 0, 0, total_n, total_m);
-            if (threadIdx.x < C) peer(&sm->go_n, threadIdx.x)[0] = sm->hit_bin;
+        __syncthreads();
+        const uint4 c4 = *reinterpret_cast<const uint4 *>(sm->cnt + threadIdx.x * S_PER);
+        uint32_t c[S_PER] = {c4.x, c4.y, c4.z, c4.w}, run = c4.x + c4.y + c4.z + c4.w;
+        run = warp_scan(run, s.lane) - run;
+        if (s.lane == 31) sm->sum[s.warp] = run + c4.x + c4.y + c4.z + c4.w;
+        if (threadIdx.x < 2) sm->floor_bin[threadIdx.x] = S_BINS - 1;
+        __syncthreads();
+        for (int i = 0; i < s.warp; ++i) run += static_cast<uint32_t>(sm->sum[i]);
+        const uint32_t part = (top_k + C - 1) / C;
+#pragma unroll
+        for (int j = 0; j < S_PER; ++j) {
+            const uint32_t next = run + c[j];
+            if (run < static_cast<uint32_t>(top_k) && next >= static_cast<uint32_t>(top_k)) sm->floor_bin[0] = threadIdx.x * S_PER + j;
+            if (run < part && next >= part) sm->floor_bin[1] = threadIdx.x * S_PER + j;
+            run = next;
         }
+        __syncthreads();
+        if (threadIdx.x < C) peer(&sm->in_word[s.rank], threadIdx.x)[0] = (static_cast<u64>(sm->floor_bin[0]) << 32) | sm->floor_bin[1];
         cluster_sync();
+        uint32_t best = S_BINS - 1, worst = 0;
+        for (int q = 0; q < C; ++q)
+            best = min(best, static_cast<uint32_t>(sm->in_word[q] >> 32)), worst = max(worst, static_cast<uint32_t>(sm->in_word[q]));
         // up to the bin's far end, and a little more for the rounding of the bins
-        s.t_cap = fminf(s.t_cap, (static_cast<float>(sm->go_n + 1) / s.t_scale) * 1.00001f);
+        s.t_cap = fminf(s.t_cap, (static_cast<float>(min(best, worst) + 1) / s.t_scale) * 1.00001f);
         s.t_scale = S_BINS / s.t_cap;
+    }
+    if ((by_k && top_k <= S_LIST / 2) || s.z_floor > NEG_INF) {
+        // few tokens, perhaps: all of them into the first CTA's list, which then answers everything
+        uint32_t *list_n = peer(&sm->list_n[3], 0);
+        u64 *list = peer(sm->list, 0);
+        s.each([&](float z, int i) {
+            if (s.inside(z, s.mass.template t_of<BF16>(z))) {
+                const uint32_t at = atomicAdd(list_n, 1u);
+                if (at < S_LIST) list[at] = (static_cast<u64>(s.key_of(z)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(s.id0 + i));
+            }
+        });
+        cluster_sync();
+        const uint32_t many = *list_n;
+        if (many <= S_LIST) {
+            if (s.rank != 0) {
+                __syncwarp();
+                asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the count has been read
+                return;
+            }
+            s.sort_list(static_cast<int>(many));
+            u64 *mass = reinterpret_cast<u64 *>(sm->cnt);  // running masses of the ranking
+            const int i0 = threadIdx.x * 2;
+            u64 q[2];
+            uint32_t kept = 0;  // of this thread's, by min_p
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float z = ord2f(static_cast<uint32_t>(sm->list[i0 + j] >> 32));
+                const bool in = i0 + j < static_cast<int>(many);
+                q[j] = in ? s.mass.template of<BF16>(z) : 0;
+                kept += in && z >= z_min;
+            }
+            const u64 inc = warp_scan(q[0] + q[1], s.lane);
+            if (s.lane == 31) sm->sum[s.warp] = inc;
+            kept = __reduce_add_sync(FULL, kept);
+            if (s.lane == 0) sm->sum2[s.warp] = kept;
+            if (threadIdx.x < 3) sm->go_i[threadIdx.x] = S_LIST;
+            __syncthreads();
+            u64 run = inc - q[0] - q[1];
+            uint32_t keep = by_k ? min(many, static_cast<uint32_t>(top_k)) : many, floor_n = 0;
+            for (int i = 0; i < S_WARPS; ++i) {
+                if (i < s.warp) run += sm->sum[i];
+                floor_n += static_cast<uint32_t>(sm->sum2[i]);
+            }
+            mass[i0] = run + q[0], mass[i0 + 1] = run + q[0] + q[1];
+            __syncthreads();
+            // the first place whose running mass reaches a goal
+            auto place = [&](u64 goal, int slot) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const u64 before = i0 + j ? mass[i0 + j - 1] : 0;
+                    if (before < goal && mass[i0 + j] >= goal) sm->go_i[slot] = i0 + j;
+                }
+                __syncthreads();
+                return sm->go_i[slot];
+            };
+            if (top_p < 1.0f) {
+                const u64 goal = __double2ull_ru(static_cast<double>(top_p) * __ull2double_rn(mass[keep - 1]));
+                keep = min(keep, static_cast<uint32_t>(place(goal < 1 ? 1 : goal, 0)) + 1);
+            }
+            if (min_p > 0.0f) keep = min(keep, max(floor_n, 1u));
+            const u64 Z = mass[keep - 1];
+            const u64 goal = __double2ull_rd(static_cast<double>(fminf(fmaxf(u, 0.0f), 1.0f)) * __ull2double_rn(Z)) + 1;
+            const int at = place(goal < Z ? goal : Z, 1);
+            if (threadIdx.x == 0) {
+                const u64 k = sm->list[at];
+                a.token[r] = key_idx(k);
+                a.prob[r] = static_cast<float>(s.mass.template exactly<BF16>(key_val(k), inv_t) / ldexp(__ull2double_rn(Z), -a.shift));
+            }
+            cluster_sync();  // the others' reads of the count
+            return;
+        }
     }
     // ---- masses into bins.  Asked again where a wide bin's splitting has overwritten them.
     u64 kept_min = 0;
