@@ -167,27 +167,75 @@ struct Sampler {
                     : static_cast<const float *>(data)[i];
     }
 
+    __device__ __forceinline__ uint4 vector(int i) const {
+        return *reinterpret_cast<const uint4 *>(static_cast<const char *>(data) + static_cast<size_t>(i) * (16 / VEC));
+    }
+    __device__ __forceinline__ static void split(const uint4 &v, float (&z)[VEC]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (BF16) z[2 * j] = bf16lo(w[j]), z[(2 * j + 1) % VEC] = bf16hi(w[j]);
+            else z[j] = __uint_as_float(w[j]);
+        }
+    }
+    __device__ __forceinline__ void rest(int i, float (&z)[VEC]) const {  // the last, cut vector
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) z[j] = i + j < n ? entry(i + j) : NEG_INF;
+    }
+
     // f(z, place) for every entry of the slice, by vectors dealt to the threads in turn.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
         for (int i = threadIdx.x * VEC; i < n; i += S_THREADS * VEC) {
             float z[VEC];
-            if (i + VEC <= n) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(data) + static_cast<size_t>(i) * (16 / VEC));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (BF16) z[2 * j] = bf16lo(w[j]), z[(2 * j + 1) % VEC] = bf16hi(w[j]);
-                    else z[j] = __uint_as_float(w[j]);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) z[j] = i + j < n ? entry(i + j) : NEG_INF;
-            }
+            if (i + VEC <= n) split(vector(i), z);
+            else rest(i, z);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) f(z[j], i + j);
         }
     }
+    // The same for those with lo <= z <= hi: few.
+    template <class F>
+    __device__ __forceinline__ void each_within(float lo, float hi, F f) const {
+        for (int i = threadIdx.x * VEC; i < n; i += S_THREADS * VEC) {
+            float z[VEC];
+            if (i + VEC <= n) split(vector(i), z);
+            else rest(i, z);
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) any |= z[j] >= lo && z[j] <= hi;
+            if (any)
+#pragma unroll 1
+                for (int j = 0; j < VEC; ++j) {
+                    float x = z[0];
+#pragma unroll
+                    for (int k = 1; k < VEC; ++k) x = k == j ? z[k] : x;
+                    if (x >= lo && x <= hi) f(x, i + j);
+                }
+        }
+    }
+    // This thread's largest entry; NaN if it has one.
+    __device__ __forceinline__ float largest() const {
+        float m = NEG_INF;
+        if (BF16) {
+            uint32_t m2 = 0xff80ff80u;  // two -infinities
+            for (int i = threadIdx.x * VEC; i < n; i += S_THREADS * VEC) {
+                if (i + VEC <= n) {
+                    const uint4 v = vector(i);
+                    m2 = bmax2_nan(m2, bmax2_nan(bmax2_nan(v.x, v.y), bmax2_nan(v.z, v.w)));
+                } else {
+                    for (int j = i; j < n; ++j) m = fmax_nan(m, entry(j));
+                }
+            }
+            m = fmax_nan(m, fmax_nan(bf16lo(m2), bf16hi(m2)));
+        } else {
+            each([&](float z, int) { m = fmax_nan(m, z); });
+        }
+        return m;
+    }
+    // Bounds of z where t lies in [lo, hi], a little further out than rounding goes.
+    __device__ __forceinline__ float z_below(float t) const { return __fsub_rd(mass.m, t * 1.00001f / mass.ch); }
+    __device__ __forceinline__ float z_above(float t) const { return __fsub_ru(mass.m, t * 0.99999f / mass.ch); }
 
     __device__ __forceinline__ int bin_of(float t) const { return min(static_cast<int>(t * t_scale), S_BINS - 1); }
     __device__ __forceinline__ bool inside(float z, float t) const { return t < t_cap && z >= z_floor; }
@@ -328,7 +376,8 @@ struct Sampler {
         ++calls;
         u64 *list = peer(sm->list, 0);
         uint32_t k_min = 0xffffffffu, k_max = 0;
-        each([&](float z, int i) {
+        const float z_lo = z_below(static_cast<float>(bin + 1) / t_scale), z_hi = bin == 0 ? mass.m : z_above(static_cast<float>(bin) / t_scale);
+        each_within(bin == S_BINS - 1 ? fminf(z_lo, z_below(t_cap)) : z_lo, z_hi, [&](float z, int i) {
             const float t = mass.template t_of<BF16>(z);
             if (inside(z, t) && bin_of(t) == bin) {
                 const uint32_t k = key_of(z);
@@ -516,15 +565,9 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
     asm volatile("cp.async.wait_all;" ::: "memory");
 
     // ---- the largest logit
-    float m = NEG_INF;
-    bool bad = false;
-    s.each([&](float z, int) {
-        bad |= !(z < __builtin_huge_valf());
-        m = fmaxf(m, z);
-    });
-    const float mine = m;
-    m = warp_max_f(m);
-    bad = __any_sync(FULL, bad);
+    const float mine = s.largest();
+    bool bad = __any_sync(FULL, !(mine < __builtin_huge_valf()));
+    float m = warp_max_f(mine);
     if (s.lane == 0) sm->sum[s.warp] = (static_cast<u64>(bad) << 32) | __float_as_uint(m);
     __syncthreads();
     for (int i = 0; i < S_WARPS; ++i) {
@@ -619,7 +662,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
         // few tokens, perhaps: all of them into the first CTA's list, which then answers everything
         uint32_t *list_n = peer(&sm->list_n[3], 0);
         u64 *list = peer(sm->list, 0);
-        s.each([&](float z, int i) {
+        s.each_within(fmaxf(s.z_floor, s.z_below(s.t_cap)), m, [&](float z, int i) {
             if (s.inside(z, s.mass.template t_of<BF16>(z))) {
                 const uint32_t at = atomicAdd(list_n, 1u);
                 if (at < S_LIST) list[at] = (static_cast<u64>(s.key_of(z)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(s.id0 + i));
