@@ -57,6 +57,8 @@ struct alignas(128) SampleSmem {
     uint32_t cnt[S_BINS], lo[S_BINS], hi[S_BINS];  // the first CTA's, once added: what lies above the bin
     u64 list[S_LIST];
     float2 root[32];  // 2^(-j/32), and what the float lacks
+    double inv_t, t_log;
+    float ch, cl;
     u64 sum[S_WARPS + 1], sum2[S_WARPS + 1];
     // written by the cluster's CTAs, each in its own place
     float in_max[S_CLUSTER];
@@ -146,6 +148,16 @@ __device__ __forceinline__ T warp_scan(T v, int lane) {
         if (lane >= d) v += o;
     }
     return v;
+}
+
+// Where a running mass has to come to: share of Z, rounded up (at least 1), or just past it (at most Z).
+__device__ __forceinline__ u64 goal_reach(float share, u64 Z) {
+    const u64 g = __double2ull_ru(static_cast<double>(share) * __ull2double_rn(Z));
+    return g < 1 ? 1 : g;
+}
+__device__ __forceinline__ u64 goal_pass(float u, u64 Z) {
+    const u64 g = __double2ull_rd(static_cast<double>(fminf(fmaxf(u, 0.0f), 1.0f)) * __ull2double_rn(Z)) + 1;
+    return g < Z ? g : Z;
 }
 
 template <bool BF16>
@@ -332,6 +344,17 @@ struct Sampler {
 
     // First CTA: the first cnt of the list, descending (bitonic), behind a barrier.
     __device__ void sort_list(int cnt) {
+        if (cnt <= 256) {  // keys are distinct: a key's place is the number of larger ones
+            const u64 mine = threadIdx.x < cnt ? sm->list[threadIdx.x] : 0;
+            int place = 0;
+            if (threadIdx.x < ((cnt + 31) & ~31))
+#pragma unroll 8
+                for (int i = 0; i < cnt; ++i) place += sm->list[i] > mine;
+            __syncthreads();
+            if (threadIdx.x < cnt) sm->list[place] = mine;
+            __syncthreads();
+            return;
+        }
         int pow = 32;
         while (pow < cnt) pow *= 2;
         for (int i = threadIdx.x; i < pow; i += S_THREADS)
@@ -557,10 +580,17 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
     if (a.min_p) min_p = a.min_p[r / a.rows_per_param];
     const float u = a.u[r];
     if (threadIdx.x < 4) sm->list_n[threadIdx.x] = 0;
-    if (threadIdx.x < 32) {
-        const double v = exp2(-static_cast<double>(threadIdx.x) / 32);
+    // 64-bit arithmetic is slow here: one thread's, for all
+    if (threadIdx.x == 0) {
+        const double inv_t = 1.0 / static_cast<double>(T == 0.0f ? 1.0f : T), c = fmin(1.4426950408889634074 * inv_t, 3.0e38);
+        sm->inv_t = inv_t;
+        sm->ch = static_cast<float>(c), sm->cl = static_cast<float>(c - static_cast<double>(sm->ch));
+        sm->t_log = min_p > 0.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0;
+    }
+    if (threadIdx.x >= 32 && threadIdx.x < 64) {
+        const double v = exp2(-static_cast<double>(threadIdx.x - 32) / 32);
         const float h = static_cast<float>(v);
-        sm->root[threadIdx.x] = make_float2(h, static_cast<float>(v - h));
+        sm->root[threadIdx.x - 32] = make_float2(h, static_cast<float>(v - h));
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
@@ -607,17 +637,15 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
         }
         return;
     }
-    const double inv_t = 1.0 / static_cast<double>(T), c = 1.4426950408889634074 * inv_t;
     s.mass.m = m;
-    s.mass.ch = static_cast<float>(fmin(c, 3.0e38));
-    s.mass.cl = static_cast<float>(fmin(c, 3.0e38) - static_cast<double>(s.mass.ch));
+    s.mass.ch = sm->ch, s.mass.cl = sm->cl;
     s.mass.shift = a.shift;
     s.mass.root = sm->root;
     s.t_cap = static_cast<float>(a.shift + 1);
     s.z_floor = NEG_INF;
     float z_min = NEG_INF;  // min_p's tokens: z >= z_min
     if (min_p > 0.0f) {
-        z_min = __double2float_ru(static_cast<double>(m) + static_cast<double>(T) * log(static_cast<double>(min_p)));
+        z_min = __double2float_ru(static_cast<double>(m) + sm->t_log);
         if (top_p == 1.0f) {
             s.z_floor = z_min;
             s.t_cap = fminf(s.t_cap, fmaf(m - z_min, s.mass.ch, 1.0f));
@@ -702,8 +730,9 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
             }
             mass[i0] = run + q[0], mass[i0 + 1] = run + q[0] + q[1];
             __syncthreads();
-            // the first place whose running mass reaches a goal
-            auto place = [&](u64 goal, int slot) {
+            // the first place whose running mass reaches the goal, which one thread works out
+            auto place = [&](int slot) {
+                const u64 goal = sm->go_a;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const u64 before = i0 + j ? mass[i0 + j - 1] : 0;
@@ -713,17 +742,19 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
                 return sm->go_i[slot];
             };
             if (top_p < 1.0f) {
-                const u64 goal = __double2ull_ru(static_cast<double>(top_p) * __ull2double_rn(mass[keep - 1]));
-                keep = min(keep, static_cast<uint32_t>(place(goal < 1 ? 1 : goal, 0)) + 1);
+                if (threadIdx.x == 0) sm->go_a = goal_reach(top_p, mass[keep - 1]);
+                __syncthreads();
+                keep = min(keep, static_cast<uint32_t>(place(0)) + 1);
             }
             if (min_p > 0.0f) keep = min(keep, max(floor_n, 1u));
             const u64 Z = mass[keep - 1];
-            const u64 goal = __double2ull_rd(static_cast<double>(fminf(fmaxf(u, 0.0f), 1.0f)) * __ull2double_rn(Z)) + 1;
-            const int at = place(goal < Z ? goal : Z, 1);
+            if (threadIdx.x == 0) sm->go_a = goal_pass(u, Z);
+            __syncthreads();
+            const int at = place(1);
             if (threadIdx.x == 0) {
                 const u64 k = sm->list[at];
                 a.token[r] = key_idx(k);
-                a.prob[r] = static_cast<float>(s.mass.template exactly<BF16>(key_val(k), inv_t) / ldexp(__ull2double_rn(Z), -a.shift));
+                a.prob[r] = static_cast<float>(s.mass.template exactly<BF16>(key_val(k), sm->inv_t) / ldexp(__ull2double_rn(Z), -a.shift));
             }
             cluster_sync();  // the others' reads of the count
             return;
@@ -772,19 +803,21 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
             if (!sm->go_a) continue;
             goal = top_k;
         } else if (stage == 1) {
-            goal = __double2ull_ru(static_cast<double>(top_p) * __ull2double_rn(Z));
-            goal = goal < 1 ? 1 : goal;
+            if (threadIdx.x == 0) goal = goal_reach(top_p, Z);
         } else {
             Z = kept_min < Z ? kept_min : Z;
-            goal = __double2ull_rd(static_cast<double>(fminf(fmaxf(u, 0.0f), 1.0f)) * __ull2double_rn(Z)) + 1;
-            goal = goal < Z ? goal : Z;
+            if (threadIdx.x == 0) goal = goal_pass(u, Z);
         }
+        if (s.rank == 0 && threadIdx.x == 0) sm->hit_above_m = goal;
+        __syncthreads();
+        goal = sm->hit_above_m;
+        __syncthreads();
         f = s.find(stage != 0, goal, total_n, total_m, stage == 2);
         if (stage != 2) Z = f.through;
     }
     if (s.rank == 0 && threadIdx.x == 0) {
         a.token[r] = static_cast<int32_t>(f.id);
-        a.prob[r] = static_cast<float>(s.mass.template exactly<BF16>(ord2f(f.key), inv_t) / ldexp(__ull2double_rn(Z), -a.shift));
+        a.prob[r] = static_cast<float>(s.mass.template exactly<BF16>(ord2f(f.key), sm->inv_t) / ldexp(__ull2double_rn(Z), -a.shift));
     }
     cluster_sync();  // the first CTA's list is read until here
 }
