@@ -18,6 +18,13 @@
 //   collected there, sorted and summed.  A bin with more than S_LIST elements is
 //   split by the bits of its keys until few are left or all are one value.
 //
+// A bf16 row has few values: there a bin is one value, its mass the tokens times
+// the value's, and the questions are answered without a list (by_values).  The
+// 6144 bins reach down from the largest value past some 47 binades; the values
+// between -2^-8 and 2^-8, of which there are 30000 and hardly ever many tokens,
+// and those past the bins have a sum each, and a question that ends among them
+// goes the general way.
+//
 // Masses are whole numbers of 2^-shift of the best token's, exp in two floats
 // (relative error about 2^-37, below), so sums do not depend on their order:
 // a row's token is the same alone, in a batch and over any cluster.  In f32 they
@@ -63,7 +70,7 @@ struct alignas(128) SampleSmem {
     // written by the cluster's CTAs, each in its own place
     float in_max[S_CLUSTER];
     int in_bad[S_CLUSTER];
-    u64 in_word[S_CLUSTER];
+    u64 in_word[S_CLUSTER], in_far[S_CLUSTER], in_near[S_CLUSTER];
     // written by the first CTA in all of them
     u64 go_a, go_b;
     uint32_t go_key, go_n;
@@ -508,6 +515,149 @@ struct Sampler {
         return r;
     }
 
+    // ---- bf16 rows by the values themselves: see the head of this file.
+    static constexpr int KEYS = 3 * S_BINS, K_PER = KEYS / S_THREADS;  // bins, and a thread's in a scan
+    static constexpr uint32_t K_POS = 0xbb80u, K_NEG = 0x447fu;        // the keys of 2^-8 and -2^-8
+
+    // What the first CTA finds: the key of the drawn token, which of its ties it is, and Z.  All CTAs; false where a
+    // question ends among values that have no bin of their own.
+    __device__ bool by_values(const SampleArgs &a, int top_k, bool by_k, float top_p, float z_min, float u, uint32_t *key,
+                              u64 *tie, u64 *Z_out) {
+        uint32_t *bins = sm->cnt;  // and lo, hi behind it
+        for (int i = threadIdx.x * 4; i < KEYS; i += S_THREADS * 4) *reinterpret_cast<uint4 *>(bins + i) = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        const uint32_t k_max = key_of(mass.m) >> 16;
+        // place of a value: its key below the largest, the keys between -2^-8 and 2^-8 counting as one
+        const int np = k_max >= K_POS ? static_cast<int>(k_max - K_POS) + 1 : 0;
+        const int gap = k_max >= K_POS ? static_cast<int>(K_POS - K_NEG) - 2 : k_max > K_NEG ? static_cast<int>(k_max - K_NEG) - 1 : -1;
+        u64 near = 0, far = 0;  // masses between -2^-8 and 2^-8, and past the bins
+        uint32_t near_n = 0;
+        each([&](float z, int) {
+            const uint32_t k = key_of(z) >> 16;
+            const int at = static_cast<int>(k_max - k) - (k <= K_NEG ? gap : 0);
+            const bool is_near = k > K_NEG && k < K_POS;
+            if (!is_near && at < KEYS) {
+                atomicAdd(bins + at, 1u);
+            } else if (t_of_z(z) < 47.0f) {
+                const u64 q = mass.template of<BF16>(z);
+                if (is_near) near += q, ++near_n;
+                else far += q;
+            }
+        });
+        near = block_sum(near), far = block_sum(far);
+        const u64 nn = block_sum(near_n);
+        if (threadIdx.x == 0) peer(&sm->in_word[rank], 0)[0] = near, peer(&sm->in_far[rank], 0)[0] = far, peer(&sm->in_near[rank], 0)[0] = nn;
+        cluster_sync();
+        if (rank == 0) {
+            near = far = 0, near_n = 0;
+            for (int q = 0; q < C; ++q) near += sm->in_word[q], far += sm->in_far[q], near_n += static_cast<uint32_t>(sm->in_near[q]);
+            const int b0 = threadIdx.x * K_PER;
+            uint32_t c[K_PER];
+            u64 w[K_PER];  // mass of one token
+#pragma unroll
+            for (int j = 0; j < K_PER; ++j) c[j] = 0;
+            for (int q = 0; q < C; ++q) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(peer(bins, q) + b0);
+#pragma unroll
+                for (int j = 0; j < K_PER / 4; ++j) {
+                    const uint4 v = src[j];
+                    c[4 * j] += v.x, c[4 * j + 1] += v.y, c[4 * j + 2] += v.z, c[4 * j + 3] += v.w;
+                }
+            }
+            u64 tn = 0, tm = 0, kept = 0;
+            bool open = false;  // min_p ends where values have no bin
+#pragma unroll
+            for (int j = 0; j < K_PER; ++j) {
+                const int b = b0 + j;
+                w[j] = 0;
+                u64 all = 0;
+                if (b == np && near_n) {
+                    c[j] = near_n;
+                    all = near;
+                    w[j] = ~0ull;
+                    if (z_min > -0.00390625f && z_min <= 0.00390625f) open = true;
+                    if (z_min <= -0.00390625f) kept += near;
+                } else if (c[j]) {
+                    const float z = value_at(b, k_max, np, gap);
+                    w[j] = mass.template of<BF16>(z);
+                    all = c[j] * w[j];
+                    if (z >= z_min) kept += all;
+                }
+                tn += c[j], tm += all;
+            }
+            const u64 in = warp_scan(tn, lane), im = warp_scan(tm, lane);
+            if (lane == 31) sm->sum[warp] = in, sm->sum2[warp] = im;
+            __syncthreads();
+            u64 an = in - tn, am = im - tm, N = 0, M = 0;
+#pragma unroll
+            for (int i = 0; i < S_WARPS; ++i) {
+                const u64 x = sm->sum[i], y = sm->sum2[i];
+                if (i < warp) an += x, am += y;
+                N += x, M += y;
+            }
+            u64 Z = M + far;
+            kept = block_sum(kept);
+            if (far && z_min <= value_at(KEYS - 1, k_max, np, gap)) kept = z_min == NEG_INF ? Z : 0, open |= z_min != NEG_INF;
+            bool fine = !__syncthreads_or(open);
+            // where count or mass comes to the goal: key, tie, mass through it; false among values without a bin
+            auto settle = [&](bool by_mass, u64 goal) {
+                if (threadIdx.x == 0) sm->go_n = 0;
+                __syncthreads();
+                if (by_mass ? am < goal && am + tm >= goal : an < goal && an + tn >= goal) {
+                    u64 n = an, m = am;
+#pragma unroll
+                    for (int j = 0; j < K_PER; ++j) {
+                        const u64 all = w[j] == ~0ull ? near : c[j] * w[j];
+                        if (by_mass ? m < goal && m + all >= goal : n < goal && n + c[j] >= goal) {
+                            if (w[j] != ~0ull) {
+                                const u64 t = by_mass ? (goal - m + w[j] - 1) / w[j] : goal - n;
+                                sm->go_n = 1;
+                                sm->go_key = key_of(value_at(b0 + j, k_max, np, gap));
+                                sm->go_a = t;
+                                sm->hit_above_m = m + t * w[j];
+                            }
+                        }
+                        n += c[j], m += all;
+                    }
+                }
+                __syncthreads();
+                return sm->go_n != 0;
+            };
+            if (fine && by_k && static_cast<u64>(top_k) < N) {
+                fine = settle(false, top_k);
+                Z = sm->hit_above_m;
+            } else if (by_k && far) {
+                fine = false;
+            }
+            if (fine && top_p < 1.0f) {
+                if (threadIdx.x == 0) sm->hit_above_n = goal_reach(top_p, Z);
+                __syncthreads();
+                fine = settle(true, sm->hit_above_n);
+                Z = sm->hit_above_m;
+            }
+            if (fine) {
+                Z = kept < Z ? kept : Z;
+                if (threadIdx.x == 0) sm->hit_above_n = goal_pass(u, Z);
+                __syncthreads();
+                fine = settle(true, sm->hit_above_n);
+            }
+            const uint32_t k = sm->go_key;
+            *key = k, *tie = sm->go_a, *Z_out = Z;
+            __syncthreads();
+            if (threadIdx.x < C) peer(&sm->go_n, threadIdx.x)[0] = fine, peer(&sm->go_key, threadIdx.x)[0] = k;
+        }
+        cluster_sync();
+        *key = sm->go_key;
+        return sm->go_n != 0;
+    }
+    __device__ __forceinline__ float t_of_z(float z) const { return mass.template t_of<BF16>(z); }
+    // The value whose place is b.
+    __device__ __forceinline__ static float value_at(int b, uint32_t k_max, int np, int gap) {
+        const int k = static_cast<int>(k_max) - b - (b < np ? 0 : gap);
+        const uint32_t o = static_cast<uint32_t>(k < 0 ? 0 : k) << 16;
+        return ord2f((o & 0x80000000u) ? o : o | 0xffffu);
+    }
+
     // The id of the tie-th (known to the first CTA) entry with a key.  All CTAs; the answer is the first CTA's.
     __device__ int64_t place_of(uint32_t key, u64 tie) {
         if (rank == 0 && threadIdx.x < C) peer(&sm->go_a, threadIdx.x)[0] = tie;
@@ -757,6 +907,18 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
                 a.prob[r] = static_cast<float>(s.mass.template exactly<BF16>(key_val(k), sm->inv_t) / ldexp(__ull2double_rn(Z), -a.shift));
             }
             cluster_sync();  // the others' reads of the count
+            return;
+        }
+    }
+    if constexpr (BF16) {
+        uint32_t key;
+        u64 tie = 0, Z = 0;
+        if (s.by_values(a, top_k, by_k, top_p, z_min, u, &key, &tie, &Z)) {
+            const int64_t id = s.place_of(key, tie);
+            if (s.rank == 0 && threadIdx.x == 0) {
+                a.token[r] = static_cast<int32_t>(id);
+                a.prob[r] = static_cast<float>(s.mass.template exactly<BF16>(ord2f(key), sm->inv_t) / ldexp(__ull2double_rn(Z), -a.shift));
+            }
             return;
         }
     }
