@@ -195,11 +195,9 @@ constexpr int L4_THREADS = 256;
 constexpr int L4_WARPS = L4_THREADS / 32;
 constexpr int L4_STAGES = 4;
 constexpr int64_t L4_MAX_K = 1 << 17, L4_MAX_ROWS = 1 << 19;
-constexpr int64_t L4_MANY_ROWS = 17, L4_MANY_N = 4096;
+constexpr int64_t L4_MANY_ROWS = 9, L4_MANY_N = 4096;
 constexpr int L4_SMEM_MAX = 226 * 1024;
-constexpr int L4_SMEM_GOOD = 112 * 1024;  // two CTAs to an SM
-constexpr int L4_WARP_TARGET = 16;        // warps of an SM that have a tile before tiles are shared no further
-constexpr int L4_PER_SM = 2;              // CTAs of an SM that share the tiles
+constexpr int L4_PER_SM = 2;  // CTAs of an SM that share the tiles
 
 struct Lin4 {
     const void *x;
@@ -314,26 +312,54 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
             s_gi += 4, s_at0 += 4, s_at1 += 4, --s_left;
         }
     };
+    const int chunks = nkb * (L4_BLOCK / 8);
+    const bool vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride * (F32X ? 4 : 2) % 16 == 0;
+    const bool staged = !F32X && vec;  // the range of x comes to its place as it is, and is worked on there
+    if (staged) {
+        for (int i = threadIdx.x; i < nr * chunks; i += L4_THREADS) {
+            const int r = i / chunks, c = i - r * chunks, k = c * 8 + kb_lo * L4_BLOCK;
+            const int left = static_cast<int>(p.w.K) - k, bytes = left <= 0 ? 0 : left < 8 ? left * 2 : 16;
+            const void *src = static_cast<const uint16_t *>(p.x) + (r0 + r) * p.x_stride + (bytes ? k : 0);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(xs) + r * pitch + c * 16), "l"(src),
+                         "r"(bytes)
+                         : "memory");
+        }
+        cp_async_commit();
+    }
 #pragma unroll
     for (int s = 0; s < L4_STAGES - 1; ++s) copy(s * 1024);
     sides();
 
     // ---- x: largest entry of each row, then scaled, split, reordered, and its group sums
     if (threadIdx.x < NT * 8) top[threadIdx.x] = 0;
+    if (staged) cp_async_wait<L4_STAGES - 1>();  // x was asked for first
     __syncthreads();
-    const int chunks = nkb * (L4_BLOCK / 8);
-    const bool vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride * (F32X ? 4 : 2) % 16 == 0;
-    for (int i = threadIdx.x; i < nr * chunks; i += L4_THREADS) {
-        const int r = i / chunks, k = (i - r * chunks) * 8 + kb_lo * L4_BLOCK;
-        float v[8];
-        load8<F32X>(p.x, (r0 + r) * p.x_stride + k, static_cast<int>(p.w.K) - k, vec, v);
+    auto take8 = [&](int r, int c, float (&v)[8]) {
+        if (staged) {
+            uint32_t q[4];
+            lds128(smem_addr(xs) + r * pitch + c * 16, q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[2 * i] = bf16lo(q[i]), v[2 * i + 1] = bf16hi(q[i]);
+        } else {
+            const int k = c * 8 + kb_lo * L4_BLOCK;
+            load8<F32X>(p.x, (r0 + r) * p.x_stride + k, static_cast<int>(p.w.K) - k, vec, v);
+        }
+    };
+    // rows are dealt to the warps, or the warps to the rows
+    int wpr = L4_WARPS;
+    while (wpr > 1 && wpr / 2 >= (L4_WARPS + nr - 1) / nr) wpr /= 2;
+    const int x_first = (warp & (wpr - 1)) * 32 + lane, x_step = wpr * 32, x_rows = L4_WARPS / wpr;
+    for (int r = warp / wpr; r < nr; r += x_rows) {
         uint32_t m = 0;
+#pragma unroll 2
+        for (int c = x_first; c < chunks; c += x_step) {
+            float v[8];
+            take8(r, c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-        // lanes of one half-warp share a row (a range has a multiple of 16 chunks)
-#pragma unroll
-        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffu << (lane & 16), m, d));
-        if ((lane & 15) == 0) atomicMax(&top[r], m);
+            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        }
+        m = __reduce_max_sync(FULL, m);
+        if (lane == 0) atomicMax(&top[r], m);
     }
     __syncthreads();
     if (threadIdx.x < nr) {
@@ -343,20 +369,25 @@ __global__ void __launch_bounds__(L4_THREADS, 2) k_linear4_mma(const Lin4 p) {
         top[threadIdx.x] = static_cast<uint32_t>(e);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nr * chunks; i += L4_THREADS) {
-        const int r = i / chunks, c = i - r * chunks, k = c * 8 + kb_lo * L4_BLOCK;
+    for (int r = warp / wpr; r < nr; r += x_rows)
+#pragma unroll 2
+    for (int c = x_first; c < chunks; c += x_step) {  // a range has a multiple of 16 chunks: half-warps stay whole
         float v[8];
-        load8<F32X>(p.x, (r0 + r) * p.x_stride + k, static_cast<int>(p.w.K) - k, vec, v);
-        const int e = static_cast<int>(top[r]);
-        const bool bad = isnan(half[r]);
-        float sum = scale8(v, e, bad);
+        take8(r, c, v);
+        if (isnan(half[r])) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        }
+        float sum = scale8(v, static_cast<int>(top[r]));
         constexpr int LANES = 16 >> LG;  // chunks of a group
 #pragma unroll
         for (int d = LANES >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (lane & 16), sum, d);
         if ((c & (LANES - 1)) == 0) xsum[c / LANES * sums_ld + r] = sum;
-        // where thread t finds its j-th word's columns: the words of a group lie WPG to a thread
+        // where thread t finds its j-th word's columns: the words of a group lie WPG to a thread.  A block is written over
+        // by the half-warp that has just read it.
         const int cc = c & 15, cg = cc / LANES, ci = cc % LANES;
         unsigned char *dst = xs + r * pitch + ((c & ~15) + (cg * WPG + ci % WPG) * 4 + ci / WPG) * 16;
+        __syncwarp(0xffffu << (lane & 16));
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
             uint4 o;
@@ -575,30 +606,40 @@ static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
     p.tiles = (p.w.N + 15) / 16;
     p.kblocks = static_cast<int>((p.w.K + L4_BLOCK - 1) / L4_BLOCK);
     const int64_t sms = sm_count();
+    // The split with the least estimated time (in ns; the constants were measured): a block takes an SM 31 ns and a warp
+    // 130 ns at least, more with more tiles of x rows; x takes its CTA 30 ns for 256 chunks; warps that share a tile meet
+    // in 300 ns, CTAs that share one in 1200 ns.
+    int64_t ctas = 0;
     for (;; p.rb = (p.rb + 1) / 2) {
-        const int nt = (p.rb + 7) / 8;
-        // warps that share a tile: until every warp slot of the GPU has work
-        p.kw_log2 = 0;
-        while (p.kw_log2 < 3 && (p.tiles << p.kw_log2) < sms * L4_WARP_TARGET && (2 << p.kw_log2) <= p.kblocks) ++p.kw_log2;
-        for (p.ks = 1;; p.ks *= 2) {
-            p.kper = (p.kblocks + p.ks - 1) / p.ks;
-            const bool fits = l4_smem(p, nt, parts) <= L4_SMEM_GOOD;
-            const int64_t ctas = (p.tiles + (L4_WARPS >> p.kw_log2) - 1) / (L4_WARPS >> p.kw_log2);
-            const bool more = ctas * p.ks * 2 <= sms && (p.kper >> p.kw_log2) >= 2;
-            if (p.ks == 8 || p.ks * 2 > p.kblocks || (fits && !more)) break;
+        const int nt = (p.rb + 7) / 8 * parts;
+        const int64_t gy = (p.rows + p.rb - 1) / p.rb;
+        int64_t best = -1;
+        Lin4 q = p;
+        for (q.ks = 1; q.ks <= 8 && q.ks <= p.kblocks; q.ks *= 2) {
+            q.kper = (p.kblocks + q.ks - 1) / q.ks;
+            for (q.kw_log2 = 0; q.kw_log2 <= 3 && (q.kw_log2 == 0 || (1 << q.kw_log2) <= p.kblocks / q.ks); ++q.kw_log2) {
+                const int64_t smem = static_cast<int64_t>(l4_smem(q, (p.rb + 7) / 8, parts));
+                if (smem > L4_SMEM_MAX) continue;
+                const int64_t per_sm = 2 * (smem + 1024) <= 227 * 1024 ? L4_PER_SM : 1;
+                const int64_t sets = (p.tiles + (L4_WARPS >> q.kw_log2) - 1) / (L4_WARPS >> q.kw_log2);
+                int64_t slots = sms * per_sm / (q.ks * gy);
+                slots = slots < 1 ? 1 : slots < sets ? slots : sets;
+                const int64_t rounds = (sets + slots - 1) / slots, blocks = (q.kper + (1 << q.kw_log2) - 1) >> q.kw_log2;
+                const int64_t warps = (slots * q.ks * gy * L4_WARPS + sms - 1) / sms, full = warps < per_sm * L4_WARPS ? warps : per_sm * L4_WARPS;
+                const int64_t block = full * (23 + 8 * nt) > 100 + 30 * nt ? full * (23 + 8 * nt) : 100 + 30 * nt;
+                const int64_t waves = (slots * q.ks * gy + sms * per_sm - 1) / (sms * per_sm);
+                const int64_t time = waves * (p.rb * parts * q.kper * 2 +
+                                              rounds * (blocks * block + (q.kw_log2 ? 300 : 0) + (q.ks > 1 ? 1200 : 0)));
+                if (best < 0 || time < best) best = time, p.kper = q.kper, p.ks = q.ks, p.kw_log2 = q.kw_log2, ctas = slots;
+            }
         }
-        if (l4_smem(p, nt, parts) <= L4_SMEM_MAX) break;
+        if (best >= 0) break;
         if (p.rb == 1) return DFLASH2_ERR_UNSUPPORTED;
     }
     const int nt = (p.rb + 7) / 8;
     const size_t smem = l4_smem(p, nt, parts);
     const int64_t gy = (p.rows + p.rb - 1) / p.rb;
-    const int64_t sets = (p.tiles + (L4_WARPS >> p.kw_log2) - 1) / (L4_WARPS >> p.kw_log2);
-    int64_t per_sm = static_cast<int64_t>(L4_SMEM_MAX + 1024) / static_cast<int64_t>(smem + 1024);
-    if (per_sm > L4_PER_SM) per_sm = L4_PER_SM;
-    int64_t ctas = sms * per_sm / (gy < per_sm ? gy : per_sm) / p.ks;
-    if (ctas < 1) ctas = 1;
-    if (ctas > sets) ctas = sets;
+    if (gy > 65535) return DFLASH2_ERR_UNSUPPORTED;
     const unsigned gx = static_cast<unsigned>(ctas * p.ks);
     if (f32x) return nt == 1 ? launch_l4_groups<1, true>(p, smem, gx, gy, s) : launch_l4_groups<2, true>(p, smem, gx, gy, s);
     if (nt == 1) return launch_l4_groups<1, false>(p, smem, gx, gy, s);

@@ -63,16 +63,17 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return r;
 }
 
-// Eight columns of a row scaled for the operand (exponent e); returns their sum in the product's units.
-__device__ __forceinline__ float scale8(float (&v)[8], int e, bool bad) {
+// Eight columns of a row scaled for the operand (exponent e, odd; no infinities); returns their sum in the product's units.
+__device__ __forceinline__ float scale8(float (&v)[8], int e) {
+    const float f1 = pow2f(e >> 1), f2 = pow2f(e - (e >> 1)), f3 = pow2f(e - (e >> 1) - 4);
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        if (bad) v[j] = 0.0f;
-        sum += scale2(v[j], e - 133);
-        v[j] = scale2(v[j], (j & 1) ? e - 4 : e);
+        v[j] *= f1;  // below 2^64, so that sums of a group do not overflow
+        sum += v[j];
+        v[j] *= (j & 1) ? f3 : f2;
     }
-    return sum;
+    return sum * pow2f((e - 133) / 2 - (e >> 1) / 2) * pow2f(e - 133 - (e >> 1) - ((e - 133) / 2 - (e >> 1) / 2));
 }
 
 // Many rows (linear4_tc.cu).  bf16 rows only.

@@ -101,11 +101,12 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
     for (int c = threadIdx.x; c < chunks; c += 256) {  // chunks is a multiple of 16: half-warps stay whole
         float v[8] = {};
         if (r < rows) load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
-        if (!scaled) {
+        if (bad) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = bad ? 0.0f : v[j];
-        } else {
-            float sum = scale8(v, e, bad);
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        }
+        if (scaled) {
+            float sum = scale8(v, e);
             for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), sum, d);
             if ((c & (lanes - 1)) == 0) sums[(r / R * (chunks / lanes) + c / lanes) * R + r % R] = sum;
         }

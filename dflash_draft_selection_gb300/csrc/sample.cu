@@ -526,98 +526,128 @@ struct Sampler {
         uint32_t *bins = sm->cnt;  // and lo, hi behind it
         for (int i = threadIdx.x * 4; i < KEYS; i += S_THREADS * 4) *reinterpret_cast<uint4 *>(bins + i) = make_uint4(0, 0, 0, 0);
         __syncthreads();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the first CTA's bins may be added to
         const uint32_t k_max = key_of(mass.m) >> 16;
         // place of a value: its key below the largest, the keys between -2^-8 and 2^-8 counting as one
         const int np = k_max >= K_POS ? static_cast<int>(k_max - K_POS) + 1 : 0;
         const int gap = k_max >= K_POS ? static_cast<int>(K_POS - K_NEG) - 2 : k_max > K_NEG ? static_cast<int>(k_max - K_NEG) - 1 : -1;
+        // ... for a value's upper 16 bits h: above - h, or below + (h less its sign)
+        const int above = static_cast<int>(k_max) - 0x8000, below = static_cast<int>(k_max) - 0x7fff - gap;
         u64 near = 0, far = 0;  // masses between -2^-8 and 2^-8, and past the bins
         uint32_t near_n = 0;
-        each([&](float z, int) {
-            const uint32_t k = key_of(z) >> 16;
-            const int at = static_cast<int>(k_max - k) - (k <= K_NEG ? gap : 0);
-            const bool is_near = k > K_NEG && k < K_POS;
-            if (!is_near && at < KEYS) {
-                atomicAdd(bins + at, 1u);
-            } else if (t_of_z(z) < 47.0f) {
-                const u64 q = mass.template of<BF16>(z);
-                if (is_near) near += q, ++near_n;
+        for (int i = threadIdx.x * VEC; i < n; i += S_THREADS * VEC) {
+            float z[VEC];
+            if (i + VEC <= n) split(vector(i), z);
+            else rest(i, z);
+            uint32_t others = 0;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                // the bits of a positive value below the largest one's, of a negative one above its own sign's first
+                const int h = __float_as_int(z[j]) >> 16, at = (h < 0 ? (h & 0x7fff) + below : above - h);
+                if ((h & 0x7fff) >= 0x3b80 && at < KEYS) atomicAdd(bins + at, 1u);
+                else if (z[j] != NEG_INF) others |= 1u << j;
+            }
+            while (others) {
+                const int j = __ffs(others) - 1;
+                others &= others - 1;
+                float x = z[0];
+#pragma unroll
+                for (int k = 1; k < VEC; ++k) x = k == j ? z[k] : x;
+                const u64 q = mass.template of<BF16>(x);
+                if (x < 0.00390625f && x > -0.00390625f) near += q, ++near_n;
                 else far += q;
             }
-        });
-        near = block_sum(near), far = block_sum(far);
-        const u64 nn = block_sum(near_n);
-        if (threadIdx.x == 0) peer(&sm->in_word[rank], 0)[0] = near, peer(&sm->in_far[rank], 0)[0] = far, peer(&sm->in_near[rank], 0)[0] = nn;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) near += __shfl_xor_sync(FULL, near, d), far += __shfl_xor_sync(FULL, far, d);
+        near_n = __reduce_add_sync(FULL, near_n);
+        if (lane == 0) sm->list[warp] = near, sm->list[32 + warp] = far, sm->list[64 + warp] = near_n;
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x < 3) {
+            u64 all = 0;
+            for (int i = 0; i < S_WARPS; ++i) all += sm->list[32 * threadIdx.x + i];
+            peer(threadIdx.x == 0 ? &sm->in_word[rank] : threadIdx.x == 1 ? &sm->in_far[rank] : &sm->in_near[rank], 0)[0] = all;
+        }
+        if (rank != 0) {
+            uint32_t *first = peer(bins, 0);
+            for (int i = threadIdx.x; i < KEYS; i += S_THREADS)
+                if (const uint32_t c = bins[i]) atomicAdd(first + i, c);
+        }
         cluster_sync();
         if (rank == 0) {
             near = far = 0, near_n = 0;
             for (int q = 0; q < C; ++q) near += sm->in_word[q], far += sm->in_far[q], near_n += static_cast<uint32_t>(sm->in_near[q]);
-            const int b0 = threadIdx.x * K_PER;
-            uint32_t c[K_PER];
-            u64 w[K_PER];  // mass of one token
-#pragma unroll
-            for (int j = 0; j < K_PER; ++j) c[j] = 0;
-            for (int q = 0; q < C; ++q) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(peer(bins, q) + b0);
-#pragma unroll
-                for (int j = 0; j < K_PER / 4; ++j) {
-                    const uint4 v = src[j];
-                    c[4 * j] += v.x, c[4 * j + 1] += v.y, c[4 * j + 2] += v.z, c[4 * j + 3] += v.w;
-                }
-            }
+            // Runs of K_PER bins, neighbouring ones to different warps: most tokens lie in a few hundred bins.  The counts
+            // stay in this CTA's bins, what lies above a run in the list's place.
+            const int g = lane * S_WARPS + warp, b0 = g * K_PER;
             u64 tn = 0, tm = 0, kept = 0;
             bool open = false;  // min_p ends where values have no bin
-#pragma unroll
-            for (int j = 0; j < K_PER; ++j) {
-                const int b = b0 + j;
-                w[j] = 0;
-                u64 all = 0;
-                if (b == np && near_n) {
-                    c[j] = near_n;
-                    all = near;
-                    w[j] = ~0ull;
-                    if (z_min > -0.00390625f && z_min <= 0.00390625f) open = true;
-                    if (z_min <= -0.00390625f) kept += near;
-                } else if (c[j]) {
-                    const float z = value_at(b, k_max, np, gap);
-                    w[j] = mass.template of<BF16>(z);
-                    all = c[j] * w[j];
-                    if (z >= z_min) kept += all;
+#pragma unroll 1
+            for (int j = 0; j < K_PER; j += 4) {
+                uint4 c4 = *reinterpret_cast<const uint4 *>(bins + b0 + j);
+                if (np >= b0 + j && np < b0 + j + 4) {
+                    uint32_t *c = np == b0 + j ? &c4.x : np == b0 + j + 1 ? &c4.y : np == b0 + j + 2 ? &c4.z : &c4.w;
+                    if (near_n) {
+                        *c = near_n;
+                        open = z_min > -0.00390625f && z_min <= 0.00390625f;
+                        tm += near, kept += z_min <= -0.00390625f ? near : 0;
+                    }
                 }
-                tn += c[j], tm += all;
+                *reinterpret_cast<uint4 *>(bins + b0 + j) = c4;
+                tn += static_cast<u64>(c4.x) + c4.y + c4.z + c4.w;
+                if ((c4.x | c4.y | c4.z | c4.w) == 0) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t n1 = i == 0 ? c4.x : i == 1 ? c4.y : i == 2 ? c4.z : c4.w;
+                    const float z = value_at(b0 + j + i, k_max, np, gap);
+                    const u64 all = b0 + j + i == np && near_n ? 0 : n1 * mass.template of<BF16>(z);
+                    tm += all, kept += z >= z_min ? all : 0;
+                }
             }
-            const u64 in = warp_scan(tn, lane), im = warp_scan(tm, lane);
+            u64 *run_m = sm->list, *run_n = sm->list + S_THREADS;
+            run_m[g] = tm, run_n[g] = tn;
+            __syncthreads();
+            const u64 my_n = run_n[threadIdx.x], my_m = run_m[threadIdx.x];
+            const u64 in = warp_scan(my_n, lane), im = warp_scan(my_m, lane);
             if (lane == 31) sm->sum[warp] = in, sm->sum2[warp] = im;
             __syncthreads();
-            u64 an = in - tn, am = im - tm, N = 0, M = 0;
+            u64 an = in - my_n, am = im - my_m, N = 0, M = 0;
 #pragma unroll
             for (int i = 0; i < S_WARPS; ++i) {
                 const u64 x = sm->sum[i], y = sm->sum2[i];
                 if (i < warp) an += x, am += y;
                 N += x, M += y;
             }
+            run_m[threadIdx.x] = am, run_n[threadIdx.x] = an;
             u64 Z = M + far;
             kept = block_sum(kept);
             if (far && z_min <= value_at(KEYS - 1, k_max, np, gap)) kept = z_min == NEG_INF ? Z : 0, open |= z_min != NEG_INF;
             bool fine = !__syncthreads_or(open);
             // where count or mass comes to the goal: key, tie, mass through it; false among values without a bin
             auto settle = [&](bool by_mass, u64 goal) {
-                if (threadIdx.x == 0) sm->go_n = 0;
+                if (threadIdx.x == 0) sm->go_n = 0, sm->go_i[0] = -1;
                 __syncthreads();
-                if (by_mass ? am < goal && am + tm >= goal : an < goal && an + tn >= goal) {
-                    u64 n = an, m = am;
-#pragma unroll
-                    for (int j = 0; j < K_PER; ++j) {
-                        const u64 all = w[j] == ~0ull ? near : c[j] * w[j];
-                        if (by_mass ? m < goal && m + all >= goal : n < goal && n + c[j] >= goal) {
-                            if (w[j] != ~0ull) {
-                                const u64 t = by_mass ? (goal - m + w[j] - 1) / w[j] : goal - n;
-                                sm->go_n = 1;
-                                sm->go_key = key_of(value_at(b0 + j, k_max, np, gap));
-                                sm->go_a = t;
-                                sm->hit_above_m = m + t * w[j];
-                            }
-                        }
-                        n += c[j], m += all;
+                if (by_mass ? am < goal && am + my_m >= goal : an < goal && an + my_n >= goal) sm->go_i[0] = threadIdx.x;
+                __syncthreads();
+                const int run = sm->go_i[0];
+                if (warp == 0 && run >= 0) {  // a lane to a bin of the run
+                    const int b = run * K_PER + lane;
+                    u64 n1 = 0, w = 0, all = 0;
+                    if (lane < K_PER) {
+                        n1 = bins[b];
+                        const bool is_near = b == np && near_n;
+                        w = n1 == 0 || is_near ? 0 : mass.template of<BF16>(value_at(b, k_max, np, gap));
+                        all = is_near ? near : n1 * w;
+                    }
+                    const u64 nn1 = run_n[run] + warp_scan(n1, lane), mm = run_m[run] + warp_scan(all, lane);
+                    if (lane < K_PER && w && (by_mass ? mm - all < goal && mm >= goal : nn1 - n1 < goal && nn1 >= goal)) {
+                        const u64 t = by_mass ? (goal - (mm - all) + w - 1) / w : goal - (nn1 - n1);
+                        sm->go_n = 1;
+                        sm->go_key = key_of(value_at(b, k_max, np, gap));
+                        sm->go_a = t;
+                        sm->hit_above_m = mm - all + t * w;
                     }
                 }
                 __syncthreads();
@@ -650,7 +680,6 @@ struct Sampler {
         *key = sm->go_key;
         return sm->go_n != 0;
     }
-    __device__ __forceinline__ float t_of_z(float z) const { return mass.template t_of<BF16>(z); }
     // The value whose place is b.
     __device__ __forceinline__ static float value_at(int b, uint32_t k_max, int np, int gap) {
         const int k = static_cast<int>(k_max) - b - (b < np ? 0 : gap);
@@ -661,9 +690,16 @@ struct Sampler {
     // The id of the tie-th (known to the first CTA) entry with a key.  All CTAs; the answer is the first CTA's.
     __device__ int64_t place_of(uint32_t key, u64 tie) {
         if (rank == 0 && threadIdx.x < C) peer(&sm->go_a, threadIdx.x)[0] = tie;
-        const int per = (n + S_THREADS - 1) / S_THREADS, a = per * threadIdx.x, b = min(a + per, n);
+        const int per = (n + S_THREADS * VEC - 1) / (S_THREADS * VEC) * VEC, a = per * threadIdx.x, b = min(a + per, n);
+        const float value = ord2f(key);
         uint32_t mine = 0;
-        for (int i = a; i < b; ++i) mine += key_of(entry(i)) == key;
+        for (int i = a; i < b; i += VEC) {
+            float z[VEC];
+            if (i + VEC <= n) split(vector(i), z);
+            else rest(i, z);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) mine += z[j] == value;
+        }
         const uint32_t inc = warp_scan(mine, lane);
         __syncthreads();
         if (lane == 31) sm->sum[warp] = inc;
@@ -679,8 +715,21 @@ struct Sampler {
         const u64 want = sm->go_a;
         if (want > before && want <= before + mine) {
             u64 left = want - before;
-            for (int i = a; i < b; ++i)
-                if (key_of(entry(i)) == key && --left == 0) peer(&sm->go_b, 0)[0] = static_cast<u64>(id0 + i);
+            for (int i = a; i < b; i += VEC) {
+                float z[VEC];
+                if (i + VEC <= n) split(vector(i), z);
+                else rest(i, z);
+                uint32_t hits = 0;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) hits |= z[j] == value ? 1u << j : 0u;
+                const uint32_t c = __popc(hits);
+                if (left <= c) {
+                    while (--left) hits &= hits - 1;
+                    peer(&sm->go_b, 0)[0] = static_cast<u64>(id0 + i + __ffs(hits) - 1);
+                    break;
+                }
+                left -= c;
+            }
         }
         cluster_sync();
         return static_cast<int64_t>(sm->go_b);
