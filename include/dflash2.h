@@ -673,7 +673,7 @@ dflash2_status dflash2_sample(const void *logits, dflash2_dtype dt, int64_t rows
  * Error word of the library's kernels on the current device: nonzero after a
  * kernel gave up on a bounded wait (it then wrote -1 / NaN outputs instead of
  * hanging, dflash2_rope_append NaN to the cached keys and values and
- * dflash2_paged_attn to the weights too; the word then holds
+ * dflash2_paged_attn to the weights too, dflash2_linear4 NaN to the outputs; the word then holds
  * DFLASH2_DEVERR_WAIT_TIMEOUT).  Synchronises the device.  clear != 0 resets
  * the word.
  */
@@ -692,8 +692,9 @@ dflash2_status dflash2_device_error(uint32_t *code, int clear);
  * verify request that reads such a row gets status DFLASH2_ST_NAN.  The same
  * holds for the warps of dflash2_paged_attn's tensor-core kernels that copy
  * the values (with DFLASH2_ATTN_WEIGHTS, the keys of the weights' pass
- * instead) and of dflash2_rope_append's kernel for long blocks: they give up
- * as after any time-out.  flag NULL switches the hook off.  Kernels already
+ * instead), of dflash2_rope_append's kernel for long blocks and of the one of
+ * dflash2_linear4's for many rows that copies x: they give up as after any
+ * time-out.  flag NULL switches the hook off.  Kernels already
  * launched or captured keep the setting they were launched with.
  * Errors: INVALID_ARG for a misaligned flag or max_cycles out of range.
  */
