@@ -5,9 +5,10 @@ Every step drafts a block of K tokens per request (fused LM head, context gate, 
 block's keys and values to the paged cache with their rotary positions, lets the K + 1 queries attend to the cache
 causally while the cache collects the attention weights, verifies the block against the target logits, keeps the
 accepted tokens' slots (the rejected ones are overwritten by the next block), and cuts a request that has outgrown its
-budget down to its newest, first and most attended keys.
+budget down to its newest, first and most attended keys.  The requests' first tokens are sampled from given uniforms; the
+target's head may be held in 4 bits.
 
-  python examples/cached_decode.py [--requests 8] [--steps 64] [--budget 256]
+  python examples/cached_decode.py [--requests 8] [--steps 64] [--budget 256] [--head4]
 """
 from __future__ import annotations
 
@@ -39,6 +40,16 @@ class Model:
         angle = torch.arange(max_pos, device=device).double()[:, None] * \
             1e4 ** (-torch.arange(0, d, 2, device=device).double() / d)
         self.cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float()
+        self.head4 = None
+
+    def hold_head_in_4_bits(self, group: int = 64):
+        """The target's logits come from 4-bit weights from here on (the drafter's from the weights that they stand
+        for)."""
+        self.head4 = d2.quant4(self.head, group=group)
+        d2.dequant4(self.head4, out=self.head)
+
+    def logits(self, states: torch.Tensor) -> torch.Tensor:
+        return states @ self.head.T if self.head4 is None else d2.linear4(states, self.head4)
 
 
 class Server:
@@ -59,6 +70,14 @@ class Server:
         self.ws_attn = d2.Workspace.for_paged_attn(B, self.T, m.Hq, m.Hkv, m.d, torch.bfloat16)
         self.ws_verify = d2.Workspace.for_verify(B, m.K)
         self.ws_evict = d2.Workspace.for_kv_evict(B, m.Hkv, self.capacity, budget)
+
+    def first(self, tokens: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=20, top_p=0.95, min_p=0.0):
+        """The token that every request starts from [B], drawn with the uniforms u [B] after the tokens of a prompt's end
+        [B].  Returns the tokens' probabilities."""
+        params = d2.sampling_params(temperature, top_k, top_p, n=self.B, device=u.device)
+        logits = self.m.logits(self.m.embed[tokens.long()])
+        self.last, prob = d2.sample(logits, u, params=params, min_p=torch.full_like(u, min_p))
+        return prob
 
     def layer(self, tokens: torch.Tensor) -> torch.Tensor:
         """Hidden states [B, T, hidden] of a block of tokens [B, T] behind the cache; the block is in the cache
@@ -84,7 +103,7 @@ class Server:
         path, slot, q_sel, _ = d2.pair_score_walk(cand, U, self.last, m.A, m.Bt, gate.view(B, K, -1))
         block = torch.cat([self.last[:, None], path], 1)
         states = self.layer(block)
-        logits = states.view(B * self.T, -1) @ m.head.T
+        logits = m.logits(states.view(B * self.T, -1))
         accepted, out, _ = d2.verify(logits, path, cand, q_sel, slot, ws=self.ws_verify)
         keep = accepted + 1                                    # the block's first token and the accepted ones
         self.slots, self.length = self.slots + keep, self.length + keep
@@ -99,9 +118,14 @@ def main():
     ap.add_argument("--requests", type=int, default=8)
     ap.add_argument("--steps", type=int, default=64)
     ap.add_argument("--budget", type=int, default=256)
+    ap.add_argument("--head4", action="store_true", help="hold the target's head in 4 bits")
     a = ap.parse_args()
     # positions: a warm-up step and a.steps more take up to K + 1 = 8 tokens each
-    server = Server(Model(max_pos=max(4096, 8 * (a.steps + 1))), a.requests, a.budget)
+    model = Model(max_pos=max(4096, 8 * (a.steps + 1)))
+    if a.head4:
+        model.hold_head_in_4_bits()
+    server = Server(model, a.requests, a.budget)
+    server.first(server.last, torch.rand(a.requests, device="cuda"))
     total = torch.zeros(a.requests, dtype=torch.int64, device="cuda")
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     server.step()

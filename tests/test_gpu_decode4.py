@@ -1,5 +1,8 @@
 """A 4-bit head as it is used: quantised when it is loaded, its logits sampled for a first token, ranked for a draft and
 verified, on one stream and in one graph."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -54,4 +57,31 @@ def test_head_sample_verify(zero):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(step[0], token) and torch.equal(step[1], prob)
+    assert d2.device_error() == 0
+
+
+def test_the_serving_loop_on_a_4_bit_head():
+    """examples/cached_decode.py: the first tokens are the sampler's, and every block is verified against the 4-bit
+    head's logits."""
+    dev = cuda_or_skip()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("cached_decode", os.path.join(root, "examples", "cached_decode.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    m = example.Model(seed=2)
+    m.hold_head_in_4_bits()
+    assert torch.equal(m.head, d2.dequant4(m.head4))
+    server = example.Server(m, 5, budget=512)
+    start, u = server.last.clone(), torch.rand(5, generator=torch.Generator(device=dev).manual_seed(1), device=dev)
+    prob = server.first(start, u, min_p=0.01)
+    logits = m.logits(m.embed[start.long()])
+    for b in range(5):
+        t, q, _ = ref.draw(logits[b], float(u[b]), 1.0, 20, float(torch.tensor(0.95)), float(torch.tensor(0.01)))
+        assert int(server.last[b]) == t and abs(float(prob[b]) - q) <= 2.0 ** -23 * q
+    for _ in range(6):
+        accepted, out, block, states = server.step()
+        best = m.logits(states.view(-1, m.hidden)).float().argmax(1).view(5, -1)
+        for b, n in enumerate(accepted.tolist()):
+            assert out[b, :n].tolist() == block[b, 1:n + 1].tolist() == best[b, :n].tolist()
+            assert int(out[b, n]) == int(best[b, n])
     assert d2.device_error() == 0
