@@ -144,6 +144,20 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
             const int64_t left = p.w.K - static_cast<int64_t>(c) * 8, at = n * p.ld + c * 8;
             if (left <= 0) break;
             const float s = side_of(sb[i], p.w.side_dt), z = p.w.zero ? side_of(zb[i], p.w.side_dt) : 8.0f;
+            if (!F32W && left >= 8 && p.vec && p.w.side_dt == DFLASH2_BF16 && fabsf(s) < 1e30f && (!p.w.zero || z == rintf(z))) {
+                // In packed bf16: 128 + code is a number whose low bits are the code, code - zero is exact for whole zero
+                // points, and one rounding is left.
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t c2 = sub_bf16x2(((word[i] >> (4 * j)) & 0x000f000fu) | 0x43004300u, 0x43004300u);
+                    o[j] = mul_bf16x2(sub_bf16x2(c2, pair_of(z)), pair_of(s));
+                }
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) =
+                    make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[0], o[1], 0x7632),
+                               __byte_perm(o[2], o[3], 0x7632));
+                continue;
+            }
             float v[8];
             // 2^23 + code is a float whose low bits are the code
 #pragma unroll
@@ -197,7 +211,6 @@ constexpr int L4_STAGES = 4;
 constexpr int64_t L4_MAX_K = 1 << 17, L4_MAX_ROWS = 1 << 19;
 constexpr int64_t L4_MANY_ROWS = 9, L4_MANY_N = 4096;
 constexpr int L4_SMEM_MAX = 226 * 1024;
-constexpr int L4_PER_SM = 2;  // CTAs of an SM that share the tiles
 
 struct Lin4 {
     const void *x;
@@ -620,7 +633,7 @@ static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
             for (q.kw_log2 = 0; q.kw_log2 <= 3 && (q.kw_log2 == 0 || (1 << q.kw_log2) <= p.kblocks / q.ks); ++q.kw_log2) {
                 const int64_t smem = static_cast<int64_t>(l4_smem(q, (p.rb + 7) / 8, parts));
                 if (smem > L4_SMEM_MAX) continue;
-                const int64_t per_sm = 2 * (smem + 1024) <= 227 * 1024 ? L4_PER_SM : 1;
+                const int64_t per_sm = 2 * (smem + 1024) <= 227 * 1024 ? 2 : 1;
                 const int64_t sets = (p.tiles + (L4_WARPS >> q.kw_log2) - 1) / (L4_WARPS >> q.kw_log2);
                 int64_t slots = sms * per_sm / (q.ks * gy);
                 slots = slots < 1 ? 1 : slots < sets ? slots : sets;

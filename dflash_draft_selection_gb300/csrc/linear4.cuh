@@ -63,6 +63,28 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return r;
 }
 
+// Packed bf16 arithmetic, each half rounded once; subnormals are kept.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// A number of bf16, twice.
+__device__ __forceinline__ uint32_t pair_of(float v) {
+    const uint32_t h = __float_as_uint(v) >> 16;
+    return h | h << 16;
+}
+
 // Eight columns of a row scaled for the operand (exponent e, odd; no infinities); returns their sum in the product's units.
 __device__ __forceinline__ float scale8(float (&v)[8], int e) {
     const float f1 = pow2f(e >> 1), f2 = pow2f(e - (e >> 1)), f3 = pow2f(e - (e >> 1) - 4);

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
     const int64_t r = blockIdx.x;
     const int chunks = kblocks * (L4_BLOCK / 8), lanes = 16 >> lg;
     const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0;
+    pdl_trigger();  // the product may start; it waits before it reads what is written here
     if (threadIdx.x == 0) top = 0;
     __syncthreads();
     uint32_t m = 0;
@@ -141,21 +142,6 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
-}
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {  // subnormals are kept
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-// A number of bf16, twice.
-__device__ __forceinline__ uint32_t pair_of(float v) {
-    const uint32_t h = __float_as_uint(v) >> 16;
-    return h | h << 16;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -278,6 +264,7 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
             bool ok = true;
             if (p.hold != nullptr && !hold_wait(p.hold, p.hold_cycles)) t4_abort(sm), ok = false;
             Walk4 at{0, 0, 0};
+            pdl_wait();  // x' and its sums
             for (; ok && i < total / SB; ++i) {
                 const int s = i % XS;
                 if (i >= XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / XS - 1) & 1)) break;
@@ -460,6 +447,7 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
         int i = 0;
         uint32_t d = 0;
         bool ok = true;
+        pdl_wait();  // the roots
         for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
             const int64_t n = tile * T4_M + quad * 32 + lane;
             for (int rb = 0; rb < p.rblocks; ++rb) {
@@ -569,7 +557,15 @@ static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, c
     static_assert(smem + sizeof(Tc4Shared) <= 227 * 1024, "shared memory of a CTA");
     blocks_per_sm(reinterpret_cast<const void *>(fn), threads, smem);  // raises the shared-memory limit once per device
     const int64_t sms = sm_count();
-    fn<<<static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), threads, smem, s>>>(tm, tc, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};  // beside the kernel that prepares x: the codes' first copies
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, tm, tc, p) != cudaSuccess) return DFLASH2_ERR_CUDA;
     return after_launch();
 }
 
