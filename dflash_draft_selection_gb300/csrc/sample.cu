@@ -68,7 +68,7 @@ struct alignas(128) SampleSmem {
     float ch, cl;
     u64 sum[S_WARPS + 1], sum2[S_WARPS + 1];
     // written by the cluster's CTAs, each in its own place
-    float in_max[S_CLUSTER];
+    float in_max[S_CLUSTER], in_min[S_CLUSTER];
     int in_bad[S_CLUSTER];
     u64 in_word[S_CLUSTER], in_far[S_CLUSTER], in_near[S_CLUSTER];
     // written by the first CTA in all of them
@@ -233,9 +233,10 @@ struct Sampler {
                 }
         }
     }
-    // This thread's largest entry; NaN if it has one.
-    __device__ __forceinline__ float largest() const {
+    // This thread's largest entry; NaN if it has one.  least: of f32 rows, the smallest above -infinity.
+    __device__ __forceinline__ float largest(float &least) const {
         float m = NEG_INF;
+        least = __builtin_huge_valf();
         if (BF16) {
             uint32_t m2 = 0xff80ff80u;  // two -infinities
             for (int i = threadIdx.x * VEC; i < n; i += S_THREADS * VEC) {
@@ -248,7 +249,10 @@ struct Sampler {
             }
             m = fmax_nan(m, fmax_nan(bf16lo(m2), bf16hi(m2)));
         } else {
-            each([&](float z, int) { m = fmax_nan(m, z); });
+            each([&](float z, int) {
+                m = fmax_nan(m, z);
+                least = fminf(least, z == NEG_INF ? least : z);
+            });
         }
         return m;
     }
@@ -794,23 +798,27 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
     asm volatile("cp.async.wait_all;" ::: "memory");
 
     // ---- the largest logit
-    const float mine = s.largest();
+    float least;
+    const float mine = s.largest(least);
     bool bad = __any_sync(FULL, !(mine < __builtin_huge_valf()));
     float m = warp_max_f(mine);
-    if (s.lane == 0) sm->sum[s.warp] = (static_cast<u64>(bad) << 32) | __float_as_uint(m);
+    least = -warp_max_f(-least);
+    if (s.lane == 0) sm->sum[s.warp] = (static_cast<u64>(bad) << 32) | __float_as_uint(m), sm->sum2[s.warp] = __float_as_uint(least);
     __syncthreads();
     for (int i = 0; i < S_WARPS; ++i) {
         m = fmaxf(m, __uint_as_float(static_cast<uint32_t>(sm->sum[i])));
         bad |= (sm->sum[i] >> 32) != 0;
+        least = fminf(least, __uint_as_float(static_cast<uint32_t>(sm->sum2[i])));
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (threadIdx.x < C) {
         peer(&sm->in_max[s.rank], threadIdx.x)[0] = m;
         peer(&sm->in_bad[s.rank], threadIdx.x)[0] = bad;
+        peer(&sm->in_min[s.rank], threadIdx.x)[0] = least;
     }
     cluster_sync();
-    for (int q = 0; q < C; ++q) m = fmaxf(m, sm->in_max[q]), bad |= sm->in_bad[q] != 0;
+    for (int q = 0; q < C; ++q) m = fmaxf(m, sm->in_max[q]), bad |= sm->in_bad[q] != 0, least = fminf(least, sm->in_min[q]);
     if (bad || m == NEG_INF || !(T >= 0.0f) || isinf(T) || top_k < 0 || !(top_p > 0.0f && top_p <= 1.0f) ||
         !(min_p >= 0.0f && min_p <= 1.0f) || isnan(u)) {
         if (s.rank == 0 && threadIdx.x == 0) a.token[r] = -1, a.prob[r] = __uint_as_float(0x7fc00000u);
@@ -850,6 +858,8 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
             s.t_cap = fminf(s.t_cap, fmaf(m - z_min, s.mass.ch, 1.0f));
         }
     }
+    // no further than the row goes, so that the bins are as fine as they can be
+    if (!BF16) s.t_cap = fminf(s.t_cap, fmaf(m - least, s.mass.ch * 1.00001f, 1e-30f));
     s.t_scale = S_BINS / s.t_cap;
     const bool by_k = top_k > 0 && top_k < a.V;
     u64 total_n = 0, total_m = 0;
