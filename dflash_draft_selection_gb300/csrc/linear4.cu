@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
             const int c = c0 + i * span;
             const int64_t at = n * p.w.side_stride + c / LANES;
             word[i] = sb[i] = zb[i] = 0;
-            if (c * 8 < p.w.K) {
+            if (static_cast<int64_t>(c) * 8 < p.w.K) {
                 word[i] = *reinterpret_cast<const uint32_t *>(codes + c * 4);
                 sb[i] = side_bits(p.w.scale, p.w.side_dt, at);
                 if (p.w.zero) zb[i] = side_bits(p.w.zero, p.w.side_dt, at);
@@ -141,12 +141,13 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
 #pragma unroll
         for (int i = 0; i < Q4_AHEAD; ++i) {
             const int c = c0 + i * span;
-            const int64_t left = p.w.K - static_cast<int64_t>(c) * 8, at = n * p.ld + c * 8;
+            const int64_t left = p.w.K - static_cast<int64_t>(c) * 8, at = n * p.ld + static_cast<int64_t>(c) * 8;
             if (left <= 0) break;
             const float s = side_of(sb[i], p.w.side_dt), z = p.w.zero ? side_of(zb[i], p.w.side_dt) : 8.0f;
-            if (!F32W && left >= 8 && p.vec && p.w.side_dt == DFLASH2_BF16 && fabsf(s) < 1e30f && (!p.w.zero || z == rintf(z))) {
+            if (!F32W && left >= 8 && p.vec && p.w.side_dt == DFLASH2_BF16 && fabsf(s) < 1e30f &&
+                (!p.w.zero || (fabsf(z) <= 128.0f && z == rintf(z)))) {
                 // In packed bf16: 128 + code is a number whose low bits are the code, code - zero is exact for whole zero
-                // points, and one rounding is left.
+                // points up to 128, and one rounding is left.
                 uint32_t o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -210,6 +211,7 @@ constexpr int L4_WARPS = L4_THREADS / 32;
 constexpr int L4_STAGES = 4;
 constexpr int64_t L4_MAX_K = 1 << 17, L4_MAX_ROWS = 1 << 19;
 constexpr int64_t L4_MANY_ROWS = 9, L4_MANY_N = 4096;
+constexpr int64_t L4_LONG_ROWS = 1 << 15, L4_LONG_K = 1 << 13;
 constexpr int L4_SMEM_MAX = 226 * 1024;
 
 struct Lin4 {
@@ -647,14 +649,11 @@ static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
                 if (best < 0 || time < best) best = time, p.kper = q.kper, p.ks = q.ks, p.kw_log2 = q.kw_log2, ctas = slots;
             }
         }
-        if (best >= 0) break;
-        if (p.rb == 1) return DFLASH2_ERR_UNSUPPORTED;
+        if (best >= 0) break;  // one row of L4_MAX_K columns fits
     }
     const int nt = (p.rb + 7) / 8;
     const size_t smem = l4_smem(p, nt, parts);
-    const int64_t gy = (p.rows + p.rb - 1) / p.rb;
-    if (gy > 65535) return DFLASH2_ERR_UNSUPPORTED;
-    const unsigned gx = static_cast<unsigned>(ctas * p.ks);
+    const unsigned gx = static_cast<unsigned>(ctas * p.ks), gy = static_cast<unsigned>((p.rows + p.rb - 1) / p.rb);
     if (f32x) return nt == 1 ? launch_l4_groups<1, true>(p, smem, gx, gy, s) : launch_l4_groups<2, true>(p, smem, gx, gy, s);
     if (nt == 1) return launch_l4_groups<1, false>(p, smem, gx, gy, s);
     if (nt == 2) return launch_l4_groups<2, false>(p, smem, gx, gy, s);
@@ -756,6 +755,8 @@ extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64
         if (ws_bytes < linear4_tc_bytes(rows, w->K)) return DFLASH2_ERR_WORKSPACE;
         return linear4_tc(x, rows, x_stride, w, y, y_dt, y_stride, ws, s);
     }
+    // blocks of rows are counted in 16 bits: of up to L4_LONG_K columns they have 16 rows, of more one at least
+    if (rows > L4_LONG_ROWS && w->K > L4_LONG_K) return DFLASH2_ERR_UNSUPPORTED;
     Lin4 p = {};
     p.x = x, p.rows = rows, p.x_stride = x_stride, p.w = *w, p.y = y, p.y_stride = y_stride, p.y_dt = y_dt;
     p.G = static_cast<int>(groups_of(w));

@@ -45,7 +45,9 @@ constexpr int T4_AS = 4;      // blocks of A in tensor memory
 constexpr int t4_sides(int lg) { return lg == 0 ? 8 : 6; }
 constexpr int T4_DS = 4;      // accumulators, at most: 2 of 128 columns
 constexpr int T4_M = 128;
-constexpr int T4_DOWN = 40;   // weights in bf16 are held times 2^-40: scales from 2^-80 to 2^30 neither vanish nor overflow
+// Weights in bf16 are held times 2^-40, and their rows of x have their largest entry near 2^80: with scales from 2^-80 to
+// 2^30 and entries from 2^-80 of a row's largest nothing vanishes or overflows.
+constexpr int T4_DOWN = 40, T4_TOP = 207;  // (and the field of that entry's exponent)
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
 struct Tc4Shared {
@@ -72,8 +74,8 @@ struct Tc4 {
 };
 
 // ---------------------------------------------------------------- x' ----
-// One CTA per row: x' [rows_pad, kblocks * 128], the groups' sums, the root of the power of two.  Rows past the last are
-// zeros.
+// One CTA per row: x' [rows_pad, kblocks * 128], scaled for the codes as operands or for weights in bf16 (then without
+// the groups' sums), and the root of the power of two.  Rows past the last are zeros.
 __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t rows, int64_t x_stride, int K, int lg,
                                                       int kblocks, int R, bool scaled, uint16_t *out, float *sums,
                                                       float *root) {
@@ -96,9 +98,9 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
     if ((threadIdx.x & 31) == 0) atomicMax(&top, m);
     __syncthreads();
     m = top;
-    const int e = x_exponent(m);
+    const int e = scaled ? x_exponent(m) : (T4_TOP - static_cast<int>(m >> 23)) & ~1;  // even: the result's power has a root
     const bool bad = m >= 0x7f800000u;
-    if (threadIdx.x == 0) root[r] = scaled || bad ? x_root(m, e) : pow2f(T4_DOWN / 2);
+    if (threadIdx.x == 0) root[r] = scaled || bad ? x_root(m, e) : pow2f((T4_DOWN - e) / 2);
     for (int c = threadIdx.x; c < chunks; c += 256) {  // chunks is a multiple of 16: half-warps stay whole
         float v[8] = {};
         if (r < rows) load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
@@ -110,6 +112,9 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
             float sum = scale8(v, e);
             for (int d = lanes >> 1; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), sum, d);
             if ((c & (lanes - 1)) == 0) sums[(r / R * (chunks / lanes) + c / lanes) * R + r % R] = sum;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = scale2(v[j], e);
         }
         uint4 o;
         o.x = bf16_pair(v[0], v[4]), o.y = bf16_pair(v[1], v[5]), o.z = bf16_pair(v[2], v[6]), o.w = bf16_pair(v[3], v[7]);

@@ -1082,6 +1082,7 @@ extern "C" dflash2_status dflash2_sample(const void *logits, dflash2_dtype dt, i
     if (!dtype_ok(dt) || rows < 0 || V < 1 || V > 0x7fffffff || ld < V || ld * esize(dt) % 16 != 0 || rows_per_param < 1)
         return DFLASH2_ERR_INVALID_ARG;
     if (rows == 0) return DFLASH2_OK;
+    if (rows > 0x7fffffff / S_CLUSTER) return DFLASH2_ERR_UNSUPPORTED;
     if (!logits || !u || !token || !prob || !aligned16(logits)) return DFLASH2_ERR_INVALID_ARG;
     for (const void *p : {static_cast<const void *>(params), static_cast<const void *>(min_p),
                           static_cast<const void *>(u), static_cast<const void *>(token),
@@ -1100,7 +1101,6 @@ extern "C" dflash2_status dflash2_sample(const void *logits, dflash2_dtype dt, i
     a.slice = static_cast<int>(slice_of(C));
     const bool resident = slice_of(C) * static_cast<int64_t>(e) <= static_cast<int64_t>(226 * 1024 - fixed);
     a.resident = resident;
-    if (rows > 0x7fffffff / C) return DFLASH2_ERR_UNSUPPORTED;
     const size_t smem = fixed + (resident ? slice_of(C) * e : 0);
     const unsigned grid = static_cast<unsigned>(rows * C);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -594,16 +594,16 @@ typedef struct {
  *   with zero points     scale = max(w, 0) / 15 - min(w, 0) / 15;
  *                        zero = -min(w, 0) / scale;  code = w / scale + zero
  * with scale rounded to side_dt before it divides, the quotients rounded to
- * whole numbers, zero and code held within 0..15, and a scale of 0 dividing as 1.  A group
- * with a NaN or an infinity gets scale NaN (codes and zero 8).  The codes
- * behind K, up to a multiple of 32, are 8.
+ * whole numbers, zero and code held within 0..15, and a scale of 0 dividing
+ * as 1.  A group with a NaN or an infinity gets scale NaN (codes and zero 8).
+ * The codes behind K, up to a multiple of 32, are 8.
  *
  * dflash2_dequant4 -- out [N, ld] (dt): what the record stands for, in f32
  * and rounded once.
  *
  * Errors: INVALID_ARG for a NULL or misaligned pointer (W and out: aligned to
- * their type), N < 0 or above 2^31 - 1, K < 1 or above 2^31 - 129, a group other than 32, 64, 128,
- * strides that are too small or (code_stride) no multiple of 16, ld < K;
+ * their type), N < 0 or above 2^31 - 1, K < 1 or above 2^31 - 129, a group
+ * other than 32, 64, 128, strides that are too small or (code_stride) no multiple of 16, ld < K;
  * UNSUPPORTED for matrices of 2^36 entries and more, counted in whole groups.
  */
 dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w,
@@ -623,14 +623,18 @@ dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dty
  *   entries of x below 2^-130 of their row's largest and scales below 2^-100
  *   lose bits.  bf16 results for many rows (those that take a workspace) with
  *   bf16 scales are sums of x times the weights rounded to bf16 (code - zero,
- *   then its product with the scale); scales from 2^-80 to 2^30.
+ *   then its product with the scale), for scales from 2^-80 to 2^30 (and 0);
+ *   entries of x below 2^-80 of their row's largest lose bits.  Scales beyond
+ *   those are for f32 results.
  * ws: dflash2_linear4_workspace_bytes(dt, rows, N, K) bytes, which is 0 for
  *   few rows (ws may then be NULL).  It needs no zeros and is left with
  *   scratch.
  * Errors: INVALID_ARG for a NULL or misaligned pointer (x and y: aligned to
  * their type), rows < 0, x_stride < K, y_stride < N, f32 x with bf16 y, or a
- * record that dflash2_dequant4 refuses; UNSUPPORTED for K above 2^17 or rows
- * above 2^19; WORKSPACE if ws_bytes is too small.
+ * record that dflash2_dequant4 refuses; UNSUPPORTED for K above 2^17, rows
+ * above 2^19, rows above 2^15 with K above 2^13 where no workspace is taken,
+ * and some products with N K rows above 2^54; WORKSPACE if ws_bytes is too
+ * small.
  */
 size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K);
 dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
@@ -663,7 +667,7 @@ dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, in
  * prob NaN.
  * Errors: INVALID_ARG for a NULL or misaligned pointer (logits: 16 bytes; the
  * others: 4), rows < 0, V < 1 or V >= 2^31, ld < V, ld * elem size not a
- * multiple of 16, rows_per_param < 1.
+ * multiple of 16, rows_per_param < 1; UNSUPPORTED for 2^28 rows and more.
  */
 dflash2_status dflash2_sample(const void *logits, dflash2_dtype dt, int64_t rows, int64_t V, int64_t ld,
                               const dflash2_sampling *params, const float *min_p, int64_t rows_per_param,
@@ -673,7 +677,8 @@ dflash2_status dflash2_sample(const void *logits, dflash2_dtype dt, int64_t rows
  * Error word of the library's kernels on the current device: nonzero after a
  * kernel gave up on a bounded wait (it then wrote -1 / NaN outputs instead of
  * hanging, dflash2_rope_append NaN to the cached keys and values and
- * dflash2_paged_attn to the weights too, dflash2_linear4 NaN to the outputs; the word then holds
+ * dflash2_paged_attn to the weights too, dflash2_linear4 NaN to
+ * the outputs; the word then holds
  * DFLASH2_DEVERR_WAIT_TIMEOUT).  Synchronises the device.  clear != 0 resets
  * the word.
  */

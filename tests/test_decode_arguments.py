@@ -72,6 +72,8 @@ def test_calls_on_records():
     assert linear(rows=0, x=None, y=None) == linear(dict(N=0, codes=None, scale=None)) == OK
     assert linear(dict(K=(1 << 17) + 1, code_stride=1 << 17, side_stride=1 << 17), x_stride=1 << 18) == UNSUPPORTED
     assert linear(rows=(1 << 19) + 1) == UNSUPPORTED
+    long = dict(K=(1 << 13) + 1, code_stride=1 << 13, side_stride=65)
+    assert linear(long, rows=(1 << 15) + 1, x_stride=1 << 14) == linear(long, rows=(1 << 15) + 1, x_stride=1 << 14, dt=0, y_dt=0) == UNSUPPORTED
     L = library()
     need = L.dflash2_linear4_workspace_bytes
     assert need(1, 1, 40, 200) == need(0, 512, 151936, 200) == need(1, 0, 40, 200) == need(1, 1 << 20, 1 << 20, 1) == 0
@@ -90,6 +92,7 @@ def test_sample():
         assert sample(**kw) == INVALID, kw
     assert sample(rows=0, logits=None, u=None, token=None, prob=None) == OK
     assert sample(rows=0, V=0) == INVALID
+    assert sample(rows=1 << 28) == UNSUPPORTED
 
 
 class Shape:

@@ -107,6 +107,37 @@ def test_quant_takes_strided_weights_and_fills_strided_records():
     assert (out == -3.0).all()
 
 
+def test_any_zero_point_is_taken_back_with_one_rounding():
+    cuda_or_skip()
+    side = torch.tensor([[8.0, 0.0, -1.0, 15.0, 128.0, -128.0, 130.0, -130.0, 200.0, -255.0, 300.0, 7.5, 0.125, 1e20, -1e20,
+                          math.inf, math.nan]], device="cuda", dtype=BF)
+    G = side.shape[1]
+    for dt in (BF, F32):
+        w = d2.Weight4(torch.randint(0, 256, (5, 16 * G), generator=gen(1), device="cuda", dtype=torch.uint8),
+                       (0.5 + torch.rand(5, G, generator=gen(2), device="cuda")).to(dt), side.to(dt).repeat(5, 1), K=32 * G,
+                       group=32)
+        want = (ref.unpack(w).float() - ref.per_column(w.zero, w.K, 32).float()) * ref.per_column(w.scale, w.K, 32).float()
+        for out in (BF, F32):
+            got = d2.dequant4(w, dtype=out)
+            assert torch.equal(got.nan_to_num(nan=1e4), want.to(out).nan_to_num(nan=1e4))
+
+
+def test_the_longest_row():
+    """A row whose columns come next to 2^31."""
+    cuda_or_skip()
+    K, end = (1 << 31) - 129, (1 << 31) - 512
+    W = torch.zeros(1, K, dtype=BF, device="cuda")
+    tail = torch.randn(1, K - end, generator=gen(1), device="cuda", dtype=BF)
+    W[:, end:] = tail
+    w, last = d2.quant4(W), d2.quant4(tail)
+    assert torch.equal(w.codes[:, end // 2:], last.codes) and torch.equal(w.scale[:, end // 128:], last.scale)
+    assert (w.codes[:, :end // 2] == 0x88).all() and (w.scale[:, :end // 128] == 0).all()
+    W.fill_(1.0)
+    d2.dequant4(w, out=W)
+    assert torch.equal(W[:, end:], d2.dequant4(last))
+    assert (W[:, :end] == 0).all()
+
+
 # --------------------------------------------------------------- products ----
 @pytest.mark.parametrize("rows", [1, 2, 7, 8, 9, 16, 17, 33, 64, 65, 130])
 @pytest.mark.parametrize("N,K,group,zero", [(1, 1, 32, False), (15, 31, 32, True), (16, 64, 64, False), (130, 200, 64, True),
@@ -206,6 +237,29 @@ def test_magnitudes(rows, N):
         assert ((y.double() - want).abs() <= (512 + 16) * 2.0 ** -24 * B + drop + 2.0 ** -149).all()
         if rows > 2:
             assert (y[1] == 0).all()
+
+
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("rows", [9, 24, 100])
+def test_magnitudes_of_bf16_results(rows, zero):
+    """Rows from 2^-120 to 2^90 against weights of the tensor cores' tiles, scales from 2^-80 to 2^20."""
+    cuda_or_skip()
+    w = weights(4096, 512, 128, zero, seed=3)
+    w.scale.mul_(torch.tensor([2.0 ** -80, 2.0 ** -20, 1.0, 2.0 ** 20], device="cuda")[torch.arange(4096, device="cuda") % 4][:, None])
+    x = torch.randn(rows, 512, generator=gen(9), device="cuda")
+    x *= torch.exp2((torch.arange(rows, device="cuda")[:, None] * 61 % 211 - 120).float())
+    x = x.bfloat16()
+    x[1] = 0
+    W = ref.values(w)
+    want = x.double() @ W.T
+    z = torch.full_like(W, 8.0) if w.zero is None else ref.per_column(w.zero, w.K, w.group)
+    B = x.double().abs() @ ((ref.unpack(w).double() + z) * ref.per_column(w.scale, w.K, w.group).abs()).T
+    # f32 sums, bf16 weights, a bf16 result as elsewhere; results next to bf16's least are whole multiples of 2^-133, and
+    # what f32 drops in between (2^-149) is less than 2^-140 of that
+    tol = (512 + 16) * 2.0 ** -24 * B + 2.0 ** -8 * (want.abs() + x.double().abs() @ W.abs().T) + 2.0 ** -133
+    got = d2.linear4(x, w)
+    assert ((got.double() - want).abs() <= tol).all()
+    assert (got[1] == 0).all()
 
 
 @pytest.mark.parametrize("N", [200, 4096])
