@@ -210,7 +210,7 @@ constexpr int L4_THREADS = 256;
 constexpr int L4_WARPS = L4_THREADS / 32;
 constexpr int L4_STAGES = 4;
 constexpr int64_t L4_MAX_K = 1 << 17, L4_MAX_ROWS = 1 << 19;
-constexpr int64_t L4_MANY_ROWS = 9, L4_MANY_N = 4096;
+constexpr int64_t L4_MANY_ROWS = 9;
 constexpr int64_t L4_LONG_ROWS = 1 << 15, L4_LONG_K = 1 << 13;
 constexpr int L4_SMEM_MAX = 226 * 1024;
 
@@ -730,13 +730,17 @@ extern "C" dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, 
     return after_launch();
 }
 
-// Many rows: the tensor cores' tiles have to be enough for the GPU.
-static bool l4_many(dflash2_dtype dt, int64_t rows, int64_t N) {
-    return dt == DFLASH2_BF16 && rows >= L4_MANY_ROWS && N >= L4_MANY_N;
+// Whether the tensor cores' kernel is the faster one.  Its time follows K while its items are no more than the SMs (5120
+// columns: 18 to 24 us, f32 results 20 to 35; 1024: 8 to 11 and 8 to 14), that of the kernel for few rows N x rows (5120
+// columns, 32 rows of 1024, 4096, 8192: 16, 20, 36 us).  At 396 sizes (9 to 512 rows, N 128 to 8192, K 256 to 17408) the
+// choice takes 1.5 % more than the faster one on average and 27 % at most, but for 128 rows of 4096 x 256 in f32 (10 us for 7).
+static bool l4_many(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K, bool exact) {
+    const int64_t at = (1 << 17) - (3 << 26) / K;
+    return dt == DFLASH2_BF16 && rows >= L4_MANY_ROWS && rows * N >= (!exact ? at : rows > 64 ? 2 * at : at + at / 2);
 }
 
 extern "C" size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K) {
-    if (!dtype_ok(dt) || rows < 1 || N < 1 || K < 1 || K > L4_MAX_K || rows > L4_MAX_ROWS || !l4_many(dt, rows, N)) return 0;
+    if (!dtype_ok(dt) || rows < 1 || N < 1 || K < 1 || K > L4_MAX_K || rows > L4_MAX_ROWS || !l4_many(dt, rows, N, K, false)) return 0;
     return linear4_tc_bytes(rows, K);
 }
 
@@ -750,10 +754,12 @@ extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64
     if (!x || !y || !aligned_to(x, dt) || !aligned_to(y, y_dt)) return DFLASH2_ERR_INVALID_ARG;
     if (w->K > L4_MAX_K || rows > L4_MAX_ROWS) return DFLASH2_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (l4_many(dt, rows, w->N)) {
+    if (l4_many(dt, rows, w->N, w->K, false)) {
         if (!ws || !aligned16(ws)) return DFLASH2_ERR_INVALID_ARG;
         if (ws_bytes < linear4_tc_bytes(rows, w->K)) return DFLASH2_ERR_WORKSPACE;
-        return linear4_tc(x, rows, x_stride, w, y, y_dt, y_stride, ws, s);
+        // f32 results and f32 scales keep their bits; other results are taken on weights in bf16
+        const bool exact = y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
+        if (l4_many(dt, rows, w->N, w->K, exact)) return linear4_tc(x, rows, x_stride, w, y, y_dt, y_stride, exact, ws, s);
     }
     // blocks of rows are counted in 16 bits: of up to L4_LONG_K columns they have 16 rows, of more one at least
     if (rows > L4_LONG_ROWS && w->K > L4_LONG_K) return DFLASH2_ERR_UNSUPPORTED;

@@ -13,8 +13,9 @@
 // kernel of its own into the workspace) comes by TMA, 128-byte swizzle, with its
 // groups' sums beside it.
 //
-// One CTA per SM walks its tiles of 128 weight rows; a tile's blocks of x rows
-// follow each other, so its codes come from L2 after the first.
+// One CTA per SM walks its items: a tile of 128 weight rows and a block of x
+// rows.  A tile's items go to neighbouring CTAs at one time, so its codes come
+// from HBM once.
 //   warps 0-7    epilogue: a weight row per lane, half of the R columns each
 //   4 or 8 warps operand and scales: 32 weight rows each; of 8, 4 take the odd pairs of
 //                blocks of 128 columns
@@ -66,7 +67,8 @@ struct Tc4 {
     int64_t rows, y_stride;
     dflash2_dtype y_dt;
     int lg, G, kpairs, rblocks;  // lg: log2 of the groups in a block
-    int64_t tiles;
+    int tiles;
+    int step_tile, step_rb;  // from an item to the CTA's next
     const float *sums;  // [row block][2 * kpairs << lg][R]
     const float *root;  // [rows_pad]
     const unsigned int *hold;
@@ -177,15 +179,16 @@ __device__ __forceinline__ void bulk_g2s(void *sdst, const void *gsrc, uint32_t 
                  : "memory");
 }
 
-// Walks a CTA's blocks: tile by tile, the tile's blocks of x rows, their blocks of columns.
+// Walks a CTA's blocks: item by item, their blocks of columns.
 struct Walk4 {
-    int64_t tile;
-    int rb, kb;
-    __device__ __forceinline__ void next(const Tc4 &p) {
-        if (++kb == 2 * p.kpairs) {
-            kb = 0;
-            if (++rb == p.rblocks) rb = 0, tile += gridDim.x;
-        }
+    int tile, rb, kb;
+    __device__ __forceinline__ explicit Walk4(const Tc4 &p)
+        : tile(static_cast<int>(blockIdx.x) / p.rblocks), rb(static_cast<int>(blockIdx.x) % p.rblocks), kb(0) {}
+    __device__ __forceinline__ void next(const Tc4 &p, int blocks) {  // 1 or 2: an item has pairs
+        kb += blocks;
+        if (kb < 2 * p.kpairs) return;
+        kb = 0, tile += p.step_tile, rb += p.step_rb;
+        if (rb >= p.rblocks) rb -= p.rblocks, ++tile;
     }
 };
 
@@ -260,15 +263,15 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
     // accumulators, and how many of them the epilogue is given at a time
     constexpr uint32_t DS = R > 64 || !EXACT ? 2 : 4, U = R > 64 || !EXACT ? 1 : 2;
     const uint32_t tmem = sm.tmem, tmem_a = tmem + DS * R;
-    const int mine = static_cast<int>((p.tiles - blockIdx.x - 1) / gridDim.x) + 1;  // tiles of this CTA
-    const int total = mine * p.rblocks * p.kpairs * 2;                              // and their blocks
+    const int mine = static_cast<int>((static_cast<int64_t>(p.tiles) * p.rblocks - blockIdx.x - 1) / gridDim.x) + 1;  // items of this CTA
+    const int total = mine * p.kpairs * 2;                                                      // and their blocks
 
     if (warp == T4_COPY) {
         if (lane == 0) {
             int i = 0;
             bool ok = true;
             if (p.hold != nullptr && !hold_wait(p.hold, p.hold_cycles)) t4_abort(sm), ok = false;
-            Walk4 at{0, 0, 0};
+            Walk4 at(p);
             pdl_wait();  // x' and its sums
             for (; ok && i < total / SB; ++i) {
                 const int s = i % XS;
@@ -281,8 +284,7 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
                 if (EXACT)
                     bulk_g2s(sums + s * SB * gpb * R, p.sums + (static_cast<int64_t>(at.rb) * 2 * p.kpairs + at.kb) * gpb * R,
                              SB * gpb * R * 4, &sm.x_full[s]);
-#pragma unroll
-                for (int h = 0; h < SB; ++h) at.next(p);
+                at.next(p, SB);
             }
             // Leave no copy in flight into this CTA's shared memory.  A block is waited for with its scales; after a
             // time-out those may not come, and the copies have the whole limit to land.
@@ -355,34 +357,34 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
         unsigned char *ring = rings + me * (RING * 4096);
         const uint32_t ring_row = smem_addr(ring) + lane * 128;
         const int pairs = total / 2;
-        Walk4 cw{blockIdx.x, 0, 0};  // pair to copy next, and how far it is
-        auto pair_step = [&](Walk4 &w) { w.next(p), w.next(p); };
+        Walk4 cw(p);  // pair to copy next, and how far it is
         int c = odd;
         auto copy = [&](int stage) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(&sm.c_full[me][stage], 4096);
-                tma_load_2d(ring + stage * 4096, &tm_c, cw.kb * (L4_BLOCK / 2), static_cast<int>(cw.tile * T4_M) + quad * 32,
+                tma_load_2d(ring + stage * 4096, &tm_c, cw.kb * (L4_BLOCK / 2), cw.tile * T4_M + quad * 32,
                             &sm.c_full[me][stage]);
             }
-            for (int j = 0; j < SETS; ++j) pair_step(cw);
+#pragma unroll
+            for (int j = 0; j < SETS; ++j) cw.next(p, 2);
             c += SETS;
         };
-        if (odd) pair_step(cw);
+        if (odd) cw.next(p, 2);
         int issued = 0;
 #pragma unroll
         for (int j = 0; j < RING; ++j)
             if (c < pairs) copy(j), ++issued;
         // scales and zero points of the lane's own row, one of the warp's pairs ahead
-        Walk4 sw{blockIdx.x, 0, 0};
+        Walk4 sw(p);
         int64_t side0 = 0;
         uint32_t sr[2 * gpb], zr[2 * gpb];
         auto side_row = [&]() {
-            const int64_t n = sw.tile * T4_M + quad * 32 + lane;
+            const int64_t n = static_cast<int64_t>(sw.tile) * T4_M + quad * 32 + lane;
             side0 = (n < p.w.N ? n : p.w.N - 1) * p.w.side_stride;
         };
         auto load_sides = [&]() {
             if (sw.tile >= p.tiles) return;
-            const int64_t was = sw.tile;
+            const int was = sw.tile;
 #pragma unroll
             for (int j = 0; j < 2 * gpb; ++j) {
                 const int gi = sw.kb * gpb + j;
@@ -392,10 +394,11 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
                     if (p.w.zero) zr[j] = side_bits(p.w.zero, p.w.side_dt, side0 + gi);
                 }
             }
-            for (int j = 0; j < SETS; ++j) pair_step(sw);
+#pragma unroll
+            for (int j = 0; j < SETS; ++j) sw.next(p, 2);
             if (sw.tile != was) side_row();
         };
-        if (odd) pair_step(sw);
+        if (odd) sw.next(p, 2);
         side_row();
         load_sides();
         int st = 0;
@@ -453,87 +456,86 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
         uint32_t d = 0;
         bool ok = true;
         pdl_wait();  // the roots
-        for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-            const int64_t n = tile * T4_M + quad * 32 + lane;
-            for (int rb = 0; rb < p.rblocks; ++rb) {
-                uint64_t acc[RH / 2];
+        for (int item = 0; item < mine; ++item) {
+            uint64_t acc[RH / 2];
 #pragma unroll
-                for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
-                if constexpr (EXACT) {
-                    for (int kb = 0; ok && kb < 2 * p.kpairs; ++kb, ++i) {
-                        const int s = i / SB % XS;
+            for (int j = 0; j < RH / 2; ++j) acc[j] = 0;
+            if constexpr (EXACT) {
+                for (int kb = 0; ok && kb < 2 * p.kpairs; ++kb, ++i) {
+                    const int s = i / SB % XS;
 #pragma unroll
-                        for (int j = 0; j < gpb; ++j, ++d) {
-                            const uint32_t u = d / U;
-                            if (d % U == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[u % (DS / U)], (u / (DS / U)) & 1));
-                            if (!ok) break;
-                            tc_fence_after();
-                            const float2 side = sides[((i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane];
-                            const uint64_t s2 = pack2(__float_as_uint(side.x), __float_as_uint(side.x));
-                            const uint64_t z2 = pack2(__float_as_uint(side.y), __float_as_uint(side.y));
-                            const float *xg = sums + ((s * SB + i % SB) * gpb + j) * R + half * RH;
-                            constexpr int CH = RH < 16 ? RH : RH < 32 ? 16 : 32;
-#pragma unroll
-                            for (int c = 0; c < RH; c += CH) {
-                                uint32_t v[CH];
-                                if constexpr (CH == 8) {
-                                    tmem_ld8(tm + (d % DS) * R, v);
-                                } else {
-#pragma unroll
-                                    for (int k = 0; k < CH; k += 16) tmem_ld16_nowait(tm + (d % DS) * R + c + k, v + k);
-                                }
-                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                                for (int k = 0; k < CH; k += 4) {
-                                    const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(xg + c + k);
-                                    const int at = (c + k) / 2;
-                                    acc[at] = fma2(z2, x2.x, fma2(s2, pack2(v[k], v[k + 1]), acc[at]));
-                                    acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[k + 2], v[k + 3]), acc[at + 1]));
-                                }
-                            }
-                            if (d % U == U - 1) {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&sm.d_empty[u % (DS / U)]);
-                            }
-                        }
-                        __syncwarp();
-                        if (i % SB == SB - 1 && ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
-                    }
-                } else {
-                    ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[d % DS], (d / DS) & 1));
-                    if (ok) {
+                    for (int j = 0; j < gpb; ++j, ++d) {
+                        const uint32_t u = d / U;
+                        if (d % U == 0) ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[u % (DS / U)], (u / (DS / U)) & 1));
+                        if (!ok) break;
                         tc_fence_after();
-                        uint32_t v[RH];
-                        if constexpr (RH == 8) {
-                            tmem_ld8(tm + (d % DS) * R, v);
-                        } else {
+                        const float2 side = sides[((i % T4_SIDES) * gpb + j) * T4_M + quad * 32 + lane];
+                        const uint64_t s2 = pack2(__float_as_uint(side.x), __float_as_uint(side.x));
+                        const uint64_t z2 = pack2(__float_as_uint(side.y), __float_as_uint(side.y));
+                        const float *xg = sums + ((s * SB + i % SB) * gpb + j) * R + half * RH;
+                        constexpr int CH = RH < 16 ? RH : RH < 32 ? 16 : 32;
 #pragma unroll
-                            for (int c = 0; c < RH; c += 16) tmem_ld16_nowait(tm + (d % DS) * R + c, v + c);
+                        for (int c = 0; c < RH; c += CH) {
+                            uint32_t v[CH];
+                            if constexpr (CH == 8) {
+                                tmem_ld8(tm + (d % DS) * R, v);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < CH; k += 16) tmem_ld16_nowait(tm + (d % DS) * R + c + k, v + k);
+                            }
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int k = 0; k < CH; k += 4) {
+                                const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(xg + c + k);
+                                const int at = (c + k) / 2;
+                                acc[at] = fma2(z2, x2.x, fma2(s2, pack2(v[k], v[k + 1]), acc[at]));
+                                acc[at + 1] = fma2(z2, x2.y, fma2(s2, pack2(v[k + 2], v[k + 3]), acc[at + 1]));
+                            }
                         }
-                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                        for (int c = 0; c < RH; c += 2) acc[c / 2] = pack2(v[c], v[c + 1]);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.d_empty[d % DS]);
-                        ++d;
+                        if (d % U == U - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.d_empty[u % (DS / U)]);
+                        }
                     }
+                    __syncwarp();
+                    if (i % SB == SB - 1 && ok && lane == 0) mbar_arrive(&sm.x_empty[s]);
                 }
-                // the roots of columns l and 32 + l
-                const int64_t r0 = static_cast<int64_t>(rb) * R + half * RH;
-                const float f0 = lane < RH ? p.root[r0 + lane] : 0.0f, f1 = RH > 32 ? p.root[r0 + 32 + lane] : 0.0f;
+            } else {
+                ok = ok && __all_sync(FULL, t4_wait(sm, &sm.d_full[d % DS], (d / DS) & 1));
+                if (ok) {
+                    tc_fence_after();
+                    uint32_t v[RH];
+                    if constexpr (RH == 8) {
+                        tmem_ld8(tm + (d % DS) * R, v);
+                    } else {
 #pragma unroll
-                for (int j = 0; j < RH; ++j) {
-                    const float f = __shfl_sync(FULL, j < 32 ? f0 : f1, j & 31);
-                    if (r0 + j < p.rows && n < p.w.N) {
-                        const float v = ok ? __uint_as_float((j & 1) ? hi32(acc[j / 2]) : lo32(acc[j / 2])) * f * f : NAN;
-                        if (p.y_dt == DFLASH2_F32) static_cast<float *>(p.y)[(r0 + j) * p.y_stride + n] = v;
-                        else static_cast<uint16_t *>(p.y)[(r0 + j) * p.y_stride + n] = bf16_bits(v);
+                        for (int c = 0; c < RH; c += 16) tmem_ld16_nowait(tm + (d % DS) * R + c, v + c);
                     }
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int c = 0; c < RH; c += 2) acc[c / 2] = pack2(v[c], v[c + 1]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.d_empty[d % DS]);
+                    ++d;
                 }
-                __syncwarp();
             }
+            const uint32_t nth = blockIdx.x + item * gridDim.x, tile = nth / p.rblocks;
+            const int64_t n = static_cast<int64_t>(tile) * T4_M + quad * 32 + lane;
+            // the roots of columns l and 32 + l
+            const int64_t r0 = static_cast<int64_t>(nth - tile * p.rblocks) * R + half * RH;
+            const float f0 = lane < RH ? p.root[r0 + lane] : 0.0f, f1 = RH > 32 ? p.root[r0 + 32 + lane] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < RH; ++j) {
+                const float f = __shfl_sync(FULL, j < 32 ? f0 : f1, j & 31);
+                if (r0 + j < p.rows && n < p.w.N) {
+                    const float v = ok ? __uint_as_float((j & 1) ? hi32(acc[j / 2]) : lo32(acc[j / 2])) * f * f : NAN;
+                    if (p.y_dt == DFLASH2_F32) static_cast<float *>(p.y)[(r0 + j) * p.y_stride + n] = v;
+                    else static_cast<uint16_t *>(p.y)[(r0 + j) * p.y_stride + n] = bf16_bits(v);
+                }
+            }
+            __syncwarp();
         }
     }
     tc_fence_before();
@@ -554,7 +556,7 @@ size_t linear4_tc_bytes(int64_t rows, int64_t K) {
 }
 
 template <int RH, int LG, bool EXACT>
-static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, cudaStream_t s) {
+static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, Tc4 p, cudaStream_t s) {
     auto fn = &k_linear4_tc<RH, LG, EXACT>;
     constexpr int R = RH * 2, threads = t4_threads(RH, EXACT);
     constexpr size_t smem = 1024 + T4_XS * t4_blocks(RH) * (R * L4_BLOCK * 2 + (EXACT ? R * 4 << LG : 0)) +
@@ -563,7 +565,9 @@ static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, c
     blocks_per_sm(reinterpret_cast<const void *>(fn), threads, smem);  // raises the shared-memory limit once per device
     const int64_t sms = sm_count();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles < sms ? p.tiles : sms), 1, 1);
+    const int64_t items = static_cast<int64_t>(p.tiles) * p.rblocks, grid = items < sms ? items : sms;
+    p.step_tile = static_cast<int>(grid / p.rblocks), p.step_rb = static_cast<int>(grid % p.rblocks);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -599,12 +603,11 @@ static bool codes_map(CUtensorMap *m, const dflash2_weight4 *w) {
 }
 
 dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
-                          dflash2_dtype y_dt, int64_t y_stride, void *ws, cudaStream_t s) {
-    // a CTA's blocks are counted in 31 bits
-    if ((w->N / T4_M / sm_count() + 1) * (t4_pad(rows) / t4_rows(rows)) * (t4_kpad(w->K) / L4_BLOCK) > (1 << 30))
+                          dflash2_dtype y_dt, int64_t y_stride, bool exact, void *ws, cudaStream_t s) {
+    // items, and a CTA's blocks, are counted in 31 bits
+    const int64_t items = (w->N + T4_M - 1) / T4_M * (t4_pad(rows) / t4_rows(rows));
+    if (items > 0x7fffffff || (items / sm_count() + 1) * (t4_kpad(w->K) / L4_BLOCK) > (1 << 30))
         return DFLASH2_ERR_UNSUPPORTED;
-    // f32 results and f32 scales keep their bits; bf16 results are taken on weights in bf16
-    const bool exact = y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
     Tc4 p = {};
     const int R = t4_rows(rows);
     const int64_t kp = t4_kpad(w->K);
@@ -614,7 +617,7 @@ dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const d
     p.kpairs = static_cast<int>(kp / (2 * L4_BLOCK));
     const int64_t rows_pad = t4_pad(rows);
     p.rblocks = static_cast<int>(rows_pad / R);
-    p.tiles = (w->N + T4_M - 1) / T4_M;
+    p.tiles = static_cast<int>((w->N + T4_M - 1) / T4_M);
     uint16_t *xp = static_cast<uint16_t *>(ws);
     float *sums = reinterpret_cast<float *>(xp + rows_pad * kp);
     float *root = sums + rows_pad * (kp / 32);
