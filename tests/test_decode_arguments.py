@@ -74,7 +74,7 @@ def test_calls_on_records():
     assert linear(rows=(1 << 19) + 1) == UNSUPPORTED
     long = dict(K=(1 << 13) + 1, code_stride=1 << 13, side_stride=65)
     assert linear(long, rows=(1 << 15) + 1, x_stride=1 << 14, dt=0, y_dt=0) == UNSUPPORTED
-    assert linear({**long, "N": 4}, rows=(1 << 15) + 1, x_stride=1 << 14) == UNSUPPORTED
+    assert linear({**long, "N": 3}, rows=(1 << 15) + 1, x_stride=1 << 14) == UNSUPPORTED
     assert linear(long, rows=(1 << 15) + 1, x_stride=1 << 14) == INVALID     # these take a workspace
     L = library()
     need = L.dflash2_linear4_workspace_bytes
