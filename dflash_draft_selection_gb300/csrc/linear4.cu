@@ -26,7 +26,8 @@ struct Quant4 {
 // 32 columns to a thread, so that what a group costs (a scale and two or three divisions) is shared by as many; a group is
 // 4, 2 or 1 neighbouring lanes.  A quotient's whole number comes from the product with the reciprocal; where that (off by
 // at most 2^-18) is next to a half, the entry is read again and divided.
-// Bound: HBM, then the instructions (about 10 to an entry).
+// 151936 x 2560 bf16: 264 us (4.0 TB/s), with zero points 299 us.  Bound by instruction issue (2.6 a cycle, about 15 to an
+// entry).  One entry to a thread with a division each, the two directions of a head took 3.9 ms, now 0.46.
 template <bool F32W, int LG, bool ZERO>
 __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
     constexpr int LANES = 4 >> LG;
@@ -116,7 +117,8 @@ __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
 }
 
 // Eight columns to a thread (4 bytes of codes, 16 of bf16); a warp takes a row, or several short ones, and reads Q4_AHEAD
-// vectors before it works on them.  Bound: HBM.
+// vectors before it works on them.  151936 x 2560 to bf16: 155 us (6.3 TB/s),
+// HBM-bound; in f32 arithmetic throughout it took 30 us more.
 constexpr int Q4_AHEAD = 4;
 template <bool F32W, int LG>
 __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
@@ -206,6 +208,12 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
 // The CTA's range of x stays in shared memory for all its tiles.  Few tiles are
 // cut along K: over the warps of a CTA (kw), then over a cluster (ks CTAs, read
 // back through distributed shared memory); parts are added in order.
+//
+// 151936 x 5120, one row: 77 us (5.2 TB/s).  Bound by instruction issue: about
+// 150 for a block of 1 KB, most of them masks and shifts that share one pipe;
+// three CTAs to an SM leave too few registers for the copies (112 us).  Eight
+// rows 99 us: the same and the MMAs' operands of x.  Few tiles are bound by
+// their latency (2560 x 2560, one row: 6.2 us).
 constexpr int L4_THREADS = 256;
 constexpr int L4_WARPS = L4_THREADS / 32;
 constexpr int L4_STAGES = 4;

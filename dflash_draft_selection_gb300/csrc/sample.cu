@@ -30,6 +30,11 @@
 // a row's token is the same alone, in a batch and over any cluster.  In f32 they
 // would be off by 2^-24, and one draw in a few hundred of a flat row of 150000
 // tokens would be another token than in 64 bits.
+//
+// Bound by latency: a chain of passes, cluster barriers and one thread's 64-bit
+// arithmetic.  One row of 151936 takes 7 us greedy, 13 with top_k 20, 23 with top_p
+// in bf16 and 38 in f32; 64 rows in bf16 with top_p 38 us (bins and lists took 65),
+// 512 rows of 262144 with top_k and min_p 261 us, 1.0 TB/s.
 #include "common.cuh"
 #include "host.hpp"
 #include "tc.cuh"
