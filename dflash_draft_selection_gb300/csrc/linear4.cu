@@ -742,14 +742,18 @@ extern "C" dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, 
 // columns: 18 to 24 us, f32 results 20 to 35; 1024: 8 to 11 and 8 to 14), that of the kernel for few rows N x rows (5120
 // columns, 32 rows of 1024, 4096, 8192: 16, 20, 36 us).  At 396 sizes (9 to 512 rows, N 128 to 8192, K 256 to 17408) the
 // choice takes 1.5 % more than the faster one on average and 27 % at most, but for 128 rows of 4096 x 256 in f32 (10 us for 7).
+// f32 rows (three times the products either way) at 300 sizes up to 32768 x 17408: 1.2 % more, at most 47 % (9 rows of 8192 x
+// 17408, 111 us for 76); 64 rows of 32768 x 5120 take 267 and 87 us.
 static bool l4_many(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K, bool exact) {
+    if (rows < L4_MANY_ROWS) return false;
+    if (dt == DFLASH2_F32) return rows * N >= 3 << 15;
     const int64_t at = (1 << 17) - (3 << 26) / K;
-    return dt == DFLASH2_BF16 && rows >= L4_MANY_ROWS && rows * N >= (!exact ? at : rows > 64 ? 2 * at : at + at / 2);
+    return rows * N >= (!exact ? at : rows > 64 ? 2 * at : at + at / 2);
 }
 
 extern "C" size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K) {
     if (!dtype_ok(dt) || rows < 1 || N < 1 || K < 1 || K > L4_MAX_K || rows > L4_MAX_ROWS || !l4_many(dt, rows, N, K, false)) return 0;
-    return linear4_tc_bytes(rows, K);
+    return linear4_tc_bytes(dt == DFLASH2_F32, rows, K);
 }
 
 extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
@@ -764,10 +768,10 @@ extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (l4_many(dt, rows, w->N, w->K, false)) {
         if (!ws || !aligned16(ws)) return DFLASH2_ERR_INVALID_ARG;
-        if (ws_bytes < linear4_tc_bytes(rows, w->K)) return DFLASH2_ERR_WORKSPACE;
+        if (ws_bytes < linear4_tc_bytes(dt == DFLASH2_F32, rows, w->K)) return DFLASH2_ERR_WORKSPACE;
         // f32 results and f32 scales keep their bits; other results are taken on weights in bf16
         const bool exact = y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
-        if (l4_many(dt, rows, w->N, w->K, exact)) return linear4_tc(x, rows, x_stride, w, y, y_dt, y_stride, exact, ws, s);
+        if (l4_many(dt, rows, w->N, w->K, exact)) return linear4_tc(x, dt == DFLASH2_F32, rows, x_stride, w, y, y_dt, y_stride, exact, ws, s);
     }
     // blocks of rows are counted in 16 bits: of up to L4_LONG_K columns they have 16 rows, of more one at least
     if (rows > L4_LONG_ROWS && w->K > L4_LONG_K) return DFLASH2_ERR_UNSUPPORTED;

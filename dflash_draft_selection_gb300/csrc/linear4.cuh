@@ -98,9 +98,9 @@ __device__ __forceinline__ float scale8(float (&v)[8], int e) {
     return sum * pow2f((e - 133) / 2 - (e >> 1) / 2) * pow2f(e - 133 - (e >> 1) - ((e - 133) / 2 - (e >> 1) / 2));
 }
 
-// Many rows (linear4_tc.cu).  bf16 rows only.
-size_t linear4_tc_bytes(int64_t rows, int64_t K);
-dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
+// Many rows (linear4_tc.cu).
+size_t linear4_tc_bytes(bool f32x, int64_t rows, int64_t K);
+dflash2_status linear4_tc(const void *x, bool f32x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
                           dflash2_dtype y_dt, int64_t y_stride, bool exact, void *ws, cudaStream_t s);
 
 }  // namespace dfl

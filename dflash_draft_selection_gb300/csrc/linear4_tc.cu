@@ -4,7 +4,9 @@
 // Weights on the M side (128 rows), x on the N side (up to 128 rows):
 //   part[128 x R] = codes[128 x group] . x'[R x group]^T     per group of columns
 //   acc += scale * (part - zero * sum of x)                  in registers, f32
-// so products are exact whatever the scales, and a result is rounded once.
+// so products are exact whatever the scales, and a result is rounded once.  f32
+// rows are three bf16 parts, which is exact too: three products into the same
+// accumulator, blocks of up to 32 rows.
 //
 // The codes go by TMA into a warp's own ring in shared memory and through its
 // registers into tensor memory, where the MMA takes its A operand: with A in
@@ -29,7 +31,7 @@
 // 151936 x 2560 in groups of 128 94 us, of 32 228 us; bound by the chain MMA -
 // barrier - tensor memory load - barrier per group; loads of a second group ahead
 // gained nothing, and spilled at 128 rows.  512 rows of 7168 x 5120 by items 40 us,
-// by whole tiles 73.
+// by whole tiles 73.  64 f32 rows of 32768 x 5120 87 us (k_linear4_mma: 267).
 //
 // Waits are bounded: after a time-out every role stops waiting, the error word
 // is set and the CTA's remaining outputs are NaN.
@@ -46,7 +48,8 @@ static __device__ unsigned int g_err_linear4;
 constexpr int t4_sets(int rh, bool exact) { return exact && rh > 32 ? 1 : 2; }
 constexpr int t4_threads(int rh, bool exact) { return (8 + 4 * t4_sets(rh, exact) + 2) * 32; }
 constexpr int T4_XS = 4;                                     // stages of x'
-constexpr int t4_blocks(int rh) { return rh > 32 ? 1 : 2; }  // of 128 columns in a stage: a barrier costs its waiter 150 cycles
+// Blocks of 128 columns in a stage: a barrier costs its waiter 150 cycles.  The parts of f32 rows leave room for one.
+constexpr int t4_blocks(int rh, int parts) { return rh > 32 || parts > 1 ? 1 : 2; }
 constexpr int t4_ring(int rh, bool exact) { return exact && rh > 32 ? 4 : 2; }  // pairs of blocks of codes that an operand warp has room for
 constexpr int T4_AS = 4;      // blocks of A in tensor memory
 // Blocks whose scales are kept.  A block's are overwritten when the operand is this many further on: it is at most 4
@@ -85,15 +88,16 @@ struct Tc4 {
 };
 
 // ---------------------------------------------------------------- x' ----
-// One CTA per row: x' [rows_pad, kblocks * 128], scaled for the codes as operands or for weights in bf16 (then without
+// One CTA per row: x' [rows_pad, kblocks * 128] (f32: three matrices of bf16 parts, exact), scaled for the codes as operands or for weights in bf16 (then without
 // the groups' sums), and the root of the power of two.  Rows past the last are zeros.
+template <bool F32X>
 __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t rows, int64_t x_stride, int K, int lg,
                                                       int kblocks, int R, bool scaled, uint16_t *out, float *sums,
                                                       float *root) {
     __shared__ uint32_t top;
     const int64_t r = blockIdx.x;
     const int chunks = kblocks * (L4_BLOCK / 8), lanes = 16 >> lg;
-    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride % 8 == 0;
+    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride * (F32X ? 4 : 2) % 16 == 0;
     pdl_trigger();  // the product may start; it waits before it reads what is written here
     if (threadIdx.x == 0) top = 0;
     __syncthreads();
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
     if (r < rows)
         for (int c = threadIdx.x; c < chunks; c += 256) {
             float v[8];
-            load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
+            load8<F32X>(x, r * x_stride + c * 8, K - c * 8, vec, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
         }
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
     if (threadIdx.x == 0) root[r] = scaled || bad ? x_root(m, e) : pow2f((T4_DOWN - e) / 2);
     for (int c = threadIdx.x; c < chunks; c += 256) {  // chunks is a multiple of 16: half-warps stay whole
         float v[8] = {};
-        if (r < rows) load8<false>(x, r * x_stride + c * 8, K - c * 8, vec, v);
+        if (r < rows) load8<F32X>(x, r * x_stride + c * 8, K - c * 8, vec, v);
         if (bad) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = 0.0f;
@@ -127,9 +131,17 @@ __global__ void __launch_bounds__(256) k_linear4_rows(const void *x, int64_t row
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = scale2(v[j], e);
         }
-        uint4 o;
-        o.x = bf16_pair(v[0], v[4]), o.y = bf16_pair(v[1], v[5]), o.z = bf16_pair(v[2], v[6]), o.w = bf16_pair(v[3], v[7]);
-        *reinterpret_cast<uint4 *>(out + (r * kblocks * L4_BLOCK + c * 8)) = o;
+#pragma unroll
+        for (int q = 0; q < (F32X ? 3 : 1); ++q) {
+            uint4 o;
+            uint32_t *ow = &o.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ow[j] = bf16_pair(v[j], v[j + 4]);
+                if (F32X) v[j] -= bf16lo(ow[j]), v[j + 4] -= bf16hi(ow[j]);
+            }
+            *reinterpret_cast<uint4 *>(out + ((q * static_cast<int64_t>(gridDim.x) + r) * kblocks * L4_BLOCK + c * 8)) = o;
+        }
     }
 }
 
@@ -236,18 +248,18 @@ __device__ __forceinline__ void operand(const uint32_t *v, uint32_t to, const ui
 }
 
 // RH: half of the block's rows of x, the columns of an epilogue warp.  LG: log2 of the groups in a block.  EXACT: the
-// operand is the codes; otherwise it is the weights in bf16.
-template <int RH, int LG, bool EXACT>
+// operand is the codes; otherwise it is the weights in bf16.  PARTS: matrices of x', 3 for f32 rows.
+template <int RH, int LG, bool EXACT, int PARTS>
 __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const __grid_constant__ CUtensorMap tm_x,
                                                               const __grid_constant__ CUtensorMap tm_c, const Tc4 p) {
-    constexpr int R = RH * 2, XB = R * L4_BLOCK * 2;  // bytes of a stage of x'
+    constexpr int R = RH * 2, XB = R * L4_BLOCK * 2;  // bytes of a block of a part of x'
     constexpr int gpb = 1 << LG, STEPS = 8 >> LG;      // groups of a block, steps of 16 columns in a group
     constexpr int T4_SIDES = t4_sides(LG);
-    constexpr int XS = T4_XS, SB = t4_blocks(RH), RING = t4_ring(RH, EXACT), SETS = t4_sets(RH, EXACT), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
+    constexpr int XS = T4_XS, SB = t4_blocks(RH, PARTS), RING = t4_ring(RH, EXACT), SETS = t4_sets(RH, EXACT), T4_COPY = 8 + 4 * SETS, T4_MMA = T4_COPY + 1;
     extern __shared__ unsigned char raw[];
     __shared__ Tc4Shared sm;
     unsigned char *xs = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char *rings = xs + XS * SB * XB;                              // 4 KB each: 32 rows of 256 codes
+    unsigned char *rings = xs + XS * SB * PARTS * XB;                              // 4 KB each: 32 rows of 256 codes
     float *sums = reinterpret_cast<float *>(rings + 4 * SETS * RING * 4096);  // [stage][group of the stage][R]
     float2 *sides = reinterpret_cast<float2 *>(sums + XS * SB * gpb * R);  // [block][group][weight row]: scale, -scale * zero
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -285,10 +297,13 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
             for (; ok && i < total / SB; ++i) {
                 const int s = i % XS;
                 if (i >= XS && !t4_wait(sm, &sm.x_empty[s], static_cast<uint32_t>(i / XS - 1) & 1)) break;
-                mbar_arrive_expect_tx(&sm.x_full[s], SB * (XB + (EXACT ? gpb * R * 4 : 0)));
+                mbar_arrive_expect_tx(&sm.x_full[s], SB * (PARTS * XB + (EXACT ? gpb * R * 4 : 0)));
 #pragma unroll
-                for (int h = 0; h < 2 * SB; ++h)
-                    tma_load_2d(xs + (s * 2 * SB + h) * (XB / 2), &tm_x, at.kb * L4_BLOCK + h * 64, at.rb * R, &sm.x_full[s]);
+                for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2 * SB; ++h)
+                        tma_load_2d(xs + ((s * PARTS + q) * 2 * SB + h) * (XB / 2), &tm_x, at.kb * L4_BLOCK + h * 64,
+                                    (q * p.rblocks + at.rb) * R, &sm.x_full[s]);
                 // sums [row block][group][R]: a stage's lie together
                 if (EXACT)
                     bulk_g2s(sums + s * SB * gpb * R, p.sums + (static_cast<int64_t>(at.rb) * 2 * p.kpairs + at.kb) * gpb * R,
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
             const int s = i / SB % XS, sa = i % T4_AS;
             if (i % SB == 0) ok = __all_sync(FULL, t4_wait(sm, &sm.x_full[s], static_cast<uint32_t>(i / SB / XS) & 1));
             if (!ok) break;
-            const uint64_t b0 = x0 + ((s * SB + i % SB) * XB >> 4);
+            const uint64_t b0 = x0 + ((s * SB * PARTS + i % SB) * XB >> 4);
             const uint32_t a0 = tmem_a + sa * 64;
             if constexpr (EXACT) {
 #pragma unroll
@@ -326,10 +341,13 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
                     const uint32_t to = tmem + (d % DS) * R;
                     if (leader) {
 #pragma unroll
-                        for (int k = 0; k < STEPS; ++k) {
-                            const int at = j * STEPS + k;  // 16 columns: 32 bytes of x', 8 columns of tensor memory
-                            mma_bf16_ts(to, a0 + at * 8, b0 + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc, k > 0);
-                        }
+                        for (int q = PARTS - 1; q >= 0; --q)  // the small parts first
+#pragma unroll
+                            for (int k = 0; k < STEPS; ++k) {
+                                const int at = j * STEPS + k;  // 16 columns: 32 bytes of x', 8 columns of tensor memory
+                                mma_bf16_ts(to, a0 + at * 8, b0 + (q * XB >> 4) + (at & 4 ? (XB / 2 >> 4) : 0) + 2 * (at & 3), idesc,
+                                            q < PARTS - 1 || k > 0);
+                            }
                         if (d % U == U - 1) mma_commit(&sm.d_full[u % (DS / U)]), mbar_arrive(&sm.d_full[u % (DS / U)]);
                     }
                     __syncwarp();
@@ -555,20 +573,20 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
 
 // ------------------------------------------------------------------ host ----
 // Rows of x to a block.
-static int t4_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
-static int64_t t4_pad(int64_t rows) { return (rows + t4_rows(rows) - 1) / t4_rows(rows) * t4_rows(rows); }
+static int t4_rows(int64_t rows, bool f32x) { return rows <= 16 ? 16 : rows <= 32 || f32x ? 32 : rows <= 64 ? 64 : 128; }
+static int64_t t4_pad(int64_t rows, bool f32x) { return (rows + t4_rows(rows, f32x) - 1) / t4_rows(rows, f32x) * t4_rows(rows, f32x); }
 static int64_t t4_kpad(int64_t K) { return (K + 2 * L4_BLOCK - 1) / (2 * L4_BLOCK) * (2 * L4_BLOCK); }
 
 // Workspace: x', the sums (of the smallest groups), the roots.
-size_t linear4_tc_bytes(int64_t rows, int64_t K) {
-    return static_cast<size_t>(t4_pad(rows)) * (t4_kpad(K) * 2 + t4_kpad(K) / 32 * 4 + 4);
+size_t linear4_tc_bytes(bool f32x, int64_t rows, int64_t K) {
+    return static_cast<size_t>(t4_pad(rows, f32x)) * (t4_kpad(K) * (f32x ? 6 : 2) + t4_kpad(K) / 32 * 4 + 4);
 }
 
-template <int RH, int LG, bool EXACT>
+template <int RH, int LG, bool EXACT, int PARTS>
 static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, Tc4 p, cudaStream_t s) {
-    auto fn = &k_linear4_tc<RH, LG, EXACT>;
+    auto fn = &k_linear4_tc<RH, LG, EXACT, PARTS>;
     constexpr int R = RH * 2, threads = t4_threads(RH, EXACT);
-    constexpr size_t smem = 1024 + T4_XS * t4_blocks(RH) * (R * L4_BLOCK * 2 + (EXACT ? R * 4 << LG : 0)) +
+    constexpr size_t smem = 1024 + T4_XS * t4_blocks(RH, PARTS) * (PARTS * R * L4_BLOCK * 2 + (EXACT ? R * 4 << LG : 0)) +
                             4 * t4_sets(RH, EXACT) * t4_ring(RH, EXACT) * 4096 + (EXACT ? t4_sides(LG) * T4_M * 8 << LG : 0);
     static_assert(smem + sizeof(Tc4Shared) <= 227 * 1024, "shared memory of a CTA");
     blocks_per_sm(reinterpret_cast<const void *>(fn), threads, smem);  // raises the shared-memory limit once per device
@@ -587,16 +605,15 @@ static dflash2_status launch_tc4(const CUtensorMap &tm, const CUtensorMap &tc, T
     return after_launch();
 }
 
+template <int RH, bool EXACT, int PARTS>
+static dflash2_status launch_tc4_groups(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, cudaStream_t s) {
+    if (p.lg == 0) return launch_tc4<RH, 0, EXACT, PARTS>(tm, tc, p, s);
+    if (p.lg == 1) return launch_tc4<RH, 1, EXACT, PARTS>(tm, tc, p, s);
+    return launch_tc4<RH, 2, EXACT, PARTS>(tm, tc, p, s);
+}
 template <int RH>
-static dflash2_status launch_tc4_groups(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, bool exact, cudaStream_t s) {
-    if (exact) {
-        if (p.lg == 0) return launch_tc4<RH, 0, true>(tm, tc, p, s);
-        if (p.lg == 1) return launch_tc4<RH, 1, true>(tm, tc, p, s);
-        return launch_tc4<RH, 2, true>(tm, tc, p, s);
-    }
-    if (p.lg == 0) return launch_tc4<RH, 0, false>(tm, tc, p, s);
-    if (p.lg == 1) return launch_tc4<RH, 1, false>(tm, tc, p, s);
-    return launch_tc4<RH, 2, false>(tm, tc, p, s);
+static dflash2_status launch_tc4_kind(const CUtensorMap &tm, const CUtensorMap &tc, const Tc4 &p, bool exact, cudaStream_t s) {
+    return exact ? launch_tc4_groups<RH, true, 1>(tm, tc, p, s) : launch_tc4_groups<RH, false, 1>(tm, tc, p, s);
 }
 
 // Codes [N, bytes of a row], boxes of 32 rows of 128 bytes; zeros past the edges.
@@ -611,40 +628,42 @@ static bool codes_map(CUtensorMap *m, const dflash2_weight4 *w) {
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-dflash2_status linear4_tc(const void *x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
+dflash2_status linear4_tc(const void *x, bool f32x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
                           dflash2_dtype y_dt, int64_t y_stride, bool exact, void *ws, cudaStream_t s) {
     // items, and a CTA's blocks, are counted in 31 bits
-    const int64_t items = (w->N + T4_M - 1) / T4_M * (t4_pad(rows) / t4_rows(rows));
+    const int R = t4_rows(rows, f32x);
+    const int64_t rows_pad = t4_pad(rows, f32x), items = (w->N + T4_M - 1) / T4_M * (rows_pad / R);
     if (items > 0x7fffffff || (items / sm_count() + 1) * (t4_kpad(w->K) / L4_BLOCK) > (1 << 30))
         return DFLASH2_ERR_UNSUPPORTED;
     Tc4 p = {};
-    const int R = t4_rows(rows);
     const int64_t kp = t4_kpad(w->K);
     p.w = *w, p.y = y, p.rows = rows, p.y_stride = y_stride, p.y_dt = y_dt;
     p.lg = w->group == 128 ? 0 : w->group == 64 ? 1 : 2;
     p.G = static_cast<int>(groups_of(w));
     p.kpairs = static_cast<int>(kp / (2 * L4_BLOCK));
-    const int64_t rows_pad = t4_pad(rows);
     p.rblocks = static_cast<int>(rows_pad / R);
     p.tiles = static_cast<int>((w->N + T4_M - 1) / T4_M);
     uint16_t *xp = static_cast<uint16_t *>(ws);
-    float *sums = reinterpret_cast<float *>(xp + rows_pad * kp);
+    const int parts = f32x ? 3 : 1;
+    float *sums = reinterpret_cast<float *>(xp + parts * rows_pad * kp);
     float *root = sums + rows_pad * (kp / 32);
     p.sums = sums, p.root = root;
     scan_hold(&p.hold, &p.hold_cycles);
     CUtensorMap tm;
-    if (!make_map_k64(&tm, xp, static_cast<uint64_t>(kp), static_cast<uint64_t>(rows_pad), static_cast<uint32_t>(R)))
+    if (!make_map_k64(&tm, xp, static_cast<uint64_t>(kp), static_cast<uint64_t>(parts * rows_pad), static_cast<uint32_t>(R)))
         return DFLASH2_ERR_CUDA;
     CUtensorMap tc;
     if (!codes_map(&tc, w)) return DFLASH2_ERR_CUDA;
-    k_linear4_rows<<<static_cast<unsigned>(rows_pad), 256, 0, s>>>(x, rows, x_stride, static_cast<int>(w->K), p.lg,
-                                                                     2 * p.kpairs, R, exact, xp, sums, root);
+    auto prepare = f32x ? &k_linear4_rows<true> : &k_linear4_rows<false>;
+    prepare<<<static_cast<unsigned>(rows_pad), 256, 0, s>>>(x, rows, x_stride, static_cast<int>(w->K), p.lg, 2 * p.kpairs, R,
+                                                            exact, xp, sums, root);
     const dflash2_status st = after_launch();
     if (st != DFLASH2_OK) return st;
-    if (R == 16) return launch_tc4_groups<8>(tm, tc, p, exact, s);
-    if (R == 32) return launch_tc4_groups<16>(tm, tc, p, exact, s);
-    if (R == 64) return launch_tc4_groups<32>(tm, tc, p, exact, s);
-    return launch_tc4_groups<64>(tm, tc, p, exact, s);
+    if (f32x) return R == 16 ? launch_tc4_groups<8, true, 3>(tm, tc, p, s) : launch_tc4_groups<16, true, 3>(tm, tc, p, s);
+    if (R == 16) return launch_tc4_kind<8>(tm, tc, p, exact, s);
+    if (R == 32) return launch_tc4_kind<16>(tm, tc, p, exact, s);
+    if (R == 64) return launch_tc4_kind<32>(tm, tc, p, exact, s);
+    return launch_tc4_kind<64>(tm, tc, p, exact, s);
 }
 
 unsigned int read_error_linear4(bool clear) {

@@ -73,12 +73,13 @@ def test_calls_on_records():
     assert linear(dict(K=(1 << 17) + 1, code_stride=1 << 17, side_stride=1 << 17), x_stride=1 << 18) == UNSUPPORTED
     assert linear(rows=(1 << 19) + 1) == UNSUPPORTED
     long = dict(K=(1 << 13) + 1, code_stride=1 << 13, side_stride=65)
-    assert linear(long, rows=(1 << 15) + 1, x_stride=1 << 14, dt=0, y_dt=0) == UNSUPPORTED
+    assert linear({**long, "N": 2}, rows=(1 << 15) + 1, x_stride=1 << 14, dt=0, y_dt=0) == UNSUPPORTED
     assert linear({**long, "N": 3}, rows=(1 << 15) + 1, x_stride=1 << 14) == UNSUPPORTED
     assert linear(long, rows=(1 << 15) + 1, x_stride=1 << 14) == INVALID     # these take a workspace
     L = library()
     need = L.dflash2_linear4_workspace_bytes
-    assert need(1, 1, 40, 200) == need(0, 512, 151936, 200) == need(1, 0, 40, 200) == need(1, 1 << 20, 1 << 20, 1) == 0
+    assert need(1, 1, 40, 200) == need(0, 8, 151936, 200) == need(1, 0, 40, 200) == need(1, 1 << 20, 1 << 20, 1) == 0
+    assert need(0, 512, 151936, 200) >= 512 * 256 * 6
     big = dict(N=151936)
     assert need(1, 512, 151936, 200) >= 512 * 256 * 2
     assert linear(big, rows=512, y_stride=151936) == linear(big, rows=512, y_stride=151936, ws=4104, ws_bytes=1 << 40) == INVALID

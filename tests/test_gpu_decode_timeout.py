@@ -30,6 +30,21 @@ def test_products_give_up_and_recover(rows, N, K, group, out):
     assert d2.device_error() == 0
 
 
+@pytest.mark.parametrize("rows", [16, 70])
+def test_products_of_f32_rows_give_up_and_recover(rows):
+    dev = cuda_or_skip()
+    w = weights(11000, 640, 64, True, seed=1)
+    x = torch.randn(rows, 640, generator=gen(rows), device=dev)
+    ws = d2.Workspace.for_linear4(rows, 11000, 640, F32)
+    assert ws.nbytes > 16
+    y = torch.zeros(rows, 11000, device=dev)
+    _, code = held(lambda: d2.linear4(x, w, ws=ws, out=y))
+    assert code == 1   # DFLASH2_DEVERR_WAIT_TIMEOUT
+    assert y.isnan().all()
+    check(d2.linear4(x, w, ws=ws, out=y), x, w)
+    assert d2.device_error() == 0
+
+
 def test_a_hook_that_is_set_in_time_changes_nothing():
     dev = cuda_or_skip()
     w = weights(5000, 300, 128, False, seed=1)

@@ -175,6 +175,21 @@ def test_products_f32(rows, N, K, group, zero, side):
     check(d2.linear4(x, w), x, w)
 
 
+@pytest.mark.parametrize("rows", [9, 16, 17, 32, 33, 100, 300])
+@pytest.mark.parametrize("N,K,group,zero,side", [(11000, 200, 64, True, BF), (10925, 1312, 32, True, F32), (11223, 31, 32, False, BF),
+                                                 (12000, 2560, 128, False, BF), (25000, 520, 128, True, F32)])
+def test_products_of_many_f32_rows(rows, N, K, group, zero, side):
+    """Wide enough for the tensor cores' tiles: one and several to a CTA, the last ones cut."""
+    cuda_or_skip()
+    w = weights(N, K, group, zero, side, seed=N)
+    x = torch.randn(rows, K, generator=gen(rows), device="cuda")
+    check(d2.linear4(x, w), x, w)
+    ws = d2.Workspace.for_linear4(rows, N, K, F32)
+    assert ws.nbytes > 16
+    check(d2.linear4(x, w, ws=ws), x, w)
+    assert d2.device_error() == 0
+
+
 @pytest.mark.parametrize("rows", [1, 8, 40, 200])
 def test_products_of_a_wide_head(rows):
     """More weight rows than the GPU has warps; N odd, so that output rows are not aligned."""
