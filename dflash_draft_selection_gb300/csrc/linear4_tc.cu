@@ -572,14 +572,14 @@ __global__ void __launch_bounds__(t4_threads(RH, EXACT), 1) k_linear4_tc(const _
 }
 
 // ------------------------------------------------------------------ host ----
-// Rows of x to a block.
-static int t4_rows(int64_t rows, bool f32x) { return rows <= 16 ? 16 : rows <= 32 || f32x ? 32 : rows <= 64 ? 64 : 128; }
-static int64_t t4_pad(int64_t rows, bool f32x) { return (rows + t4_rows(rows, f32x) - 1) / t4_rows(rows, f32x) * t4_rows(rows, f32x); }
+// Rows of x to a block, 32, 64 or 128 at most.
+static int t4_rows(int64_t rows, int most) { return rows <= 16 ? 16 : rows <= 32 || most == 32 ? 32 : rows <= 64 || most == 64 ? 64 : 128; }
+static int64_t t4_pad(int64_t rows, int most) { return (rows + t4_rows(rows, most) - 1) / t4_rows(rows, most) * t4_rows(rows, most); }
 static int64_t t4_kpad(int64_t K) { return (K + 2 * L4_BLOCK - 1) / (2 * L4_BLOCK) * (2 * L4_BLOCK); }
 
 // Workspace: x', the sums (of the smallest groups), the roots.
 size_t linear4_tc_bytes(bool f32x, int64_t rows, int64_t K) {
-    return static_cast<size_t>(t4_pad(rows, f32x)) * (t4_kpad(K) * (f32x ? 6 : 2) + t4_kpad(K) / 32 * 4 + 4);
+    return static_cast<size_t>(t4_pad(rows, f32x ? 32 : 128)) * (t4_kpad(K) * (f32x ? 6 : 2) + t4_kpad(K) / 32 * 4 + 4);
 }
 
 template <int RH, int LG, bool EXACT, int PARTS>
@@ -631,8 +631,10 @@ static bool codes_map(CUtensorMap *m, const dflash2_weight4 *w) {
 dflash2_status linear4_tc(const void *x, bool f32x, int64_t rows, int64_t x_stride, const dflash2_weight4 *w, void *y,
                           dflash2_dtype y_dt, int64_t y_stride, bool exact, void *ws, cudaStream_t s) {
     // items, and a CTA's blocks, are counted in 31 bits
-    const int R = t4_rows(rows, f32x);
-    const int64_t rows_pad = t4_pad(rows, f32x), items = (w->N + T4_M - 1) / T4_M * (rows_pad / R);
+    // several groups to a block of columns take the epilogue of 128 rows more registers than it has (512 rows of 151936 x
+    // 5120 in groups of 32: 4125 us, with 64 rows 3373; of 64: 2075 and 1896)
+    const int most = f32x ? 32 : exact && w->group < 128 ? 64 : 128, R = t4_rows(rows, most);
+    const int64_t rows_pad = t4_pad(rows, most), items = (w->N + T4_M - 1) / T4_M * (rows_pad / R);
     if (items > 0x7fffffff || (items / sm_count() + 1) * (t4_kpad(w->K) / L4_BLOCK) > (1 << 30))
         return DFLASH2_ERR_UNSUPPORTED;
     Tc4 p = {};
@@ -663,7 +665,7 @@ dflash2_status linear4_tc(const void *x, bool f32x, int64_t rows, int64_t x_stri
     if (R == 16) return launch_tc4_kind<8>(tm, tc, p, exact, s);
     if (R == 32) return launch_tc4_kind<16>(tm, tc, p, exact, s);
     if (R == 64) return launch_tc4_kind<32>(tm, tc, p, exact, s);
-    return launch_tc4_kind<64>(tm, tc, p, exact, s);
+    return exact ? launch_tc4<64, 0, true, 1>(tm, tc, p, s) : launch_tc4_groups<64, false, 1>(tm, tc, p, s);
 }
 
 unsigned int read_error_linear4(bool clear) {
