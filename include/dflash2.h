@@ -620,8 +620,8 @@ dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dty
  *   y_dt is dt, or f32.  A row of x that holds a NaN or an infinity gives a
  *   row of NaN.
  *   Sums are f32 sums of exact products of codes and of zero points with x;
- *   entries of x below 2^-130 of their row's largest and scales below 2^-100
- *   lose bits.  bf16 results for many rows (those that take a workspace) with
+ *   entries of x below 2^-130 of their row's largest (f32: 2^-110) and scales
+ *   below 2^-100 lose bits.  bf16 results for many rows (those that take a workspace) with
  *   bf16 scales are sums of x times the weights rounded to bf16 (code - zero,
  *   then its product with the scale), for scales from 2^-80 to 2^30 (and 0);
  *   entries of x below 2^-80 of their row's largest lose bits.  Scales beyond
@@ -664,7 +664,7 @@ dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, in
  *   how the row is split.
  * A row with a NaN or +Inf, nothing above -Inf, a NaN uniform or invalid
  * parameters (as DFLASH2_ST_BAD_PARAMS; min_p outside [0, 1]) gets token -1 and
- * prob NaN.
+ * prob NaN.  f32 logits further below the largest than f32 reaches have no mass.
  * Errors: INVALID_ARG for a NULL or misaligned pointer (logits: 16 bytes; the
  * others: 4), rows < 0, V < 1 or V >= 2^31, ld < V, ld * elem size not a
  * multiple of 16, rows_per_param < 1; UNSUPPORTED for 2^28 rows and more.

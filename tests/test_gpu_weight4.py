@@ -366,3 +366,33 @@ def test_calls_are_repeatable_and_captured(rows):
     torch.cuda.synchronize()
     assert torch.equal(out, d2.linear4(x2, w))
     assert d2.device_error() == 0
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_two_streams_and_two_graphs(dt):
+    """Calls at one time, each with its workspace; two graphs that share one, replayed in turn."""
+    dev = cuda_or_skip()
+    w = [weights(9000, 640, 64, True, seed=s) for s in (1, 2)]
+    x = [torch.randn(40, 640, generator=gen(s), device=dev, dtype=dt) for s in (3, 4)]
+    want = [d2.linear4(a, b) for a, b in zip(x, w)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [d2.Workspace.for_linear4(40, 9000, 640, dt) for _ in range(2)]
+    out = [torch.full_like(want[0], math.nan) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                d2.linear4(x[i], w[i], ws=ws[i], out=out[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        out[i].fill_(math.nan)
+        with torch.cuda.graph(g):
+            d2.linear4(x[i], w[i], ws=ws[0], out=out[i])
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert d2.device_error() == 0
