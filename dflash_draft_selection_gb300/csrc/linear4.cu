@@ -119,12 +119,46 @@ __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
 // Eight columns to a thread (4 bytes of codes, 16 of bf16); a warp takes a row, or several short ones, and reads Q4_AHEAD
 // vectors before it works on them.  151936 x 2560 to bf16: 155 us (6.3 TB/s),
 // HBM-bound; in f32 arithmetic throughout it took 30 us more.
+//
+// VEC: the rows start on 16-byte boundaries.  Where they do not, a warp's 256 values take their places in shared memory and
+// are written as neighbours by neighbouring lanes (152001 x 2561: 456 us, by the lanes that have them 949).
 constexpr int Q4_AHEAD = 4;
-template <bool F32W, int LG>
+template <bool F32W, int LG, bool VEC>
 __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
     constexpr int LANES = 16 >> LG;
     const int lane = threadIdx.x & 31, span = 1 << p.span_log2;
     const int64_t n = (((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) << (5 - p.span_log2)) + (lane >> p.span_log2);
+    if constexpr (!VEC) {
+        __shared__ float4 place[8][64];
+        const int64_t n0 = n - (lane >> p.span_log2);
+        float4 *mine = place[threadIdx.x >> 5];
+        for (int c0 = 0; c0 < p.codes; c0 += span) {
+            const int c = c0 + (lane & (span - 1));
+            float v[8] = {};
+            if (n < p.w.N && static_cast<int64_t>(c) * 8 < p.w.K) {
+                const uint32_t word = *reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(p.w.codes) +
+                                                                          n * p.w.code_stride + static_cast<int64_t>(c) * 4);
+                const int64_t at = n * p.w.side_stride + c / LANES;
+                const float s = side_at(p.w.scale, p.w.side_dt, at), z = p.w.zero ? side_at(p.w.zero, p.w.side_dt, at) : 8.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = (static_cast<float>((word >> (4 * j)) & 15u) - z) * s;
+            }
+            __syncwarp();  // the last values have been read
+            mine[lane * 2] = make_float4(v[0], v[1], v[2], v[3]), mine[lane * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int e = j * 32 + lane, from = e >> 3;
+                const int64_t row = n0 + (from >> p.span_log2), k = static_cast<int64_t>(c0 + (from & (span - 1))) * 8 + (e & 7);
+                const float o = reinterpret_cast<const float *>(mine)[e];
+                if (row < p.w.N && k < p.w.K) {
+                    if (F32W) static_cast<float *>(out)[row * p.ld + k] = o;
+                    else static_cast<uint16_t *>(out)[row * p.ld + k] = bf16_bits(o);
+                }
+            }
+        }
+        return;
+    }
     if (n >= p.w.N) return;
     const uint8_t *codes = static_cast<const uint8_t *>(p.w.codes) + n * p.w.code_stride;
     for (int c0 = lane & (span - 1); c0 < p.codes; c0 += span * Q4_AHEAD) {
@@ -146,7 +180,7 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
             const int64_t left = p.w.K - static_cast<int64_t>(c) * 8, at = n * p.ld + static_cast<int64_t>(c) * 8;
             if (left <= 0) break;
             const float s = side_of(sb[i], p.w.side_dt), z = p.w.zero ? side_of(zb[i], p.w.side_dt) : 8.0f;
-            if (!F32W && left >= 8 && p.vec && p.w.side_dt == DFLASH2_BF16 && fabsf(s) < 1e30f &&
+            if (!F32W && left >= 8 && p.w.side_dt == DFLASH2_BF16 && fabsf(s) < 1e30f &&
                 (!p.w.zero || (fabsf(z) <= 128.0f && z == rintf(z)))) {
                 // In packed bf16: 128 + code is a number whose low bits are the code, code - zero is exact for whole zero
                 // points up to 128, and one rounding is left.
@@ -172,7 +206,7 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = (v[j] - 8388616.0f) * s;
             }
-            if (left >= 8 && p.vec) {
+            if (left >= 8) {
                 if (F32W) {
                     float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
                     o[0] = make_float4(v[0], v[1], v[2], v[3]), o[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -703,11 +737,16 @@ static void launch_quant4_groups(const Quant4 &p, unsigned grid, cudaStream_t s)
     else if (p.w.group == 64) launch_quant4<F32W, 1>(p, grid, s);
     else launch_quant4<F32W, 2>(p, grid, s);
 }
+template <bool F32W, int LG>
+static void launch_dequant4_rows(const Quant4 &p, void *out, unsigned grid, cudaStream_t s) {
+    if (p.vec) k_dequant4<F32W, LG, true><<<grid, 256, 0, s>>>(p, out);
+    else k_dequant4<F32W, LG, false><<<grid, 256, 0, s>>>(p, out);
+}
 template <bool F32W>
 static void launch_dequant4(const Quant4 &p, void *out, unsigned grid, cudaStream_t s) {
-    if (p.w.group == 128) k_dequant4<F32W, 0><<<grid, 256, 0, s>>>(p, out);
-    else if (p.w.group == 64) k_dequant4<F32W, 1><<<grid, 256, 0, s>>>(p, out);
-    else k_dequant4<F32W, 2><<<grid, 256, 0, s>>>(p, out);
+    if (p.w.group == 128) launch_dequant4_rows<F32W, 0>(p, out, grid, s);
+    else if (p.w.group == 64) launch_dequant4_rows<F32W, 1>(p, out, grid, s);
+    else launch_dequant4_rows<F32W, 2>(p, out, grid, s);
 }
 
 extern "C" dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w,
