@@ -98,6 +98,7 @@ def load_library():
         L.dflash2_linear4_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.dflash2_linear4_workspace_bytes.restype = sz
         L.dflash2_linear4.argtypes = [vp, i32, i64, i64, vp, vp, i32, i64, vp, sz, vp]
+        L.dflash2_linear4_rounded.argtypes = L.dflash2_linear4.argtypes
         L.dflash2_sample.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp]
         L.dflash2_status_string.argtypes = [i32]
         L.dflash2_status_string.restype = ctypes.c_char_p
@@ -108,7 +109,7 @@ def load_library():
                    "dflash2_ctx_gate", "dflash2_pair_score_walk",
                    "dflash2_verify", "dflash2_conv2tap", "dflash2_dynconv2tap", "dflash2_device_error",
                    "dflash2_test_hold", "dflash2_rope_append", "dflash2_paged_attn", "dflash2_kv_evict",
-                   "dflash2_quant4", "dflash2_dequant4", "dflash2_linear4", "dflash2_sample"):
+                   "dflash2_quant4", "dflash2_dequant4", "dflash2_linear4", "dflash2_linear4_rounded", "dflash2_sample"):
             getattr(L, fn).restype = i32
         _lib = L
         return _lib
@@ -660,9 +661,10 @@ def dequant4(w: Weight4, dtype=torch.bfloat16, out=None) -> torch.Tensor:
     return out
 
 
-def linear4(x: torch.Tensor, w: Weight4, dtype=None, ws=None, out=None) -> torch.Tensor:
+def linear4(x: torch.Tensor, w: Weight4, dtype=None, ws=None, out=None, rounded: bool = False) -> torch.Tensor:
     """dflash2_linear4.  x [rows, K] (bf16/f32, contiguous rows).  Returns x . W^T [rows, N] of x's type or float32, or
-    fills `out` (contiguous rows, any distance from row to row)."""
+    fills `out` (contiguous rows, any distance from row to row).  With rounded, dflash2_linear4_rounded: many rows of bf16
+    may be taken on weights rounded to bf16, which is faster."""
     dev = _here(w, "weights")
     rows = x.shape[0]
     xp, xs = _rows("x", x, (rows, w.K), dev)
@@ -676,8 +678,8 @@ def linear4(x: torch.Tensor, w: Weight4, dtype=None, ws=None, out=None) -> torch
         scratch = (buf.data_ptr(), need) if need else (None, 0)
     else:
         scratch = _scratch(ws, dev)
-    _check("dflash2_linear4", L.dflash2_linear4(xp, dt, rows, xs, w._ref, yp, _dtype(out), ys, *scratch,
-                                                _raw_stream(dev)))
+    call = L.dflash2_linear4_rounded if rounded else L.dflash2_linear4
+    _check("dflash2_linear4", call(xp, dt, rows, xs, w._ref, yp, _dtype(out), ys, *scratch, _raw_stream(dev)))
     return out
 
 

@@ -795,9 +795,10 @@ extern "C" size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows
     return linear4_tc_bytes(dt == DFLASH2_F32, rows, K);
 }
 
-extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
-                                          const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride,
-                                          void *ws, size_t ws_bytes, dflash2_stream stream) {
+// rounded: bf16 results of bf16 scales may be taken on weights in bf16.
+static dflash2_status linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride, const dflash2_weight4 *w,
+                              void *y, dflash2_dtype y_dt, int64_t y_stride, bool rounded, void *ws, size_t ws_bytes,
+                              dflash2_stream stream) {
     if (!dtype_ok(dt) || !dtype_ok(y_dt) || (dt == DFLASH2_F32 && y_dt != DFLASH2_F32) || !weight4_ok(w) || rows < 0 ||
         x_stride < w->K || y_stride < w->N)
         return DFLASH2_ERR_INVALID_ARG;
@@ -808,8 +809,7 @@ extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64
     if (l4_many(dt, rows, w->N, w->K, false)) {
         if (!ws || !aligned16(ws)) return DFLASH2_ERR_INVALID_ARG;
         if (ws_bytes < linear4_tc_bytes(dt == DFLASH2_F32, rows, w->K)) return DFLASH2_ERR_WORKSPACE;
-        // f32 results and f32 scales keep their bits; other results are taken on weights in bf16
-        const bool exact = y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
+        const bool exact = !rounded || y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
         if (l4_many(dt, rows, w->N, w->K, exact)) return linear4_tc(x, dt == DFLASH2_F32, rows, x_stride, w, y, y_dt, y_stride, exact, ws, s);
     }
     // blocks of rows are counted in 16 bits: of up to L4_LONG_K columns they have 16 rows, of more one at least
@@ -819,4 +819,16 @@ extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64
     p.G = static_cast<int>(groups_of(w));
     p.gpb_log2 = w->group == 128 ? 0 : w->group == 64 ? 1 : 2;
     return linear4_mma(p, dt == DFLASH2_F32, s);
+}
+
+extern "C" dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
+                                          const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride,
+                                          void *ws, size_t ws_bytes, dflash2_stream stream) {
+    return linear4(x, dt, rows, x_stride, w, y, y_dt, y_stride, false, ws, ws_bytes, stream);
+}
+
+extern "C" dflash2_status dflash2_linear4_rounded(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
+                                                  const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride,
+                                                  void *ws, size_t ws_bytes, dflash2_stream stream) {
+    return linear4(x, dt, rows, x_stride, w, y, y_dt, y_stride, true, ws, ws_bytes, stream);
 }

@@ -24,10 +24,10 @@
 //   2 warps      copies of x', MMAs
 // Tensor memory: 4 accumulators of R columns (2 of 128), 4 blocks of A of 64 columns.
 //
-// Results in bf16 on weights in bf16: one accumulator over all columns.  512 rows
+// Results in bf16 on weights in bf16 (dflash2_linear4_rounded): one accumulator over all columns.  512 rows
 // of 151936 x 5120: 538 us, 1480 TFLOP/s; bound by the operand's conversion (two
 // instructions a pair of codes, three with zero points) and a barrier's 150 cycles.
-// 64 rows: 122 us, all of it the operand.  Results in f32 on codes: 64 rows of
+// 64 rows: 122 us, all of it the operand.  Results on codes: 64 rows of
 // 151936 x 2560 in groups of 128 94 us, of 32 228 us; bound by the chain MMA -
 // barrier - tensor memory load - barrier per group; loads of a second group ahead
 // gained nothing, and spilled at 128 rows.  512 rows of 7168 x 5120 by items 40 us,
@@ -61,6 +61,12 @@ constexpr int T4_M = 128;
 // Weights in bf16 are held times 2^-40, and their rows of x have their largest entry near 2^80: with scales from 2^-80 to
 // 2^30 and entries from 2^-80 of a row's largest nothing vanishes or overflows.
 constexpr int T4_DOWN = 40, T4_TOP = 207;  // (and the field of that entry's exponent)
+constexpr uint32_t T4_SCALE_LO = (127u - 80u) << 7, T4_SCALE_HI = (127u + 30u) << 7, T4_ZERO_HI = (127u + 39u) << 7;
+// Bits of a scale as the weights in bf16 take it: NaN where it, or its zero point, leaves that range.
+__device__ __forceinline__ uint32_t t4_scale(uint32_t scale, uint32_t zero) {
+    const uint32_t m = scale & 0x7fffu;
+    return (m == 0 || m - T4_SCALE_LO <= T4_SCALE_HI - T4_SCALE_LO) && (zero & 0x7fffu) <= T4_ZERO_HI ? scale : 0x7fc0u;
+}
 constexpr long long T4_WAIT = 4000000000ll, T4_DRAIN = 200000000ll;
 
 struct Tc4Shared {
@@ -224,10 +230,11 @@ __device__ __forceinline__ void operand(const uint32_t *v, uint32_t to, const ui
     for (int q = 0; q < 4; ++q) {  // 32 columns
         uint32_t first = 0, second = 0, less = 0, scale = 0;
         if constexpr (KIND != 0) {
-            const float sc = __uint_as_float(sr[q * 32 >> (7 - LG)] << 16);
+            const uint32_t sb = t4_scale(sr[q * 32 >> (7 - LG)], KIND == 2 ? zr[q * 32 >> (7 - LG)] : 0);
+            const float sc = __uint_as_float(sb << 16);
             const float f = KIND == 1 ? sc : 1.0f, z = KIND == 1 ? 8.0f * sc : __uint_as_float(zr[q * 32 >> (7 - LG)] << 16);
             first = pair_of(f * pow2f(133 - T4_DOWN)), second = pair_of(f * pow2f(129 - T4_DOWN));
-            less = pair_of(-z * pow2f(-T4_DOWN)), scale = sr[q * 32 >> (7 - LG)] * 0x10001u;
+            less = pair_of(-z * pow2f(-T4_DOWN)), scale = sb * 0x10001u;
         }
         uint32_t a[16];
 #pragma unroll

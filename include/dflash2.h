@@ -619,13 +619,10 @@ dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dty
  * y [rows, y_stride] (y_dt): the first N entries of a row are written.
  *   y_dt is dt, or f32.  A row of x that holds a NaN or an infinity gives a
  *   row of NaN.
- *   Sums are f32 sums of exact products of codes and of zero points with x;
+ *   Sums are f32 sums of exact products of codes and of zero points with x,
+ *   rounded once to y_dt, for any number of rows;
  *   entries of x below 2^-130 of their row's largest (f32: 2^-110) and scales
- *   below 2^-100 lose bits.  bf16 results for many rows (those that take a workspace) with
- *   bf16 scales are sums of x times the weights rounded to bf16 (code - zero,
- *   then its product with the scale), for scales from 2^-80 to 2^30 (and 0);
- *   entries of x below 2^-80 of their row's largest lose bits.  Scales beyond
- *   those are for f32 results.
+ *   below 2^-100 lose bits.
  * ws: dflash2_linear4_workspace_bytes(dt, rows, N, K) bytes, which is 0 for
  *   few rows (ws may then be NULL).  It needs no zeros and is left with
  *   scratch.
@@ -635,11 +632,23 @@ dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dty
  * above 2^19, rows above 2^15 with K above 2^13 where no workspace is taken,
  * and some products with N K rows above 2^54; WORKSPACE if ws_bytes is too
  * small.
+ *
+ * dflash2_linear4_rounded -- the same, where the weights of a call with bf16
+ * x, results and scales that takes a workspace may be rounded to bf16 (code - zero, then
+ * its product with the scale): faster for many rows, and most of all for
+ * small groups.  Its results are off by the weights' rounding besides their
+ * own, so a row's are not those that it has in a call of few rows.  A weight
+ * row with a scale outside 2^-80 .. 2^30 (and not 0) or a zero point above
+ * 2^40 gives NaN in such a call; entries of x below 2^-80 of their row's
+ * largest lose bits.  Every other call is dflash2_linear4.
  */
 size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K);
 dflash2_status dflash2_linear4(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
                                const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride, void *ws,
                                size_t ws_bytes, dflash2_stream stream);
+dflash2_status dflash2_linear4_rounded(const void *x, dflash2_dtype dt, int64_t rows, int64_t x_stride,
+                                       const dflash2_weight4 *w, void *y, dflash2_dtype y_dt, int64_t y_stride,
+                                       void *ws, size_t ws_bytes, dflash2_stream stream);
 
 /*
  * dflash2_sample -- one token per row of logits from a given uniform: what a
