@@ -588,6 +588,8 @@ struct Sampler {
         if (rank == 0) {
             near = far = 0, near_n = 0;
             for (int q = 0; q < C; ++q) near += sm->in_word[q], far += sm->in_far[q], near_n += static_cast<uint32_t>(sm->in_near[q]);
+            // below a largest value of about 2^40 and more the place between -2^-8 and 2^-8 is past the bins like what lies below it
+            if (np >= KEYS) far += near, near = 0, near_n = 0;
             // Runs of K_PER bins, neighbouring ones to different warps: most tokens lie in a few hundred bins.  The counts
             // stay in this CTA's bins, what lies above a run in the list's place.
             const int g = lane * S_WARPS + warp, b0 = g * K_PER;

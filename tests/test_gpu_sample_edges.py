@@ -1,0 +1,33 @@
+"""Sampling where the rows' values leave the usual range, against the definition in 64 bits."""
+import pytest
+import torch
+
+import dflash_draft_selection_gb300 as d2
+from tests import _decode as ref
+from tests._util import cuda_or_skip, padded
+from tests.test_gpu_sample import check, gen
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("M", [2.0 ** 39, 1e12, 1e13, 2.0 ** 60, 1e30])
+@pytest.mark.parametrize("V", [1000, 40000])
+def test_small_values_beside_a_huge_one(V, M, dt):
+    """The largest logit is so large that values next to zero are past 6144 steps of bf16 from it; a temperature of its
+    size gives them their mass all the same."""
+    cuda_or_skip()
+    g = gen(V)
+    zeros = torch.zeros(V, device="cuda")
+    tiny = torch.randn(V, generator=g, device="cuda") * 1e-3
+    mixed = torch.where(torch.rand(V, generator=g, device="cuda") < 0.5, tiny, -M / 2)
+    spread = torch.randn(V, generator=g, device="cuda") * M / 8
+    base = torch.stack([zeros, tiny, mixed, torch.where(tiny > 0, spread, tiny)]).repeat(3, 1)
+    base[:, V // 3] = M
+    n = base.shape[0]
+    for i, (T, k, p, mp) in enumerate([(M, 0, 1.0, 0.0), (M, 0, 0.9, 0.0), (M, 600, 1.0, 0.0), (M, 700, 0.9, 0.0),
+                                       (M, 0, 0.95, 0.1), (M, 0, 0.95, 0.5), (M / 4, 0, 1.0, 0.0), (M, V - 1, 0.99, 0.0),
+                                       (4 * M, 0, 0.5, 0.01)]):
+        u = torch.rand(n, generator=gen(20 + i), device="cuda")
+        check(base.to(dt), u, [T] * n, [k] * n, [p] * n, [mp] * n)
