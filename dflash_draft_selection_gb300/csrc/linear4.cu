@@ -810,7 +810,9 @@ static dflash2_status linear4(const void *x, dflash2_dtype dt, int64_t rows, int
         if (!ws || !aligned16(ws)) return DFLASH2_ERR_INVALID_ARG;
         if (ws_bytes < linear4_tc_bytes(dt == DFLASH2_F32, rows, w->K)) return DFLASH2_ERR_WORKSPACE;
         const bool exact = !rounded || y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
-        if (l4_many(dt, rows, w->N, w->K, exact)) return linear4_tc(x, dt == DFLASH2_F32, rows, x_stride, w, y, y_dt, y_stride, exact, ws, s);
+        // (also where the kernel for few rows does not count as many blocks, as below)
+        if (l4_many(dt, rows, w->N, w->K, exact) || (rows > L4_LONG_ROWS && w->K > L4_LONG_K))
+            return linear4_tc(x, dt == DFLASH2_F32, rows, x_stride, w, y, y_dt, y_stride, exact, ws, s);
     }
     // blocks of rows are counted in 16 bits: of up to L4_LONG_K columns they have 16 rows, of more one at least
     if (rows > L4_LONG_ROWS && w->K > L4_LONG_K) return DFLASH2_ERR_UNSUPPORTED;
