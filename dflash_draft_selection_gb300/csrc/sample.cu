@@ -115,10 +115,9 @@ struct Mass {
         if (!(th < 47.0f)) return 0;
         float tl = fmaf(d, ch, -th);
         tl = fmaf(d, cl, tl);
-        if (!BF16) {  // m - z of two bf16 loses at most 2^-24 of a difference next to m; of two f32 it loses that always
-            const float b = d - m;
-            tl = fmaf((m - (d - b)) + (-z - b), ch, tl);
-        }
+        // what d lacks of m - z (of bf16 too, where z's last bit is below 2^-24 of m)
+        const float b = d - m;
+        tl = fmaf((m - (d - b)) + (-z - b), ch, tl);
         const float f = fmaf(th, 32.0f, S_MAGIC);
         const int n = __float_as_int(f) - __float_as_int(S_MAGIC);
         const float r = fmaf(f - S_MAGIC, -1.0f / 32.0f, th);

@@ -31,3 +31,19 @@ def test_small_values_beside_a_huge_one(V, M, dt):
                                        (4 * M, 0, 0.5, 0.01)]):
         u = torch.rand(n, generator=gen(20 + i), device="cuda")
         check(base.to(dt), u, [T] * n, [k] * n, [p] * n, [mp] * n)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_differences_that_f32_does_not_hold(dt):
+    """A logit of 16 and many whose difference from it takes 25 bits (a tie in f32): their masses are those of the exact
+    difference.  Rounded it would move the mass by 2^-21 / T of itself."""
+    cuda_or_skip()
+    V, n = 150000, 8
+    z = torch.full((n, V), 2.0 ** -14 + 2.0 ** -21, device="cuda")
+    z[:, V // 2] = 16.0
+    assert torch.equal(z.to(dt).float(), z)
+    for i, (T, k, p, mp) in enumerate([(1.0, 0, 1.0, 0.0), (2.0, 0, 1.0, 0.0), (2.0, 0, 0.9, 0.0), (4.0, 0, 1.0, 0.0),
+                                       (4.0, 0, 0.7, 0.0), (2.0, 5000, 1.0, 0.0), (4.0, 100, 1.0, 0.0)]):
+        # uniforms in the middle of a token's share
+        u = (torch.randint(0, 4096, (n,), generator=gen(i), device="cuda").float() + 0.5) / 4096
+        check(z.to(dt), u, [T] * n, [k] * n, [p] * n, [mp] * n)
