@@ -791,10 +791,11 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
     if (threadIdx.x < 4) sm->list_n[threadIdx.x] = 0;
     // 64-bit arithmetic is slow here: one thread's, for all
     if (threadIdx.x == 0) {
-        const double inv_t = 1.0 / static_cast<double>(T == 0.0f ? 1.0f : T), c = fmin(1.4426950408889634074 * inv_t, 3.0e38);
+        const double t = T == 0.0f ? 1.0 : fmax(static_cast<double>(T), 0x1p-127);  // so that c is a float
+        const double inv_t = 1.0 / t, c = 1.4426950408889634074 * inv_t;
         sm->inv_t = inv_t;
         sm->ch = static_cast<float>(c), sm->cl = static_cast<float>(c - static_cast<double>(sm->ch));
-        sm->t_log = min_p > 0.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0;
+        sm->t_log = min_p > 0.0f ? t * log(static_cast<double>(min_p)) : 0.0;
     }
     if (threadIdx.x >= 32 && threadIdx.x < 64) {
         const double v = exp2(-static_cast<double>(threadIdx.x - 32) / 32);

@@ -671,6 +671,7 @@ dflash2_status dflash2_linear4_rounded(const void *x, dflash2_dtype dt, int64_t 
  * Masses are summed as whole numbers of 2^-44 (of 2^-(63 - ceil(log2(V + 1)))
  *   for V above 2^19), so a row's token depends neither on the other rows nor on
  *   how the row is split.
+ * A temperature between 0 and 2^-127 counts as 2^-127.
  * A row with a NaN or +Inf, nothing above -Inf, a NaN uniform or invalid
  * parameters (as DFLASH2_ST_BAD_PARAMS; min_p outside [0, 1]) gets token -1 and
  * prob NaN.  f32 logits further below the largest than f32 reaches have no mass.

@@ -47,3 +47,21 @@ def test_differences_that_f32_does_not_hold(dt):
         # uniforms in the middle of a token's share
         u = (torch.randint(0, 4096, (n,), generator=gen(i), device="cuda").float() + 0.5) / 4096
         check(z.to(dt), u, [T] * n, [k] * n, [p] * n, [mp] * n)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_temperatures_next_to_zero(dt):
+    """Above 0 the least one is 2^-127: what lies between counts as that.  The logits are its size."""
+    cuda_or_skip()
+    V, n, least = 90, 24, 2.0 ** -127
+    z = (torch.arange(V, device="cuda") * -2.0 ** -133).flip(0).expand(n, V).contiguous().to(dt)
+    assert z.float().unique().numel() == V
+    u = torch.rand(n, generator=gen(4), device="cuda")
+    for k, p, mp in ((0, 1.0, 0.0), (30, 0.9, 0.0), (0, 0.8, 0.0), (0, 1.0, 0.5)):
+        check(z, u, [least] * n, [k] * n, [p] * n, [mp] * n)
+        rec = lambda T: d2.sampling_params([T] * n, [k] * n, [p] * n)  # noqa: E731
+        m = torch.full((n,), mp, device="cuda")
+        want = d2.sample(padded(z), u, params=rec(least), min_p=m)
+        for T in (5e-39, 1e-40, 2.0 ** -149):
+            got = d2.sample(padded(z), u, params=rec(T), min_p=m)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
