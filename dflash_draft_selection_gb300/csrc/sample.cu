@@ -1002,11 +1002,12 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
             }
         });
         own = s.block_sum(own);
-        if (threadIdx.x == 0) peer(&sm->in_word[s.rank], 0)[0] = own;
+        // (not in in_word: the first CTA may still be reading its floors there)
+        if (threadIdx.x == 0) peer(&sm->in_far[s.rank], 0)[0] = own;
         cluster_sync();
         if (s.rank == 0) {
             kept_min = 0;
-            for (int q = 0; q < C; ++q) kept_min += sm->in_word[q];
+            for (int q = 0; q < C; ++q) kept_min += sm->in_far[q];
             s.gather_bins(&total_n, &total_m);
         }
     };

@@ -65,3 +65,15 @@ def test_temperatures_next_to_zero(dt):
         for T in (5e-39, 1e-40, 2.0 ** -149):
             got = d2.sample(padded(z), u, params=rec(T), min_p=m)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("rows,V", [(1, 151936), (40, 20000), (300, 9000), (64, 151936)])
+@pytest.mark.parametrize("k", [513, 1000, 2100, 4096])
+def test_top_k_past_the_short_list(k, rows, V):
+    """f32 rows over several CTAs whose top_k is no short list: a floor, then bins."""
+    cuda_or_skip()
+    z = torch.randn(rows, V, generator=gen(k), device="cuda") * 2
+    u = torch.rand(rows, generator=gen(rows), device="cuda")
+    for p in (1.0, 0.9):
+        for dt in (F32, BF):
+            check(z.to(dt), u, [1.0] * rows, [k] * rows, [p] * rows, [0.0] * rows)
