@@ -20,6 +20,7 @@ struct Quant4 {
     uint32_t all;     // of them in all rows
     int codes;        // vectors of 8 columns that have a place in a row
     int span_log2;    // log2 of the lanes to a row (back)
+    int part;         // vectors of a row to a warp (back), a multiple of what it reads at once
     bool vec;
 };
 
@@ -116,8 +117,8 @@ __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
     }
 }
 
-// Eight columns to a thread (4 bytes of codes, 16 of bf16); a warp takes a row, or several short ones, and reads Q4_AHEAD
-// vectors before it works on them.  151936 x 2560 to bf16: 155 us (6.3 TB/s),
+// Eight columns to a thread (4 bytes of codes, 16 of bf16); a warp takes a row, or several short ones, or a part of a long
+// one where rows are few, and reads Q4_AHEAD vectors before it works on them.  151936 x 2560 to bf16: 155 us (6.3 TB/s),
 // HBM-bound; in f32 arithmetic throughout it took 30 us more.
 //
 // VEC: the rows start on 16-byte boundaries.  Where they do not, a warp's 256 values take their places in shared memory and
@@ -128,11 +129,12 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
     constexpr int LANES = 16 >> LG;
     const int lane = threadIdx.x & 31, span = 1 << p.span_log2;
     const int64_t n = (((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) << (5 - p.span_log2)) + (lane >> p.span_log2);
+    const int first = static_cast<int>(blockIdx.y) * p.part, end = min(first + p.part, p.codes);
     if constexpr (!VEC) {
         __shared__ float4 place[8][64];
         const int64_t n0 = n - (lane >> p.span_log2);
         float4 *mine = place[threadIdx.x >> 5];
-        for (int c0 = 0; c0 < p.codes; c0 += span) {
+        for (int c0 = first; c0 < end; c0 += span) {
             const int c = c0 + (lane & (span - 1));
             float v[8] = {};
             if (n < p.w.N && static_cast<int64_t>(c) * 8 < p.w.K) {
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
     }
     if (n >= p.w.N) return;
     const uint8_t *codes = static_cast<const uint8_t *>(p.w.codes) + n * p.w.code_stride;
-    for (int c0 = lane & (span - 1); c0 < p.codes; c0 += span * Q4_AHEAD) {
+    for (int c0 = first + (lane & (span - 1)); c0 < end; c0 += span * Q4_AHEAD) {
         uint32_t word[Q4_AHEAD], sb[Q4_AHEAD], zb[Q4_AHEAD];
 #pragma unroll
         for (int i = 0; i < Q4_AHEAD; ++i) {
@@ -708,7 +710,7 @@ static dflash2_status linear4_mma(Lin4 p, bool f32x, cudaStream_t s) {
 using namespace dfl;
 
 // The sizes that the two kernels share, and their grid.
-static Quant4 quant4_of(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w, bool back, unsigned *grid) {
+static Quant4 quant4_of(const void *W, dflash2_dtype dt, int64_t ld, const dflash2_weight4 *w, bool back, dim3 *grid) {
     Quant4 p = {};
     p.W = W, p.w = *w, p.ld = ld;
     p.pieces = static_cast<uint32_t>(groups_of(w) * (w->group / 32));
@@ -717,7 +719,11 @@ static Quant4 quant4_of(const void *W, dflash2_dtype dt, int64_t ld, const dflas
     for (p.span_log2 = 2; p.span_log2 < 5 && (1 << p.span_log2) < p.codes;) ++p.span_log2;
     p.vec = aligned16(W) && ld * esize(dt) % 16 == 0;
     const int64_t warps = (w->N + (32 >> p.span_log2) - 1) / (32 >> p.span_log2);
-    *grid = back ? static_cast<unsigned>((warps + 7) / 8) : (p.all + 255) / 256;
+    // rows are cut while warps are fewer than the GPU holds: 16 x 20480 2.6 us (a warp to a row 15), of 20481 columns 4.2 (49)
+    const int64_t room = sm_count() * int64_t(64), parts = warps < room ? room / warps : 1, once = Q4_AHEAD << p.span_log2;
+    p.part = static_cast<int>(((p.codes + parts - 1) / parts + once - 1) / once * once);
+    *grid = back ? dim3(static_cast<unsigned>((warps + 7) / 8), static_cast<unsigned>((p.codes + p.part - 1) / p.part))
+                 : dim3((p.all + 255) / 256);
     return p;
 }
 
@@ -727,23 +733,23 @@ static bool quant4_fits(const dflash2_weight4 *w) {
 }
 
 template <bool F32W, int LG>
-static void launch_quant4(const Quant4 &p, unsigned grid, cudaStream_t s) {
+static void launch_quant4(const Quant4 &p, dim3 grid, cudaStream_t s) {
     if (p.w.zero) k_quant4<F32W, LG, true><<<grid, 256, 0, s>>>(p);
     else k_quant4<F32W, LG, false><<<grid, 256, 0, s>>>(p);
 }
 template <bool F32W>
-static void launch_quant4_groups(const Quant4 &p, unsigned grid, cudaStream_t s) {
+static void launch_quant4_groups(const Quant4 &p, dim3 grid, cudaStream_t s) {
     if (p.w.group == 128) launch_quant4<F32W, 0>(p, grid, s);
     else if (p.w.group == 64) launch_quant4<F32W, 1>(p, grid, s);
     else launch_quant4<F32W, 2>(p, grid, s);
 }
 template <bool F32W, int LG>
-static void launch_dequant4_rows(const Quant4 &p, void *out, unsigned grid, cudaStream_t s) {
+static void launch_dequant4_rows(const Quant4 &p, void *out, dim3 grid, cudaStream_t s) {
     if (p.vec) k_dequant4<F32W, LG, true><<<grid, 256, 0, s>>>(p, out);
     else k_dequant4<F32W, LG, false><<<grid, 256, 0, s>>>(p, out);
 }
 template <bool F32W>
-static void launch_dequant4(const Quant4 &p, void *out, unsigned grid, cudaStream_t s) {
+static void launch_dequant4(const Quant4 &p, void *out, dim3 grid, cudaStream_t s) {
     if (p.w.group == 128) launch_dequant4_rows<F32W, 0>(p, out, grid, s);
     else if (p.w.group == 64) launch_dequant4_rows<F32W, 1>(p, out, grid, s);
     else launch_dequant4_rows<F32W, 2>(p, out, grid, s);
@@ -755,7 +761,7 @@ extern "C" dflash2_status dflash2_quant4(const void *W, dflash2_dtype dt, int64_
     if (w->N == 0) return DFLASH2_OK;
     if (!W || !aligned_to(W, dt)) return DFLASH2_ERR_INVALID_ARG;
     if (!quant4_fits(w)) return DFLASH2_ERR_UNSUPPORTED;
-    unsigned grid;
+    dim3 grid;
     const Quant4 p = quant4_of(W, dt, ld, w, false, &grid);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dt == DFLASH2_F32) launch_quant4_groups<true>(p, grid, s);
@@ -769,7 +775,7 @@ extern "C" dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, 
     if (w->N == 0) return DFLASH2_OK;
     if (!out || !aligned_to(out, dt)) return DFLASH2_ERR_INVALID_ARG;
     if (!quant4_fits(w)) return DFLASH2_ERR_UNSUPPORTED;
-    unsigned grid;
+    dim3 grid;
     const Quant4 p = quant4_of(out, dt, ld, w, true, &grid);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dt == DFLASH2_F32) launch_dequant4<true>(p, out, grid, s);
