@@ -27,7 +27,7 @@ struct Quant4 {
 // 32 columns to a thread, so that what a group costs (a scale and two or three divisions) is shared by as many; a group is
 // 4, 2 or 1 neighbouring lanes.  A quotient's whole number comes from the product with the reciprocal; where that (off by
 // at most 2^-18) is next to a half, the entry is read again and divided.
-// 151936 x 2560 bf16: 264 us (4.0 TB/s), with zero points 299 us.  Bound by instruction issue (2.6 a cycle, about 15 to an
+// 151936 x 2560 bf16: 264 us (3.7 TB/s), with zero points 299 us.  Bound by instruction issue (2.6 a cycle, about 15 to an
 // entry).  One entry to a thread with a division each, the two directions of a head took 3.9 ms, now 0.46.
 template <bool F32W, int LG, bool ZERO>
 __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(256) k_dequant4(const Quant4 p, void *out) {
 // 150 for a block of 1 KB, most of them masks and shifts that share one pipe;
 // three CTAs to an SM leave too few registers for the copies (112 us).  Eight
 // rows 99 us: the same and the MMAs' operands of x.  Few tiles are bound by
-// their latency (2560 x 2560, one row: 6.2 us).
+// their latency (2560 x 2560, one row: 6.2 us).  25 to 32 rows at a time spill 20 to 32
+// bytes at 128 registers.
 constexpr int L4_THREADS = 256;
 constexpr int L4_WARPS = L4_THREADS / 32;
 constexpr int L4_STAGES = 4;
@@ -784,20 +785,27 @@ extern "C" dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, 
 }
 
 // Whether the tensor cores' kernel is the faster one.  Its time follows K while its items are no more than the SMs (5120
-// columns: 18 to 24 us, f32 results 20 to 35; 1024: 8 to 11 and 8 to 14), that of the kernel for few rows N x rows (5120
-// columns, 32 rows of 1024, 4096, 8192: 16, 20, 36 us).  At 396 sizes (9 to 512 rows, N 128 to 8192, K 256 to 17408) the
-// choice takes 1.5 % more than the faster one on average and 27 % at most, but for 128 rows of 4096 x 256 in f32 (10 us for 7).
+// columns: 20 to 35 us, on rounded weights 18 to 24; 1024: 8 to 14 and 8 to 11), that of the kernel for few rows N x rows
+// (5120 columns, 32 rows of 1024, 4096, 8192: 16, 20, 36 us).  At 396 sizes (9 to 512 rows, N 128 to 8192, K 256 to 17408;
+// groups of 128) the choice takes 1.5 % more than the faster one on average and 27 % at most, but for 128 exact rows of
+// 4096 x 256 (10 us for 7).  In groups of 32 the tensor cores' kernel takes up to twice as long on exact weights, and the
+// other one 1.1 times: there the choice (180 sizes) takes 1.4 % more on average and 41 % at most; that of the other groups
+// took 9 and 81 %.  `group`: 0 for rounded weights.
 // f32 rows (three times the products either way) at 300 sizes up to 32768 x 17408: 1.2 % more, at most 47 % (9 rows of 8192 x
 // 17408, 111 us for 76); 64 rows of 32768 x 5120 take 267 and 87 us.
-static bool l4_many(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K, bool exact) {
+static bool l4_many(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K, int group) {
     if (rows < L4_MANY_ROWS) return false;
     if (dt == DFLASH2_F32) return rows * N >= 3 << 15;
+    if (group == 32) {
+        const int64_t at = (1 << 18) - (1 << 24) / K;
+        return rows * N >= (rows > 64 ? at + at / 2 : 2 * at);
+    }
     const int64_t at = (1 << 17) - (3 << 26) / K;
-    return rows * N >= (!exact ? at : rows > 64 ? 2 * at : at + at / 2);
+    return rows * N >= (group == 0 ? at : rows > 64 ? 2 * at : at + at / 2);
 }
 
 extern "C" size_t dflash2_linear4_workspace_bytes(dflash2_dtype dt, int64_t rows, int64_t N, int64_t K) {
-    if (!dtype_ok(dt) || rows < 1 || N < 1 || K < 1 || K > L4_MAX_K || rows > L4_MAX_ROWS || !l4_many(dt, rows, N, K, false)) return 0;
+    if (!dtype_ok(dt) || rows < 1 || N < 1 || K < 1 || K > L4_MAX_K || rows > L4_MAX_ROWS || !l4_many(dt, rows, N, K, 0)) return 0;
     return linear4_tc_bytes(dt == DFLASH2_F32, rows, K);
 }
 
@@ -812,12 +820,12 @@ static dflash2_status linear4(const void *x, dflash2_dtype dt, int64_t rows, int
     if (!x || !y || !aligned_to(x, dt) || !aligned_to(y, y_dt)) return DFLASH2_ERR_INVALID_ARG;
     if (w->K > L4_MAX_K || rows > L4_MAX_ROWS) return DFLASH2_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (l4_many(dt, rows, w->N, w->K, false)) {
+    if (l4_many(dt, rows, w->N, w->K, 0)) {
         if (!ws || !aligned16(ws)) return DFLASH2_ERR_INVALID_ARG;
         if (ws_bytes < linear4_tc_bytes(dt == DFLASH2_F32, rows, w->K)) return DFLASH2_ERR_WORKSPACE;
         const bool exact = !rounded || y_dt == DFLASH2_F32 || w->side_dt == DFLASH2_F32;
         // (also where the kernel for few rows does not count as many blocks, as below)
-        if (l4_many(dt, rows, w->N, w->K, exact) || (rows > L4_LONG_ROWS && w->K > L4_LONG_K))
+        if (l4_many(dt, rows, w->N, w->K, exact ? w->group : 0) || (rows > L4_LONG_ROWS && w->K > L4_LONG_K))
             return linear4_tc(x, dt == DFLASH2_F32, rows, x_stride, w, y, y_dt, y_stride, exact, ws, s);
     }
     // blocks of rows are counted in 16 bits: of up to L4_LONG_K columns they have 16 rows, of more one at least
