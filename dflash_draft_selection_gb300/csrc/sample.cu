@@ -31,10 +31,13 @@
 // would be off by 2^-24, and one draw in a few hundred of a flat row of 150000
 // tokens would be another token than in 64 bits.
 //
-// Bound by latency: a chain of passes, cluster barriers and one thread's 64-bit
-// arithmetic.  One row of 151936 takes 7 us greedy, 13 with top_k 20, 23 with top_p
-// in bf16 and 38 in f32; 64 rows in bf16 with top_p 38 us (bins and lists took 65),
-// 512 rows of 262144 with top_k and min_p 261 us, 1.0 TB/s.
+// Up to some 40 to 80 rows: bound by latency, a chain of passes, cluster barriers and
+// one thread's 64-bit arithmetic.  One row of 151936 takes 7 us greedy, 13 with top_k
+// 20, 23 with top_p in bf16 and 40 in f32; 64 rows in bf16 with top_p 38 us (bins and
+// lists took 65).  More rows than fit the SMs' shared memory go in waves, each of which
+// waits through the chain while little is read: 512 rows of 262144 with top_k and min_p
+// 261 us, 1.0 TB/s.  At 64 registers a thread (two CTAs to an SM) 168 bytes spill in
+// f32 and 60 in bf16.
 #include "common.cuh"
 #include "host.hpp"
 #include "tc.cuh"
@@ -370,7 +373,7 @@ struct Sampler {
             __syncthreads();
             return;
         }
-        int pow = 32;
+        int pow = 512;
         while (pow < cnt) pow *= 2;
         for (int i = threadIdx.x; i < pow; i += S_THREADS)
             if (i >= cnt) sm->list[i] = 0;
@@ -382,10 +385,8 @@ struct Sampler {
                     const u64 x = sm->list[a], y = sm->list[b];
                     if ((x < y) == ((a & k) == 0)) sm->list[a] = y, sm->list[b] = x;
                 }
-                if (pow > 64) __syncthreads();
-                else __syncwarp();
+                __syncthreads();
             }
-        __syncthreads();
     }
 
     // Where the ranking's running count or mass reaches `target` (known to the first CTA; within the totals).  In the
@@ -529,7 +530,7 @@ struct Sampler {
 
     // What the first CTA finds: the key of the drawn token, which of its ties it is, and Z.  All CTAs; false where a
     // question ends among values that have no bin of their own.
-    __device__ bool by_values(const SampleArgs &a, int top_k, bool by_k, float top_p, float z_min, float u, uint32_t *key,
+    __device__ bool by_values(int top_k, bool by_k, float top_p, float z_min, float u, uint32_t *key,
                               u64 *tie, u64 *Z_out) {
         uint32_t *bins = sm->cnt;  // and lo, hi behind it
         for (int i = threadIdx.x * 4; i < KEYS; i += S_THREADS * 4) *reinterpret_cast<uint4 *>(bins + i) = make_uint4(0, 0, 0, 0);
@@ -979,7 +980,7 @@ __global__ void __launch_bounds__(S_THREADS, 2) k_sample(const SampleArgs a, int
     if constexpr (BF16) {
         uint32_t key;
         u64 tie = 0, Z = 0;
-        if (s.by_values(a, top_k, by_k, top_p, z_min, u, &key, &tie, &Z)) {
+        if (s.by_values(top_k, by_k, top_p, z_min, u, &key, &tie, &Z)) {
             const int64_t id = s.place_of(key, tie);
             if (s.rank == 0 && threadIdx.x == 0) {
                 a.token[r] = static_cast<int32_t>(id);

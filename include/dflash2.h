@@ -622,7 +622,8 @@ dflash2_status dflash2_dequant4(const dflash2_weight4 *w, void *out, dflash2_dty
  *   Sums are f32 sums of exact products of codes and of zero points with x,
  *   rounded once to y_dt, for any number of rows;
  *   entries of x below 2^-130 of their row's largest (f32: 2^-110) and scales
- *   below 2^-100 lose bits.
+ *   below 2^-100 lose bits, and (code + |zero|) * |scale| * K from 2^132 on
+ *   may overflow where y does not.
  * ws: dflash2_linear4_workspace_bytes(dt, rows, N, K) bytes, which is 0 for
  *   few rows (ws may then be NULL).  It needs no zeros and is left with
  *   scratch.
@@ -669,7 +670,7 @@ dflash2_status dflash2_linear4_rounded(const void *x, dflash2_dtype dt, int64_t 
  * token [rows] int32; prob [rows] f32: the drawn token's share of the kept
  *   mass (1 for greedy rows).
  * Masses are summed as whole numbers of 2^-44 (of 2^-(63 - ceil(log2(V + 1)))
- *   for V above 2^19), so a row's token depends neither on the other rows nor on
+ *   for V of 2^19 and more), so a row's token depends neither on the other rows nor on
  *   how the row is split.
  * A temperature between 0 and 2^-127 counts as 2^-127.
  * A row with a NaN or +Inf, nothing above -Inf, a NaN uniform or invalid
