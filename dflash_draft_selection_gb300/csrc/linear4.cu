@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256) k_quant4(const Quant4 p) {
 }
 
 // Eight columns to a thread (4 bytes of codes, 16 of bf16); a warp takes a row, or several short ones, or a part of a long
-// one where rows are few, and reads Q4_AHEAD vectors before it works on them.  151936 x 2560 to bf16: 155 us (6.3 TB/s),
+// one where rows are few, and reads Q4_AHEAD vectors before it works on them.  151936 x 2560 to bf16: 146 us (6.7 TB/s),
 // HBM-bound; in f32 arithmetic throughout it took 30 us more.
 //
 // VEC: the rows start on 16-byte boundaries.  Where they do not, a warp's 256 values take their places in shared memory and

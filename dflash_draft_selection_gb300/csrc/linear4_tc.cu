@@ -27,11 +27,12 @@
 // Results in bf16 on weights in bf16 (dflash2_linear4_rounded): one accumulator over all columns.  512 rows
 // of 151936 x 5120: 538 us, 1480 TFLOP/s; bound by the operand's conversion (two
 // instructions a pair of codes, three with zero points) and a barrier's 150 cycles.
-// 64 rows: 122 us, all of it the operand.  Results on codes: 64 rows of
+// 64 rows: 122 us, all of it the operand.  Results on codes: 512 rows of the same
+// in groups of 128 854 us, of 64 1898, of 32 (zero points) 3983; 64 rows of
 // 151936 x 2560 in groups of 128 94 us, of 32 228 us; bound by the chain MMA -
 // barrier - tensor memory load - barrier per group; loads of a second group ahead
-// gained nothing, and spilled at 128 rows.  512 rows of 7168 x 5120 by items 40 us,
-// by whole tiles 73.  64 f32 rows of 32768 x 5120 87 us (k_linear4_mma: 267).
+// gained nothing, and spilled at 128 rows.  512 rounded rows of 7168 x 5120 by items
+// 40 us, by whole tiles 73.  64 f32 rows of 32768 x 5120 87 us (k_linear4_mma: 267).
 //
 // Waits are bounded: after a time-out every role stops waiting, the error word
 // is set and the CTA's remaining outputs are NaN.

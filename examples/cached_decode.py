@@ -43,8 +43,8 @@ class Model:
         self.head4 = None
 
     def hold_head_in_4_bits(self, group: int = 64):
-        """The target's logits come from 4-bit weights from here on (the drafter's from the weights that they stand
-        for)."""
+        """The target's logits come from 4-bit weights from here on (the drafter's, whose fused head reads bf16, from the
+        weights that they stand for, so both are held)."""
         self.head4 = d2.quant4(self.head, group=group)
         d2.dequant4(self.head4, out=self.head)
 
